@@ -268,6 +268,146 @@ int kdtv_verify_attn_noalloc(const kdtv_dims* dims, const void* q_nope, const vo
                              const int32_t* prefix_len, const int32_t* page_table,
                              float* out, unsigned int* status_out, cudaStream_t stream);
 
+/* ---- rotary positions, cache writes and grouped-query attention ------------------------
+ * The steps that stand before the verify attention (rotating queries and new
+ * keys; writing, and where the cache has one byte per element quantising, the
+ * new rows) and the tree-verify attention for caches that hold keys and
+ * values per head (GQA) instead of a latent.
+ *
+ * Conventions shared by these calls, beside the ones above:
+ *   - Row i of request b, i < N, is live if i < n_live[b] (n_live NULL: all N
+ *     rows; values outside [0, N] are clamped).  What is not live is neither
+ *     read nor written.
+ *   - Its cache row is prefix_len[b] + i, its position prefix_len[b] +
+ *     depth[b][i] (depth NULL: prefix_len[b] + i; prefix_len NULL: 0).
+ *     kdtv_tree_build writes depth and n_nodes in this form.
+ *   - Device-side problems go to *status (a device word that the caller
+ *     clears, first error wins), as with kdtv_compact_kv.
+ */
+
+/* Rotary embedding.  Pair j of the rot_dim rotated elements turns by
+ * position * f_j, f_j = base^(-2 j / rot_dim):
+ *   (u, v) -> amp * (u cos - v sin, v cos + u sin)
+ * Pairs are (2j, 2j + 1) or (j, j + rot_dim / 2). */
+#define KDTV_ROPE_MAX_DIM 256
+enum kdtv_rope_layout { KDTV_ROPE_HALF = 0, KDTV_ROPE_INTERLEAVED = 1 };
+enum kdtv_rope_scaling {
+  KDTV_ROPE_PLAIN = 0,
+  KDTV_ROPE_LINEAR = 1,  /* f_j / factor                                          */
+  KDTV_ROPE_NTK = 2,     /* base * factor^(rot_dim / (rot_dim - 2))               */
+  KDTV_ROPE_YARN = 3     /* f_j for pairs that turn more than beta_fast times over
+                            orig_ctx positions, f_j / factor below beta_slow
+                            turns, a linear ramp over the pairs between; amp =
+                            attn_factor                                           */
+};
+typedef struct kdtv_rope_config {
+  int32_t rot_dim;      /* even, 2 .. KDTV_ROPE_MAX_DIM (NTK: >= 4)                */
+  int32_t layout;       /* enum kdtv_rope_layout                                   */
+  int32_t scaling;      /* enum kdtv_rope_scaling                                  */
+  int32_t orig_ctx;     /* YARN: context length before scaling                     */
+  double base;          /* > 1                                                     */
+  double factor;        /* >= 1 (ignored by PLAIN)                                 */
+  double beta_fast;     /* YARN; <= 0 selects 32                                   */
+  double beta_slow;     /* YARN; <= 0 selects 1                                    */
+  double attn_factor;   /* YARN; <= 0 selects 0.1 ln(factor) + 1                   */
+} kdtv_rope_config;
+
+/* Filled once by kdtv_rope_init (host memory; passed to kernels by value). */
+typedef struct kdtv_rope_table {
+  int32_t rot_dim;
+  int32_t layout;
+  float amp;
+  int32_t reserved;
+  uint64_t turn[KDTV_ROPE_MAX_DIM / 2];   /* f_j / 2 pi, in units of 2^-64 turns   */
+} kdtv_rope_table;
+
+/* Host only: KDTV_OK, KDTV_ERR_INVALID_ARG or KDTV_ERR_UNSUPPORTED (rot_dim
+ * above KDTV_ROPE_MAX_DIM). */
+int kdtv_rope_init(const kdtv_rope_config* config, kdtv_rope_table* table);
+
+typedef struct kdtv_rope_args {
+  int32_t B, N, H;      /* requests, rows per request, heads                       */
+  int32_t dim;          /* elements of a head                                      */
+  int32_t rot_off;      /* first rotated element; rot_off + rot_dim <= dim         */
+  int32_t dtype;        /* KDTV_F32 or KDTV_BF16, of x, y and rest                 */
+  int64_t x_stride[3];  /* elements between requests, rows, heads (the last        */
+  int64_t y_stride[3];  /* dimension is contiguous); {0, 0, 0}: contiguous         */
+  int64_t rest_stride[3];
+} kdtv_rope_args;
+
+/*
+ * kdtv_rope — rotary positions.
+ *   x          [B, N, H, dim]
+ *   y          rest NULL: [B, N, H, dim], x with the rotated part replaced (y
+ *              may be x with the same strides: in place);
+ *              else [B, N, H, rot_dim], the rotated part alone
+ *   rest       [B, N, H, dim - rot_dim] or NULL: the other elements, copied
+ *              (the MLA query projection's output becomes q_rope and q_nope)
+ *   prefix_len, n_live [B], depth [B, N] int32, each may be NULL
+ * Angles are reduced exactly in 64-bit fixed point; computed in fp32 and
+ * rounded once.  y and rest must not overlap x otherwise, nor each other.
+ */
+int kdtv_rope(const kdtv_rope_table* table, const kdtv_rope_args* args, const void* x, void* y,
+              void* rest, const int32_t* prefix_len, const int32_t* depth,
+              const int32_t* n_live, cudaStream_t stream);
+
+/* One tensor of a cache.  A cached row is [heads, dim], contiguous; rows lie
+ * [B, t_stride, heads, dim] or [num_pages, page_size, heads, dim]. */
+typedef struct kdtv_kv_part {
+  void* cache;
+  uint8_t* scale;       /* one-byte cache: NULL (value = fp8 * kv_scale) or one byte
+                           per row and head, [rows, heads]: value = fp8 *
+                           2^(byte - 127)                                          */
+  const void* src;      /* append: [B, N, heads, dim], src_stride apart            */
+  void* out;            /* read: [B, N, heads, dim], contiguous                    */
+  int64_t src_stride[3];/* elements between requests, rows, heads; {0,0,0}:
+                           contiguous                                              */
+  int32_t heads, dim;   /* dim <= 512                                              */
+  int32_t rotate;       /* append: nonzero: elements rot_off .. rot_off + rot_dim
+                           of each head are rotated first                          */
+  int32_t rot_off;
+} kdtv_kv_part;
+
+typedef struct kdtv_kv_dims {
+  int32_t B, N;         /* requests, rows per request in src / out                 */
+  int32_t dtype;        /* KDTV_F32 or KDTV_BF16: src / out                        */
+  int32_t cache_dtype;  /* KDTV_F32, KDTV_BF16, or KDTV_BF16_FP8KV: E4M3 bytes     */
+  int32_t page_size;    /* 0: contiguous; > 0: rows per page                       */
+  int32_t t_stride, max_pages, num_pages;   /* as in kdtv_dims                     */
+  float kv_scale;       /* parts without scale bytes; <= 0 selects 1               */
+  int32_t parts;        /* 1 or 2                                                  */
+} kdtv_kv_dims;
+
+/*
+ * kdtv_kv_append — writes row i of request b (live rows) of every part to its
+ * cache row, rotated where the part asks for it, then converted: the latent
+ * cache's c_kv and k_rope, or a GQA cache's K and V.  A one-byte cache without
+ * scale bytes holds the E4M3 value nearest x / kv_scale (what kdtv_verify_attn
+ * reads).  With them, the exponent e of a row's head is the smallest with
+ * max|x| <= 448 * 2^e over its finite elements, clamped to [-117, 119]; the
+ * codes are the E4M3 values nearest x * 2^-e and the byte is e + 127, so that
+ * widening to bf16 is exact.  Rounding is to nearest even, larger magnitudes
+ * and infinities become +-448, NaN stays NaN.
+ * A request whose rows do not fit (KDTV_ERR_BAD_PREFIX) or whose pages are out
+ * of range (KDTV_ERR_BAD_PAGE) is left unwritten.  Requests must not share the
+ * pages that they write.  rope may be NULL if no part rotates.
+ */
+int kdtv_kv_append(const kdtv_kv_dims* dims, const kdtv_kv_part* parts,
+                   const kdtv_rope_table* rope, const int32_t* prefix_len, const int32_t* depth,
+                   const int32_t* n_live, const int32_t* page_table, unsigned int* status,
+                   cudaStream_t stream);
+
+/*
+ * kdtv_kv_read — cache rows start[b] .. start[b] + n_live[b] - 1 of every part
+ * into out[b][0 .. n_live[b]) (start NULL: 0), as values of dtype.  The other
+ * rows of out are left as they were.  A request whose rows lie outside the
+ * cache (KDTV_ERR_BAD_PREFIX) or on a page out of range (KDTV_ERR_BAD_PAGE) is
+ * left unwritten.
+ */
+int kdtv_kv_read(const kdtv_kv_dims* dims, const kdtv_kv_part* parts, const int32_t* start,
+                 const int32_t* n_live, const int32_t* page_table, unsigned int* status,
+                 cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,583 @@
+// Rotary positions of queries, and rows written to and read back from a cache
+// (rotated, quantised).  All three move each byte once, so DRAM bounds them at
+// prompt sizes and launch latency at a few rows.
+
+#include "kdtv_rope.cuh"
+
+#include <math.h>
+#include <string.h>
+
+namespace kdtv {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---- rotary ---------------------------------------------------------------------------
+struct RopeArgs {
+  int N, H, rot_off, rot;
+  int items, rot_items;        // per row: rotated items first, then copied vectors
+  int heads, hgroups;          // heads per thread, groups of them
+  unsigned rows;               // B * N
+  long long xs[3], ys[3], rs[3];
+  const void* x;
+  void* y;
+  void* rest;
+  const int32_t *prefix_len, *depth, *n_live;
+};
+
+// Thread = (row, group of heads, item); neighbouring threads hold neighbouring
+// items, so a head's elements are read and written in 16-byte pieces by
+// neighbouring lanes.  An item is one vector of V elements (interleaved), a
+// vector and its partner rot / 2 further (half), or a vector that is only
+// copied.  The angles of an item are computed once and serve all heads of the
+// group; the loads of kBatch heads are issued before their stores, which also
+// makes x == y safe: no other thread touches the item's elements.
+template <typename T, int V, bool kHalf>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ kdtv_rope_table tab,
+                                                        const __grid_constant__ RopeArgs a) {
+  constexpr int kBatch = 4;
+  const unsigned t = blockIdx.x * kThreads + threadIdx.x;   // < 2^32 (host)
+  const int item = (int)(t % (unsigned)a.items);
+  const unsigned u = t / (unsigned)a.items;
+  const int hg = (int)(u % (unsigned)a.hgroups);
+  const unsigned row = u / (unsigned)a.hgroups;
+  if (row >= a.rows) return;
+  const int b = (int)(row / (unsigned)a.N), i = (int)(row % (unsigned)a.N);
+  if (i >= live_rows(a.n_live, b, a.N)) return;
+  const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + i * a.xs[1];
+  T* y = static_cast<T*>(a.y) + b * a.ys[0] + i * a.ys[1];
+  const int h0 = hg * a.heads, h1 = min(h0 + a.heads, a.H);
+  if (item >= a.rot_items) {
+    const int c = (item - a.rot_items) * V;             // among the elements that are copied
+    const int e = c < a.rot_off ? c : c + a.rot;
+    T* dst;
+    long long dh;
+    if (a.rest) {
+      dst = static_cast<T*>(a.rest) + b * a.rs[0] + i * a.rs[1] + c;
+      dh = a.rs[2];
+    } else {
+      dst = y + e;
+      dh = a.ys[2];
+    }
+    for (int h = h0; h < h1; h += kBatch) {
+      float v[kBatch][V];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (h + k < h1) load_v<V>(x + (h + k) * a.xs[2] + e, v[k]);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (h + k < h1) store_v<V>(dst + (h + k) * dh, v[k]);
+    }
+    return;
+  }
+  const long long pos = (long long)(a.prefix_len ? a.prefix_len[b] : 0) + (a.depth ? a.depth[row] : i);
+  if (!a.rest) y += a.rot_off;
+  x += a.rot_off;
+  if constexpr (kHalf || V == 1) {
+    // u elements at e0, their partners at e1
+    const int e0 = kHalf ? item * V : 2 * item;
+    const int e1 = kHalf ? e0 + a.rot / 2 : e0 + 1;
+    float2 cs[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) cs[k] = rope_cos_sin(tab.turn[item * V + k], pos, tab.amp);
+    for (int h = h0; h < h1; h += kBatch) {
+      float p[kBatch][V], q[kBatch][V];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (h + k < h1) {
+          load_v<V>(x + (h + k) * a.xs[2] + e0, p[k]);
+          load_v<V>(x + (h + k) * a.xs[2] + e1, q[k]);
+        }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (h + k < h1) {
+          float o0[V], o1[V];
+#pragma unroll
+          for (int m = 0; m < V; ++m) {
+            o0[m] = p[k][m] * cs[m].x - q[k][m] * cs[m].y;
+            o1[m] = q[k][m] * cs[m].x + p[k][m] * cs[m].y;
+          }
+          store_v<V>(y + (h + k) * a.ys[2] + e0, o0);
+          store_v<V>(y + (h + k) * a.ys[2] + e1, o1);
+        }
+    }
+  } else {
+    float2 cs[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) cs[k] = rope_cos_sin(tab.turn[item * (V / 2) + k], pos, tab.amp);
+    for (int h = h0; h < h1; h += kBatch) {
+      float p[kBatch][V];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (h + k < h1) load_v<V>(x + (h + k) * a.xs[2] + item * V, p[k]);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (h + k < h1) {
+          float o[V];
+#pragma unroll
+          for (int m = 0; m < V / 2; ++m) {
+            o[2 * m] = p[k][2 * m] * cs[m].x - p[k][2 * m + 1] * cs[m].y;
+            o[2 * m + 1] = p[k][2 * m + 1] * cs[m].x + p[k][2 * m] * cs[m].y;
+          }
+          store_v<V>(y + (h + k) * a.ys[2] + item * V, o);
+        }
+    }
+  }
+}
+
+// ---- cache rows -------------------------------------------------------------------------
+struct KvPart {
+  void* cache;
+  uint8_t* scale;
+  const void* src;
+  void* out;
+  long long ss[3];
+  int heads, dim, rotate, rot_off;
+  int group;                   // append: lanes of one head's row (a power of two)
+};
+struct KvArgs {
+  int B, N, page_size, t_stride, max_pages, num_pages, parts, hgroups;
+  float kv_scale;
+  const int32_t *prefix_len, *depth, *n_live, *page_table;
+  unsigned int* status;
+  KvPart part[2];
+};
+
+// Whether rows L .. L + n - 1 of request b lie in the cache and on pages in
+// range; the block's threads check the pages together.  Uniform per block.
+__device__ __forceinline__ bool rows_ok(const KvArgs& a, int b, int L, int n) {
+  const long long cap = a.page_size ? (long long)a.max_pages * a.page_size : a.t_stride;
+  if (L < 0 || (long long)L + n > cap) {
+    if (threadIdx.x == 0) atomicCAS(a.status, 0u, (unsigned)KDTV_ERR_BAD_PREFIX);
+    return false;
+  }
+  if (!a.page_size) return true;
+  int bad = 0;
+  for (int p = L / a.page_size + threadIdx.x; p <= (L + n - 1) / a.page_size; p += kThreads) {
+    const int pg = a.page_table[(long long)b * a.max_pages + p];
+    bad |= pg < 0 || pg >= a.num_pages;
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) atomicCAS(a.status, 0u, (unsigned)KDTV_ERR_BAD_PAGE);
+    return false;
+  }
+  return true;
+}
+__device__ __forceinline__ long long row_of(const KvArgs& a, int b, int t) {
+  if (!a.page_size) return (long long)b * a.t_stride + t;
+  return (long long)a.page_table[(long long)b * a.max_pages + t / a.page_size] * a.page_size +
+         t % a.page_size;
+}
+
+// A group of `group` lanes takes one row's heads h0, h0 + 1, .. of one part;
+// lane l holds elements (p * group + l) * V + k, p < P, k < V, of the head.
+// The angles are computed once per row and serve its heads.  Rotated
+// elements of the half layout read their partner from memory a second time (a
+// cache hit: the partner's lane reads the same line).
+template <typename S, typename D, int V, int P>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ kdtv_rope_table tab,
+                                                             const __grid_constant__ KvArgs a) {
+  const KvPart& part = a.part[blockIdx.z];
+  const int b = blockIdx.y;
+  const int n = live_rows(a.n_live, b, a.N);
+  if (n == 0) return;
+  const int L = a.prefix_len ? a.prefix_len[b] : 0;
+  if (!rows_ok(a, b, L, n)) return;
+  const int group = part.group, lane = threadIdx.x % group;
+  const long long u = ((long long)blockIdx.x * kThreads + threadIdx.x) / group;
+  const int hg = (int)(u % a.hgroups);
+  const long long i = u / a.hgroups;
+  const bool live = i < n;                     // dead lanes stay for the shuffles
+  const int ii = live ? (int)i : 0;
+  const int per = (part.heads + a.hgroups - 1) / a.hgroups;
+  const int h0 = hg * per, h1 = min(h0 + per, part.heads);
+  const long long row = row_of(a, b, L + ii);
+  const S* src = static_cast<const S*>(part.src) + b * part.ss[0] + ii * part.ss[1];
+  const bool half = tab.layout == KDTV_ROPE_HALF;
+
+  // this lane's angles; mate: distance to the rotation partner (half layout)
+  float2 cs[P][V];
+  int mate[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    mate[p] = 0;
+    const int r0 = (p * group + lane) * V - part.rot_off;     // first element, in the rotated part
+    if (part.rotate && live && r0 >= 0 && r0 < tab.rot_dim) {
+      const long long pos = (long long)L + (a.depth ? a.depth[(long long)b * a.N + ii] : ii);
+      const int hd = tab.rot_dim / 2;
+      mate[p] = half ? (r0 < hd ? hd : -hd) : ((r0 & 1) ? -1 : 1);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (half) cs[p][k] = rope_cos_sin(tab.turn[(r0 < hd ? r0 : r0 - hd) + k], pos, tab.amp);
+        else if (V == 1 || (k & 1) == 0) cs[p][k] = rope_cos_sin(tab.turn[(r0 + k) / 2], pos, tab.amp);
+        else cs[p][k] = cs[p][k - 1];
+      }
+    }
+  }
+
+  for (int h = h0; h < h0 + per; ++h) {
+    const bool on = live && h < h1;
+    float x[P][V];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int e = (p * group + lane) * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[p][k] = 0.f;
+      if (!on || e >= part.dim) continue;
+      const S* s = src + h * part.ss[2] + e;
+      load_v<V>(s, x[p]);
+      if (mate[p] == 0) continue;
+      if (half || V == 1) {
+        float m[V];
+        load_v<V>(s + mate[p], m);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          x[p][k] = mate[p] > 0 ? x[p][k] * cs[p][k].x - m[k] * cs[p][k].y
+                                : x[p][k] * cs[p][k].x + m[k] * cs[p][k].y;
+      } else {
+#pragma unroll
+        for (int k = 0; k + 1 < V; k += 2) {
+          const float u0 = x[p][k], v0 = x[p][k + 1];
+          x[p][k] = u0 * cs[p][k].x - v0 * cs[p][k].y;
+          x[p][k + 1] = v0 * cs[p][k].x + u0 * cs[p][k].y;
+        }
+      }
+    }
+    D* dst = static_cast<D*>(part.cache) + (row * part.heads + h) * part.dim;
+    if constexpr (sizeof(D) == 1) {
+      if (part.scale) {
+        // The smallest e with max <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of
+        // the largest finite magnitude.  2^-e is a power of two, so x * 2^-e loses
+        // nothing; a power also makes a code's value exact in bf16.
+        float m = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const float f = fabsf(x[p][k]);
+            m = f < INFINITY ? fmaxf(m, f) : m;
+          }
+        for (int o = group / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t bits = __float_as_uint(m);
+        int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+        e = max(-117, min(119, e));
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int k = 0; k < V; ++k) x[p][k] *= f;
+        if (on && lane == 0) part.scale[row * part.heads + h] = (uint8_t)(e + 127);
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int k = 0; k < V; ++k) x[p][k] = __fdiv_rn(x[p][k], a.kv_scale);
+      }
+    }
+    if (on)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int e = (p * group + lane) * V;
+        if (e < part.dim) store_v<V>(dst + e, x[p]);
+      }
+  }
+}
+
+// Thread = kRows vectors of V elements, a block apart, of one part's rows
+// (rows of a part are contiguous in the cache and in out).
+template <typename C, typename O, int V>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvArgs a) {
+  constexpr int kRows = 4;
+  const KvPart& part = a.part[blockIdx.z];
+  const int b = blockIdx.y;
+  const int n = live_rows(a.n_live, b, a.N);
+  if (n == 0) return;
+  const int L = a.prefix_len ? a.prefix_len[b] : 0;
+  if (!rows_ok(a, b, L, n)) return;
+  const int width = part.heads * part.dim, vecs = width / V;
+  const unsigned total = (unsigned)n * (unsigned)vecs;            // < 2^32 (host)
+  const C* cache = static_cast<const C*>(part.cache);
+  O* out = static_cast<O*>(part.out) + (long long)b * a.N * width;
+  float x[kRows][V], s[kRows];
+  const unsigned t0 = blockIdx.x * (unsigned)(kThreads * kRows) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const unsigned t = t0 + k * kThreads;
+    if (t >= total) continue;
+    const int i = (int)(t / (unsigned)vecs), c = (int)(t % (unsigned)vecs) * V;
+    const long long row = row_of(a, b, L + i);
+    load_v<V>(cache + row * width + c, x[k]);
+    s[k] = 1.f;
+    if constexpr (sizeof(C) == 1)
+      s[k] = part.scale ? scale_of_byte(part.scale[row * part.heads + c / part.dim]) : a.kv_scale;
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const unsigned t = t0 + k * kThreads;
+    if (t >= total) continue;
+    if constexpr (sizeof(C) == 1)
+#pragma unroll
+      for (int m = 0; m < V; ++m) x[k][m] *= s[k];
+    store_v<V>(out + (long long)t * V, x[k]);
+  }
+}
+
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool multiple(const long long (&s)[3], int v) { return s[0] % v == 0 && s[1] % v == 0 && s[2] % v == 0; }
+// Element strides; {0, 0, 0} is contiguous.
+void strides(const int64_t (&in)[3], long long N, long long H, long long dim, long long (&out)[3]) {
+  const bool given = in[0] || in[1] || in[2];
+  out[0] = given ? in[0] : N * H * dim;
+  out[1] = given ? in[1] : H * dim;
+  out[2] = given ? in[2] : dim;
+}
+
+template <typename T>
+int launch_rope(const kdtv_rope_table& tab, RopeArgs& a, int dim, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const bool half = tab.layout == KDTV_ROPE_HALF;
+  // 16-byte accesses where every address that they would have is a multiple of 16.
+  bool vec = aligned(a.x, 16) && aligned(a.y, 16) && aligned(a.rest, 16) && multiple(a.xs, V) &&
+             multiple(a.ys, V) && (!a.rest || multiple(a.rs, V)) && dim % V == 0 &&
+             a.rot_off % V == 0 && (half ? a.rot / 2 : a.rot) % V == 0;
+  const int v = vec ? V : 1;
+  a.rot_items = half || !vec ? a.rot / 2 / v : a.rot / v;
+  const bool in_place = a.x == a.y && !a.rest;
+  a.items = a.rot_items + (in_place ? 0 : (dim - a.rot) / v);
+  // Heads per thread: an item's angles cost about as much as four heads' moves,
+  // but threads come first.
+  const long long threads = (long long)a.rows * a.items * a.H;
+  a.heads = 1;
+  while (a.heads < 8 && a.heads < a.H && threads / (2 * a.heads) >= 152ll * 1024) a.heads *= 2;
+  a.hgroups = (a.H + a.heads - 1) / a.heads;
+  const long long blocks = ((long long)a.rows * a.hgroups * a.items + kThreads - 1) / kThreads;
+  if (blocks > (1ll << 32) / kThreads - 1) return KDTV_ERR_UNSUPPORTED;   // 32-bit thread indices
+  auto kern = vec ? (half ? rope_kernel<T, V, true> : rope_kernel<T, V, false>)
+                  : (half ? rope_kernel<T, 1, true> : rope_kernel<T, 1, false>);
+  kern<<<(unsigned)blocks, kThreads, 0, st>>>(tab, a);
+  return cudaGetLastError() == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+}
+
+template <typename S, typename D>
+cudaError_t launch_append(const kdtv_rope_table& tab, KvArgs& a, cudaStream_t st) {
+  bool vec = true, wide = false;
+  int heads = 1;
+  for (int k = 0; k < a.parts; ++k) {
+    const KvPart& p = a.part[k];
+    vec = vec && aligned(p.src, 16) && aligned(p.cache, 16) && p.dim % 8 == 0 && multiple(p.ss, 8) &&
+          (!p.rotate || (p.rot_off % 8 == 0 &&
+                         (tab.layout == KDTV_ROPE_HALF ? tab.rot_dim / 2 : tab.rot_dim) % 8 == 0));
+    wide = wide || p.dim > 256;
+    heads = p.heads > heads ? p.heads : heads;
+  }
+  int lanes = 1;
+  for (int k = 0; k < a.parts; ++k) {
+    KvPart& p = a.part[k];
+    p.group = 32;
+    if (vec)
+      while (p.group > 1 && p.group / 2 * 8 >= p.dim) p.group /= 2;
+    lanes = p.group > lanes ? p.group : lanes;
+  }
+  // Groups of heads per row: one thread's heads share its angles, but a few
+  // rows are spread over more threads.
+  a.hgroups = 1;
+  while (2 * a.hgroups <= heads && (long long)a.B * a.N * a.hgroups * lanes < 152ll * 1024) a.hgroups *= 2;
+  const long long bx = ((long long)a.N * a.hgroups * lanes + kThreads - 1) / kThreads;
+  const dim3 grid((unsigned)bx, (unsigned)a.B, (unsigned)a.parts);
+  auto kern = !vec ? kv_append_kernel<S, D, 1, 16>
+                   : (wide ? kv_append_kernel<S, D, 8, 2> : kv_append_kernel<S, D, 8, 1>);
+  kern<<<grid, kThreads, 0, st>>>(tab, a);
+  return cudaGetLastError();
+}
+
+template <typename C, typename O>
+cudaError_t launch_read(KvArgs& a, cudaStream_t st) {
+  bool vec = true;
+  long long vecs = 1;
+  for (int k = 0; k < a.parts; ++k) {
+    const KvPart& p = a.part[k];
+    vec = vec && aligned(p.cache, 16) && aligned(p.out, 16) && p.dim % 8 == 0;
+    const long long w = (long long)p.heads * p.dim;
+    vecs = w > vecs ? w : vecs;
+  }
+  const long long per_block = (vec ? 8 : 1) * 4ll * kThreads;
+  const long long bx = (a.N * vecs + per_block - 1) / per_block;
+  const dim3 grid((unsigned)bx, (unsigned)a.B, (unsigned)a.parts);
+  auto kern = vec ? kv_read_kernel<C, O, 8> : kv_read_kernel<C, O, 1>;
+  kern<<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+// Host checks that append and read share.
+int kv_args(const kdtv_kv_dims* d, const kdtv_kv_part* parts, const int32_t* page_table,
+            unsigned int* status, KvArgs* a) {
+  if (!d || !parts || !status) return KDTV_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->N <= 0 || d->parts < 1 || d->parts > 2) return KDTV_ERR_INVALID_ARG;
+  if (d->dtype != KDTV_F32 && d->dtype != KDTV_BF16) return KDTV_ERR_INVALID_ARG;
+  if (d->cache_dtype != KDTV_F32 && d->cache_dtype != KDTV_BF16 && d->cache_dtype != KDTV_BF16_FP8KV)
+    return KDTV_ERR_INVALID_ARG;
+  if (d->page_size < 0 || (d->page_size > 0) != (page_table != nullptr)) return KDTV_ERR_INVALID_ARG;
+  if (d->page_size == 0 ? d->t_stride <= 0 : (d->max_pages <= 0 || d->num_pages <= 0))
+    return KDTV_ERR_INVALID_ARG;
+  if (d->page_size > 0 && (long long)d->max_pages * d->page_size > (1ll << 30)) return KDTV_ERR_INVALID_ARG;
+  if (d->B > 65535) return KDTV_ERR_UNSUPPORTED;      // one grid row each
+  memset(a, 0, sizeof(*a));
+  for (int k = 0; k < d->parts; ++k) {
+    const kdtv_kv_part& p = parts[k];
+    if (!p.cache || p.heads <= 0 || p.dim <= 0) return KDTV_ERR_INVALID_ARG;
+    if (p.scale && d->cache_dtype != KDTV_BF16_FP8KV) return KDTV_ERR_INVALID_ARG;
+    if (p.dim > 512 || p.heads > (1 << 16) || (long long)d->N * p.heads * p.dim > (1ll << 31))
+      return KDTV_ERR_UNSUPPORTED;                      // 32-bit indices within a request's rows
+    KvPart& o = a->part[k];
+    o.cache = p.cache; o.scale = p.scale; o.src = p.src; o.out = p.out;
+    o.heads = p.heads; o.dim = p.dim; o.rotate = p.rotate != 0; o.rot_off = p.rot_off;
+    strides(p.src_stride, d->N, p.heads, p.dim, o.ss);
+  }
+  a->B = d->B; a->N = d->N; a->page_size = d->page_size; a->t_stride = d->t_stride;
+  a->max_pages = d->max_pages; a->num_pages = d->num_pages; a->parts = d->parts;
+  a->kv_scale = d->kv_scale > 0.f ? d->kv_scale : 1.f;
+  a->page_table = page_table;
+  a->status = status;
+  return KDTV_OK;
+}
+
+bool table_ok(const kdtv_rope_table* t) {
+  return t && t->rot_dim >= 2 && t->rot_dim <= KDTV_ROPE_MAX_DIM && t->rot_dim % 2 == 0 &&
+         (t->layout == KDTV_ROPE_HALF || t->layout == KDTV_ROPE_INTERLEAVED);
+}
+
+}  // namespace
+}  // namespace kdtv
+
+using namespace kdtv;
+
+extern "C" int kdtv_rope_init(const kdtv_rope_config* c, kdtv_rope_table* t) {
+  if (!c || !t) return KDTV_ERR_INVALID_ARG;
+  if (c->rot_dim < 2 || c->rot_dim % 2) return KDTV_ERR_INVALID_ARG;
+  if (c->rot_dim > KDTV_ROPE_MAX_DIM) return KDTV_ERR_UNSUPPORTED;
+  if (c->layout != KDTV_ROPE_HALF && c->layout != KDTV_ROPE_INTERLEAVED) return KDTV_ERR_INVALID_ARG;
+  if (c->scaling < KDTV_ROPE_PLAIN || c->scaling > KDTV_ROPE_YARN) return KDTV_ERR_INVALID_ARG;
+  if (!(c->base > 1.0) || !isfinite(c->base)) return KDTV_ERR_INVALID_ARG;
+  if (c->scaling != KDTV_ROPE_PLAIN && (!(c->factor >= 1.0) || !isfinite(c->factor)))
+    return KDTV_ERR_INVALID_ARG;
+  const int r = c->rot_dim;
+  double base = c->base, amp = 1.0, lo = 0.0, hi = 0.0;
+  if (c->scaling == KDTV_ROPE_NTK) {
+    if (r < 4) return KDTV_ERR_INVALID_ARG;
+    base *= pow(c->factor, r / (r - 2.0));
+    if (!isfinite(base)) return KDTV_ERR_INVALID_ARG;
+  }
+  if (c->scaling == KDTV_ROPE_YARN) {
+    if (c->orig_ctx <= 0) return KDTV_ERR_INVALID_ARG;
+    const double fast = c->beta_fast > 0.0 ? c->beta_fast : 32.0;
+    const double slow = c->beta_slow > 0.0 ? c->beta_slow : 1.0;
+    if (!(slow <= fast) || !isfinite(fast)) return KDTV_ERR_INVALID_ARG;
+    // Pair j turns orig_ctx f_j / 2 pi times over the original context; the
+    // pairs at which that is `fast` and `slow` bound the ramp.
+    const double two_pi = 6.283185307179586;
+    lo = floor(r * log(c->orig_ctx / (fast * two_pi)) / (2.0 * log(base)));
+    hi = ceil(r * log(c->orig_ctx / (slow * two_pi)) / (2.0 * log(base)));
+    lo = lo > 0.0 ? lo : 0.0;
+    hi = hi < r - 1.0 ? hi : r - 1.0;
+    amp = c->attn_factor > 0.0 ? c->attn_factor : 0.1 * log(c->factor) + 1.0;
+    if (!isfinite(amp)) return KDTV_ERR_INVALID_ARG;
+  }
+  memset(t, 0, sizeof(*t));
+  t->rot_dim = r;
+  t->layout = c->layout;
+  t->amp = (float)amp;
+  for (int j = 0; j < r / 2; ++j) {
+    double f = pow(base, -2.0 * j / r);
+    if (c->scaling == KDTV_ROPE_LINEAR) f /= c->factor;
+    if (c->scaling == KDTV_ROPE_YARN) {
+      const double span = hi - lo > 0.001 ? hi - lo : 0.001;
+      double ramp = (j - lo) / span;
+      ramp = ramp < 0.0 ? 0.0 : (ramp > 1.0 ? 1.0 : ramp);
+      f = f / c->factor * ramp + f * (1.0 - ramp);
+    }
+    // f / 2 pi < 1/6 in two doubles (1 / 2 pi is known to 2^-109), then in 2^-64 turns.
+    const double inv_hi = 0.15915494309189535, inv_lo = -9.839338337591243e-18;
+    const double hi_t = f * inv_hi, lo_t = fma(f, inv_hi, -hi_t) + f * inv_lo;
+    t->turn[j] = (uint64_t)(hi_t * 0x1p64) + (uint64_t)(int64_t)llrint(lo_t * 0x1p64);
+  }
+  return KDTV_OK;
+}
+
+extern "C" int kdtv_rope(const kdtv_rope_table* t, const kdtv_rope_args* d, const void* x, void* y,
+                         void* rest, const int32_t* prefix_len, const int32_t* depth,
+                         const int32_t* n_live, cudaStream_t stream) {
+  if (!table_ok(t) || !d || !x || !y) return KDTV_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->N <= 0 || d->H <= 0 || d->dim <= 0 || d->rot_off < 0 ||
+      (long long)d->rot_off + t->rot_dim > d->dim)
+    return KDTV_ERR_INVALID_ARG;
+  if (d->dtype != KDTV_F32 && d->dtype != KDTV_BF16) return KDTV_ERR_INVALID_ARG;
+  if (rest && (rest == x || rest == y || x == y)) return KDTV_ERR_INVALID_ARG;
+  if (d->dim > 65536 || d->H > 65536 || (long long)d->B * d->N > 0x7fffffffll) return KDTV_ERR_UNSUPPORTED;
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.N = d->N; a.H = d->H; a.rot_off = d->rot_off; a.rot = t->rot_dim;
+  a.rows = (unsigned)((long long)d->B * d->N);
+  a.x = x; a.y = y; a.rest = rest;
+  a.prefix_len = prefix_len; a.depth = depth; a.n_live = n_live;
+  strides(d->x_stride, d->N, d->H, d->dim, a.xs);
+  strides(d->y_stride, d->N, d->H, rest ? t->rot_dim : d->dim, a.ys);
+  strides(d->rest_stride, d->N, d->H, d->dim - t->rot_dim, a.rs);
+  // in place is element by element: another stride would overwrite what is still to be read
+  if (x == y && (a.xs[0] != a.ys[0] || a.xs[1] != a.ys[1] || a.xs[2] != a.ys[2])) return KDTV_ERR_INVALID_ARG;
+  return d->dtype == KDTV_BF16 ? launch_rope<__nv_bfloat16>(*t, a, d->dim, stream)
+                               : launch_rope<float>(*t, a, d->dim, stream);
+}
+
+extern "C" int kdtv_kv_append(const kdtv_kv_dims* d, const kdtv_kv_part* parts,
+                              const kdtv_rope_table* rope, const int32_t* prefix_len,
+                              const int32_t* depth, const int32_t* n_live,
+                              const int32_t* page_table, unsigned int* status,
+                              cudaStream_t stream) {
+  KvArgs a;
+  const int rc = kv_args(d, parts, page_table, status, &a);
+  if (rc != KDTV_OK) return rc;
+  kdtv_rope_table tab;
+  memset(&tab, 0, sizeof(tab));
+  for (int k = 0; k < a.parts; ++k) {
+    const KvPart& p = a.part[k];
+    if (!p.src) return KDTV_ERR_INVALID_ARG;
+    if (!p.rotate) continue;
+    if (!table_ok(rope) || p.rot_off < 0 || (long long)p.rot_off + rope->rot_dim > p.dim)
+      return KDTV_ERR_INVALID_ARG;
+    tab = *rope;
+  }
+  a.prefix_len = prefix_len; a.depth = depth; a.n_live = n_live;
+  const bool f32 = d->dtype == KDTV_F32;
+  cudaError_t e;
+  if (d->cache_dtype == KDTV_F32)
+    e = f32 ? launch_append<float, float>(tab, a, stream) : launch_append<__nv_bfloat16, float>(tab, a, stream);
+  else if (d->cache_dtype == KDTV_BF16)
+    e = f32 ? launch_append<float, __nv_bfloat16>(tab, a, stream)
+            : launch_append<__nv_bfloat16, __nv_bfloat16>(tab, a, stream);
+  else
+    e = f32 ? launch_append<float, __nv_fp8_e4m3>(tab, a, stream)
+            : launch_append<__nv_bfloat16, __nv_fp8_e4m3>(tab, a, stream);
+  return e == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+}
+
+extern "C" int kdtv_kv_read(const kdtv_kv_dims* d, const kdtv_kv_part* parts, const int32_t* start,
+                            const int32_t* n_live, const int32_t* page_table,
+                            unsigned int* status, cudaStream_t stream) {
+  KvArgs a;
+  const int rc = kv_args(d, parts, page_table, status, &a);
+  if (rc != KDTV_OK) return rc;
+  for (int k = 0; k < a.parts; ++k)
+    if (!a.part[k].out) return KDTV_ERR_INVALID_ARG;
+  a.prefix_len = start; a.n_live = n_live;
+  const bool f32 = d->dtype == KDTV_F32;
+  cudaError_t e;
+  if (d->cache_dtype == KDTV_F32)
+    e = f32 ? launch_read<float, float>(a, stream) : launch_read<float, __nv_bfloat16>(a, stream);
+  else if (d->cache_dtype == KDTV_BF16)
+    e = f32 ? launch_read<__nv_bfloat16, float>(a, stream)
+            : launch_read<__nv_bfloat16, __nv_bfloat16>(a, stream);
+  else
+    e = f32 ? launch_read<__nv_fp8_e4m3, float>(a, stream)
+            : launch_read<__nv_fp8_e4m3, __nv_bfloat16>(a, stream);
+  return e == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+}

@@ -283,21 +283,33 @@ extern "C" int kdtv_compact_kv(const kdtv_dims* d, void* c_kv, void* k_rope,
   if ((d->page_size > 0) != (page_table != nullptr)) return KDTV_ERR_INVALID_ARG;
   if (d->page_size == 0 && d->t_stride < d->N) return KDTV_ERR_INVALID_ARG;
   if (d->page_size > 0 && (d->max_pages <= 0 || d->num_pages <= 0)) return KDTV_ERR_INVALID_ARG;
-  const int W = d->d_c + d->d_rope;
+  const long long W = (long long)d->d_c + d->d_rope;
+  // A chunk of rows in shared memory: over 47 KiB (a GQA cache's keys and
+  // values as the two tensors) by opt-in, up to what a CTA can have.
+  const auto opt_in = [](auto kern, size_t bytes) -> int {
+    if (bytes <= 47 * 1024) return KDTV_OK;
+    if (bytes > 227 * 1024 - 1024) return KDTV_ERR_UNSUPPORTED;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+                   cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+  };
+  int rc;
   if (d->dtype == KDTV_BF16) {
     const size_t sm = sizeof(__nv_bfloat16) * kRowsChunk * W;
+    if ((rc = opt_in(compact_kernel<__nv_bfloat16>, sm)) != KDTV_OK) return rc;
     compact_kernel<__nv_bfloat16><<<d->B, kCompactThreads, sm, stream>>>(
         d->N, d->d_c, d->d_rope, d->page_size, d->t_stride, d->max_pages, d->num_pages,
         static_cast<__nv_bfloat16*>(c_kv), static_cast<__nv_bfloat16*>(k_rope), prefix_len, path,
         path_len, page_table, status);
   } else if (d->dtype == KDTV_BF16_FP8KV) {   // one-byte cache elements, moved as bytes
     const size_t sm = sizeof(unsigned char) * kRowsChunk * W;
+    if ((rc = opt_in(compact_kernel<unsigned char>, sm)) != KDTV_OK) return rc;
     compact_kernel<unsigned char><<<d->B, kCompactThreads, sm, stream>>>(
         d->N, d->d_c, d->d_rope, d->page_size, d->t_stride, d->max_pages, d->num_pages,
         static_cast<unsigned char*>(c_kv), static_cast<unsigned char*>(k_rope), prefix_len, path,
         path_len, page_table, status);
   } else if (d->dtype == KDTV_F32) {
     const size_t sm = sizeof(float) * kRowsChunk * W;
+    if ((rc = opt_in(compact_kernel<float>, sm)) != KDTV_OK) return rc;
     compact_kernel<float><<<d->B, kCompactThreads, sm, stream>>>(
         d->N, d->d_c, d->d_rope, d->page_size, d->t_stride, d->max_pages, d->num_pages,
         static_cast<float*>(c_kv), static_cast<float*>(k_rope), prefix_len, path, path_len,

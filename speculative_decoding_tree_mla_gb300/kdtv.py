@@ -26,7 +26,8 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 # Every symbol include/kdtv.h declares (checked by the CPU tests).
 EXPORTS = ("kdtv_workspace_size", "kdtv_verify_attn", "kdtv_get_device_status",
            "kdtv_strerror", "kdtv_launches_per_call", "kdtv_tree_accept", "kdtv_compact_kv",
-           "kdtv_tree_build", "kdtv_verify_attn_noalloc")
+           "kdtv_tree_build", "kdtv_verify_attn_noalloc", "kdtv_rope_init", "kdtv_rope",
+           "kdtv_kv_append", "kdtv_kv_read")
 
 
 class KdtvDims(ctypes.Structure):
@@ -41,6 +42,48 @@ class KdtvDims(ctypes.Structure):
         ("kv_scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t), ("phase_events", ctypes.c_void_p),
     ]
+
+
+ROPE_MAX_DIM = 256
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class KdtvRopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("orig_ctx", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attn_factor", ctypes.c_double)]
+
+
+class KdtvRopeTable(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("amp", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turn", ctypes.c_uint64 * (ROPE_MAX_DIM // 2))]
+
+
+class KdtvRopeArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("rot_off", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64 * 3),
+                ("y_stride", ctypes.c_int64 * 3), ("rest_stride", ctypes.c_int64 * 3)]
+
+
+class KdtvKvPart(ctypes.Structure):
+    _fields_ = [("cache", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("src", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("src_stride", ctypes.c_int64 * 3), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("rotate", ctypes.c_int32),
+                ("rot_off", ctypes.c_int32)]
+
+
+class KdtvKvDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("t_stride", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("kv_scale", ctypes.c_float),
+                ("parts", ctypes.c_int32)]
 
 
 class KdtvError(RuntimeError):
@@ -81,6 +124,15 @@ def lib():
         L.kdtv_tree_build.restype = ctypes.c_int
         L.kdtv_verify_attn_noalloc.argtypes = [P] + [vp] * 11 + [vp]
         L.kdtv_verify_attn_noalloc.restype = ctypes.c_int
+        L.kdtv_rope_init.argtypes = [ctypes.POINTER(KdtvRopeConfig), ctypes.POINTER(KdtvRopeTable)]
+        L.kdtv_rope_init.restype = ctypes.c_int
+        L.kdtv_rope.argtypes = [ctypes.POINTER(KdtvRopeTable), ctypes.POINTER(KdtvRopeArgs)] + [vp] * 6 + [vp]
+        L.kdtv_rope.restype = ctypes.c_int
+        KP = [ctypes.POINTER(KdtvKvDims), ctypes.POINTER(KdtvKvPart)]
+        L.kdtv_kv_append.argtypes = KP + [ctypes.POINTER(KdtvRopeTable)] + [vp] * 5 + [vp]
+        L.kdtv_kv_append.restype = ctypes.c_int
+        L.kdtv_kv_read.argtypes = KP + [vp] * 4 + [vp]
+        L.kdtv_kv_read.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -262,3 +314,241 @@ def tree_build(logp, tokens, root_token, n_nodes, stream=None):
     if code:
         raise KdtvError(code, "kdtv_tree_build")
     return out
+
+
+# ---- rotary positions, cache writes and reads -----------------------------------------
+# Each caller below binds its tensors once, as VerifyAttn does, checks them, and launches on
+# their device when called; the functions of the same names in lower case bind and call.
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _index(t, shape, device, name):
+    """An int32 index tensor of one of the calls (None passes)."""
+    import torch
+    if t is None:
+        return None
+    _need(t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous()
+          and t.device == device, f"{name}: contiguous int32 {list(shape)} on {device}")
+    return t
+
+
+class _Bound:
+    """A library call over bound tensors, launched on their device."""
+
+    def _bind(self, name, device, args, keep):
+        import torch
+        self.torch, self._name, self.device = torch, name, device
+        self._fn, self._args, self._keep = getattr(lib(), name), tuple(args), keep
+
+    def _launch(self, stream):
+        torch = self.torch
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if torch.cuda.current_device() == self.device.index:
+            code = self._fn(*self._args, s.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                code = self._fn(*self._args, s.cuda_stream)
+        if code:
+            raise KdtvError(code, self._name)
+
+
+def _on(stream):
+    """What a call allocates belongs to the stream that it runs on."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+class RopeTable:
+    """Rotary frequencies (kdtv_rope_init): `rot_dim` rotated elements per head, pairs
+    (j, j + rot_dim / 2) ("half") or (2j, 2j + 1) ("interleaved"); `scaling` "none", "linear",
+    "ntk" or "yarn" for long contexts."""
+
+    def __init__(self, rot_dim, *, layout="half", base=10000.0, scaling="none", factor=1.0,
+                 orig_ctx=0, beta_fast=0.0, beta_slow=0.0, attn_factor=0.0):
+        _need(layout in ROPE_LAYOUT, f"layout: one of {list(ROPE_LAYOUT)}")
+        _need(scaling in ROPE_SCALING, f"scaling: one of {list(ROPE_SCALING)}")
+        c = KdtvRopeConfig(rot_dim, ROPE_LAYOUT[layout], ROPE_SCALING[scaling], orig_ctx, base,
+                           factor, beta_fast, beta_slow, attn_factor)
+        self.c = KdtvRopeTable()
+        code = lib().kdtv_rope_init(ctypes.byref(c), ctypes.byref(self.c))
+        if code:
+            raise KdtvError(code, "kdtv_rope_init")
+        self.rot_dim, self.layout, self.amp = rot_dim, layout, self.c.amp
+
+
+class Rope(_Bound):
+    """Caller of kdtv_rope.  x: [B, N, H, dim], last dimension contiguous, float32 or bfloat16.
+
+    Without `split`, out is like x with elements rot_off .. rot_off + rot_dim of every head
+    rotated (out=x: in place).  With `split` (or a `rest` tensor), out holds the rotated part
+    alone and rest the other elements: what VerifyAttn takes as q_rope and q_nope.
+    """
+
+    def __init__(self, table, x, *, prefix_len=None, depth=None, n_live=None, rot_off=0, out=None,
+                 rest=None, split=False):
+        import torch
+        _need(isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 4 and x.numel() > 0
+              and x.dtype in (torch.float32, torch.bfloat16) and x.stride(3) == 1,
+              "x: a float32 or bfloat16 CUDA tensor [B, N, H, dim] with a contiguous last dimension")
+        B, N, H, dim = x.shape
+        split = split or rest is not None
+        _need(0 <= rot_off and rot_off + table.rot_dim <= dim, "the rotated part lies outside the head")
+
+        def result(t, d, name):
+            if t is None:
+                return torch.empty((B, N, H, d), dtype=x.dtype, device=x.device)
+            _need(tuple(t.shape) == (B, N, H, d) and t.dtype == x.dtype and t.device == x.device
+                  and (d == 0 or t.stride(3) == 1), f"{name}: {[B, N, H, d]} like x")
+            return t
+
+        self.out = result(out, table.rot_dim if split else dim, "out")
+        self.rest = result(rest, dim - table.rot_dim, "rest") if split else None
+        # a head that is rotated whole has nothing left to copy: plain rotation
+        copied = self.rest if self.rest is not None and self.rest.numel() else None
+        a = KdtvRopeArgs(B, N, H, dim, rot_off, KDTV_F32 if x.dtype == torch.float32 else KDTV_BF16)
+        for name, t in (("x_stride", x), ("y_stride", self.out), ("rest_stride", copied)):
+            if t is not None:
+                setattr(a, name, (ctypes.c_int64 * 3)(*t.stride()[:3]))
+        pl = _index(prefix_len, (B,), x.device, "prefix_len")
+        dp = _index(depth, (B, N), x.device, "depth")
+        nl = _index(n_live, (B,), x.device, "n_live")
+        self._bind("kdtv_rope", x.device,
+                   (ctypes.byref(table.c), ctypes.byref(a), _p(x), _p(self.out), _p(copied), _p(pl),
+                    _p(dp), _p(nl)), (table, a, x, self.out, self.rest, pl, dp, nl))
+
+    def __call__(self, stream=None):
+        self._launch(stream)
+        return self.out if self.rest is None else (self.out, self.rest)
+
+
+def rope(table, x, *, stream=None, **kw):
+    """Rotates x (see Rope); returns out, or (out, rest) when split.  Rows that are not live
+    are left as they were in a given out, and undefined in a new one."""
+    with _on(stream):
+        return Rope(table, x, **kw)(stream)
+
+
+class KvPart:
+    """One tensor of a cache: [B, T, heads, dim] or [num_pages, page_size, heads, dim] (or
+    without `heads`), float32, bfloat16, or one byte per element (uint8 or float8_e4m3fn);
+    `scale`, for one-byte caches: exponent bytes, the cache's shape without dim, uint8.
+
+    append: `src` [B, N, heads, dim] (last dimension contiguous), rotated from `rot_off` on
+    unless that is None.  read: `out` [B, N, heads, dim], contiguous.
+    """
+
+    def __init__(self, cache, *, src=None, out=None, scale=None, rot_off=None):
+        self.cache, self.src, self.out, self.scale, self.rot_off = cache, src, out, scale, rot_off
+
+
+def _kv_setup(parts, which, page_table, kv_scale):
+    """kdtv_kv_dims and kdtv_kv_part[] of KvPart objects; the rows come from their `which`."""
+    import torch
+    _need(1 <= len(parts) <= 2, "one or two parts")
+    one_byte = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+    d, cp, first, keep = KdtvKvDims(), (KdtvKvPart * len(parts))(), None, [page_table]
+    for k, part in enumerate(parts):
+        x, cache, scale = getattr(part, which), part.cache, part.scale
+        _need(isinstance(x, torch.Tensor) and isinstance(cache, torch.Tensor) and x.is_cuda
+              and cache.device == x.device, f"cache and {which}: CUDA tensors of one device")
+        if cache.dim() == 3:
+            cache = cache.unsqueeze(2)
+            scale = scale.unsqueeze(2) if scale is not None and scale.dim() == 2 else scale
+        if x.dim() == 3:
+            x = x.unsqueeze(2)
+        _need(x.dim() == 4 and cache.dim() == 4 and x.numel() > 0 and cache.numel() > 0
+              and x.shape[2:] == cache.shape[2:], f"{which}: [B, N, heads, dim] with the cache's heads and dim")
+        _need(cache.is_contiguous(), "cache: contiguous")
+        _need(x.dtype in (torch.float32, torch.bfloat16), f"{which}: float32 or bfloat16")
+        _need(x.stride(3) == 1 if which == "src" else x.is_contiguous(),
+              f"{which}: " + ("last dimension contiguous" if which == "src" else "contiguous"))
+        _need(cache.dtype in (torch.float32, torch.bfloat16) + one_byte,
+              "cache: float32, bfloat16, uint8 or float8_e4m3fn")
+        if scale is not None:
+            _need(cache.dtype in one_byte and scale.dtype == torch.uint8 and scale.is_contiguous()
+                  and scale.device == x.device and scale.shape == cache.shape[:3],
+                  "scale: contiguous uint8, one byte per row and head of a one-byte cache")
+        kind = (x.shape[:2], x.dtype, x.device, cache.dtype in one_byte or cache.dtype, cache.shape[:2])
+        first = first or kind
+        _need(kind == first, "the parts differ in rows, types or cache extent")
+        cp[k].cache, cp[k].scale = _p(cache), _p(scale)
+        setattr(cp[k], which, _p(x))
+        if which == "src":
+            cp[k].src_stride = (ctypes.c_int64 * 3)(*x.stride()[:3])
+            cp[k].rotate, cp[k].rot_off = part.rot_off is not None, part.rot_off or 0
+        cp[k].heads, cp[k].dim = x.shape[2], x.shape[3]
+        keep += [x, cache, scale]
+    (B, N), dtype, device, cdtype, extent = first
+    d.B, d.N, d.parts, d.kv_scale = B, N, len(parts), kv_scale
+    d.dtype = KDTV_F32 if dtype == torch.float32 else KDTV_BF16
+    d.cache_dtype = KDTV_BF16_FP8KV if cdtype is True else KDTV_F32 if cdtype == torch.float32 else KDTV_BF16
+    if page_table is None:
+        _need(extent[0] == B, "a contiguous cache has one row block per request")
+        d.t_stride = extent[1]
+    else:
+        _need(page_table.dim() == 2, "page_table: [B, max_pages]")
+        _index(page_table, (B, page_table.shape[1]), device, "page_table")
+        d.num_pages, d.page_size, d.max_pages = extent[0], extent[1], page_table.shape[1]
+    return d, cp, device, B, N, keep
+
+
+def _status_word(status, device):
+    import torch
+    if status is None:
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    return _index(status, (1,), device, "status")
+
+
+class KvAppend(_Bound):
+    """Caller of kdtv_kv_append: the live rows of every part's src, rotated and quantised, to
+    cache rows prefix_len[b] + i.  Calling it returns the status word (a tensor, 0 if all is
+    well; it keeps the first error until it is cleared)."""
+
+    def __init__(self, parts, prefix_len, *, rope=None, depth=None, n_live=None, page_table=None,
+                 kv_scale=0.0, status=None):
+        d, cp, device, B, N, keep = _kv_setup(parts, "src", page_table, kv_scale)
+        _need(rope is not None or all(p.rot_off is None for p in parts), "a part rotates: rope is missing")
+        pl = _index(prefix_len, (B,), device, "prefix_len")
+        dp = _index(depth, (B, N), device, "depth")
+        nl = _index(n_live, (B,), device, "n_live")
+        self.status = _status_word(status, device)
+        self._bind("kdtv_kv_append", device,
+                   (ctypes.byref(d), cp, ctypes.byref(rope.c) if rope is not None else None, _p(pl), _p(dp),
+                    _p(nl), _p(page_table), _p(self.status)), (d, cp, rope, pl, dp, nl, keep))
+
+    def __call__(self, stream=None):
+        self._launch(stream)
+        return self.status
+
+
+class KvRead(_Bound):
+    """Caller of kdtv_kv_read: cache rows start[b] .. start[b] + n_live[b] - 1 into every part's
+    out[b].  Calling it returns the status word."""
+
+    def __init__(self, parts, start=None, n_live=None, *, page_table=None, kv_scale=0.0, status=None):
+        d, cp, device, B, N, keep = _kv_setup(parts, "out", page_table, kv_scale)
+        st = _index(start, (B,), device, "start")
+        nl = _index(n_live, (B,), device, "n_live")
+        self.status = _status_word(status, device)
+        self._bind("kdtv_kv_read", device, (ctypes.byref(d), cp, _p(st), _p(nl), _p(page_table),
+                                            _p(self.status)), (d, cp, st, nl, keep))
+
+    def __call__(self, stream=None):
+        self._launch(stream)
+        return self.status
+
+
+def kv_append(parts, prefix_len, *, stream=None, **kw):
+    """Writes rows to a cache (see KvAppend); returns the status word."""
+    with _on(stream):
+        return KvAppend(parts, prefix_len, **kw)(stream)
+
+
+def kv_read(parts, start=None, n_live=None, *, stream=None, **kw):
+    """Reads rows of a cache (see KvRead); returns the status word."""
+    with _on(stream):
+        return KvRead(parts, start, n_live, **kw)(stream)
