@@ -408,6 +408,56 @@ int kdtv_kv_read(const kdtv_kv_dims* dims, const kdtv_kv_part* parts, const int3
                  const int32_t* n_live, const int32_t* page_table, unsigned int* status,
                  cudaStream_t stream);
 
+typedef struct kdtv_gqa_dims {
+  int32_t B, N;         /* requests, tree nodes per request (1..128)               */
+  int32_t H, H_kv;      /* query heads, key/value heads (H a multiple of H_kv;
+                           query head h reads key/value head h / (H / H_kv))       */
+  int32_t d;            /* head dim, <= 256                                        */
+  int32_t dtype;        /* enum kdtv_dtype: KDTV_F32 (everything fp32), KDTV_BF16,
+                           KDTV_BF16_FP8KV (q and out bf16, E4M3 cache with scale
+                           bytes)                                                  */
+  int32_t page_size;    /* 0: contiguous; > 0: rows per page                       */
+  int32_t t_stride, max_pages, num_pages;   /* as in kdtv_dims                     */
+  float scale;          /* softmax scale; <= 0 selects 1/sqrt(d)                   */
+  uint32_t flags;       /* KDTV_FLAG_SIMT, KDTV_FLAG_TEST_STALL                    */
+  void* workspace;      /* >= kdtv_gqa_workspace_size() bytes, 256-byte aligned    */
+  size_t workspace_bytes;
+} kdtv_gqa_dims;
+
+/* Bytes of workspace kdtv_gqa_verify_attn needs for these dims on the current
+ * device; 0 if the dims are invalid. */
+size_t kdtv_gqa_workspace_size(const kdtv_gqa_dims* dims);
+
+/* Kernels kdtv_gqa_verify_attn launches for these dims, or -1. */
+int kdtv_gqa_launches_per_call(const kdtv_gqa_dims* dims);
+
+/*
+ * kdtv_gqa_verify_attn — tree-verify attention over a cache of keys and values
+ * per head.  Node i of request b sees the prefix and its own root path:
+ *   out[b,i,h] = sum_t softmax_t(scale * q[b,i,h] . K[t]) V[t],  t in Vis(i)
+ * with K, V of head h / (H / H_kv); N = 1 is plain single-token decoding.
+ *   q, out     [B, N, H, d], contiguous, fp32 or bf16; 16-byte aligned
+ *   k, v       the caches, [B, t_stride, H_kv, d] or [num_pages, page_size,
+ *              H_kv, d]; 16-byte aligned
+ *   k_scale, v_scale  KDTV_BF16_FP8KV: [rows, H_kv] exponent bytes as
+ *              kdtv_kv_append writes them; else NULL
+ *   parent     [B, N] int32, as in kdtv_verify_attn, of the live nodes
+ *   prefix_len [B], n_nodes [B] int32 (n_nodes may be NULL: N)
+ * Rows of out behind n_nodes[b] are left as they were, and so are rows whose
+ * root path is malformed (KDTV_ERR_BAD_TREE) and requests with a bad prefix or
+ * page.  Cache rows at and behind prefix_len[b] + n_nodes[b] may hold
+ * anything; a key or value that a node does not see never reaches its output,
+ * not even as 0 * infinity.  *status: see above.
+ * bf16 and one-byte caches with d 64 or 128, H / H_kv <= 128 and page_size 0,
+ * 16, 32, 64 or 128 run on tensor cores, everything else (and
+ * KDTV_FLAG_SIMT) in fp32 on CUDA cores.
+ */
+int kdtv_gqa_verify_attn(const kdtv_gqa_dims* dims, const void* q, const void* k, const void* v,
+                         const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* parent,
+                         const int32_t* prefix_len, const int32_t* n_nodes,
+                         const int32_t* page_table, void* out, unsigned int* status,
+                         cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,8 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 EXPORTS = ("kdtv_workspace_size", "kdtv_verify_attn", "kdtv_get_device_status",
            "kdtv_strerror", "kdtv_launches_per_call", "kdtv_tree_accept", "kdtv_compact_kv",
            "kdtv_tree_build", "kdtv_verify_attn_noalloc", "kdtv_rope_init", "kdtv_rope",
-           "kdtv_kv_append", "kdtv_kv_read")
+           "kdtv_kv_append", "kdtv_kv_read", "kdtv_gqa_workspace_size",
+           "kdtv_gqa_launches_per_call", "kdtv_gqa_verify_attn")
 
 
 class KdtvDims(ctypes.Structure):
@@ -86,6 +87,15 @@ class KdtvKvDims(ctypes.Structure):
                 ("parts", ctypes.c_int32)]
 
 
+class KdtvGqaDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("t_stride", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 class KdtvError(RuntimeError):
     def __init__(self, code, what=""):
         self.code = code
@@ -133,6 +143,13 @@ def lib():
         L.kdtv_kv_append.restype = ctypes.c_int
         L.kdtv_kv_read.argtypes = KP + [vp] * 4 + [vp]
         L.kdtv_kv_read.restype = ctypes.c_int
+        G = ctypes.POINTER(KdtvGqaDims)
+        L.kdtv_gqa_workspace_size.argtypes = [G]
+        L.kdtv_gqa_workspace_size.restype = ctypes.c_size_t
+        L.kdtv_gqa_launches_per_call.argtypes = [G]
+        L.kdtv_gqa_launches_per_call.restype = ctypes.c_int
+        L.kdtv_gqa_verify_attn.argtypes = [G] + [vp] * 11 + [vp]
+        L.kdtv_gqa_verify_attn.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -552,3 +569,84 @@ def kv_read(parts, start=None, n_live=None, *, stream=None, **kw):
     """Reads rows of a cache (see KvRead); returns the status word."""
     with _on(stream):
         return KvRead(parts, start, n_live, **kw)(stream)
+
+
+class GqaVerifyAttn(_Bound):
+    """Caller of kdtv_gqa_verify_attn: a draft tree over a cache of keys and values per head.
+
+    q, out: [B, N, H, d]; k, v: the caches, [B, T, H_kv, d] or (with page_table [B, max_pages])
+    [num_pages, page_size, H_kv, d]; float32 or bfloat16, the caches also one byte per element
+    with exponent bytes k_scale, v_scale (the caches' shape without d).  Holds the workspace:
+    calls of one object must not overlap on the GPU.  status() reads the status word.
+    """
+
+    def __init__(self, q, k, v, parent, prefix_len, *, n_nodes=None, page_table=None, k_scale=None,
+                 v_scale=None, scale=0.0, flags=0, out=None):
+        import torch
+        one_byte = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+        _need(isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 4 and q.is_contiguous()
+              and q.numel() > 0 and q.dtype in (torch.float32, torch.bfloat16),
+              "q: a contiguous float32 or bfloat16 CUDA tensor [B, N, H, d]")
+        B, N, H, d = q.shape
+        for t in (k, v):
+            _need(isinstance(t, torch.Tensor) and t.device == q.device and t.dim() == 4 and t.is_contiguous()
+                  and t.shape == k.shape and t.dtype == k.dtype and t.shape[3] == d and t.numel() > 0
+                  and H % t.shape[2] == 0, "k, v: contiguous caches of one shape, [.., .., H_kv, d], on q's device")
+        fp8 = k.dtype in one_byte
+        _need(q.dtype == (torch.bfloat16 if fp8 else k.dtype), "q: the cache's type, bfloat16 for a one-byte cache")
+        for t in (k_scale, v_scale):
+            _need((t is not None) == fp8, "k_scale, v_scale: with a one-byte cache, and only there")
+            _need(t is None or (t.dtype == torch.uint8 and t.is_contiguous() and t.device == q.device
+                                and t.shape == k.shape[:3]), "k_scale, v_scale: contiguous uint8 [.., .., H_kv]")
+        pa = _index(parent, (B, N), q.device, "parent")
+        pl = _index(prefix_len, (B,), q.device, "prefix_len")
+        _need(pa is not None and pl is not None, "parent and prefix_len")
+        nn = _index(n_nodes, (B,), q.device, "n_nodes")
+        D = KdtvGqaDims(B, N, H, k.shape[2], d)
+        D.dtype = KDTV_BF16_FP8KV if fp8 else KDTV_F32 if q.dtype == torch.float32 else KDTV_BF16
+        if page_table is None:
+            _need(k.shape[0] == B, "a contiguous cache has one row block per request")
+            D.t_stride = k.shape[1]
+        else:
+            _need(page_table.dim() == 2, "page_table: [B, max_pages]")
+            _index(page_table, (B, page_table.shape[1]), q.device, "page_table")
+            D.num_pages, D.page_size, D.max_pages = k.shape[0], k.shape[1], page_table.shape[1]
+        D.scale, D.flags = scale, flags
+        self.out = torch.empty_like(q) if out is None else out
+        _need(self.out.shape == q.shape and self.out.dtype == q.dtype and self.out.device == q.device
+              and self.out.is_contiguous(), "out: like q")
+        with torch.cuda.device(q.device):
+            nbytes = int(lib().kdtv_gqa_workspace_size(ctypes.byref(D)))
+        if nbytes == 0:
+            raise KdtvError(STATUS_CODE["KDTV_ERR_UNSUPPORTED"], "workspace size")
+        self.dims = D
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        D.workspace, D.workspace_bytes = self.workspace.data_ptr(), nbytes
+        self._status = torch.zeros(1, dtype=torch.int32, device=q.device)
+        self._bind("kdtv_gqa_verify_attn", q.device,
+                   (ctypes.byref(D), _p(q), _p(k), _p(v), _p(k_scale), _p(v_scale), _p(pa), _p(pl), _p(nn),
+                    _p(page_table), _p(self.out), _p(self._status)),
+                   (q, k, v, k_scale, v_scale, pa, pl, nn, page_table))
+
+    def __call__(self, stream=None):
+        self._launch(stream)
+        return self.out
+
+    def status(self):
+        """First device-side error since it was last read (0: none); waits for the device, clears it."""
+        self.torch.cuda.synchronize(self.device)
+        code = int(self._status.item())
+        if code:
+            self._status.zero_()
+            self.torch.cuda.synchronize(self.device)
+        return code
+
+    def launches(self):
+        return int(lib().kdtv_gqa_launches_per_call(ctypes.byref(self.dims)))
+
+
+def gqa_verify_attn(q, k, v, parent, prefix_len, *, stream=None, **kw):
+    """Tree attention over a GQA cache (see GqaVerifyAttn); returns (out, status word)."""
+    with _on(stream):
+        op = GqaVerifyAttn(q, k, v, parent, prefix_len, **kw)
+        return op(stream), op._status
