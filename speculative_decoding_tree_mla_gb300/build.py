@@ -23,7 +23,7 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkdtv.so")
 SOURCES = ["kdtv_api.cu", "kdtv_simt.cu", "kdtv_tc.cu", "kdtv_tc_gemm.cu", "kdtv_next.cu",
            "kdtv_noalloc.cu", "kdtv_fp8.cu", "kdtv_kv.cu",
-           "kdtv_gqa.cu"]
+           "kdtv_gqa.cu", "kdtv_gqa_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -277,11 +277,6 @@ int make_plan(const kdtv_gqa_dims* d, GqaArgs* a, size_t* off_ml, size_t* total)
 
 }  // namespace
 
-// until the tensor-core path is built
-int gqa_tc_supported(const kdtv_gqa_dims*) { return 0; }
-size_t gqa_tc_workspace(const kdtv_gqa_dims*, int, GqaArgs*) { return 0; }
-int launch_gqa_tc(const GqaArgs&, bool, cudaStream_t) { return KDTV_ERR_UNSUPPORTED; }
-
 }  // namespace kdtv
 
 using namespace kdtv;

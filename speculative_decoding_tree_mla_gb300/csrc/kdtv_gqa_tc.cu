@@ -1,0 +1,991 @@
+// Tensor-core (tcgen05) path of kdtv_gqa_verify_attn: bf16 queries, bf16 or
+// one-byte caches, head dims 64 and 128.
+//
+// Work.  The query rows of a key/value head are (node, query head) pairs, cut
+// into tiles of npt = 128 / G nodes (at most 128 rows, one per TMEM lane).  An
+// item is (request, key/value head, pair of tiles); its work is its 128-key
+// tiles.  All (item, key tile) units form one sequence and CTA c takes the W
+// consecutive units [cW, (c + 1)W), so ragged batches and few long requests
+// spread evenly; a piece (the part of an item in one CTA) that is not the
+// whole item leaves a partial {max, sum, O} that the combine kernel merges.
+// Each CTA derives the sequence from prefix_len by itself: no plan kernel.
+//
+// A CTA runs two score streams s = 0, 1, each with a 128 x 128 score tile, an
+// output accumulator in TMEM and four softmax warps, so that one stream's
+// products run while the other's softmax does:
+//   two tiles of rows: stream s holds tile s, both read the same keys;
+//   one tile: both hold it, stream s takes the key tiles of parity s, and
+//             their results are merged at the end of the piece.
+// P replaces its scores in TMEM (bf16) and is the A operand of P.V, so only
+// keys, values and Q pass through shared memory.
+//
+// Keys and values enter one ring in the order in which the products need
+// them.  With lag = 1 (two tiles) or 2 (one tile), step i of a piece multiplies
+// P.V of tile i - lag, then Q.K^T of tile i; the entry number of K_i within the
+// piece is i + max(0, i - lag + 1) and of V_i is i + min(n, i + lag).
+//
+// One-byte caches: TMA brings raw rows into a ring of their own, and four
+// warps widen them to bf16 with the row's power-of-two scale (exact) into the
+// operand ring.  bf16 caches: the same warps touch only the last key tiles,
+// where they zero the value rows behind the tree, and (both) replace values
+// that are not finite in the tree's own rows by 0, noting the keys: 0 * inf
+// must not reach nodes that do not see them.  The epilogue adds them back to
+// the rows that do.
+//
+// Every wait has a time limit; one that runs out records
+// KDTV_ERR_DEVICE_TIMEOUT and ends the CTA's work.
+
+#include <cuda.h>
+
+#include "kdtv_gqa.cuh"
+#include "kdtv_ptx.cuh"
+#include "kdtv_tmap.cuh"
+
+namespace kdtv {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 128;                  // rows of a score tile, keys of a key tile
+constexpr int kThreads = 512;
+constexpr int kWarpAux = 8, kWarpTma = 12, kWarpMma = 13;
+constexpr int kRing = 8;                    // bound on ring sizes (barriers)
+constexpr int kPieces = 8;                  // pieces whose flags may be in flight
+
+// barriers
+enum {
+  B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + kRing, B_RAW_FULL = B_KV_EMPTY + kRing,
+  B_RAW_EMPTY = B_RAW_FULL + kRing, B_FIX = B_RAW_EMPTY + kRing, B_Q_FULL = B_FIX + kRing,
+  B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 2, B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2,
+  B_O1_FREE, B_MMA_DONE, B_STALL, B_COUNT
+};
+
+template <int D, bool kFp8>
+struct Cfg {
+  static constexpr int kTileBytes = kTile * D * 2;            // Q, K or V tile in bf16
+  static constexpr int kChunk = kTile * 128;                  // its 64 columns, 128-byte rows
+  static constexpr int kRawBytes = kTile * D;
+  // D = 128: Q 64 KiB and 5 tiles of 32 KiB, or 3 and 4 raw ones of 16 KiB
+  static constexpr int kSlots = kFp8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr int kRaw = kFp8 ? (D == 128 ? 4 : 8) : 0;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = 2 * kTileBytes;
+  static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
+  static constexpr int kOffMisc = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kMiscBytes = B_COUNT * 8 + 64 + kPieces * 4 + kPieces * 16 + kTile * 8;
+  static constexpr int kSmem = kOffMisc + kMiscBytes;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr uint32_t kColS = 0, kColO = 2 * kTile;     // S0, S1, O0, O1
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];"
+      :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// ---- the sequence of units ---------------------------------------------------------------
+__device__ __forceinline__ int key_tiles(int L, int n) { return (L + n + kTile - 1) / kTile; }
+__device__ __forceinline__ int row_pairs(const GqaArgs& a, int n) { return (n + 2 * a.npt - 1) / (2 * a.npt); }
+__device__ __forceinline__ int units_of(const GqaArgs& a, int b) {
+  int L, n;
+  gqa_request(a, b, &L, &n);
+  return n > 0 ? a.Hkv * row_pairs(a, n) * key_tiles(L, n) : 0;
+}
+
+struct Piece {
+  int b, L, n, nt, rps;      // request, prefix, live nodes, key tiles, pairs of row tiles
+  int item;                  // kvh * rps + pair within the request
+  int t0, t1;                // key tiles
+  int at;                    // unit of t0
+  int index;                 // of this CTA's pieces
+  __device__ __forceinline__ int kvh() const { return item / rps; }
+  __device__ __forceinline__ int pair() const { return item % rps; }
+  __device__ __forceinline__ bool two(const GqaArgs& a) const { return n - pair() * 2 * a.npt > a.npt; }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+  __device__ __forceinline__ bool tail() const { return t1 == nt || t1 * kTile > L; }
+};
+__device__ __forceinline__ void load_request(const GqaArgs& a, Piece& p) {
+  gqa_request(a, p.b, &p.L, &p.n);
+  p.nt = p.n > 0 ? key_tiles(p.L, p.n) : 0;
+  p.rps = p.n > 0 ? row_pairs(a, p.n) : 1;
+}
+// plan: {first request, unit within it, first unit, end}
+__device__ __forceinline__ bool first_piece(const GqaArgs& a, const int* plan, Piece& p) {
+  const int beg = plan[2], end = plan[3];
+  if (beg >= end) return false;
+  p.b = plan[0];
+  load_request(a, p);
+  p.item = plan[1] / p.nt;
+  p.t0 = plan[1] % p.nt;
+  p.t1 = min(p.nt, p.t0 + end - beg);
+  p.at = beg;
+  p.index = 0;
+  return true;
+}
+__device__ __forceinline__ bool next_piece(const GqaArgs& a, const int* plan, Piece& p) {
+  p.at += p.t1 - p.t0;
+  const int end = plan[3];
+  if (p.at >= end) return false;
+  ++p.index;
+  if (++p.item == a.Hkv * p.rps) {
+    p.item = 0;
+    do {
+      ++p.b;
+      load_request(a, p);
+    } while (p.nt == 0);          // units are left, so such a request exists
+  }
+  p.t0 = 0;
+  p.t1 = min(p.nt, end - p.at);
+  return true;
+}
+
+// ---- bounded waits -------------------------------------------------------------------------
+struct Guard {
+  volatile uint32_t* abort;      // shared memory
+  unsigned int* status;
+  uint64_t limit;
+};
+__device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (*g.abort) return false;
+    if (globaltimer() - t0 > g.limit) {
+      atomicCAS(g.status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
+      *g.abort = 1u;
+      return false;
+    }
+  }
+}
+// The same by polling: for the one thread that issues the products, where waking
+// from a suspended wait would be paid on every tile.
+__device__ __forceinline__ bool wait_spin(const Guard& g, uint32_t bar, uint32_t parity) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*g.abort) return false;
+      if (globaltimer() - t0 > g.limit) {
+        atomicCAS(g.status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
+        *g.abort = 1u;
+        return false;
+      }
+    }
+  }
+}
+// Waits for asynchronous work that is in flight and will finish (limited all the same).
+__device__ __forceinline__ void drain(const Guard& g, uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > g.limit) return;
+}
+__device__ __forceinline__ bool wait_warp(const Guard& g, uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(g, bar, parity));
+}
+
+// Four E4M3 bytes as four bf16, times 2^-120: the seven bits below the sign
+// moved onto the bf16 exponent and mantissa (subnormals stay subnormal).
+__device__ __forceinline__ uint2 e4m3_bits(uint32_t w) {
+  const uint32_t m = w & 0x7f7f7f7fu, s = w & 0x80808080u;
+  const uint32_t m0 = __byte_perm(m, 0u, 0x4140), m1 = __byte_perm(m, 0u, 0x4342);   // bytes in 16-bit lanes
+  const uint32_t s0 = __byte_perm(s, 0u, 0x1404), s1 = __byte_perm(s, 0u, 0x3424);   // sign at bit 15 of each
+  return make_uint2(m0 * 16u + s0, m1 * 16u + s1);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
+  return y;
+}
+__device__ __forceinline__ uint32_t pow2_bf16x2(int e) {      // e in [-126, 127]
+  const uint32_t h = (uint32_t)(e + 127) << 7;
+  return h | (h << 16);
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// Zeroes the elements of a bf16 pair that are not finite; true if there were any.
+__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
+  const bool lo = (w & 0x00007f80u) == 0x00007f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
+  if (lo) w &= 0xffff0000u;
+  if (hi) w &= 0x0000ffffu;
+  return lo || hi;
+}
+
+// V[t] of one key for elements e .. e + 31, what of it is not finite (else 0).
+template <bool kFp8>
+__device__ __forceinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int t, int e, float (&o)[32]) {
+  const long long row = gqa_row(a, b, t);
+  if (row < 0) return;
+  const long long at = (row * a.Hkv + kvh) * a.d + e;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float x = kFp8 ? to_f32(static_cast<const __nv_fp8_e4m3*>(a.v)[at + k])
+                         : to_f32(static_cast<const __nv_bfloat16*>(a.v)[at + k]);
+    if (!(fabsf(x) < INFINITY)) o[k] += x;
+  }
+}
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1)
+gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ GqaArgs a, int stall) {
+  using C = Cfg<D, kFp8>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffMisc);
+  const uint32_t bar0 = smem_u32(bars);
+  auto BAR = [&](int i) { return bar0 + 8u * i; };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + B_COUNT);   // [0] tmem, [1] abort, [4..7] plan
+  int* plan = reinterpret_cast<int*>(misc + 4);
+  volatile uint32_t* bad_page = misc + 16;                         // [kPieces]
+  uint32_t* nonfinite = misc + 16 + kPieces;                       // [kPieces][4] keys of the tree
+  float2* ml1 = reinterpret_cast<float2*>(nonfinite + 4 * kPieces);   // [128] stream 1's {max, sum}
+  const Guard guard{misc + 1, a.status, stall ? 20000000ull : 2000000000ull};
+
+  grid_dep_launch();               // the combine kernel may be launched; it waits for this grid
+  if (threadIdx.x == 0) {
+    misc[1] = 0u;
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(BAR(B_KV_FULL + i), kFp8 ? 4 : 1);
+      mbar_init(BAR(B_KV_EMPTY + i), 1);
+      mbar_init(BAR(B_RAW_FULL + i), 1);
+      mbar_init(BAR(B_RAW_EMPTY + i), 4);
+      mbar_init(BAR(B_FIX + i), 4);
+    }
+    mbar_init(BAR(B_Q_FULL), 1);
+    mbar_init(BAR(B_Q_EMPTY), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(B_S_FULL + i), 1);
+      mbar_init(BAR(B_P_READY + i), 4);
+      mbar_init(BAR(B_O_FULL + i), 1);
+    }
+    mbar_init(BAR(B_ML), 4);
+    mbar_init(BAR(B_O1_FREE), 4);
+    mbar_init(BAR(B_MMA_DONE), 1);
+    mbar_init(BAR(B_STALL), 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < kPieces) bad_page[threadIdx.x] = 0u;
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(misc), 512);
+    tmem_relinquish();
+  }
+  if (warp == kWarpTma && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 0) {
+    // W and this CTA's first request: one pass for the total, one to its start
+    int sum = 0;
+    for (int b = lane; b < a.B; b += 32) sum += units_of(a, b);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    const int W = (sum + a.ctas - 1) / a.ctas;
+    const long long beg = (long long)blockIdx.x * W;
+    if (beg >= sum) {
+      if (lane == 0) plan[2] = plan[3] = 0;
+    } else {
+      int before = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int u = b0 + lane < a.B ? units_of(a, b0 + lane) : 0;
+        int scan = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, scan, o);
+          if (lane >= o) scan += x;
+        }
+        const int lo = before + scan - u;
+        if (u > 0 && beg >= lo && beg < lo + u) {
+          plan[0] = b0 + lane;
+          plan[1] = (int)(beg - lo);
+          plan[2] = (int)beg;
+          plan[3] = (int)(beg + W < sum ? beg + W : sum);
+        }
+        before += __shfl_sync(0xffffffffu, scan, 31);
+        if (before > beg) break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  if (warp == kWarpTma) {
+    // ---- TMA producer: the warp's lanes hold page ids; lane l loads box l of a tile ---------
+    const int boxes = a.page_size ? kTile / a.page_size : 1;      // page_size divides 128
+    const int box_rows = kTile / boxes;
+    const uint32_t full0 = kFp8 ? B_RAW_FULL : B_KV_FULL, empty0 = kFp8 ? B_RAW_EMPTY : B_KV_EMPTY;
+    constexpr int kEntries = kFp8 ? C::kRaw : C::kSlots;
+    constexpr int kEntryBytes = kFp8 ? C::kRawBytes : C::kTileBytes;
+    const uint32_t ring = sbase + (kFp8 ? C::kOffRaw : C::kOffKV);
+    Piece p;
+    bool have = first_piece(a, plan, p), alive = true;
+    if (stall && have) alive = wait_warp(guard, BAR(B_STALL), 0);
+    int g = 0, q_loads = 0;
+    while (alive && have) {
+      const int kvh = p.kvh(), n = p.t1 - p.t0, T = p.L + p.n;
+      const bool two = p.two(a);
+      const int lag = two ? 1 : 2;
+      if (p.index > 0) alive = wait_warp(guard, BAR(B_Q_EMPTY), (p.index - 1) & 1);
+      if (!alive) break;
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)a.npt * a.G * 128;
+        mbar_expect_tx(BAR(B_Q_FULL), bytes * (D / 64) * (two ? 2 : 1));
+        for (int s = 0; s < (two ? 2 : 1); ++s)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + c * C::kChunk, &tm_q, BAR(B_Q_FULL), 64 * c,
+                        kvh * a.G, p.b * a.N + (2 * p.pair() + s) * a.npt);
+      }
+      ++q_loads;
+      // windows of 32 page ids, the next one loaded ahead; a page out of range is read as page 0
+      // and marks the piece
+      const int32_t* table = a.page_table + (long long)p.b * a.max_pages;
+      auto page_at = [&](int k) {                 // k-th box of the piece
+        const int box = p.t0 * boxes + k;
+        if (!a.page_size || (long long)box * box_rows >= T) return 0;
+        return table[box];
+      };
+      int win = page_at(lane), win_next = page_at(32 + lane);
+      int page0 = 0, page1 = 0, page2 = 0;        // of tiles i, i - 1, i - 2
+      uint32_t bad = 0;
+      for (int i = 0; alive && i < n + lag; ++i) {
+        page2 = page1;
+        page1 = page0;
+        if (i < n) {
+          const int k = i * boxes;
+          if (k > 0 && (k & 31) == 0) {
+            win = win_next;
+            win_next = page_at(k + 32 + lane);
+          }
+          page0 = __shfl_sync(0xffffffffu, win, (k + lane) & 31);
+          if (page0 < 0 || page0 >= (a.page_size ? a.num_pages : 1)) {
+            if (lane < boxes) bad = 1;
+            page0 = 0;
+          }
+          if (i == n - 1) {                       // before the piece's last loads: seen by its epilogue
+            const bool any = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+              bad_page[p.index % kPieces] = any ? 1u : 0u;
+              if (any) gqa_error(a, KDTV_ERR_BAD_PAGE);
+            }
+          }
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {          // V of tile i - lag, then K of tile i
+          const int kt = kv == 0 ? i - lag : i;
+          if (kt < 0 || kt >= n) continue;
+          const int slot = g % kEntries;
+          if (g >= kEntries) alive = wait_warp(guard, BAR(empty0 + slot), (g / kEntries - 1) & 1);
+          if (!alive) break;
+          const int t = (p.t0 + kt) * kTile;
+          const int live = a.page_size ? min(boxes, (T - t + box_rows - 1) / box_rows) : 1;
+          const uint32_t bar = BAR(full0 + slot), dst = ring + slot * kEntryBytes;
+          if (lane == 0) mbar_expect_tx(bar, (uint32_t)live * box_rows * D * (kFp8 ? 1 : 2));
+          __syncwarp();
+          if (lane < live) {
+            const int page = kv == 1 ? page0 : (lag == 1 ? page1 : page2);
+            const void* map = kv == 0 ? &tm_v : &tm_k;
+            const int y = a.page_size ? 0 : t, z = a.page_size ? page : p.b;
+            if constexpr (kFp8) {
+              tma_load_4d(dst + lane * box_rows * D, map, bar, 0, kvh, y, z);
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(dst + c * C::kChunk + lane * box_rows * 128, map, bar, 64 * c, kvh, y, z);
+            }
+          }
+          ++g;
+        }
+      }
+      if (!alive) break;
+      have = next_piece(a, plan, p);
+    }
+    // every copy has landed before the CTA may exit
+    if (q_loads) drain(guard, BAR(B_Q_FULL), (q_loads - 1) & 1);
+    for (int x = g > kEntries ? g - kEntries : 0; x < g; ++x)
+      drain(guard, BAR(full0 + x % kEntries), (x / kEntries) & 1);
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // ---- MMA issuer -----------------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_bf16(kTile, kTile, 0, 0), kIdescO = idesc_bf16(kTile, D, 0, 1);
+      Piece p;
+      bool have = first_piece(a, plan, p), alive = true;
+      int g = 0;
+      uint32_t p_phase = 0u, fix_phase = 0u;
+      auto scores = [&](int s, int qs, uint32_t kv) {           // S_s = Q K^T
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kChunk + (kk & 3) * 32;
+          mma_bf16(tmem + C::kColS + kTile * s, smem_desc(sbase + C::kOffQ + qs * C::kTileBytes + off, 16, 1024),
+                   smem_desc(kv + off, 16, 1024), kIdescS, kk > 0);
+        }
+        mma_commit(BAR(B_S_FULL + s));
+      };
+      auto values = [&](int s, uint32_t kv, bool first) {       // O_s (+)= P_s V
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_bf16_ts(tmem + C::kColO + D * s, tmem + C::kColS + kTile * s + 8 * kk,
+                      smem_desc(kv + kk * 16 * 128, C::kChunk, 1024), kIdescO, !first || kk > 0);
+      };
+      while (alive && have) {
+        const int n = p.t1 - p.t0;
+        const bool two = p.two(a);
+        const int lag = two ? 1 : 2;
+        alive = wait_spin(guard, BAR(B_Q_FULL), p.index & 1);
+        for (int i = 0; alive && i < n + lag; ++i) {
+          int vslot = 0, kslot = 0;
+          const int vt = i - lag;
+          if (vt >= 0) {
+            vslot = g % C::kSlots;
+            alive = wait_spin(guard, BAR(B_KV_FULL + vslot), (g / C::kSlots) & 1);
+            if (!kFp8 && alive && (p.t0 + vt + 1) * kTile > p.L) {
+              alive = wait_spin(guard, BAR(B_FIX + vslot), (fix_phase >> vslot) & 1);
+              fix_phase ^= 1u << vslot;
+            }
+            if (!alive) break;
+            ++g;
+          }
+          if (i < n) kslot = g % C::kSlots;
+          const uint32_t vaddr = sbase + C::kOffKV + vslot * C::kTileBytes;
+          const uint32_t kaddr = sbase + C::kOffKV + kslot * C::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (!two && k == 1) break;
+            const int s = two ? k : (i & 1);
+            const bool last_k = !two || k == 1;
+            if (vt >= 0) {
+              alive = wait_spin(guard, BAR(B_P_READY + s), (p_phase >> s) & 1);
+              p_phase ^= 1u << s;
+              if (!alive) break;
+              tc_fence_after();
+              values(s, vaddr, two ? vt == 0 : vt < 2);
+              if (last_k) mma_commit(BAR(B_KV_EMPTY + vslot));
+              if (vt + (two ? 1 : 2) >= n) mma_commit(BAR(B_O_FULL + s));
+            }
+            if (i < n) {
+              if (k == 0) {
+                alive = wait_spin(guard, BAR(B_KV_FULL + kslot), (g / C::kSlots) & 1);
+                if (!alive) break;
+                ++g;
+              }
+              tc_fence_after();
+              scores(s, two ? s : 0, kaddr);
+              if (last_k) mma_commit(BAR(B_KV_EMPTY + kslot));
+              if (last_k && i == n - 1) mma_commit(BAR(B_Q_EMPTY));
+            }
+          }
+        }
+        if (!alive) break;
+        have = next_piece(a, plan, p);
+      }
+      mma_commit(BAR(B_MMA_DONE));                 // every product has finished before TMEM is freed
+      drain(guard, BAR(B_MMA_DONE), 0);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpAux && warp < kWarpTma) {
+    // ---- widening (one-byte caches) and the last tiles: thread = key row of the tile -----------
+    const int row = threadIdx.x - kWarpAux * 32;
+    const int swz = row & 7;
+    Piece p;
+    bool have = first_piece(a, plan, p), alive = true;
+    int g = 0;
+    while (alive && have) {
+      const int kvh = p.kvh(), n = p.t1 - p.t0, T = p.L + p.n;
+      const int lag = p.two(a) ? 1 : 2;
+      uint32_t* nf = nonfinite + 4 * (p.index % kPieces);
+      if (row < 4) nf[row] = 0u;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if constexpr (kFp8) {
+        // scale bytes: tile i + 1's are loaded while tile i is widened, from a row index
+        // (page table) loaded a tile before that
+        auto row_at = [&](int i) -> long long {
+          const int t = (p.t0 + i) * kTile + row;
+          if (i >= n || t >= T) return 0;
+          const long long r = gqa_row(a, p.b, t);
+          return r < 0 ? 0 : r;
+        };
+        auto at = [&](long long r) { return r * a.Hkv + kvh; };
+        long long r_next = row_at(0);
+        int k_next = a.k_scale[at(r_next)], v_next = a.v_scale[at(r_next)];
+        r_next = row_at(1);
+        int v0 = 127, v1 = 127, v2 = 127;
+        for (int i = 0; alive && i < n + lag; ++i) {
+          const int k0 = k_next;
+          v2 = v1;
+          v1 = v0;
+          v0 = v_next;
+          const long long r = r_next;
+          k_next = a.k_scale[at(r)];
+          v_next = a.v_scale[at(r)];
+          r_next = row_at(i + 2);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int kt = kv == 0 ? i - lag : i;
+            if (kt < 0 || kt >= n) continue;
+            const int rs = g % C::kRaw, slot = g % C::kSlots;
+            alive = wait_warp(guard, BAR(B_RAW_FULL + rs), (g / C::kRaw) & 1);
+            if (alive && g >= C::kSlots) alive = wait_warp(guard, BAR(B_KV_EMPTY + slot), (g / C::kSlots - 1) & 1);
+            if (!alive) break;
+            const int e = (kv == 1 ? k0 : (lag == 1 ? v1 : v2)) - 127;
+            const uint32_t src = sbase + C::kOffRaw + rs * C::kRawBytes + row * D;
+            const uint32_t dst = sbase + C::kOffKV + slot * C::kTileBytes + row * 128;
+            const int t = (p.t0 + kt) * kTile + row;
+            // 2^(e + 120) as two factors, each a bf16
+            const int ea = max(-126, min(127, e + 120)), eb = e + 120 - ea;
+            const uint32_t fa = pow2_bf16x2(ea), fb = pow2_bf16x2(eb);
+            const bool zero = kv == 0 && t >= T, own = kv == 0 && t >= p.L && t < T;
+            bool found = false;
+            const bool two_factors = __any_sync(0xffffffffu, eb != 0);
+            // 16-byte chunk c of the row at its XOR-permuted turn: no bank conflicts, for the
+            // reads (rows D bytes apart) nor for the swizzled writes
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const int c = D == 128 ? (k ^ swz) : (k ^ (swz & 3));
+              uint4 w = lds128(src + 16 * c);
+              if (zero) w = make_uint4(0u, 0u, 0u, 0u);
+              uint32_t u[4] = {w.x, w.y, w.z, w.w};
+              uint32_t y[8];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                if (own) {                       // E4M3 NaN: all seven bits set
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    if (((u[m] >> (8 * x)) & 0x7fu) == 0x7fu) {
+                      u[m] &= ~(0xffu << (8 * x));
+                      found = true;
+                    }
+                }
+                const uint2 z = e4m3_bits(u[m]);
+                y[2 * m] = mul_bf16x2(z.x, fa);
+                y[2 * m + 1] = mul_bf16x2(z.y, fa);
+                // NaN codes of other rows are 480 after the shift: make them NaN
+                if (((u[m] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    if (((u[m] >> (8 * x)) & 0x7fu) == 0x7fu)
+                      y[2 * m + (x >> 1)] |= (x & 1) ? 0x7fff0000u : 0x7fffu;
+                }
+              }
+              if (two_factors) {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) y[m] = mul_bf16x2(y[m], fb);
+              }
+              const uint32_t half = dst + (c >> 2) * C::kChunk;
+              const int j = (2 * c) & 7;
+              sts128(half + ((j ^ swz) << 4), y[0], y[1], y[2], y[3]);
+              sts128(half + (((j + 1) ^ swz) << 4), y[4], y[5], y[6], y[7]);
+            }
+            if (found) atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(BAR(B_KV_FULL + slot));
+              mbar_arrive(BAR(B_RAW_EMPTY + rs));
+            }
+            ++g;
+          }
+        }
+      } else {
+        const int from = max(p.t0, p.L / kTile);          // the first key tile that reaches past the prefix
+        for (int kt = from; alive && kt < p.t1; ++kt) {
+          const int i = kt - p.t0, x = g + i + min(n, i + lag), slot = x % C::kSlots;
+          alive = wait_warp(guard, BAR(B_KV_FULL + slot), (x / C::kSlots) & 1);
+          if (!alive) break;
+          const int t = kt * kTile + row;
+          if (t >= p.L) {
+            const uint32_t dst = sbase + C::kOffKV + slot * C::kTileBytes + row * 128;
+            bool found = false;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              const uint32_t addr = dst + (k >> 3) * C::kChunk + (((k & 7) ^ swz) << 4);
+              if (t >= T) {
+                sts128(addr, 0u, 0u, 0u, 0u);
+              } else {
+                uint4 w = lds128(addr);
+                bool any = drop_nonfinite(w.x);
+                any |= drop_nonfinite(w.y);
+                any |= drop_nonfinite(w.z);
+                any |= drop_nonfinite(w.w);
+                if (any) sts128(addr, w.x, w.y, w.z, w.w);
+                found |= any;
+              }
+            }
+            if (found) atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_FIX + slot));
+        }
+        g += 2 * n;
+      }
+      if (!alive) break;
+      have = next_piece(a, plan, p);
+    }
+  } else if (warp < kWarpAux) {
+    // ---- softmax and epilogue: thread = row 32 q + lane of stream s -----------------------------
+    const int s = warp >> 2, q = warp & 3, r = 32 * q + lane;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t tS = tmem + lanes + C::kColS + kTile * s, tO = tmem + lanes + C::kColO + D * s;
+    const float sl2 = a.scale * 1.4426950408889634f;      // base-2 exponentials
+    Piece p;
+    bool have = first_piece(a, plan, p), alive = true;
+    uint32_t s_phase = 0u, o_phase = 0u, one_pieces = 0u;
+    while (alive && have) {
+      const int n = p.t1 - p.t0, kvh = p.kvh();
+      const bool two = p.two(a);
+      const int node = (2 * p.pair() + (two ? s : 0)) * a.npt + r / a.G;
+      const bool valid = r < a.npt * a.G && node < p.n;
+      uint32_t path[4] = {0u, 0u, 0u, 0u};
+      bool dead = false;
+      if (valid && p.tail()) {
+        dead = !gqa_path(a, p.b, node, path);
+        if (dead) gqa_error(a, KDTV_ERR_BAD_TREE);
+      }
+      float m = -INFINITY, l = 0.f;
+      bool first = true, o1_check = s == 1 && one_pieces > 0;
+      for (int i = two ? 0 : s; i < n; i += two ? 1 : 2) {
+        const int t0 = (p.t0 + i) * kTile;
+        alive = wait_warp(guard, BAR(B_S_FULL + s), s_phase & 1);
+        ++s_phase;
+        if (!alive) break;
+        tc_fence_after();
+        const bool masked = t0 + kTile > p.L;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(tS + 32 * c, v);
+          tmem_wait_ld();
+          if (masked) {
+            const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, (see >> k) & 1u ? v[k] : -INFINITY);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
+          }
+        }
+        mx *= sl2;
+        // The reference maximum moves only when the tile's is over 2^8 above it: a weight
+        // stays below 2^8, and O is rescaled rarely.  O is at rest: the commit that made these
+        // scores visible came after this stream's previous P.V.
+        float alpha = 1.f;
+        if (mx > m + 8.f) {
+          if (m != -INFINITY) alpha = ex2(m - mx);
+          m = mx;
+        }
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+          l *= alpha;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32(tO + 32 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= alpha;
+            tmem_st32(tO + 32 * c, v);
+          }
+        }
+        first = false;
+        const float ref = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(tS + 32 * c, v);
+          tmem_wait_ld();
+          const uint32_t see = masked ? gqa_visible(path, t0 + 32 * c, p.L) : 0xffffffffu;
+          uint32_t w[16];
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float x = ex2(fmaf(v[k], sl2, ref)), y = ex2(fmaf(v[k + 1], sl2, ref));
+            if (masked) {
+              x = (see >> k) & 1u ? x : 0.f;
+              y = (see >> (k + 1)) & 1u ? y : 0.f;
+            }
+            sum += x + y;
+            w[k / 2] = pack_bf16x2(x, y);        // bf16: the tensor cores' operand type
+          }
+          l += sum;
+          tmem_st16u(tS + 16 * c, w);            // over scores that are read already
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        // stream 1's accumulator: stream 0's warps must have merged the last one-tile piece
+        if (o1_check) {
+          o1_check = false;
+          alive = wait_warp(guard, BAR(B_O1_FREE), (one_pieces - 1) & 1);
+          if (!alive) break;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_P_READY + s));
+      }
+      if (!alive) break;
+
+      // ---- the end of the piece ---------------------------------------------------------------
+      const bool mine = two || n > s;              // this stream had a tile
+      if (mine) {
+        alive = wait_warp(guard, BAR(B_O_FULL + s), o_phase & 1);
+        ++o_phase;
+        if (!alive) break;
+        tc_fence_after();
+      }
+      if (!two && s == 1) {
+        if (o1_check) {                            // no tile of its own: not waited for above
+          alive = wait_warp(guard, BAR(B_O1_FREE), (one_pieces - 1) & 1);
+          if (!alive) break;
+        }
+        ml1[r] = make_float2(m, l);
+        __syncwarp();
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(BAR(B_ML));
+        ++one_pieces;
+      } else {
+        float w0 = 1.f, w1 = 0.f;
+        bool merge = false;
+        if (!two) {
+          alive = wait_warp(guard, BAR(B_ML), one_pieces & 1);
+          if (!alive) break;
+          tc_fence_after();
+          const float2 o = ml1[r];
+          merge = n > 1;
+          if (merge) {
+            const float mm = fmaxf(m, o.x), ref = mm == -INFINITY ? 0.f : mm;
+            w0 = ex2(m - ref);
+            w1 = ex2(o.x - ref);
+            l = l * w0 + o.y * w1;
+            m = mm;
+          }
+        }
+        const bool bad = bad_page[p.index % kPieces] != 0u;
+        uint32_t nf[4];
+        uint32_t any_nf = 0u;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          nf[w] = p.tail() ? nonfinite[4 * (p.index % kPieces) + w] & path[w] : 0u;
+          any_nf |= nf[w];
+        }
+        const bool whole = p.whole();
+        const bool write = valid && !bad && !dead;
+        const float inv = 1.f / l;
+        const long long orow = ((long long)p.b * a.N + node) * a.H + (long long)kvh * a.G + r % a.G;
+        const long long slot = 2ll * blockIdx.x + (p.at != plan[2]);
+        const long long prow = slot * (2 * kTile) + (two ? kTile * s : 0) + r;
+        if (!whole && valid) a.part_ml[prow] = make_float2(m, write ? l : -1.f);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          __syncwarp();                            // lanes without a row to write rejoin
+          tmem_ld32(tO + 32 * c, v);
+          tmem_wait_ld();
+          if (merge) {
+            float u[32];
+            tmem_ld32(tO + D + 32 * c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = v[k] * w0 + u[k] * w1;
+          }
+          if (any_nf) {
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              uint32_t x = w == 0 ? nf[0] : w == 1 ? nf[1] : w == 2 ? nf[2] : nf[3];
+#pragma unroll 1
+              while (x) {
+                add_nonfinite<kFp8>(a, p.b, kvh, p.L + 32 * w + __ffs(x) - 1, 32 * c, v);
+                x &= x - 1;
+              }
+            }
+          }
+          if (!write) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
+                                  pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                                  pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                                  pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (!two) {
+          ++one_pieces;
+          if (lane == 0) mbar_arrive(BAR(B_O1_FREE));
+        }
+      }
+      have = next_piece(a, plan, p);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// ---- combine --------------------------------------------------------------------------------
+// Output rows of items that were cut into pieces: the pieces' sums and outputs
+// meet at their common maximum.  blockIdx.y is the request; a warp per row, the
+// row's d elements across its lanes.  Item [S, S + nt) was cut at the multiples
+// of W; CTA c's piece that starts its range is partial 2c, one that starts
+// later 2c + 1.
+template <int D>
+__global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant__ GqaArgs a) {
+  __shared__ int s_sum[8], s_before[8];
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int sum = 0, before = 0;
+  for (int x = threadIdx.x; x < a.B; x += 256) {
+    const int u = units_of(a, x);
+    sum += u;
+    if (x < b) before += u;
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) {
+    s_sum[warp] = sum;
+    s_before[warp] = before;
+  }
+  __syncthreads();
+  sum = before = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    sum += s_sum[w];
+    before += s_before[w];
+  }
+  int L, n;
+  gqa_request(a, b, &L, &n);
+  grid_dep_wait();                                 // the partials are written
+  if (n == 0 || *reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
+  const int W = (sum + a.ctas - 1) / a.ctas;
+  const int nt = key_tiles(L, n), rps = row_pairs(a, n);
+  const int rows = n * a.H;
+  constexpr int V = D / 32;                        // elements per lane
+  for (int row = blockIdx.x * 8 + warp; row < rows; row += gridDim.x * 8) {
+    const int node = row / a.H, h = row % a.H, kvh = h / a.G;
+    const int tile = node / a.npt;
+    const int start = before + (kvh * rps + tile / 2) * nt, end = start + nt;
+    const int c0 = start / W, c1 = (end - 1) / W;
+    if (c0 == c1) continue;                        // whole: written by its CTA
+    const int r = (tile & 1) * kTile + (node % a.npt) * a.G + h % a.G;
+    auto prow = [&](int c) {
+      const long long slot = 2ll * c + (c == c0 && start != c0 * W);
+      return slot * (2 * kTile) + r;
+    };
+    float m = -INFINITY;
+    bool skip = false;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float2 ml = a.part_ml[prow(c)];
+      skip |= ml.y < 0.f;
+      m = fmaxf(m, ml.x);
+    }
+    if (__any_sync(0xffffffffu, skip)) continue;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      const long long pr = prow(c);
+      const float2 ml = a.part_ml[pr];
+      const float w = ex2(ml.x - ref);
+      l += ml.y * w;
+      const float* src = a.part_o + pr * D + V * lane;
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = fmaf(src[k], w, o[k]);
+    }
+    const float inv = 1.f / l;
+    uint32_t y[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) y[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
+                                                (((long long)b * a.N + node) * a.H + h) * D) + V / 2 * lane;
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) dst[k] = y[k];
+  }
+}
+
+template <int D, bool kFp8>
+int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
+  using C = Cfg<D, kFp8>;
+  CUtensorMap tq, tk, tv;
+  {
+    // Q: [B * N, H, d]; a box is the G heads of npt nodes, 64 columns
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.H, (uint64_t)a.B * a.N};
+    const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)a.H * D * 2};
+    const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.npt};
+    if (encode_nd(&tq, a.q, 3, dims, strides, box, 2, true) != CUDA_SUCCESS) return KDTV_ERR_CUDA;
+  }
+  const uint64_t es = kFp8 ? 1 : 2;
+  const uint64_t rows = a.page_size ? a.page_size : a.t_stride, blocks = a.page_size ? a.num_pages : a.B;
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.Hkv, rows, blocks};
+  const uint64_t strides[3] = {D * es, (uint64_t)a.Hkv * D * es, rows * a.Hkv * D * es};
+  const uint32_t box[4] = {kFp8 ? (uint32_t)D : 64u, 1u, a.page_size ? (uint32_t)a.page_size : (uint32_t)kTile, 1u};
+  if (encode_nd(&tk, a.k, 4, dims, strides, box, (int)es, !kFp8) != CUDA_SUCCESS ||
+      encode_nd(&tv, a.v, 4, dims, strides, box, (int)es, !kFp8) != CUDA_SUCCESS)
+    return KDTV_ERR_CUDA;
+  const auto kern = gqa_tc_kernel<D, kFp8>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+    return KDTV_ERR_CUDA;
+  if (launch_ex(kern, dim3((unsigned)a.ctas), dim3(kThreads), C::kSmem, st, false, tq, tk, tv, a, stall ? 1 : 0) !=
+      cudaSuccess)
+    return KDTV_ERR_CUDA;
+  // rows of a request in up to 16 CTAs, 8 rows at a time
+  const int gx = (a.N * a.H + 63) / 64 < 64 ? (a.N * a.H + 63) / 64 : 64;
+  if (launch_ex(gqa_combine_kernel<D>, dim3((unsigned)gx, (unsigned)a.B), dim3(256), 0, st, true, a) != cudaSuccess)
+    return KDTV_ERR_CUDA;
+  return KDTV_OK;
+}
+
+}  // namespace
+
+int gqa_tc_supported(const kdtv_gqa_dims* d) {
+  if (d->dtype != KDTV_BF16 && d->dtype != KDTV_BF16_FP8KV) return 0;
+  if (d->d != 64 && d->d != 128) return 0;
+  if (d->H / d->H_kv > kTile) return 0;
+  const int ps = d->page_size;
+  return ps == 0 || ps == 16 || ps == 32 || ps == 64 || ps == 128;
+}
+
+size_t gqa_tc_workspace(const kdtv_gqa_dims* d, int sms, GqaArgs* a) {
+  a->npt = kTile / a->G;
+  a->ctas = sms;
+  const long long cap = d->page_size ? (long long)d->max_pages * d->page_size : d->t_stride;
+  const long long units = (long long)d->B * d->H_kv * ((d->N + 2 * a->npt - 1) / (2 * a->npt)) *
+                          ((cap + kTile - 1) / kTile);
+  if (units >= (1ll << 30)) return 0;               // 32-bit unit numbers
+  return (size_t)2 * sms * 2 * kTile;
+}
+
+int launch_gqa_tc(const GqaArgs& a, bool stall, cudaStream_t st) {
+  if (a.dtype == KDTV_BF16_FP8KV)
+    return a.d == 128 ? launch_t<128, true>(a, stall, st) : launch_t<64, true>(a, stall, st);
+  return a.d == 128 ? launch_t<128, false>(a, stall, st) : launch_t<64, false>(a, stall, st);
+}
+
+}  // namespace kdtv

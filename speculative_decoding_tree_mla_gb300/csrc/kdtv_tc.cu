@@ -1324,6 +1324,24 @@ CUresult encode_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+CUresult encode_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box, int elem_bytes, bool swizzle) {
+  EncodeTiledFn fn = encoder();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4];
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  return fn(m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank,
+            const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 int tc_supported(const kdtv_dims* d) {
   if (d->dtype != KDTV_BF16 || d->d_c != 512 || d->d_rope != 64) return 0;
   if (d->page_size != 0 && d->page_size != 64) return 0;

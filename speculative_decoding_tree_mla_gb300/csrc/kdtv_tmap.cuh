@@ -13,4 +13,10 @@ CUresult encode_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
                    uint32_t box_cols, uint32_t box_rows, uint64_t row_stride_elems = 0,
                    int swizzle_bytes = 128);
 
+// Tensor map of `rank` (3..4) dimensions, innermost first, of 2-byte (bf16) or
+// 1-byte elements; strides in bytes, of all but the innermost dimension.  128-byte
+// swizzle, or none.
+CUresult encode_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box, int elem_bytes, bool swizzle);
+
 }  // namespace kdtv

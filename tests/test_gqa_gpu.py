@@ -108,7 +108,9 @@ class Case:
         for b in range(self.B):
             n = int(self.n[b])
             assert (got[b, n:] == 9.0).all()
-            kk = np.repeat(np.abs(k[b]).max(0), G, axis=0)             # [H, d]
+            # finite keys only: a row that sees another has NaN for its weights, and the scores of
+            # a row that does not are made of finite keys alone
+            kk = np.repeat(np.where(np.isfinite(k[b]), np.abs(k[b]), 0.0).max(0), G, axis=0)   # [H, d]
             delta = (self.d + 4) * 2.0 ** -24 * scale * (np.abs(q[b, :n]) * kk).sum(-1)[..., None]
             rel = 2 * delta + 2.0 ** -20 + T * 2.0 ** -24 + (2.0 ** -8 if tensor_cores else 0.0)
             for i in range(n) if rows is None else rows(b):
