@@ -55,7 +55,7 @@ constexpr int kPieces = 8;                  // pieces whose flags may be in flig
 // barriers
 enum {
   B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + kRing, B_RAW_FULL = B_KV_EMPTY + kRing,
-  B_RAW_EMPTY = B_RAW_FULL + kRing, B_FIX = B_RAW_EMPTY + kRing, B_Q_FULL = B_FIX + kRing,
+  B_RAW_EMPTY = B_RAW_FULL + kRing, B_TAIL = B_RAW_EMPTY + kRing, B_Q_FULL = B_TAIL + kRing,
   B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 2, B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2,
   B_O1_FREE, B_MMA_DONE, B_STALL, B_COUNT
 };
@@ -268,7 +268,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       mbar_init(BAR(B_KV_EMPTY + i), 1);
       mbar_init(BAR(B_RAW_FULL + i), 1);
       mbar_init(BAR(B_RAW_EMPTY + i), 4);
-      mbar_init(BAR(B_FIX + i), 4);
+      mbar_init(BAR(B_TAIL + i), 1);
     }
     mbar_init(BAR(B_Q_FULL), 1);
     mbar_init(BAR(B_Q_EMPTY), 1);
@@ -398,7 +398,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (!alive) break;
           const int t = (p.t0 + kt) * kTile;
           const int live = a.page_size ? min(boxes, (T - t + box_rows - 1) / box_rows) : 1;
-          const uint32_t bar = BAR(full0 + slot), dst = ring + slot * kEntryBytes;
+          // bf16 values of a tile that reaches past the prefix go to the four warps first, which
+          // then arrive on the entry's full barrier (every wait sees each phase of its barrier)
+          const bool to_aux = !kFp8 && kv == 0 && t + kTile > p.L;
+          const uint32_t bar = BAR((to_aux ? B_TAIL : full0) + slot), dst = ring + slot * kEntryBytes;
           if (lane == 0) mbar_expect_tx(bar, (uint32_t)live * box_rows * D * (kFp8 ? 1 : 2));
           __syncwarp();
           if (lane < live) {
@@ -431,7 +434,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       Piece p;
       bool have = first_piece(a, plan, p), alive = true;
       int g = 0;
-      uint32_t p_phase = 0u, fix_phase = 0u;
+      uint32_t p_phase = 0u;
       auto scores = [&](int s, int qs, uint32_t kv) {           // S_s = Q K^T
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -458,10 +461,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (vt >= 0) {
             vslot = g % C::kSlots;
             alive = wait_spin(guard, BAR(B_KV_FULL + vslot), (g / C::kSlots) & 1);
-            if (!kFp8 && alive && (p.t0 + vt + 1) * kTile > p.L) {
-              alive = wait_spin(guard, BAR(B_FIX + vslot), (fix_phase >> vslot) & 1);
-              fix_phase ^= 1u << vslot;
-            }
             if (!alive) break;
             ++g;
           }
@@ -509,12 +508,13 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     Piece p;
     bool have = first_piece(a, plan, p), alive = true;
     int g = 0;
+    uint32_t tail_phase = 0u;
     while (alive && have) {
       const int kvh = p.kvh(), n = p.t1 - p.t0, T = p.L + p.n;
       const int lag = p.two(a) ? 1 : 2;
       uint32_t* nf = nonfinite + 4 * (p.index % kPieces);
       if (row < 4) nf[row] = 0u;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 2, 128;" ::: "memory");
       if constexpr (kFp8) {
         // scale bytes: tile i + 1's are loaded while tile i is widened, from a row index
         // (page table) loaded a tile before that
@@ -608,9 +608,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       } else {
         const int from = max(p.t0, p.L / kTile);          // the first key tile that reaches past the prefix
         for (int kt = from; alive && kt < p.t1; ++kt) {
-          const int i = kt - p.t0, x = g + i + min(n, i + lag), slot = x % C::kSlots;
-          alive = wait_warp(guard, BAR(B_KV_FULL + slot), (x / C::kSlots) & 1);
+          const int i = kt - p.t0, slot = (g + i + min(n, i + lag)) % C::kSlots;
+          alive = wait_warp(guard, BAR(B_TAIL + slot), (tail_phase >> slot) & 1);
           if (!alive) break;
+          tail_phase ^= 1u << slot;
           const int t = kt * kTile + row;
           if (t >= p.L) {
             const uint32_t dst = sbase + C::kOffKV + slot * C::kTileBytes + row * 128;
@@ -633,8 +634,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (found) atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
           }
           fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(B_FIX + slot));
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (row == 0) mbar_arrive(BAR(B_KV_FULL + slot));
         }
         g += 2 * n;
       }
