@@ -119,7 +119,7 @@ __device__ __forceinline__ void load_request(const GqaArgs& a, Piece& p) {
   p.rps = p.n > 0 ? row_pairs(a, p.n) : 1;
 }
 // plan: {first request, unit within it, first unit, end}
-__device__ __forceinline__ bool first_piece(const GqaArgs& a, const int* plan, Piece& p) {
+__device__ __noinline__ bool first_piece(const GqaArgs& a, const int* plan, Piece& p) {
   const int beg = plan[2], end = plan[3];
   if (beg >= end) return false;
   p.b = plan[0];
@@ -131,7 +131,7 @@ __device__ __forceinline__ bool first_piece(const GqaArgs& a, const int* plan, P
   p.index = 0;
   return true;
 }
-__device__ __forceinline__ bool next_piece(const GqaArgs& a, const int* plan, Piece& p) {
+__device__ __noinline__ bool next_piece(const GqaArgs& a, const int* plan, Piece& p) {
   p.at += p.t1 - p.t0;
   const int end = plan[3];
   if (p.at >= end) return false;
@@ -154,35 +154,31 @@ struct Guard {
   unsigned int* status;
   uint64_t limit;
 };
-__device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+// (the rest of a wait is out of line: the roles' loops have to share an instruction cache)
+__device__ __noinline__ bool wait_long(volatile uint32_t* abort, unsigned int* status, uint64_t limit,
+                                       uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   for (;;) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-    if (*g.abort) return false;
-    if (globaltimer() - t0 > g.limit) {
-      atomicCAS(g.status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
-      *g.abort = 1u;
+    if (*abort) return false;
+    if (globaltimer() - t0 > limit) {
+      atomicCAS(status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
+      *abort = 1u;
       return false;
     }
   }
 }
-// The same by polling: for the one thread that issues the products, where waking
-// from a suspended wait would be paid on every tile.
+__device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_long(g.abort, g.status, g.limit, bar, parity);
+}
+// The same, polling at first: for the one thread that issues the products,
+// where waking from a suspended wait would be paid on every tile.
 __device__ __forceinline__ bool wait_spin(const Guard& g, uint32_t bar, uint32_t parity) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
+#pragma unroll 1
+  for (int i = 0; i < 4096; ++i)
     if (mbar_test_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*g.abort) return false;
-      if (globaltimer() - t0 > g.limit) {
-        atomicCAS(g.status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
-        *g.abort = 1u;
-        return false;
-      }
-    }
-  }
+  return wait_long(g.abort, g.status, g.limit, bar, parity);
 }
 // Waits for asynchronous work that is in flight and will finish (limited all the same).
 __device__ __forceinline__ void drain(const Guard& g, uint32_t bar, uint32_t parity) {
@@ -196,8 +192,8 @@ __device__ __forceinline__ bool wait_warp(const Guard& g, uint32_t bar, uint32_t
 
 // Four E4M3 bytes as four bf16, times 2^-120: the seven bits below the sign
 // moved onto the bf16 exponent and mantissa (subnormals stay subnormal).
-__device__ __forceinline__ uint2 e4m3_bits(uint32_t w) {
-  const uint32_t m = w & 0x7f7f7f7fu, s = w & 0x80808080u;
+__device__ __forceinline__ uint2 e4m3_bits(uint32_t w, uint32_t keep) {   // keep: 0x7f7f7f7f, or 0
+  const uint32_t m = w & keep, s = w & 0x80808080u;
   const uint32_t m0 = __byte_perm(m, 0u, 0x4140), m1 = __byte_perm(m, 0u, 0x4342);   // bytes in 16-bit lanes
   const uint32_t s0 = __byte_perm(s, 0u, 0x1404), s1 = __byte_perm(s, 0u, 0x3424);   // sign at bit 15 of each
   return make_uint2(m0 * 16u + s0, m1 * 16u + s1);
@@ -228,18 +224,64 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
-// V[t] of one key for elements e .. e + 31, what of it is not finite (else 0).
-template <bool kFp8>
-__device__ __forceinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int t, int e, float (&o)[32]) {
+// What of a tree node's value row is not finite, added to the output row that a
+// thread has just written (o: bf16 output, or fp32 partial).  Rare: out of line.
+template <int D, bool kFp8, typename T>
+__device__ __noinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int t, T* o) {
   const long long row = gqa_row(a, b, t);
   if (row < 0) return;
-  const long long at = (row * a.Hkv + kvh) * a.d + e;
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
+  const long long at = (row * a.Hkv + kvh) * D;
+#pragma unroll 1
+  for (int k = 0; k < D; ++k) {
     const float x = kFp8 ? to_f32(static_cast<const __nv_fp8_e4m3*>(a.v)[at + k])
                          : to_f32(static_cast<const __nv_bfloat16*>(a.v)[at + k]);
-    if (!(fabsf(x) < INFINITY)) o[k] += x;
+    if (fabsf(x) < INFINITY) continue;
+    const float y[1] = {to_f32(o[k]) + x};
+    store_v<1>(o + k, y);
   }
+}
+// E4M3 NaN codes of a widened row: NaN in bf16, or (a tree node's values) 0.
+// True if there were any.  Rare: out of line.
+template <int D>
+__device__ __noinline__ bool patch_nan_codes(uint32_t src, uint32_t dst, int swz, int chunk_bytes, bool to_zero) {
+  bool found = false;
+#pragma unroll 1
+  for (int e = 0; e < D; ++e) {
+    uint32_t code;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(src + e) : "memory");
+    if ((code & 0x7fu) != 0x7fu) continue;
+    found = true;
+    const uint32_t at = dst + (e >> 6) * chunk_bytes + ((((e >> 3) & 7) ^ swz) << 4) + (e & 7) * 2;
+    asm volatile("st.shared.u16 [%0], %1;" :: "r"(at), "h"((unsigned short)(to_zero ? 0 : 0x7fff)) : "memory");
+  }
+  return found;
+}
+template <int N>
+__device__ __forceinline__ void pin(float (&v)[N]) {     // values loaded from TMEM: not before the wait
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+f"(v[k]));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
 }
 
 template <int D, bool kFp8>
@@ -435,20 +477,27 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       bool have = first_piece(a, plan, p), alive = true;
       int g = 0;
       uint32_t p_phase = 0u;
-      auto scores = [&](int s, int qs, uint32_t kv) {           // S_s = Q K^T
+      // operands at fixed places, as descriptors to which a byte offset / 16 is added
+      const uint64_t q_desc = smem_desc(sbase + C::kOffQ, 16, 1024);
+      const uint64_t k_desc = smem_desc(sbase + C::kOffKV, 16, 1024);
+      const uint64_t v_desc = smem_desc(sbase + C::kOffKV, C::kChunk, 1024);
+      auto scores = [&](int s, int qs, int slot) {              // S_s = Q K^T
+        const uint64_t ad = q_desc + (uint32_t)(qs * (C::kTileBytes >> 4));
+        const uint64_t bd = k_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kChunk + (kk & 3) * 32;
-          mma_bf16(tmem + C::kColS + kTile * s, smem_desc(sbase + C::kOffQ + qs * C::kTileBytes + off, 16, 1024),
-                   smem_desc(kv + off, 16, 1024), kIdescS, kk > 0);
+          constexpr uint32_t kC = C::kChunk >> 4;
+          const uint32_t off = (kk >> 2) * kC + (kk & 3) * 2;
+          mma_bf16(tmem + C::kColS + kTile * s, ad + off, bd + off, kIdescS, kk > 0);
         }
         mma_commit(BAR(B_S_FULL + s));
       };
-      auto values = [&](int s, uint32_t kv, bool first) {       // O_s (+)= P_s V
+      auto values = [&](int s, int slot, bool first) {          // O_s (+)= P_s V
+        const uint64_t bd = v_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_bf16_ts(tmem + C::kColO + D * s, tmem + C::kColS + kTile * s + 8 * kk,
-                      smem_desc(kv + kk * 16 * 128, C::kChunk, 1024), kIdescO, !first || kk > 0);
+          mma_bf16_ts(tmem + C::kColO + D * s, tmem + C::kColS + kTile * s + 8 * kk, bd + kk * 128, kIdescO,
+                      !first || kk > 0);
       };
       while (alive && have) {
         const int n = p.t1 - p.t0;
@@ -465,11 +514,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             ++g;
           }
           if (i < n) kslot = g % C::kSlots;
-          const uint32_t vaddr = sbase + C::kOffKV + vslot * C::kTileBytes;
-          const uint32_t kaddr = sbase + C::kOffKV + kslot * C::kTileBytes;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (!two && k == 1) break;
+#pragma unroll 1
+          for (int k = 0; k < (two ? 2 : 1); ++k) {
             const int s = two ? k : (i & 1);
             const bool last_k = !two || k == 1;
             if (vt >= 0) {
@@ -477,7 +523,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               p_phase ^= 1u << s;
               if (!alive) break;
               tc_fence_after();
-              values(s, vaddr, two ? vt == 0 : vt < 2);
+              values(s, vslot, two ? vt == 0 : vt < 2);
               if (last_k) mma_commit(BAR(B_KV_EMPTY + vslot));
               if (vt + (two ? 1 : 2) >= n) mma_commit(BAR(B_O_FULL + s));
             }
@@ -488,7 +534,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 ++g;
               }
               tc_fence_after();
-              scores(s, two ? s : 0, kaddr);
+              scores(s, two ? s : 0, kslot);
               if (last_k) mma_commit(BAR(B_KV_EMPTY + kslot));
               if (last_k && i == n - 1) mma_commit(BAR(B_Q_EMPTY));
             }
@@ -553,38 +599,23 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             // 2^(e + 120) as two factors, each a bf16
             const int ea = max(-126, min(127, e + 120)), eb = e + 120 - ea;
             const uint32_t fa = pow2_bf16x2(ea), fb = pow2_bf16x2(eb);
-            const bool zero = kv == 0 && t >= T, own = kv == 0 && t >= p.L && t < T;
-            bool found = false;
+            const uint32_t keep = kv == 0 && t >= T ? 0u : 0x7f7f7f7fu;   // values behind the tree: 0
             const bool two_factors = __any_sync(0xffffffffu, eb != 0);
+            uint32_t nan = 0u;                   // bit 7 of a byte: a code of all ones was seen there
             // 16-byte chunk c of the row at its XOR-permuted turn: no bank conflicts, for the
             // reads (rows D bytes apart) nor for the swizzled writes
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < D / 16; ++k) {
               const int c = D == 128 ? (k ^ swz) : (k ^ (swz & 3));
-              uint4 w = lds128(src + 16 * c);
-              if (zero) w = make_uint4(0u, 0u, 0u, 0u);
-              uint32_t u[4] = {w.x, w.y, w.z, w.w};
+              const uint4 w = lds128(src + 16 * c);
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
               uint32_t y[8];
 #pragma unroll
               for (int m = 0; m < 4; ++m) {
-                if (own) {                       // E4M3 NaN: all seven bits set
-#pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    if (((u[m] >> (8 * x)) & 0x7fu) == 0x7fu) {
-                      u[m] &= ~(0xffu << (8 * x));
-                      found = true;
-                    }
-                }
-                const uint2 z = e4m3_bits(u[m]);
+                nan |= (u[m] & keep) + 0x01010101u;
+                const uint2 z = e4m3_bits(u[m], keep);
                 y[2 * m] = mul_bf16x2(z.x, fa);
                 y[2 * m + 1] = mul_bf16x2(z.y, fa);
-                // NaN codes of other rows are 480 after the shift: make them NaN
-                if (((u[m] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {
-#pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    if (((u[m] >> (8 * x)) & 0x7fu) == 0x7fu)
-                      y[2 * m + (x >> 1)] |= (x & 1) ? 0x7fff0000u : 0x7fffu;
-                }
               }
               if (two_factors) {
 #pragma unroll
@@ -595,7 +626,11 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               sts128(half + ((j ^ swz) << 4), y[0], y[1], y[2], y[3]);
               sts128(half + (((j + 1) ^ swz) << 4), y[4], y[5], y[6], y[7]);
             }
-            if (found) atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
+            if (nan & 0x80808080u) {
+              const bool own = kv == 0 && t >= p.L;
+              if (patch_nan_codes<D>(src, dst, swz, C::kChunk, own) && own)
+                atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
+            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -616,7 +651,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (t >= p.L) {
             const uint32_t dst = sbase + C::kOffKV + slot * C::kTileBytes + row * 128;
             bool found = false;
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < D / 8; ++k) {
               const uint32_t addr = dst + (k >> 3) * C::kChunk + (((k & 7) ^ swz) << 4);
               if (t >= T) {
@@ -672,18 +707,27 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tc_fence_after();
         const bool masked = t0 + kTile > p.L;
         float mx = -INFINITY;
+        if (!masked) {
+          float v[2][32];
+          tmem_ld32(tS, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(tS + 32 * c, v);
-          tmem_wait_ld();
-          if (masked) {
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld();
+            pin(v[c & 1]);
+            if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) mx = max3(mx, v[c & 1][k], v[c & 1][k + 1]);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(tS + 32 * c, v);
+            tmem_wait_ld();
+            pin(v);
             const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
 #pragma unroll
             for (int k = 0; k < 32; ++k) mx = fmaxf(mx, (see >> k) & 1u ? v[k] : -INFINITY);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
           }
         }
         mx *= sl2;
@@ -697,11 +741,12 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
           l *= alpha;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
             tmem_ld32(tO + 32 * c, v);
             tmem_wait_ld();
+            pin(v);
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= alpha;
             tmem_st32(tO + 32 * c, v);
@@ -709,26 +754,47 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         first = false;
         const float ref = m == -INFINITY ? 0.f : -m;
+        if (!masked) {
+          const float2 scale2 = make_float2(sl2, sl2), ref2 = make_float2(ref, ref);
+          float2 sum = make_float2(0.f, 0.f);
+          float v[2][32];
+          tmem_ld32(tS, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(tS + 32 * c, v);
-          tmem_wait_ld();
-          const uint32_t see = masked ? gqa_visible(path, t0 + 32 * c, p.L) : 0xffffffffu;
-          uint32_t w[16];
-          float sum = 0.f;
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld();
+            pin(v[c & 1]);
+            if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
+            uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float x = ex2(fmaf(v[k], sl2, ref)), y = ex2(fmaf(v[k + 1], sl2, ref));
-            if (masked) {
-              x = (see >> k) & 1u ? x : 0.f;
-              y = (see >> (k + 1)) & 1u ? y : 0.f;
+            for (int k = 0; k < 32; k += 2) {
+              float2 x = fma2(make_float2(v[c & 1][k], v[c & 1][k + 1]), scale2, ref2);
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              sum = add2(sum, x);
+              w[k / 2] = pack_bf16x2(x.x, x.y);  // bf16: the tensor cores' operand type
             }
-            sum += x + y;
-            w[k / 2] = pack_bf16x2(x, y);        // bf16: the tensor cores' operand type
+            tmem_st16u(tS + 16 * c, w);          // over scores that are read already
           }
-          l += sum;
-          tmem_st16u(tS + 16 * c, w);            // over scores that are read already
+          l += sum.x + sum.y;
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(tS + 32 * c, v);
+            tmem_wait_ld();
+            pin(v);
+            const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              // a score that is not seen may be NaN: it is dropped, not multiplied away
+              const float x = (see >> k) & 1u ? ex2(fmaf(v[k], sl2, ref)) : 0.f;
+              const float y = (see >> (k + 1)) & 1u ? ex2(fmaf(v[k + 1], sl2, ref)) : 0.f;
+              l += x + y;
+              w[k / 2] = pack_bf16x2(x, y);
+            }
+            tmem_st16u(tS + 16 * c, w);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -779,13 +845,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           }
         }
         const bool bad = bad_page[p.index % kPieces] != 0u;
-        uint32_t nf[4];
-        uint32_t any_nf = 0u;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          nf[w] = p.tail() ? nonfinite[4 * (p.index % kPieces) + w] & path[w] : 0u;
-          any_nf |= nf[w];
-        }
         const bool whole = p.whole();
         const bool write = valid && !bad && !dead;
         const float inv = 1.f / l;
@@ -793,29 +852,20 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const long long slot = 2ll * blockIdx.x + (p.at != plan[2]);
         const long long prow = slot * (2 * kTile) + (two ? kTile * s : 0) + r;
         if (!whole && valid) a.part_ml[prow] = make_float2(m, write ? l : -1.f);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
           __syncwarp();                            // lanes without a row to write rejoin
           tmem_ld32(tO + 32 * c, v);
           tmem_wait_ld();
+          pin(v);
           if (merge) {
             float u[32];
             tmem_ld32(tO + D + 32 * c, u);
             tmem_wait_ld();
+            pin(u);
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = v[k] * w0 + u[k] * w1;
-          }
-          if (any_nf) {
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
-              uint32_t x = w == 0 ? nf[0] : w == 1 ? nf[1] : w == 2 ? nf[2] : nf[3];
-#pragma unroll 1
-              while (x) {
-                add_nonfinite<kFp8>(a, p.b, kvh, p.L + 32 * w + __ffs(x) - 1, 32 * c, v);
-                x &= x - 1;
-              }
-            }
           }
           if (!write) continue;
           if (whole) {
@@ -831,6 +881,18 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+        }
+        if (write && p.tail()) {
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            uint32_t x = nonfinite[4 * (p.index % kPieces) + w] &
+                         (w == 0 ? path[0] : w == 1 ? path[1] : w == 2 ? path[2] : path[3]);
+            for (; x; x &= x - 1) {
+              const int t = p.L + 32 * w + __ffs(x) - 1;
+              if (whole) add_nonfinite<D, kFp8>(a, p.b, kvh, t, static_cast<__nv_bfloat16*>(a.out) + orow * D);
+              else add_nonfinite<D, kFp8>(a, p.b, kvh, t, a.part_o + prow * D);
+            }
           }
         }
         tc_fence_before();
