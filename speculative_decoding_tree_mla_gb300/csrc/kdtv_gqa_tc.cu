@@ -48,16 +48,17 @@ using namespace ptx;
 
 constexpr int kTile = 128;                  // rows of a score tile, keys of a key tile
 constexpr int kThreads = 512;
-constexpr int kWarpAux = 8, kWarpTma = 12, kWarpMma = 13;
+constexpr int kWarpAux = 8, kWarpTma = 12, kWarpMma = 13, kWarpPlan = 14;
 constexpr int kRing = 8;                    // bound on ring sizes (barriers)
-constexpr int kPieces = 8;                  // pieces whose flags may be in flight
+constexpr int kPieces = 8;                  // pieces that may be in flight
 
 // barriers
 enum {
   B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + kRing, B_RAW_FULL = B_KV_EMPTY + kRing,
   B_RAW_EMPTY = B_RAW_FULL + kRing, B_TAIL = B_RAW_EMPTY + kRing, B_Q_FULL = B_TAIL + kRing,
   B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 2, B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2,
-  B_O1_FREE, B_MMA_DONE, B_STALL, B_COUNT
+  B_O1_FREE, B_MMA_DONE, B_STALL, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
+  B_COUNT = B_PIECE_READ + kPieces
 };
 
 template <int D, bool kFp8>
@@ -72,7 +73,10 @@ struct Cfg {
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
   static constexpr int kOffMisc = kOffRaw + kRaw * kRawBytes;
-  static constexpr int kMiscBytes = B_COUNT * 8 + 64 + kPieces * 4 + kPieces * 16 + kTile * 8;
+  // barriers (padded to 16 bytes), TMEM address and abort flag, then per piece its record, the
+  // page flag and the key mask, and stream 1's {max, sum}
+  static constexpr int kBarBytes = (B_COUNT * 8 + 15) / 16 * 16;
+  static constexpr int kMiscBytes = kBarBytes + 16 + kPieces * (32 + 16 + 4) + kTile * 8;
   static constexpr int kSmem = kOffMisc + kMiscBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColS = 0, kColO = 2 * kTile;     // S0, S1, O0, O1
@@ -101,52 +105,17 @@ __device__ __forceinline__ int units_of(const GqaArgs& a, int b) {
   return n > 0 ? a.Hkv * row_pairs(a, n) * key_tiles(L, n) : 0;
 }
 
-struct Piece {
-  int b, L, n, nt, rps;      // request, prefix, live nodes, key tiles, pairs of row tiles
-  int item;                  // kvh * rps + pair within the request
-  int t0, t1;                // key tiles
-  int at;                    // unit of t0
-  int index;                 // of this CTA's pieces
-  __device__ __forceinline__ int kvh() const { return item / rps; }
-  __device__ __forceinline__ int pair() const { return item % rps; }
-  __device__ __forceinline__ bool two(const GqaArgs& a) const { return n - pair() * 2 * a.npt > a.npt; }
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
-  __device__ __forceinline__ bool tail() const { return t1 == nt || t1 * kTile > L; }
+// A piece: the part of an item in one CTA.  The planning warp walks the CTA's
+// units and hands the pieces to the other roles through a ring in shared memory.
+struct __align__(16) Piece {
+  int b, L, n, kvh;          // request, its prefix and live nodes, key/value head
+  int node0, t0, t1, flags;  // first node of its first tile, key tiles
+  __device__ __forceinline__ bool two() const { return flags & 1; }      // two tiles of rows
+  __device__ __forceinline__ bool whole() const { return flags & 2; }    // all key tiles of the item
+  __device__ __forceinline__ bool tail() const { return flags & 4; }     // reaches past the prefix
+  __device__ __forceinline__ bool later() const { return flags & 8; }    // not at the CTA's first unit
 };
-__device__ __forceinline__ void load_request(const GqaArgs& a, Piece& p) {
-  gqa_request(a, p.b, &p.L, &p.n);
-  p.nt = p.n > 0 ? key_tiles(p.L, p.n) : 0;
-  p.rps = p.n > 0 ? row_pairs(a, p.n) : 1;
-}
-// plan: {first request, unit within it, first unit, end}
-__device__ __noinline__ bool first_piece(const GqaArgs& a, const int* plan, Piece& p) {
-  const int beg = plan[2], end = plan[3];
-  if (beg >= end) return false;
-  p.b = plan[0];
-  load_request(a, p);
-  p.item = plan[1] / p.nt;
-  p.t0 = plan[1] % p.nt;
-  p.t1 = min(p.nt, p.t0 + end - beg);
-  p.at = beg;
-  p.index = 0;
-  return true;
-}
-__device__ __noinline__ bool next_piece(const GqaArgs& a, const int* plan, Piece& p) {
-  p.at += p.t1 - p.t0;
-  const int end = plan[3];
-  if (p.at >= end) return false;
-  ++p.index;
-  if (++p.item == a.Hkv * p.rps) {
-    p.item = 0;
-    do {
-      ++p.b;
-      load_request(a, p);
-    } while (p.nt == 0);          // units are left, so such a request exists
-  }
-  p.t0 = 0;
-  p.t1 = min(p.nt, end - p.at);
-  return true;
-}
+constexpr int kEnd = 16;     // flag: no piece is left
 
 // ---- bounded waits -------------------------------------------------------------------------
 struct Guard {
@@ -295,11 +264,11 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffMisc);
   const uint32_t bar0 = smem_u32(bars);
   auto BAR = [&](int i) { return bar0 + 8u * i; };
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + B_COUNT);   // [0] tmem, [1] abort, [4..7] plan
-  int* plan = reinterpret_cast<int*>(misc + 4);
-  volatile uint32_t* bad_page = misc + 16;                         // [kPieces]
-  uint32_t* nonfinite = misc + 16 + kPieces;                       // [kPieces][4] keys of the tree
-  float2* ml1 = reinterpret_cast<float2*>(nonfinite + 4 * kPieces);   // [128] stream 1's {max, sum}
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + C::kBarBytes);   // [0] tmem, [1] abort
+  Piece* pieces = reinterpret_cast<Piece*>(misc + 4);                 // [kPieces]
+  uint4* nonfinite = reinterpret_cast<uint4*>(pieces + kPieces);      // [kPieces] keys of the tree
+  volatile uint32_t* bad_page = reinterpret_cast<uint32_t*>(nonfinite + kPieces);   // [kPieces]
+  float2* ml1 = reinterpret_cast<float2*>(smem + C::kOffMisc + C::kMiscBytes - kTile * 8);   // [128]
   const Guard guard{misc + 1, a.status, stall ? 20000000ull : 2000000000ull};
 
   grid_dep_launch();               // the combine kernel may be launched; it waits for this grid
@@ -323,6 +292,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     mbar_init(BAR(B_O1_FREE), 4);
     mbar_init(BAR(B_MMA_DONE), 1);
     mbar_init(BAR(B_STALL), 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(BAR(B_PIECE + i), 1);
+      mbar_init(BAR(B_PIECE_READ + i), 14);      // producer, issuer, 4 + 8 warps
+    }
     fence_mbar_init();
   }
   if (threadIdx.x < kPieces) bad_page[threadIdx.x] = 0u;
@@ -335,16 +308,31 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if (warp == 0) {
-    // W and this CTA's first request: one pass for the total, one to its start
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  // The k-th piece (k counts up in every role); false: none is left, or the CTA gave up.
+  auto get_piece = [&](int k, Piece& p) -> bool {
+    if (!wait_warp(guard, BAR(B_PIECE + k % kPieces), (k / kPieces) & 1)) return false;
+    p = pieces[k % kPieces];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(B_PIECE_READ + k % kPieces));
+    return !(p.flags & kEnd);
+  };
+
+  if (warp == kWarpPlan) {
+    // ---- planner: W and this CTA's first unit (one pass over the requests for the total, one
+    // to the unit), then its pieces
     int sum = 0;
     for (int b = lane; b < a.B; b += 32) sum += units_of(a, b);
     sum = __reduce_add_sync(0xffffffffu, sum);
     const int W = (sum + a.ctas - 1) / a.ctas;
-    const long long beg = (long long)blockIdx.x * W;
-    if (beg >= sum) {
-      if (lane == 0) plan[2] = plan[3] = 0;
-    } else {
+    const long long first = (long long)blockIdx.x * W;
+    const int end = first < sum ? (int)(first + W < sum ? first + W : sum) : 0;
+    int at = first < sum ? (int)first : 0, b = 0, off = 0;
+    if (end > 0) {
       int before = 0;
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int u = b0 + lane < a.B ? units_of(a, b0 + lane) : 0;
@@ -355,23 +343,54 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (lane >= o) scan += x;
         }
         const int lo = before + scan - u;
-        if (u > 0 && beg >= lo && beg < lo + u) {
-          plan[0] = b0 + lane;
-          plan[1] = (int)(beg - lo);
-          plan[2] = (int)beg;
-          plan[3] = (int)(beg + W < sum ? beg + W : sum);
+        const uint32_t here = __ballot_sync(0xffffffffu, u > 0 && at >= lo && at < lo + u);
+        if (here) {
+          b = b0 + __ffs(here) - 1;
+          off = at - __shfl_sync(0xffffffffu, lo, __ffs(here) - 1);
+          break;
         }
         before += __shfl_sync(0xffffffffu, scan, 31);
-        if (before > beg) break;
       }
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = misc[0];
-
-  if (warp == kWarpTma) {
+    int L = 0, n = 0, nt = 1, rps = 1, kvh = 0, pair = 0, t0 = 0;
+    if (end > 0) {
+      gqa_request(a, b, &L, &n);
+      nt = key_tiles(L, n);
+      rps = row_pairs(a, n);
+      t0 = off % nt;
+      kvh = off / nt / rps;
+      pair = off / nt % rps;
+    }
+    for (int k = 0;; ++k) {
+      if (k >= kPieces && !wait_warp(guard, BAR(B_PIECE_READ + k % kPieces), (k / kPieces - 1) & 1)) break;
+      const int t1 = min(nt, t0 + end - at);
+      if (lane == 0) {
+        Piece p;
+        p.b = b; p.L = L; p.n = n; p.kvh = kvh;
+        p.node0 = pair * 2 * a.npt;
+        p.t0 = t0; p.t1 = t1;
+        p.flags = (n - p.node0 > a.npt ? 1 : 0) | (t0 == 0 && t1 == nt ? 2 : 0) |
+                  (t1 == nt || t1 * kTile > L ? 4 : 0) | (k > 0 ? 8 : 0) | (at >= end ? kEnd : 0);
+        pieces[k % kPieces] = p;
+        mbar_arrive(BAR(B_PIECE + k % kPieces));
+      }
+      __syncwarp();
+      if (at >= end) break;
+      at += t1 - t0;
+      t0 = 0;
+      if (at < end && ++pair == rps) {
+        pair = 0;
+        if (++kvh == a.Hkv) {
+          kvh = 0;
+          do {
+            gqa_request(a, ++b, &L, &n);         // units are left, so a request with some exists
+          } while (n == 0);
+          nt = key_tiles(L, n);
+          rps = row_pairs(a, n);
+        }
+      }
+    }
+  } else if (warp == kWarpTma) {
     // ---- TMA producer: the warp's lanes hold page ids; lane l loads box l of a tile ---------
     const int boxes = a.page_size ? kTile / a.page_size : 1;      // page_size divides 128
     const int box_rows = kTile / boxes;
@@ -380,14 +399,14 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     constexpr int kEntryBytes = kFp8 ? C::kRawBytes : C::kTileBytes;
     const uint32_t ring = sbase + (kFp8 ? C::kOffRaw : C::kOffKV);
     Piece p;
-    bool have = first_piece(a, plan, p), alive = true;
-    if (stall && have) alive = wait_warp(guard, BAR(B_STALL), 0);
+    bool alive = true;
+    if (stall) alive = wait_warp(guard, BAR(B_STALL), 0);
     int g = 0, q_loads = 0;
-    while (alive && have) {
-      const int kvh = p.kvh(), n = p.t1 - p.t0, T = p.L + p.n;
-      const bool two = p.two(a);
+    for (int index = 0; alive && get_piece(index, p); ++index) {
+      const int kvh = p.kvh, n = p.t1 - p.t0, T = p.L + p.n;
+      const bool two = p.two();
       const int lag = two ? 1 : 2;
-      if (p.index > 0) alive = wait_warp(guard, BAR(B_Q_EMPTY), (p.index - 1) & 1);
+      if (index > 0) alive = wait_warp(guard, BAR(B_Q_EMPTY), (index - 1) & 1);
       if (!alive) break;
       if (lane == 0) {
         const uint32_t bytes = (uint32_t)a.npt * a.G * 128;
@@ -395,7 +414,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int s = 0; s < (two ? 2 : 1); ++s)
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + c * C::kChunk, &tm_q, BAR(B_Q_FULL), 64 * c,
-                        kvh * a.G, p.b * a.N + (2 * p.pair() + s) * a.npt);
+                        kvh * a.G, p.b * a.N + p.node0 + s * a.npt);
       }
       ++q_loads;
       // windows of 32 page ids, the next one loaded ahead; a page out of range is read as page 0
@@ -426,7 +445,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (i == n - 1) {                       // before the piece's last loads: seen by its epilogue
             const bool any = __any_sync(0xffffffffu, bad);
             if (lane == 0) {
-              bad_page[p.index % kPieces] = any ? 1u : 0u;
+              bad_page[index % kPieces] = any ? 1u : 0u;
               if (any) gqa_error(a, KDTV_ERR_BAD_PAGE);
             }
           }
@@ -461,8 +480,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           ++g;
         }
       }
-      if (!alive) break;
-      have = next_piece(a, plan, p);
     }
     // every copy has landed before the CTA may exit
     if (q_loads) drain(guard, BAR(B_Q_FULL), (q_loads - 1) & 1);
@@ -470,11 +487,11 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       drain(guard, BAR(full0 + x % kEntries), (x / kEntries) & 1);
     __syncwarp();
   } else if (warp == kWarpMma) {
-    // ---- MMA issuer -----------------------------------------------------------------------
-    if (lane == 0) {
+    // ---- MMA issuer (one lane; the others follow piece by piece) --------------------------------
+    {
       constexpr uint32_t kIdescS = idesc_bf16(kTile, kTile, 0, 0), kIdescO = idesc_bf16(kTile, D, 0, 1);
       Piece p;
-      bool have = first_piece(a, plan, p), alive = true;
+      bool alive = true;
       int g = 0;
       uint32_t p_phase = 0u;
       // operands at fixed places, as descriptors to which a byte offset / 16 is added
@@ -499,11 +516,12 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           mma_bf16_ts(tmem + C::kColO + D * s, tmem + C::kColS + kTile * s + 8 * kk, bd + kk * 128, kIdescO,
                       !first || kk > 0);
       };
-      while (alive && have) {
+      for (int index = 0; __all_sync(0xffffffffu, alive) && get_piece(index, p); ++index) {
         const int n = p.t1 - p.t0;
-        const bool two = p.two(a);
+        const bool two = p.two();
         const int lag = two ? 1 : 2;
-        alive = wait_spin(guard, BAR(B_Q_FULL), p.index & 1);
+        if (lane != 0) continue;
+        alive = wait_spin(guard, BAR(B_Q_FULL), index & 1);
         for (int i = 0; alive && i < n + lag; ++i) {
           int vslot = 0, kslot = 0;
           const int vt = i - lag;
@@ -540,11 +558,11 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
           }
         }
-        if (!alive) break;
-        have = next_piece(a, plan, p);
       }
-      mma_commit(BAR(B_MMA_DONE));                 // every product has finished before TMEM is freed
-      drain(guard, BAR(B_MMA_DONE), 0);
+      if (lane == 0) {
+        mma_commit(BAR(B_MMA_DONE));               // every product has finished before TMEM is freed
+        drain(guard, BAR(B_MMA_DONE), 0);
+      }
     }
     __syncwarp();
   } else if (warp >= kWarpAux && warp < kWarpTma) {
@@ -552,13 +570,13 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int row = threadIdx.x - kWarpAux * 32;
     const int swz = row & 7;
     Piece p;
-    bool have = first_piece(a, plan, p), alive = true;
+    bool alive = true;
     int g = 0;
     uint32_t tail_phase = 0u;
-    while (alive && have) {
-      const int kvh = p.kvh(), n = p.t1 - p.t0, T = p.L + p.n;
-      const int lag = p.two(a) ? 1 : 2;
-      uint32_t* nf = nonfinite + 4 * (p.index % kPieces);
+    for (int index = 0; alive && get_piece(index, p); ++index) {
+      const int kvh = p.kvh, n = p.t1 - p.t0, T = p.L + p.n;
+      const int lag = p.two() ? 1 : 2;
+      uint32_t* nf = reinterpret_cast<uint32_t*>(nonfinite + index % kPieces);
       if (row < 4) nf[row] = 0u;
       asm volatile("bar.sync 2, 128;" ::: "memory");
       if constexpr (kFp8) {
@@ -674,8 +692,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         g += 2 * n;
       }
-      if (!alive) break;
-      have = next_piece(a, plan, p);
     }
   } else if (warp < kWarpAux) {
     // ---- softmax and epilogue: thread = row 32 q + lane of stream s -----------------------------
@@ -683,14 +699,15 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t tS = tmem + lanes + C::kColS + kTile * s, tO = tmem + lanes + C::kColO + D * s;
     const float sl2 = a.scale * 1.4426950408889634f;      // base-2 exponentials
+    const int r_node = r / a.G, r_head = r % a.G;
     Piece p;
-    bool have = first_piece(a, plan, p), alive = true;
+    bool alive = true;
     uint32_t s_phase = 0u, o_phase = 0u, one_pieces = 0u;
-    while (alive && have) {
-      const int n = p.t1 - p.t0, kvh = p.kvh();
-      const bool two = p.two(a);
-      const int node = (2 * p.pair() + (two ? s : 0)) * a.npt + r / a.G;
-      const bool valid = r < a.npt * a.G && node < p.n;
+    for (int index = 0; alive && get_piece(index, p); ++index) {
+      const int n = p.t1 - p.t0, kvh = p.kvh;
+      const bool two = p.two();
+      const int node = p.node0 + (two && s ? a.npt : 0) + r_node;
+      const bool valid = r_node < a.npt && node < p.n;
       uint32_t path[4] = {0u, 0u, 0u, 0u};
       bool dead = false;
       if (valid && p.tail()) {
@@ -844,12 +861,12 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             m = mm;
           }
         }
-        const bool bad = bad_page[p.index % kPieces] != 0u;
+        const bool bad = bad_page[index % kPieces] != 0u;
         const bool whole = p.whole();
         const bool write = valid && !bad && !dead;
         const float inv = 1.f / l;
-        const long long orow = ((long long)p.b * a.N + node) * a.H + (long long)kvh * a.G + r % a.G;
-        const long long slot = 2ll * blockIdx.x + (p.at != plan[2]);
+        const long long orow = ((long long)p.b * a.N + node) * a.H + (long long)kvh * a.G + r_head;
+        const long long slot = 2ll * blockIdx.x + p.later();
         const long long prow = slot * (2 * kTile) + (two ? kTile * s : 0) + r;
         if (!whole && valid) a.part_ml[prow] = make_float2(m, write ? l : -1.f);
 #pragma unroll 1
@@ -884,14 +901,15 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           }
         }
         if (write && p.tail()) {
+          const uint4 nf = nonfinite[index % kPieces];
+          uint32_t x[4] = {nf.x & path[0], nf.y & path[1], nf.z & path[2], nf.w & path[3]};
+          if (x[0] | x[1] | x[2] | x[3]) {
 #pragma unroll 1
-          for (int w = 0; w < 4; ++w) {
-            uint32_t x = nonfinite[4 * (p.index % kPieces) + w] &
-                         (w == 0 ? path[0] : w == 1 ? path[1] : w == 2 ? path[2] : path[3]);
-            for (; x; x &= x - 1) {
-              const int t = p.L + 32 * w + __ffs(x) - 1;
-              if (whole) add_nonfinite<D, kFp8>(a, p.b, kvh, t, static_cast<__nv_bfloat16*>(a.out) + orow * D);
-              else add_nonfinite<D, kFp8>(a, p.b, kvh, t, a.part_o + prow * D);
+            for (int j = 0; j < p.n; ++j) {
+              const uint32_t word = j < 32 ? x[0] : j < 64 ? x[1] : j < 96 ? x[2] : x[3];
+              if (!((word >> (j & 31)) & 1u)) continue;
+              if (whole) add_nonfinite<D, kFp8>(a, p.b, kvh, p.L + j, static_cast<__nv_bfloat16*>(a.out) + orow * D);
+              else add_nonfinite<D, kFp8>(a, p.b, kvh, p.L + j, a.part_o + prow * D);
             }
           }
         }
@@ -902,7 +920,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (lane == 0) mbar_arrive(BAR(B_O1_FREE));
         }
       }
-      have = next_piece(a, plan, p);
     }
   }
   tc_fence_before();
@@ -955,10 +972,9 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant_
     const int c0 = start / W, c1 = (end - 1) / W;
     if (c0 == c1) continue;                        // whole: written by its CTA
     const int r = (tile & 1) * kTile + (node % a.npt) * a.G + h % a.G;
-    auto prow = [&](int c) {
-      const long long slot = 2ll * c + (c == c0 && start != c0 * W);
-      return slot * (2 * kTile) + r;
-    };
+    const bool later = start != c0 * W;            // of the first piece; the others start their CTA's range
+    auto prow = [&](int c) { return (2ll * c + (c == c0 && later)) * (2 * kTile) + r; };
+    // lane k: {max, sum} of piece k of each 32, and the weight that brings it to the common maximum
     float m = -INFINITY;
     bool skip = false;
     for (int c = c0 + lane; c <= c1; c += 32) {
@@ -973,23 +989,41 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant_
     float l = 0.f, o[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const long long pr = prow(c);
-      const float2 ml = a.part_ml[pr];
-      const float w = ex2(ml.x - ref);
-      l += ml.y * w;
-      const float* src = a.part_o + pr * D + V * lane;
+    for (int cb = c0; cb <= c1; cb += 32) {
+      const int cl = min(cb + lane, c1);
+      const float2 ml = a.part_ml[prow(cl)];
+      const float w = cb + lane <= c1 ? ex2(ml.x - ref) : 0.f;
+      if (cb + lane <= c1) l += ml.y * w;
+      const int count = min(32, c1 - cb + 1);
+      for (int j = 0; j < count; j += 8) {         // eight partial rows in flight
+        float x[8][V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = fmaf(src[k], w, o[k]);
+        for (int k = 0; k < 8; ++k) {
+          const float* src = a.part_o + prow(min(cb + j + k, c1)) * D + V * lane;
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(src + e);
+            x[k][e] = f.x;
+            x[k][e + 1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (j + k) & 31);
+          if (j + k < count) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = fmaf(x[k][e], wk, o[e]);
+          }
+        }
+      }
     }
-    const float inv = 1.f / l;
-    uint32_t y[V / 2];
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) y[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
+    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    const float inv = 1.f / l;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
                                                 (((long long)b * a.N + node) * a.H + h) * D) + V / 2 * lane;
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) dst[k] = y[k];
+    for (int k = 0; k < V / 2; ++k) dst[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
   }
 }
 
@@ -1018,8 +1052,9 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
   if (launch_ex(kern, dim3((unsigned)a.ctas), dim3(kThreads), C::kSmem, st, false, tq, tk, tv, a, stall ? 1 : 0) !=
       cudaSuccess)
     return KDTV_ERR_CUDA;
-  // rows of a request in up to 16 CTAs, 8 rows at a time
-  const int gx = (a.N * a.H + 63) / 64 < 64 ? (a.N * a.H + 63) / 64 : 64;
+  // a warp per row, up to about eight CTAs per SM
+  const long long want = ((long long)a.N * a.H + 7) / 8, most = 8ll * a.ctas / a.B + 1;
+  const int gx = (int)(want < most ? want : most);
   if (launch_ex(gqa_combine_kernel<D>, dim3((unsigned)gx, (unsigned)a.B), dim3(256), 0, st, true, a) != cudaSuccess)
     return KDTV_ERR_CUDA;
   return KDTV_OK;
