@@ -48,7 +48,7 @@ using namespace ptx;
 
 constexpr int kTile = 128;                  // rows of a score tile, keys of a key tile
 constexpr int kThreads = 512;
-constexpr int kWarpAux = 8, kWarpTma = 12, kWarpMma = 13, kWarpPlan = 14;
+constexpr int kWarpAux = 8, kWarpTma = 12, kWarpPlan = 13, kWarpMma = 14;   // (14, 15: one per stream)
 constexpr int kRing = 8;                    // bound on ring sizes (barriers)
 constexpr int kPieces = 8;                  // pieces that may be in flight
 
@@ -123,8 +123,8 @@ struct Guard {
   unsigned int* status;
   uint64_t limit;
 };
-// (the rest of a wait is out of line: the roles' loops have to share an instruction cache)
-__device__ __noinline__ bool wait_long(volatile uint32_t* abort, unsigned int* status, uint64_t limit,
+
+__device__ __forceinline__ bool wait_long(volatile uint32_t* abort, unsigned int* status, uint64_t limit,
                                        uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   for (;;) {
@@ -138,7 +138,10 @@ __device__ __noinline__ bool wait_long(volatile uint32_t* abort, unsigned int* s
   }
 }
 __device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  // the clock is read only in a wait that lasts: reading it costs more than a key tile's softmax
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   return wait_long(g.abort, g.status, g.limit, bar, parity);
 }
 // The same, polling at first: for the one thread that issues the products,
@@ -225,6 +228,18 @@ __device__ __noinline__ bool patch_nan_codes(uint32_t src, uint32_t dst, int swz
   }
   return found;
 }
+// Register split: the launch has 512 x 128; the softmax warps take most (a row's
+// 128 scores stay in registers).
+constexpr int kRegsSoftmax = 192, kRegsAux = 64, kRegsControl = 64;
+static_assert(256 * kRegsSoftmax + 128 * kRegsAux + 128 * kRegsControl <= 512 * 128, "registers of the launch");
+template <int R>
+__device__ __forceinline__ void reg_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R));
+}
+template <int R>
+__device__ __forceinline__ void reg_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R));
+}
 template <int N>
 __device__ __forceinline__ void pin(float (&v)[N]) {     // values loaded from TMEM: not before the wait
 #pragma unroll
@@ -276,13 +291,13 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     misc[1] = 0u;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(BAR(B_KV_FULL + i), kFp8 ? 4 : 1);
-      mbar_init(BAR(B_KV_EMPTY + i), 1);
+      mbar_init(BAR(B_KV_EMPTY + i), 2);      // both issuers
       mbar_init(BAR(B_RAW_FULL + i), 1);
       mbar_init(BAR(B_RAW_EMPTY + i), 4);
       mbar_init(BAR(B_TAIL + i), 1);
     }
     mbar_init(BAR(B_Q_FULL), 1);
-    mbar_init(BAR(B_Q_EMPTY), 1);
+    mbar_init(BAR(B_Q_EMPTY), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(B_S_FULL + i), 1);
       mbar_init(BAR(B_P_READY + i), 4);
@@ -290,11 +305,11 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
     mbar_init(BAR(B_ML), 4);
     mbar_init(BAR(B_O1_FREE), 4);
-    mbar_init(BAR(B_MMA_DONE), 1);
+    mbar_init(BAR(B_MMA_DONE), 2);
     mbar_init(BAR(B_STALL), 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(BAR(B_PIECE + i), 1);
-      mbar_init(BAR(B_PIECE_READ + i), 14);      // producer, issuer, 4 + 8 warps
+      mbar_init(BAR(B_PIECE_READ + i), 15);      // producer, two issuers, 4 + 8 warps
     }
     fence_mbar_init();
   }
@@ -322,6 +337,9 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     return !(p.flags & kEnd);
   };
 
+  // (the split is the first statement of each branch: the compiler allocates by branch)
+  if (warp >= kWarpTma) {
+  reg_shrink<kRegsControl>();
   if (warp == kWarpPlan) {
     // ---- planner: W and this CTA's first unit (one pass over the requests for the total, one
     // to the unit), then its pieces
@@ -486,86 +504,89 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     for (int x = g > kEntries ? g - kEntries : 0; x < g; ++x)
       drain(guard, BAR(full0 + x % kEntries), (x / kEntries) & 1);
     __syncwarp();
-  } else if (warp == kWarpMma) {
-    // ---- MMA issuer (one lane; the others follow piece by piece) --------------------------------
-    {
-      constexpr uint32_t kIdescS = idesc_bf16(kTile, kTile, 0, 0), kIdescO = idesc_bf16(kTile, D, 0, 1);
-      Piece p;
-      bool alive = true;
-      int g = 0;
-      uint32_t p_phase = 0u;
-      // operands at fixed places, as descriptors to which a byte offset / 16 is added
-      const uint64_t q_desc = smem_desc(sbase + C::kOffQ, 16, 1024);
-      const uint64_t k_desc = smem_desc(sbase + C::kOffKV, 16, 1024);
-      const uint64_t v_desc = smem_desc(sbase + C::kOffKV, C::kChunk, 1024);
-      auto scores = [&](int s, int qs, int slot) {              // S_s = Q K^T
-        const uint64_t ad = q_desc + (uint32_t)(qs * (C::kTileBytes >> 4));
-        const uint64_t bd = k_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          constexpr uint32_t kC = C::kChunk >> 4;
-          const uint32_t off = (kk >> 2) * kC + (kk & 3) * 2;
-          mma_bf16(tmem + C::kColS + kTile * s, ad + off, bd + off, kIdescS, kk > 0);
-        }
-        mma_commit(BAR(B_S_FULL + s));
-      };
-      auto values = [&](int s, int slot, bool first) {          // O_s (+)= P_s V
-        const uint64_t bd = v_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_bf16_ts(tmem + C::kColO + D * s, tmem + C::kColS + kTile * s + 8 * kk, bd + kk * 128, kIdescO,
-                      !first || kk > 0);
-      };
-      for (int index = 0; __all_sync(0xffffffffu, alive) && get_piece(index, p); ++index) {
-        const int n = p.t1 - p.t0;
-        const bool two = p.two();
-        const int lag = two ? 1 : 2;
-        if (lane != 0) continue;
-        alive = wait_spin(guard, BAR(B_Q_FULL), index & 1);
-        for (int i = 0; alive && i < n + lag; ++i) {
-          int vslot = 0, kslot = 0;
-          const int vt = i - lag;
-          if (vt >= 0) {
-            vslot = g % C::kSlots;
-            alive = wait_spin(guard, BAR(B_KV_FULL + vslot), (g / C::kSlots) & 1);
-            if (!alive) break;
-            ++g;
+  } else {
+    // ---- MMA issuers: warp 14 + s issues stream s (one lane of it; the others follow piece by
+    // piece).  A thread needs a few hundred cycles from a wait to its next product, about as long
+    // as the products it then issues take, so the streams' issuers are two warps.  Each waits on
+    // every entry of the ring, also the other stream's, so that it sees each phase of the barriers.
+    const int s = warp - kWarpMma;
+    constexpr uint32_t kIdescS = idesc_bf16(kTile, kTile, 0, 0), kIdescO = idesc_bf16(kTile, D, 0, 1);
+    // operands at fixed places, as descriptors to which a byte offset / 16 is added
+    const uint64_t q_desc = smem_desc(sbase + C::kOffQ, 16, 1024);
+    const uint64_t k_desc = smem_desc(sbase + C::kOffKV, 16, 1024);
+    const uint64_t v_desc = smem_desc(sbase + C::kOffKV, C::kChunk, 1024);
+    const uint32_t dS = tmem + C::kColS + kTile * s, dO = tmem + C::kColO + D * s;
+    Piece p;
+    bool alive = true;
+    int slot = 0;
+    uint32_t phase = 0u, p_phase = 0u;
+    for (int index = 0; __all_sync(0xffffffffu, alive) && get_piece(index, p); ++index) {
+      const int n = p.t1 - p.t0;
+      const bool two = p.two();
+      const int lag = two ? 1 : 2;
+      if (lane != 0) continue;
+      const uint64_t ad = q_desc + (uint32_t)(two ? s * (C::kTileBytes >> 4) : 0);
+      alive = wait_spin(guard, BAR(B_Q_FULL), index & 1);
+      for (int i = 0; alive && i < n + lag; ++i) {
+        const int vt = i - lag;
+        const bool mine = two || (i & 1) == s;
+        if (vt >= 0) {                                          // O_s (+)= P_s V
+          alive = wait_spin(guard, BAR(B_KV_FULL + slot), phase);
+          if (alive && mine) {
+            alive = wait_spin(guard, BAR(B_P_READY + s), p_phase);
+            p_phase ^= 1u;
           }
-          if (i < n) kslot = g % C::kSlots;
-#pragma unroll 1
-          for (int k = 0; k < (two ? 2 : 1); ++k) {
-            const int s = two ? k : (i & 1);
-            const bool last_k = !two || k == 1;
-            if (vt >= 0) {
-              alive = wait_spin(guard, BAR(B_P_READY + s), (p_phase >> s) & 1);
-              p_phase ^= 1u << s;
-              if (!alive) break;
-              tc_fence_after();
-              values(s, vslot, two ? vt == 0 : vt < 2);
-              if (last_k) mma_commit(BAR(B_KV_EMPTY + vslot));
-              if (vt + (two ? 1 : 2) >= n) mma_commit(BAR(B_O_FULL + s));
-            }
-            if (i < n) {
-              if (k == 0) {
-                alive = wait_spin(guard, BAR(B_KV_FULL + kslot), (g / C::kSlots) & 1);
-                if (!alive) break;
-                ++g;
-              }
-              tc_fence_after();
-              scores(s, two ? s : 0, kslot);
-              if (last_k) mma_commit(BAR(B_KV_EMPTY + kslot));
-              if (last_k && i == n - 1) mma_commit(BAR(B_Q_EMPTY));
-            }
+          if (!alive) break;
+          if (mine) {
+            tc_fence_after();
+            const uint64_t bd = v_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
+            const uint32_t acc = two ? vt > 0 : vt > 1;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, kk > 0 ? 1u : acc);
+            mma_commit(BAR(B_KV_EMPTY + slot));
+            if (vt + (two ? 1 : 2) >= n) mma_commit(BAR(B_O_FULL + s));
+          } else {
+            mbar_arrive(BAR(B_KV_EMPTY + slot));
+          }
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
-      }
-      if (lane == 0) {
-        mma_commit(BAR(B_MMA_DONE));               // every product has finished before TMEM is freed
-        drain(guard, BAR(B_MMA_DONE), 0);
+        if (i < n) {                                            // S_s = Q K^T, over P_s
+          alive = wait_spin(guard, BAR(B_KV_FULL + slot), phase);
+          if (!alive) break;
+          if (mine) {
+            tc_fence_after();
+            const uint64_t bd = k_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              constexpr uint32_t kC = C::kChunk >> 4;
+              const uint32_t off = (kk >> 2) * kC + (kk & 3) * 2;
+              mma_bf16(dS, ad + off, bd + off, kIdescS, kk > 0);
+            }
+            mma_commit(BAR(B_S_FULL + s));
+            mma_commit(BAR(B_KV_EMPTY + slot));
+          } else {
+            mbar_arrive(BAR(B_KV_EMPTY + slot));
+          }
+          if (i == n - 1) mma_commit(BAR(B_Q_EMPTY));
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
       }
     }
+    if (lane == 0) {
+      mma_commit(BAR(B_MMA_DONE));                 // every product has finished before TMEM is freed
+      drain(guard, BAR(B_MMA_DONE), 0);
+    }
     __syncwarp();
-  } else if (warp >= kWarpAux && warp < kWarpTma) {
+  }
+  } else if (warp >= kWarpAux) {
+    reg_shrink<kRegsAux>();
     // ---- widening (one-byte caches) and the last tiles: thread = key row of the tile -----------
     const int row = threadIdx.x - kWarpAux * 32;
     const int swz = row & 7;
@@ -693,7 +714,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         g += 2 * n;
       }
     }
-  } else if (warp < kWarpAux) {
+  } else {
+    reg_grow<kRegsSoftmax>();
     // ---- softmax and epilogue: thread = row 32 q + lane of stream s -----------------------------
     const int s = warp >> 2, q = warp & 3, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
@@ -723,30 +745,26 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!alive) break;
         tc_fence_after();
         const bool masked = t0 + kTile > p.L;
-        float mx = -INFINITY;
-        if (!masked) {
-          float v[2][32];
-          tmem_ld32(tS, v[0]);
+        float v[kTile];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<float(&)[32]>(v[32 * c]));
+        tmem_wait_ld();
+        pin(v);
+        if (masked) {                            // dropped, whatever it is: a masked score may be NaN
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            tmem_wait_ld();
-            pin(v[c & 1]);
-            if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) mx = max3(mx, v[c & 1][k], v[c & 1][k + 1]);
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            tmem_ld32(tS + 32 * c, v);
-            tmem_wait_ld();
-            pin(v);
             const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, (see >> k) & 1u ? v[k] : -INFINITY);
+            for (int k = 0; k < 32; ++k) v[32 * c + k] = (see >> k) & 1u ? v[32 * c + k] : -INFINITY;
           }
         }
+        float mx0 = max3(v[0], v[1], v[2]), mx1 = max3(v[3], v[4], v[5]);
+#pragma unroll
+        for (int k = 6; k + 3 < kTile; k += 4) {
+          mx0 = max3(mx0, v[k], v[k + 1]);
+          mx1 = max3(mx1, v[k + 2], v[k + 3]);
+        }
+        float mx = max3(mx0, mx1, fmaxf(v[126], v[127]));
         mx *= sl2;
         // The reference maximum moves only when the tile's is over 2^8 above it: a weight
         // stays below 2^8, and O is rescaled rarely.  O is at rest: the commit that made these
@@ -771,48 +789,22 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         first = false;
         const float ref = m == -INFINITY ? 0.f : -m;
-        if (!masked) {
-          const float2 scale2 = make_float2(sl2, sl2), ref2 = make_float2(ref, ref);
-          float2 sum = make_float2(0.f, 0.f);
-          float v[2][32];
-          tmem_ld32(tS, v[0]);
+        const float2 scale2 = make_float2(sl2, sl2), ref2 = make_float2(ref, ref);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_wait_ld();
-            pin(v[c & 1]);
-            if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-            uint32_t w[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float2 x = fma2(make_float2(v[c & 1][k], v[c & 1][k + 1]), scale2, ref2);
-              x.x = ex2(x.x);
-              x.y = ex2(x.y);
-              sum = add2(sum, x);
-              w[k / 2] = pack_bf16x2(x.x, x.y);  // bf16: the tensor cores' operand type
-            }
-            tmem_st16u(tS + 16 * c, w);          // over scores that are read already
+          for (int k = 0; k < 32; k += 2) {
+            float2 x = fma2(make_float2(v[32 * c + k], v[32 * c + k + 1]), scale2, ref2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum = add2(sum, x);
+            w[k / 2] = pack_bf16x2(x.x, x.y);    // bf16: the tensor cores' operand type
           }
-          l += sum.x + sum.y;
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            tmem_ld32(tS + 32 * c, v);
-            tmem_wait_ld();
-            pin(v);
-            const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              // a score that is not seen may be NaN: it is dropped, not multiplied away
-              const float x = (see >> k) & 1u ? ex2(fmaf(v[k], sl2, ref)) : 0.f;
-              const float y = (see >> (k + 1)) & 1u ? ex2(fmaf(v[k + 1], sl2, ref)) : 0.f;
-              l += x + y;
-              w[k / 2] = pack_bf16x2(x, y);
-            }
-            tmem_st16u(tS + 16 * c, w);
-          }
+          tmem_st16u(tS + 16 * c, w);            // over the scores
         }
+        l += sum.x + sum.y;
         tmem_wait_st();
         tc_fence_before();
         // stream 1's accumulator: stream 0's warps must have merged the last one-tile piece
