@@ -56,8 +56,9 @@ constexpr int kPieces = 8;                  // pieces that may be in flight
 enum {
   B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + kRing, B_RAW_FULL = B_KV_EMPTY + kRing,
   B_RAW_EMPTY = B_RAW_FULL + kRing, B_TAIL = B_RAW_EMPTY + kRing, B_Q_FULL = B_TAIL + kRing,
-  B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 2, B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2,
-  B_O1_FREE, B_MMA_DONE, B_STALL, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
+  B_Q_EMPTY, B_S_FULL, B_P_HALF = B_S_FULL + 2, B_P_READY = B_P_HALF + 2, B_O_FULL = B_P_READY + 2,
+  B_ML = B_O_FULL + 2,
+  B_O1_FREE, B_MMA_DONE, B_STALL, B_STAGGER, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
   B_COUNT = B_PIECE_READ + kPieces
 };
 
@@ -300,6 +301,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     mbar_init(BAR(B_Q_EMPTY), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(B_S_FULL + i), 1);
+      mbar_init(BAR(B_P_HALF + i), 4);
       mbar_init(BAR(B_P_READY + i), 4);
       mbar_init(BAR(B_O_FULL + i), 1);
     }
@@ -307,6 +309,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     mbar_init(BAR(B_O1_FREE), 4);
     mbar_init(BAR(B_MMA_DONE), 2);
     mbar_init(BAR(B_STALL), 1);
+    mbar_init(BAR(B_STAGGER), 4);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(BAR(B_PIECE + i), 1);
       mbar_init(BAR(B_PIECE_READ + i), 15);      // producer, two issuers, 4 + 8 warps
@@ -519,7 +522,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     Piece p;
     bool alive = true;
     int slot = 0;
-    uint32_t phase = 0u, p_phase = 0u;
+    uint32_t phase = 0u, p_phase = 0u, stagger = 0u;
     for (int index = 0; __all_sync(0xffffffffu, alive) && get_piece(index, p); ++index) {
       const int n = p.t1 - p.t0;
       const bool two = p.two();
@@ -527,39 +530,56 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (lane != 0) continue;
       const uint64_t ad = q_desc + (uint32_t)(two ? s * (C::kTileBytes >> 4) : 0);
       alive = wait_spin(guard, BAR(B_Q_FULL), index & 1);
+      if (alive && two && s == 1) {
+        // Half a turn behind stream 0, so that one's products run beside the other's softmax
+        alive = wait_spin(guard, BAR(B_STAGGER), stagger);
+        stagger ^= 1u;
+      }
       for (int i = 0; alive && i < n + lag; ++i) {
         const int vt = i - lag;
-        const bool mine = two || (i & 1) == s;
-        if (vt >= 0) {                                          // O_s (+)= P_s V
+        const bool mine = two || (i & 1) == s, has_v = vt >= 0, has_k = i < n;
+        // the entries first (loaded long ago), then the softmax: from there on the products follow
+        // one another
+        const int v_slot = slot;
+        if (has_v) {
           alive = wait_spin(guard, BAR(B_KV_FULL + slot), phase);
-          if (alive && mine) {
-            alive = wait_spin(guard, BAR(B_P_READY + s), p_phase);
-            p_phase ^= 1u;
-          }
-          if (!alive) break;
-          if (mine) {
-            tc_fence_after();
-            const uint64_t bd = v_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
-            const uint32_t acc = two ? vt > 0 : vt > 1;
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, kk > 0 ? 1u : acc);
-            mma_commit(BAR(B_KV_EMPTY + slot));
-            if (vt + (two ? 1 : 2) >= n) mma_commit(BAR(B_O_FULL + s));
-          } else {
-            mbar_arrive(BAR(B_KV_EMPTY + slot));
-          }
           if (++slot == C::kSlots) {
             slot = 0;
             phase ^= 1u;
           }
         }
-        if (i < n) {                                            // S_s = Q K^T, over P_s
-          alive = wait_spin(guard, BAR(B_KV_FULL + slot), phase);
-          if (!alive) break;
-          if (mine) {
+        const int k_slot = slot;
+        if (has_k) {
+          alive = alive && wait_spin(guard, BAR(B_KV_FULL + slot), phase);
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!alive) break;
+        if (!mine) {
+          if (has_v) mbar_arrive(BAR(B_KV_EMPTY + v_slot));
+          if (has_k) mbar_arrive(BAR(B_KV_EMPTY + k_slot));
+        } else {
+          if (has_v) {                                          // O_s (+)= P_s V
+            const uint64_t bd = v_desc + (uint32_t)(v_slot * (C::kTileBytes >> 4));
+            const uint32_t acc = two ? vt > 0 : vt > 1;
+            alive = wait_spin(guard, BAR(B_P_HALF + s), p_phase);
+            if (!alive) break;
             tc_fence_after();
-            const uint64_t bd = k_desc + (uint32_t)(slot * (C::kTileBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, kk > 0 ? 1u : acc);
+            alive = wait_spin(guard, BAR(B_P_READY + s), p_phase);
+            if (!alive) break;
+            p_phase ^= 1u;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk) mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, 1u);
+          }
+          if (has_k) {                                          // S_s = Q K^T, over P_s
+            const uint64_t bd = k_desc + (uint32_t)(k_slot * (C::kTileBytes >> 4));
+            tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               constexpr uint32_t kC = C::kChunk >> 4;
@@ -567,16 +587,14 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               mma_bf16(dS, ad + off, bd + off, kIdescS, kk > 0);
             }
             mma_commit(BAR(B_S_FULL + s));
-            mma_commit(BAR(B_KV_EMPTY + slot));
-          } else {
-            mbar_arrive(BAR(B_KV_EMPTY + slot));
+            mma_commit(BAR(B_KV_EMPTY + k_slot));
           }
-          if (i == n - 1) mma_commit(BAR(B_Q_EMPTY));
-          if (++slot == C::kSlots) {
-            slot = 0;
-            phase ^= 1u;
+          if (has_v) {
+            mma_commit(BAR(B_KV_EMPTY + v_slot));
+            if (vt + (two ? 1 : 2) >= n) mma_commit(BAR(B_O_FULL + s));
           }
         }
+        if (i == n - 1) mma_commit(BAR(B_Q_EMPTY));
       }
     }
     if (lane == 0) {
@@ -758,13 +776,16 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             for (int k = 0; k < 32; ++k) v[32 * c + k] = (see >> k) & 1u ? v[32 * c + k] : -INFINITY;
           }
         }
-        float mx0 = max3(v[0], v[1], v[2]), mx1 = max3(v[3], v[4], v[5]);
+        float mc[8];                             // eight chains
 #pragma unroll
-        for (int k = 6; k + 3 < kTile; k += 4) {
-          mx0 = max3(mx0, v[k], v[k + 1]);
-          mx1 = max3(mx1, v[k + 2], v[k + 3]);
-        }
-        float mx = max3(mx0, mx1, fmaxf(v[126], v[127]));
+        for (int c = 0; c < 8; ++c) mc[c] = max3(v[16 * c], v[16 * c + 1], v[16 * c + 2]);
+#pragma unroll
+        for (int k = 3; k < 15; k += 2)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mc[c] = max3(mc[c], v[16 * c + k], v[16 * c + k + 1]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mc[c] = fmaxf(mc[c], v[16 * c + 15]);
+        float mx = max3(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
         mx *= sl2;
         // The reference maximum moves only when the tile's is over 2^8 above it: a weight
         // stays below 2^8, and O is rescaled rarely.  O is at rest: the commit that made these
@@ -790,7 +811,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         first = false;
         const float ref = m == -INFINITY ? 0.f : -m;
         const float2 scale2 = make_float2(sl2, sl2), ref2 = make_float2(ref, ref);
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum[4] = {};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
@@ -799,21 +820,30 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             float2 x = fma2(make_float2(v[32 * c + k], v[32 * c + k + 1]), scale2, ref2);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
-            sum = add2(sum, x);
+            sum[(k / 2) & 3] = add2(sum[(k / 2) & 3], x);
             w[k / 2] = pack_bf16x2(x.x, x.y);    // bf16: the tensor cores' operand type
           }
           tmem_st16u(tS + 16 * c, w);            // over the scores
+          if (c == 1) {                          // half of the keys: their products may start
+            // stream 1's accumulator: stream 0's warps must have merged the last one-tile piece
+            if (o1_check) {
+              o1_check = false;
+              alive = wait_warp(guard, BAR(B_O1_FREE), (one_pieces - 1) & 1);
+              if (!alive) break;
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_P_HALF + s));
+          }
         }
-        l += sum.x + sum.y;
+        if (!alive) break;
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
         tmem_wait_st();
         tc_fence_before();
-        // stream 1's accumulator: stream 0's warps must have merged the last one-tile piece
-        if (o1_check) {
-          o1_check = false;
-          alive = wait_warp(guard, BAR(B_O1_FREE), (one_pieces - 1) & 1);
-          if (!alive) break;
-        }
         __syncwarp();
+        if (lane == 0 && two && s == 0 && i == 0) mbar_arrive(BAR(B_STAGGER));
         if (lane == 0) mbar_arrive(BAR(B_P_READY + s));
       }
       if (!alive) break;
