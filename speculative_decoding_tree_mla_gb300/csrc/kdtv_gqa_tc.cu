@@ -49,38 +49,58 @@ using namespace ptx;
 constexpr int kTile = 128;                  // rows of a score tile, keys of a key tile
 constexpr int kThreads = 512;
 constexpr int kWarpAux = 8, kWarpTma = 12, kWarpPlan = 13, kWarpMma = 14;   // (14, 15: one per stream)
-constexpr int kRing = 8;                    // bound on ring sizes (barriers)
+constexpr int kRing = 6;                    // bound on ring sizes (barriers)
 constexpr int kPieces = 8;                  // pieces that may be in flight
 
 // barriers
 enum {
-  B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + kRing, B_RAW_FULL = B_KV_EMPTY + kRing,
-  B_RAW_EMPTY = B_RAW_FULL + kRing, B_TAIL = B_RAW_EMPTY + kRing, B_Q_FULL = B_TAIL + kRing,
-  B_Q_EMPTY, B_S_FULL, B_P_HALF = B_S_FULL + 2, B_P_READY = B_P_HALF + 2, B_O_FULL = B_P_READY + 2,
-  B_ML = B_O_FULL + 2,
-  B_O1_FREE, B_MMA_DONE, B_STALL, B_STAGGER, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
+  // bf16 caches: one ring of keys and values, and the values of the last tiles on their way
+  // through the four warps.  One-byte caches: widened values, raw values, raw keys.
+  B_KV_FULL = 0, B_KV_EMPTY = B_KV_FULL + kRing, B_TAIL = B_KV_EMPTY + kRing,
+  B_RAW_FULL = B_TAIL, B_RAW_EMPTY = B_RAW_FULL + kRing, B_K_FULL = B_RAW_EMPTY + kRing,
+  B_K_EMPTY = B_K_FULL + kRing, B_Q_FULL = B_K_EMPTY + kRing,
+  B_Q_READY, B_Q_EMPTY, B_S_FULL, B_P_HALF = B_S_FULL + 2, B_P_READY = B_P_HALF + 2,
+  B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2, B_O1_FREE, B_MMA_DONE, B_STALL, B_STAGGER,
+  B_SCALE_FREE, B_PIECE = B_SCALE_FREE + 2, B_PIECE_READ = B_PIECE + kPieces,
   B_COUNT = B_PIECE_READ + kPieces
 };
 
 template <int D, bool kFp8>
 struct Cfg {
-  static constexpr int kTileBytes = kTile * D * 2;            // Q, K or V tile in bf16
+  static constexpr int kTileBytes = kTile * D * 2;            // Q or V tile (bf16 caches: K too) in bf16
   static constexpr int kChunk = kTile * 128;                  // its 64 columns, 128-byte rows
-  static constexpr int kRawBytes = kTile * D;
-  // D = 128: Q 64 KiB and 5 tiles of 32 KiB, or 3 and 4 raw ones of 16 KiB
-  static constexpr int kSlots = kFp8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-  static constexpr int kRaw = kFp8 ? (D == 128 ? 4 : 8) : 0;
+  static constexpr int kRawBytes = kTile * D;                 // one-byte K or V tile
+  // D = 128: Q 64 KiB, then 5 tiles of 32 KiB, or 2 of widened values, 3 raw ones of 16 KiB and 3
+  // of keys
+  static constexpr int kSlots = kFp8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 6);
+  static constexpr int kRaw = kFp8 ? (D == 128 ? 3 : 6) : 0;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
-  static constexpr int kOffMisc = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kOffK = kOffRaw + kRaw * kRawBytes;    // (the key ring has kRaw entries too)
+  static constexpr int kOffMisc = kOffK + kRaw * kRawBytes;
   // barriers (padded to 16 bytes), TMEM address and abort flag, then per piece its record, the
-  // page flag and the key mask, and stream 1's {max, sum}
+  // page flag and the key mask, stream 1's {max, sum}, the key scales of two tiles
   static constexpr int kBarBytes = (B_COUNT * 8 + 15) / 16 * 16;
-  static constexpr int kMiscBytes = kBarBytes + 16 + kPieces * (32 + 16 + 4) + kTile * 8;
-  static constexpr int kSmem = kOffMisc + kMiscBytes;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr int kOffMl = kOffMisc + kBarBytes + 16 + kPieces * (32 + 16 + 4);
+  static constexpr int kOffScale = kOffMl + kTile * 8;
+  static constexpr int kSmem = kOffScale + (kFp8 ? 2 * kTile * 4 : 0);
+  static_assert(kSmem <= 227 * 1024 && kRing >= kSlots && kRing >= kRaw, "shared memory");
   static constexpr uint32_t kColS = 0, kColO = 2 * kTile;     // S0, S1, O0, O1
+};
+
+// A place in a ring of N entries; its barriers' phase.  (A fresh barrier counts
+// as having completed a phase of parity 1, so the first round finds it empty.)
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0u;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int x, int y, int z) {
@@ -122,63 +142,60 @@ constexpr int kEnd = 16;     // flag: no piece is left
 struct Guard {
   volatile uint32_t* abort;      // shared memory
   unsigned int* status;
-  uint64_t limit;
+  uint32_t limit;                // ns, below 2^32
 };
-
-__device__ __forceinline__ bool wait_long(volatile uint32_t* abort, unsigned int* status, uint64_t limit,
-                                       uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  for (;;) {
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-    if (*abort) return false;
-    if (globaltimer() - t0 > limit) {
-      atomicCAS(status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
-      *abort = 1u;
+__device__ __forceinline__ uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+// Short code: a wait stands at some thirty places of loops that share an
+// instruction cache.
+__device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  const uint32_t t0 = timer_lo();
+#pragma unroll 1
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (*g.abort) return false;
+    if (timer_lo() - t0 > g.limit) {
+      atomicCAS(g.status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
+      *g.abort = 1u;
       return false;
     }
   }
-}
-__device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
-  // the clock is read only in a wait that lasts: reading it costs more than a key tile's softmax
-#pragma unroll 1
-  for (int i = 0; i < 256; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return wait_long(g.abort, g.status, g.limit, bar, parity);
-}
-// The same, polling at first: for the one thread that issues the products,
-// where waking from a suspended wait would be paid on every tile.
-__device__ __forceinline__ bool wait_spin(const Guard& g, uint32_t bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < 4096; ++i)
-    if (mbar_test_wait(bar, parity)) return true;
-  return wait_long(g.abort, g.status, g.limit, bar, parity);
+  return true;
 }
 // Waits for asynchronous work that is in flight and will finish (limited all the same).
 __device__ __forceinline__ void drain(const Guard& g, uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
+  const uint32_t t0 = timer_lo();
+#pragma unroll 1
   while (!mbar_try_wait(bar, parity))
-    if (globaltimer() - t0 > g.limit) return;
+    if (timer_lo() - t0 > g.limit) return;
 }
 __device__ __forceinline__ bool wait_warp(const Guard& g, uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(g, bar, parity));
 }
 
-// Four E4M3 bytes as four bf16, times 2^-120: the seven bits below the sign
-// moved onto the bf16 exponent and mantissa (subnormals stay subnormal).
-__device__ __forceinline__ uint2 e4m3_bits(uint32_t w, uint32_t keep) {   // keep: 0x7f7f7f7f, or 0
-  const uint32_t m = w & keep, s = w & 0x80808080u;
-  const uint32_t m0 = __byte_perm(m, 0u, 0x4140), m1 = __byte_perm(m, 0u, 0x4342);   // bytes in 16-bit lanes
-  const uint32_t s0 = __byte_perm(s, 0u, 0x1404), s1 = __byte_perm(s, 0u, 0x3424);   // sign at bit 15 of each
-  return make_uint2(m0 * 16u + s0, m1 * 16u + s1);
+// Four E4M3 bytes as four bf16, exactly (NaN stays NaN): through f16, which
+// holds every code, and fp32.  The conversions run beside the integer pipe,
+// where moving the bits by masks and permutes took a quarter longer.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  uint32_t a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(a), "=r"(b) : "r"(w));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  return make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(g.x, g.y));
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
   uint32_t y;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
   return y;
 }
-__device__ __forceinline__ uint32_t pow2_bf16x2(int e) {      // e in [-126, 127]
-  const uint32_t h = (uint32_t)(e + 127) << 7;
-  return h | (h << 16);
+// The scale of an exponent byte (2^(byte - 127)), twice.
+__device__ __forceinline__ uint32_t scale_bf16x2(int byte) {
+  return (uint32_t)byte << 7 | (uint32_t)byte << 23;
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -188,6 +205,46 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, E4M3 operands, 32 elements deep, fp32 accumulation.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "setp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Exponent k of a query row's scale 2^k, from the largest finite magnitude of its bf16 bits: the
+// largest element lands in [2^7, 2^8), below E4M3's 448.
+__device__ __forceinline__ int q_exponent(uint32_t max_bits) {
+  return min(134 - (int)(max_bits >> 7), 120);
+}
+// Largest finite magnitude (bits) of a bf16 pair and one so far.
+__device__ __forceinline__ uint32_t max_finite(uint32_t w, uint32_t m) {
+  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  if (lo < 0x7f80u) m = max(m, lo);
+  if (hi < 0x7f80u) m = max(m, hi);
+  return m;
+}
+// Four floats as E4M3 high parts and what they leave, as E4M3 too.  A bf16 has eight significant
+// bits, a part four: the two are exact down to 2^-2 (the parts' own steps end at 2^-9), a row's
+// largest element being at least 2^7.  Infinities become NaN, as their scores would.
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  const uint32_t x = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t y = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return x | (y << 16);
+}
+__device__ __forceinline__ void split_e4m3(uint32_t w0, uint32_t w1, float f, uint32_t& hi, uint32_t& lo) {
+  float x[4] = {__uint_as_float(w0 << 16) * f, __uint_as_float(w0 & 0xffff0000u) * f,
+                __uint_as_float(w1 << 16) * f, __uint_as_float(w1 & 0xffff0000u) * f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = fabsf(x[k]) < INFINITY ? x[k] : __uint_as_float(0x7fffffffu);
+  hi = pack_e4m3(x[0], x[1], x[2], x[3]);
+  const float2 g0 = widen2(hi & 0xffffu), g1 = widen2(hi >> 16);
+  lo = pack_e4m3(x[0] - g0.x, x[1] - g0.y, x[2] - g1.x, x[3] - g1.y);
 }
 // Zeroes the elements of a bf16 pair that are not finite; true if there were any.
 __device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
@@ -213,10 +270,9 @@ __device__ __noinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int
     store_v<1>(o + k, y);
   }
 }
-// E4M3 NaN codes of a widened row: NaN in bf16, or (a tree node's values) 0.
-// True if there were any.  Rare: out of line.
+// E4M3 NaN codes of a row in shared memory become 0; true if there were any.
 template <int D>
-__device__ __noinline__ bool patch_nan_codes(uint32_t src, uint32_t dst, int swz, int chunk_bytes, bool to_zero) {
+__device__ __forceinline__ bool drop_nan_codes(uint32_t src) {
   bool found = false;
 #pragma unroll 1
   for (int e = 0; e < D; ++e) {
@@ -224,8 +280,7 @@ __device__ __noinline__ bool patch_nan_codes(uint32_t src, uint32_t dst, int swz
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(src + e) : "memory");
     if ((code & 0x7fu) != 0x7fu) continue;
     found = true;
-    const uint32_t at = dst + (e >> 6) * chunk_bytes + ((((e >> 3) & 7) ^ swz) << 4) + (e & 7) * 2;
-    asm volatile("st.shared.u16 [%0], %1;" :: "r"(at), "h"((unsigned short)(to_zero ? 0 : 0x7fff)) : "memory");
+    asm volatile("st.shared.u8 [%0], %1;" :: "r"(src + e), "r"(0u) : "memory");
   }
   return found;
 }
@@ -284,19 +339,22 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   Piece* pieces = reinterpret_cast<Piece*>(misc + 4);                 // [kPieces]
   uint4* nonfinite = reinterpret_cast<uint4*>(pieces + kPieces);      // [kPieces] keys of the tree
   volatile uint32_t* bad_page = reinterpret_cast<uint32_t*>(nonfinite + kPieces);   // [kPieces]
-  float2* ml1 = reinterpret_cast<float2*>(smem + C::kOffMisc + C::kMiscBytes - kTile * 8);   // [128]
-  const Guard guard{misc + 1, a.status, stall ? 20000000ull : 2000000000ull};
+  float2* ml1 = reinterpret_cast<float2*>(smem + C::kOffMl);          // [128] stream 1's {max, sum}
+  const Guard guard{misc + 1, a.status, stall ? 20000000u : 2000000000u};
 
   grid_dep_launch();               // the combine kernel may be launched; it waits for this grid
   if (threadIdx.x == 0) {
     misc[1] = 0u;
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(BAR(B_KV_FULL + i), kFp8 ? 4 : 1);
-      mbar_init(BAR(B_KV_EMPTY + i), 2);      // both issuers
-      mbar_init(BAR(B_RAW_FULL + i), 1);
+      mbar_init(BAR(B_KV_FULL + i), kFp8 ? 4 : 1);   // (widened by four warps)
+      mbar_init(BAR(B_KV_EMPTY + i), 2);             // both issuers
+      mbar_init(BAR(B_RAW_FULL + i), 1);             // (B_TAIL)
       mbar_init(BAR(B_RAW_EMPTY + i), 4);
-      mbar_init(BAR(B_TAIL + i), 1);
+      mbar_init(BAR(B_K_FULL + i), 5);               // the copy, and the scales from four warps
+      mbar_init(BAR(B_K_EMPTY + i), 2);
     }
+    mbar_init(BAR(B_Q_READY), 4);
+    for (int i = 0; i < 2; ++i) mbar_init(BAR(B_SCALE_FREE + i), 8);
     mbar_init(BAR(B_Q_FULL), 1);
     mbar_init(BAR(B_Q_EMPTY), 2);
     for (int i = 0; i < 2; ++i) {
@@ -415,29 +473,33 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     // ---- TMA producer: the warp's lanes hold page ids; lane l loads box l of a tile ---------
     const int boxes = a.page_size ? kTile / a.page_size : 1;      // page_size divides 128
     const int box_rows = kTile / boxes;
-    const uint32_t full0 = kFp8 ? B_RAW_FULL : B_KV_FULL, empty0 = kFp8 ? B_RAW_EMPTY : B_KV_EMPTY;
-    constexpr int kEntries = kFp8 ? C::kRaw : C::kSlots;
-    constexpr int kEntryBytes = kFp8 ? C::kRawBytes : C::kTileBytes;
-    const uint32_t ring = sbase + (kFp8 ? C::kOffRaw : C::kOffKV);
     Piece p;
     bool alive = true;
     if (stall) alive = wait_warp(guard, BAR(B_STALL), 0);
-    int g = 0, q_loads = 0;
+    Ring<C::kSlots> ring;                         // bf16
+    Ring<kFp8 ? C::kRaw : 1> kring, vring;        // one byte
+    int entries = 0, k_entries = 0, v_entries = 0, q_loads = 0;
     for (int index = 0; alive && get_piece(index, p); ++index) {
       const int kvh = p.kvh, n = p.t1 - p.t0, T = p.L + p.n;
       const bool two = p.two();
       const int lag = two ? 1 : 2;
-      if (index > 0) alive = wait_warp(guard, BAR(B_Q_EMPTY), (index - 1) & 1);
-      if (!alive) break;
-      if (lane == 0) {
-        const uint32_t bytes = (uint32_t)a.npt * a.G * 128;
-        mbar_expect_tx(BAR(B_Q_FULL), bytes * (D / 64) * (two ? 2 : 1));
-        for (int s = 0; s < (two ? 2 : 1); ++s)
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + c * C::kChunk, &tm_q, BAR(B_Q_FULL), 64 * c,
-                        kvh * a.G, p.b * a.N + p.node0 + s * a.npt);
-      }
-      ++q_loads;
+      // Q once its previous contents are used up.  Keys and values come first where they have room:
+      // the next piece's are on their way while the last one's products run.
+      bool q_pending = true;
+      auto load_q = [&]() -> bool {
+        q_pending = false;
+        if (index > 0 && !wait_warp(guard, BAR(B_Q_EMPTY), (index - 1) & 1)) return false;
+        if (lane == 0) {
+          const uint32_t bytes = (uint32_t)a.npt * a.G * 128;
+          mbar_expect_tx(BAR(B_Q_FULL), bytes * (D / 64) * (two ? 2 : 1));
+          for (int s = 0; s < (two ? 2 : 1); ++s)
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + c * C::kChunk, &tm_q, BAR(B_Q_FULL), 64 * c,
+                          kvh * a.G, p.b * a.N + p.node0 + s * a.npt);
+        }
+        ++q_loads;
+        return true;
+      };
       // windows of 32 page ids, the next one loaded ahead; a page out of range is read as page 0
       // and marks the piece
       const int32_t* table = a.page_table + (long long)p.b * a.max_pages;
@@ -475,15 +537,23 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int kv = 0; kv < 2; ++kv) {          // V of tile i - lag, then K of tile i
           const int kt = kv == 0 ? i - lag : i;
           if (kt < 0 || kt >= n) continue;
-          const int slot = g % kEntries;
-          if (g >= kEntries) alive = wait_warp(guard, BAR(empty0 + slot), (g / kEntries - 1) & 1);
+          const int slot = kFp8 ? (kv == 0 ? vring.slot : kring.slot) : ring.slot;
+          const uint32_t phase = kFp8 ? (kv == 0 ? vring.phase : kring.phase) : ring.phase;
+          const uint32_t empty = BAR((kFp8 ? (kv == 0 ? B_RAW_EMPTY : B_K_EMPTY) : B_KV_EMPTY) + slot);
+          if (q_pending && (index == 0 || __all_sync(0xffffffffu, mbar_test_wait(BAR(B_Q_EMPTY), (index - 1) & 1)) ||
+                            !__all_sync(0xffffffffu, mbar_test_wait(empty, phase ^ 1u))))
+            alive = load_q();
+          alive = alive && wait_warp(guard, empty, phase ^ 1u);
           if (!alive) break;
           const int t = (p.t0 + kt) * kTile;
           const int live = a.page_size ? min(boxes, (T - t + box_rows - 1) / box_rows) : 1;
           // bf16 values of a tile that reaches past the prefix go to the four warps first, which
           // then arrive on the entry's full barrier (every wait sees each phase of its barrier)
           const bool to_aux = !kFp8 && kv == 0 && t + kTile > p.L;
-          const uint32_t bar = BAR((to_aux ? B_TAIL : full0) + slot), dst = ring + slot * kEntryBytes;
+          const uint32_t bar =
+              BAR((kFp8 ? (kv == 0 ? B_RAW_FULL : B_K_FULL) : (to_aux ? B_TAIL : B_KV_FULL)) + slot);
+          const uint32_t dst = sbase + (kFp8 ? (kv == 0 ? C::kOffRaw : C::kOffK) + slot * C::kRawBytes
+                                             : C::kOffKV + slot * C::kTileBytes);
           if (lane == 0) mbar_expect_tx(bar, (uint32_t)live * box_rows * D * (kFp8 ? 1 : 2));
           __syncwarp();
           if (lane < live) {
@@ -498,14 +568,34 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 tma_load_4d(dst + c * C::kChunk + lane * box_rows * 128, map, bar, 64 * c, kvh, y, z);
             }
           }
-          ++g;
+          if constexpr (kFp8) {
+            if (kv == 0) {
+              vring.next();
+              ++v_entries;
+            } else {
+              kring.next();
+              ++k_entries;
+            }
+          } else {
+            ring.next();
+            ++entries;
+          }
         }
       }
+      if (alive && q_pending) alive = load_q();
     }
     // every copy has landed before the CTA may exit
     if (q_loads) drain(guard, BAR(B_Q_FULL), (q_loads - 1) & 1);
-    for (int x = g > kEntries ? g - kEntries : 0; x < g; ++x)
-      drain(guard, BAR(full0 + x % kEntries), (x / kEntries) & 1);
+    auto drain_ring = [&](uint32_t full, int count, int size) {
+      for (int x = count > size ? count - size : 0; x < count; ++x)
+        drain(guard, BAR(full + x % size), (x / size) & 1);
+    };
+    if constexpr (kFp8) {
+      drain_ring(B_K_FULL, k_entries, C::kRaw);
+      drain_ring(B_RAW_FULL, v_entries, C::kRaw);
+    } else {
+      drain_ring(B_KV_FULL, entries, C::kSlots);
+    }
     __syncwarp();
   } else {
     // ---- MMA issuers: warp 14 + s issues stream s (one lane of it; the others follow piece by
@@ -513,26 +603,31 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     // as the products it then issues take, so the streams' issuers are two warps.  Each waits on
     // every entry of the ring, also the other stream's, so that it sees each phase of the barriers.
     const int s = warp - kWarpMma;
-    constexpr uint32_t kIdescS = idesc_bf16(kTile, kTile, 0, 0), kIdescO = idesc_bf16(kTile, D, 0, 1);
+    constexpr uint32_t kIdescS = kFp8 ? idesc_e4m3(kTile, kTile) : idesc_bf16(kTile, kTile, 0, 0);
+    constexpr uint32_t kIdescO = idesc_bf16(kTile, D, 0, 1);
     // operands at fixed places, as descriptors to which a byte offset / 16 is added
-    const uint64_t q_desc = smem_desc(sbase + C::kOffQ, 16, 1024);
-    const uint64_t k_desc = smem_desc(sbase + C::kOffKV, 16, 1024);
+    // (one-byte keys: rows of D bytes, 128- or 64-byte swizzle)
+    const bool narrow = kFp8 && D == 64;
+    const uint64_t q_desc = narrow ? smem_desc_sw64(sbase + C::kOffQ, 16, 512) : smem_desc(sbase + C::kOffQ, 16, 1024);
+    const uint32_t k_at = sbase + (kFp8 ? C::kOffK : C::kOffKV);
+    const uint64_t k_desc = narrow ? smem_desc_sw64(k_at, 16, 512) : smem_desc(k_at, 16, 1024);
     const uint64_t v_desc = smem_desc(sbase + C::kOffKV, C::kChunk, 1024);
     const uint32_t dS = tmem + C::kColS + kTile * s, dO = tmem + C::kColO + D * s;
     Piece p;
     bool alive = true;
-    int slot = 0;
-    uint32_t phase = 0u, p_phase = 0u, stagger = 0u;
+    Ring<C::kSlots> ring;
+    Ring<kFp8 ? C::kRaw : 1> kring;
+    uint32_t p_phase = 0u, stagger = 0u;
     for (int index = 0; __all_sync(0xffffffffu, alive) && get_piece(index, p); ++index) {
       const int n = p.t1 - p.t0;
       const bool two = p.two();
       const int lag = two ? 1 : 2;
       if (lane != 0) continue;
       const uint64_t ad = q_desc + (uint32_t)(two ? s * (C::kTileBytes >> 4) : 0);
-      alive = wait_spin(guard, BAR(B_Q_FULL), index & 1);
+      alive = wait(guard, BAR(kFp8 ? B_Q_READY : B_Q_FULL), index & 1);
       if (alive && two && s == 1) {
         // Half a turn behind stream 0, so that one's products run beside the other's softmax
-        alive = wait_spin(guard, BAR(B_STAGGER), stagger);
+        alive = wait(guard, BAR(B_STAGGER), stagger);
         stagger ^= 1u;
       }
       for (int i = 0; alive && i < n + lag; ++i) {
@@ -540,37 +635,33 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const bool mine = two || (i & 1) == s, has_v = vt >= 0, has_k = i < n;
         // the entries first (loaded long ago), then the softmax: from there on the products follow
         // one another
-        const int v_slot = slot;
+        const int v_slot = ring.slot;
         if (has_v) {
-          alive = wait_spin(guard, BAR(B_KV_FULL + slot), phase);
-          if (++slot == C::kSlots) {
-            slot = 0;
-            phase ^= 1u;
-          }
+          alive = wait(guard, BAR(B_KV_FULL + ring.slot), ring.phase);
+          ring.next();
         }
-        const int k_slot = slot;
+        const int k_slot = kFp8 ? kring.slot : ring.slot;
+        const uint32_t k_empty = BAR((kFp8 ? B_K_EMPTY : B_KV_EMPTY) + k_slot);
         if (has_k) {
-          alive = alive && wait_spin(guard, BAR(B_KV_FULL + slot), phase);
-          if (++slot == C::kSlots) {
-            slot = 0;
-            phase ^= 1u;
-          }
+          alive = alive && wait(guard, BAR((kFp8 ? B_K_FULL : B_KV_FULL) + k_slot), kFp8 ? kring.phase : ring.phase);
+          if constexpr (kFp8) kring.next();
+          else ring.next();
         }
         if (!alive) break;
         if (!mine) {
           if (has_v) mbar_arrive(BAR(B_KV_EMPTY + v_slot));
-          if (has_k) mbar_arrive(BAR(B_KV_EMPTY + k_slot));
+          if (has_k) mbar_arrive(k_empty);
         } else {
           if (has_v) {                                          // O_s (+)= P_s V
             const uint64_t bd = v_desc + (uint32_t)(v_slot * (C::kTileBytes >> 4));
             const uint32_t acc = two ? vt > 0 : vt > 1;
-            alive = wait_spin(guard, BAR(B_P_HALF + s), p_phase);
+            alive = wait(guard, BAR(B_P_HALF + s), p_phase);
             if (!alive) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, kk > 0 ? 1u : acc);
-            alive = wait_spin(guard, BAR(B_P_READY + s), p_phase);
+            alive = wait(guard, BAR(B_P_READY + s), p_phase);
             if (!alive) break;
             p_phase ^= 1u;
             tc_fence_after();
@@ -578,16 +669,24 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             for (int kk = 4; kk < 8; ++kk) mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, 1u);
           }
           if (has_k) {                                          // S_s = Q K^T, over P_s
-            const uint64_t bd = k_desc + (uint32_t)(k_slot * (C::kTileBytes >> 4));
+            const uint64_t bd = k_desc + (uint32_t)(k_slot * ((kFp8 ? C::kRawBytes : C::kTileBytes) >> 4));
             tc_fence_after();
+            if constexpr (kFp8) {                               // the queries' two parts, 32 columns a product
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              constexpr uint32_t kC = C::kChunk >> 4;
-              const uint32_t off = (kk >> 2) * kC + (kk & 3) * 2;
-              mma_bf16(dS, ad + off, bd + off, kIdescS, kk > 0);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t part = (kk / (D / 32)) * (C::kRawBytes >> 4), off = (kk % (D / 32)) * 2;
+                mma_e4m3(dS, ad + part + off, bd + off, kIdescS, kk > 0);
+              }
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                constexpr uint32_t kC = C::kChunk >> 4;
+                const uint32_t off = (kk >> 2) * kC + (kk & 3) * 2;
+                mma_bf16(dS, ad + off, bd + off, kIdescS, kk > 0);
+              }
             }
             mma_commit(BAR(B_S_FULL + s));
-            mma_commit(BAR(B_KV_EMPTY + k_slot));
+            mma_commit(k_empty);
           }
           if (has_v) {
             mma_commit(BAR(B_KV_EMPTY + v_slot));
@@ -612,6 +711,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     bool alive = true;
     int g = 0;
     uint32_t tail_phase = 0u;
+    Ring<kFp8 ? C::kRaw : 1> kring, vring;
+    Ring<C::kSlots> ring;
+    Ring<2> sring;                                // of key scales
+    float* scales = reinterpret_cast<float*>(smem + C::kOffScale);
     for (int index = 0; alive && get_piece(index, p); ++index) {
       const int kvh = p.kvh, n = p.t1 - p.t0, T = p.L + p.n;
       const int lag = p.two() ? 1 : 2;
@@ -619,83 +722,132 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (row < 4) nf[row] = 0u;
       asm volatile("bar.sync 2, 128;" ::: "memory");
       if constexpr (kFp8) {
-        // scale bytes: tile i + 1's are loaded while tile i is widened, from a row index
-        // (page table) loaded a tile before that
-        auto row_at = [&](int i) -> long long {
+        // The scale bytes of a tile are loaded a tile before they are used, its page id a tile
+        // before that.
+        auto page_of = [&](int i) -> int {
           const int t = (p.t0 + i) * kTile + row;
-          if (i >= n || t >= T) return 0;
-          const long long r = gqa_row(a, p.b, t);
-          return r < 0 ? 0 : r;
+          if (!a.page_size || i >= n || t >= T) return 0;
+          return a.page_table[(long long)p.b * a.max_pages + (t >> a.page_shift)];
         };
-        auto at = [&](long long r) { return r * a.Hkv + kvh; };
-        long long r_next = row_at(0);
-        int k_next = a.k_scale[at(r_next)], v_next = a.v_scale[at(r_next)];
-        r_next = row_at(1);
+        auto byte_at = [&](int i, int page) -> long long {         // of tile i's row, with its page id
+          const int t = (p.t0 + i) * kTile + row;
+          if (i >= n || t >= T) return kvh;
+          if (!a.page_size) return ((long long)p.b * a.t_stride + t) * a.Hkv + kvh;
+          if (page < 0 || page >= a.num_pages) page = 0;
+          return (((long long)page << a.page_shift) + (t & (a.page_size - 1))) * a.Hkv + kvh;
+        };
+        const int page_first = page_of(0);
+        int page_next = page_of(1);
+        long long at = byte_at(0, page_first);
+        int k_next = a.k_scale[at], v_next = a.v_scale[at];
         int v0 = 127, v1 = 127, v2 = 127;
+
+        // Q: each row's two E4M3 parts in place of its bf16 (while the scale bytes arrive)
+        alive = wait_warp(guard, BAR(B_Q_FULL), index & 1);
+        if (!alive) break;
+#pragma unroll 1
+        for (int tile = 0; tile < (p.two() ? 2 : 1); ++tile) {
+          const uint32_t q0 = sbase + C::kOffQ + tile * C::kTileBytes, qr = q0 + row * 128;
+          uint32_t mxb = 0u;
+#pragma unroll 2
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 w = lds128(qr + (u >> 3) * C::kChunk + (((u & 7) ^ swz) << 4));
+            mxb = max_finite(w.w, max_finite(w.z, max_finite(w.y, max_finite(w.x, mxb))));
+          }
+          const float f = __uint_as_float((uint32_t)(q_exponent(mxb) + 127) << 23);
+          uint32_t hi[D / 4], lo[D / 4];
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 w = lds128(qr + (u >> 3) * C::kChunk + (((u & 7) ^ swz) << 4));
+            split_e4m3(w.x, w.y, f, hi[2 * u], lo[2 * u]);
+            split_e4m3(w.z, w.w, f, hi[2 * u + 1], lo[2 * u + 1]);
+            if (D == 128 && (u & 1) && u < 8)       // 16 bytes of the high part, where both were read
+              sts128(qr + (((u >> 1) ^ swz) << 4), hi[2 * u - 2], hi[2 * u - 1], hi[2 * u], hi[2 * u + 1]);
+          }
+          if (D == 64) asm volatile("bar.sync 2, 128;" ::: "memory");   // rows of the parts overlap others' rows
+#pragma unroll
+          for (int u = 0; u < D / 16; ++u) {
+            if (D == 128) {
+              if (u >= 4) sts128(qr + ((u ^ swz) << 4), hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+              sts128(qr + C::kRawBytes + ((u ^ swz) << 4), lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+            } else {                                // 64-byte rows, chunk c at c ^ ((row >> 1) & 3)
+              const uint32_t at64 = q0 + row * 64 + ((u ^ ((row >> 1) & 3)) << 4);
+              sts128(at64, hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+              sts128(at64 + C::kRawBytes, lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_Q_READY));
+
         for (int i = 0; alive && i < n + lag; ++i) {
           const int k0 = k_next;
           v2 = v1;
           v1 = v0;
           v0 = v_next;
-          const long long r = r_next;
-          k_next = a.k_scale[at(r)];
-          v_next = a.v_scale[at(r)];
-          r_next = row_at(i + 2);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const int kt = kv == 0 ? i - lag : i;
-            if (kt < 0 || kt >= n) continue;
-            const int rs = g % C::kRaw, slot = g % C::kSlots;
-            alive = wait_warp(guard, BAR(B_RAW_FULL + rs), (g / C::kRaw) & 1);
-            if (alive && g >= C::kSlots) alive = wait_warp(guard, BAR(B_KV_EMPTY + slot), (g / C::kSlots - 1) & 1);
+          at = byte_at(i + 1, page_next);
+          k_next = a.k_scale[at];
+          v_next = a.v_scale[at];
+          page_next = page_of(i + 2);
+          if (i < n) {                              // tile i's key scales, for the softmax
+            alive = wait_warp(guard, BAR(B_SCALE_FREE + sring.slot), sring.phase ^ 1u);
             if (!alive) break;
-            const int e = (kv == 1 ? k0 : (lag == 1 ? v1 : v2)) - 127;
-            const uint32_t src = sbase + C::kOffRaw + rs * C::kRawBytes + row * D;
-            const uint32_t dst = sbase + C::kOffKV + slot * C::kTileBytes + row * 128;
-            const int t = (p.t0 + kt) * kTile + row;
-            // 2^(e + 120) as two factors, each a bf16
-            const int ea = max(-126, min(127, e + 120)), eb = e + 120 - ea;
-            const uint32_t fa = pow2_bf16x2(ea), fb = pow2_bf16x2(eb);
-            const uint32_t keep = kv == 0 && t >= T ? 0u : 0x7f7f7f7fu;   // values behind the tree: 0
-            const bool two_factors = __any_sync(0xffffffffu, eb != 0);
-            uint32_t nan = 0u;                   // bit 7 of a byte: a code of all ones was seen there
-            // 16-byte chunk c of the row at its XOR-permuted turn: no bank conflicts, for the
-            // reads (rows D bytes apart) nor for the swizzled writes
-#pragma unroll 2
-            for (int k = 0; k < D / 16; ++k) {
-              const int c = D == 128 ? (k ^ swz) : (k ^ (swz & 3));
-              const uint4 w = lds128(src + 16 * c);
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            scales[sring.slot * kTile + row] = scale_of_byte(k0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_K_FULL + kring.slot));
+            sring.next();
+            kring.next();
+          }
+          if (i < lag) continue;
+          // the values of tile i - lag
+          alive = wait_warp(guard, BAR(B_RAW_FULL + vring.slot), vring.phase) &&
+                  wait_warp(guard, BAR(B_KV_EMPTY + ring.slot), ring.phase ^ 1u);
+          if (!alive) break;
+          const uint32_t f = scale_bf16x2(lag == 1 ? v1 : v2);
+          const uint32_t src = sbase + C::kOffRaw + vring.slot * C::kRawBytes + row * D;
+          const uint32_t dst = sbase + C::kOffKV + ring.slot * C::kTileBytes + row * 128;
+          const int t = (p.t0 + i - lag) * kTile + row;
+          // values of the tree's own rows: NaN becomes 0, noted for the epilogue
+          if (t >= p.L && t < T && drop_nan_codes<D>(src))
+            atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
+          const bool zero = t >= T;                 // values behind the tree: 0
+          // 16-byte chunk c of the row at its XOR-permuted turn: no bank conflicts, for the
+          // reads (rows D bytes apart) nor for the swizzled writes.  Four chunks are read before
+          // the first is widened: one warp a scheduler has to hide its own latencies.
+#pragma unroll 1
+          for (int k4 = 0; k4 < D / 16; k4 += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              w[k] = lds128(src + 16 * (D == 128 ? ((k4 + k) ^ swz) : (k ^ (swz & 3))));
+              if (zero) w[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int c = D == 128 ? ((k4 + k) ^ swz) : (k ^ (swz & 3));
+              const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
               uint32_t y[8];
 #pragma unroll
               for (int m = 0; m < 4; ++m) {
-                nan |= (u[m] & keep) + 0x01010101u;
-                const uint2 z = e4m3_bits(u[m], keep);
-                y[2 * m] = mul_bf16x2(z.x, fa);
-                y[2 * m + 1] = mul_bf16x2(z.y, fa);
-              }
-              if (two_factors) {
-#pragma unroll
-                for (int m = 0; m < 8; ++m) y[m] = mul_bf16x2(y[m], fb);
+                const uint2 z = widen4(u[m]);
+                y[2 * m] = mul_bf16x2(z.x, f);
+                y[2 * m + 1] = mul_bf16x2(z.y, f);
               }
               const uint32_t half = dst + (c >> 2) * C::kChunk;
               const int j = (2 * c) & 7;
               sts128(half + ((j ^ swz) << 4), y[0], y[1], y[2], y[3]);
               sts128(half + (((j + 1) ^ swz) << 4), y[4], y[5], y[6], y[7]);
             }
-            if (nan & 0x80808080u) {
-              const bool own = kv == 0 && t >= p.L;
-              if (patch_nan_codes<D>(src, dst, swz, C::kChunk, own) && own)
-                atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(BAR(B_KV_FULL + slot));
-              mbar_arrive(BAR(B_RAW_EMPTY + rs));
-            }
-            ++g;
           }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR(B_KV_FULL + ring.slot));
+            mbar_arrive(BAR(B_RAW_EMPTY + vring.slot));
+          }
+          vring.next();
+          ring.next();
         }
       } else {
         const int from = max(p.t0, p.L / kTile);          // the first key tile that reaches past the prefix
@@ -743,6 +895,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     Piece p;
     bool alive = true;
     uint32_t s_phase = 0u, o_phase = 0u, one_pieces = 0u;
+    int k_tiles = 0;                              // of the pieces before: the parity of their scales' places
     for (int index = 0; alive && get_piece(index, p); ++index) {
       const int n = p.t1 - p.t0, kvh = p.kvh;
       const bool two = p.two();
@@ -754,6 +907,23 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         dead = !gqa_path(a, p.b, node, path);
         if (dead) gqa_error(a, KDTV_ERR_BAD_TREE);
       }
+      const bool any_valid = __any_sync(0xffffffffu, valid);
+      // One-byte keys: the row's queries were scaled by 2^k (the four warps found the same k in
+      // their copy of the row)
+      float row_scale = sl2;
+      if constexpr (kFp8) {
+        uint32_t mxb = 0u;
+        if (valid) {
+          const uint4* qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+              (((long long)p.b * a.N + node) * a.H + (long long)kvh * a.G + r_head) * D);
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 w = qrow[u];
+            mxb = max_finite(w.w, max_finite(w.z, max_finite(w.y, max_finite(w.x, mxb))));
+          }
+        }
+        row_scale *= __uint_as_float((uint32_t)(127 - q_exponent(mxb)) << 23);
+      }
       float m = -INFINITY, l = 0.f;
       bool first = true, o1_check = s == 1 && one_pieces > 0;
       for (int i = two ? 0 : s; i < n; i += two ? 1 : 2) {
@@ -761,6 +931,22 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         alive = wait_warp(guard, BAR(B_S_FULL + s), s_phase & 1);
         ++s_phase;
         if (!alive) break;
+        if (!any_valid) {                        // no row of this warp is written: its weights may be anything
+          if (o1_check) {
+            o1_check = false;
+            alive = wait_warp(guard, BAR(B_O1_FREE), (one_pieces - 1) & 1);
+            if (!alive) break;
+          }
+          if (lane == 0) {
+            if constexpr (kFp8)
+              for (int k = 0; k < (two ? 1 : 2); ++k) mbar_arrive(BAR(B_SCALE_FREE + ((k_tiles + i) & 1)));
+            mbar_arrive(BAR(B_P_HALF + s));
+            mbar_arrive(BAR(B_P_READY + s));
+            if (two && s == 0 && i == 0) mbar_arrive(BAR(B_STAGGER));
+          }
+          __syncwarp();
+          continue;
+        }
         tc_fence_after();
         const bool masked = t0 + kTile > p.L;
         float v[kTile];
@@ -768,6 +954,21 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<float(&)[32]>(v[32 * c]));
         tmem_wait_ld();
         pin(v);
+        if constexpr (kFp8) {                    // a column's power of two, one for all rows
+          const int place = (k_tiles + i) & 1;
+          const uint32_t at = sbase + C::kOffScale + place * (kTile * 4);
+#pragma unroll
+          for (int k = 0; k < kTile; k += 4) {
+            const uint4 f = lds128(at + 4 * k);
+            v[k] *= __uint_as_float(f.x);
+            v[k + 1] *= __uint_as_float(f.y);
+            v[k + 2] *= __uint_as_float(f.z);
+            v[k + 3] *= __uint_as_float(f.w);
+          }
+          __syncwarp();
+          if (lane == 0)                         // eight arrivals: two streams, or one twice
+            for (int k = 0; k < (two ? 1 : 2); ++k) mbar_arrive(BAR(B_SCALE_FREE + place));
+        }
         if (masked) {                            // dropped, whatever it is: a masked score may be NaN
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -786,7 +987,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
         for (int c = 0; c < 8; ++c) mc[c] = fmaxf(mc[c], v[16 * c + 15]);
         float mx = max3(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
-        mx *= sl2;
+        mx *= row_scale;
         // The reference maximum moves only when the tile's is over 2^8 above it: a weight
         // stays below 2^8, and O is rescaled rarely.  O is at rest: the commit that made these
         // scores visible came after this stream's previous P.V.
@@ -810,7 +1011,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         first = false;
         const float ref = m == -INFINITY ? 0.f : -m;
-        const float2 scale2 = make_float2(sl2, sl2), ref2 = make_float2(ref, ref);
+        const float2 scale2 = make_float2(row_scale, row_scale), ref2 = make_float2(ref, ref);
         float2 sum[4] = {};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -847,6 +1048,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (lane == 0) mbar_arrive(BAR(B_P_READY + s));
       }
       if (!alive) break;
+      k_tiles += n;
 
       // ---- the end of the piece ---------------------------------------------------------------
       const bool mine = two || n > s;              // this stream had a tile
@@ -1058,15 +1260,15 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.H, (uint64_t)a.B * a.N};
     const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)a.H * D * 2};
     const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.npt};
-    if (encode_nd(&tq, a.q, 3, dims, strides, box, 2, true) != CUDA_SUCCESS) return KDTV_ERR_CUDA;
+    if (encode_nd(&tq, a.q, 3, dims, strides, box, 2, 128) != CUDA_SUCCESS) return KDTV_ERR_CUDA;
   }
   const uint64_t es = kFp8 ? 1 : 2;
   const uint64_t rows = a.page_size ? a.page_size : a.t_stride, blocks = a.page_size ? a.num_pages : a.B;
   const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.Hkv, rows, blocks};
   const uint64_t strides[3] = {D * es, (uint64_t)a.Hkv * D * es, rows * a.Hkv * D * es};
   const uint32_t box[4] = {kFp8 ? (uint32_t)D : 64u, 1u, a.page_size ? (uint32_t)a.page_size : (uint32_t)kTile, 1u};
-  if (encode_nd(&tk, a.k, 4, dims, strides, box, (int)es, !kFp8) != CUDA_SUCCESS ||
-      encode_nd(&tv, a.v, 4, dims, strides, box, (int)es, !kFp8) != CUDA_SUCCESS)
+  if (encode_nd(&tk, a.k, 4, dims, strides, box, (int)es, kFp8 && D == 64 ? 64 : 128) != CUDA_SUCCESS ||
+      encode_nd(&tv, a.v, 4, dims, strides, box, (int)es, kFp8 ? 0 : 128) != CUDA_SUCCESS)
     return KDTV_ERR_CUDA;
   const auto kern = gqa_tc_kernel<D, kFp8>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
@@ -1094,6 +1296,8 @@ int gqa_tc_supported(const kdtv_gqa_dims* d) {
 
 size_t gqa_tc_workspace(const kdtv_gqa_dims* d, int sms, GqaArgs* a) {
   a->npt = kTile / a->G;
+  a->page_shift = 0;
+  while ((1 << a->page_shift) < d->page_size) ++a->page_shift;
   a->ctas = sms;
   const long long cap = d->page_size ? (long long)d->max_pages * d->page_size : d->t_stride;
   const long long units = (long long)d->B * d->H_kv * ((d->N + 2 * a->npt - 1) / (2 * a->npt)) *

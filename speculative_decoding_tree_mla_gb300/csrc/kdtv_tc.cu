@@ -1325,7 +1325,7 @@ CUresult encode_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
 }
 
 CUresult encode_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                   const uint64_t* strides, const uint32_t* box, int elem_bytes, bool swizzle) {
+                   const uint64_t* strides, const uint32_t* box, int elem_bytes, int swizzle_bytes) {
   EncodeTiledFn fn = encoder();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
   cuuint64_t d[4], s[3];
@@ -1338,7 +1338,8 @@ CUresult encode_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* d
   }
   return fn(m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank,
             const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+            : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

@@ -14,9 +14,9 @@ CUresult encode_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
                    int swizzle_bytes = 128);
 
 // Tensor map of `rank` (3..4) dimensions, innermost first, of 2-byte (bf16) or
-// 1-byte elements; strides in bytes, of all but the innermost dimension.  128-byte
-// swizzle, or none.
+// 1-byte elements; strides in bytes, of all but the innermost dimension.  128-
+// or 64-byte swizzle, or none (0).
 CUresult encode_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                   const uint64_t* strides, const uint32_t* box, int elem_bytes, bool swizzle);
+                   const uint64_t* strides, const uint32_t* box, int elem_bytes, int swizzle_bytes);
 
 }  // namespace kdtv
