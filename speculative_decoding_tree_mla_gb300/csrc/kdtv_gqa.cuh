@@ -20,7 +20,9 @@ struct GqaArgs {
   float* part_o;               // partial rows (unnormalised), fp32
   float2* part_ml;             // {reference maximum (log2 units), sum}; sum < 0: the row is not written
   int chunk, splits;           // CUDA cores: keys per split, splits
-  int ctas, npt, page_shift;   // tensor cores: CTAs, nodes per 128-row tile (128 / G), log2 of page_size
+  // tensor cores: heads side by side in a group of CTAs, groups, nodes per 128-row tile (128 / G),
+  // log2 of page_size
+  int hg, groups, npt, page_shift;
 };
 
 __device__ __forceinline__ void gqa_error(const GqaArgs& a, unsigned int code) {

@@ -3,10 +3,12 @@
 //
 // Work.  The query rows of a key/value head are (node, query head) pairs, cut
 // into tiles of npt = 128 / G nodes (at most 128 rows, one per TMEM lane).  An
-// item is (request, key/value head, pair of tiles); its work is its 128-key
-// tiles.  All (item, key tile) units form one sequence and CTA c takes the W
-// consecutive units [cW, (c + 1)W), so ragged batches and few long requests
-// spread evenly; a piece (the part of an item in one CTA) that is not the
+// item is (request, block of hg heads, pair of tiles); its work is its 128-key
+// tiles.  All (item, key tile) units form one sequence and group c of hg CTAs
+// takes the W consecutive units [cW, (c + 1)W), so ragged batches and few long
+// requests spread evenly; CTA h of the group works on head h of the block.  The
+// heads of a cache row are neighbours in memory, and the group reads them at
+// about the same time.  A piece (the part of an item in one CTA) that is not the
 // whole item leaves a partial {max, sum, O} that the combine kernel merges.
 // Each CTA derives the sequence from prefix_len by itself: no plan kernel.
 //
@@ -123,7 +125,7 @@ __device__ __forceinline__ int row_pairs(const GqaArgs& a, int n) { return (n + 
 __device__ __forceinline__ int units_of(const GqaArgs& a, int b) {
   int L, n;
   gqa_request(a, b, &L, &n);
-  return n > 0 ? a.Hkv * row_pairs(a, n) * key_tiles(L, n) : 0;
+  return n > 0 ? a.Hkv / a.hg * row_pairs(a, n) * key_tiles(L, n) : 0;
 }
 
 // A piece: the part of an item in one CTA.  The planning warp walks the CTA's
@@ -315,6 +317,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return y;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 y;
   asm("{\n\t.reg .b64 a, b, d;\n\t"
@@ -407,8 +417,9 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     int sum = 0;
     for (int b = lane; b < a.B; b += 32) sum += units_of(a, b);
     sum = __reduce_add_sync(0xffffffffu, sum);
-    const int W = (sum + a.ctas - 1) / a.ctas;
-    const long long first = (long long)blockIdx.x * W;
+    const int W = (sum + a.groups - 1) / a.groups;
+    const long long first = (long long)(blockIdx.x / a.hg) * W;
+    const int my_head = blockIdx.x % a.hg;
     const int end = first < sum ? (int)(first + W < sum ? first + W : sum) : 0;
     int at = first < sum ? (int)first : 0, b = 0, off = 0;
     if (end > 0) {
@@ -431,13 +442,13 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         before += __shfl_sync(0xffffffffu, scan, 31);
       }
     }
-    int L = 0, n = 0, nt = 1, rps = 1, kvh = 0, pair = 0, t0 = 0;
+    int L = 0, n = 0, nt = 1, rps = 1, hb = 0, pair = 0, t0 = 0;
     if (end > 0) {
       gqa_request(a, b, &L, &n);
       nt = key_tiles(L, n);
       rps = row_pairs(a, n);
       t0 = off % nt;
-      kvh = off / nt / rps;
+      hb = off / nt / rps;
       pair = off / nt % rps;
     }
     for (int k = 0;; ++k) {
@@ -445,7 +456,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const int t1 = min(nt, t0 + end - at);
       if (lane == 0) {
         Piece p;
-        p.b = b; p.L = L; p.n = n; p.kvh = kvh;
+        p.b = b; p.L = L; p.n = n; p.kvh = hb * a.hg + my_head;
         p.node0 = pair * 2 * a.npt;
         p.t0 = t0; p.t1 = t1;
         p.flags = (n - p.node0 > a.npt ? 1 : 0) | (t0 == 0 && t1 == nt ? 2 : 0) |
@@ -459,8 +470,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       t0 = 0;
       if (at < end && ++pair == rps) {
         pair = 0;
-        if (++kvh == a.Hkv) {
-          kvh = 0;
+        if (++hb == a.Hkv / a.hg) {
+          hb = 0;
           do {
             gqa_request(a, ++b, &L, &n);         // units are left, so a request with some exists
           } while (n == 0);
@@ -635,18 +646,22 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const bool mine = two || (i & 1) == s, has_v = vt >= 0, has_k = i < n;
         // the entries first (loaded long ago), then the softmax: from there on the products follow
         // one another
+        // the entries and the softmax; one look at all three, because each costs its latency
         const int v_slot = ring.slot;
-        if (has_v) {
-          alive = wait(guard, BAR(B_KV_FULL + ring.slot), ring.phase);
-          ring.next();
-        }
+        const uint32_t v_full = BAR(B_KV_FULL + v_slot), v_phase = ring.phase;
+        if (has_v) ring.next();
         const int k_slot = kFp8 ? kring.slot : ring.slot;
-        const uint32_t k_empty = BAR((kFp8 ? B_K_EMPTY : B_KV_EMPTY) + k_slot);
+        const uint32_t k_full = BAR((kFp8 ? B_K_FULL : B_KV_FULL) + k_slot), k_phase = kFp8 ? kring.phase : ring.phase;
+        const uint32_t k_empty = BAR((kFp8 ? B_K_EMPTY : B_KV_EMPTY) + k_slot), p_half = BAR(B_P_HALF + s);
         if (has_k) {
-          alive = alive && wait(guard, BAR((kFp8 ? B_K_FULL : B_KV_FULL) + k_slot), kFp8 ? kring.phase : ring.phase);
           if constexpr (kFp8) kring.next();
           else ring.next();
         }
+        const bool v_ok = mbar_try_wait(v_full, v_phase) || !has_v, k_ok = mbar_try_wait(k_full, k_phase) || !has_k;
+        const bool p_ok = mbar_try_wait(p_half, p_phase) || !(has_v && mine);
+        if (!(v_ok && k_ok && p_ok))
+          alive = (v_ok || wait(guard, v_full, v_phase)) && (k_ok || wait(guard, k_full, k_phase)) &&
+                  (p_ok || wait(guard, p_half, p_phase));
         if (!alive) break;
         if (!mine) {
           if (has_v) mbar_arrive(BAR(B_KV_EMPTY + v_slot));
@@ -655,8 +670,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (has_v) {                                          // O_s (+)= P_s V
             const uint64_t bd = v_desc + (uint32_t)(v_slot * (C::kTileBytes >> 4));
             const uint32_t acc = two ? vt > 0 : vt > 1;
-            alive = wait(guard, BAR(B_P_HALF + s), p_phase);
-            if (!alive) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -722,8 +735,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (row < 4) nf[row] = 0u;
       asm volatile("bar.sync 2, 128;" ::: "memory");
       if constexpr (kFp8) {
-        // The scale bytes of a tile are loaded a tile before they are used, its page id a tile
-        // before that.
+        // The scale bytes of tile i + 2 are loaded at the end of step i, with a page id loaded a step
+        // before: behind the step's proxy fence, which waits for every load that is under way.
         auto page_of = [&](int i) -> int {
           const int t = (p.t0 + i) * kTile + row;
           if (!a.page_size || i >= n || t >= T) return 0;
@@ -736,11 +749,11 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (page < 0 || page >= a.num_pages) page = 0;
           return (((long long)page << a.page_shift) + (t & (a.page_size - 1))) * a.Hkv + kvh;
         };
-        const int page_first = page_of(0);
-        int page_next = page_of(1);
-        long long at = byte_at(0, page_first);
-        int k_next = a.k_scale[at], v_next = a.v_scale[at];
-        int v0 = 127, v1 = 127, v2 = 127;
+        const int page_first = page_of(0), page_second = page_of(1);
+        int page_next = page_of(2);
+        const long long at0 = byte_at(0, page_first), at1 = byte_at(1, page_second);
+        int k0 = a.k_scale[at0], k1 = a.k_scale[at1];      // of tiles i, i + 1
+        int v1 = a.v_scale[at1], v0 = a.v_scale[at0], vm1 = 0, vm2 = 0;   // of tiles i + 1 .. i - 2
 
         // Q: each row's two E4M3 parts in place of its bf16 (while the scale bytes arrive)
         alive = wait_warp(guard, BAR(B_Q_FULL), index & 1);
@@ -782,29 +795,15 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (lane == 0) mbar_arrive(BAR(B_Q_READY));
 
         for (int i = 0; alive && i < n + lag; ++i) {
-          const int k0 = k_next;
-          v2 = v1;
-          v1 = v0;
-          v0 = v_next;
-          at = byte_at(i + 1, page_next);
-          k_next = a.k_scale[at];
-          v_next = a.v_scale[at];
-          page_next = page_of(i + 2);
-          if (i < n) {                              // tile i's key scales, for the softmax
-            alive = wait_warp(guard, BAR(B_SCALE_FREE + sring.slot), sring.phase ^ 1u);
-            if (!alive) break;
-            scales[sring.slot * kTile + row] = scale_of_byte(k0);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_K_FULL + kring.slot));
-            sring.next();
-            kring.next();
-          }
-          if (i < lag) continue;
+          if (i >= lag) {
           // the values of tile i - lag
-          alive = wait_warp(guard, BAR(B_RAW_FULL + vring.slot), vring.phase) &&
-                  wait_warp(guard, BAR(B_KV_EMPTY + ring.slot), ring.phase ^ 1u);
+          const bool full = mbar_try_wait(BAR(B_RAW_FULL + vring.slot), vring.phase);
+          const bool empty = mbar_try_wait(BAR(B_KV_EMPTY + ring.slot), ring.phase ^ 1u);
+          if (!__all_sync(0xffffffffu, full && empty))
+            alive = wait_warp(guard, BAR(B_RAW_FULL + vring.slot), vring.phase) &&
+                    wait_warp(guard, BAR(B_KV_EMPTY + ring.slot), ring.phase ^ 1u);
           if (!alive) break;
-          const uint32_t f = scale_bf16x2(lag == 1 ? v1 : v2);
+          const uint32_t f = scale_bf16x2(lag == 1 ? vm1 : vm2);
           const uint32_t src = sbase + C::kOffRaw + vring.slot * C::kRawBytes + row * D;
           const uint32_t dst = sbase + C::kOffKV + ring.slot * C::kTileBytes + row * 128;
           const int t = (p.t0 + i - lag) * kTile + row;
@@ -813,19 +812,19 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
           const bool zero = t >= T;                 // values behind the tree: 0
           // 16-byte chunk c of the row at its XOR-permuted turn: no bank conflicts, for the
-          // reads (rows D bytes apart) nor for the swizzled writes.  Four chunks are read before
+          // reads (rows D bytes apart) nor for the swizzled writes.  Two chunks are read before
           // the first is widened: one warp a scheduler has to hide its own latencies.
 #pragma unroll 1
-          for (int k4 = 0; k4 < D / 16; k4 += 4) {
-            uint4 w[4];
+          for (int k2 = 0; k2 < D / 16; k2 += 2) {
+            uint4 w[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              w[k] = lds128(src + 16 * (D == 128 ? ((k4 + k) ^ swz) : (k ^ (swz & 3))));
+            for (int k = 0; k < 2; ++k) {
+              w[k] = lds128(src + 16 * ((k2 + k) ^ (D == 128 ? swz : swz & 3)));
               if (zero) w[k] = make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int c = D == 128 ? ((k4 + k) ^ swz) : (k ^ (swz & 3));
+            for (int k = 0; k < 2; ++k) {
+              const int c = (k2 + k) ^ (D == 128 ? swz : swz & 3);
               const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
               uint32_t y[8];
 #pragma unroll
@@ -848,6 +847,26 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           }
           vring.next();
           ring.next();
+          }
+          // Tile i's key scales, for the softmax: after the values, because the place is that of
+          // tile i - 2, whose softmax may still be at work while its values are widened.
+          if (i < n) {
+            alive = wait_warp(guard, BAR(B_SCALE_FREE + sring.slot), sring.phase ^ 1u);
+            if (!alive) break;
+            scales[sring.slot * kTile + row] = scale_of_byte(k0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_K_FULL + kring.slot));
+            sring.next();
+            kring.next();
+          }
+          k0 = k1;
+          vm2 = vm1;
+          vm1 = v0;
+          v0 = v1;
+          const long long at = byte_at(i + 2, page_next);
+          k1 = a.k_scale[at];
+          v1 = a.v_scale[at];
+          page_next = page_of(i + 3);
         }
       } else {
         const int from = max(p.t0, p.L / kTile);          // the first key tile that reaches past the prefix
@@ -949,44 +968,67 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         tc_fence_after();
         const bool masked = t0 + kTile > p.L;
-        float v[kTile];
+        // bf16 keys: a row's 128 scores stay in registers.  One-byte keys: two passes over them, a
+        // chunk at a time; this instance has more roles at work, and their loops together must stay
+        // in the SM's instruction cache.
+        constexpr int kChunkCols = 32;
+        float v[kFp8 ? kChunkCols : kTile];
+        auto load_chunk = [&](int c) {
+          tmem_ld32(tS + kChunkCols * c, reinterpret_cast<float(&)[32]>(v[0]));
+          if constexpr (kChunkCols == 64) tmem_ld32(tS + kChunkCols * c + 32, reinterpret_cast<float(&)[32]>(v[32]));
+          tmem_wait_ld();
+          pin(v);
+          const uint32_t at = sbase + C::kOffScale + ((k_tiles + i) & 1) * (kTile * 4) + c * (kChunkCols * 4);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<float(&)[32]>(v[32 * c]));
-        tmem_wait_ld();
-        pin(v);
-        if constexpr (kFp8) {                    // a column's power of two, one for all rows
-          const int place = (k_tiles + i) & 1;
-          const uint32_t at = sbase + C::kOffScale + place * (kTile * 4);
-#pragma unroll
-          for (int k = 0; k < kTile; k += 4) {
+          for (int k = 0; k < kChunkCols; k += 4) {   // a column's power of two, one for all rows
             const uint4 f = lds128(at + 4 * k);
-            v[k] *= __uint_as_float(f.x);
-            v[k + 1] *= __uint_as_float(f.y);
-            v[k + 2] *= __uint_as_float(f.z);
-            v[k + 3] *= __uint_as_float(f.w);
+            const float2 x = mul2(make_float2(v[k], v[k + 1]), make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
+            const float2 y = mul2(make_float2(v[k + 2], v[k + 3]), make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
+            v[k] = x.x; v[k + 1] = x.y; v[k + 2] = y.x; v[k + 3] = y.y;
           }
-          __syncwarp();
-          if (lane == 0)                         // eight arrivals: two streams, or one twice
-            for (int k = 0; k < (two ? 1 : 2); ++k) mbar_arrive(BAR(B_SCALE_FREE + place));
-        }
-        if (masked) {                            // dropped, whatever it is: a masked score may be NaN
+          if (masked) {                          // dropped, whatever it is: a masked score may be NaN
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
+            for (int h = 0; h < kChunkCols / 32; ++h) {
+              const uint32_t see = gqa_visible(path, t0 + kChunkCols * c + 32 * h, p.L);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[32 * c + k] = (see >> k) & 1u ? v[32 * c + k] : -INFINITY;
+              for (int k = 0; k < 32; ++k) v[32 * h + k] = (see >> k) & 1u ? v[32 * h + k] : -INFINITY;
+            }
           }
+        };
+        float mx = -INFINITY;
+        if constexpr (kFp8) {
+#pragma unroll 1
+          for (int c = 0; c < kTile / kChunkCols; ++c) {
+            load_chunk(c);
+            float mc[4] = {mx, v[0], v[1], v[2]};
+#pragma unroll
+            for (int k = 3; k + 1 < kChunkCols; k += 2) mc[(k / 2) & 3] = max3(mc[(k / 2) & 3], v[k], v[k + 1]);
+            mx = max3(max3(mc[0], mc[1], mc[2]), mc[3], v[kChunkCols - 1]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, reinterpret_cast<float(&)[32]>(v[32 * c]));
+          tmem_wait_ld();
+          pin(v);
+          if (masked) {                            // dropped, whatever it is: a masked score may be NaN
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[32 * c + k] = (see >> k) & 1u ? v[32 * c + k] : -INFINITY;
+            }
+          }
+          float mc[8];                             // eight chains
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mc[c] = max3(v[16 * c], v[16 * c + 1], v[16 * c + 2]);
+#pragma unroll
+          for (int k = 3; k < 15; k += 2)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mc[c] = max3(mc[c], v[16 * c + k], v[16 * c + k + 1]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mc[c] = fmaxf(mc[c], v[16 * c + 15]);
+          mx = max3(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
         }
-        float mc[8];                             // eight chains
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mc[c] = max3(v[16 * c], v[16 * c + 1], v[16 * c + 2]);
-#pragma unroll
-        for (int k = 3; k < 15; k += 2)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) mc[c] = max3(mc[c], v[16 * c + k], v[16 * c + k + 1]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mc[c] = fmaxf(mc[c], v[16 * c + 15]);
-        float mx = max3(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
         mx *= row_scale;
         // The reference maximum moves only when the tile's is over 2^8 above it: a weight
         // stays below 2^8, and O is rescaled rarely.  O is at rest: the commit that made these
@@ -1013,32 +1055,48 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const float ref = m == -INFINITY ? 0.f : -m;
         const float2 scale2 = make_float2(row_scale, row_scale), ref2 = make_float2(ref, ref);
         float2 sum[4] = {};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        if (o1_check) {
+          // stream 1's accumulator: stream 0's warps must have merged the last one-tile piece
+          o1_check = false;
+          alive = wait_warp(guard, BAR(B_O1_FREE), (one_pieces - 1) & 1);
+          if (!alive) break;
+        }
+        auto weights = [&](const float (&x32)[32], int c) {   // of 32 columns, over scores that are read already
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            float2 x = fma2(make_float2(v[32 * c + k], v[32 * c + k + 1]), scale2, ref2);
+            float2 x = fma2(make_float2(x32[k], x32[k + 1]), scale2, ref2);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
             sum[(k / 2) & 3] = add2(sum[(k / 2) & 3], x);
             w[k / 2] = pack_bf16x2(x.x, x.y);    // bf16: the tensor cores' operand type
           }
-          tmem_st16u(tS + 16 * c, w);            // over the scores
-          if (c == 1) {                          // half of the keys: their products may start
-            // stream 1's accumulator: stream 0's warps must have merged the last one-tile piece
-            if (o1_check) {
-              o1_check = false;
-              alive = wait_warp(guard, BAR(B_O1_FREE), (one_pieces - 1) & 1);
-              if (!alive) break;
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_P_HALF + s));
+          tmem_st16u(tS + 16 * c, w);
+        };
+        auto half_ready = [&]() {                // half of the keys: their products may start
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_P_HALF + s));
+        };
+        if constexpr (kFp8) {
+#pragma unroll 1
+          for (int c = 0; c < kTile / kChunkCols; ++c) {
+            load_chunk(c);
+#pragma unroll
+            for (int h = 0; h < kChunkCols / 32; ++h)
+              weights(reinterpret_cast<const float(&)[32]>(v[32 * h]), c * (kChunkCols / 32) + h);
+            if (c == kTile / kChunkCols / 2 - 1) half_ready();
+          }
+          if (lane == 0)                         // the scales' place: two streams arrive, or one twice
+            for (int k = 0; k < (two ? 1 : 2); ++k) mbar_arrive(BAR(B_SCALE_FREE + ((k_tiles + i) & 1)));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            weights(reinterpret_cast<const float(&)[32]>(v[32 * c]), c);
+            if (c == 1) half_ready();
           }
         }
-        if (!alive) break;
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
         tmem_wait_st();
@@ -1156,8 +1214,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // Output rows of items that were cut into pieces: the pieces' sums and outputs
 // meet at their common maximum.  blockIdx.y is the request; a warp per row, the
 // row's d elements across its lanes.  Item [S, S + nt) was cut at the multiples
-// of W; CTA c's piece that starts its range is partial 2c, one that starts
-// later 2c + 1.
+// of W; a CTA's piece that starts its range is partial 2 cta, one that starts
+// later 2 cta + 1.
 template <int D>
 __global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant__ GqaArgs a) {
   __shared__ int s_sum[8], s_before[8];
@@ -1185,19 +1243,19 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant_
   gqa_request(a, b, &L, &n);
   grid_dep_wait();                                 // the partials are written
   if (n == 0 || *reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
-  const int W = (sum + a.ctas - 1) / a.ctas;
+  const int W = (sum + a.groups - 1) / a.groups;
   const int nt = key_tiles(L, n), rps = row_pairs(a, n);
   const int rows = n * a.H;
   constexpr int V = D / 32;                        // elements per lane
   for (int row = blockIdx.x * 8 + warp; row < rows; row += gridDim.x * 8) {
     const int node = row / a.H, h = row % a.H, kvh = h / a.G;
     const int tile = node / a.npt;
-    const int start = before + (kvh * rps + tile / 2) * nt, end = start + nt;
+    const int start = before + (kvh / a.hg * rps + tile / 2) * nt, end = start + nt;
     const int c0 = start / W, c1 = (end - 1) / W;
     if (c0 == c1) continue;                        // whole: written by its CTA
     const int r = (tile & 1) * kTile + (node % a.npt) * a.G + h % a.G;
     const bool later = start != c0 * W;            // of the first piece; the others start their CTA's range
-    auto prow = [&](int c) { return (2ll * c + (c == c0 && later)) * (2 * kTile) + r; };
+    auto prow = [&](int c) { return (2ll * (c * a.hg + kvh % a.hg) + (c == c0 && later)) * (2 * kTile) + r; };
     // lane k: {max, sum} of piece k of each 32, and the weight that brings it to the common maximum
     float m = -INFINITY;
     bool skip = false;
@@ -1273,11 +1331,11 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
   const auto kern = gqa_tc_kernel<D, kFp8>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return KDTV_ERR_CUDA;
-  if (launch_ex(kern, dim3((unsigned)a.ctas), dim3(kThreads), C::kSmem, st, false, tq, tk, tv, a, stall ? 1 : 0) !=
+  if (launch_ex(kern, dim3((unsigned)(a.groups * a.hg)), dim3(kThreads), C::kSmem, st, false, tq, tk, tv, a, stall ? 1 : 0) !=
       cudaSuccess)
     return KDTV_ERR_CUDA;
   // a warp per row, up to about eight CTAs per SM
-  const long long want = ((long long)a.N * a.H + 7) / 8, most = 8ll * a.ctas / a.B + 1;
+  const long long want = ((long long)a.N * a.H + 7) / 8, most = 8ll * a.groups * a.hg / a.B + 1;
   const int gx = (int)(want < most ? want : most);
   if (launch_ex(gqa_combine_kernel<D>, dim3((unsigned)gx, (unsigned)a.B), dim3(256), 0, st, true, a) != cudaSuccess)
     return KDTV_ERR_CUDA;
@@ -1298,12 +1356,15 @@ size_t gqa_tc_workspace(const kdtv_gqa_dims* d, int sms, GqaArgs* a) {
   a->npt = kTile / a->G;
   a->page_shift = 0;
   while ((1 << a->page_shift) < d->page_size) ++a->page_shift;
-  a->ctas = sms;
+  // heads side by side: the largest divisor of H_kv up to 8 (and the CTAs there are)
+  a->hg = 8 < sms ? 8 : sms;
+  while (d->H_kv % a->hg) --a->hg;
+  a->groups = sms / a->hg;
   const long long cap = d->page_size ? (long long)d->max_pages * d->page_size : d->t_stride;
   const long long units = (long long)d->B * d->H_kv * ((d->N + 2 * a->npt - 1) / (2 * a->npt)) *
                           ((cap + kTile - 1) / kTile);
   if (units >= (1ll << 30)) return 0;               // 32-bit unit numbers
-  return (size_t)2 * sms * 2 * kTile;
+  return (size_t)2 * a->groups * a->hg * 2 * kTile;
 }
 
 int launch_gqa_tc(const GqaArgs& a, bool stall, cudaStream_t st) {
