@@ -15,7 +15,8 @@ constexpr int kThreads = 256;
 // ---- rotary ---------------------------------------------------------------------------
 struct RopeArgs {
   int N, H, rot_off, rot;
-  int items, rot_items;        // per row: rotated items first, then copied vectors
+  int rot_items, copy_items;   // per row and head
+  unsigned rot_blocks;         // blocks of rotated items; the copied ones follow
   int heads, hgroups;          // heads per thread, groups of them
   unsigned rows;               // B * N
   long long xs[3], ys[3], rs[3];
@@ -29,16 +30,19 @@ struct RopeArgs {
 // items, so a head's elements are read and written in 16-byte pieces by
 // neighbouring lanes.  An item is one vector of V elements (interleaved), a
 // vector and its partner rot / 2 further (half), or a vector that is only
-// copied.  The angles of an item are computed once and serve all heads of the
-// group; the loads of kBatch heads are issued before their stores, which also
-// makes x == y safe: no other thread touches the item's elements.
+// copied; a block has rotated or copied items, so its warps do not diverge.
+// The angles of an item are computed once and serve all heads of the group; the
+// loads of a batch of heads are issued before their stores, which also makes
+// x == y safe: no other thread touches the item's elements.  Four blocks an SM:
+// bound by DRAM at prompt sizes, and by the loads in flight.
 template <typename T, int V, bool kHalf>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ kdtv_rope_table tab,
-                                                        const __grid_constant__ RopeArgs a) {
-  constexpr int kBatch = 4;
-  const unsigned t = blockIdx.x * kThreads + threadIdx.x;   // < 2^32 (host)
-  const int item = (int)(t % (unsigned)a.items);
-  const unsigned u = t / (unsigned)a.items;
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ kdtv_rope_table tab,
+                                                           const __grid_constant__ RopeArgs a) {
+  const bool copied = blockIdx.x >= a.rot_blocks;
+  const unsigned t = (blockIdx.x - (copied ? a.rot_blocks : 0u)) * kThreads + threadIdx.x;   // < 2^32 (host)
+  const unsigned items = (unsigned)(copied ? a.copy_items : a.rot_items);
+  const int item = (int)(t % items);
+  const unsigned u = t / items;
   const int hg = (int)(u % (unsigned)a.hgroups);
   const unsigned row = u / (unsigned)a.hgroups;
   if (row >= a.rows) return;
@@ -47,8 +51,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + i * a.xs[1];
   T* y = static_cast<T*>(a.y) + b * a.ys[0] + i * a.ys[1];
   const int h0 = hg * a.heads, h1 = min(h0 + a.heads, a.H);
-  if (item >= a.rot_items) {
-    const int c = (item - a.rot_items) * V;             // among the elements that are copied
+  if (copied) {
+    constexpr int kBatch = 4;
+    const int c = item * V;                             // among the elements that are copied
     const int e = c < a.rot_off ? c : c + a.rot;
     T* dst;
     long long dh;
@@ -73,6 +78,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const long long pos = (long long)(a.prefix_len ? a.prefix_len[b] : 0) + (a.depth ? a.depth[row] : i);
   if (!a.rest) y += a.rot_off;
   x += a.rot_off;
+  constexpr int kBatch = 2;
   if constexpr (kHalf || V == 1) {
     // u elements at e0, their partners at e1
     const int e0 = kHalf ? item * V : 2 * item;
@@ -91,35 +97,35 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (h + k < h1) {
-          float o0[V], o1[V];
 #pragma unroll
           for (int m = 0; m < V; ++m) {
-            o0[m] = p[k][m] * cs[m].x - q[k][m] * cs[m].y;
-            o1[m] = q[k][m] * cs[m].x + p[k][m] * cs[m].y;
+            const float o = p[k][m] * cs[m].x - q[k][m] * cs[m].y;
+            q[k][m] = q[k][m] * cs[m].x + p[k][m] * cs[m].y;
+            p[k][m] = o;
           }
-          store_v<V>(y + (h + k) * a.ys[2] + e0, o0);
-          store_v<V>(y + (h + k) * a.ys[2] + e1, o1);
+          store_v<V>(y + (h + k) * a.ys[2] + e0, p[k]);
+          store_v<V>(y + (h + k) * a.ys[2] + e1, q[k]);
         }
     }
   } else {
     float2 cs[V / 2];
 #pragma unroll
     for (int k = 0; k < V / 2; ++k) cs[k] = rope_cos_sin(tab.turn[item * (V / 2) + k], pos, tab.amp);
-    for (int h = h0; h < h1; h += kBatch) {
-      float p[kBatch][V];
+    for (int h = h0; h < h1; h += 2 * kBatch) {
+      float p[2 * kBatch][V];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
+      for (int k = 0; k < 2 * kBatch; ++k)
         if (h + k < h1) load_v<V>(x + (h + k) * a.xs[2] + item * V, p[k]);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
+      for (int k = 0; k < 2 * kBatch; ++k)
         if (h + k < h1) {
-          float o[V];
 #pragma unroll
           for (int m = 0; m < V / 2; ++m) {
-            o[2 * m] = p[k][2 * m] * cs[m].x - p[k][2 * m + 1] * cs[m].y;
-            o[2 * m + 1] = p[k][2 * m + 1] * cs[m].x + p[k][2 * m] * cs[m].y;
+            const float o = p[k][2 * m] * cs[m].x - p[k][2 * m + 1] * cs[m].y;
+            p[k][2 * m + 1] = p[k][2 * m + 1] * cs[m].x + p[k][2 * m] * cs[m].y;
+            p[k][2 * m] = o;
           }
-          store_v<V>(y + (h + k) * a.ys[2] + item * V, o);
+          store_v<V>(y + (h + k) * a.ys[2] + item * V, p[k]);
         }
     }
   }
@@ -215,110 +221,138 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     }
   }
 
-  for (int h = h0; h < h0 + per; ++h) {
-    const bool on = live && h < h1;
-    float x[P][V];
+  // kBatch heads a turn: their loads are under way together
+  constexpr int kBatch = P * V <= 8 ? 4 : 1;
+  for (int hh = h0; hh < h0 + per; hh += kBatch) {
+    float x[kBatch][P][V], m[kBatch][P][V];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int e = (p * group + lane) * V;
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[p][k] = 0.f;
-      if (!on || e >= part.dim) continue;
-      const S* s = src + h * part.ss[2] + e;
-      load_v<V>(s, x[p]);
-      if (mate[p] == 0) continue;
-      if (half || V == 1) {
-        float m[V];
-        load_v<V>(s + mate[p], m);
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          x[p][k] = mate[p] > 0 ? x[p][k] * cs[p][k].x - m[k] * cs[p][k].y
-                                : x[p][k] * cs[p][k].x + m[k] * cs[p][k].y;
-      } else {
-#pragma unroll
-        for (int k = 0; k + 1 < V; k += 2) {
-          const float u0 = x[p][k], v0 = x[p][k + 1];
-          x[p][k] = u0 * cs[p][k].x - v0 * cs[p][k].y;
-          x[p][k + 1] = v0 * cs[p][k].x + u0 * cs[p][k].y;
-        }
-      }
-    }
-    D* dst = static_cast<D*>(part.cache) + (row * part.heads + h) * part.dim;
-    if constexpr (sizeof(D) == 1) {
-      if (part.scale) {
-        // The smallest e with max <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of
-        // the largest finite magnitude.  2^-e is a power of two, so x * 2^-e loses
-        // nothing; a power also makes a code's value exact in bf16.
-        float m = 0.f;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            const float f = fabsf(x[p][k]);
-            m = f < INFINITY ? fmaxf(m, f) : m;
-          }
-        for (int o = group / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t bits = __float_as_uint(m);
-        int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-        e = max(-117, min(119, e));
-        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int k = 0; k < V; ++k) x[p][k] *= f;
-        if (on && lane == 0) part.scale[row * part.heads + h] = (uint8_t)(e + 127);
-      } else {
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int k = 0; k < V; ++k) x[p][k] = __fdiv_rn(x[p][k], a.kv_scale);
-      }
-    }
-    if (on)
+    for (int j = 0; j < kBatch; ++j)
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int e = (p * group + lane) * V;
-        if (e < part.dim) store_v<V>(dst + e, x[p]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[j][p][k] = 0.f;
+        if (!live || hh + j >= h1 || e >= part.dim) continue;
+        const S* s = src + (hh + j) * part.ss[2] + e;
+        load_v<V>(s, x[j][p]);
+        if (mate[p] != 0 && (half || V == 1)) load_v<V>(s + mate[p], m[j][p]);
       }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = hh + j;
+      const bool on = live && h < h1;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (mate[p] == 0 || !on) continue;
+        if (half || V == 1) {
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            x[j][p][k] = mate[p] > 0 ? x[j][p][k] * cs[p][k].x - m[j][p][k] * cs[p][k].y
+                                     : x[j][p][k] * cs[p][k].x + m[j][p][k] * cs[p][k].y;
+        } else {
+#pragma unroll
+          for (int k = 0; k + 1 < V; k += 2) {
+            const float u0 = x[j][p][k], v0 = x[j][p][k + 1];
+            x[j][p][k] = u0 * cs[p][k].x - v0 * cs[p][k].y;
+            x[j][p][k + 1] = v0 * cs[p][k].x + u0 * cs[p][k].y;
+          }
+        }
+      }
+      D* dst = static_cast<D*>(part.cache) + (row * part.heads + h) * part.dim;
+      if constexpr (sizeof(D) == 1) {
+        if (part.scale) {
+          // The smallest e with max <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of
+          // the largest finite magnitude.  2^-e is a power of two, so x * 2^-e loses
+          // nothing; a power also makes a code's value exact in bf16.
+          float mx = 0.f;
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              const float f = fabsf(x[j][p][k]);
+              mx = f < INFINITY ? fmaxf(mx, f) : mx;
+            }
+          for (int o = group / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const uint32_t bits = __float_as_uint(mx);
+          int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+          e = max(-117, min(119, e));
+          const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[j][p][k] *= f;
+          if (on && lane == 0) part.scale[row * part.heads + h] = (uint8_t)(e + 127);
+        } else {
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[j][p][k] = __fdiv_rn(x[j][p][k], a.kv_scale);
+        }
+      }
+      if (on)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int e = (p * group + lane) * V;
+          if (e < part.dim) store_v<V>(dst + e, x[j][p]);
+        }
+    }
   }
 }
 
-// Thread = kRows vectors of V elements, a block apart, of one part's rows
-// (rows of a part are contiguous in the cache and in out).
+// A request's rows of one part are contiguous in out, and row by row in the
+// cache.  A block takes a span of vectors of V elements, kBatch of them per
+// thread under way together; the spans are long enough that looking the
+// request up does not count, and as many as fill the SMs.
 template <typename C, typename O, int V>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvArgs a) {
-  constexpr int kRows = 4;
+__global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const __grid_constant__ KvArgs a, unsigned span) {
+  constexpr int kBatch = V == 16 ? 2 : 4;
   const KvPart& part = a.part[blockIdx.z];
   const int b = blockIdx.y;
   const int n = live_rows(a.n_live, b, a.N);
   if (n == 0) return;
+  const unsigned width = (unsigned)(part.heads * part.dim), vecs = width / V;
+  const unsigned total = (unsigned)n * vecs, t0 = blockIdx.x * span, t1 = min(total, t0 + span);   // < 2^31 (host)
   const int L = a.prefix_len ? a.prefix_len[b] : 0;
   if (!rows_ok(a, b, L, n)) return;
-  const int width = part.heads * part.dim, vecs = width / V;
-  const unsigned total = (unsigned)n * (unsigned)vecs;            // < 2^32 (host)
   const C* cache = static_cast<const C*>(part.cache);
   O* out = static_cast<O*>(part.out) + (long long)b * a.N * width;
-  float x[kRows][V], s[kRows];
-  const unsigned t0 = blockIdx.x * (unsigned)(kThreads * kRows) + threadIdx.x;
+  for (unsigned t = t0 + threadIdx.x; t < t1; t += kBatch * kThreads) {
+    float x[kBatch][V], s[kBatch];
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const unsigned t = t0 + k * kThreads;
-    if (t >= total) continue;
-    const int i = (int)(t / (unsigned)vecs), c = (int)(t % (unsigned)vecs) * V;
-    const long long row = row_of(a, b, L + i);
-    load_v<V>(cache + row * width + c, x[k]);
-    s[k] = 1.f;
-    if constexpr (sizeof(C) == 1)
-      s[k] = part.scale ? scale_of_byte(part.scale[row * part.heads + c / part.dim]) : a.kv_scale;
-  }
+    for (int k = 0; k < kBatch; ++k) {
+      const unsigned tk = t + k * kThreads;
+      if (tk >= t1) continue;
+      const unsigned i = tk / vecs, c = (tk - i * vecs) * V;
+      const long long row = row_of(a, b, L + (int)i);
+      if constexpr (V == 16) {               // one-byte elements, 16 bytes
+        const uint4 w = *reinterpret_cast<const uint4*>(cache + row * width + c);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const unsigned t = t0 + k * kThreads;
-    if (t >= total) continue;
-    if constexpr (sizeof(C) == 1)
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = widen2(u[j] & 0xffffu), g = widen2(u[j] >> 16);
+          x[k][4 * j] = f.x; x[k][4 * j + 1] = f.y; x[k][4 * j + 2] = g.x; x[k][4 * j + 3] = g.y;
+        }
+      } else {
+        load_v<V>(cache + row * width + c, x[k]);
+      }
+      s[k] = 1.f;
+      if constexpr (sizeof(C) == 1)
+        s[k] = part.scale ? scale_of_byte(part.scale[row * part.heads + c / part.dim]) : a.kv_scale;
+    }
 #pragma unroll
-      for (int m = 0; m < V; ++m) x[k][m] *= s[k];
-    store_v<V>(out + (long long)t * V, x[k]);
+    for (int k = 0; k < kBatch; ++k) {
+      const unsigned tk = t + k * kThreads;
+      if (tk >= t1) continue;
+      if constexpr (sizeof(C) == 1)
+#pragma unroll
+        for (int m = 0; m < V; ++m) x[k][m] *= s[k];
+      if constexpr (V == 16) {
+        store_v<8>(out + (long long)tk * V, reinterpret_cast<const float(&)[8]>(x[k][0]));
+        store_v<8>(out + (long long)tk * V + 8, reinterpret_cast<const float(&)[8]>(x[k][8]));
+      } else {
+        store_v<V>(out + (long long)tk * V, x[k]);
+      }
+    }
   }
 }
 
@@ -343,15 +377,18 @@ int launch_rope(const kdtv_rope_table& tab, RopeArgs& a, int dim, cudaStream_t s
   const int v = vec ? V : 1;
   a.rot_items = half || !vec ? a.rot / 2 / v : a.rot / v;
   const bool in_place = a.x == a.y && !a.rest;
-  a.items = a.rot_items + (in_place ? 0 : (dim - a.rot) / v);
+  a.copy_items = in_place ? 0 : (dim - a.rot) / v;
   // Heads per thread: an item's angles cost about as much as four heads' moves,
-  // but threads come first.
-  const long long threads = (long long)a.rows * a.items * a.H;
+  // but threads come first.  (64 heads, 8000 rows: 4 heads 90 us, 8 82, 16 76.)
+  const long long threads = (long long)a.rows * (a.rot_items + a.copy_items) * a.H;
   a.heads = 1;
-  while (a.heads < 8 && a.heads < a.H && threads / (2 * a.heads) >= 152ll * 1024) a.heads *= 2;
+  while (a.heads < 16 && a.heads < a.H && threads / (2 * a.heads) >= 152ll * 1024) a.heads *= 2;
   a.hgroups = (a.H + a.heads - 1) / a.heads;
-  const long long blocks = ((long long)a.rows * a.hgroups * a.items + kThreads - 1) / kThreads;
+  const long long per = (long long)a.rows * a.hgroups;
+  const long long rot_blocks = (per * a.rot_items + kThreads - 1) / kThreads;
+  const long long blocks = rot_blocks + (per * a.copy_items + kThreads - 1) / kThreads;
   if (blocks > (1ll << 32) / kThreads - 1) return KDTV_ERR_UNSUPPORTED;   // 32-bit thread indices
+  a.rot_blocks = (unsigned)rot_blocks;
   auto kern = vec ? (half ? rope_kernel<T, V, true> : rope_kernel<T, V, false>)
                   : (half ? rope_kernel<T, 1, true> : rope_kernel<T, 1, false>);
   kern<<<(unsigned)blocks, kThreads, 0, st>>>(tab, a);
@@ -392,19 +429,23 @@ cudaError_t launch_append(const kdtv_rope_table& tab, KvArgs& a, cudaStream_t st
 
 template <typename C, typename O>
 cudaError_t launch_read(KvArgs& a, cudaStream_t st) {
+  constexpr int kWide = sizeof(C) == 1 ? 16 : 8;
   bool vec = true;
-  long long vecs = 1;
+  long long width = 1;
   for (int k = 0; k < a.parts; ++k) {
     const KvPart& p = a.part[k];
-    vec = vec && aligned(p.cache, 16) && aligned(p.out, 16) && p.dim % 8 == 0;
+    vec = vec && aligned(p.cache, 16) && aligned(p.out, 16) && p.dim % kWide == 0;
     const long long w = (long long)p.heads * p.dim;
-    vecs = w > vecs ? w : vecs;
+    width = w > width ? w : width;
   }
-  const long long per_block = (vec ? 8 : 1) * 4ll * kThreads;
-  const long long bx = (a.N * vecs + per_block - 1) / per_block;
-  const dim3 grid((unsigned)bx, (unsigned)a.B, (unsigned)a.parts);
-  auto kern = vec ? kv_read_kernel<C, O, 8> : kv_read_kernel<C, O, 1>;
-  kern<<<grid, kThreads, 0, st>>>(a);
+  // Spans of at least one turn of the block's threads, else about eight blocks an SM in all.
+  const long long total = a.N * (width / (vec ? kWide : 1)), turn = (kWide == 16 && vec ? 2 : 4) * kThreads;
+  long long blocks = 8ll * 152 / ((long long)a.B * a.parts);
+  blocks = blocks < 1 ? 1 : blocks;
+  const long long span = ((total + blocks - 1) / blocks + turn - 1) / turn * turn;
+  const dim3 grid((unsigned)((total + span - 1) / span), (unsigned)a.B, (unsigned)a.parts);
+  auto kern = vec ? kv_read_kernel<C, O, kWide> : kv_read_kernel<C, O, 1>;
+  kern<<<grid, kThreads, 0, st>>>(a, (unsigned)span);
   return cudaGetLastError();
 }
 
