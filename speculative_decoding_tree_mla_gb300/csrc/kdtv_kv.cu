@@ -221,8 +221,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     }
   }
 
-  // kBatch heads a turn: their loads are under way together
-  constexpr int kBatch = P * V <= 8 ? 4 : 1;
+  // (one head a turn: two or four, with their loads under way together, took
+  // 50 and 70 us against 42 for 16000 rows of 8 + 8 heads, in registers and so in warps)
+  constexpr int kBatch = 1;
   for (int hh = h0; hh < h0 + per; hh += kBatch) {
     float x[kBatch][P][V], m[kBatch][P][V];
 #pragma unroll
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
 // request up does not count, and as many as fill the SMs.
 template <typename C, typename O, int V>
 __global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const __grid_constant__ KvArgs a, unsigned span) {
-  constexpr int kBatch = V == 16 ? 2 : 4;
+  constexpr int kBatch = 4;
   const KvPart& part = a.part[blockIdx.z];
   const int b = blockIdx.y;
   const int n = live_rows(a.n_live, b, a.N);
@@ -317,24 +318,17 @@ __global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const __grid_const
   const C* cache = static_cast<const C*>(part.cache);
   O* out = static_cast<O*>(part.out) + (long long)b * a.N * width;
   for (unsigned t = t0 + threadIdx.x; t < t1; t += kBatch * kThreads) {
-    float x[kBatch][V], s[kBatch];
+    // 16-byte vectors stay as they are until they are stored
+    float x[kBatch][V == 16 ? 1 : V], s[kBatch];
+    uint4 raw[V == 16 ? kBatch : 1];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const unsigned tk = t + k * kThreads;
       if (tk >= t1) continue;
       const unsigned i = tk / vecs, c = (tk - i * vecs) * V;
       const long long row = row_of(a, b, L + (int)i);
-      if constexpr (V == 16) {               // one-byte elements, 16 bytes
-        const uint4 w = *reinterpret_cast<const uint4*>(cache + row * width + c);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = widen2(u[j] & 0xffffu), g = widen2(u[j] >> 16);
-          x[k][4 * j] = f.x; x[k][4 * j + 1] = f.y; x[k][4 * j + 2] = g.x; x[k][4 * j + 3] = g.y;
-        }
-      } else {
-        load_v<V>(cache + row * width + c, x[k]);
-      }
+      if constexpr (V == 16) raw[k] = *reinterpret_cast<const uint4*>(cache + row * width + c);
+      else load_v<V>(cache + row * width + c, x[k]);
       s[k] = 1.f;
       if constexpr (sizeof(C) == 1)
         s[k] = part.scale ? scale_of_byte(part.scale[row * part.heads + c / part.dim]) : a.kv_scale;
@@ -343,14 +337,24 @@ __global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const __grid_const
     for (int k = 0; k < kBatch; ++k) {
       const unsigned tk = t + k * kThreads;
       if (tk >= t1) continue;
-      if constexpr (sizeof(C) == 1)
-#pragma unroll
-        for (int m = 0; m < V; ++m) x[k][m] *= s[k];
+      O* dst = out + (long long)tk * V;
       if constexpr (V == 16) {
-        store_v<8>(out + (long long)tk * V, reinterpret_cast<const float(&)[8]>(x[k][0]));
-        store_v<8>(out + (long long)tk * V + 8, reinterpret_cast<const float(&)[8]>(x[k][8]));
+        const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float y[8];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 f = widen2(u[2 * h + j] & 0xffffu), g = widen2(u[2 * h + j] >> 16);
+            y[4 * j] = f.x * s[k]; y[4 * j + 1] = f.y * s[k]; y[4 * j + 2] = g.x * s[k]; y[4 * j + 3] = g.y * s[k];
+          }
+          store_v<8>(dst + 8 * h, y);
+        }
       } else {
-        store_v<V>(out + (long long)tk * V, x[k]);
+        if constexpr (sizeof(C) == 1)
+#pragma unroll
+          for (int m = 0; m < V; ++m) x[k][m] *= s[k];
+        store_v<V>(dst, x[k]);
       }
     }
   }
@@ -439,7 +443,7 @@ cudaError_t launch_read(KvArgs& a, cudaStream_t st) {
     width = w > width ? w : width;
   }
   // Spans of at least one turn of the block's threads, else about eight blocks an SM in all.
-  const long long total = a.N * (width / (vec ? kWide : 1)), turn = (kWide == 16 && vec ? 2 : 4) * kThreads;
+  const long long total = a.N * (width / (vec ? kWide : 1)), turn = 4 * kThreads;
   long long blocks = 8ll * 152 / ((long long)a.B * a.parts);
   blocks = blocks < 1 ? 1 : blocks;
   const long long span = ((total + blocks - 1) / blocks + turn - 1) / turn * turn;

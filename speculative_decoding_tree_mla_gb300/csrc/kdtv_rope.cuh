@@ -8,14 +8,17 @@ namespace kdtv {
 // cos and sin of position * f_j, times amp.  The table holds f_j / 2 pi in
 // units of 2^-64 turns, so the product modulo 2^64 is the fraction of a turn:
 // whole turns fall off the top and the reduction is exact for any position.
-// The fraction is split into the nearest quarter turn and a remainder within
-// an eighth of a turn, which fp32 holds to 2^-24 of itself.
+// Its upper 32 bits (2^-32 turns: 1.5e-9 of angle) split into the nearest
+// quarter turn and a remainder within an eighth of a turn, pi / 4, where the
+// Taylor polynomials up to x^9 and x^10 leave less than 2e-9.
 __device__ __forceinline__ float2 rope_cos_sin(uint64_t turn, long long pos, float amp) {
-  const uint64_t x = turn * (uint64_t)pos;
-  const uint64_t q = (x + (1ull << 61)) >> 62;
-  const long long r = (long long)(x - (q << 62));          // [-2^61, 2^61)
-  float s, c;
-  sincospif(__ll2float_rn(r) * 0x1p-63f, &s, &c);          // half turns
+  const uint32_t x = (uint32_t)((turn * (uint64_t)pos) >> 32);
+  const uint32_t q = (x + (1u << 29)) >> 30;
+  const float t = (float)(int)(x - (q << 30)) * 1.4629180792671596e-9f;   // 2 pi 2^-32
+  const float z = t * t;
+  const float s = fmaf(t * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), t);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f),
+                                       1.f / 24.f), -0.5f), 1.f);
   const float cq = (q & 1) ? -s : c, sq = (q & 1) ? c : s;
   const float sign = (q & 2) ? -amp : amp;
   return make_float2(cq * sign, sq * sign);

@@ -1,8 +1,8 @@
 """Rotary positions and cache writes / reads against the fp64 oracle.
 
 Tolerances, fixed before the first run.  Rotation: cos and sin are off by at
-most 2 ulp (the fraction of a turn is exact to 2^-24 of itself and |sin| <=
-that angle; sincospif adds one), each of the two products and the sum rounds
+most 2^-23 (the angle is exact to 2^-32 turns and 2^-24 of itself, below pi / 4
+after the reduction; the polynomials' steps add less than that again), each of the two products and the sum rounds
 once: 8 * 2^-24 * amp * (|u| + |v|) covers it, then one rounding to the output
 type, at most half a step (bf16 2^-8 of the value with its eps of 2^-7, fp32
 2^-24).  E4M3: half a step is 2^-4 of the value, or 2^-10 of the scale among
