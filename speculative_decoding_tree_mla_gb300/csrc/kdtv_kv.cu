@@ -175,127 +175,182 @@ __device__ __forceinline__ long long row_of(const KvArgs& a, int b, int t) {
          t % a.page_size;
 }
 
-// A group of `group` lanes takes one row's heads h0, h0 + 1, .. of one part;
+// Converts a lane's elements of one head's row and stores them.  All lanes of
+// the group come along (shuffles); `on` lanes store.
+template <typename D, int V, int P>
+__device__ __forceinline__ void put_head(const KvPart& part, float kv_scale, int group, int lane, bool on,
+                                         float (&y)[P][V], D* dst, uint8_t* scale) {
+  if constexpr (sizeof(D) == 1) {
+    if (part.scale) {
+      // The smallest e with max <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of
+      // the largest finite magnitude.  2^-e is a power of two, so x * 2^-e loses
+      // nothing; a power also makes a code's value exact in bf16.
+      float mx = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int k = 0; k < V; ++k) mx = fmaxf(mx, fabsf(y[p][k]));   // (passes NaN by)
+      if (!(mx < INFINITY)) {
+        mx = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int k = 0; k < V; ++k) mx = fabsf(y[p][k]) < INFINITY ? fmaxf(mx, fabsf(y[p][k])) : mx;
+      }
+      for (int o = group / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const uint32_t bits = __float_as_uint(mx);
+      int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+      e = max(-117, min(119, e));
+      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[p][k] *= f;
+      if (on && lane == 0) *scale = (uint8_t)(e + 127);
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[p][k] = __fdiv_rn(y[p][k], kv_scale);
+    }
+  }
+  if (on)
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if ((p * group + lane) * V < part.dim) store_v<V>(dst + p * group * V, y[p]);
+}
+
+// A group of `group` lanes takes rows of one part, one head after the other;
 // lane l holds elements (p * group + l) * V + k, p < P, k < V, of the head.
-// The angles are computed once per row and serve its heads.  Rotated
-// elements of the half layout read their partner from memory a second time (a
-// cache hit: the partner's lane reads the same line).
+// The angles are computed once per row and serve its heads.  A block takes a
+// span of rows, so that looking its request's pages up does not count.
+//   V = 8, P = 1 (heads of up to 256, 16-byte accesses): the 16-byte vectors of
+// kBatch heads are loaded together and unpacked one by one, and the half
+// layout's rotation partners come from the lane that holds them.  DRAM bound
+// at prompt sizes, by way of the loads in flight: one head at a time, with the
+// partners read again, took 42 us for 13000 rows of 8 + 8 heads of 128.
+//   Otherwise one head at a time, partners read again.
 template <typename S, typename D, int V, int P>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ kdtv_rope_table tab,
-                                                             const __grid_constant__ KvArgs a) {
+                                                             const __grid_constant__ KvArgs a, int span) {
   const KvPart& part = a.part[blockIdx.z];
   const int b = blockIdx.y;
   const int n = live_rows(a.n_live, b, a.N);
-  if (n == 0) return;
+  const int i0 = (int)(blockIdx.x / a.hgroups) * span, i1 = min(n, i0 + span);
   const int L = a.prefix_len ? a.prefix_len[b] : 0;
-  if (!rows_ok(a, b, L, n)) return;
-  const int group = part.group, lane = threadIdx.x % group;
-  const long long u = ((long long)blockIdx.x * kThreads + threadIdx.x) / group;
-  const int hg = (int)(u % a.hgroups);
-  const long long i = u / a.hgroups;
-  const bool live = i < n;                     // dead lanes stay for the shuffles
-  const int ii = live ? (int)i : 0;
+  // (every block looks the whole request up: it is written as a whole or not at all)
+  if (n == 0 || i0 >= i1 || !rows_ok(a, b, L, n)) return;
+  const int group = part.group, lane = threadIdx.x % group, groups = kThreads / group;
   const int per = (part.heads + a.hgroups - 1) / a.hgroups;
-  const int h0 = hg * per, h1 = min(h0 + per, part.heads);
-  const long long row = row_of(a, b, L + ii);
-  const S* src = static_cast<const S*>(part.src) + b * part.ss[0] + ii * part.ss[1];
+  const int h0 = (int)(blockIdx.x % a.hgroups) * per, h1 = min(h0 + per, part.heads);
+  if (h0 >= h1) return;
   const bool half = tab.layout == KDTV_ROPE_HALF;
 
-  // this lane's angles; mate: distance to the rotation partner (half layout)
-  float2 cs[P][V];
+  // distance to this lane's rotation partners (0: not rotated)
   int mate[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    mate[p] = 0;
     const int r0 = (p * group + lane) * V - part.rot_off;     // first element, in the rotated part
-    if (part.rotate && live && r0 >= 0 && r0 < tab.rot_dim) {
-      const long long pos = (long long)L + (a.depth ? a.depth[(long long)b * a.N + ii] : ii);
-      const int hd = tab.rot_dim / 2;
-      mate[p] = half ? (r0 < hd ? hd : -hd) : ((r0 & 1) ? -1 : 1);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        if (half) cs[p][k] = rope_cos_sin(tab.turn[(r0 < hd ? r0 : r0 - hd) + k], pos, tab.amp);
-        else if (V == 1 || (k & 1) == 0) cs[p][k] = rope_cos_sin(tab.turn[(r0 + k) / 2], pos, tab.amp);
-        else cs[p][k] = cs[p][k - 1];
-      }
-    }
+    const bool in = part.rotate && r0 >= 0 && r0 < tab.rot_dim;
+    mate[p] = !in ? 0 : half ? (r0 < tab.rot_dim / 2 ? tab.rot_dim / 2 : -(tab.rot_dim / 2)) : ((r0 & 1) ? -1 : 1);
   }
-
-  // (one head a turn: two or four, with their loads under way together, took
-  // 50 and 70 us against 42 for 16000 rows of 8 + 8 heads, in registers and so in warps)
-  constexpr int kBatch = 1;
-  for (int hh = h0; hh < h0 + per; hh += kBatch) {
-    float x[kBatch][P][V], m[kBatch][P][V];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int e = (p * group + lane) * V;
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[j][p][k] = 0.f;
-        if (!live || hh + j >= h1 || e >= part.dim) continue;
-        const S* s = src + (hh + j) * part.ss[2] + e;
-        load_v<V>(s, x[j][p]);
-        if (mate[p] != 0 && (half || V == 1)) load_v<V>(s + mate[p], m[j][p]);
-      }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int h = hh + j;
-      const bool on = live && h < h1;
+  const int turns = (i1 - i0 + groups - 1) / groups;          // of rows: the same for all lanes (shuffles)
+  int i = i0 + threadIdx.x / group;
+  for (int turn = 0; turn < turns; ++turn, i += groups) {
+    const bool on = i < i1;
+    const long long row = on ? row_of(a, b, L + i) : 0;
+    const S* src = static_cast<const S*>(part.src) + b * part.ss[0] + (on ? i : i0) * part.ss[1] + lane * V;
+    D* dst = static_cast<D*>(part.cache) + row * part.heads * part.dim + lane * V;
+    uint8_t* scale = part.scale ? part.scale + row * part.heads : nullptr;
+    auto angles = [&](float2 (&cs)[P][V]) {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         if (mate[p] == 0 || !on) continue;
-        if (half || V == 1) {
+        const int r0 = (p * group + lane) * V - part.rot_off, hd = tab.rot_dim / 2;
+        const long long pos = (long long)L + (a.depth ? a.depth[(long long)b * a.N + i] : i);
 #pragma unroll
-          for (int k = 0; k < V; ++k)
-            x[j][p][k] = mate[p] > 0 ? x[j][p][k] * cs[p][k].x - m[j][p][k] * cs[p][k].y
-                                     : x[j][p][k] * cs[p][k].x + m[j][p][k] * cs[p][k].y;
-        } else {
-#pragma unroll
-          for (int k = 0; k + 1 < V; k += 2) {
-            const float u0 = x[j][p][k], v0 = x[j][p][k + 1];
-            x[j][p][k] = u0 * cs[p][k].x - v0 * cs[p][k].y;
-            x[j][p][k + 1] = v0 * cs[p][k].x + u0 * cs[p][k].y;
-          }
+        for (int k = 0; k < V; ++k) {
+          if (half) cs[p][k] = rope_cos_sin(tab.turn[(r0 < hd ? r0 : r0 - hd) + k], pos, tab.amp);
+          else if (V == 1 || (k & 1) == 0) cs[p][k] = rope_cos_sin(tab.turn[(r0 + k) / 2], pos, tab.amp);
+          else cs[p][k] = cs[p][k - 1];
+          if (mate[p] < 0 && (half || V == 1)) cs[p][k].y = -cs[p][k].y;   // the second of its pair
         }
       }
-      D* dst = static_cast<D*>(part.cache) + (row * part.heads + h) * part.dim;
-      if constexpr (sizeof(D) == 1) {
-        if (part.scale) {
-          // The smallest e with max <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of
-          // the largest finite magnitude.  2^-e is a power of two, so x * 2^-e loses
-          // nothing; a power also makes a code's value exact in bf16.
-          float mx = 0.f;
+    };
+    float2 cs[P][V];
+    if constexpr (V == 8 && P == 1) {
+      constexpr int kWords = 8 * sizeof(S) / 16, kBatch = 8 / kWords;
+      const int from = threadIdx.x % 32 + mate[0] / 8;         // lane with the partners (half layout)
+      for (int hh = h0; hh < h1; hh += kBatch) {
+        uint4 raw[kBatch][kWords];
 #pragma unroll
-          for (int p = 0; p < P; ++p)
+        for (int j = 0; j < kBatch; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-              const float f = fabsf(x[j][p][k]);
-              mx = f < INFINITY ? fmaxf(mx, f) : mx;
+          for (int w = 0; w < kWords; ++w)
+            raw[j][w] = on && hh + j < h1 && lane * V < part.dim
+                            ? reinterpret_cast<const uint4*>(src + (hh + j) * part.ss[2])[w] : make_uint4(0u, 0u, 0u, 0u);
+        if (hh == h0) angles(cs);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (hh + j >= h1) break;
+          float y[1][8];
+          unpack8<S>(raw[j], y[0]);
+          if (part.rotate) {
+            if (half) {
+              uint4 other[kWords];
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                other[w].x = __shfl_sync(0xffffffffu, raw[j][w].x, from);
+                other[w].y = __shfl_sync(0xffffffffu, raw[j][w].y, from);
+                other[w].z = __shfl_sync(0xffffffffu, raw[j][w].z, from);
+                other[w].w = __shfl_sync(0xffffffffu, raw[j][w].w, from);
+              }
+              float m[8];
+              unpack8<S>(other, m);
+              if (mate[0] != 0)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[0][k] = y[0][k] * cs[0][k].x - m[k] * cs[0][k].y;
+            } else if (mate[0] != 0) {
+#pragma unroll
+              for (int k = 0; k < 8; k += 2) {
+                const float u = y[0][k], v = y[0][k + 1];
+                y[0][k] = u * cs[0][k].x - v * cs[0][k].y;
+                y[0][k + 1] = v * cs[0][k].x + u * cs[0][k].y;
+              }
             }
-          for (int o = group / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const uint32_t bits = __float_as_uint(mx);
-          int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-          e = max(-117, min(119, e));
-          const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int k = 0; k < V; ++k) x[j][p][k] *= f;
-          if (on && lane == 0) part.scale[row * part.heads + h] = (uint8_t)(e + 127);
-        } else {
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int k = 0; k < V; ++k) x[j][p][k] = __fdiv_rn(x[j][p][k], a.kv_scale);
+          }
+          put_head<D, V, P>(part, a.kv_scale, group, lane, on, y, dst + (hh + j) * part.dim, scale + (hh + j));
         }
       }
-      if (on)
+    } else {
+      angles(cs);
+      for (int h = h0; h < h1; ++h) {
+        float y[P][V];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const int e = (p * group + lane) * V;
-          if (e < part.dim) store_v<V>(dst + e, x[j][p]);
+#pragma unroll
+          for (int k = 0; k < V; ++k) y[p][k] = 0.f;
+          const int e = p * group * V;
+          if (!on || e + lane * V >= part.dim) continue;
+          const S* s = src + h * part.ss[2] + e;
+          load_v<V>(s, y[p]);
+          if (mate[p] == 0) continue;
+          if (half || V == 1) {
+            float m[V];
+            load_v<V>(s + mate[p], m);
+#pragma unroll
+            for (int k = 0; k < V; ++k) y[p][k] = y[p][k] * cs[p][k].x - m[k] * cs[p][k].y;
+          } else {
+#pragma unroll
+            for (int k = 0; k + 1 < V; k += 2) {
+              const float u = y[p][k], v = y[p][k + 1];
+              y[p][k] = u * cs[p][k].x - v * cs[p][k].y;
+              y[p][k + 1] = v * cs[p][k].x + u * cs[p][k].y;
+            }
+          }
         }
+        put_head<D, V, P>(part, a.kv_scale, group, lane, on, y, dst + h * part.dim, scale + h);
+      }
     }
   }
 }
@@ -419,15 +474,18 @@ cudaError_t launch_append(const kdtv_rope_table& tab, KvArgs& a, cudaStream_t st
       while (p.group > 1 && p.group / 2 * 8 >= p.dim) p.group /= 2;
     lanes = p.group > lanes ? p.group : lanes;
   }
-  // Groups of heads per row: one thread's heads share its angles, but a few
-  // rows are spread over more threads.
+  // A few rows are spread over more blocks by heads; many rows get spans of them, about eight
+  // blocks an SM in all.
+  const int rows_turn = kThreads / lanes;                    // rows a block has at a time
   a.hgroups = 1;
   while (2 * a.hgroups <= heads && (long long)a.B * a.N * a.hgroups * lanes < 152ll * 1024) a.hgroups *= 2;
-  const long long bx = ((long long)a.N * a.hgroups * lanes + kThreads - 1) / kThreads;
-  const dim3 grid((unsigned)bx, (unsigned)a.B, (unsigned)a.parts);
+  long long blocks = 8ll * 152 / ((long long)a.B * a.parts * a.hgroups);
+  blocks = blocks < 1 ? 1 : blocks;
+  const int span = (int)(((a.N + blocks - 1) / blocks + rows_turn - 1) / rows_turn * rows_turn);
+  const dim3 grid((unsigned)((a.N + span - 1) / span * a.hgroups), (unsigned)a.B, (unsigned)a.parts);
   auto kern = !vec ? kv_append_kernel<S, D, 1, 16>
                    : (wide ? kv_append_kernel<S, D, 8, 2> : kv_append_kernel<S, D, 8, 1>);
-  kern<<<grid, kThreads, 0, st>>>(tab, a);
+  kern<<<grid, kThreads, 0, st>>>(tab, a, span);
   return cudaGetLastError();
 }
 

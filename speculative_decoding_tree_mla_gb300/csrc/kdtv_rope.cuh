@@ -41,6 +41,26 @@ __device__ __forceinline__ void load_v(const __nv_bfloat16* p, float (&x)[V]) {
     for (int k = 0; k < V; ++k) x[k] = __bfloat162float(p[k]);
   }
 }
+// Eight elements from their 16-byte words.
+template <typename S>
+__device__ __forceinline__ void unpack8(const uint4* w, float (&x)[8]) {
+  if constexpr (sizeof(S) == 2) {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = __uint_as_float(u[k] << 16);
+      x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x[4 * h] = __uint_as_float(w[h].x);
+      x[4 * h + 1] = __uint_as_float(w[h].y);
+      x[4 * h + 2] = __uint_as_float(w[h].z);
+      x[4 * h + 3] = __uint_as_float(w[h].w);
+    }
+  }
+}
 template <int V>
 __device__ __forceinline__ void load_v(const float* p, float (&x)[V]) {
   if constexpr (V % 4 == 0) {
