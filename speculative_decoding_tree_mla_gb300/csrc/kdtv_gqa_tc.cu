@@ -62,8 +62,8 @@ enum {
   B_RAW_FULL = B_TAIL, B_RAW_EMPTY = B_RAW_FULL + kRing, B_K_FULL = B_RAW_EMPTY + kRing,
   B_K_EMPTY = B_K_FULL + kRing, B_Q_FULL = B_K_EMPTY + kRing,
   B_Q_READY, B_Q_EMPTY, B_S_FULL, B_P_HALF = B_S_FULL + 2, B_P_READY = B_P_HALF + 2,
-  B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2, B_O1_FREE, B_MMA_DONE, B_STALL, B_STAGGER,
-  B_SCALE_FREE, B_PIECE = B_SCALE_FREE + 2, B_PIECE_READ = B_PIECE + kPieces,
+  B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2, B_O1_FREE, B_MMA_DONE, B_STALL, B_TURN,
+  B_SCALE_FREE = B_TURN + 2, B_PIECE = B_SCALE_FREE + 2, B_PIECE_READ = B_PIECE + kPieces,
   B_COUNT = B_PIECE_READ + kPieces
 };
 
@@ -377,7 +377,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     mbar_init(BAR(B_O1_FREE), 4);
     mbar_init(BAR(B_MMA_DONE), 2);
     mbar_init(BAR(B_STALL), 1);
-    mbar_init(BAR(B_STAGGER), 4);
+    mbar_init(BAR(B_TURN), 1);
+    mbar_init(BAR(B_TURN + 1), 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(BAR(B_PIECE + i), 1);
       mbar_init(BAR(B_PIECE_READ + i), 15);      // producer, two issuers, 4 + 8 warps
@@ -628,7 +629,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     bool alive = true;
     Ring<C::kSlots> ring;
     Ring<kFp8 ? C::kRaw : 1> kring;
-    uint32_t p_phase = 0u, stagger = 0u;
+    uint32_t p_phase = 0u, turn = s == 0 ? 1u : 0u;   // (stream 0 begins)
     for (int index = 0; __all_sync(0xffffffffu, alive) && get_piece(index, p); ++index) {
       const int n = p.t1 - p.t0;
       const bool two = p.two();
@@ -636,14 +637,14 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (lane != 0) continue;
       const uint64_t ad = q_desc + (uint32_t)(two ? s * (C::kTileBytes >> 4) : 0);
       alive = wait(guard, BAR(kFp8 ? B_Q_READY : B_Q_FULL), index & 1);
-      if (alive && two && s == 1) {
-        // Half a turn behind stream 0, so that one's products run beside the other's softmax
-        alive = wait(guard, BAR(B_STAGGER), stagger);
-        stagger ^= 1u;
-      }
-      for (int i = 0; alive && i < n + lag; ++i) {
+      // The streams take turns: a step's products run as one, and beside the other stream's softmax.
+      // (Products that share the tensor cores end together, and then so do the softmaxes.)  In a
+      // one-tile piece the steps alternate between the streams; an even number of them, so that the
+      // next piece begins with stream 0 again.
+      const int steps = two ? n + lag : (n + lag + 1) & ~1;
+      for (int i = 0; alive && i < steps; ++i) {
         const int vt = i - lag;
-        const bool mine = two || (i & 1) == s, has_v = vt >= 0, has_k = i < n;
+        const bool mine = two || (i & 1) == s, has_v = vt >= 0 && vt < n, has_k = i < n;
         // the entries first (loaded long ago), then the softmax: from there on the products follow
         // one another
         // the entries and the softmax; one look at all three, because each costs its latency
@@ -662,6 +663,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!(v_ok && k_ok && p_ok))
           alive = (v_ok || wait(guard, v_full, v_phase)) && (k_ok || wait(guard, k_full, k_phase)) &&
                   (p_ok || wait(guard, p_half, p_phase));
+        if (mine) {
+          alive = alive && wait(guard, BAR(B_TURN + s), turn);
+          turn ^= 1u;
+        }
         if (!alive) break;
         if (!mine) {
           if (has_v) mbar_arrive(BAR(B_KV_EMPTY + v_slot));
@@ -699,7 +704,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               }
             }
             mma_commit(BAR(B_S_FULL + s));
+            mbar_arrive(BAR(B_TURN + 1 - s));
             mma_commit(k_empty);
+          } else {
+            mbar_arrive(BAR(B_TURN + 1 - s));
           }
           if (has_v) {
             mma_commit(BAR(B_KV_EMPTY + v_slot));
@@ -961,7 +969,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               for (int k = 0; k < (two ? 1 : 2); ++k) mbar_arrive(BAR(B_SCALE_FREE + ((k_tiles + i) & 1)));
             mbar_arrive(BAR(B_P_HALF + s));
             mbar_arrive(BAR(B_P_READY + s));
-            if (two && s == 0 && i == 0) mbar_arrive(BAR(B_STAGGER));
           }
           __syncwarp();
           continue;
@@ -1102,7 +1109,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && two && s == 0 && i == 0) mbar_arrive(BAR(B_STAGGER));
         if (lane == 0) mbar_arrive(BAR(B_P_READY + s));
       }
       if (!alive) break;
