@@ -663,9 +663,11 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!(v_ok && k_ok && p_ok))
           alive = (v_ok || wait(guard, v_full, v_phase)) && (k_ok || wait(guard, k_full, k_phase)) &&
                   (p_ok || wait(guard, p_half, p_phase));
+        bool all_ready = false;
         if (mine) {
           alive = alive && wait(guard, BAR(B_TURN + s), turn);
           turn ^= 1u;
+          all_ready = mbar_try_wait(BAR(B_P_READY + s), p_phase);
         }
         if (!alive) break;
         if (!mine) {
@@ -679,10 +681,12 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, kk > 0 ? 1u : acc);
-            alive = wait(guard, BAR(B_P_READY + s), p_phase);
-            if (!alive) break;
+            if (!all_ready) {                                   // the second half, looked at before the turn
+              alive = wait(guard, BAR(B_P_READY + s), p_phase);
+              if (!alive) break;
+              tc_fence_after();
+            }
             p_phase ^= 1u;
-            tc_fence_after();
 #pragma unroll
             for (int kk = 4; kk < 8; ++kk) mma_bf16_ts(dO, dS + 8 * kk, bd + kk * 128, kIdescO, 1u);
           }
@@ -694,6 +698,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t part = (kk / (D / 32)) * (C::kRawBytes >> 4), off = (kk % (D / 32)) * 2;
                 mma_e4m3(dS, ad + part + off, bd + off, kIdescS, kk > 0);
+                // the other stream's issuer needs about as long to begin as the rest takes
+                if (kk == D / 32) mbar_arrive(BAR(B_TURN + 1 - s));
               }
             } else {
 #pragma unroll
@@ -701,10 +707,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 constexpr uint32_t kC = C::kChunk >> 4;
                 const uint32_t off = (kk >> 2) * kC + (kk & 3) * 2;
                 mma_bf16(dS, ad + off, bd + off, kIdescS, kk > 0);
+                if (kk == D / 32) mbar_arrive(BAR(B_TURN + 1 - s));   // (as above)
               }
             }
             mma_commit(BAR(B_S_FULL + s));
-            mbar_arrive(BAR(B_TURN + 1 - s));
             mma_commit(k_empty);
           } else {
             mbar_arrive(BAR(B_TURN + 1 - s));
