@@ -286,8 +286,10 @@ __device__ __forceinline__ bool drop_nan_codes(uint32_t src) {
   }
   return found;
 }
-// Register split: the launch has 512 x 128; the softmax warps take most (a row's
-// 128 scores stay in registers).
+// Register split with bf16 caches: the launch has 512 x 128; the softmax warps
+// take most (a row's 128 scores stay in registers).  With one-byte caches the
+// scores come in chunks and every role keeps its 128: 64 for the warps that
+// widen the values spilled, and 64 requests took 467 us instead of 426.
 constexpr int kRegsSoftmax = 192, kRegsAux = 64, kRegsControl = 64;
 static_assert(256 * kRegsSoftmax + 128 * kRegsAux + 128 * kRegsControl <= 512 * 128, "registers of the launch");
 template <int R>
@@ -411,7 +413,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
   // (the split is the first statement of each branch: the compiler allocates by branch)
   if (warp >= kWarpTma) {
-  reg_shrink<kRegsControl>();
+  if constexpr (!kFp8) reg_shrink<kRegsControl>();
   if (warp == kWarpPlan) {
     // ---- planner: W and this CTA's first unit (one pass over the requests for the total, one
     // to the unit), then its pieces
@@ -730,7 +732,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     __syncwarp();
   }
   } else if (warp >= kWarpAux) {
-    reg_shrink<kRegsAux>();
+    if constexpr (!kFp8) reg_shrink<kRegsAux>();
     // ---- widening (one-byte caches) and the last tiles: thread = key row of the tile -----------
     const int row = threadIdx.x - kWarpAux * 32;
     const int swz = row & 7;
@@ -751,23 +753,28 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if constexpr (kFp8) {
         // The scale bytes of tile i + 2 are loaded at the end of step i, with a page id loaded a step
         // before: behind the step's proxy fence, which waits for every load that is under way.
-        auto page_of = [&](int i) -> int {
-          const int t = (p.t0 + i) * kTile + row;
-          if (!a.page_size || i >= n || t >= T) return 0;
-          return a.page_table[(long long)p.b * a.max_pages + (t >> a.page_shift)];
+        // (Positions behind the last are read as the last: every address is one of the request's.)
+        const int32_t* table = a.page_table + (long long)p.b * a.max_pages;
+        const uint8_t* ks = a.k_scale + kvh;
+        const uint8_t* vs = a.v_scale + kvh;
+        int t_at = p.t0 * kTile + row;                // of the tile whose page id is loaded next
+        auto next_page = [&]() -> int {
+          const int t = min(t_at, T - 1);
+          return a.page_size ? table[t >> a.page_shift] : 0;
         };
-        auto byte_at = [&](int i, int page) -> long long {         // of tile i's row, with its page id
-          const int t = (p.t0 + i) * kTile + row;
-          if (i >= n || t >= T) return kvh;
-          if (!a.page_size) return ((long long)p.b * a.t_stride + t) * a.Hkv + kvh;
-          if (page < 0 || page >= a.num_pages) page = 0;
-          return (((long long)page << a.page_shift) + (t & (a.page_size - 1))) * a.Hkv + kvh;
+        auto row_of_scale = [&](int page) -> long long {   // of t_at's row; moves on to the next tile
+          const int t = min(t_at, T - 1);
+          t_at += kTile;
+          const int pg = (unsigned)page < (unsigned)a.num_pages ? page : 0;
+          const long long r = a.page_size ? ((long long)pg << a.page_shift) + (t & (a.page_size - 1))
+                                          : (long long)p.b * a.t_stride + t;
+          return r * a.Hkv;
         };
-        const int page_first = page_of(0), page_second = page_of(1);
-        int page_next = page_of(2);
-        const long long at0 = byte_at(0, page_first), at1 = byte_at(1, page_second);
-        int k0 = a.k_scale[at0], k1 = a.k_scale[at1];      // of tiles i, i + 1
-        int v1 = a.v_scale[at1], v0 = a.v_scale[at0], vm1 = 0, vm2 = 0;   // of tiles i + 1 .. i - 2
+        long long at = row_of_scale(next_page());
+        int k0 = ks[at], v0 = vs[at];                      // of tiles i, i + 1
+        at = row_of_scale(next_page());
+        int k1 = ks[at], v1 = vs[at], vm1 = 0, vm2 = 0;    // values: of tiles i + 1 .. i - 2
+        int page_next = next_page();
 
         // Q: each row's two E4M3 parts in place of its bf16 (while the scale bytes arrive)
         alive = wait_warp(guard, BAR(B_Q_FULL), index & 1);
@@ -877,10 +884,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           vm2 = vm1;
           vm1 = v0;
           v0 = v1;
-          const long long at = byte_at(i + 2, page_next);
-          k1 = a.k_scale[at];
-          v1 = a.v_scale[at];
-          page_next = page_of(i + 3);
+          at = row_of_scale(page_next);
+          k1 = ks[at];
+          v1 = vs[at];
+          page_next = next_page();
         }
       } else {
         const int from = max(p.t0, p.L / kTile);          // the first key tile that reaches past the prefix
@@ -918,7 +925,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       }
     }
   } else {
-    reg_grow<kRegsSoftmax>();
+    if constexpr (!kFp8) reg_grow<kRegsSoftmax>();
     // ---- softmax and epilogue: thread = row 32 q + lane of stream s -----------------------------
     const int s = warp >> 2, q = warp & 3, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
