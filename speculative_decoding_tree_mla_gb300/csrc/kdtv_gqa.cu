@@ -246,7 +246,7 @@ bool on_tensor_cores(const kdtv_gqa_dims* d) {
 }
 
 // Fills the plan of `a` and the offsets of its partials; the status a call returns.
-int make_plan(const kdtv_gqa_dims* d, GqaArgs* a, size_t* off_ml, size_t* total) {
+int make_plan(const kdtv_gqa_dims* d, GqaArgs* a, size_t* off_ml, size_t* off_plan, size_t* total) {
   const int rc = check(d);
   if (rc != KDTV_OK) return rc;
   memset(a, 0, sizeof(*a));
@@ -271,7 +271,8 @@ int make_plan(const kdtv_gqa_dims* d, GqaArgs* a, size_t* off_ml, size_t* total)
     rows = a->splits > 1 ? (size_t)a->splits * d->B * d->N * d->H : 0;
   }
   *off_ml = align256(rows * d->d * sizeof(float));
-  *total = *off_ml + align256(rows * sizeof(float2)) + 256;
+  *off_plan = *off_ml + align256(rows * sizeof(float2));
+  *total = *off_plan + align256((size_t)(1 + d->B) * sizeof(int));
   return KDTV_OK;
 }
 
@@ -283,14 +284,14 @@ using namespace kdtv;
 
 extern "C" size_t kdtv_gqa_workspace_size(const kdtv_gqa_dims* d) {
   GqaArgs a;
-  size_t off, total;
-  return make_plan(d, &a, &off, &total) == KDTV_OK ? total : 0;
+  size_t off, plan, total;
+  return make_plan(d, &a, &off, &plan, &total) == KDTV_OK ? total : 0;
 }
 
 extern "C" int kdtv_gqa_launches_per_call(const kdtv_gqa_dims* d) {
   GqaArgs a;
-  size_t off, total;
-  if (make_plan(d, &a, &off, &total) != KDTV_OK) return -1;
+  size_t off, plan, total;
+  if (make_plan(d, &a, &off, &plan, &total) != KDTV_OK) return -1;
   return on_tensor_cores(d) ? 2 : (a.splits > 1 ? 2 : 1);
 }
 
@@ -300,8 +301,8 @@ extern "C" int kdtv_gqa_verify_attn(const kdtv_gqa_dims* d, const void* q, const
                                     const int32_t* n_nodes, const int32_t* page_table, void* out,
                                     unsigned int* status, cudaStream_t stream) {
   GqaArgs a;
-  size_t off_ml, total;
-  const int rc = make_plan(d, &a, &off_ml, &total);
+  size_t off_ml, off_plan, total;
+  const int rc = make_plan(d, &a, &off_ml, &off_plan, &total);
   if (rc != KDTV_OK) return rc;
   if (!q || !k || !v || !parent || !prefix_len || !out || !status) return KDTV_ERR_INVALID_ARG;
   if ((d->page_size > 0) != (page_table != nullptr)) return KDTV_ERR_INVALID_ARG;
@@ -318,6 +319,7 @@ extern "C" int kdtv_gqa_verify_attn(const kdtv_gqa_dims* d, const void* q, const
   a.status = status;
   a.part_o = static_cast<float*>(d->workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(d->workspace) + off_ml);
+  a.plan = reinterpret_cast<int*>(static_cast<char*>(d->workspace) + off_plan);
   if (on_tensor_cores(d)) return launch_gqa_tc(a, (d->flags & KDTV_FLAG_TEST_STALL) != 0, stream);
   return launch_gqa_simt(a, stream);
 }

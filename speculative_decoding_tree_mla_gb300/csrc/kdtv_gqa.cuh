@@ -19,6 +19,7 @@ struct GqaArgs {
   unsigned int* status;
   float* part_o;               // partial rows (unnormalised), fp32
   float2* part_ml;             // {reference maximum (log2 units), sum}; sum < 0: the row is not written
+  int* plan;                   // tensor cores: units per group of CTAs, then each request's first unit
   int chunk, splits;           // CUDA cores: keys per split, splits
   // tensor cores: heads side by side in a group of CTAs, groups, nodes per 128-row tile (128 / G),
   // log2 of page_size

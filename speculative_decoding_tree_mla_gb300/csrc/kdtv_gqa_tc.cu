@@ -418,6 +418,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     // ---- planner: W and this CTA's first unit (one pass over the requests for the total, one
     // to the unit), then its pieces
     int sum = 0;
+#pragma unroll 1
     for (int b = lane; b < a.B; b += 32) sum += units_of(a, b);
     sum = __reduce_add_sync(0xffffffffu, sum);
     const int W = (sum + a.groups - 1) / a.groups;
@@ -427,6 +428,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     int at = first < sum ? (int)first : 0, b = 0, off = 0;
     if (end > 0) {
       int before = 0;
+      if (blockIdx.x == 0 && lane == 0) a.plan[0] = W;          // for the combine kernel
+#pragma unroll 1
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int u = b0 + lane < a.B ? units_of(a, b0 + lane) : 0;
         int scan = u;
@@ -436,11 +439,12 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (lane >= o) scan += x;
         }
         const int lo = before + scan - u;
+        if (blockIdx.x == 0 && b0 + lane < a.B) a.plan[1 + b0 + lane] = lo;
         const uint32_t here = __ballot_sync(0xffffffffu, u > 0 && at >= lo && at < lo + u);
         if (here) {
           b = b0 + __ffs(here) - 1;
           off = at - __shfl_sync(0xffffffffu, lo, __ffs(here) - 1);
-          break;
+          if (blockIdx.x > 0) break;               // (the first CTA goes on: it writes the plan)
         }
         before += __shfl_sync(0xffffffffu, scan, 31);
       }
@@ -1231,96 +1235,79 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
 // ---- combine --------------------------------------------------------------------------------
 // Output rows of items that were cut into pieces: the pieces' sums and outputs
-// meet at their common maximum.  blockIdx.y is the request; a warp per row, the
-// row's d elements across its lanes.  Item [S, S + nt) was cut at the multiples
-// of W; a CTA's piece that starts its range is partial 2 cta, one that starts
-// later 2 cta + 1.
+// meet at their common maximum.  A CTA takes kRowsCta rows of a (request, head,
+// row tile), a warp one row at a time, the row's d elements across its lanes.
+// Item [S, S + nt) was cut at the multiples of W; a CTA's piece that starts its
+// range is partial 2 cta, one that starts later 2 cta + 1.  W and the requests'
+// first units were left by the attention kernel.  Latency bound: the first
+// pieces' rows are loaded along with their {max, sum}.
+constexpr int kRowsCombine = 32;
+
 template <int D>
-__global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant__ GqaArgs a) {
-  __shared__ int s_sum[8], s_before[8];
-  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int sum = 0, before = 0;
-  for (int x = threadIdx.x; x < a.B; x += 256) {
-    const int u = units_of(a, x);
-    sum += u;
-    if (x < b) before += u;
-  }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  before = __reduce_add_sync(0xffffffffu, before);
-  if (lane == 0) {
-    s_sum[warp] = sum;
-    s_before[warp] = before;
-  }
-  __syncthreads();
-  sum = before = 0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    sum += s_sum[w];
-    before += s_before[w];
-  }
+__global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant__ GqaArgs a, int tiles) {
+  const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.x / tiles, tile = blockIdx.x % tiles, r0 = blockIdx.y * kRowsCombine;
   int L, n;
   gqa_request(a, b, &L, &n);
-  grid_dep_wait();                                 // the partials are written
-  if (n == 0 || *reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
-  const int W = (sum + a.groups - 1) / a.groups;
-  const int nt = key_tiles(L, n), rps = row_pairs(a, n);
-  const int rows = n * a.H;
+  const int rows = min(a.npt, n - tile * a.npt) * a.G;           // of the tile
+  if (r0 >= rows) return;
+  grid_dep_wait();                                 // the partials and the plan are written
+  if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
+  const int W = a.plan[0], nt = key_tiles(L, n);
+  const int start = a.plan[1 + b] + (kvh / a.hg * row_pairs(a, n) + tile / 2) * nt;
+  const int c0 = start / W, count = (start + nt - 1) / W - c0 + 1;
+  if (count == 1) return;                          // whole: written by its CTA
   constexpr int V = D / 32;                        // elements per lane
-  for (int row = blockIdx.x * 8 + warp; row < rows; row += gridDim.x * 8) {
-    const int node = row / a.H, h = row % a.H, kvh = h / a.G;
-    const int tile = node / a.npt;
-    const int start = before + (kvh / a.hg * rps + tile / 2) * nt, end = start + nt;
-    const int c0 = start / W, c1 = (end - 1) / W;
-    if (c0 == c1) continue;                        // whole: written by its CTA
-    const int r = (tile & 1) * kTile + (node % a.npt) * a.G + h % a.G;
-    const bool later = start != c0 * W;            // of the first piece; the others start their CTA's range
-    auto prow = [&](int c) { return (2ll * (c * a.hg + kvh % a.hg) + (c == c0 && later)) * (2 * kTile) + r; };
-    // lane k: {max, sum} of piece k of each 32, and the weight that brings it to the common maximum
-    float m = -INFINITY;
+  const int head = kvh % a.hg;
+  const bool later = start != c0 * W;              // of the first piece; the others start their CTA's range
+  const int recip = 65536 / a.G + 1;               // r / G = (r recip) >> 16 for r, G <= 128
+  for (int r = r0 + warp; r < min(rows, r0 + kRowsCombine); r += 8) {
+    const int i = (r * recip) >> 16, node = tile * a.npt + i, h = kvh * a.G + r - i * a.G;
+    auto prow = [&](int k) {                       // partial row of piece k
+      return (2ll * ((c0 + k) * a.hg + head) + (k == 0 && later)) * (2 * kTile) + (tile & 1) * kTile + r;
+    };
+    float m = -INFINITY, l = 0.f, o[V];
     bool skip = false;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float2 ml = a.part_ml[prow(c)];
-      skip |= ml.y < 0.f;
-      m = fmaxf(m, ml.x);
-    }
-    if (__any_sync(0xffffffffu, skip)) continue;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] = 0.f;
-    for (int cb = c0; cb <= c1; cb += 32) {
-      const int cl = min(cb + lane, c1);
-      const float2 ml = a.part_ml[prow(cl)];
-      const float w = cb + lane <= c1 ? ex2(ml.x - ref) : 0.f;
-      if (cb + lane <= c1) l += ml.y * w;
-      const int count = min(32, c1 - cb + 1);
-      for (int j = 0; j < count; j += 8) {         // eight partial rows in flight
-        float x[8][V];
+#pragma unroll 1
+    for (int base = 0; base < count; base += 8) {  // eight pieces in flight; a running maximum over the eights
+      float2 x[8][V / 2];
+      const bool have = lane < 8 && base + lane < count;
+      const float2 ml = have ? a.part_ml[prow(base + lane)] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float* src = a.part_o + prow(min(cb + j + k, c1)) * D + V * lane;
+      for (int k = 0; k < 8; ++k)
+        if (base + k < count) {
+          const float2* src = reinterpret_cast<const float2*>(a.part_o + prow(base + k) * D + V * lane);
 #pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(src + e);
-            x[k][e] = f.x;
-            x[k][e + 1] = f.y;
-          }
+          for (int e = 0; e < V / 2; ++e) x[k][e] = src[e];
         }
+      skip |= ml.y < 0.f;
+      float mx = ml.x;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, w, (j + k) & 31);
-          if (j + k < count) {
+      for (int w = 4; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      mx = fmaxf(m, __shfl_sync(0xffffffffu, mx, 0));
+      const float ref = mx == -INFINITY ? 0.f : mx, alpha = ex2(m - ref), weight = ex2(ml.x - ref);
+      m = mx;
+      l = l * alpha + ml.y * weight;               // lanes 0 .. 7 hold parts of the sum
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = fmaf(x[k][e], wk, o[e]);
+      for (int e = 0; e < V; ++e) o[e] *= alpha;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = __shfl_sync(0xffffffffu, weight, k);
+        if (base + k < count)
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            o[2 * e] = fmaf(x[k][e].x, w, o[2 * e]);
+            o[2 * e + 1] = fmaf(x[k][e].y, w, o[2 * e + 1]);
           }
-        }
       }
     }
+    if (__any_sync(0xffffffffu, skip)) continue;
+    l = lane < 8 ? l : 0.f;
 #pragma unroll
-    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-    const float inv = 1.f / l;
+    for (int w = 4; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    const float inv = 1.f / __shfl_sync(0xffffffffu, l, 0);
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
                                                 (((long long)b * a.N + node) * a.H + h) * D) + V / 2 * lane;
 #pragma unroll
@@ -1353,10 +1340,10 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
   if (launch_ex(kern, dim3((unsigned)(a.groups * a.hg)), dim3(kThreads), C::kSmem, st, false, tq, tk, tv, a, stall ? 1 : 0) !=
       cudaSuccess)
     return KDTV_ERR_CUDA;
-  // a warp per row, up to about eight CTAs per SM
-  const long long want = ((long long)a.N * a.H + 7) / 8, most = 8ll * a.groups * a.hg / a.B + 1;
-  const int gx = (int)(want < most ? want : most);
-  if (launch_ex(gqa_combine_kernel<D>, dim3((unsigned)gx, (unsigned)a.B), dim3(256), 0, st, true, a) != cudaSuccess)
+  const int tiles = (a.N + a.npt - 1) / a.npt;
+  const int most = (a.N < a.npt ? a.N : a.npt) * a.G;          // rows of a tile
+  const dim3 grid((unsigned)(a.Hkv * tiles), (unsigned)((most + kRowsCombine - 1) / kRowsCombine), (unsigned)a.B);
+  if (launch_ex(gqa_combine_kernel<D>, grid, dim3(256), 0, st, true, a, tiles) != cudaSuccess)
     return KDTV_ERR_CUDA;
   return KDTV_OK;
 }
