@@ -12,21 +12,28 @@ namespace {
 
 // ---- CUDA cores -----------------------------------------------------------------------
 // A CTA of 4 warps takes 16 rows of one key/value head and one split of the
-// keys, 32 keys at a time: K and V staged in shared memory as fp32, each warp
-// four rows.  Scores: a lane per key (K rows padded by one word against bank
-// conflicts, four rows share each K load).  Softmax: online, across the lanes.
-// Output: a lane holds elements lane + 32 k of the four rows.  Bound by the
-// fp32 pipe and shared-memory reads; the path exists for fp32 and for head
-// dims outside the tensor-core instances, not for speed.
+// keys, 32 keys at a time: K and V staged in shared memory as fp32 (a warp per
+// key row, rows padded with zeros to dp = 8 ceil(d / 8) elements and set 16
+// bytes apart from a multiple of the banks), each warp four rows.  Scores: a
+// lane per key, four elements an access, four rows share each K access.
+// Softmax: online, across the lanes.  Output: a lane holds elements lane + 32 k
+// of the four rows; four rows' weights of a key are one 16-byte read.  Bound by
+// the fp32 pipe and shared-memory reads; the path exists for fp32 and for head
+// dims outside the tensor-core instances.
 constexpr int kRowsCta = 16, kRowsWarp = 4, kKeys = 32, kSimtThreads = 128;
+__host__ __device__ constexpr int simt_padded(int d) { return (d + 7) / 8 * 8; }
+__host__ __device__ constexpr int simt_words(int d) {     // of shared memory
+  return 2 * kKeys * (simt_padded(d) + 4) + kRowsCta * simt_padded(d) + 4 * kKeys * kRowsWarp;
+}
 
-template <typename T, typename C, int DK>     // DK = ceil(d / 32)
+template <typename T, typename C, int DK>     // DK = ceil(d / 32), rounded up to an instance
 __global__ void __launch_bounds__(kSimtThreads) gqa_simt_kernel(const __grid_constant__ GqaArgs a) {
   extern __shared__ __align__(16) float sm[];
-  const int d = a.d, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* ks = sm;                                  // [kKeys][d + 1]
-  float* vs = ks + kKeys * (d + 1);                // [kKeys][d]
-  float* qs = vs + kKeys * d;                      // [kRowsCta][d]
+  const int d = a.d, dp = simt_padded(d), ld = dp + 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* ks = sm;                                  // [kKeys][ld]
+  float* vs = ks + kKeys * ld;                     // [kKeys][ld]
+  float* qs = vs + kKeys * ld;                     // [kRowsCta][dp]
+  float4* ps = reinterpret_cast<float4*>(qs + kRowsCta * dp) + warp * kKeys;   // this warp's weights, [kKeys]
   __shared__ uint32_t s_mask[kRowsCta][4];
   __shared__ int s_dead[kRowsCta];                 // 1: not a live row, 2: malformed root path
   const int b = blockIdx.z / a.Hkv, kvh = blockIdx.z % a.Hkv;
@@ -52,9 +59,9 @@ __global__ void __launch_bounds__(kSimtThreads) gqa_simt_kernel(const __grid_con
   auto out_row = [&](int r) {
     return ((long long)b * a.N + r / a.G) * a.H + (long long)kvh * a.G + r % a.G;
   };
-  for (int i = threadIdx.x; i < kRowsCta * d; i += kSimtThreads) {
-    const int r = r0 + i / d;
-    qs[i] = r < rows ? to_f32(static_cast<const T*>(a.q)[out_row(r) * d + i % d]) : 0.f;
+  for (int j = warp; j < kRowsCta; j += 4) {
+    const T* src = static_cast<const T*>(a.q) + out_row(min(r0 + j, rows - 1)) * d;
+    for (int e = lane; e < dp; e += 32) qs[j * dp + e] = e < d ? to_f32(src[e]) : 0.f;
   }
   __syncthreads();
 
@@ -74,70 +81,105 @@ __global__ void __launch_bounds__(kSimtThreads) gqa_simt_kernel(const __grid_con
   for (int t0 = t_lo; t0 < t_hi; t0 += kKeys) {
     __syncthreads();
     const int nk = min(kKeys, t_hi - t0);
-    for (int i = threadIdx.x; i < kKeys * d; i += kSimtThreads) {
-      const int j = i / d, e = i % d;
-      float kx = 0.f, vx = 0.f;
-      if (j < nk) {
-        const long long row = gqa_row(a, b, t0 + j);
-        if (row < 0) {
-          bad_page = 1;
-        } else {
-          const long long at = (row * a.Hkv + kvh) * d + e;
-          kx = to_f32(static_cast<const C*>(a.k)[at]);
-          vx = to_f32(static_cast<const C*>(a.v)[at]);
+#pragma unroll 1
+    for (int j0 = 0; j0 < kKeys; j0 += 16) {         // a warp's four rows of these: under way together
+      float kx[4][DK], vx[4][DK];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 4 * u + warp;
+        const long long row = j < nk ? gqa_row(a, b, t0 + j) : 0;
+        if (row < 0) bad_page = 1;
+        const bool on = j < nk && row >= 0;
+        const long long at = (row * a.Hkv + kvh) * d;
+        float fk = 1.f, fv = 1.f;
+        if constexpr (sizeof(C) == 1) {
+          if (on) {
+            fk = scale_of_byte(a.k_scale[row * a.Hkv + kvh]);
+            fv = scale_of_byte(a.v_scale[row * a.Hkv + kvh]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < DK; ++k) {
+          const int e = lane + 32 * k;
+          kx[u][k] = on && e < d ? to_f32(static_cast<const C*>(a.k)[at + e]) : 0.f;
+          vx[u][k] = on && e < d ? to_f32(static_cast<const C*>(a.v)[at + e]) : 0.f;
           if constexpr (sizeof(C) == 1) {
-            kx *= scale_of_byte(a.k_scale[row * a.Hkv + kvh]);
-            vx *= scale_of_byte(a.v_scale[row * a.Hkv + kvh]);
+            kx[u][k] *= fk;
+            vx[u][k] *= fv;
           }
         }
       }
-      ks[j * (d + 1) + e] = kx;
-      vs[j * d + e] = vx;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < DK; ++k)
+          if (lane + 32 * k < dp) {
+            ks[(j0 + 4 * u + warp) * ld + lane + 32 * k] = kx[u][k];
+            vs[(j0 + 4 * u + warp) * ld + lane + 32 * k] = vx[u][k];
+          }
     }
     __syncthreads();
     float s[kRowsWarp];
 #pragma unroll
     for (int r = 0; r < kRowsWarp; ++r) s[r] = 0.f;
-    const float* kr = ks + lane * (d + 1);
-    const float* qr = qs + warp * kRowsWarp * d;
-    for (int e = 0; e < d; ++e) {
-      const float x = kr[e];
+    const float4* kr = reinterpret_cast<const float4*>(ks + lane * ld);
+    const float4* qr = reinterpret_cast<const float4*>(qs + warp * kRowsWarp * dp);
+#pragma unroll 4
+    for (int e = 0; e < dp / 4; ++e) {
+      const float4 x = kr[e];
 #pragma unroll
-      for (int r = 0; r < kRowsWarp; ++r) s[r] = fmaf(qr[r * d + e], x, s[r]);
+      for (int r = 0; r < kRowsWarp; ++r) {
+        const float4 y = qr[r * (dp / 4) + e];
+        s[r] = fmaf(y.x, x.x, s[r]);
+        s[r] = fmaf(y.y, x.y, s[r]);
+        s[r] = fmaf(y.z, x.z, s[r]);
+        s[r] = fmaf(y.w, x.w, s[r]);
+      }
     }
+    uint32_t see[kRowsWarp], any = 0u;
+    float p[kRowsWarp];
 #pragma unroll
     for (int r = 0; r < kRowsWarp; ++r) {
-      uint32_t see = gqa_visible(mask[r], t0, L);
-      if (nk < 32) see &= (1u << nk) - 1u;
-      const float x = (see >> lane) & 1u ? s[r] * sl2 : -INFINITY;
+      see[r] = gqa_visible(mask[r], t0, L);
+      if (nk < 32) see[r] &= (1u << nk) - 1u;
+      any |= see[r];
+      const float x = (see[r] >> lane) & 1u ? s[r] * sl2 : -INFINITY;
       float mx = x;
 #pragma unroll
       for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
       const float mn = fmaxf(m[r], mx);
       const float ref = mn == -INFINITY ? 0.f : mn;
-      const float p = gqa_ex2(x - ref), alpha = gqa_ex2(m[r] - ref);
-      float ps = p;
-#pragma unroll
-      for (int w = 16; w; w >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, w);
-      l[r] = l[r] * alpha + ps;
+      p[r] = gqa_ex2(x - ref);
+      const float alpha = gqa_ex2(m[r] - ref);
+      l[r] = l[r] * alpha + p[r];                    // lanes keep parts of the sum
       m[r] = mn;
 #pragma unroll
       for (int k = 0; k < DK; ++k) o[r][k] *= alpha;
-      // only what the row sees: a masked value may be infinite or NaN
-      while (see) {
-        const int j = __ffs(see) - 1;
-        see &= see - 1;
-        const float pj = __shfl_sync(0xffffffffu, p, j);
+    }
+    __syncwarp();
+    ps[lane] = make_float4(p[0], p[1], p[2], p[3]);
+    __syncwarp();
+    // only what a row sees: a masked value may be infinite or NaN
+    while (any) {
+      const int j = __ffs(any) - 1;
+      any &= any - 1;
+      const float4 w = ps[j];
+      float v[DK];
 #pragma unroll
-        for (int k = 0; k < DK; ++k)
-          if (lane + 32 * k < d) o[r][k] = fmaf(pj, vs[j * d + lane + 32 * k], o[r][k]);
-      }
+      for (int k = 0; k < DK; ++k) v[k] = lane + 32 * k < dp ? vs[j * ld + lane + 32 * k] : 0.f;
+#pragma unroll
+      for (int r = 0; r < kRowsWarp; ++r)
+        if ((see[r] >> j) & 1u)
+#pragma unroll
+          for (int k = 0; k < DK; ++k) o[r][k] = fmaf(r == 0 ? w.x : r == 1 ? w.y : r == 2 ? w.z : w.w, v[k], o[r][k]);
     }
   }
   const bool bad = __syncthreads_or(bad_page);
   if (bad && threadIdx.x == 0) gqa_error(a, KDTV_ERR_BAD_PAGE);
 #pragma unroll
   for (int r = 0; r < kRowsWarp; ++r) {
+#pragma unroll
+    for (int w = 16; w; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
     const int rr = r0 + warp * kRowsWarp + r;
     const int dead = s_dead[warp * kRowsWarp + r];
     if (dead == 1) continue;
@@ -161,7 +203,8 @@ __global__ void __launch_bounds__(kSimtThreads) gqa_simt_kernel(const __grid_con
   }
 }
 
-// Merges the splits of an output row; a warp per row.
+// Merges the splits of an output row; a warp per row, lane k the {max, sum} of
+// splits k and k + 32, four splits' elements under way together.
 template <typename T>
 __global__ void __launch_bounds__(256) gqa_simt_combine_kernel(const __grid_constant__ GqaArgs a) {
   const int lane = threadIdx.x & 31;
@@ -172,32 +215,40 @@ __global__ void __launch_bounds__(256) gqa_simt_combine_kernel(const __grid_cons
   int L, n;
   gqa_request(a, b, &L, &n);
   if (i >= n) return;
-  const int pieces = (L + n + a.chunk - 1) / a.chunk;
-  float m = -INFINITY;
-  for (int p = 0; p < pieces; ++p) {
-    const float2 ml = a.part_ml[p * all + row];
-    if (ml.y < 0.f) return;
-    m = fmaxf(m, ml.x);
-  }
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  for (int p = 0; p < pieces; ++p) {
-    const float2 ml = a.part_ml[p * all + row];
-    l += ml.y * gqa_ex2(ml.x - ref);
-  }
-  for (int e = lane; e < a.d; e += 32) {
+  const int pieces = (L + n + a.chunk - 1) / a.chunk;       // <= 64
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 x0 = lane < pieces ? a.part_ml[lane * all + row] : none;
+  const float2 x1 = lane + 32 < pieces ? a.part_ml[(lane + 32) * all + row] : none;
+  if (__any_sync(0xffffffffu, x0.y < 0.f || x1.y < 0.f)) return;
+  float m = fmaxf(x0.x, x1.x);
+#pragma unroll
+  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  const float ref = m == -INFINITY ? 0.f : m, w0 = gqa_ex2(x0.x - ref), w1 = gqa_ex2(x1.x - ref);
+  float l = x0.y * w0 + x1.y * w1;
+#pragma unroll
+  for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  for (int e0 = 0; e0 < a.d; e0 += 32) {
+    const int e = e0 + lane;
     float o = 0.f;
-    for (int p = 0; p < pieces; ++p)
-      o = fmaf(a.part_o[(p * all + row) * a.d + e], gqa_ex2(a.part_ml[p * all + row].x - ref), o);
-    const float x[1] = {o / l};
-    store_v<1>(static_cast<T*>(a.out) + row * a.d + e, x);
+    for (int p = 0; p < pieces; p += 4) {
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = p + k < pieces && e < a.d ? a.part_o[((p + k) * all + row) * a.d + e] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float w = __shfl_sync(0xffffffffu, p + k < 32 ? w0 : w1, (p + k) & 31);
+        if (p + k < pieces) o = fmaf(x[k], w, o);
+      }
+    }
+    const float y[1] = {o / l};
+    if (e < a.d) store_v<1>(static_cast<T*>(a.out) + row * a.d + e, y);
   }
 }
 
 template <typename T, typename C>
 int launch_simt_t(const GqaArgs& a, cudaStream_t st) {
   const int dk = (a.d + 31) / 32;
-  const size_t smem = sizeof(float) * (kKeys * (a.d + 1) + kKeys * a.d + kRowsCta * a.d);
+  const size_t smem = sizeof(float) * simt_words(a.d);
   auto kern = dk <= 2 ? gqa_simt_kernel<T, C, 2> : dk <= 4 ? gqa_simt_kernel<T, C, 4> : gqa_simt_kernel<T, C, 8>;
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
