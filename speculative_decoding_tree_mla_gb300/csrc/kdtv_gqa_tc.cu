@@ -63,7 +63,7 @@ enum {
   B_K_EMPTY = B_K_FULL + kRing, B_Q_FULL = B_K_EMPTY + kRing,
   B_Q_READY, B_Q_EMPTY, B_S_FULL, B_P_HALF = B_S_FULL + 2, B_P_READY = B_P_HALF + 2,
   B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2, B_O1_FREE, B_MMA_DONE, B_STALL, B_TURN,
-  B_SCALE_FREE = B_TURN + 2, B_PIECE = B_SCALE_FREE + 2, B_PIECE_READ = B_PIECE + kPieces,
+  B_SCALE_FREE = B_TURN + 2, B_AUX = B_SCALE_FREE + 2, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
   B_COUNT = B_PIECE_READ + kPieces
 };
 
@@ -368,6 +368,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     mbar_init(BAR(B_Q_READY), 4);
     for (int i = 0; i < 2; ++i) mbar_init(BAR(B_SCALE_FREE + i), 8);
     mbar_init(BAR(B_Q_FULL), 1);
+    mbar_init(BAR(B_AUX), 4);
     mbar_init(BAR(B_Q_EMPTY), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(B_S_FULL + i), 1);
@@ -743,7 +744,16 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     Piece p;
     bool alive = true;
     int g = 0;
-    uint32_t tail_phase = 0u;
+    uint32_t tail_phase = 0u, aux_phase = 0u;
+    // The four warps meet (with a time limit, which a named barrier does not have: a warp may have
+    // given up).
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_AUX));
+      const bool ok = wait_warp(guard, BAR(B_AUX), aux_phase);
+      aux_phase ^= 1u;
+      return ok;
+    };
     Ring<kFp8 ? C::kRaw : 1> kring, vring;
     Ring<C::kSlots> ring;
     Ring<2> sring;                                // of key scales
@@ -753,7 +763,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const int lag = p.two() ? 1 : 2;
       uint32_t* nf = reinterpret_cast<uint32_t*>(nonfinite + index % kPieces);
       if (row < 4) nf[row] = 0u;
-      asm volatile("bar.sync 2, 128;" ::: "memory");
+      alive = meet();
+      if (!alive) break;
       if constexpr (kFp8) {
         // The scale bytes of tile i + 2 are loaded at the end of step i, with a page id loaded a step
         // before: behind the step's proxy fence, which waits for every load that is under way.
@@ -802,7 +813,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (D == 128 && (u & 1) && u < 8)       // 16 bytes of the high part, where both were read
               sts128(qr + (((u >> 1) ^ swz) << 4), hi[2 * u - 2], hi[2 * u - 1], hi[2 * u], hi[2 * u + 1]);
           }
-          if (D == 64) asm volatile("bar.sync 2, 128;" ::: "memory");   // rows of the parts overlap others' rows
+          if (D == 64) {                            // rows of the parts overlap others' rows
+            alive = meet();
+            if (!alive) break;
+          }
 #pragma unroll
           for (int u = 0; u < D / 16; ++u) {
             if (D == 128) {
@@ -815,6 +829,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
           }
         }
+        if (!alive) break;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_Q_READY));
@@ -922,7 +937,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (found) atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
           }
           fence_async_smem();
-          asm volatile("bar.sync 1, 128;" ::: "memory");
+          alive = meet();
+          if (!alive) break;
           if (row == 0) mbar_arrive(BAR(B_KV_FULL + slot));
         }
         g += 2 * n;
@@ -1250,8 +1266,10 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant_
   int L, n;
   gqa_request(a, b, &L, &n);
   const int rows = min(a.npt, n - tile * a.npt) * a.G;           // of the tile
+  // The partials and the plan are written.  (Blocks without rows wait as well: what comes next in
+  // the stream may start when this grid has ended.)
+  grid_dep_wait();
   if (r0 >= rows) return;
-  grid_dep_wait();                                 // the partials and the plan are written
   if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
   const int W = a.plan[0], nt = key_tiles(L, n);
   const int start = a.plan[1 + b] + (kvh / a.hg * row_pairs(a, n) + tile / 2) * nt;
