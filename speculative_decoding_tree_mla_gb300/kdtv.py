@@ -352,17 +352,51 @@ def _index(t, shape, device, name):
     return t
 
 
+def _strides(t):
+    """Strides of [B, N, H, ..] for the library, where all zero means contiguous."""
+    s = t.stride()[:3]
+    _need(any(s) or t.shape[:3].numel() == 1, "a tensor that repeats one row: make it contiguous")
+    return (ctypes.c_int64 * 3)(*s)
+
+
+def _apart(t):
+    """Whether no two elements of a result share memory."""
+    reach = 0
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+        if stride <= reach:
+            return False
+        reach += stride * (size - 1)
+    return True
+
+
 class _Bound:
     """A library call over bound tensors, launched on their device."""
 
-    def _bind(self, name, device, args, keep):
+    def _bind(self, name, device, args, keep, own=()):
         import torch
         self.torch, self._name, self.device = torch, name, device
         self._fn, self._args, self._keep = getattr(lib(), name), tuple(args), keep
+        # what was allocated here belongs to the stream that is current now
+        self._own, self._home = own, torch.cuda.current_stream(device)
+        self._streams = {self._home.cuda_stream}
+
+    def _join(self, s):
+        """First launch on another stream than the one that was current at binding: behind what
+        that one has under way (a word being cleared, the memory's last user), and what was
+        allocated here stays until this stream is done with it."""
+        torch = self.torch
+        with torch.cuda.stream(s):
+            if not torch.cuda.is_current_stream_capturing():
+                s.wait_stream(self._home)
+        for t in self._own:
+            t.record_stream(s)
+        self._streams.add(s.cuda_stream)
 
     def _launch(self, stream):
         torch = self.torch
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if s.cuda_stream not in self._streams:
+            self._join(s)
         if torch.cuda.current_device() == self.device.index:
             code = self._fn(*self._args, s.cuda_stream)
         else:
@@ -419,7 +453,8 @@ class Rope(_Bound):
             if t is None:
                 return torch.empty((B, N, H, d), dtype=x.dtype, device=x.device)
             _need(tuple(t.shape) == (B, N, H, d) and t.dtype == x.dtype and t.device == x.device
-                  and (d == 0 or t.stride(3) == 1), f"{name}: {[B, N, H, d]} like x")
+                  and (d == 0 or t.stride(3) == 1 and _apart(t)),
+                  f"{name}: {[B, N, H, d]} like x, no two elements in one place")
             return t
 
         self.out = result(out, table.rot_dim if split else dim, "out")
@@ -429,13 +464,14 @@ class Rope(_Bound):
         a = KdtvRopeArgs(B, N, H, dim, rot_off, KDTV_F32 if x.dtype == torch.float32 else KDTV_BF16)
         for name, t in (("x_stride", x), ("y_stride", self.out), ("rest_stride", copied)):
             if t is not None:
-                setattr(a, name, (ctypes.c_int64 * 3)(*t.stride()[:3]))
+                setattr(a, name, _strides(t))
         pl = _index(prefix_len, (B,), x.device, "prefix_len")
         dp = _index(depth, (B, N), x.device, "depth")
         nl = _index(n_live, (B,), x.device, "n_live")
         self._bind("kdtv_rope", x.device,
                    (ctypes.byref(table.c), ctypes.byref(a), _p(x), _p(self.out), _p(copied), _p(pl),
-                    _p(dp), _p(nl)), (table, a, x, self.out, self.rest, pl, dp, nl))
+                    _p(dp), _p(nl)), (table, a, x, self.out, self.rest, pl, dp, nl),
+                   [t for t in (self.out, self.rest) if t is not None])
 
     def __call__(self, stream=None):
         self._launch(stream)
@@ -495,7 +531,7 @@ def _kv_setup(parts, which, page_table, kv_scale):
         cp[k].cache, cp[k].scale = _p(cache), _p(scale)
         setattr(cp[k], which, _p(x))
         if which == "src":
-            cp[k].src_stride = (ctypes.c_int64 * 3)(*x.stride()[:3])
+            cp[k].src_stride = _strides(x)
             cp[k].rotate, cp[k].rot_off = part.rot_off is not None, part.rot_off or 0
         cp[k].heads, cp[k].dim = x.shape[2], x.shape[3]
         keep += [x, cache, scale]
@@ -535,7 +571,7 @@ class KvAppend(_Bound):
         self.status = _status_word(status, device)
         self._bind("kdtv_kv_append", device,
                    (ctypes.byref(d), cp, ctypes.byref(rope.c) if rope is not None else None, _p(pl), _p(dp),
-                    _p(nl), _p(page_table), _p(self.status)), (d, cp, rope, pl, dp, nl, keep))
+                    _p(nl), _p(page_table), _p(self.status)), (d, cp, rope, pl, dp, nl, keep), [self.status])
 
     def __call__(self, stream=None):
         self._launch(stream)
@@ -552,7 +588,7 @@ class KvRead(_Bound):
         nl = _index(n_live, (B,), device, "n_live")
         self.status = _status_word(status, device)
         self._bind("kdtv_kv_read", device, (ctypes.byref(d), cp, _p(st), _p(nl), _p(page_table),
-                                            _p(self.status)), (d, cp, st, nl, keep))
+                                            _p(self.status)), (d, cp, st, nl, keep), [self.status])
 
     def __call__(self, stream=None):
         self._launch(stream)
@@ -626,7 +662,7 @@ class GqaVerifyAttn(_Bound):
         self._bind("kdtv_gqa_verify_attn", q.device,
                    (ctypes.byref(D), _p(q), _p(k), _p(v), _p(k_scale), _p(v_scale), _p(pa), _p(pl), _p(nn),
                     _p(page_table), _p(self.out), _p(self._status)),
-                   (q, k, v, k_scale, v_scale, pa, pl, nn, page_table))
+                   (q, k, v, k_scale, v_scale, pa, pl, nn, page_table), [self.out, self.workspace, self._status])
 
     def __call__(self, stream=None):
         self._launch(stream)

@@ -395,10 +395,11 @@ def test_python_checks():
     i = torch.zeros(2, dtype=torch.int32, device="cuda")
     for bad in (dict(prefix_len=i.long()), dict(prefix_len=i.cpu()), dict(prefix_len=i[:1]),
                 dict(depth=i), dict(rot_off=1), dict(out=x.bfloat16()), dict(out=x[:1]),
-                dict(rest=x)):
+                dict(rest=x), dict(out=x[:, :, :1].expand(2, 3, 4, 64)),
+                dict(out=x.as_strided((2, 3, 4, 64), (768, 256, 32, 1)))):
         with pytest.raises(ValueError):
             kdtv.rope(t, x, **bad)
-    for bad in (x.half(), x.cpu(), x.transpose(2, 3), x[:0], x[0]):
+    for bad in (x.half(), x.cpu(), x.transpose(2, 3), x[:0], x[0], x[0, 0, 0].expand(2, 3, 4, 64)):
         with pytest.raises(ValueError):
             kdtv.rope(t, bad)
     cache = torch.zeros((2, 8, 4, 64), dtype=torch.uint8, device="cuda")
@@ -407,6 +408,23 @@ def test_python_checks():
                      (kdtv.KvPart(cache, src=x, scale=s[:, :4]), {}), (kdtv.KvPart(cache, src=x, rot_off=0), {}),
                      (kdtv.KvPart(cache.float(), src=x, scale=s), {}), (kdtv.KvPart(cache.int(), src=x), {}),
                      (kdtv.KvPart(cache[..., :32].contiguous(), src=x), {}), (kdtv.KvPart(cache, src=None), {}),
-                     (kdtv.KvPart(cache, src=x), dict(page_table=i))):
+                     (kdtv.KvPart(cache, src=x), dict(page_table=i)),
+                     (kdtv.KvPart(cache, src=x[0, 0, 0].expand(2, 3, 4, 64)), {})):
         with pytest.raises(ValueError):
             kdtv.kv_append([part], i, **kw)
+
+
+def test_broadcast_rows():
+    """One row for all heads, or all requests: strides of 0 beside others."""
+    rng = np.random.default_rng(7)
+    t = kdtv.RopeTable(64)
+    base = dev(rng.standard_normal((1, 3, 1, 64), dtype=np.float32))
+    x = base.expand(2, 3, 4, 64)
+    assert torch.equal(kdtv.rope(t, x), kdtv.rope(t, x.contiguous()))
+    a, b = (torch.zeros((2, 8, 4, 64), device="cuda") for _ in range(2))
+    at = dev(np.array([1, 5], np.int32))
+    for cache, src in ((a, x), (b, x.contiguous())):
+        assert int(kdtv.kv_append([kdtv.KvPart(cache, src=src, rot_off=0)], at, rope=t).item()) == 0
+    assert torch.equal(a, b) and not torch.equal(a, torch.zeros_like(a))
+    one = base[:, :1]                                  # one row: any strides
+    assert torch.equal(kdtv.rope(t, one), kdtv.rope(t, one.clone()))
