@@ -205,6 +205,10 @@ int kdtv_tree_accept(int B, int N, const int32_t* parent, const int32_t* draft_t
  * path, prefix overflow, bad page id) leave that request untouched and set
  * *status (device word, first error wins) to KDTV_ERR_BAD_TREE /
  * KDTV_ERR_BAD_PREFIX / KDTV_ERR_BAD_PAGE.  Requests must not share pages.
+ * A cache of keys and values per head: K and V as the two tensors, d_c =
+ * d_rope = H_kv * d; its scale bytes in a second call, dtype KDTV_BF16_FP8KV,
+ * d_c = d_rope = H_kv.  KDTV_ERR_UNSUPPORTED: 16 rows of d_c + d_rope elements
+ * exceed a CTA's shared memory (226 KiB).
  */
 int kdtv_compact_kv(const kdtv_dims* dims, void* c_kv, void* k_rope,
                     const int32_t* prefix_len, const int32_t* path, const int32_t* path_len,
@@ -443,6 +447,11 @@ int kdtv_gqa_launches_per_call(const kdtv_gqa_dims* dims);
  *              kdtv_kv_append writes them; else NULL
  *   parent     [B, N] int32, as in kdtv_verify_attn, of the live nodes
  *   prefix_len [B], n_nodes [B] int32 (n_nodes may be NULL: N)
+ * Scale bytes 1 .. 254 stand for 2^-126 .. 2^127.  On tensor cores a one-byte
+ * key's product with a query row scaled to 2^8 is formed before both scales are
+ * taken back, so key bytes above 227 (2^100) may overflow a score.
+ * While *status holds KDTV_ERR_DEVICE_TIMEOUT (a wait that ran out), rows whose
+ * keys are spread over several CTAs are not written: clear it first.
  * Rows of out behind n_nodes[b] are left as they were, and so are rows whose
  * root path is malformed (KDTV_ERR_BAD_TREE) and requests with a bad prefix or
  * page.  Cache rows at and behind prefix_len[b] + n_nodes[b] may hold

@@ -289,6 +289,9 @@ int check(const kdtv_gqa_dims* d) {
   if (d->N > kMaxNodes || d->d > 256) return KDTV_ERR_UNSUPPORTED;
   if ((long long)d->B * d->H_kv > 65535) return KDTV_ERR_UNSUPPORTED;
   if ((long long)d->B * d->N * d->H > (1ll << 28)) return KDTV_ERR_UNSUPPORTED;
+  // 32-bit positions; a grid row per 16 query rows of a key/value head
+  if (d->t_stride > (1 << 30) && d->page_size == 0) return KDTV_ERR_UNSUPPORTED;
+  if ((long long)d->N * (d->H / d->H_kv) > 65535ll * kRowsCta) return KDTV_ERR_UNSUPPORTED;
   return KDTV_OK;
 }
 

@@ -62,3 +62,19 @@ def test_workspace(L):
     for ws, size in ((None, 1 << 40), (4096 + 16, 1 << 40), (4096, n - 1)):
         assert call(L, dims(workspace=ws, workspace_bytes=size)) == "KDTV_ERR_INVALID_ARG"
     assert L.kdtv_gqa_workspace_size(None) == 0 and L.kdtv_gqa_launches_per_call(None) == -1
+
+
+@pytest.mark.parametrize("flags", [0, kdtv.KDTV_FLAG_SIMT])
+@pytest.mark.parametrize("fields", [dict(B=1, t_stride=(1 << 30) + 1), dict(B=1, N=128, H=1 << 15, H_kv=1, d=64)])
+def test_sizes_beyond_the_grid(L, fields, flags):
+    """Positions beyond 2^30, query rows of a head beyond 16 * 65535."""
+    d = dims(flags=flags, **fields)
+    assert L.kdtv_gqa_workspace_size(ctypes.byref(d)) == 0
+    assert call(L, d) == "KDTV_ERR_UNSUPPORTED"
+
+
+def test_compaction_of_rows_too_wide(L):
+    """Rows whose accepted chunk does not fit a CTA's shared memory are refused before any launch."""
+    d = kdtv.KdtvDims(2, 8, 8, 128, 64, 128, 1 << 17, kdtv.KDTV_BF16, 0, 512)
+    assert kdtv.STATUS[L.kdtv_compact_kv(ctypes.byref(d), 256, 256, 256, 256, 256, None, 256, None)] == \
+        "KDTV_ERR_UNSUPPORTED"

@@ -13,7 +13,6 @@ max_t sum_e |k_te|.  Against the oracle's A = sum_t p_t |v_t| this gives (2 delt
 (bf16) or 2^-24 |o|.
 """
 
-import ctypes
 
 import numpy as np
 import pytest
@@ -379,3 +378,46 @@ def test_function_form_and_checks():
     with pytest.raises(kdtv.KdtvError):
         kdtv.gqa_verify_attn(torch.zeros((1, 129, 8, 64), dtype=torch.bfloat16, device="cuda"), k, v,
                              torch.zeros((1, 129), dtype=torch.int32, device="cuda"), pl)
+
+
+@pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64)])
+def test_a_wait_that_runs_out(cache, d):
+    """The loads never start (a test flag; every wait has a limit): the status says so, and the next
+    call is as if nothing had been."""
+    x = Case(2, 9, 8, 2, d, cache, 16, [300, 20], seed=4)
+    stalled, op = x.op(kdtv.KDTV_FLAG_TEST_STALL), x.op()
+    stalled()
+    assert kdtv.STATUS[stalled.status()] == "KDTV_ERR_DEVICE_TIMEOUT"
+    assert stalled.status() == 0
+    x.check(op(), True)
+    assert op.status() == 0
+
+
+def test_bound_on_one_stream_called_on_another():
+    """The words and results that a caller allocates are cleared on the stream it was bound on; its
+    first call elsewhere waits for that."""
+    x = Case(2, 4, 8, 2, 64, "bf16", 0, [40, 7], seed=5)
+    x.prefix[1] = -3                       # an error to be kept
+    big = torch.empty(1 << 28, device="cuda")
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for _ in range(8):
+            big.zero_()                    # the clearing of the status word lies behind these
+        op = x.op()
+        op(side)
+        assert kdtv.STATUS[op.status()] == "KDTV_ERR_BAD_PREFIX"
+
+
+def test_extreme_exponents():
+    """Key and value scales from the smallest to 2^90, queries tiny and huge beside them: fp32
+    attention and tensor cores agree with the oracle."""
+    x = Case(1, 3, 4, 2, 64, "fp8", 0, [150], seed=6)
+    for byte, q_scale in ((1, 2.0 ** 100), (40, 2.0 ** 60), (217, 2.0 ** -100)):
+        x.scales[0].fill_(byte)
+        x.scales[1].fill_(240 - byte)
+        x.q.copy_((torch.randn(x.q.shape, device="cuda") * q_scale).to(x.q.dtype))
+        for flags in (0, SIMT):
+            op = x.op(flags)
+            x.check(op(), flags == 0)
+            assert op.status() == 0
