@@ -7,6 +7,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 namespace kdtv {
 namespace {
 
@@ -132,6 +134,20 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
 }
 
 // ---- cache rows -------------------------------------------------------------------------
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
+// m = floor(2^32 (2^s - d) / d) + 1 the quotient is (n + floor(m n / 2^32)) >> s
+// (Granlund and Montgomery, 1994).
+struct Divisor {
+  uint32_t m, s;
+};
+Divisor divisor(uint32_t d) {
+  Divisor r{0u, 0u};
+  while ((1ull << r.s) < d) ++r.s;
+  r.m = (uint32_t)((((1ull << r.s) - d) << 32) / d + 1);
+  return r;
+}
+__device__ __forceinline__ unsigned divide(unsigned n, Divisor d) { return (n + __umulhi(n, d.m)) >> d.s; }
+
 struct KvPart {
   void* cache;
   uint8_t* scale;
@@ -140,10 +156,12 @@ struct KvPart {
   long long ss[3];
   int heads, dim, rotate, rot_off;
   int group;                   // append: lanes of one head's row (a power of two)
+  Divisor by_vecs, by_dim;     // read: vectors of a row, elements of a head
 };
 struct KvArgs {
   int B, N, page_size, t_stride, max_pages, num_pages, parts, hgroups;
-  float kv_scale;
+  float kv_scale, kv_inv;      // kv_inv: 1 / kv_scale if that is exact (a power of two), else 0
+  Divisor by_page;
   const int32_t *prefix_len, *depth, *n_live, *page_table;
   unsigned int* status;
   KvPart part[2];
@@ -171,187 +189,297 @@ __device__ __forceinline__ bool rows_ok(const KvArgs& a, int b, int L, int n) {
 }
 __device__ __forceinline__ long long row_of(const KvArgs& a, int b, int t) {
   if (!a.page_size) return (long long)b * a.t_stride + t;
-  return (long long)a.page_table[(long long)b * a.max_pages + t / a.page_size] * a.page_size +
-         t % a.page_size;
+  const int p = (int)divide((unsigned)t, a.by_page);
+  return (long long)a.page_table[(long long)b * a.max_pages + p] * a.page_size + (t - p * a.page_size);
 }
 
-// Converts a lane's elements of one head's row and stores them.  All lanes of
-// the group come along (shuffles); `on` lanes store.
-template <typename D, int V, int P>
-__device__ __forceinline__ void put_head(const KvPart& part, float kv_scale, int group, int lane, bool on,
-                                         float (&y)[P][V], D* dst, uint8_t* scale) {
+// Largest magnitude of a lane's elements (fmaxf passes NaN by), and the largest finite one.
+template <int V, int P>
+__device__ __forceinline__ float max_magnitude(const float (&y)[P][V]) {
+  float mx = 0.f;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int k = 0; k < V; ++k) mx = fmaxf(mx, fabsf(y[p][k]));
+  return mx;
+}
+template <int V, int P>
+__device__ __forceinline__ float max_finite(const float (&y)[P][V]) {
+  float mx = 0.f;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int k = 0; k < V; ++k) mx = fabsf(y[p][k]) < INFINITY ? fmaxf(mx, fabsf(y[p][k])) : mx;
+  return mx;
+}
+// The maxima of J heads over the lanes of a group (all lanes of the warp come along).
+template <int J>
+__device__ __forceinline__ void reduce_group(float (&mx)[J], int group) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < group)
+#pragma unroll
+      for (int j = 0; j < J; ++j) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
+}
+// The smallest e with mx <= 448 * 2^e = 1.75 * 2^(e + 8), from mx's bits.
+__device__ __forceinline__ int exponent_of(float mx) {
+  const uint32_t bits = __float_as_uint(mx);
+  const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+  return max(-117, min(119, e));
+}
+
+// A lane's elements of one head's row as they are to be rounded; mx: the row's largest finite
+// magnitude.  2^-e is a power of two, so x * 2^-e loses nothing; a power also makes a code's value
+// exact in bf16.
+template <typename D, bool kScaled, int V, int P>
+__device__ __forceinline__ void convert(const KvArgs& a, float (&y)[P][V], float mx, bool put_scale, uint8_t* scale) {
   if constexpr (sizeof(D) == 1) {
-    if (part.scale) {
-      // The smallest e with max <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of
-      // the largest finite magnitude.  2^-e is a power of two, so x * 2^-e loses
-      // nothing; a power also makes a code's value exact in bf16.
-      float mx = 0.f;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int k = 0; k < V; ++k) mx = fmaxf(mx, fabsf(y[p][k]));   // (passes NaN by)
-      if (!(mx < INFINITY)) {
-        mx = 0.f;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int k = 0; k < V; ++k) mx = fabsf(y[p][k]) < INFINITY ? fmaxf(mx, fabsf(y[p][k])) : mx;
-      }
-      for (int o = group / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const uint32_t bits = __float_as_uint(mx);
-      int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-      e = max(-117, min(119, e));
-      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+    float f = a.kv_inv;
+    if constexpr (kScaled) {
+      const int e = exponent_of(mx);
+      f = __uint_as_float((uint32_t)(127 - e) << 23);
+      if (put_scale) *scale = (uint8_t)(e + 127);
+    }
+    if (kScaled || f != 0.f) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int k = 0; k < V; ++k) y[p][k] *= f;
-      if (on && lane == 0) *scale = (uint8_t)(e + 127);
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int k = 0; k < V; ++k) y[p][k] = __fdiv_rn(y[p][k], kv_scale);
+        for (int k = 0; k < V; ++k) y[p][k] = __fdiv_rn(y[p][k], a.kv_scale);
     }
   }
-  if (on)
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-      if ((p * group + lane) * V < part.dim) store_v<V>(dst + p * group * V, y[p]);
 }
 
-// A group of `group` lanes takes rows of one part, one head after the other;
-// lane l holds elements (p * group + l) * V + k, p < P, k < V, of the head.
-// The angles are computed once per row and serve its heads.  A block takes a
-// span of rows, so that looking its request's pages up does not count.
-//   V = 8, P = 1 (heads of up to 256, 16-byte accesses): the 16-byte vectors of
-// kBatch heads are loaded together and unpacked one by one, and the half
-// layout's rotation partners come from the lane that holds them.  DRAM bound
-// at prompt sizes, by way of the loads in flight: one head at a time, with the
-// partners read again, took 42 us for 13000 rows of 8 + 8 heads of 128.
-//   Otherwise one head at a time, partners read again.
+// Rows of a part are taken by groups of `group` lanes, a row at a time, heads
+// h0 .. h1 one after the other; a block has a span of rows, so that looking its
+// request up does not count.  Every lane of a warp goes through the same turns
+// (shuffles).
+struct Rows {
+  int b, L, i0, i1, h0, h1, group;
+};
+template <int V>
+__device__ __forceinline__ int partner(const KvPart& part, int rot_dim, bool half, int e) {
+  // distance from element e to its rotation partner (0: not rotated)
+  const int r0 = e - part.rot_off;
+  if (!part.rotate || r0 < 0 || r0 >= rot_dim) return 0;
+  return half ? (r0 < rot_dim / 2 ? rot_dim / 2 : -(rot_dim / 2)) : ((r0 & 1) ? -1 : 1);
+}
+__device__ __forceinline__ long long position(const KvArgs& a, const Rows& r, int i) {
+  return (long long)r.L + (a.depth ? a.depth[(long long)r.b * a.N + i] : i);
+}
+
+enum { kPlain = 0, kHalves = 1, kPairs = 2 };          // a part's rotation
+
+// Heads of up to 256 elements, 16-byte accesses: a lane has eight elements of a
+// head.  The vectors of kBatch heads are loaded together, the next ones while
+// the last are converted, and the first before the request is looked up; the
+// half layout's rotation partners come from the lane that holds them; the angles
+// are computed once per row.  Bound by instructions more than by DRAM at prompt
+// sizes (the rotation, the search for the largest magnitude), so what a part needs
+// is known at compile time: 13000 rows of 8 + 8 heads of 128 from bf16 into a
+// one-byte cache take 21 us, 30 with one code for all parts; DRAM alone would
+// need 12.  Three blocks an SM (two: 3 us more).
+template <typename S, typename D, int kRot, bool kScaled>
+__device__ __forceinline__ void append_rows(const KvArgs& a, const KvPart& part, const Rows& r, int n, int rot_dim,
+                                            float amp, const uint64_t* turn_of) {
+  constexpr int kWords = 8 * sizeof(S) / 16, kBatch = 4 / kWords;
+  const int lane = threadIdx.x % r.group, groups = kThreads / r.group;
+  const bool in_dim = lane * 8 < part.dim;
+  uint4 raw[kBatch][kWords];
+  auto load_heads = [&](int i, int hh) {
+    const S* src = static_cast<const S*>(part.src) + r.b * part.ss[0] + i * part.ss[1] + hh * part.ss[2] + lane * 8;
+    const bool row = i < r.i1 && in_dim;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+        raw[j][w] = row && hh + j < r.h1 ? reinterpret_cast<const uint4*>(src + j * part.ss[2])[w]
+                                         : make_uint4(0u, 0u, 0u, 0u);
+  };
+  int i = r.i0 + threadIdx.x / r.group;
+  load_heads(i, r.h0);
+  // (every block looks the whole request up: it is written as a whole or not at all)
+  if (!rows_ok(a, r.b, r.L, n)) return;
+  if constexpr (kRot != kPlain) __syncthreads();      // the table
+  const int mate = kRot == kPlain ? 0 : partner<8>(part, rot_dim, kRot == kHalves, lane * 8);
+  const int from = threadIdx.x % 32 + (kRot == kHalves ? mate / 8 : 0);   // lane with the partners
+  long long row = i < r.i1 ? row_of(a, r.b, r.L + i) : 0;
+  for (int i_turn = r.i0; i_turn < r.i1; i_turn += groups, i += groups) {
+    const bool on = i < r.i1;
+    D* dst = static_cast<D*>(part.cache) + row * part.heads * part.dim + lane * 8;
+    uint8_t* scale = kScaled ? part.scale + row * part.heads : nullptr;
+    row = i + groups < r.i1 ? row_of(a, r.b, r.L + i + groups) : 0;    // of the next turn
+    float2 cs[8];                                     // (pairs: four of them)
+    if (kRot != kPlain && mate != 0 && on) {
+      const long long pos = position(a, r, i);
+      const int r0 = lane * 8 - part.rot_off, first = kRot == kPairs ? r0 / 2 : r0 < rot_dim / 2 ? r0 : r0 - rot_dim / 2;
+#pragma unroll
+      for (int k = 0; k < (kRot == kPairs ? 4 : 8); ++k) {
+        cs[k] = rope_cos_sin(turn_of[first + k], pos, amp);
+        if (kRot == kHalves && mate < 0) cs[k].y = -cs[k].y;          // the second of its pair
+      }
+    }
+    for (int hh = r.h0; hh < r.h1; hh += kBatch) {
+      float y[kBatch][1][8], mx[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        unpack8<S>(raw[j], y[j][0]);
+        if constexpr (kRot == kHalves) {
+          uint4 other[kWords];
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            other[w].x = __shfl_sync(0xffffffffu, raw[j][w].x, from);
+            other[w].y = __shfl_sync(0xffffffffu, raw[j][w].y, from);
+            other[w].z = __shfl_sync(0xffffffffu, raw[j][w].z, from);
+            other[w].w = __shfl_sync(0xffffffffu, raw[j][w].w, from);
+          }
+          float m[8];
+          unpack8<S>(other, m);
+          if (mate != 0)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[j][0][k] = y[j][0][k] * cs[k].x - m[k] * cs[k].y;
+        } else if (kRot == kPairs && mate != 0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float u = y[j][0][2 * k], v = y[j][0][2 * k + 1];
+            y[j][0][2 * k] = u * cs[k].x - v * cs[k].y;
+            y[j][0][2 * k + 1] = v * cs[k].x + u * cs[k].y;
+          }
+        }
+      }
+      if (hh + kBatch < r.h1) load_heads(i, hh + kBatch);
+      else load_heads(i + groups, r.h0);
+      if constexpr (kScaled) {
+        bool inf = false;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) mx[j] = max_magnitude(y[j]);
+        reduce_group(mx, r.group);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) inf |= !(mx[j] < INFINITY);
+        if (__any_sync(0xffffffffu, inf)) {           // rare: over the finite elements
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) mx[j] = max_finite(y[j]);
+          reduce_group(mx, r.group);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (hh + j < r.h1) {
+          convert<D, kScaled>(a, y[j], kScaled ? mx[j] : 0.f, on && lane == 0, scale + (hh + j));
+          if (on && in_dim) store_v<8>(dst + (hh + j) * part.dim, y[j][0]);
+        }
+    }
+  }
+}
+
+// Otherwise (longer heads, P > 1; odd sizes or addresses, V = 1) one head at a
+// time, the partners read again.  Lane l holds elements (p * group + l) * V + k,
+// p < P, k < V, of the head.
 template <typename S, typename D, int V, int P>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ kdtv_rope_table tab,
-                                                             const __grid_constant__ KvArgs a, int span) {
+__device__ __forceinline__ void append_rows_any(const KvArgs& a, const KvPart& part, const Rows& r, int n, int rot_dim,
+                                                bool half, float amp, const uint64_t* turn_of) {
+  if (!rows_ok(a, r.b, r.L, n)) return;
+  __syncthreads();                                   // the table
+  const int group = r.group, lane = threadIdx.x % group, groups = kThreads / group;
+  int mate[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) mate[p] = partner<V>(part, rot_dim, half, (p * group + lane) * V);
+  int i = r.i0 + threadIdx.x / group;
+  for (int i_turn = r.i0; i_turn < r.i1; i_turn += groups, i += groups) {
+    const bool on = i < r.i1;
+    const long long row = on ? row_of(a, r.b, r.L + i) : 0;
+    const S* src = static_cast<const S*>(part.src) + r.b * part.ss[0] + (on ? i : r.i0) * part.ss[1] + lane * V;
+    D* dst = static_cast<D*>(part.cache) + row * part.heads * part.dim + lane * V;
+    uint8_t* scale = part.scale ? part.scale + row * part.heads : nullptr;
+    float2 cs[P][V];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (mate[p] == 0 || !on) continue;
+      const int r0 = (p * group + lane) * V - part.rot_off, hd = rot_dim / 2;
+      const long long pos = position(a, r, i);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (half) cs[p][k] = rope_cos_sin(turn_of[(r0 < hd ? r0 : r0 - hd) + k], pos, amp);
+        else if (V == 1 || (k & 1) == 0) cs[p][k] = rope_cos_sin(turn_of[(r0 + k) / 2], pos, amp);
+        else cs[p][k] = cs[p][k - 1];
+        if (mate[p] < 0 && (half || V == 1)) cs[p][k].y = -cs[p][k].y;   // the second of its pair
+      }
+    }
+    for (int h = r.h0; h < r.h1; ++h) {
+      float y[P][V];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[p][k] = 0.f;
+        const int e = p * group * V;
+        if (!on || e + lane * V >= part.dim) continue;
+        const S* s = src + h * part.ss[2] + e;
+        load_v<V>(s, y[p]);
+        if (mate[p] == 0) continue;
+        if (half || V == 1) {
+          float m[V];
+          load_v<V>(s + mate[p], m);
+#pragma unroll
+          for (int k = 0; k < V; ++k) y[p][k] = y[p][k] * cs[p][k].x - m[k] * cs[p][k].y;
+        } else {
+#pragma unroll
+          for (int k = 0; k + 1 < V; k += 2) {
+            const float u = y[p][k], v = y[p][k + 1];
+            y[p][k] = u * cs[p][k].x - v * cs[p][k].y;
+            y[p][k + 1] = v * cs[p][k].x + u * cs[p][k].y;
+          }
+        }
+      }
+      if (part.scale) {
+        float mx[1] = {max_finite(y)};
+        reduce_group(mx, group);
+        convert<D, true>(a, y, mx[0], on && lane == 0, scale + h);
+      } else {
+        convert<D, false>(a, y, 0.f, false, scale);
+      }
+      if (on)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          if ((p * group + lane) * V < part.dim) store_v<V>(dst + h * part.dim + p * group * V, y[p]);
+    }
+  }
+}
+
+template <typename S, typename D, int V, int P>
+__global__ void __launch_bounds__(kThreads, V == 8 && P == 1 ? 3 : 1)
+kv_append_kernel(const __grid_constant__ kdtv_rope_table tab, const __grid_constant__ KvArgs a, int span) {
+  __shared__ uint64_t turn_of[KDTV_ROPE_MAX_DIM / 2];
   const KvPart& part = a.part[blockIdx.z];
   const int b = blockIdx.y;
   const int n = live_rows(a.n_live, b, a.N);
   const int i0 = (int)(blockIdx.x / a.hgroups) * span, i1 = min(n, i0 + span);
-  const int L = a.prefix_len ? a.prefix_len[b] : 0;
-  // (every block looks the whole request up: it is written as a whole or not at all)
-  if (n == 0 || i0 >= i1 || !rows_ok(a, b, L, n)) return;
-  const int group = part.group, lane = threadIdx.x % group, groups = kThreads / group;
   const int per = (part.heads + a.hgroups - 1) / a.hgroups;
   const int h0 = (int)(blockIdx.x % a.hgroups) * per, h1 = min(h0 + per, part.heads);
-  if (h0 >= h1) return;
+  if (i0 >= i1 || h0 >= h1) return;
+  const Rows r{b, a.prefix_len ? a.prefix_len[b] : 0, i0, i1, h0, h1, part.group};
+  if (part.rotate)                                   // (lanes want different entries)
+    for (int j = threadIdx.x; j < tab.rot_dim / 2; j += kThreads) turn_of[j] = tab.turn[j];
   const bool half = tab.layout == KDTV_ROPE_HALF;
-
-  // distance to this lane's rotation partners (0: not rotated)
-  int mate[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int r0 = (p * group + lane) * V - part.rot_off;     // first element, in the rotated part
-    const bool in = part.rotate && r0 >= 0 && r0 < tab.rot_dim;
-    mate[p] = !in ? 0 : half ? (r0 < tab.rot_dim / 2 ? tab.rot_dim / 2 : -(tab.rot_dim / 2)) : ((r0 & 1) ? -1 : 1);
-  }
-  const int turns = (i1 - i0 + groups - 1) / groups;          // of rows: the same for all lanes (shuffles)
-  int i = i0 + threadIdx.x / group;
-  for (int turn = 0; turn < turns; ++turn, i += groups) {
-    const bool on = i < i1;
-    const long long row = on ? row_of(a, b, L + i) : 0;
-    const S* src = static_cast<const S*>(part.src) + b * part.ss[0] + (on ? i : i0) * part.ss[1] + lane * V;
-    D* dst = static_cast<D*>(part.cache) + row * part.heads * part.dim + lane * V;
-    uint8_t* scale = part.scale ? part.scale + row * part.heads : nullptr;
-    auto angles = [&](float2 (&cs)[P][V]) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        if (mate[p] == 0 || !on) continue;
-        const int r0 = (p * group + lane) * V - part.rot_off, hd = tab.rot_dim / 2;
-        const long long pos = (long long)L + (a.depth ? a.depth[(long long)b * a.N + i] : i);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          if (half) cs[p][k] = rope_cos_sin(tab.turn[(r0 < hd ? r0 : r0 - hd) + k], pos, tab.amp);
-          else if (V == 1 || (k & 1) == 0) cs[p][k] = rope_cos_sin(tab.turn[(r0 + k) / 2], pos, tab.amp);
-          else cs[p][k] = cs[p][k - 1];
-          if (mate[p] < 0 && (half || V == 1)) cs[p][k].y = -cs[p][k].y;   // the second of its pair
-        }
-      }
+  if constexpr (V == 8 && P == 1) {
+    auto run = [&](auto scaled) {
+      constexpr bool kScaled = decltype(scaled)::value;
+      if (!part.rotate) append_rows<S, D, kPlain, kScaled>(a, part, r, n, 0, 1.f, turn_of);
+      else if (half) append_rows<S, D, kHalves, kScaled>(a, part, r, n, tab.rot_dim, tab.amp, turn_of);
+      else append_rows<S, D, kPairs, kScaled>(a, part, r, n, tab.rot_dim, tab.amp, turn_of);
     };
-    float2 cs[P][V];
-    if constexpr (V == 8 && P == 1) {
-      constexpr int kWords = 8 * sizeof(S) / 16, kBatch = 8 / kWords;
-      const int from = threadIdx.x % 32 + mate[0] / 8;         // lane with the partners (half layout)
-      for (int hh = h0; hh < h1; hh += kBatch) {
-        uint4 raw[kBatch][kWords];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-          for (int w = 0; w < kWords; ++w)
-            raw[j][w] = on && hh + j < h1 && lane * V < part.dim
-                            ? reinterpret_cast<const uint4*>(src + (hh + j) * part.ss[2])[w] : make_uint4(0u, 0u, 0u, 0u);
-        if (hh == h0) angles(cs);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (hh + j >= h1) break;
-          float y[1][8];
-          unpack8<S>(raw[j], y[0]);
-          if (part.rotate) {
-            if (half) {
-              uint4 other[kWords];
-#pragma unroll
-              for (int w = 0; w < kWords; ++w) {
-                other[w].x = __shfl_sync(0xffffffffu, raw[j][w].x, from);
-                other[w].y = __shfl_sync(0xffffffffu, raw[j][w].y, from);
-                other[w].z = __shfl_sync(0xffffffffu, raw[j][w].z, from);
-                other[w].w = __shfl_sync(0xffffffffu, raw[j][w].w, from);
-              }
-              float m[8];
-              unpack8<S>(other, m);
-              if (mate[0] != 0)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[0][k] = y[0][k] * cs[0][k].x - m[k] * cs[0][k].y;
-            } else if (mate[0] != 0) {
-#pragma unroll
-              for (int k = 0; k < 8; k += 2) {
-                const float u = y[0][k], v = y[0][k + 1];
-                y[0][k] = u * cs[0][k].x - v * cs[0][k].y;
-                y[0][k + 1] = v * cs[0][k].x + u * cs[0][k].y;
-              }
-            }
-          }
-          put_head<D, V, P>(part, a.kv_scale, group, lane, on, y, dst + (hh + j) * part.dim, scale + (hh + j));
-        }
-      }
-    } else {
-      angles(cs);
-      for (int h = h0; h < h1; ++h) {
-        float y[P][V];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) y[p][k] = 0.f;
-          const int e = p * group * V;
-          if (!on || e + lane * V >= part.dim) continue;
-          const S* s = src + h * part.ss[2] + e;
-          load_v<V>(s, y[p]);
-          if (mate[p] == 0) continue;
-          if (half || V == 1) {
-            float m[V];
-            load_v<V>(s + mate[p], m);
-#pragma unroll
-            for (int k = 0; k < V; ++k) y[p][k] = y[p][k] * cs[p][k].x - m[k] * cs[p][k].y;
-          } else {
-#pragma unroll
-            for (int k = 0; k + 1 < V; k += 2) {
-              const float u = y[p][k], v = y[p][k + 1];
-              y[p][k] = u * cs[p][k].x - v * cs[p][k].y;
-              y[p][k + 1] = v * cs[p][k].x + u * cs[p][k].y;
-            }
-          }
-        }
-        put_head<D, V, P>(part, a.kv_scale, group, lane, on, y, dst + h * part.dim, scale + h);
+    if constexpr (sizeof(D) == 1) {
+      if (part.scale) {
+        run(std::true_type{});
+        return;
       }
     }
+    run(std::false_type{});
+  } else {
+    append_rows_any<S, D, V, P>(a, part, r, n, tab.rot_dim, half, tab.amp, turn_of);
   }
 }
 
@@ -380,13 +508,13 @@ __global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const __grid_const
     for (int k = 0; k < kBatch; ++k) {
       const unsigned tk = t + k * kThreads;
       if (tk >= t1) continue;
-      const unsigned i = tk / vecs, c = (tk - i * vecs) * V;
+      const unsigned i = divide(tk, part.by_vecs), c = (tk - i * vecs) * V;
       const long long row = row_of(a, b, L + (int)i);
       if constexpr (V == 16) raw[k] = *reinterpret_cast<const uint4*>(cache + row * width + c);
       else load_v<V>(cache + row * width + c, x[k]);
       s[k] = 1.f;
       if constexpr (sizeof(C) == 1)
-        s[k] = part.scale ? scale_of_byte(part.scale[row * part.heads + c / part.dim]) : a.kv_scale;
+        s[k] = part.scale ? scale_of_byte(part.scale[row * part.heads + divide(c, part.by_dim)]) : a.kv_scale;
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -500,9 +628,16 @@ cudaError_t launch_read(KvArgs& a, cudaStream_t st) {
     const long long w = (long long)p.heads * p.dim;
     width = w > width ? w : width;
   }
-  // Spans of at least one turn of the block's threads, else about eight blocks an SM in all.
+  // Spans of at least one turn of the block's threads, else about 12 blocks an SM in all: one long
+  // prefix wants fewer (65536 rows of 8 + 8 heads of 128, with 8 / 12 / 24 an SM: 71 / 73 / 74 us),
+  // ragged ones more (8 of up to 8192 latent rows: 20.0 / 17.3 / 17.9).
+  for (int k = 0; k < a.parts; ++k) {
+    KvPart& p = a.part[k];
+    p.by_vecs = divisor((unsigned)(p.heads * p.dim / (vec ? kWide : 1)));
+    p.by_dim = divisor((unsigned)p.dim);
+  }
   const long long total = a.N * (width / (vec ? kWide : 1)), turn = 4 * kThreads;
-  long long blocks = 8ll * 152 / ((long long)a.B * a.parts);
+  long long blocks = 12ll * 152 / ((long long)a.B * a.parts);
   blocks = blocks < 1 ? 1 : blocks;
   const long long span = ((total + blocks - 1) / blocks + turn - 1) / turn * turn;
   const dim3 grid((unsigned)((total + span - 1) / span), (unsigned)a.B, (unsigned)a.parts);
@@ -539,6 +674,9 @@ int kv_args(const kdtv_kv_dims* d, const kdtv_kv_part* parts, const int32_t* pag
   a->B = d->B; a->N = d->N; a->page_size = d->page_size; a->t_stride = d->t_stride;
   a->max_pages = d->max_pages; a->num_pages = d->num_pages; a->parts = d->parts;
   a->kv_scale = d->kv_scale > 0.f ? d->kv_scale : 1.f;
+  int k2;
+  a->kv_inv = frexpf(a->kv_scale, &k2) == 0.5f && isnormal(1.f / a->kv_scale) ? 1.f / a->kv_scale : 0.f;
+  if (d->page_size > 0) a->by_page = divisor((unsigned)d->page_size);
   a->page_table = page_table;
   a->status = status;
   return KDTV_OK;
