@@ -178,26 +178,23 @@ __device__ __forceinline__ bool wait_warp(const Guard& g, uint32_t bar, uint32_t
   return __all_sync(0xffffffffu, wait(g, bar, parity));
 }
 
-// Four E4M3 bytes as four bf16, exactly (NaN stays NaN): through f16, which
-// holds every code, and fp32.  The conversions run beside the integer pipe,
-// where moving the bits by masks and permutes took a quarter longer.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
+// Four E4M3 bytes as bf16 pairs of their values times 2^-120: a code's exponent
+// and mantissa bits moved to bf16's places (also of its subnormals, which become
+// bf16's).  A byte and its sign, spread over the next one, are one permute; the
+// conversion instructions, through f16 and fp32, took 1.8 times as long.  NaN is
+// a number here (480): see has_nan_code.
+__device__ __forceinline__ uint2 spread4(uint32_t w) {
   uint32_t a, b;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(a), "=r"(b) : "r"(w));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  return make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(g.x, g.y));
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));   // {b0, its sign, b1, its sign}
+  asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w));
+  return make_uint2((a << 4) & 0x87f087f0u, (b << 4) & 0x87f087f0u);
 }
+// Bit 7 of each byte whose code is NaN (other bits: anything).
+__device__ __forceinline__ uint32_t has_nan_code(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
   uint32_t y;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
   return y;
-}
-// The scale of an exponent byte (2^(byte - 127)), twice.
-__device__ __forceinline__ uint32_t scale_bf16x2(int byte) {
-  return (uint32_t)byte << 7 | (uint32_t)byte << 23;
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -272,19 +269,18 @@ __device__ __noinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int
     store_v<1>(o + k, y);
   }
 }
-// E4M3 NaN codes of a row in shared memory become 0; true if there were any.
-template <int D>
-__device__ __forceinline__ bool drop_nan_codes(uint32_t src) {
-  bool found = false;
+// A row of values in shared memory with NaN codes (src: the codes; dst: bf16, swizzled, 64 columns
+// a chunk): they become NaN, or 0 if `drop`.  Rare: out of line.
+template <int D, int kChunk>
+__device__ __noinline__ void put_nan(uint32_t src, uint32_t dst, int swz, bool drop) {
 #pragma unroll 1
   for (int e = 0; e < D; ++e) {
     uint32_t code;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(src + e) : "memory");
     if ((code & 0x7fu) != 0x7fu) continue;
-    found = true;
-    asm volatile("st.shared.u8 [%0], %1;" :: "r"(src + e), "r"(0u) : "memory");
+    const uint32_t at = dst + (e >> 6) * kChunk + ((((e >> 3) & 7) ^ swz) << 4) + (e & 7) * 2;
+    asm volatile("st.shared.u16 [%0], %1;" :: "r"(at), "h"((unsigned short)(drop ? 0 : 0x7fff)) : "memory");
   }
-  return found;
 }
 // Register split with bf16 caches: the launch has 512 x 128; the softmax warps
 // take most (a row's 128 scores stay in registers).  With one-byte caches the
@@ -843,14 +839,14 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             alive = wait_warp(guard, BAR(B_RAW_FULL + vring.slot), vring.phase) &&
                     wait_warp(guard, BAR(B_KV_EMPTY + ring.slot), ring.phase ^ 1u);
           if (!alive) break;
-          const uint32_t f = scale_bf16x2(lag == 1 ? vm1 : vm2);
+          // the row's scale times 2^120; above 2^127 the rest follows in a second pass (rare)
+          const int byte = lag == 1 ? vm1 : vm2, low = min(byte, 134);
+          const uint32_t f = (uint32_t)(low + 120) * 0x00800080u;
           const uint32_t src = sbase + C::kOffRaw + vring.slot * C::kRawBytes + row * D;
           const uint32_t dst = sbase + C::kOffKV + ring.slot * C::kTileBytes + row * 128;
           const int t = (p.t0 + i - lag) * kTile + row;
-          // values of the tree's own rows: NaN becomes 0, noted for the epilogue
-          if (t >= p.L && t < T && drop_nan_codes<D>(src))
-            atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
           const bool zero = t >= T;                 // values behind the tree: 0
+          uint32_t nan = 0u;
           // 16-byte chunk c of the row at its XOR-permuted turn: no bank conflicts, for the
           // reads (rows D bytes apart) nor for the swizzled writes.  Two chunks are read before
           // the first is widened: one warp a scheduler has to hide its own latencies.
@@ -869,7 +865,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               uint32_t y[8];
 #pragma unroll
               for (int m = 0; m < 4; ++m) {
-                const uint2 z = widen4(u[m]);
+                const uint2 z = spread4(u[m]);
+                nan |= has_nan_code(u[m]);
                 y[2 * m] = mul_bf16x2(z.x, f);
                 y[2 * m + 1] = mul_bf16x2(z.y, f);
               }
@@ -878,6 +875,21 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               sts128(half + ((j ^ swz) << 4), y[0], y[1], y[2], y[3]);
               sts128(half + (((j + 1) ^ swz) << 4), y[4], y[5], y[6], y[7]);
             }
+          }
+          if (byte > low) {
+            const uint32_t f2 = (uint32_t)(byte - low + 127) * 0x00800080u;
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+              const uint32_t addr = dst + (c >> 3) * C::kChunk + (((c & 7) ^ swz) << 4);
+              const uint4 x = lds128(addr);
+              sts128(addr, mul_bf16x2(x.x, f2), mul_bf16x2(x.y, f2), mul_bf16x2(x.z, f2), mul_bf16x2(x.w, f2));
+            }
+          }
+          // NaN in the tree's own rows becomes 0, noted for the epilogue
+          if (nan & 0x80808080u) {
+            const bool drop = t >= p.L;
+            put_nan<D, C::kChunk>(src, dst, swz, drop);
+            if (drop) atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
           }
           fence_async_smem();
           __syncwarp();

@@ -421,3 +421,27 @@ def test_extreme_exponents():
             op = x.op(flags)
             x.check(op(), flags == 0)
             assert op.status() == 0
+
+
+@pytest.mark.parametrize("flags", [0, SIMT], ids=["auto", "simt"])
+@pytest.mark.parametrize("d,page", [(128, 0), (64, 16)])
+def test_every_code_and_scale(d, page, flags):
+    """One node and nothing before it: its output is its own value row, every code at scales from
+    2^-126 to 2^119 (exactly; below 2^-117 a code may not be exact in bf16), NaN included."""
+    bytes_ = [1, 5, 10, 64, 120, 127, 133, 134, 135, 200, 246]
+    Hkv = 256 // d
+    x = Case(len(bytes_), 1, Hkv, Hkv, d, "fp8", page, [0] * len(bytes_), seed=7)
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").view(Hkv, d)
+    for b, byte in enumerate(bytes_):
+        r = x.rows(b, 1).cuda()
+        x.kv[1].view(-1, Hkv, d)[r] = codes
+        x.scales[1].view(-1, Hkv)[r] = byte
+    op = x.op(flags)
+    got = op().float().cpu().double().numpy()
+    assert op.status() == 0
+    value = W.fp8_e4m3_decode(codes.cpu().numpy()).astype(np.float64)
+    for b, byte in enumerate(bytes_):
+        want = value * 2.0 ** (byte - 127)
+        fin = np.isfinite(want)
+        assert (np.isnan(got[b, 0]) == ~fin).all()
+        assert (np.abs(got[b, 0] - want)[fin] <= (2.0 ** -134 if byte < 10 else 0.0)).all()
