@@ -1269,7 +1269,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // range is partial 2 cta, one that starts later 2 cta + 1.  W and the requests'
 // first units were left by the attention kernel.  Latency bound: the first
 // pieces' rows are loaded along with their {max, sum}.
-constexpr int kRowsCombine = 16;         // (32 / 8: 5 and 2 % slower on 16 trees of 17 nodes)
+constexpr int kRowsCombine = 16;         // (32 / 8: 5 and 2 % slower on 8 trees of 32 nodes)
 
 template <int D>
 __global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant__ GqaArgs a, int tiles) {
