@@ -307,6 +307,7 @@ int make_plan(const kdtv_gqa_dims* d, GqaArgs* a, size_t* off_ml, size_t* off_pl
   a->B = d->B; a->N = d->N; a->H = d->H; a->Hkv = d->H_kv; a->G = d->H / d->H_kv; a->d = d->d;
   a->dtype = d->dtype; a->page_size = d->page_size; a->t_stride = d->t_stride;
   a->max_pages = d->max_pages; a->num_pages = d->num_pages;
+  a->cap = d->page_size ? (long long)d->max_pages * d->page_size : d->t_stride;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   size_t rows;                                     // partial rows
   if (on_tensor_cores(d)) {
@@ -314,7 +315,7 @@ int make_plan(const kdtv_gqa_dims* d, GqaArgs* a, size_t* off_ml, size_t* off_pl
     if (!rows) return KDTV_ERR_UNSUPPORTED;
   } else {
     // Splits until the grid holds four CTAs per SM, each of 64 keys or more.
-    const long long cap = d->page_size ? (long long)d->max_pages * d->page_size : d->t_stride;
+    const long long cap = a->cap;
     const long long ctas = (long long)d->B * d->H_kv * ((d->N * a->G + kRowsCta - 1) / kRowsCta);
     long long splits = (4ll * sms + ctas - 1) / ctas;
     const long long most = (cap + 63) / 64;

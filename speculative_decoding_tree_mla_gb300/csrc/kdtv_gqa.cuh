@@ -21,9 +21,11 @@ struct GqaArgs {
   float2* part_ml;             // {reference maximum (log2 units), sum}; sum < 0: the row is not written
   int* plan;                   // tensor cores: units per group of CTAs, then each request's first unit
   int chunk, splits;           // CUDA cores: keys per split, splits
+  long long cap;               // rows a request may have
   // tensor cores: heads side by side in a group of CTAs, groups, nodes per 128-row tile (128 / G),
-  // log2 of page_size
-  int hg, groups, npt, page_shift;
+  // log2 of page_size, blocks of hg heads, row tiles
+  int hg, groups, npt, page_shift, blocks, tiles;
+  Divisor by_hg, by_groups, by_pair, by_G, by_tiles;   // (pair: two tiles' nodes)
 };
 
 __device__ __forceinline__ void gqa_error(const GqaArgs& a, unsigned int code) {
@@ -35,8 +37,7 @@ __device__ __forceinline__ void gqa_error(const GqaArgs& a, unsigned int code) {
 __device__ __forceinline__ void gqa_request(const GqaArgs& a, int b, int* L, int* n) {
   *L = a.prefix_len[b];
   *n = live_rows(a.n_nodes, b, a.N);
-  const long long cap = a.page_size ? (long long)a.max_pages * a.page_size : a.t_stride;
-  if (*n > 0 && (*L < 0 || (long long)*L + *n > cap)) {
+  if (*n > 0 && (*L < 0 || (long long)*L + *n > a.cap)) {
     gqa_error(a, KDTV_ERR_BAD_PREFIX);
     *n = 0;
   }

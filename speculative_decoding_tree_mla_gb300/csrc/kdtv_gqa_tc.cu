@@ -121,11 +121,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint3
 
 // ---- the sequence of units ---------------------------------------------------------------
 __device__ __forceinline__ int key_tiles(int L, int n) { return (L + n + kTile - 1) / kTile; }
-__device__ __forceinline__ int row_pairs(const GqaArgs& a, int n) { return (n + 2 * a.npt - 1) / (2 * a.npt); }
-__device__ __forceinline__ int units_of(const GqaArgs& a, int b) {
-  int L, n;
-  gqa_request(a, b, &L, &n);
-  return n > 0 ? a.Hkv / a.hg * row_pairs(a, n) * key_tiles(L, n) : 0;
+__device__ __forceinline__ int row_pairs(const GqaArgs& a, int n) {
+  return (int)divide((unsigned)(n + 2 * a.npt - 1), a.by_pair);
+}
+__device__ __forceinline__ int units_of(const GqaArgs& a, int b, int* L, int* n) {
+  gqa_request(a, b, L, n);
+  return *n > 0 ? a.blocks * row_pairs(a, *n) * key_tiles(*L, *n) : 0;
 }
 
 // A piece: the part of an item in one CTA.  The planning warp walks the CTA's
@@ -253,10 +254,17 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // What of a tree node's value row is not finite, added to the output row that a
 // thread has just written (o: bf16 output, or fp32 partial).  Rare: out of line.
+// Its elements 8 i .. 8 i + 7 stand `step` elements from the previous eight.
 template <int D, bool kFp8, typename T>
-__device__ __noinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int t, T* o) {
+__device__ __noinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int t, T* o, int step) {
   const long long row = gqa_row(a, b, t);
   if (row < 0) return;
   const long long at = (row * a.Hkv + kvh) * D;
@@ -265,8 +273,9 @@ __device__ __noinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int
     const float x = kFp8 ? to_f32(static_cast<const __nv_fp8_e4m3*>(a.v)[at + k])
                          : to_f32(static_cast<const __nv_bfloat16*>(a.v)[at + k]);
     if (fabsf(x) < INFINITY) continue;
-    const float y[1] = {to_f32(o[k]) + x};
-    store_v<1>(o + k, y);
+    T* at_k = o + (k >> 3) * step + (k & 7);
+    const float y[1] = {to_f32(*at_k) + x};
+    store_v<1>(at_k, y);
   }
 }
 // A row of values in shared memory with NaN codes (src: the codes; dst: bf16, swizzled, 64 columns
@@ -412,15 +421,21 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   if (warp >= kWarpTma) {
   if constexpr (!kFp8) reg_shrink<kRegsControl>();
   if (warp == kWarpPlan) {
-    // ---- planner: W and this CTA's first unit (one pass over the requests for the total, one
-    // to the unit), then its pieces
-    int sum = 0;
+    // ---- planner: W and this CTA's first unit, then its pieces.  All else waits for the first
+    // piece, and the code is cold: the first 32 requests stay in registers, and what a launch knows
+    // is divided by multiplication (together 1.2 us of a call).
+    int L0 = 0, n0 = 0;
+    const int u0 = lane < a.B ? units_of(a, lane, &L0, &n0) : 0;
+    int sum = u0;
 #pragma unroll 1
-    for (int b = lane; b < a.B; b += 32) sum += units_of(a, b);
+    for (int b = lane + 32; b < a.B; b += 32) {
+      int Lb, nb;
+      sum += units_of(a, b, &Lb, &nb);
+    }
     sum = __reduce_add_sync(0xffffffffu, sum);
-    const int W = (sum + a.groups - 1) / a.groups;
-    const long long first = (long long)(blockIdx.x / a.hg) * W;
-    const int my_head = blockIdx.x % a.hg;
+    const int W = (int)divide((unsigned)(sum + a.groups - 1), a.by_groups);
+    const int group = (int)divide(blockIdx.x, a.by_hg), my_head = blockIdx.x - group * a.hg;
+    const long long first = (long long)group * W;
     const int end = first < sum ? (int)(first + W < sum ? first + W : sum) : 0;
     int at = first < sum ? (int)first : 0, b = 0, off = 0;
     if (end > 0) {
@@ -428,7 +443,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (blockIdx.x == 0 && lane == 0) a.plan[0] = W;          // for the combine kernel
 #pragma unroll 1
       for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int u = b0 + lane < a.B ? units_of(a, b0 + lane) : 0;
+        int Lb, nb;
+        const int u = b0 == 0 ? u0 : b0 + lane < a.B ? units_of(a, b0 + lane, &Lb, &nb) : 0;
         int scan = u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -446,14 +462,18 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         before += __shfl_sync(0xffffffffu, scan, 31);
       }
     }
-    int L = 0, n = 0, nt = 1, rps = 1, hb = 0, pair = 0, t0 = 0;
+    int L = __shfl_sync(0xffffffffu, L0, b & 31), n = __shfl_sync(0xffffffffu, n0, b & 31);
+    int nt = 1, rps = 1, hb = 0, pair = 0, t0 = 0;
     if (end > 0) {
-      gqa_request(a, b, &L, &n);
+      if (b >= 32) gqa_request(a, b, &L, &n);
       nt = key_tiles(L, n);
       rps = row_pairs(a, n);
-      t0 = off % nt;
-      hb = off / nt / rps;
-      pair = off / nt % rps;
+      if (off > 0) {
+        const int item = off / nt;
+        t0 = off - item * nt;
+        hb = item / rps;
+        pair = item - hb * rps;
+      }
     }
     for (int k = 0;; ++k) {
       if (k >= kPieces && !wait_warp(guard, BAR(B_PIECE_READ + k % kPieces), (k / kPieces - 1) & 1)) break;
@@ -474,7 +494,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       t0 = 0;
       if (at < end && ++pair == rps) {
         pair = 0;
-        if (++hb == a.Hkv / a.hg) {
+        if (++hb == a.blocks) {
           hb = 0;
           do {
             gqa_request(a, ++b, &L, &n);         // units are left, so a request with some exists
@@ -963,7 +983,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t tS = tmem + lanes + C::kColS + kTile * s, tO = tmem + lanes + C::kColO + D * s;
     const float sl2 = a.scale * 1.4426950408889634f;      // base-2 exponentials
-    const int r_node = r / a.G, r_head = r % a.G;
+    const int r_node = (int)divide(r, a.by_G), r_head = r - r_node * a.G;
     Piece p;
     bool alive = true;
     uint32_t s_phase = 0u, o_phase = 0u, one_pieces = 0u;
@@ -1200,7 +1220,9 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const float inv = 1.f / l;
         const long long orow = ((long long)p.b * a.N + node) * a.H + (long long)kvh * a.G + r_head;
         const long long slot = 2ll * blockIdx.x + p.later();
-        const long long prow = slot * (2 * kTile) + (two ? kTile * s : 0) + r;
+        const long long block = slot * 2 + (two ? s : 0);   // of 128 partial rows
+        const long long prow = block * kTile + r;
+        float* part = a.part_o + (block * (D / 8) * kTile + r) * 8;
         if (!whole && valid) a.part_ml[prow] = make_float2(m, write ? l : -1.f);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -1227,10 +1249,9 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                                   pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
                                   pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
           } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            for (int k = 0; k < 4; ++k)
+              store8(part + (4 * c + k) * (kTile * 8), reinterpret_cast<const float(&)[8]>(v[8 * k]));
           }
         }
         if (write && p.tail()) {
@@ -1241,8 +1262,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             for (int j = 0; j < p.n; ++j) {
               const uint32_t word = j < 32 ? x[0] : j < 64 ? x[1] : j < 96 ? x[2] : x[3];
               if (!((word >> (j & 31)) & 1u)) continue;
-              if (whole) add_nonfinite<D, kFp8>(a, p.b, kvh, p.L + j, static_cast<__nv_bfloat16*>(a.out) + orow * D);
-              else add_nonfinite<D, kFp8>(a, p.b, kvh, p.L + j, a.part_o + prow * D);
+              if (whole) add_nonfinite<D, kFp8>(a, p.b, kvh, p.L + j, static_cast<__nv_bfloat16*>(a.out) + orow * D, 8);
+              else add_nonfinite<D, kFp8>(a, p.b, kvh, p.L + j, part, kTile * 8);
             }
           }
         }
@@ -1263,86 +1284,95 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
 // ---- combine --------------------------------------------------------------------------------
 // Output rows of items that were cut into pieces: the pieces' sums and outputs
-// meet at their common maximum.  A CTA takes kRowsCta rows of a (request, head,
-// row tile), a warp one row at a time, the row's d elements across its lanes.
-// Item [S, S + nt) was cut at the multiples of W; a CTA's piece that starts its
-// range is partial 2 cta, one that starts later 2 cta + 1.  W and the requests'
-// first units were left by the attention kernel.  Latency bound: the first
-// pieces' rows are loaded along with their {max, sum}.
-constexpr int kRowsCombine = 16;         // (32 / 8: 5 and 2 % slower on 8 trees of 32 nodes)
+// meet at their common maximum.  Item [S, S + nt) was cut at the multiples of W;
+// a CTA's piece that starts its range is partial 2 cta, one that starts later
+// 2 cta + 1.  W and the requests' first units were left by the attention kernel.
+// Partial rows lie [block of 128 rows][D / 8][row][8 elements], so that the
+// attention warps, a row per lane, write whole lines (row by row, the 32 lines
+// of a store took 4 us at the end of a call).  Here a warp takes four rows, whose
+// eight elements of a column are a line too; lane (column / 8 % 4, row, half).
+// Latency bound: the first pieces' rows are loaded along with their {max, sum}.
+constexpr int kCombineThreads = 128, kRowsCombine = kCombineThreads / 32 * 4, kInFlight = 4;
 
 template <int D>
-__global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant__ GqaArgs a, int tiles) {
+__global__ void __launch_bounds__(kCombineThreads) gqa_combine_kernel(const __grid_constant__ GqaArgs a) {
   const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x / tiles, tile = blockIdx.x % tiles, r0 = blockIdx.y * kRowsCombine;
+  const int kvh = (int)divide(blockIdx.x, a.by_tiles), tile = blockIdx.x - kvh * a.tiles;
+  const int r0 = blockIdx.y * kRowsCombine + 4 * warp;
   int L, n;
   gqa_request(a, b, &L, &n);
   const int rows = min(a.npt, n - tile * a.npt) * a.G;           // of the tile
+  const int hb = (int)divide(kvh, a.by_hg), head = kvh - hb * a.hg;
   // The partials and the plan are written.  (Blocks without rows wait as well: what comes next in
   // the stream may start when this grid has ended.)
   grid_dep_wait();
   if (r0 >= rows) return;
   if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
   const int W = a.plan[0], nt = key_tiles(L, n);
-  const int start = a.plan[1 + b] + (kvh / a.hg * row_pairs(a, n) + tile / 2) * nt;
+  const int start = a.plan[1 + b] + (hb * row_pairs(a, n) + tile / 2) * nt;
   const int c0 = start / W, count = (start + nt - 1) / W - c0 + 1;
   if (count == 1) return;                          // whole: written by its CTA
-  constexpr int V = D / 32;                        // elements per lane
-  const int head = kvh % a.hg;
   const bool later = start != c0 * W;              // of the first piece; the others start their CTA's range
-  const int recip = 65536 / a.G + 1;               // r / G = (r recip) >> 16 for r, G <= 128
-  for (int r = r0 + warp; r < min(rows, r0 + kRowsCombine); r += 8) {
-    const int i = (r * recip) >> 16, node = tile * a.npt + i, h = kvh * a.G + r - i * a.G;
-    auto prow = [&](int k) {                       // partial row of piece k
-      return (2ll * ((c0 + k) * a.hg + head) + (k == 0 && later)) * (2 * kTile) + (tile & 1) * kTile + r;
-    };
-    float m = -INFINITY, l = 0.f, o[V];
-    bool skip = false;
+  auto block = [&](int k) {                        // 128 partial rows of piece k
+    return (2ll * ((c0 + k) * a.hg + head) + (k == 0 && later)) * 2 + (tile & 1);
+  };
+  constexpr int T = D / 32;                        // fours of elements per lane
+  const int sub = (lane >> 1) & 3, r = r0 + sub, column = (lane >> 3) * 8, half = (lane & 1) * 4;
+  const bool live = r < rows, ml_live = lane < 4 * kInFlight && r0 + (lane & 3) < rows;
+  // lanes 4 k + i < 16: piece k of row r0 + i
+  float m2 = -INFINITY, l2 = 0.f, m = -INFINITY, o[4 * T];
+  bool skip = false;
 #pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = 0.f;
+  for (int k = 0; k < 4 * T; ++k) o[k] = 0.f;
 #pragma unroll 1
-    for (int base = 0; base < count; base += 8) {  // eight pieces in flight; a running maximum over the eights
-      float2 x[8][V / 2];
-      const bool have = lane < 8 && base + lane < count;
-      const float2 ml = have ? a.part_ml[prow(base + lane)] : make_float2(-INFINITY, 0.f);
+  for (int base = 0; base < count; base += kInFlight) {   // a running maximum over these
+    float4 x[kInFlight][T];
+    const float2 ml = ml_live && base + (lane >> 2) < count
+                          ? a.part_ml[block(base + (lane >> 2)) * kTile + r0 + (lane & 3)] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (base + k < count) {
-          const float2* src = reinterpret_cast<const float2*>(a.part_o + prow(base + k) * D + V * lane);
+    for (int k = 0; k < kInFlight; ++k)
+      if (live && base + k < count) {
+        const float* src = a.part_o + (block(base + k) * (D / 8) * kTile + r) * 8 + half;
 #pragma unroll
-          for (int e = 0; e < V / 2; ++e) x[k][e] = src[e];
-        }
-      skip |= ml.y < 0.f;
-      float mx = ml.x;
-#pragma unroll
-      for (int w = 4; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-      mx = fmaxf(m, __shfl_sync(0xffffffffu, mx, 0));
-      const float ref = mx == -INFINITY ? 0.f : mx, alpha = ex2(m - ref), weight = ex2(ml.x - ref);
-      m = mx;
-      l = l * alpha + ml.y * weight;               // lanes 0 .. 7 hold parts of the sum
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] *= alpha;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float w = __shfl_sync(0xffffffffu, weight, k);
-        if (base + k < count)
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            o[2 * e] = fmaf(x[k][e].x, w, o[2 * e]);
-            o[2 * e + 1] = fmaf(x[k][e].y, w, o[2 * e + 1]);
-          }
+        for (int t = 0; t < T; ++t)
+          x[k][t] = *reinterpret_cast<const float4*>(src + (4 * t + (lane >> 3)) * (kTile * 8));
       }
+    skip |= ml.y < 0.f;
+    float mx = ml.x;
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = fmaxf(m2, mx);
+    const float ref2 = mx == -INFINITY ? 0.f : mx, weight = ex2(ml.x - ref2);
+    l2 = l2 * ex2(m2 - ref2) + ml.y * weight;      // lanes hold parts of the sum
+    m2 = mx;
+    const float mo = __shfl_sync(0xffffffffu, mx, sub), ref = mo == -INFINITY ? 0.f : mo, alpha = ex2(m - ref);
+    m = mo;
+#pragma unroll
+    for (int k = 0; k < 4 * T; ++k) o[k] *= alpha;
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      const float w = __shfl_sync(0xffffffffu, weight, 4 * k + sub);
+      if (base + k < count)
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          o[4 * t] = fmaf(x[k][t].x, w, o[4 * t]);
+          o[4 * t + 1] = fmaf(x[k][t].y, w, o[4 * t + 1]);
+          o[4 * t + 2] = fmaf(x[k][t].z, w, o[4 * t + 2]);
+          o[4 * t + 3] = fmaf(x[k][t].w, w, o[4 * t + 3]);
+        }
     }
-    if (__any_sync(0xffffffffu, skip)) continue;
-    l = lane < 8 ? l : 0.f;
-#pragma unroll
-    for (int w = 4; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    const float inv = 1.f / __shfl_sync(0xffffffffu, l, 0);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                (((long long)b * a.N + node) * a.H + h) * D) + V / 2 * lane;
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) dst[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
   }
+  l2 += __shfl_xor_sync(0xffffffffu, l2, 4);
+  l2 += __shfl_xor_sync(0xffffffffu, l2, 8);
+  const float inv = 1.f / __shfl_sync(0xffffffffu, l2, sub);
+  const uint32_t dropped = __ballot_sync(0xffffffffu, skip);
+  if (!live || (dropped & (0x1111u << sub))) return;
+  const int i = (int)divide(r, a.by_G), node = tile * a.npt + i, h = kvh * a.G + r - i * a.G;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (((long long)b * a.N + node) * a.H + h) * D + column + half;
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+    *reinterpret_cast<uint2*>(dst + 32 * t) = make_uint2(pack_bf16x2(o[4 * t] * inv, o[4 * t + 1] * inv),
+                                                         pack_bf16x2(o[4 * t + 2] * inv, o[4 * t + 3] * inv));
 }
 
 template <int D, bool kFp8>
@@ -1370,10 +1400,9 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
   if (launch_ex(kern, dim3((unsigned)(a.groups * a.hg)), dim3(kThreads), C::kSmem, st, false, tq, tk, tv, a, stall ? 1 : 0) !=
       cudaSuccess)
     return KDTV_ERR_CUDA;
-  const int tiles = (a.N + a.npt - 1) / a.npt;
   const int most = (a.N < a.npt ? a.N : a.npt) * a.G;          // rows of a tile
-  const dim3 grid((unsigned)(a.Hkv * tiles), (unsigned)((most + kRowsCombine - 1) / kRowsCombine), (unsigned)a.B);
-  if (launch_ex(gqa_combine_kernel<D>, grid, dim3(256), 0, st, true, a, tiles) != cudaSuccess)
+  const dim3 grid((unsigned)(a.Hkv * a.tiles), (unsigned)((most + kRowsCombine - 1) / kRowsCombine), (unsigned)a.B);
+  if (launch_ex(gqa_combine_kernel<D>, grid, dim3(kCombineThreads), 0, st, true, a) != cudaSuccess)
     return KDTV_ERR_CUDA;
   return KDTV_OK;
 }
@@ -1396,7 +1425,14 @@ size_t gqa_tc_workspace(const kdtv_gqa_dims* d, int sms, GqaArgs* a) {
   a->hg = 8 < sms ? 8 : sms;
   while (d->H_kv % a->hg) --a->hg;
   a->groups = sms / a->hg;
-  const long long cap = d->page_size ? (long long)d->max_pages * d->page_size : d->t_stride;
+  a->blocks = d->H_kv / a->hg;
+  a->tiles = (d->N + a->npt - 1) / a->npt;
+  a->by_hg = divisor(a->hg);
+  a->by_groups = divisor(a->groups);
+  a->by_pair = divisor(2 * a->npt);
+  a->by_G = divisor(a->G);
+  a->by_tiles = divisor(a->tiles);
+  const long long cap = a->cap;
   const long long units = (long long)d->B * d->H_kv * ((d->N + 2 * a->npt - 1) / (2 * a->npt)) *
                           ((cap + kTile - 1) / kTile);
   if (units >= (1ll << 30)) return 0;               // 32-bit unit numbers

@@ -134,20 +134,6 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
 }
 
 // ---- cache rows -------------------------------------------------------------------------
-// n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
-// m = floor(2^32 (2^s - d) / d) + 1 the quotient is (n + floor(m n / 2^32)) >> s
-// (Granlund and Montgomery, 1994).
-struct Divisor {
-  uint32_t m, s;
-};
-Divisor divisor(uint32_t d) {
-  Divisor r{0u, 0u};
-  while ((1ull << r.s) < d) ++r.s;
-  r.m = (uint32_t)((((1ull << r.s) - d) << 32) / d + 1);
-  return r;
-}
-__device__ __forceinline__ unsigned divide(unsigned n, Divisor d) { return (n + __umulhi(n, d.m)) >> d.s; }
-
 struct KvPart {
   void* cache;
   uint8_t* scale;

@@ -1,4 +1,5 @@
-// Rotary angles, and 16-byte accesses, shared by the rotary and cache kernels.
+// Rotary angles, 16-byte accesses and divisions by what a launch knows, shared by the rotary, cache
+// and GQA kernels.
 #pragma once
 
 #include "kdtv_internal.cuh"
@@ -134,6 +135,20 @@ __device__ __forceinline__ void load_v(const __nv_fp8_e4m3* p, float (&x)[V]) {
     for (int k = 0; k < V; ++k) x[k] = to_f32(p[k]);
   }
 }
+
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
+// m = floor(2^32 (2^s - d) / d) + 1 the quotient is (n + floor(m n / 2^32)) >> s
+// (Granlund and Montgomery, 1994).
+struct Divisor {
+  uint32_t m, s;
+};
+inline Divisor divisor(uint32_t d) {
+  Divisor r{0u, 0u};
+  while ((1ull << r.s) < d) ++r.s;
+  r.m = (uint32_t)((((1ull << r.s) - d) << 32) / d + 1);
+  return r;
+}
+__device__ __forceinline__ unsigned divide(unsigned n, Divisor d) { return (n + __umulhi(n, d.m)) >> d.s; }
 
 // Live rows of request b.
 __device__ __forceinline__ int live_rows(const int32_t* n_live, int b, int N) {
