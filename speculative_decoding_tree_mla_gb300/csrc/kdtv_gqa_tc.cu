@@ -1289,16 +1289,20 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 // 2 cta + 1.  W and the requests' first units were left by the attention kernel.
 // Partial rows lie [block of 128 rows][D / 8][row][8 elements], so that the
 // attention warps, a row per lane, write whole lines (row by row, the 32 lines
-// of a store took 4 us at the end of a call).  Here a warp takes four rows, whose
-// eight elements of a column are a line too; lane (column / 8 % 4, row, half).
+// of a store took 4 us at the end of a call).  Here a warp takes 64 columns of
+// four rows, whose eight elements of a column are a line too; lane (column / 8 %
+// 4, row, half).
 // Latency bound: the first pieces' rows are loaded along with their {max, sum}.
-constexpr int kCombineThreads = 128, kRowsCombine = kCombineThreads / 32 * 4, kInFlight = 4;
+// (Rows of a CTA, pieces under way together, one token and 8 trees of 32 nodes: 16, 4: 13.6 and 43.8
+// us; 16, 8: 14.0 and 45.0; 8, 4: 14.8 and 43.1; 32, 4: 14.4 and 43.8.)
+constexpr int kRowsCombine = 16, kInFlight = 4;
+__host__ __device__ constexpr int combine_threads(int d) { return kRowsCombine / 4 * 32 * (d / 64); }
 
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) gqa_combine_kernel(const __grid_constant__ GqaArgs a) {
+__global__ void __launch_bounds__(combine_threads(D)) gqa_combine_kernel(const __grid_constant__ GqaArgs a) {
   const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = (int)divide(blockIdx.x, a.by_tiles), tile = blockIdx.x - kvh * a.tiles;
-  const int r0 = blockIdx.y * kRowsCombine + 4 * warp;
+  const int r0 = blockIdx.y * kRowsCombine + warp / (D / 64) * 4;
   int L, n;
   gqa_request(a, b, &L, &n);
   const int rows = min(a.npt, n - tile * a.npt) * a.G;           // of the tile
@@ -1316,8 +1320,8 @@ __global__ void __launch_bounds__(kCombineThreads) gqa_combine_kernel(const __gr
   auto block = [&](int k) {                        // 128 partial rows of piece k
     return (2ll * ((c0 + k) * a.hg + head) + (k == 0 && later)) * 2 + (tile & 1);
   };
-  constexpr int T = D / 32;                        // fours of elements per lane
-  const int sub = (lane >> 1) & 3, r = r0 + sub, column = (lane >> 3) * 8, half = (lane & 1) * 4;
+  constexpr int T = 2;                             // fours of elements per lane
+  const int sub = (lane >> 1) & 3, r = r0 + sub, column = warp % (D / 64) * 64 + (lane >> 3) * 8, half = (lane & 1) * 4;
   const bool live = r < rows, ml_live = lane < 4 * kInFlight && r0 + (lane & 3) < rows;
   // lanes 4 k + i < 16: piece k of row r0 + i
   float m2 = -INFINITY, l2 = 0.f, m = -INFINITY, o[4 * T];
@@ -1335,7 +1339,7 @@ __global__ void __launch_bounds__(kCombineThreads) gqa_combine_kernel(const __gr
         const float* src = a.part_o + (block(base + k) * (D / 8) * kTile + r) * 8 + half;
 #pragma unroll
         for (int t = 0; t < T; ++t)
-          x[k][t] = *reinterpret_cast<const float4*>(src + (4 * t + (lane >> 3)) * (kTile * 8));
+          x[k][t] = *reinterpret_cast<const float4*>(src + (4 * t + column / 8) * (kTile * 8));
       }
     skip |= ml.y < 0.f;
     float mx = ml.x;
@@ -1402,7 +1406,7 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
     return KDTV_ERR_CUDA;
   const int most = (a.N < a.npt ? a.N : a.npt) * a.G;          // rows of a tile
   const dim3 grid((unsigned)(a.Hkv * a.tiles), (unsigned)((most + kRowsCombine - 1) / kRowsCombine), (unsigned)a.B);
-  if (launch_ex(gqa_combine_kernel<D>, grid, dim3(kCombineThreads), 0, st, true, a) != cudaSuccess)
+  if (launch_ex(gqa_combine_kernel<D>, grid, dim3(combine_threads(D)), 0, st, true, a) != cudaSuccess)
     return KDTV_ERR_CUDA;
   return KDTV_OK;
 }
