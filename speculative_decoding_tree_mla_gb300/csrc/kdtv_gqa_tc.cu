@@ -1,6 +1,12 @@
 // Tensor-core (tcgen05) path of kdtv_gqa_verify_attn: bf16 queries, bf16 or
 // one-byte caches, head dims 64 and 128.
 //
+// Mathematics.  o = sum_t p_t v_t / sum_t p_t over the keys a node sees, p_t =
+// 2^(scale log2(e) q.k_t - m), with a running reference m per row: it moves only
+// when a tile's maximum is over 8 above it, so weights stay below 2^8 and O is
+// rescaled rarely.  Scores, m, sums and O are fp32; a weight is rounded to bf16
+// (to nearest, 2^-8) where it becomes an operand of the tensor cores.
+//
 // Work.  The query rows of a key/value head are (node, query head) pairs, cut
 // into tiles of npt = 128 / G nodes (at most 128 rows, one per TMEM lane).  An
 // item is (request, block of hg heads, pair of tiles); its work is its 128-key
@@ -8,31 +14,52 @@
 // takes the W consecutive units [cW, (c + 1)W), so ragged batches and few long
 // requests spread evenly; CTA h of the group works on head h of the block.  The
 // heads of a cache row are neighbours in memory, and the group reads them at
-// about the same time.  A piece (the part of an item in one CTA) that is not the
+// about the same time (most of a step from 695 to 474 us for 64 requests over
+// one-byte caches).  A piece (the part of an item in one CTA) that is not the
 // whole item leaves a partial {max, sum, O} that the combine kernel merges.
-// Each CTA derives the sequence from prefix_len by itself: no plan kernel.
+// One warp of each CTA derives the sequence from prefix_len: no plan kernel.
 //
 // A CTA runs two score streams s = 0, 1, each with a 128 x 128 score tile, an
-// output accumulator in TMEM and four softmax warps, so that one stream's
-// products run while the other's softmax does:
+// output accumulator in TMEM, four softmax warps and an issuing warp, so that one
+// stream's products run while the other's softmax does:
 //   two tiles of rows: stream s holds tile s, both read the same keys;
 //   one tile: both hold it, stream s takes the key tiles of parity s, and
 //             their results are merged at the end of the piece.
 // P replaces its scores in TMEM (bf16) and is the A operand of P.V, so only
-// keys, values and Q pass through shared memory.
+// keys, values and Q pass through shared memory.  The issuers take turns: a step's
+// products (P.V of one tile, Q.K^T of the next) run as one, since products that
+// share the tensor cores end together, and then so do the softmaxes (taking turns:
+// 258 -> 226 us for 128 nodes over 65536 keys).  A softmax hands its weights over
+// in two halves, so that the first half's products run beside the rest of it.
 //
 // Keys and values enter one ring in the order in which the products need
 // them.  With lag = 1 (two tiles) or 2 (one tile), step i of a piece multiplies
 // P.V of tile i - lag, then Q.K^T of tile i; the entry number of K_i within the
 // piece is i + max(0, i - lag + 1) and of V_i is i + min(n, i + lag).
 //
-// One-byte caches: TMA brings raw rows into a ring of their own, and four
-// warps widen them to bf16 with the row's power-of-two scale (exact) into the
-// operand ring.  bf16 caches: the same warps touch only the last key tiles,
-// where they zero the value rows behind the tree, and (both) replace values
-// that are not finite in the tree's own rows by 0, noting the keys: 0 * inf
-// must not reach nodes that do not see them.  The epilogue adds them back to
-// the rows that do.
+// One-byte caches.  Keys go to the tensor cores as they lie: a query row, scaled
+// by a power of two so that its largest element lies in [2^7, 2^8), is the sum of
+// two E4M3 parts (its eight significant bits; an element's error is at most 2^-17
+// of the row's largest), S = (Qhi + Qlo) K^T costs what bf16 would, and a
+// key's scale multiplies its column of scores in the softmax.  Values: TMA brings
+// raw rows into a ring of their own, and four warps widen them to bf16 with the
+// row's power-of-two scale (exact) into the operand ring.  bf16 caches: the same
+// warps touch only the last key tiles, where they zero the value rows behind the
+// tree, and (both) replace values that are not finite in the tree's own rows by
+// 0, noting the keys: 0 * inf must not reach nodes that do not see them.  The
+// epilogue adds them back to the rows that do.
+//
+// What bounds it (of a measured 1931 TFLOP/s and 6785 GB/s).  Many rows, long
+// prefixes: the tensor cores, 1270 TFLOP/s at 128 nodes x 64 heads over 65536 keys
+// in bf16 (216 us; 1430 from 32768 keys on, the rest is the way in and out) and 907
+// from a one-byte cache, where widening and a two-pass softmax share the issue slots.
+// Few rows: loads in flight and the chain load -> product -> softmax -> product of
+// a tile, 4960 GB/s at one node over 65536 keys, bf16.  Short calls: latency, 13.6
+// us for one token over 4096 keys, of which planning and first loads take 3, the
+// combine kernel 4.  Measured and not kept: a two-pass softmax for bf16 (284 us
+// where one pass took 258); 64 columns at a time for one-byte keys (447 us where 32
+// took 432: instruction cache); issuing loops rolled up (474 for 432); prefetching
+// scales to L2.
 //
 // Every wait has a time limit; one that runs out records
 // KDTV_ERR_DEVICE_TIMEOUT and ends the CTA's work.
