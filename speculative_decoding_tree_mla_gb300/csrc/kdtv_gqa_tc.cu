@@ -90,7 +90,7 @@ enum {
   B_K_EMPTY = B_K_FULL + kRing, B_Q_FULL = B_K_EMPTY + kRing,
   B_Q_READY, B_Q_EMPTY, B_S_FULL, B_P_HALF = B_S_FULL + 2, B_P_READY = B_P_HALF + 2,
   B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2, B_O1_FREE, B_MMA_DONE, B_STALL, B_TURN,
-  B_SCALE_FREE = B_TURN + 2, B_AUX = B_SCALE_FREE + 2, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
+  B_SCALE_FREE = B_TURN + 2, B_SCALE_FULL = B_SCALE_FREE + 2, B_AUX = B_SCALE_FULL + 2, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
   B_COUNT = B_PIECE_READ + kPieces
 };
 
@@ -394,11 +394,14 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       mbar_init(BAR(B_KV_EMPTY + i), 2);             // both issuers
       mbar_init(BAR(B_RAW_FULL + i), 1);             // (B_TAIL)
       mbar_init(BAR(B_RAW_EMPTY + i), 4);
-      mbar_init(BAR(B_K_FULL + i), 5);               // the copy, and the scales from four warps
+      mbar_init(BAR(B_K_FULL + i), 1);
       mbar_init(BAR(B_K_EMPTY + i), 2);
     }
     mbar_init(BAR(B_Q_READY), 4);
-    for (int i = 0; i < 2; ++i) mbar_init(BAR(B_SCALE_FREE + i), 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(B_SCALE_FREE + i), 8);
+      mbar_init(BAR(B_SCALE_FULL + i), 4);
+    }
     mbar_init(BAR(B_Q_FULL), 1);
     mbar_init(BAR(B_AUX), 4);
     mbar_init(BAR(B_Q_EMPTY), 2);
@@ -797,7 +800,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       aux_phase ^= 1u;
       return ok;
     };
-    Ring<kFp8 ? C::kRaw : 1> kring, vring;
+    Ring<kFp8 ? C::kRaw : 1> vring;
     Ring<C::kSlots> ring;
     Ring<2> sring;                                // of key scales
     float* scales = reinterpret_cast<float*>(smem + C::kOffScale);
@@ -948,15 +951,15 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           ring.next();
           }
           // Tile i's key scales, for the softmax: after the values, because the place is that of
-          // tile i - 2, whose softmax may still be at work while its values are widened.
+          // tile i - 2, whose softmax may still be at work while its values are widened.  (Only tile i's
+          // softmax waits for them: as part of the key entry they held tile i - 2's products back.)
           if (i < n) {
             alive = wait_warp(guard, BAR(B_SCALE_FREE + sring.slot), sring.phase ^ 1u);
             if (!alive) break;
             scales[sring.slot * kTile + row] = scale_of_byte(k0);
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_K_FULL + kring.slot));
+            if (lane == 0) mbar_arrive(BAR(B_SCALE_FULL + sring.slot));
             sring.next();
-            kring.next();
           }
           k0 = k1;
           vm2 = vm1;
@@ -1050,6 +1053,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         alive = wait_warp(guard, BAR(B_S_FULL + s), s_phase & 1);
         ++s_phase;
         if (!alive) break;
+        if constexpr (kFp8) {                    // the tile's key scales
+          alive = wait_warp(guard, BAR(B_SCALE_FULL + ((k_tiles + i) & 1)), ((k_tiles + i) >> 1) & 1);
+          if (!alive) break;
+        }
         if (!any_valid) {                        // no row of this warp is written: its weights may be anything
           if (o1_check) {
             o1_check = false;
