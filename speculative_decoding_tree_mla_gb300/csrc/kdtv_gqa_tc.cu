@@ -55,8 +55,8 @@
 // from a one-byte cache, where widening and a two-pass softmax share the issue slots.
 // Few rows: loads in flight and the chain load -> product -> softmax -> product of
 // a tile, 4960 GB/s at one node over 65536 keys, bf16.  Short calls: latency, 13.6
-// us for one token over 4096 keys, of which planning and first loads take 3, the
-// combine kernel 4.  Measured and not kept: a two-pass softmax for bf16 (284 us
+// us for one token over 4096 keys, of which planning takes 2 and the combine
+// kernel 4.  Measured and not kept: a two-pass softmax for bf16 (284 us
 // where one pass took 258); 64 columns at a time for one-byte keys (447 us where 32
 // took 432: instruction cache); issuing loops rolled up (474 for 432); prefetching
 // scales to L2.
