@@ -445,3 +445,31 @@ def test_every_code_and_scale(d, page, flags):
         fin = np.isfinite(want)
         assert (np.isnan(got[b, 0]) == ~fin).all()
         assert (np.abs(got[b, 0] - want)[fin] <= (2.0 ** -134 if byte < 10 else 0.0)).all()
+
+
+@pytest.mark.parametrize("cache,page", [("bf16", 0), ("fp8", 16)])
+def test_many_requests_some_of_them_bad(cache, page):
+    """More requests than a warp has lanes, some empty, some with a prefix that does not fit, one whose
+    last nodes have no parent (31): those rows stay, all others are right."""
+    rng = np.random.default_rng(10)
+    B = 70
+    prefix, n = rng.integers(0, 700, size=B), rng.integers(0, 6, size=B)
+    x = Case(B, 5, 8, 2, 128, cache, page, prefix, n, seed=11)
+    x.n[[33, 50]] = 0
+    x.n[[31, 32, 69]] = 5
+    good, known = x.prefix.copy(), n.copy()
+    x.prefix[[32, 69]] = [-1, 1 << 20]
+    got, want = x.op(), x.op(SIMT)
+    g, w = got().float(), want().float()
+    first = ("KDTV_ERR_BAD_PREFIX", "KDTV_ERR_BAD_TREE")
+    assert kdtv.STATUS[got.status()] in first and kdtv.STATUS[want.status()] in first
+    for out in (g, w):
+        assert (out[[32, 33, 50, 69]] == 9.0).all() and (out[31, max(known[31], 1):] == 9.0).all()
+    x.prefix, x.n[[32, 69]] = good, 0
+
+    def whole(b):                             # nodes with a root path
+        return range(min(int(x.n[b]), max(int(known[b]), 1)) if b == 31 else int(x.n[b]))
+
+    x.parent[31, max(known[31], 1):] = 0      # (for the oracle, whose rows there are not looked at)
+    x.check(got.out, True, rows=whole)
+    x.check(want.out, False, rows=whole)

@@ -300,3 +300,37 @@ def test_two_host_threads():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.uint8], ids=["bf16", "f32", "bytes"])
+@pytest.mark.parametrize("page", [0, 16])
+def test_compaction_of_wide_rows(dtype, page):
+    """A per-head cache's keys and values as the two tensors: rows whose chunk passes the 48 KiB of
+    shared memory that need no opt-in."""
+    B, N, T, width = 3, 40, 96, 1024 if dtype != torch.uint8 else 2048
+    rng = np.random.default_rng([4, page])
+    shape = (B * T // page, page, width) if page else (B, T, width)
+    table = rng.permutation(shape[0]).reshape(B, -1).astype(np.int32) if page else None
+    K, V = (dev(rng.integers(0, 200, size=shape)).to(dtype) for _ in range(2))
+    prefix, plen = np.array([0, 17, 50], np.int32), np.array([40, 1, 9], np.int32)
+    path = np.full((B, N), -1, np.int32)
+    for b in range(B):
+        path[b, :plen[b]] = [0] + sorted(rng.choice(np.arange(1, N), size=plen[b] - 1, replace=False))
+    name = {torch.bfloat16: "bf16", torch.float32: "f32", torch.uint8: "fp8kv"}[dtype]
+    spec = W.Spec("wide", 0, B=B, N=N, H=1, d_nope=width, d_rope=width, d_v=width, d_c=width, dtype=name,
+                  prefix=("fixed", 0), tree=("chain",))
+    d = kdtv.make_dims(spec, dtype=name, page_size=page, t_stride=0 if page else T,
+                       max_pages=T // page if page else 0, num_pages=shape[0] if page else 0)
+
+    def rows(x, b):
+        return x[torch.from_numpy(table[b]).long().cuda()].view(T, width) if page else x[b]
+
+    before = [[rows(x, b).clone() for b in range(B)] for x in (K, V)]
+    st = kdtv.compact_kv(d, K, V, dev(prefix), dev(path), dev(plen), dev(table) if page else None)
+    assert int(st.item()) == 0
+    for x, old in zip((K, V), before):
+        for b in range(B):
+            want = old[b].clone()
+            for k in range(plen[b]):
+                want[prefix[b] + k] = old[b][prefix[b] + path[b, k]]
+            assert torch.equal(rows(x, b), want)
