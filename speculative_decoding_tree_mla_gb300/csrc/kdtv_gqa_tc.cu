@@ -90,9 +90,28 @@ enum {
   B_K_EMPTY = B_K_FULL + kRing, B_Q_FULL = B_K_EMPTY + kRing,
   B_Q_READY, B_Q_EMPTY, B_S_FULL, B_P_HALF = B_S_FULL + 2, B_P_READY = B_P_HALF + 2,
   B_O_FULL = B_P_READY + 2, B_ML = B_O_FULL + 2, B_O1_FREE, B_MMA_DONE, B_STALL, B_TURN,
-  B_SCALE_FREE = B_TURN + 2, B_SCALE_FULL = B_SCALE_FREE + 2, B_AUX = B_SCALE_FULL + 2, B_PIECE, B_PIECE_READ = B_PIECE + kPieces,
+  B_SCALE_FREE = B_TURN + 2, B_SCALE_FULL = B_SCALE_FREE + 2, B_AUX = B_SCALE_FULL + 2, B_PIECE,
+  B_PIECE_READ = B_PIECE + kPieces,
   B_COUNT = B_PIECE_READ + kPieces
 };
+
+// Arrivals of a barrier's phase.
+template <bool kFp8>
+__device__ __forceinline__ uint32_t arrivals(int i) {
+  if (i < B_KV_EMPTY) return kFp8 ? 4 : 1;                  // (widened by four warps)
+  if (i < B_TAIL) return 2;                                 // both issuers
+  if (i < B_RAW_EMPTY) return 1;
+  if (i < B_K_FULL) return 4;
+  if (i < B_K_EMPTY) return 1;
+  if (i < B_Q_FULL) return 2;
+  if (i == B_Q_READY || i == B_ML || i == B_O1_FREE || i == B_AUX) return 4;
+  if (i == B_Q_EMPTY || i == B_MMA_DONE) return 2;
+  if (i >= B_P_HALF && i < B_O_FULL) return 4;              // (and B_P_READY)
+  if (i >= B_SCALE_FREE && i < B_SCALE_FULL) return 8;
+  if (i >= B_SCALE_FULL && i < B_AUX) return 4;
+  if (i >= B_PIECE_READ) return 15;                         // producer, two issuers, 4 + 8 warps
+  return 1;
+}
 
 template <int D, bool kFp8>
 struct Cfg {
@@ -387,42 +406,12 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   const Guard guard{misc + 1, a.status, stall ? 20000000u : 2000000000u};
 
   grid_dep_launch();               // the combine kernel may be launched; it waits for this grid
-  if (threadIdx.x == 0) {
-    misc[1] = 0u;
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(BAR(B_KV_FULL + i), kFp8 ? 4 : 1);   // (widened by four warps)
-      mbar_init(BAR(B_KV_EMPTY + i), 2);             // both issuers
-      mbar_init(BAR(B_RAW_FULL + i), 1);             // (B_TAIL)
-      mbar_init(BAR(B_RAW_EMPTY + i), 4);
-      mbar_init(BAR(B_K_FULL + i), 1);
-      mbar_init(BAR(B_K_EMPTY + i), 2);
-    }
-    mbar_init(BAR(B_Q_READY), 4);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(BAR(B_SCALE_FREE + i), 8);
-      mbar_init(BAR(B_SCALE_FULL + i), 4);
-    }
-    mbar_init(BAR(B_Q_FULL), 1);
-    mbar_init(BAR(B_AUX), 4);
-    mbar_init(BAR(B_Q_EMPTY), 2);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(BAR(B_S_FULL + i), 1);
-      mbar_init(BAR(B_P_HALF + i), 4);
-      mbar_init(BAR(B_P_READY + i), 4);
-      mbar_init(BAR(B_O_FULL + i), 1);
-    }
-    mbar_init(BAR(B_ML), 4);
-    mbar_init(BAR(B_O1_FREE), 4);
-    mbar_init(BAR(B_MMA_DONE), 2);
-    mbar_init(BAR(B_STALL), 1);
-    mbar_init(BAR(B_TURN), 1);
-    mbar_init(BAR(B_TURN + 1), 1);
-    for (int i = 0; i < kPieces; ++i) {
-      mbar_init(BAR(B_PIECE + i), 1);
-      mbar_init(BAR(B_PIECE_READ + i), 15);      // producer, two issuers, 4 + 8 warps
-    }
-    fence_mbar_init();
-  }
+  // The planner's first 32 requests are on their way while barriers and TMEM are set up.
+  int L0 = 0, n0 = 0, u0 = 0;
+  if (warp == kWarpPlan && lane < a.B) u0 = units_of(a, lane, &L0, &n0);
+  if (threadIdx.x < B_COUNT) mbar_init(BAR(threadIdx.x), arrivals<kFp8>(threadIdx.x));
+  if (threadIdx.x == 0) misc[1] = 0u;
+  fence_mbar_init();
   if (threadIdx.x < kPieces) bad_page[threadIdx.x] = 0u;
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(misc), 512);
@@ -454,8 +443,6 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     // ---- planner: W and this CTA's first unit, then its pieces.  All else waits for the first
     // piece, and the code is cold: the first 32 requests stay in registers, and what a launch knows
     // is divided by multiplication (together 1.2 us of a call).
-    int L0 = 0, n0 = 0;
-    const int u0 = lane < a.B ? units_of(a, lane, &L0, &n0) : 0;
     int sum = u0;
 #pragma unroll 1
     for (int b = lane + 32; b < a.B; b += 32) {
