@@ -561,6 +561,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         return table[box];
       };
       int win = page_at(lane), win_next = page_at(32 + lane);
+      if (index == 0) alive = load_q();           // (while the page ids are under way)
       int page0 = 0, page1 = 0, page2 = 0;        // of tiles i, i - 1, i - 2
       uint32_t bad = 0;
       for (int i = 0; alive && i < n + lag; ++i) {
@@ -592,7 +593,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           const int slot = kFp8 ? (kv == 0 ? vring.slot : kring.slot) : ring.slot;
           const uint32_t phase = kFp8 ? (kv == 0 ? vring.phase : kring.phase) : ring.phase;
           const uint32_t empty = BAR((kFp8 ? (kv == 0 ? B_RAW_EMPTY : B_K_EMPTY) : B_KV_EMPTY) + slot);
-          if (q_pending && (index == 0 || __all_sync(0xffffffffu, mbar_test_wait(BAR(B_Q_EMPTY), (index - 1) & 1)) ||
+          if (q_pending && (__all_sync(0xffffffffu, mbar_test_wait(BAR(B_Q_EMPTY), (index - 1) & 1)) ||
                             !__all_sync(0xffffffffu, mbar_test_wait(empty, phase ^ 1u))))
             alive = load_q();
           alive = alive && wait_warp(guard, empty, phase ^ 1u);
