@@ -3,6 +3,7 @@
 // cores do not take).
 
 #include "kdtv_gqa.cuh"
+#include "kdtv_ptx.cuh"
 
 #include <math.h>
 #include <string.h>
@@ -30,6 +31,7 @@ template <typename T, typename C, int DK>     // DK = ceil(d / 32), rounded up t
 __global__ void __launch_bounds__(kSimtThreads) gqa_simt_kernel(const __grid_constant__ GqaArgs a) {
   extern __shared__ __align__(16) float sm[];
   const int d = a.d, dp = simt_padded(d), ld = dp + 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::grid_dep_launch();          // the combine kernel may be launched; it waits for this grid
   float* ks = sm;                                  // [kKeys][ld]
   float* vs = ks + kKeys * ld;                     // [kKeys][ld]
   float* qs = vs + kKeys * ld;                     // [kRowsCta][dp]
@@ -210,10 +212,15 @@ __global__ void __launch_bounds__(256) gqa_simt_combine_kernel(const __grid_cons
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const long long all = (long long)a.B * a.N * a.H;
-  if (row >= all) return;
-  const int b = (int)(row / ((long long)a.N * a.H)), i = (int)(row / a.H % a.N);
-  int L, n;
-  gqa_request(a, b, &L, &n);
+  int L = 0, n = 0, i = 0;
+  if (row < all) {
+    const int b = (int)(row / ((long long)a.N * a.H));
+    i = (int)(row / a.H % a.N);
+    gqa_request(a, b, &L, &n);
+  }
+  // (warps without a row wait as well: what comes next in the stream may start when this grid has
+  // ended)
+  ptx::grid_dep_wait();
   if (i >= n) return;
   const int pieces = (L + n + a.chunk - 1) / a.chunk;       // <= 64
   const float2 none = make_float2(-INFINITY, 0.f);
@@ -259,8 +266,9 @@ int launch_simt_t(const GqaArgs& a, cudaStream_t st) {
   if (cudaGetLastError() != cudaSuccess) return KDTV_ERR_CUDA;
   if (a.splits > 1) {
     const long long rows = (long long)a.B * a.N * a.H;
-    gqa_simt_combine_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return KDTV_ERR_CUDA;
+    if (launch_ex(gqa_simt_combine_kernel<T>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, true, a) !=
+        cudaSuccess)
+      return KDTV_ERR_CUDA;
   }
   return KDTV_OK;
 }
