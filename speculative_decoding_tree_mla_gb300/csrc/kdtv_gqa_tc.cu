@@ -50,11 +50,11 @@
 // epilogue adds them back to the rows that do.
 //
 // What bounds it (of a measured 1931 TFLOP/s and 6785 GB/s).  Many rows, long
-// prefixes: the tensor cores, 1270 TFLOP/s at 128 nodes x 64 heads over 65536 keys
-// in bf16 (216 us; 1430 from 32768 keys on, the rest is the way in and out) and 907
+// prefixes: the tensor cores, 1285 TFLOP/s at 128 nodes x 64 heads over 65536 keys
+// in bf16 (213 us; 1430 from 32768 keys on, the rest is the way in and out) and 907
 // from a one-byte cache, where widening and a two-pass softmax share the issue slots.
 // Few rows: loads in flight and the chain load -> product -> softmax -> product of
-// a tile, 4960 GB/s at one node over 65536 keys, bf16.  Short calls: latency, 13.6
+// a tile, 4960 GB/s at one node over 65536 keys, bf16.  Short calls: latency, 13.2
 // us for one token over 4096 keys, of which planning takes 2 and the combine
 // kernel 4.  Measured and not kept: a two-pass softmax for bf16 (284 us
 // where one pass took 258); 64 columns at a time for one-byte keys (447 us where 32
