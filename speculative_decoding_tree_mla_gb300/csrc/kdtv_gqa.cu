@@ -161,6 +161,21 @@ __global__ void __launch_bounds__(kSimtThreads) gqa_simt_kernel(const __grid_con
     __syncwarp();
     ps[lane] = make_float4(p[0], p[1], p[2], p[3]);
     __syncwarp();
+    if (t0 + kKeys <= min(L, t_hi)) {                // all rows see all keys
+#pragma unroll 4
+      for (int j = 0; j < kKeys; ++j) {
+        const float4 w = ps[j];
+#pragma unroll
+        for (int k = 0; k < DK; ++k) {
+          const float v = lane + 32 * k < dp ? vs[j * ld + lane + 32 * k] : 0.f;
+          o[0][k] = fmaf(w.x, v, o[0][k]);
+          o[1][k] = fmaf(w.y, v, o[1][k]);
+          o[2][k] = fmaf(w.z, v, o[2][k]);
+          o[3][k] = fmaf(w.w, v, o[3][k]);
+        }
+      }
+      continue;
+    }
     // only what a row sees: a masked value may be infinite or NaN
     while (any) {
       const int j = __ffs(any) - 1;

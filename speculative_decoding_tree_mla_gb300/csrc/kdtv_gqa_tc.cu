@@ -1435,6 +1435,8 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
 
 }  // namespace
 
+// Wherever these shapes allow it: from one node over 32 keys (9.0 us, CUDA cores 15.0) and 1024
+// requests of 64 keys (304, 359) to 256 requests of 1024 (194, 1003) the CUDA cores were never ahead.
 int gqa_tc_supported(const kdtv_gqa_dims* d) {
   if (d->dtype != KDTV_BF16 && d->dtype != KDTV_BF16_FP8KV) return 0;
   if (d->d != 64 && d->d != 128) return 0;
