@@ -247,7 +247,6 @@ __device__ __forceinline__ void convert(const KvArgs& a, float (&y)[P][V], float
 struct Rows {
   int b, L, i0, i1, h0, h1, group;
 };
-template <int V>
 __device__ __forceinline__ int partner(const KvPart& part, int rot_dim, bool half, int e) {
   // distance from element e to its rotation partner (0: not rotated)
   const int r0 = e - part.rot_off;
@@ -291,7 +290,7 @@ __device__ __forceinline__ void append_rows(const KvArgs& a, const KvPart& part,
   // (every block looks the whole request up: it is written as a whole or not at all)
   if (!rows_ok(a, r.b, r.L, n)) return;
   if constexpr (kRot != kPlain) __syncthreads();      // the table
-  const int mate = kRot == kPlain ? 0 : partner<8>(part, rot_dim, kRot == kHalves, lane * 8);
+  const int mate = kRot == kPlain ? 0 : partner(part, rot_dim, kRot == kHalves, lane * 8);
   const int from = threadIdx.x % 32 + (kRot == kHalves ? mate / 8 : 0);   // lane with the partners
   long long row = i < r.i1 ? row_of(a, r.b, r.L + i) : 0;
   for (int i_turn = r.i0; i_turn < r.i1; i_turn += groups, i += groups) {
@@ -373,7 +372,7 @@ __device__ __forceinline__ void append_rows_any(const KvArgs& a, const KvPart& p
   const int group = r.group, lane = threadIdx.x % group, groups = kThreads / group;
   int mate[P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) mate[p] = partner<V>(part, rot_dim, half, (p * group + lane) * V);
+  for (int p = 0; p < P; ++p) mate[p] = partner(part, rot_dim, half, (p * group + lane) * V);
   int i = r.i0 + threadIdx.x / group;
   for (int i_turn = r.i0; i_turn < r.i1; i_turn += groups, i += groups) {
     const bool on = i < r.i1;

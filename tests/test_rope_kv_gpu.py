@@ -428,3 +428,24 @@ def test_broadcast_rows():
     assert torch.equal(a, b) and not torch.equal(a, torch.zeros_like(a))
     one = base[:, :1]                                  # one row: any strides
     assert torch.equal(kdtv.rope(t, one), kdtv.rope(t, one.clone()))
+
+
+@pytest.mark.parametrize("kv_scale", [0.07, 3e-3, 1.75, 2.0 ** -9])
+@pytest.mark.parametrize("heads,dim", [(1, 512), (1, 64), (6, 128), (3, 33)])
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+def test_static_scales_bit_by_bit(kv_scale, heads, dim, src):
+    """The code nearest x / kv_scale in fp32 (a division, also where a product would do), and the
+    code times kv_scale, rounded once."""
+    x = dev(np.random.default_rng(8).standard_normal((2, 19, heads, dim), dtype=np.float32), DT[src])
+    cache = torch.zeros((2, 30, heads, dim), dtype=torch.uint8, device="cuda")
+    at = dev(np.array([3, 11], np.int32))
+    assert int(kdtv.kv_append([kdtv.KvPart(cache, src=x)], at, kv_scale=kv_scale).item()) == 0
+    s = np.float32(kv_scale)
+    codes = torch.from_numpy(np.clip(x.float().cpu().numpy() / s, -448, 448)).to(torch.float8_e4m3fn)
+    back = torch.zeros_like(x)
+    assert int(kdtv.kv_read([kdtv.KvPart(cache, out=back)], at, dev(np.array([19, 19], np.int32)),
+                            kv_scale=kv_scale).item()) == 0
+    value = torch.from_numpy(codes.float().numpy() * s).to(DT[src])
+    for b, L in enumerate((3, 11)):
+        assert torch.equal(cache[b, L:L + 19].cpu(), codes[b].view(torch.uint8))
+        assert torch.equal(back[b].cpu(), value[b])
