@@ -286,7 +286,8 @@ int kdtv_verify_attn_noalloc(const kdtv_dims* dims, const void* q_nope, const vo
  *     depth[b][i] (depth NULL: prefix_len[b] + i; prefix_len NULL: 0).
  *     kdtv_tree_build writes depth and n_nodes in this form.
  *   - Device-side problems go to *status (a device word that the caller
- *     clears, first error wins), as with kdtv_compact_kv.
+ *     clears; the first error wins, but a wait that ran out replaces it), as
+ *     with kdtv_compact_kv.
  */
 
 /* Rotary embedding.  Pair j of the rot_dim rotated elements turns by
@@ -450,8 +451,9 @@ int kdtv_gqa_launches_per_call(const kdtv_gqa_dims* dims);
  * Scale bytes 1 .. 254 stand for 2^-126 .. 2^127.  On tensor cores a one-byte
  * key's product with a query row scaled to 2^8 is formed before both scales are
  * taken back, so key bytes above 227 (2^100) may overflow a score.
- * While *status holds KDTV_ERR_DEVICE_TIMEOUT (a wait that ran out), rows whose
- * keys are spread over several CTAs are not written: clear it first.
+ * A wait that runs out puts KDTV_ERR_DEVICE_TIMEOUT into *status in place of any
+ * other code, and while the word holds it, rows whose keys are spread over
+ * several CTAs are not written: clear it before the next call.
  * Rows of out behind n_nodes[b] are left as they were, and so are rows whose
  * root path is malformed (KDTV_ERR_BAD_TREE) and requests with a bad prefix or
  * page.  Cache rows at and behind prefix_len[b] + n_nodes[b] may hold

@@ -62,7 +62,7 @@
 // scales to L2.
 //
 // Every wait has a time limit; one that runs out records
-// KDTV_ERR_DEVICE_TIMEOUT and ends the CTA's work.
+// KDTV_ERR_DEVICE_TIMEOUT, whatever the status word held, and ends the CTA's work.
 
 #include <cuda.h>
 
@@ -207,7 +207,7 @@ __device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t pari
   while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
     if (*g.abort) return false;
     if (timer_lo() - t0 > g.limit) {
-      atomicCAS(g.status, 0u, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
+      atomicExch(g.status, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);   // over any other code: the combine kernel asks
       *g.abort = 1u;
       return false;
     }
@@ -1333,6 +1333,8 @@ __global__ void __launch_bounds__(combine_threads(D)) gqa_combine_kernel(const _
   // the stream may start when this grid has ended.)
   grid_dep_wait();
   if (r0 >= rows) return;
+  // (a wait that ran out: some partials were never written.  Its code replaces any other, and no other
+  // replaces it.)
   if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
   const int W = a.plan[0], nt = key_tiles(L, n);
   const int start = a.plan[1 + b] + (hb * row_pairs(a, n) + tile / 2) * nt;

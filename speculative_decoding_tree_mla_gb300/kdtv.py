@@ -670,7 +670,8 @@ class GqaVerifyAttn(_Bound):
         return self.out
 
     def status(self):
-        """First device-side error since it was last read (0: none); waits for the device, clears it."""
+        """First device-side error since it was last read (0: none), or the timeout of a wait, which
+        replaces any other; waits for the device, clears it."""
         self.torch.cuda.synchronize(self.device)
         code = int(self._status.item())
         if code:
