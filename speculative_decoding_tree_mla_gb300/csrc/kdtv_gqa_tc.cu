@@ -309,14 +309,17 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 // What of a tree node's value row is not finite, added to the output row that a
 // thread has just written (o: bf16 output, or fp32 partial).  Rare: out of line.
 // Its elements 8 i .. 8 i + 7 stand `step` elements from the previous eight.
+// (One-byte caches: NaN codes, and codes whose value at the row's scale is above the largest
+// bf16, which is where fp32 overflows too: a code has four significant bits.)
 template <int D, bool kFp8, typename T>
 __device__ __noinline__ void add_nonfinite(const GqaArgs& a, int b, int kvh, int t, T* o, int step) {
   const long long row = gqa_row(a, b, t);
   if (row < 0) return;
   const long long at = (row * a.Hkv + kvh) * D;
+  const float scale = kFp8 ? scale_of_byte(a.v_scale[row * a.Hkv + kvh]) : 1.f;
 #pragma unroll 1
   for (int k = 0; k < D; ++k) {
-    const float x = kFp8 ? to_f32(static_cast<const __nv_fp8_e4m3*>(a.v)[at + k])
+    const float x = kFp8 ? to_f32(static_cast<const __nv_fp8_e4m3*>(a.v)[at + k]) * scale
                          : to_f32(static_cast<const __nv_bfloat16*>(a.v)[at + k]);
     if (fabsf(x) < INFINITY) continue;
     T* at_k = o + (k >> 3) * step + (k & 7);
@@ -877,7 +880,8 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             alive = wait_warp(guard, BAR(B_RAW_FULL + vring.slot), vring.phase) &&
                     wait_warp(guard, BAR(B_KV_EMPTY + ring.slot), ring.phase ^ 1u);
           if (!alive) break;
-          // the row's scale times 2^120; above 2^127 the rest follows in a second pass (rare)
+          // the row's scale times 2^120; above 2^127 the rest follows in a second pass (rare), where
+          // what overflows in the tree's own rows becomes 0 and is noted for the epilogue
           const int byte = lag == 1 ? vm1 : vm2, low = min(byte, 134);
           const uint32_t f = (uint32_t)(low + 120) * 0x00800080u;
           const uint32_t src = sbase + C::kOffRaw + vring.slot * C::kRawBytes + row * D;
@@ -919,8 +923,16 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll 1
             for (int c = 0; c < D / 8; ++c) {
               const uint32_t addr = dst + (c >> 3) * C::kChunk + (((c & 7) ^ swz) << 4);
-              const uint4 x = lds128(addr);
-              sts128(addr, mul_bf16x2(x.x, f2), mul_bf16x2(x.y, f2), mul_bf16x2(x.z, f2), mul_bf16x2(x.w, f2));
+              uint4 x = lds128(addr);
+              x = make_uint4(mul_bf16x2(x.x, f2), mul_bf16x2(x.y, f2), mul_bf16x2(x.z, f2), mul_bf16x2(x.w, f2));
+              if (t >= p.L) {
+                bool any = drop_nonfinite(x.x);
+                any |= drop_nonfinite(x.y);
+                any |= drop_nonfinite(x.z);
+                any |= drop_nonfinite(x.w);
+                if (any) atomicOr(&nf[(t - p.L) >> 5], 1u << ((t - p.L) & 31));
+              }
+              sts128(addr, x.x, x.y, x.z, x.w);
             }
           }
           // NaN in the tree's own rows becomes 0, noted for the epilogue

@@ -1,11 +1,65 @@
-"""GQA tree attention where it is easily wrong: waits that run out behind another error."""
+"""GQA tree attention at the edges of its types, errors and head counts.
 
+Tolerance, fixed before the first run: that of bf16 caches, for one-byte caches too.  With delta =
+(d + 4) * 2^-24 * scale * max_t sum_e |q_e k_te| bounding a score's fp32 error, the weights are off
+by a factor of at most 1 + 2 delta + 2^-20, on tensor cores each is rounded to bf16 (2^-8), so with
+A = sum_t p_t |v_t| the sum is off by (2 delta + 2^-20 + T 2^-24 [+ 2^-8]) * A, and the output's
+rounding adds 2^-8 |o|.  Queries and keys count as they are: a query held in parts has to be their
+exact sum, down to 2^-31 of its row's largest element.
+"""
+
+import numpy as np
 import pytest
+import torch
 
+from oracle import rope_kv as O
 from speculative_decoding_tree_mla_gb300 import kdtv
-from tests.test_gqa_gpu import Case
+from tests.test_gqa_gpu import SIMT, Case
 
 pytestmark = pytest.mark.gpu
+
+BF16_MAX = float(torch.finfo(torch.bfloat16).max)
+
+
+def check(x, out, tensor_cores):
+    k, v = x.gathered()
+    v = np.where(np.abs(v) > BF16_MAX, np.copysign(np.inf, v), v)     # as widened
+    q = x.q.float().cpu().double().numpy()
+    scale, G, T = x.d ** -0.5, x.H // x.Hkv, k.shape[1]
+    want = O.gqa_attn(q, k, v, x.parent, x.prefix, scale, x.n)
+    A = O.gqa_attn(q, k, np.abs(v), x.parent, x.prefix, scale, x.n)
+    got = out.float().cpu().double().numpy()
+    for b in range(x.B):
+        n = int(x.n[b])
+        assert (got[b, n:] == 9.0).all()
+        kk = np.repeat(np.abs(k[b]).max(0), G, axis=0)                # [H, d]
+        delta = (x.d + 4) * 2.0 ** -24 * scale * (np.abs(q[b, :n]) * kk).sum(-1)[..., None]
+        rel = 2 * delta + 2.0 ** -20 + T * 2.0 ** -24 + (2.0 ** -8 if tensor_cores else 0.0)
+        w, g, a = want[b, :n], got[b, :n], A[b, :n]
+        fin = np.isfinite(w)
+        assert (np.isnan(g) == np.isnan(w)).all() and (g[np.isinf(w)] == w[np.isinf(w)]).all()
+        with np.errstate(invalid="ignore"):
+            err, tol = np.abs(g - w)[fin], (rel * a + 2.0 ** -8 * np.abs(w))[fin]
+        assert (err <= tol).all(), (b, (err / tol).max())
+
+
+@pytest.mark.parametrize("flags", [0, SIMT], ids=["auto", "simt"])
+@pytest.mark.parametrize("byte", [247, 250, 254])
+@pytest.mark.parametrize("d,page,prefix", [(128, 0, 20), (128, 16, 700), (64, 16, 61), (64, 0, 700)])
+def test_values_that_overflow(d, page, prefix, byte, flags):
+    """A node whose value row overflows when it is widened (scale bytes above 246) reaches itself and
+    its descendants alone; in the prefix it reaches all."""
+    for in_prefix in (False, True):
+        x = Case(1, 14, 8, 2, d, "fp8", page, [prefix], seed=23, tree=(3, 3))
+        nodes = (2, 5, 11) if not in_prefix else (-3,)
+        for node, codes in zip(nodes, ((0x7E, 0x01, 0x02, 0xFE), (0xFE, 0x7E, 0x00, 0x01), (0x00, 0x81, 0xFE, 0x7F))):
+            row = x.rows(0, prefix + node + 1)[-1].cuda()
+            x.scales[1].view(-1, 2)[row, 0] = byte
+            x.kv[1].view(-1, 2, d)[row, 0] = 0
+            x.kv[1].view(-1, 2, d)[row, 0, 3:7] = torch.tensor(codes, dtype=torch.uint8, device="cuda")
+        op = x.op(flags)
+        check(x, op(), flags == 0)
+        assert op.status() == 0
 
 
 @pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64)])
