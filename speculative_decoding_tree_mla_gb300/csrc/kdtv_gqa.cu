@@ -272,9 +272,7 @@ int launch_simt_t(const GqaArgs& a, cudaStream_t st) {
   const int dk = (a.d + 31) / 32;
   const size_t smem = sizeof(float) * simt_words(a.d);
   auto kern = dk <= 2 ? gqa_simt_kernel<T, C, 2> : dk <= 4 ? gqa_simt_kernel<T, C, 4> : gqa_simt_kernel<T, C, 8>;
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return KDTV_ERR_CUDA;
+  if (allow_smem(kern, smem) != cudaSuccess) return KDTV_ERR_CUDA;
   const dim3 grid((unsigned)a.splits, (unsigned)((a.N * a.G + kRowsCta - 1) / kRowsCta),
                   (unsigned)(a.B * a.Hkv));
   kern<<<grid, kSimtThreads, smem, st>>>(a);

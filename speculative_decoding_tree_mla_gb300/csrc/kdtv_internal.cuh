@@ -201,6 +201,18 @@ __device__ __forceinline__ bool prefix_ok(const Args& a, int b, int* L) {
   return true;
 }
 
+// Lets a kernel whose dynamic shared memory differs from call to call have `bytes` of it.  The limit
+// belongs to the kernel, not to the launch: every call sets the same one (what a CTA can have less
+// 1 KiB for what kernels declare), so that host threads with calls of different sizes do not lower it
+// between each other's setting and launch.
+constexpr size_t kMaxDynamicSmem = 226 * 1024;
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), size_t bytes) {
+  if (bytes <= 47 * 1024) return cudaSuccess;               // the limit that every kernel has
+  if (bytes > kMaxDynamicSmem) return cudaErrorInvalidValue;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynamicSmem);
+}
+
 // Launch with an optional programmatic-dependent-launch attribute: the kernel
 // may begin while the previous kernel of the stream drains, and must call
 // griddepcontrol.wait before touching that kernel's outputs.

@@ -284,13 +284,11 @@ extern "C" int kdtv_compact_kv(const kdtv_dims* d, void* c_kv, void* k_rope,
   if (d->page_size == 0 && d->t_stride < d->N) return KDTV_ERR_INVALID_ARG;
   if (d->page_size > 0 && (d->max_pages <= 0 || d->num_pages <= 0)) return KDTV_ERR_INVALID_ARG;
   const long long W = (long long)d->d_c + d->d_rope;
-  // A chunk of rows in shared memory: over 47 KiB (a GQA cache's keys and
-  // values as the two tensors) by opt-in, up to what a CTA can have.
+  // A chunk of rows in shared memory (a GQA cache's keys and values as the two
+  // tensors: more than a kernel has without asking), up to what a CTA can have.
   const auto opt_in = [](auto kern, size_t bytes) -> int {
-    if (bytes <= 47 * 1024) return KDTV_OK;
-    if (bytes > 227 * 1024 - 1024) return KDTV_ERR_UNSUPPORTED;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
-                   cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+    if (bytes > kMaxDynamicSmem) return KDTV_ERR_UNSUPPORTED;
+    return allow_smem(kern, bytes) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
   };
   int rc;
   if (d->dtype == KDTV_BF16) {
@@ -332,10 +330,7 @@ extern "C" int kdtv_tree_build(int B, int D, int K, int N, const float* logp,
   const int Ds = D < N - 1 ? D : N - 1;
   const size_t sm = (size_t)(N * K + N) * sizeof(unsigned long long) + (size_t)N * 4 * sizeof(int) +
                     (size_t)Ds * K * (sizeof(float) + sizeof(int));
-  if (sm > 48 * 1024 &&
-      cudaFuncSetAttribute(tree_build_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sm) != cudaSuccess)
-    return KDTV_ERR_CUDA;
+  if (allow_smem(tree_build_kernel, sm) != cudaSuccess) return KDTV_ERR_CUDA;
   tree_build_kernel<<<B, kBuildThreads, sm, stream>>>(D, K, N, logp, tokens, root_token, parent,
                                                       token, depth, score, n_nodes);
   return cudaGetLastError() == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;

@@ -298,9 +298,7 @@ cudaError_t launch_typed(const Args& a, const Plan& p, cudaStream_t st, cudaEven
   const int D = a.d_c + a.d_rope;
   size_t sm_attn = sizeof(float) * ((size_t)G * D + (size_t)kKeyTile * (D + 1) +
                                     (size_t)G * kKeyTile + 3 * G);
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, TC>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sm_attn);
+  const cudaError_t e = allow_smem(attn_kernel<T, TC>, sm_attn);
   if (e != cudaSuccess) return e;
   dim3 grid_attn(a.N * ((a.H + G - 1) / G), a.splits, a.B);
   attn_kernel<T, TC><<<grid_attn, kThreads, sm_attn, st>>>(a, G);

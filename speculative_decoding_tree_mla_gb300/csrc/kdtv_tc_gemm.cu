@@ -425,8 +425,7 @@ cudaError_t launch_absorb_tc(const Args& a, cudaStream_t st, bool after_plan) {
       encode_2d(&to, a.q_lat, BNr, (uint64_t)a.H * 512, 64, AB_NR) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const int smem = ab_smem(a.d_nope);
-  cudaError_t e = cudaFuncSetAttribute(absorb_tc_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(absorb_tc_kernel, smem);
   if (e != cudaSuccess) return e;
   // Row blocks per CTA: the (latent block, head) CTAs take every row block
   // unless they leave most of one wave idle; then the row blocks are split
