@@ -449,8 +449,11 @@ int kdtv_gqa_launches_per_call(const kdtv_gqa_dims* dims);
  *   parent     [B, N] int32, as in kdtv_verify_attn, of the live nodes
  *   prefix_len [B], n_nodes [B] int32 (n_nodes may be NULL: N)
  * Scale bytes 1 .. 254 stand for 2^-126 .. 2^127.  On tensor cores a one-byte
- * key's product with a query row scaled to 2^8 is formed before both scales are
- * taken back, so key bytes above 227 (2^100) may overflow a score.
+ * key's product with a query row scaled to 2^15 is formed before both scales are
+ * taken back (the queries count as they are, down to 2^-31 of a row's largest
+ * element), so key bytes above 227 (2^100) may overflow a score; and a weight is
+ * below 2^8, not 1, until the sums are divided, so values above 2^119 may
+ * overflow one.
  * A wait that runs out puts KDTV_ERR_DEVICE_TIMEOUT into *status in place of any
  * other code, and while the word holds it, rows whose keys are spread over
  * several CTAs are not written: clear it before the next call.

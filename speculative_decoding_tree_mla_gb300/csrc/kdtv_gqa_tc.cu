@@ -38,10 +38,15 @@
 // piece is i + max(0, i - lag + 1) and of V_i is i + min(n, i + lag).
 //
 // One-byte caches.  Keys go to the tensor cores as they lie: a query row, scaled
-// by a power of two so that its largest element lies in [2^7, 2^8), is the sum of
-// two E4M3 parts (its eight significant bits; an element's error is at most 2^-17
-// of the row's largest), S = (Qhi + Qlo) K^T costs what bf16 would, and a
-// key's scale multiplies its column of scores in the softmax.  Values: TMA brings
+// by a power of two so that its largest element lies in [2^14, 2^15), is the sum of
+// three E5M2 parts (three significant bits each, of a bf16's eight; exact down
+// to 2^-23 of the row's largest element, and what lies below is off by 2^-31 of
+// it), S = (Q0 + Q1 + Q2) K^T costs 1.5 times what bf16 would, and a key's scale
+// multiplies its column of scores in the softmax.  (Two E4M3 parts had the bits but
+// not the range: elements below 2^-9 of the row's largest lost theirs.  The third
+// costs 391 -> 394 us for 64 requests and 310 -> 327 for 128 nodes over 65536
+// keys, where the rings of raw keys and values gave up a third of their room to
+// it as well.)  Values: TMA brings
 // raw rows into a ring of their own, and four warps widen them to bf16 with the
 // row's power-of-two scale (exact) into the operand ring.  bf16 caches: the same
 // warps touch only the last key tiles, where they zero the value rows behind the
@@ -51,7 +56,7 @@
 //
 // What bounds it (of a measured 1931 TFLOP/s and 6785 GB/s).  Many rows, long
 // prefixes: the tensor cores, 1285 TFLOP/s at 128 nodes x 64 heads over 65536 keys
-// in bf16 (213 us; 1430 from 32768 keys on, the rest is the way in and out) and 907
+// in bf16 (213 us; 1430 from 32768 keys on, the rest is the way in and out) and 839
 // from a one-byte cache, where widening and a two-pass softmax share the issue slots.
 // Few rows: loads in flight and the chain load -> product -> softmax -> product of
 // a tile, 4960 GB/s at one node over 65536 keys, bf16.  Short calls: latency, 13.2
@@ -113,17 +118,20 @@ __device__ __forceinline__ uint32_t arrivals(int i) {
   return 1;
 }
 
+constexpr int kQParts = 3;                  // one-byte keys: E5M2 parts of a query row
+
 template <int D, bool kFp8>
 struct Cfg {
   static constexpr int kTileBytes = kTile * D * 2;            // Q or V tile (bf16 caches: K too) in bf16
   static constexpr int kChunk = kTile * 128;                  // its 64 columns, 128-byte rows
-  static constexpr int kRawBytes = kTile * D;                 // one-byte K or V tile
-  // D = 128: Q 64 KiB, then 5 tiles of 32 KiB, or 2 of widened values, 3 raw ones of 16 KiB and 3
-  // of keys
+  static constexpr int kRawBytes = kTile * D;                 // one-byte K or V tile, part of a Q tile
+  static constexpr int kQBytes = kFp8 ? kQParts * kRawBytes : kTileBytes;   // (bf16 first, then its parts)
+  // D = 128: Q 64 KiB, then 5 tiles of 32 KiB; or Q 96 KiB, 2 tiles of widened values, 2 raw ones
+  // of 16 KiB and 2 of keys
   static constexpr int kSlots = kFp8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 6);
-  static constexpr int kRaw = kFp8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int kRaw = kFp8 ? (D == 128 ? 2 : 6) : 0;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffKV = 2 * kTileBytes;
+  static constexpr int kOffKV = 2 * kQBytes;
   static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
   static constexpr int kOffK = kOffRaw + kRaw * kRawBytes;    // (the key ring has kRaw entries too)
   static constexpr int kOffMisc = kOffK + kRaw * kRawBytes;
@@ -252,22 +260,27 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, E4M3 operands, 32 elements deep, fp32 accumulation.
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, one-byte operands, 32 elements deep, fp32 accumulation.
+__device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile("{\n\t.reg .pred p;\n\t"
                "setp.ne.b32 p, %4, 0;\n\t"
                "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
                :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// A in E5M2, B in E4M3.
+__host__ __device__ constexpr uint32_t idesc_fp8(int M, int N) {
+  return (1u << 4) | (1u << 7) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // Exponent k of a query row's scale 2^k, from the largest finite magnitude of its bf16 bits: the
-// largest element lands in [2^7, 2^8), below E4M3's 448.
+// largest element lands in [2^14, 2^15), below E5M2's 57344.  (bf16's smallest steps, 2^-133, are
+// E5M2's too at 2^127.)
 __device__ __forceinline__ int q_exponent(uint32_t max_bits) {
-  return min(134 - (int)(max_bits >> 7), 120);
+  return min(141 - (int)(max_bits >> 7), 127);
 }
+// A product of such a row and a key is taken back by 2^-kBack before it meets the key's scale, so
+// that scales up to 2^100 leave it finite (448 * 2^15 * 128 terms are below 2^31).
+constexpr int kBack = 7;
 // Largest finite magnitude (bits) of a bf16 pair and one so far.
 __device__ __forceinline__ uint32_t max_finite(uint32_t w, uint32_t m) {
   const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
@@ -275,22 +288,29 @@ __device__ __forceinline__ uint32_t max_finite(uint32_t w, uint32_t m) {
   if (hi < 0x7f80u) m = max(m, hi);
   return m;
 }
-// Four floats as E4M3 high parts and what they leave, as E4M3 too.  A bf16 has eight significant
-// bits, a part four: the two are exact down to 2^-2 (the parts' own steps end at 2^-9), a row's
-// largest element being at least 2^7.  Infinities become NaN, as their scores would.
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  const uint32_t x = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t y = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return x | (y << 16);
+// Four floats as E5M2 bytes, and what the bytes leave of them (exact in fp32).
+__device__ __forceinline__ uint32_t take_e5m2(float (&x)[4]) {
+  uint32_t w = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(x[k], x[k + 1]), __NV_SATFINITE, __NV_E5M2);
+    const float2 g = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E5M2)));
+    x[k] -= g.x;
+    x[k + 1] -= g.y;
+    w |= two << (8 * k);
+  }
+  return w;
 }
-__device__ __forceinline__ void split_e4m3(uint32_t w0, uint32_t w1, float f, uint32_t& hi, uint32_t& lo) {
+// Four bf16 (two words), times f, as E5M2 parts.  A part is nearest what the earlier ones leave, so
+// after the first an element has five bits left, and after the second one.  Infinities become NaN,
+// as their scores would.
+__device__ __forceinline__ void split_e5m2(uint32_t w0, uint32_t w1, float f, uint32_t (&part)[kQParts]) {
   float x[4] = {__uint_as_float(w0 << 16) * f, __uint_as_float(w0 & 0xffff0000u) * f,
                 __uint_as_float(w1 << 16) * f, __uint_as_float(w1 & 0xffff0000u) * f};
 #pragma unroll
   for (int k = 0; k < 4; ++k) x[k] = fabsf(x[k]) < INFINITY ? x[k] : __uint_as_float(0x7fffffffu);
-  hi = pack_e4m3(x[0], x[1], x[2], x[3]);
-  const float2 g0 = widen2(hi & 0xffffu), g1 = widen2(hi >> 16);
-  lo = pack_e4m3(x[0] - g0.x, x[1] - g0.y, x[2] - g1.x, x[3] - g1.y);
+#pragma unroll
+  for (int k = 0; k < kQParts; ++k) part[k] = take_e5m2(x);
 }
 // Zeroes the elements of a bf16 pair that are not finite; true if there were any.
 __device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
@@ -549,7 +569,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           mbar_expect_tx(BAR(B_Q_FULL), bytes * (D / 64) * (two ? 2 : 1));
           for (int s = 0; s < (two ? 2 : 1); ++s)
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + c * C::kChunk, &tm_q, BAR(B_Q_FULL), 64 * c,
+              tma_load_3d(sbase + C::kOffQ + s * C::kQBytes + c * C::kChunk, &tm_q, BAR(B_Q_FULL), 64 * c,
                           kvh * a.G, p.b * a.N + p.node0 + s * a.npt);
         }
         ++q_loads;
@@ -659,7 +679,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     // as the products it then issues take, so the streams' issuers are two warps.  Each waits on
     // every entry of the ring, also the other stream's, so that it sees each phase of the barriers.
     const int s = warp - kWarpMma;
-    constexpr uint32_t kIdescS = kFp8 ? idesc_e4m3(kTile, kTile) : idesc_bf16(kTile, kTile, 0, 0);
+    constexpr uint32_t kIdescS = kFp8 ? idesc_fp8(kTile, kTile) : idesc_bf16(kTile, kTile, 0, 0);
     constexpr uint32_t kIdescO = idesc_bf16(kTile, D, 0, 1);
     // operands at fixed places, as descriptors to which a byte offset / 16 is added
     // (one-byte keys: rows of D bytes, 128- or 64-byte swizzle)
@@ -679,7 +699,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const bool two = p.two();
       const int lag = two ? 1 : 2;
       if (lane != 0) continue;
-      const uint64_t ad = q_desc + (uint32_t)(two ? s * (C::kTileBytes >> 4) : 0);
+      const uint64_t ad = q_desc + (uint32_t)(two ? s * (C::kQBytes >> 4) : 0);
       alive = wait(guard, BAR(kFp8 ? B_Q_READY : B_Q_FULL), index & 1);
       // The streams take turns: a step's products run as one, and beside the other stream's softmax.
       // (Products that share the tensor cores end together, and then so do the softmaxes.)  In a
@@ -737,13 +757,13 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (has_k) {                                          // S_s = Q K^T, over P_s
             const uint64_t bd = k_desc + (uint32_t)(k_slot * ((kFp8 ? C::kRawBytes : C::kTileBytes) >> 4));
             tc_fence_after();
-            if constexpr (kFp8) {                               // the queries' two parts, 32 columns a product
+            if constexpr (kFp8) {                               // the queries' parts, 32 columns a product
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
+              for (int kk = 0; kk < kQParts * D / 32; ++kk) {
                 const uint32_t part = (kk / (D / 32)) * (C::kRawBytes >> 4), off = (kk % (D / 32)) * 2;
-                mma_e4m3(dS, ad + part + off, bd + off, kIdescS, kk > 0);
+                mma_fp8(dS, ad + part + off, bd + off, kIdescS, kk > 0);
                 // the other stream's issuer needs about as long to begin as the rest takes
-                if (kk == D / 32) mbar_arrive(BAR(B_TURN + 1 - s));
+                if (kk == (kQParts - 1) * D / 32) mbar_arrive(BAR(B_TURN + 1 - s));
               }
             } else {
 #pragma unroll
@@ -828,12 +848,12 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         int k1 = ks[at], v1 = vs[at], vm1 = 0, vm2 = 0;    // values: of tiles i + 1 .. i - 2
         int page_next = next_page();
 
-        // Q: each row's two E4M3 parts in place of its bf16 (while the scale bytes arrive)
+        // Q: each row's E5M2 parts over and behind its bf16 (while the scale bytes arrive)
         alive = wait_warp(guard, BAR(B_Q_FULL), index & 1);
         if (!alive) break;
 #pragma unroll 1
         for (int tile = 0; tile < (p.two() ? 2 : 1); ++tile) {
-          const uint32_t q0 = sbase + C::kOffQ + tile * C::kTileBytes, qr = q0 + row * 128;
+          const uint32_t q0 = sbase + C::kOffQ + tile * C::kQBytes, qr = q0 + row * 128;
           uint32_t mxb = 0u;
 #pragma unroll 2
           for (int u = 0; u < D / 8; ++u) {
@@ -841,30 +861,38 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             mxb = max_finite(w.w, max_finite(w.z, max_finite(w.y, max_finite(w.x, mxb))));
           }
           const float f = __uint_as_float((uint32_t)(q_exponent(mxb) + 127) << 23);
-          uint32_t hi[D / 4], lo[D / 4];
+          // Part k lies at k kRawBytes, so the second of a 128-wide row's first half lies over its second
+          // half, which is read before; a 64-wide row's parts lie over other rows.
+          uint4 held[4];
 #pragma unroll
-          for (int u = 0; u < D / 8; ++u) {
-            const uint4 w = lds128(qr + (u >> 3) * C::kChunk + (((u & 7) ^ swz) << 4));
-            split_e4m3(w.x, w.y, f, hi[2 * u], lo[2 * u]);
-            split_e4m3(w.z, w.w, f, hi[2 * u + 1], lo[2 * u + 1]);
-            if (D == 128 && (u & 1) && u < 8)       // 16 bytes of the high part, where both were read
-              sts128(qr + (((u >> 1) ^ swz) << 4), hi[2 * u - 2], hi[2 * u - 1], hi[2 * u], hi[2 * u + 1]);
-          }
-          if (D == 64) {                            // rows of the parts overlap others' rows
-            alive = meet();
-            if (!alive) break;
-          }
+          for (int c = 0; c < D / 64; ++c) {
+            uint4 w[8];
 #pragma unroll
-          for (int u = 0; u < D / 16; ++u) {
-            if (D == 128) {
-              if (u >= 4) sts128(qr + ((u ^ swz) << 4), hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-              sts128(qr + C::kRawBytes + ((u ^ swz) << 4), lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
-            } else {                                // 64-byte rows, chunk c at c ^ ((row >> 1) & 3)
-              const uint32_t at64 = q0 + row * 64 + ((u ^ ((row >> 1) & 3)) << 4);
-              sts128(at64, hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-              sts128(at64 + C::kRawBytes, lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+            for (int u = 0; u < 8; ++u) w[u] = lds128(qr + c * C::kChunk + ((u ^ swz) << 4));
+            if (D == 64) {
+              alive = meet();
+              if (!alive) break;
+            }
+            if (c == 1)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) sts128(qr + C::kRawBytes + ((u ^ swz) << 4), held[u].x, held[u].y, held[u].z, held[u].w);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {           // 16 elements: 16 bytes of each part
+              uint32_t x[4][kQParts];
+              split_e5m2(w[2 * u].x, w[2 * u].y, f, x[0]);
+              split_e5m2(w[2 * u].z, w[2 * u].w, f, x[1]);
+              split_e5m2(w[2 * u + 1].x, w[2 * u + 1].y, f, x[2]);
+              split_e5m2(w[2 * u + 1].z, w[2 * u + 1].w, f, x[3]);
+              // (D = 64: 64-byte rows, chunk u at u ^ ((row >> 1) & 3))
+              const uint32_t at = D == 128 ? qr + (((4 * c + u) ^ swz) << 4) : q0 + row * 64 + ((u ^ ((row >> 1) & 3)) << 4);
+#pragma unroll
+              for (int k = 0; k < kQParts; ++k) {
+                if (D == 128 && c == 0 && k == 1) held[u] = make_uint4(x[0][k], x[1][k], x[2][k], x[3][k]);
+                else sts128(at + k * C::kRawBytes, x[0][k], x[1][k], x[2][k], x[3][k]);
+              }
             }
           }
+          if (!alive) break;
         }
         if (!alive) break;
         fence_async_smem();
@@ -956,7 +984,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (i < n) {
             alive = wait_warp(guard, BAR(B_SCALE_FREE + sring.slot), sring.phase ^ 1u);
             if (!alive) break;
-            scales[sring.slot * kTile + row] = scale_of_byte(k0);
+            scales[sring.slot * kTile + row] = scale_of_byte(k0) * (1.f / (1 << kBack));
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(B_SCALE_FULL + sring.slot));
             sring.next();
@@ -1044,7 +1072,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             mxb = max_finite(w.w, max_finite(w.z, max_finite(w.y, max_finite(w.x, mxb))));
           }
         }
-        row_scale *= __uint_as_float((uint32_t)(127 - q_exponent(mxb)) << 23);
+        row_scale *= __uint_as_float((uint32_t)(127 + kBack - q_exponent(mxb)) << 23);
       }
       float m = -INFINITY, l = 0.f;
       bool first = true, o1_check = s == 1 && one_pieces > 0;

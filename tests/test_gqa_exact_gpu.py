@@ -44,6 +44,41 @@ def check(x, out, tensor_cores):
 
 
 @pytest.mark.parametrize("flags", [0, SIMT], ids=["auto", "simt"])
+@pytest.mark.parametrize("times", [64, 1 << 10, 1 << 14], ids=lambda n: f"x{n}")
+@pytest.mark.parametrize("channel", [0, 0x28], ids=["keys0", "keys_small"])
+@pytest.mark.parametrize("N,H,Hkv,d,page", [(5, 16, 2, 128, 64), (3, 8, 2, 64, 0), (24, 16, 2, 128, 0),
+                                            (70, 8, 2, 64, 16)])
+def test_queries_with_an_outlier(N, H, Hkv, d, page, channel, times, flags):
+    """One channel of every query is `times` the others, and the keys do not tell each other apart in
+    it: the softmax follows the small elements alone.  (0x28 is E4M3's 0.25.)"""
+    x = Case(2, N, H, Hkv, d, "fp8", page, [300, 90], seed=21, sharp=2.0)
+    for s in x.scales:
+        s.fill_(120)
+    x.kv[0].view(-1, Hkv, d)[..., 5] = channel
+    x.q[..., 5] = float(times)
+    op = x.op(flags)
+    check(x, op(), flags == 0)
+    assert op.status() == 0
+
+
+@pytest.mark.parametrize("flags", [0, SIMT], ids=["auto", "simt"])
+@pytest.mark.parametrize("d,page", [(128, 0), (64, 16)])
+def test_queries_over_a_wide_range(d, page, flags):
+    """The elements of a query row spread over 2^14, the keys' over as much the other way, so that all
+    count alike in a score."""
+    x = Case(1, 9, 8, 2, d, "fp8", page, [500], seed=22)
+    e = torch.arange(d, device="cuda") % 14
+    x.q.copy_((x.q.float() * torch.exp2(7.0 - e)).to(x.q.dtype))
+    for s in x.scales:
+        s.fill_(127)
+    k = x.kv[0].view(-1, 2, d)                     # E4M3 exponents 1 .. 14, signs and mantissas as they were
+    k.copy_((k & 0x87) | (8 * (e + 1)).to(torch.uint8))
+    op = x.op(flags)
+    check(x, op(), flags == 0)
+    assert op.status() == 0
+
+
+@pytest.mark.parametrize("flags", [0, SIMT], ids=["auto", "simt"])
 @pytest.mark.parametrize("byte", [247, 250, 254])
 @pytest.mark.parametrize("d,page,prefix", [(128, 0, 20), (128, 16, 700), (64, 16, 61), (64, 0, 700)])
 def test_values_that_overflow(d, page, prefix, byte, flags):
