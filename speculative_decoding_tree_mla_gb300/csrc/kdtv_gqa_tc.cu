@@ -1105,39 +1105,34 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         // bf16 keys: a row's 128 scores stay in registers.  One-byte keys: two passes over them, a
         // chunk at a time; this instance has more roles at work, and their loops together must stay
         // in the SM's instruction cache.
-        constexpr int kChunkCols = 32;
-        float v[kFp8 ? kChunkCols : kTile];
+        float v[kFp8 ? 32 : kTile];
         auto load_chunk = [&](int c) {
-          tmem_ld32(tS + kChunkCols * c, reinterpret_cast<float(&)[32]>(v[0]));
-          if constexpr (kChunkCols == 64) tmem_ld32(tS + kChunkCols * c + 32, reinterpret_cast<float(&)[32]>(v[32]));
+          tmem_ld32(tS + 32 * c, reinterpret_cast<float(&)[32]>(v[0]));
           tmem_wait_ld();
           pin(v);
-          const uint32_t at = sbase + C::kOffScale + ((k_tiles + i) & 1) * (kTile * 4) + c * (kChunkCols * 4);
+          const uint32_t at = sbase + C::kOffScale + ((k_tiles + i) & 1) * (kTile * 4) + c * (32 * 4);
 #pragma unroll
-          for (int k = 0; k < kChunkCols; k += 4) {   // a column's power of two, one for all rows
+          for (int k = 0; k < 32; k += 4) {   // a column's power of two, one for all rows
             const uint4 f = lds128(at + 4 * k);
             const float2 x = mul2(make_float2(v[k], v[k + 1]), make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
             const float2 y = mul2(make_float2(v[k + 2], v[k + 3]), make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
             v[k] = x.x; v[k + 1] = x.y; v[k + 2] = y.x; v[k + 3] = y.y;
           }
           if (masked) {                          // dropped, whatever it is: a masked score may be NaN
+            const uint32_t see = gqa_visible(path, t0 + 32 * c, p.L);
 #pragma unroll
-            for (int h = 0; h < kChunkCols / 32; ++h) {
-              const uint32_t see = gqa_visible(path, t0 + kChunkCols * c + 32 * h, p.L);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[32 * h + k] = (see >> k) & 1u ? v[32 * h + k] : -INFINITY;
-            }
+            for (int k = 0; k < 32; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
           }
         };
         float mx = -INFINITY;
         if constexpr (kFp8) {
 #pragma unroll 1
-          for (int c = 0; c < kTile / kChunkCols; ++c) {
+          for (int c = 0; c < 4; ++c) {
             load_chunk(c);
             float mc[4] = {mx, v[0], v[1], v[2]};
 #pragma unroll
-            for (int k = 3; k + 1 < kChunkCols; k += 2) mc[(k / 2) & 3] = max3(mc[(k / 2) & 3], v[k], v[k + 1]);
-            mx = max3(max3(mc[0], mc[1], mc[2]), mc[3], v[kChunkCols - 1]);
+            for (int k = 3; k + 1 < 32; k += 2) mc[(k / 2) & 3] = max3(mc[(k / 2) & 3], v[k], v[k + 1]);
+            mx = max3(max3(mc[0], mc[1], mc[2]), mc[3], v[31]);
           }
         } else {
 #pragma unroll
@@ -1215,12 +1210,10 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         };
         if constexpr (kFp8) {
 #pragma unroll 1
-          for (int c = 0; c < kTile / kChunkCols; ++c) {
+          for (int c = 0; c < 4; ++c) {
             load_chunk(c);
-#pragma unroll
-            for (int h = 0; h < kChunkCols / 32; ++h)
-              weights(reinterpret_cast<const float(&)[32]>(v[32 * h]), c * (kChunkCols / 32) + h);
-            if (c == kTile / kChunkCols / 2 - 1) half_ready();
+            weights(reinterpret_cast<const float(&)[32]>(v[0]), c);
+            if (c == 1) half_ready();
           }
           if (lane == 0)                         // the scales' place: two streams arrive, or one twice
             for (int k = 0; k < (two ? 1 : 2); ++k) mbar_arrive(BAR(B_SCALE_FREE + ((k_tiles + i) & 1)));

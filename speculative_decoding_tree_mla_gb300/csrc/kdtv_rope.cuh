@@ -119,21 +119,11 @@ __device__ __forceinline__ void store_v(__nv_fp8_e4m3* p, const float (&x)[V]) {
 __device__ __forceinline__ float2 widen2(uint32_t two) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
 }
+// (16 bytes at a time are widened by their reader.)
 template <int V>
 __device__ __forceinline__ void load_v(const __nv_fp8_e4m3* p, float (&x)[V]) {
-  if constexpr (V == 8) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    const uint32_t u[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = widen2(u[k]);
-      x[2 * k] = f.x;
-      x[2 * k + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = to_f32(p[k]);
-  }
+  static_assert(V == 1, "one byte");
+  x[0] = to_f32(*p);
 }
 
 // n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
