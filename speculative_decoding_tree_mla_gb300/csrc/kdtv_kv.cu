@@ -528,6 +528,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const __grid_const
   }
 }
 
+// SMs of the current device (a GB300's, where there is none).
+long long sms() { return device_sm_count() > 0 ? device_sm_count() : 152; }
 bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool multiple(const long long (&s)[3], int v) { return s[0] % v == 0 && s[1] % v == 0 && s[2] % v == 0; }
 // Element strides; {0, 0, 0} is contiguous.
@@ -554,7 +556,8 @@ int launch_rope(const kdtv_rope_table& tab, RopeArgs& a, int dim, cudaStream_t s
   // but threads come first.  (64 heads, 8000 rows: 4 heads 90 us, 8 82, 16 76.)
   const long long threads = (long long)a.rows * (a.rot_items + a.copy_items) * a.H;
   a.heads = 1;
-  while (a.heads < 16 && a.heads < a.H && threads / (2 * a.heads) >= 152ll * 1024) a.heads *= 2;
+  const long long enough = sms() * 1024;
+  while (a.heads < 16 && a.heads < a.H && threads / (2 * a.heads) >= enough) a.heads *= 2;
   a.hgroups = (a.H + a.heads - 1) / a.heads;
   const long long per = (long long)a.rows * a.hgroups;
   const long long rot_blocks = (per * a.rot_items + kThreads - 1) / kThreads;
@@ -590,9 +593,10 @@ cudaError_t launch_append(const kdtv_rope_table& tab, KvArgs& a, cudaStream_t st
   // A few rows are spread over more blocks by heads; many rows get spans of them, about eight
   // blocks an SM in all.
   const int rows_turn = kThreads / lanes;                    // rows a block has at a time
+  const long long n_sms = sms();
   a.hgroups = 1;
-  while (2 * a.hgroups <= heads && (long long)a.B * a.N * a.hgroups * lanes < 152ll * 1024) a.hgroups *= 2;
-  long long blocks = 8ll * 152 / ((long long)a.B * a.parts * a.hgroups);
+  while (2 * a.hgroups <= heads && (long long)a.B * a.N * a.hgroups * lanes < n_sms * 1024) a.hgroups *= 2;
+  long long blocks = 8 * n_sms / ((long long)a.B * a.parts * a.hgroups);
   blocks = blocks < 1 ? 1 : blocks;
   const int span = (int)(((a.N + blocks - 1) / blocks + rows_turn - 1) / rows_turn * rows_turn);
   const dim3 grid((unsigned)((a.N + span - 1) / span * a.hgroups), (unsigned)a.B, (unsigned)a.parts);
@@ -622,7 +626,7 @@ cudaError_t launch_read(KvArgs& a, cudaStream_t st) {
     p.by_dim = divisor((unsigned)p.dim);
   }
   const long long total = a.N * (width / (vec ? kWide : 1)), turn = 4 * kThreads;
-  long long blocks = 12ll * 152 / ((long long)a.B * a.parts);
+  long long blocks = 12 * sms() / ((long long)a.B * a.parts);
   blocks = blocks < 1 ? 1 : blocks;
   const long long span = ((total + blocks - 1) / blocks + turn - 1) / turn * turn;
   const dim3 grid((unsigned)((total + span - 1) / span), (unsigned)a.B, (unsigned)a.parts);
