@@ -118,3 +118,49 @@ def test_a_wait_that_runs_out_behind_another_error(cache, d):
         again = x.op()
         x.check(again(), True)
         assert again.status() == 0
+
+
+HEADS = [
+    # B, N, H, Hkv, d, cache, page, prefix, n_nodes: blocks of 8, 6, 3 and 1 key heads
+    (2, 5, 16, 16, 128, "bf16", 64, [300, 20], [5, 3]),
+    (1, 1, 32, 32, 128, "bf16", 64, [700], None),
+    (2, 20, 96, 12, 64, "bf16", 0, [129, 0], [20, 1]),
+    (1, 40, 72, 9, 128, "bf16", 16, [250], None),
+    (3, 3, 22, 11, 64, "bf16", 32, [5, 400, 60], [3, 0, 2]),
+    (2, 5, 16, 16, 128, "fp8", 16, [300, 20], None),
+    (1, 10, 48, 24, 64, "fp8", 0, [513], None),
+    (35, 2, 32, 16, 128, "bf16", 16, list(range(0, 350, 10)), None),
+]
+
+
+@pytest.mark.parametrize("c", HEADS, ids=lambda c: "-".join(map(str, c[:7])))
+def test_many_key_heads(c):
+    """More key heads than a group of CTAs takes side by side: several blocks of heads per request."""
+    x = Case(*c, seed=25)
+    op = x.op()
+    out = op()
+    assert op.status() == 0
+    check(x, out, True)
+
+
+@pytest.mark.parametrize("cache,page", [("bf16", 0), ("bf16", 64), ("fp8", 64)])
+@pytest.mark.parametrize("N,H,Hkv", [(1, 32, 32), (30, 48, 12), (7, 64, 16)])
+def test_many_key_heads_in_long_ragged_batches(N, H, Hkv, cache, page):
+    """The same, cut into many pieces: tensor cores against the CUDA cores.  Both round the output
+    (2^-8 each); the weights' rounding, 2^-8, meets A = attention over |v|."""
+    rng = np.random.default_rng([26, N, H])
+    B = 7
+    prefix, n = rng.integers(1, 4000, size=B), rng.integers(0, N + 1, size=B)
+    n[0] = N
+    x = Case(B, N, H, Hkv, 128, cache, page, prefix, n, seed=27, sharp=2.0, fill=float("nan"))
+    got, want = x.op(), x.op(SIMT)
+    g, w = got().float(), want().float()
+    assert got.status() == 0 and want.status() == 0
+    if cache == "fp8":
+        x.kv[1] &= 0x7F
+    else:
+        x.kv[1].abs_()
+    a = x.op(SIMT)().float()
+    assert torch.isfinite(g).all() and torch.isfinite(w).all()
+    tol = 2.0 ** -8 * (w.abs() * 2 + a * (1 + 2.0 ** -7)) + 2.0 ** -10 * a
+    assert ((g - w).abs() <= tol).all(), ((g - w).abs() / tol).max()
