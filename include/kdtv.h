@@ -314,7 +314,9 @@ typedef struct kdtv_rope_config {
   double factor;        /* >= 1 (ignored by PLAIN)                                 */
   double beta_fast;     /* YARN; <= 0 selects 32                                   */
   double beta_slow;     /* YARN; <= 0 selects 1                                    */
-  double attn_factor;   /* YARN; <= 0 selects 0.1 ln(factor) + 1                   */
+  double attn_factor;   /* YARN; <= 0 selects 0.1 ln(factor) + 1.  Give 1 where the
+                           model puts its factor into the softmax scale, as
+                           DeepSeek and Kimi models do                             */
 } kdtv_rope_config;
 
 /* Filled once by kdtv_rope_init (host memory; passed to kernels by value). */
@@ -445,7 +447,9 @@ int kdtv_gqa_launches_per_call(const kdtv_gqa_dims* dims);
  *   k, v       the caches, [B, t_stride, H_kv, d] or [num_pages, page_size,
  *              H_kv, d]; 16-byte aligned
  *   k_scale, v_scale  KDTV_BF16_FP8KV: [rows, H_kv] exponent bytes as
- *              kdtv_kv_append writes them; else NULL
+ *              kdtv_kv_append writes them; else NULL.  (A cache that was written
+ *              without them, value = fp8 * kv_scale: bytes of 127, `scale` times
+ *              kv_scale, and out times kv_scale.)
  *   parent     [B, N] int32, as in kdtv_verify_attn, of the live nodes
  *   prefix_len [B], n_nodes [B] int32 (n_nodes may be NULL: N)
  * Scale bytes 1 .. 254 stand for 2^-126 .. 2^127.  On tensor cores a one-byte

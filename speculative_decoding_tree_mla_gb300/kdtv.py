@@ -417,7 +417,10 @@ def _on(stream):
 class RopeTable:
     """Rotary frequencies (kdtv_rope_init): `rot_dim` rotated elements per head, pairs
     (j, j + rot_dim / 2) ("half") or (2j, 2j + 1) ("interleaved"); `scaling` "none", "linear",
-    "ntk" or "yarn" for long contexts."""
+    "ntk" or "yarn" for long contexts.
+
+    "yarn" also multiplies what it rotates by attn_factor, 0.1 ln(factor) + 1 unless given.  Give 1
+    where the model puts its factor into the softmax scale (DeepSeek and Kimi models do)."""
 
     def __init__(self, rot_dim, *, layout="half", base=10000.0, scaling="none", factor=1.0,
                  orig_ctx=0, beta_fast=0.0, beta_slow=0.0, attn_factor=0.0):
@@ -613,8 +616,9 @@ class GqaVerifyAttn(_Bound):
 
     q, out: [B, N, H, d]; k, v: the caches, [B, T, H_kv, d] or (with page_table [B, max_pages])
     [num_pages, page_size, H_kv, d]; float32 or bfloat16, the caches also one byte per element
-    with exponent bytes k_scale, v_scale (the caches' shape without d).  Holds the workspace:
-    calls of one object must not overlap on the GPU.  status() reads the status word.
+    with exponent bytes k_scale, v_scale (the caches' shape without d; for a cache that was written
+    with one kv_scale: bytes of 127, `scale` times kv_scale, and the result times kv_scale).  Holds
+    the workspace: calls of one object must not overlap on the GPU.  status() reads the status word.
     """
 
     def __init__(self, q, k, v, parent, prefix_len, *, n_nodes=None, page_table=None, k_scale=None,

@@ -164,3 +164,25 @@ def test_many_key_heads_in_long_ragged_batches(N, H, Hkv, cache, page):
     assert torch.isfinite(g).all() and torch.isfinite(w).all()
     tol = 2.0 ** -8 * (w.abs() * 2 + a * (1 + 2.0 ** -7)) + 2.0 ** -10 * a
     assert ((g - w).abs() <= tol).all(), ((g - w).abs() / tol).max()
+
+
+@pytest.mark.parametrize("flags", [0, SIMT], ids=["auto", "simt"])
+@pytest.mark.parametrize("kv_scale", [0.07, 2.0 ** -5])
+def test_a_cache_written_with_one_scale(kv_scale, flags):
+    """Per-head rows written without scale bytes: bytes of 127, the softmax scale and the result times
+    kv_scale.  (fp32 products with kv_scale: 2^-24 more of a value, a key and the result each.)"""
+    B, N, H, Hkv, d, T = 2, 6, 8, 2, 64, 200
+    rng = np.random.default_rng(28)
+    rows = [torch.from_numpy(rng.standard_normal((B, T, Hkv, d), dtype=np.float32)).cuda() for _ in range(2)]
+    K, V = (torch.zeros((B, T, Hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    st = kdtv.kv_append([kdtv.KvPart(c, src=x) for c, x in zip((K, V), rows)], None, kv_scale=kv_scale)
+    back = [torch.zeros_like(x) for x in rows]
+    st2 = kdtv.kv_read([kdtv.KvPart(c, out=x) for c, x in zip((K, V), back)], kv_scale=kv_scale)
+    assert int(st.item()) == int(st2.item()) == 0
+    x = Case(B, N, H, Hkv, d, "fp8", 0, [T - N, 31], seed=29)
+    one = torch.full((B, T, Hkv), 127, dtype=torch.uint8, device="cuda")
+    out, status = kdtv.gqa_verify_attn(x.q, K, V, torch.from_numpy(x.parent).cuda(), torch.from_numpy(x.prefix).cuda(),
+                                       k_scale=one, v_scale=one, scale=d ** -0.5 * kv_scale, flags=flags)
+    assert int(status.item()) == 0
+    x.gathered = lambda: [t.cpu().double().numpy() for t in back]
+    check(x, out.float() * kv_scale, flags == 0)
