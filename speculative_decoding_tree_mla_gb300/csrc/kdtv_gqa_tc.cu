@@ -54,14 +54,15 @@
 // 0, noting the keys: 0 * inf must not reach nodes that do not see them.  The
 // epilogue adds them back to the rows that do.
 //
-// What bounds it (of a measured 1931 TFLOP/s and 6785 GB/s).  Many rows, long
-// prefixes: the tensor cores, 1285 TFLOP/s at 128 nodes x 64 heads over 65536 keys
-// in bf16 (213 us; 1430 from 32768 keys on, the rest is the way in and out) and 839
-// from a one-byte cache, where widening and a two-pass softmax share the issue slots.
-// Few rows: loads in flight and the chain load -> product -> softmax -> product of
-// a tile, 4960 GB/s at one node over 65536 keys, bf16.  Short calls: latency, 13.2
-// us for one token over 4096 keys, of which planning takes 2 and the combine
-// kernel 4.  Measured and not kept: a two-pass softmax for bf16 (284 us
+// What bounds it (of a measured 1931 TFLOP/s and 6785 GB/s; eight calls in a graph).
+// Many rows, long prefixes: the tensor cores, 1280 TFLOP/s at 128 nodes x 64 heads
+// over 65536 keys in bf16 (215 us; 1415 between 32768 and 65536 keys, the rest is
+// the way in and out; 1155 in a long row of calls, at the card's power limit) and
+// 840 from a one-byte cache, where widening and a two-pass softmax share the issue
+// slots.  Few rows: loads in flight and the chain load -> product -> softmax ->
+// product of a tile, 5090 GB/s at one node over 65536 keys, bf16.  Short calls:
+// latency, 13.0 us for one token over 4096 keys, of which planning takes 2 and the
+// combine kernel 4.  Measured and not kept: a two-pass softmax for bf16 (284 us
 // where one pass took 258); 64 columns at a time for one-byte keys (447 us where 32
 // took 432: instruction cache); issuing loops rolled up (474 for 432); prefetching
 // scales to L2.
@@ -1470,8 +1471,9 @@ int launch_t(const GqaArgs& a, bool stall, cudaStream_t st) {
 
 }  // namespace
 
-// Wherever these shapes allow it: from one node over 32 keys (9.0 us, CUDA cores 15.0) and 1024
-// requests of 64 keys (304, 359) to 256 requests of 1024 (194, 1003) the CUDA cores were never ahead.
+// Wherever these shapes allow it: from one node over 32 keys (9.1 us, CUDA cores 15.0; one byte 12.5,
+// 16.8) and 1024 requests of 64 keys (301, 359; 451, 479) to 256 requests of 1024 (191, 1003; 275,
+// 1463) the CUDA cores were never ahead.
 int gqa_tc_supported(const kdtv_gqa_dims* d) {
   if (d->dtype != KDTV_BF16 && d->dtype != KDTV_BF16_FP8KV) return 0;
   if (d->d != 64 && d->d != 128) return 0;
