@@ -77,7 +77,9 @@ enum kdtv_status {
   KDTV_ERR_DEVICE_TIMEOUT = 5,  /* device: a bounded wait ran out                 */
   KDTV_ERR_BAD_PREFIX = 6,      /* device: prefix_len[b] < 0 or L_b + N exceeds
                                    t_stride / max_pages * page_size               */
-  KDTV_ERR_BAD_PAGE = 7         /* device: a page id outside [0, num_pages)       */
+  KDTV_ERR_BAD_PAGE = 7,        /* device: a page id outside [0, num_pages)       */
+  KDTV_ERR_NO_PAGES = 8,        /* device: the free list holds too few pages      */
+  KDTV_ERR_BAD_ADAPTER = 9      /* device: an adapter index outside [-1, adapters) */
 };
 
 /* kdtv_dims.flags */
@@ -475,6 +477,139 @@ int kdtv_gqa_verify_attn(const kdtv_gqa_dims* dims, const void* q, const void* k
                          const int32_t* prefix_len, const int32_t* n_nodes,
                          const int32_t* page_table, void* out, unsigned int* status,
                          cudaStream_t stream);
+
+/* ---- between the attention calls: pages, norms, shared projections -----------------------
+ * The conventions of the calls above: row i of request b, i < N, is live if i <
+ * n_live[b] (NULL: all rows; values outside [0, N] are clamped), and what is
+ * not live is neither read for a result nor written.
+ */
+
+/* Elements that share an exponent byte in one-byte activations and weights. */
+#define KDTV_GROUP 32
+
+typedef struct kdtv_norm_args {
+  int32_t B, N, H;      /* requests, rows per request, heads (1: whole rows)       */
+  int32_t dim;          /* elements of a head: what one norm is taken over         */
+  int32_t dtype;        /* KDTV_F32 or KDTV_BF16: x, residual, residual_out, weight */
+  int32_t out_dtype;    /* dtype, or KDTV_BF16_FP8KV: E4M3 bytes with exponent bytes */
+  float eps;            /* >= 0                                                    */
+  float weight_offset;  /* added to every weight (1 for models that store w - 1)   */
+  int64_t x_stride[3];  /* elements between requests, rows, heads (the last        */
+  int64_t r_stride[3];  /* dimension is contiguous); {0, 0, 0}: contiguous.  r:    */
+  int64_t ro_stride[3]; /* residual, ro: residual_out                              */
+  int64_t y_stride[3];
+} kdtv_norm_args;
+
+/*
+ * kdtv_rmsnorm — the residual's addition and the root-mean-square norm:
+ *   h = x + residual;  residual_out = h;  y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)
+ *   x             [B, N, H, dim]
+ *   residual      [B, N, H, dim] or NULL (h = x)
+ *   residual_out  [B, N, H, dim] or NULL (not kept); with a residual only
+ *   weight        [dim] or NULL (ones; weight_offset is then ignored)
+ *   y             [B, N, H, dim]
+ *   y_scale       out_dtype KDTV_BF16_FP8KV: [B, N, H, dim / 32] exponent bytes, contiguous, as
+ *                 kdtv_project reads them: value = fp8 * 2^(byte - 127), the exponent e = byte -
+ *                 127 of 32 elements the smallest with max|y| <= 448 * 2^e over the finite ones,
+ *                 clamped to [-117, 119]; larger magnitudes and infinities become +-448, NaN
+ *                 stays NaN.  (dim must be a multiple of 32.)  Else NULL.
+ *   n_live        [B] int32 or NULL
+ * Computed in fp32 from the unrounded sum; each output is rounded once.  A squared row
+ * beyond fp32's range gives zeros, as the formula does.  y and residual_out may be x or
+ * residual (the same strides and element size); other overlaps are not allowed.
+ * dim <= 32768.
+ */
+int kdtv_rmsnorm(const kdtv_norm_args* args, const void* x, const void* residual,
+                 void* residual_out, const void* weight, void* y, uint8_t* y_scale,
+                 const int32_t* n_live, cudaStream_t stream);
+
+typedef struct kdtv_project_dims {
+  int32_t B, N;         /* requests, rows per request                              */
+  int32_t d_in, d_out;
+  int32_t dtype;        /* KDTV_F32: everything fp32, on CUDA cores; KDTV_BF16;
+                           KDTV_BF16_FP8KV: x and W E4M3 bytes with exponent bytes
+                           per 32 elements, y, A and Bm bf16 (d_in a multiple of 32) */
+  int32_t adapters;     /* adapters in A and Bm, <= KDTV_MAX_ADAPTERS; 0: none     */
+  int32_t rank;         /* of every adapter (lower ones padded with zeros), 1..256 */
+  uint32_t flags;       /* KDTV_FLAG_SIMT, KDTV_FLAG_TEST_STALL                    */
+  int64_t x_stride[2];  /* elements between requests and rows ({0, 0}: contiguous; */
+  int64_t y_stride[2];  /* one-byte x: contiguous)                                 */
+  void* workspace;      /* >= kdtv_project_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} kdtv_project_dims;
+
+#define KDTV_MAX_ADAPTERS 4096
+
+/* Bytes of workspace kdtv_project needs for these dims on the current device;
+ * 0 if the dims are invalid. */
+size_t kdtv_project_workspace_size(const kdtv_project_dims* dims);
+
+/*
+ * kdtv_project — a projection that all requests share, and beside it the
+ * low-rank adapter of each request:
+ *   y[b,i] = W x[b,i] + s_a Bm_a (A_a x[b,i]),  a = adapter[b]  (-1: W x alone)
+ *   x          [B, N, d_in];  x_scale [B, N, d_in / 32] (one-byte x, else NULL)
+ *   W          [d_out, d_in], contiguous;  W_scale [d_out, d_in / 32]
+ *   A          [adapters, rank, d_in], Bm [adapters, d_out, rank], contiguous
+ *   adapter_scale  [adapters] float32 or NULL (ones)
+ *   adapter    [B] int32, -1 .. adapters - 1, or NULL (no request has one)
+ *   n_live     [B] int32 or NULL
+ *   y          [B, N, d_out] fp32 or bf16 (one-byte x: bf16); no overlap with the inputs
+ * Sums in fp32, rounded once.  An adapter reaches the rows of its requests
+ * only, whatever values it holds.  Rows that are not live, and the rows of a
+ * request whose adapter index is out of range (*status =
+ * KDTV_ERR_BAD_ADAPTER), are left as they were.  Exponent bytes 1 .. 254 stand
+ * for 2^-126 .. 2^127.  bf16 with d_in and rank multiples of 8, 16-byte
+ * aligned pointers and x rows, and one-byte inputs with 16-byte aligned
+ * pointers and rank a multiple of 8, run on tensor cores, everything else
+ * (and KDTV_FLAG_SIMT) in fp32 on CUDA cores.
+ * *status: a device word that the caller clears; the first error stays, but a
+ * wait that ran out (KDTV_ERR_DEVICE_TIMEOUT) replaces it.
+ */
+int kdtv_project(const kdtv_project_dims* dims, const void* x, const uint8_t* x_scale,
+                 const void* W, const uint8_t* W_scale, const void* A, const void* Bm,
+                 const float* adapter_scale, const int32_t* adapter, const int32_t* n_live,
+                 void* y, unsigned int* status, cudaStream_t stream);
+
+/* Kernels kdtv_project launches for these dims, or -1. */
+int kdtv_project_launches_per_call(const kdtv_project_dims* dims);
+
+typedef struct kdtv_pages_dims {
+  int32_t B, N;         /* requests (<= KDTV_MAX_POOL_REQUESTS); rows per request
+                           behind the prefix, >= 0                                 */
+  int32_t page_size;    /* rows per page, > 0                                      */
+  int32_t max_pages;    /* length of each page_table row                           */
+  int32_t num_pages;    /* pages of the pool, length of free_pages                 */
+} kdtv_pages_dims;
+
+#define KDTV_MAX_POOL_REQUESTS 8192
+
+/*
+ * kdtv_pages_resize — block tables from the requests' lengths.  Request b is
+ * to hold ceil((prefix_len[b] + n_live[b]) / page_size) pages: what it has
+ * beyond goes back to the free list, what it lacks is taken from there.
+ *   prefix_len  [B] int32 >= 0;  n_live [B] int32 or NULL (N; clamped to [0, N])
+ *   free_pages  [num_pages] int32, a stack whose first *free_count entries are
+ *               free (a new pool: all ids in any order, *free_count = num_pages)
+ *   n_pages     [B] int32, pages that each request holds (a new pool: 0)
+ *   page_table  [B, max_pages] int32; entries given back become -1
+ *   slots       [B, N] int64 or NULL: cache row page * page_size + offset of
+ *               row prefix_len[b] + i; -1 where i is not live, the request's
+ *               pages do not hold its rows, or the page id is out of range
+ * Pages go back first, from the last request to the first and from each one's
+ * end, and are taken from the top of the stack by the requests in order: a
+ * resize followed by the one back restores the stack.  All of it is
+ * deterministic.  A request whose rows exceed max_pages (or whose prefix is
+ * negative) keeps its pages (KDTV_ERR_BAD_PREFIX), and so does one whose
+ * n_pages or returned page ids are out of range, and every request where
+ * *free_count is (KDTV_ERR_BAD_PAGE).  Where the free list runs out, the request
+ * that it does not suffice for and all behind it that need pages keep what
+ * they have (KDTV_ERR_NO_PAGES).  Requests must not share pages.
+ */
+int kdtv_pages_resize(const kdtv_pages_dims* dims, const int32_t* prefix_len,
+                      const int32_t* n_live, int32_t* free_pages, int32_t* free_count,
+                      int32_t* n_pages, int32_t* page_table, int64_t* slots,
+                      unsigned int* status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

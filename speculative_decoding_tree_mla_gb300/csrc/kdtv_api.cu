@@ -268,6 +268,8 @@ extern "C" const char* kdtv_strerror(int s) {
     case KDTV_ERR_DEVICE_TIMEOUT: return "KDTV_ERR_DEVICE_TIMEOUT";
     case KDTV_ERR_BAD_PREFIX: return "KDTV_ERR_BAD_PREFIX";
     case KDTV_ERR_BAD_PAGE: return "KDTV_ERR_BAD_PAGE";
+    case KDTV_ERR_NO_PAGES: return "KDTV_ERR_NO_PAGES";
+    case KDTV_ERR_BAD_ADAPTER: return "KDTV_ERR_BAD_ADAPTER";
     default: return "KDTV_ERR_UNKNOWN";
   }
 }

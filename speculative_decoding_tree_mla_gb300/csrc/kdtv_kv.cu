@@ -207,12 +207,6 @@ __device__ __forceinline__ void reduce_group(float (&mx)[J], int group) {
 #pragma unroll
       for (int j = 0; j < J; ++j) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
 }
-// The smallest e with mx <= 448 * 2^e = 1.75 * 2^(e + 8), from mx's bits.
-__device__ __forceinline__ int exponent_of(float mx) {
-  const uint32_t bits = __float_as_uint(mx);
-  const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-  return max(-117, min(119, e));
-}
 
 // A lane's elements of one head's row as they are to be rounded; mx: the row's largest finite
 // magnitude.  2^-e is a power of two, so x * 2^-e loses nothing; a power also makes a code's value

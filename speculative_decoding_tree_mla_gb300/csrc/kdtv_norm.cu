@@ -1,0 +1,222 @@
+// kdtv_rmsnorm: the residual's addition and the root-mean-square norm of rows,
+// to the inputs' type or to E4M3 bytes with an exponent byte per 32 elements.
+
+#include "kdtv_rope.cuh"
+
+#include <math.h>
+#include <string.h>
+
+namespace kdtv {
+namespace {
+
+struct NormArgs {
+  unsigned rows;                 // B * N * H
+  int N, dim, chunks;            // chunks of V elements in a row
+  const void *x, *residual, *weight;
+  void *residual_out, *y;
+  uint8_t* y_scale;
+  const int32_t* n_live;
+  float eps, weight_offset;
+  long long xs[3], rs[3], ros[3], ys[3];
+  Divisor by_heads, by_N;
+  int H, per_row, rows_block;    // threads of a row, rows of a block
+};
+
+// h = x + r stays in registers: x and r are read once, all of a row's loads
+// are under way together, and the second pass (scale and round) reads nothing
+// but the weights, which L1 or L2 holds.  A row has a part of a warp, or a
+// block; a thread has CH chunks of V elements, per_row chunks apart, so that
+// a warp's accesses are whole lines.
+// Bound by DRAM where there are rows enough, else by the latency of one load,
+// one reduction and one store.
+// The statistics are fp32; y is (h * (1 / sqrt(mean + eps))) * w, each step
+// rounded to fp32, and rounded once more to its type.
+template <typename T, typename O, int V, int CH>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+  const int row_in = threadIdx.x / a.per_row, t = threadIdx.x - row_in * a.per_row;
+  const unsigned r = blockIdx.x * (unsigned)a.rows_block + row_in;
+  const unsigned bi = divide(min(r, a.rows - 1), a.by_heads), head = min(r, a.rows - 1) - bi * a.H;
+  const unsigned b = divide(bi, a.by_N), i = bi - b * a.N;
+  const bool live = r < a.rows && (int)i < live_rows(a.n_live, b, a.N);
+
+  float h[CH][V];
+  const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + i * a.xs[1] + head * a.xs[2];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int at = c * a.per_row + t;
+#pragma unroll
+    for (int k = 0; k < V; ++k) h[c][k] = 0.f;
+    if (live && at < a.chunks) load_v<V>(x + (long long)at * V, h[c]);
+  }
+  if (a.residual) {
+    const T* res = static_cast<const T*>(a.residual) + b * a.rs[0] + i * a.rs[1] + head * a.rs[2];
+    T* out = static_cast<T*>(a.residual_out) + b * a.ros[0] + i * a.ros[1] + head * a.ros[2];
+    float u[CH][V];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = c * a.per_row + t;
+#pragma unroll
+      for (int k = 0; k < V; ++k) u[c][k] = 0.f;
+      if (live && at < a.chunks) load_v<V>(res + (long long)at * V, u[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = c * a.per_row + t;
+#pragma unroll
+      for (int k = 0; k < V; ++k) h[c][k] += u[c][k];
+      if (a.residual_out && live && at < a.chunks) store_v<V>(out + (long long)at * V, h[c]);
+    }
+  }
+
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    float part = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) part = fmaf(h[c][k], h[c][k], part);
+    sum += part;
+  }
+  const int lanes = min(a.per_row, 32);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (a.per_row > 32) {                               // one row in the block
+    __shared__ float part[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    sum = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  const float inv = 1.f / sqrtf(sum / (float)a.dim + a.eps);
+
+  const T* weight = static_cast<const T*>(a.weight);
+  O* y = static_cast<O*>(a.y) + b * a.ys[0] + i * a.ys[1] + head * a.ys[2];
+  uint8_t* scale = a.y_scale + (long long)min(r, a.rows - 1) * (a.dim / KDTV_GROUP);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int at = c * a.per_row + t;
+    const bool on = live && at < a.chunks;
+    if (weight && at < a.chunks) {
+      float w[V];
+      load_v<V>(weight + at * V, w);
+#pragma unroll
+      for (int k = 0; k < V; ++k) h[c][k] = h[c][k] * inv * (w[k] + a.weight_offset);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) h[c][k] *= inv;
+    }
+    if constexpr (sizeof(O) == 1) {                   // 32 / V lanes share an exponent
+      float mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < V; ++k) mx = fabsf(h[c][k]) < INFINITY ? fmaxf(mx, fabsf(h[c][k])) : mx;
+#pragma unroll
+      for (int o = 1; o < KDTV_GROUP / V; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const int e = exponent_of(mx);
+      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int k = 0; k < V; ++k) h[c][k] *= f;
+      if (on && at % (KDTV_GROUP / V) == 0) scale[at / (KDTV_GROUP / V)] = (uint8_t)(e + 127);
+    }
+    if (on) store_v<V>(y + (long long)at * V, h[c]);
+  }
+}
+
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool multiple(const long long (&s)[3], int v) { return s[0] % v == 0 && s[1] % v == 0 && s[2] % v == 0; }
+void strides(const int64_t (&in)[3], long long N, long long H, long long dim, long long (&out)[3]) {
+  const bool given = in[0] || in[1] || in[2];
+  out[0] = given ? in[0] : N * H * dim;
+  out[1] = given ? in[1] : H * dim;
+  out[2] = given ? in[2] : dim;
+}
+bool same(const long long (&s)[3], const long long (&t)[3]) { return s[0] == t[0] && s[1] == t[1] && s[2] == t[2]; }
+
+template <typename T, typename O, int V>
+int launch_v(NormArgs& a, cudaStream_t st) {
+  a.chunks = a.dim / V;
+  // Threads of a row: four chunks each (32 where a chunk is one element), or one each where the rows
+  // are too few to fill the device.
+  constexpr int most = V == 1 ? 32 : 4, some = V == 1 ? 8 : 4;
+  const int least = sizeof(O) == 1 ? KDTV_GROUP / V : 1;       // lanes that share an exponent stay together
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
+  int ch = a.rows <= 2u * sms ? 1 : some;
+  while ((a.chunks + ch - 1) / ch > 1024) ch *= 2;
+  if (ch > most) return KDTV_ERR_UNSUPPORTED;
+  int per = (a.chunks + ch - 1) / ch;
+  if (per > 32) {
+    per = (per + 31) / 32 * 32;
+    a.rows_block = 1;
+  } else {
+    int p = least;
+    while (p < per) p *= 2;
+    per = p;
+    a.rows_block = (a.rows <= 2u * sms ? 32 : 256) / per;
+  }
+  a.per_row = per;
+  const unsigned blocks = (unsigned)((a.rows + (long long)a.rows_block - 1) / a.rows_block);
+  const unsigned threads = (unsigned)(per * a.rows_block);
+  auto go = [&](auto kern) {
+    kern<<<blocks, threads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+  };
+  if constexpr (V == 1) {
+    return ch <= 1 ? go(rmsnorm_kernel<T, O, 1, 1>) : ch <= 8 ? go(rmsnorm_kernel<T, O, 1, 8>) : go(rmsnorm_kernel<T, O, 1, 32>);
+  } else {
+    return ch == 1 ? go(rmsnorm_kernel<T, O, V, 1>) : ch == 2 ? go(rmsnorm_kernel<T, O, V, 2>) : go(rmsnorm_kernel<T, O, V, 4>);
+  }
+}
+
+template <typename T, typename O>
+int launch(NormArgs& a, cudaStream_t st) {
+  // 16-byte accesses (8-byte ones of bytes) where every address that they would have allows them.
+  const int v = 16 / sizeof(T) < 8 ? 4 : 8;
+  const bool vec = a.dim % 8 == 0 && aligned(a.x, 16) && aligned(a.residual, 16) && aligned(a.residual_out, 16) &&
+                   aligned(a.weight, 16) && aligned(a.y, sizeof(O) == 1 ? 8 : 16) && multiple(a.xs, v) &&
+                   (!a.residual || multiple(a.rs, v)) && (!a.residual_out || multiple(a.ros, v)) &&
+                   multiple(a.ys, sizeof(O) == 1 ? 8 : v);
+  return vec ? launch_v<T, O, 8>(a, st) : launch_v<T, O, 1>(a, st);
+}
+
+}  // namespace
+}  // namespace kdtv
+
+using namespace kdtv;
+
+extern "C" int kdtv_rmsnorm(const kdtv_norm_args* d, const void* x, const void* residual,
+                            void* residual_out, const void* weight, void* y, uint8_t* y_scale,
+                            const int32_t* n_live, cudaStream_t stream) {
+  if (!d || !x || !y || (residual_out && !residual)) return KDTV_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->N <= 0 || d->H <= 0 || d->dim <= 0) return KDTV_ERR_INVALID_ARG;
+  if (d->dtype != KDTV_F32 && d->dtype != KDTV_BF16) return KDTV_ERR_INVALID_ARG;
+  const bool one_byte = d->out_dtype == KDTV_BF16_FP8KV;
+  if (!one_byte && d->out_dtype != d->dtype) return KDTV_ERR_INVALID_ARG;
+  if (one_byte != (y_scale != nullptr) || (one_byte && d->dim % KDTV_GROUP)) return KDTV_ERR_INVALID_ARG;
+  if (!(d->eps >= 0.f) || !isfinite(d->eps) || !isfinite(d->weight_offset)) return KDTV_ERR_INVALID_ARG;
+  if (d->dim > 32768 || (long long)d->B * d->N * d->H > 0x7fffffffll) return KDTV_ERR_UNSUPPORTED;
+  if ((const void*)y == weight || (residual_out && (residual_out == y || residual_out == weight)))
+    return KDTV_ERR_INVALID_ARG;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.rows = (unsigned)((long long)d->B * d->N * d->H);
+  a.N = d->N; a.H = d->H; a.dim = d->dim;
+  a.x = x; a.residual = residual; a.residual_out = residual_out; a.weight = weight;
+  a.y = y; a.y_scale = y_scale; a.n_live = n_live;
+  a.eps = d->eps; a.weight_offset = d->weight_offset;
+  strides(d->x_stride, d->N, d->H, d->dim, a.xs);
+  strides(d->r_stride, d->N, d->H, d->dim, a.rs);
+  strides(d->ro_stride, d->N, d->H, d->dim, a.ros);
+  strides(d->y_stride, d->N, d->H, d->dim, a.ys);
+  a.by_heads = divisor((unsigned)d->H);
+  a.by_N = divisor((unsigned)d->N);
+  // In place is element by element: other strides or element sizes would overwrite what is still to be
+  // read.
+  if ((const void*)y == x && (one_byte || !same(a.xs, a.ys))) return KDTV_ERR_INVALID_ARG;
+  if ((const void*)y == residual && (one_byte || !same(a.rs, a.ys))) return KDTV_ERR_INVALID_ARG;
+  if (residual_out && residual_out == residual && !same(a.rs, a.ros)) return KDTV_ERR_INVALID_ARG;
+  if (residual_out && (const void*)residual_out == x && !same(a.xs, a.ros)) return KDTV_ERR_INVALID_ARG;
+  if (d->dtype == KDTV_F32)
+    return one_byte ? launch<float, __nv_fp8_e4m3>(a, stream) : launch<float, float>(a, stream);
+  return one_byte ? launch<__nv_bfloat16, __nv_fp8_e4m3>(a, stream) : launch<__nv_bfloat16, __nv_bfloat16>(a, stream);
+}

@@ -1,0 +1,255 @@
+// kdtv_pages_resize: block tables and slots of a paged cache from the
+// requests' lengths, on the GPU.
+
+#include "kdtv_rope.cuh"
+#include "kdtv_ptx.cuh"
+
+#include <string.h>
+
+namespace kdtv {
+namespace {
+
+constexpr int kPageThreads = 1024;
+constexpr int kMaxCluster = 8;
+
+struct PageArgs {
+  int B, N, page_size, max_pages, num_pages;
+  const int32_t *prefix_len, *n_live;
+  int32_t *free_pages, *free_count, *n_pages, *page_table;
+  int64_t* slots;
+  unsigned int* status;
+  Divisor by_page, by_N;
+};
+
+__device__ __forceinline__ void page_error(const PageArgs& a, unsigned int code) { atomicCAS(a.status, 0u, code); }
+
+// Index of the first entry of the ascending incl[0 .. n) that is above v; v < incl[n - 1].
+__device__ __forceinline__ int first_above(const int* incl, int n, int v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (incl[mid] > v) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Inclusive sums of v[0 .. n) and w[0 .. n), in place, by the block (a thread
+// has a run of neighbours).
+__device__ __forceinline__ void scan2(int* v, int* w, int n) {
+  __shared__ int2 part[32];
+  const int per = (n + kPageThreads - 1) / kPageThreads;
+  const int lo = min((int)threadIdx.x * per, n), hi = min(lo + per, n);
+  int2 s = make_int2(0, 0);
+  for (int i = lo; i < hi; ++i) {
+    s.x += v[i];
+    s.y += w[i];
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 incl = s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int2 p = part[lane];
+    const int2 own = p;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, p.x, o), y = __shfl_up_sync(0xffffffffu, p.y, o);
+      if (lane >= o) {
+        p.x += x;
+        p.y += y;
+      }
+    }
+    part[lane] = make_int2(p.x - own.x, p.y - own.y);
+  }
+  __syncthreads();
+  int x = part[warp].x + incl.x - s.x, y = part[warp].y + incl.y - s.y;
+  for (int i = lo; i < hi; ++i) {
+    v[i] = x += v[i];
+    w[i] = y += w[i];
+  }
+  __syncthreads();
+}
+
+// Slot of row i of request b, whose pages are those of `page_at`.
+template <typename F>
+__device__ __forceinline__ int64_t slot_of(const PageArgs& a, int L, int n, int pages, int i, F page_at) {
+  if (i >= n || L < 0 || pages < 0 || pages > a.max_pages || (long long)L + n > (long long)pages * a.page_size) return -1;
+  const int t = L + i, p = (int)divide(t, a.by_page), id = page_at(p);
+  return id < 0 || id >= a.num_pages ? -1 : (int64_t)id * a.page_size + (t - p * a.page_size);
+}
+
+// One cluster of CTAs.  Each scans all requests by itself (they are few, and
+// their lengths are in L2), so that the CTAs share nothing but two barriers:
+// what all of them read (counts, the free list's length, page ids that go
+// back) is read before the first one, what goes back is on the stack before
+// the second, behind which pages are taken.  Entry e of what goes back, or is
+// taken, finds its request by bisection in the sums, so that one request with
+// many pages is spread like many with one.
+// Latency bound: two trips to L2, a scan and two barriers.
+__global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid_constant__ PageArgs a, int ctas) {
+  extern __shared__ __align__(16) int ps[];
+  int *give = ps, *take = give + a.B, *want = take + a.B, *have = want + a.B;
+  uint32_t* bad = reinterpret_cast<uint32_t*>(have + a.B);       // one bit a request
+  const int rank = ctas > 1 ? (int)ptx::cluster_ctarank() : 0, tid = threadIdx.x;
+  const int all = ctas * kPageThreads, me = rank * kPageThreads + tid;
+  for (int i = tid; i < (a.B + 31) / 32; i += kPageThreads) bad[i] = 0u;
+  const int count = *a.free_count;
+  const bool usable = count >= 0 && count <= a.num_pages;
+  for (int b = tid; b < a.B; b += kPageThreads) {
+    const int L = a.prefix_len[b], n = live_rows(a.n_live, b, a.N), h = a.n_pages[b];
+    const long long rows = (long long)L + n;
+    int w = h;
+    if (L < 0 || rows > (long long)a.max_pages * a.page_size) {
+      if (rank == 0) page_error(a, KDTV_ERR_BAD_PREFIX);
+    } else if (h < 0 || h > a.max_pages || !usable) {
+      if (rank == 0) page_error(a, KDTV_ERR_BAD_PAGE);
+    } else {
+      w = (int)divide((unsigned)(rows + a.page_size - 1), a.by_page);
+    }
+    want[b] = w;
+    have[b] = h;
+    give[b] = max(h - w, 0);
+    take[b] = max(w - h, 0);
+  }
+  __syncthreads();
+  if (ctas > 1) ptx::cluster_sync();                   // every CTA's bits are clear
+  // Pages that go back must be pages: each CTA looks at its share of the requests.
+  for (int b = rank * (kPageThreads / 32) + (tid >> 5); b < a.B; b += ctas * (kPageThreads / 32)) {
+    const int32_t* row = a.page_table + (long long)b * a.max_pages;
+    bool wrong = false;
+    if (give[b])
+      for (int p = want[b] + (tid & 31); p < have[b]; p += 32) wrong |= row[p] < 0 || row[p] >= a.num_pages;
+    if (__any_sync(0xffffffffu, wrong) && (tid & 31) == 0) {
+      page_error(a, KDTV_ERR_BAD_PAGE);
+      const uint32_t at = ptx::smem_u32(&bad[b >> 5]);
+      for (int c = 0; c < ctas; ++c)
+        asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;"
+                     :: "r"(ctas > 1 ? ptx::mapa(at, c) : at), "r"(1u << (b & 31)) : "memory");
+    }
+  }
+  if (ctas > 1) ptx::cluster_sync();
+  else __syncthreads();
+  for (int b = tid; b < a.B; b += kPageThreads)
+    if ((bad[b >> 5] >> (b & 31)) & 1u) {
+      give[b] = 0;
+      want[b] = have[b];
+    }
+  __syncthreads();
+  scan2(give, take, a.B);
+  int given = give[a.B - 1];
+  // More pages than there are: counts or tables are wrong, and nothing moves.
+  const bool over = usable && (long long)count + given > a.num_pages;
+  const int top = over ? count : count + given;
+  if (over && rank == 0 && tid == 0) page_error(a, KDTV_ERR_BAD_PAGE);
+  if (over) given = 0;
+  // Who gets pages: the sums ascend, so those that the stack suffices for come first.
+  int grant = a.B;                                     // requests from here on get none
+  if (over) grant = 0;
+  else if (take[a.B - 1] > top) grant = first_above(take, a.B, top);
+  const int taken = grant ? take[grant - 1] : 0;
+  if (!over && taken != take[a.B - 1] && rank == 0 && tid == 0) page_error(a, KDTV_ERR_NO_PAGES);
+  // What request b holds now.
+  auto pages_of = [&](int b) { return over ? have[b] : want[b] > have[b] && b >= grant ? have[b] : want[b]; };
+  for (int b = me; b < a.B; b += all) {
+    const int p = pages_of(b);
+    if (p != have[b]) a.n_pages[b] = p;
+  }
+  if (me == 0 && usable) *a.free_count = top - taken;
+  if (given) {
+    for (int e = me; e < given; e += all) {
+      const int k = given - 1 - e;                     // from the last request's last page on
+      const int b = first_above(give, a.B, k), p = want[b] + k - (b ? give[b - 1] : 0);
+      int32_t* entry = a.page_table + (long long)b * a.max_pages + p;
+      a.free_pages[count + e] = *entry;
+      *entry = -1;
+    }
+    __threadfence();
+    if (ctas > 1) ptx::cluster_sync();
+    else __syncthreads();
+  }
+  // The k-th page that is taken, from the top of the stack down.
+  auto page_taken = [&](int k) { return *reinterpret_cast<volatile int32_t*>(a.free_pages + (top - 1 - k)); };
+  for (int k = me; k < taken; k += all) {
+    const int b = first_above(take, a.B, k), p = have[b] + k - (b ? take[b - 1] : 0);
+    const int id = page_taken(k);
+    if (id < 0 || id >= a.num_pages) page_error(a, KDTV_ERR_BAD_PAGE);
+    a.page_table[(long long)b * a.max_pages + p] = id;
+  }
+  if (a.slots)
+    for (long long k = me; k < (long long)a.B * a.N; k += all) {
+      const int b = (int)divide((unsigned)k, a.by_N), i = (int)(k - (long long)b * a.N);
+      a.slots[k] = slot_of(a, a.prefix_len[b], live_rows(a.n_live, b, a.N), pages_of(b), i, [&](int p) {
+        return p >= have[b] ? page_taken(p - have[b] + (b ? take[b - 1] : 0)) : a.page_table[(long long)b * a.max_pages + p];
+      });
+    }
+}
+
+// The slots of many rows, behind the tables.
+__global__ void __launch_bounds__(256) page_slots_kernel(const __grid_constant__ PageArgs a) {
+  ptx::grid_dep_wait();
+  const int b = blockIdx.y, L = a.prefix_len[b], n = live_rows(a.n_live, b, a.N), pages = a.n_pages[b];
+  const int32_t* row = a.page_table + (long long)b * a.max_pages;
+  int64_t* out = a.slots + (long long)b * a.N;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < a.N; i += gridDim.x * 256)
+    out[i] = slot_of(a, L, n, pages, i, [&](int p) { return row[p]; });
+}
+
+}  // namespace
+}  // namespace kdtv
+
+using namespace kdtv;
+
+extern "C" int kdtv_pages_resize(const kdtv_pages_dims* d, const int32_t* prefix_len,
+                                 const int32_t* n_live, int32_t* free_pages, int32_t* free_count,
+                                 int32_t* n_pages, int32_t* page_table, int64_t* slots,
+                                 unsigned int* status, cudaStream_t stream) {
+  if (!d || !prefix_len || !free_pages || !free_count || !n_pages || !page_table || !status) return KDTV_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->N < 0 || d->page_size <= 0 || d->max_pages <= 0 || d->num_pages <= 0) return KDTV_ERR_INVALID_ARG;
+  if ((long long)d->max_pages * d->page_size > (1ll << 30)) return KDTV_ERR_INVALID_ARG;
+  if (d->B > KDTV_MAX_POOL_REQUESTS || (long long)d->B * d->N >= (1ll << 31) ||
+      (long long)d->B * d->max_pages >= (1ll << 31))          // 32-bit sums
+    return KDTV_ERR_UNSUPPORTED;
+  PageArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = d->B; a.N = d->N; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
+  a.prefix_len = prefix_len; a.n_live = n_live;
+  a.free_pages = free_pages; a.free_count = free_count; a.n_pages = n_pages; a.page_table = page_table;
+  a.status = status;
+  a.by_page = divisor((unsigned)d->page_size);
+  a.by_N = divisor((unsigned)(d->N > 0 ? d->N : 1));
+  // A second kernel writes the slots of more rows than the cluster writes in the time that its launch
+  // takes.
+  const long long rows = (long long)d->B * d->N;
+  const bool apart = slots && rows > 32768;
+  a.slots = apart || rows == 0 ? nullptr : slots;
+  const int ctas = rows <= 4096 && d->B <= 256 ? 1 : kMaxCluster;
+  const size_t smem = (size_t)d->B * 16 + (d->B + 31) / 32 * 4;
+  if (allow_smem(pages_resize_kernel, smem) != cudaSuccess) return KDTV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPageThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, pages_resize_kernel, a, ctas) != cudaSuccess) return KDTV_ERR_CUDA;
+  if (apart) {
+    a.slots = slots;
+    const unsigned blocks = (unsigned)((d->N + 1023) / 1024);
+    if (launch_ex(page_slots_kernel, dim3(blocks, (unsigned)d->B), dim3(256), 0, stream, true, a) != cudaSuccess)
+      return KDTV_ERR_CUDA;
+  }
+  return KDTV_OK;
+}

@@ -1,0 +1,260 @@
+// kdtv_project: a projection that all requests share, with a low-rank adapter
+// per request.  Host side, and the CUDA-core path (fp32, and what the tensor
+// cores do not take).
+
+#include "kdtv_proj.cuh"
+
+#include <math.h>
+#include <string.h>
+
+namespace kdtv {
+namespace {
+
+constexpr int kThreads = 256;
+
+// s_a A_a x of a request's rows: a warp per rank row and eight rows of x, the
+// lanes along d_in.
+template <typename X, typename T>
+__global__ void __launch_bounds__(kThreads) proj_low_simt_kernel(const __grid_constant__ ProjArgs a) {
+  const int b = blockIdx.y, i0 = blockIdx.x * 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = live_rows(a.n_live, b, a.N);
+  if (i0 >= n) return;
+  const int id = proj_adapter(a, b);
+  if (id < 0) return;
+  const float s = a.adapter_scale ? a.adapter_scale[id] : 1.f;
+  const X* x = static_cast<const X*>(a.x) + b * a.xs[0] + i0 * a.xs[1];
+  const uint8_t* xe = a.x_scale + ((long long)b * a.N + i0) * (a.K / KDTV_GROUP);
+  for (int r = warp; r < a.R; r += kThreads / 32) {
+    const T* A = static_cast<const T*>(a.A) + ((long long)id * a.R + r) * a.K;
+    float acc[8] = {};
+    for (int k0 = 0; k0 < a.K; k0 += 32 * 16) {        // sums of at most 16 terms a lane, then of those
+      float part[8] = {};
+      for (int k = k0 + lane; k < min(a.K, k0 + 32 * 16); k += 32) {
+        const float w = to_f32(A[k]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i0 + j < n) {
+            float v = to_f32(x[j * a.xs[1] + k]);
+            if constexpr (sizeof(X) == 1) v *= scale_of_byte(xe[(long long)j * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
+            part[j] = fmaf(v, w, part[j]);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += part[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+      if (lane == 0 && i0 + j < n) a.low[((long long)b * a.N + i0 + j) * a.R + r] = s * acc[j];
+    }
+  }
+}
+
+// y: a CTA has TM rows (of all requests' rows) and TN outputs, kStep elements
+// of d_in at a time; its threads are S groups that take alternate steps and
+// meet at the end.  A thread has 4 x 4 sums, taken anew after 128 terms and
+// added to the totals: no chain of additions is long.
+// 64 x 64 with S = 1 is bound by the fp32 pipe and shared-memory reads (two
+// 16-byte reads for 16 multiply-adds); 16 x 32 with S = 8 is for few rows, where
+// the 64 x 64 tiles would leave SMs idle.
+template <typename X, typename T, int TM, int TN, int S, int kStep>
+__global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_constant__ ProjArgs a) {
+  constexpr int kGroup = kThreads / S;
+  static_assert(TM / 4 * (TN / 4) == kGroup, "4 x 4 sums a thread");
+  __shared__ __align__(16) float xs[S][kStep][TM + 4], ws[S][kStep][TN + 4];
+  __shared__ long long s_x[TM], s_y[TM];               // offsets of the rows, -1: not live
+  __shared__ int s_row[TM], s_id[TM];
+  __shared__ int s_any;
+  const int g = threadIdx.x / kGroup, t = threadIdx.x % kGroup;
+  const long long r0 = (long long)blockIdx.y * TM, rows = (long long)a.B * a.N;
+  const int f0 = blockIdx.x * TN;
+  if (threadIdx.x == 0) s_any = 0;
+  __syncthreads();
+  if (threadIdx.x < TM) {
+    const long long r = r0 + threadIdx.x;
+    long long ox = -1, oy = -1;
+    int id = -1;
+    if (r < rows) {
+      const int b = (int)divide((unsigned)r, a.by_N), i = (int)(r - (long long)b * a.N);
+      if (i < live_rows(a.n_live, b, a.N)) {
+        id = proj_adapter(a, b);
+        if (id != -2) {
+          ox = b * a.xs[0] + i * a.xs[1];
+          oy = b * a.ys[0] + i * a.ys[1];
+          s_any = 1;
+        }
+      }
+    }
+    s_x[threadIdx.x] = ox;
+    s_y[threadIdx.x] = oy;
+    s_row[threadIdx.x] = (int)r;
+    s_id[threadIdx.x] = id;
+  }
+  __syncthreads();
+  if (!s_any) return;
+  const int tm = t / (TN / 4) * 4, tn = t % (TN / 4) * 4;
+  float total[4][4] = {}, sum[4][4] = {};
+  const int steps = (a.K + kStep - 1) / kStep;
+  const X* x = static_cast<const X*>(a.x);
+  const X* W = static_cast<const X*>(a.W);
+  int held = 0;
+  for (int first = 0; first < steps; first += S) {
+    const int k0 = (first + g) * kStep;                // (a group behind the last step adds zeros)
+    for (int e = t; e < TM * kStep; e += kGroup) {
+      const int m = e / kStep, k = k0 + e % kStep;
+      const long long o = s_x[m];
+      float v = 0.f;
+      if (o >= 0 && k < a.K) {
+        v = to_f32(x[o + k]);
+        if constexpr (sizeof(X) == 1) v *= scale_of_byte(a.x_scale[(long long)s_row[m] * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
+      }
+      xs[g][e % kStep][m] = v;
+    }
+    for (int e = t; e < TN * kStep; e += kGroup) {
+      const int f = f0 + e / kStep, k = k0 + e % kStep;
+      float v = 0.f;
+      if (f < a.M && k < a.K) {
+        v = to_f32(W[(long long)f * a.K + k]);
+        if constexpr (sizeof(X) == 1) v *= scale_of_byte(a.W_scale[(long long)f * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
+      }
+      ws[g][e % kStep][e / kStep] = v;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int k = 0; k < kStep; ++k) {
+      const float4 u = *reinterpret_cast<const float4*>(&xs[g][k][tm]), w = *reinterpret_cast<const float4*>(&ws[g][k][tn]);
+      const float uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[p][q] = fmaf(uu[p], ww[q], sum[p][q]);
+    }
+    if (++held == 128 / kStep || first + S >= steps) {
+      held = 0;
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          total[p][q] += sum[p][q];
+          sum[p][q] = 0.f;
+        }
+    }
+    __syncthreads();
+  }
+  if constexpr (S > 1) {                               // the groups' totals, in their order
+    float* part = &ws[0][0][0];
+    static_assert(sizeof(ws) >= (size_t)S * TM * TN * sizeof(float), "room for the totals");
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) part[(g * TM + tm + p) * TN + tn + q] = total[p][q];
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        for (int s = 1; s < S; ++s) total[p][q] += part[(s * TM + tm + p) * TN + tn + q];
+  }
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if (s_y[tm + p] < 0) continue;
+    const int id = s_id[tm + p];
+    T* y = static_cast<T*>(a.y) + s_y[tm + p];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int f = f0 + tn + q;
+      if (f >= a.M) continue;
+      float v = total[p][q];
+      if (id >= 0) {
+        const T* Bm = static_cast<const T*>(a.Bm) + ((long long)id * a.M + f) * a.R;
+        const float* low = a.low + (long long)s_row[tm + p] * a.R;
+        float d = 0.f;
+        for (int r = 0; r < a.R; ++r) d = fmaf(low[r], to_f32(Bm[r]), d);
+        v += d;
+      }
+      const float one[1] = {v};
+      store_v<1>(y + f, one);
+    }
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <typename X, typename T>
+int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
+  if (a.adapter)
+    proj_low_simt_kernel<X, T><<<dim3((unsigned)((a.N + 7) / 8), (unsigned)a.B), kThreads, 0, st>>>(a);
+  const long long rows = (long long)a.B * a.N;
+  const long long big = (rows + 63) / 64 * ((a.M + 63) / 64);
+  if (big >= sms || rows > 16 * 65535)
+    proj_simt_kernel<X, T, 64, 64, 1, 32><<<dim3((unsigned)((a.M + 63) / 64), (unsigned)((rows + 63) / 64)), kThreads, 0, st>>>(a);
+  else
+    proj_simt_kernel<X, T, 16, 32, 8, 16><<<dim3((unsigned)((a.M + 31) / 32), (unsigned)((rows + 15) / 16)), kThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+}
+
+int check_dims(const kdtv_project_dims* d) {
+  if (!d) return KDTV_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->N <= 0 || d->d_in <= 0 || d->d_out <= 0 || d->adapters < 0) return KDTV_ERR_INVALID_ARG;
+  if (d->dtype != KDTV_F32 && d->dtype != KDTV_BF16 && d->dtype != KDTV_BF16_FP8KV) return KDTV_ERR_INVALID_ARG;
+  if (d->adapters > 0 && d->rank <= 0) return KDTV_ERR_INVALID_ARG;
+  if (d->dtype == KDTV_BF16_FP8KV && d->d_in % KDTV_GROUP) return KDTV_ERR_INVALID_ARG;
+  if (d->adapters > KDTV_MAX_ADAPTERS || (d->adapters > 0 && d->rank > 256)) return KDTV_ERR_UNSUPPORTED;
+  if (d->B > 65535 || d->d_in > (1 << 20) || d->d_out > (1 << 20) || (long long)d->B * d->N > 64ll * 65535)
+    return KDTV_ERR_UNSUPPORTED;                           // grid rows
+  return KDTV_OK;
+}
+
+size_t workspace_of(const kdtv_project_dims* d) {
+  return align256((size_t)d->B * d->N * (d->adapters > 0 ? d->rank : 0) * sizeof(float)) + 256;
+}
+
+}  // namespace
+}  // namespace kdtv
+
+using namespace kdtv;
+
+extern "C" size_t kdtv_project_workspace_size(const kdtv_project_dims* d) {
+  return check_dims(d) == KDTV_OK ? workspace_of(d) : 0;
+}
+
+extern "C" int kdtv_project_launches_per_call(const kdtv_project_dims* d) {
+  return check_dims(d) == KDTV_OK ? 1 + (d->adapters > 0) : -1;
+}
+
+extern "C" int kdtv_project(const kdtv_project_dims* d, const void* x, const uint8_t* x_scale,
+                            const void* W, const uint8_t* W_scale, const void* A, const void* Bm,
+                            const float* adapter_scale, const int32_t* adapter, const int32_t* n_live,
+                            void* y, unsigned int* status, cudaStream_t stream) {
+  const int rc = check_dims(d);
+  if (rc != KDTV_OK) return rc;
+  if (!x || !W || !y || !status || y == x || y == W) return KDTV_ERR_INVALID_ARG;
+  const bool one_byte = d->dtype == KDTV_BF16_FP8KV;
+  if (one_byte != (x_scale != nullptr) || one_byte != (W_scale != nullptr)) return KDTV_ERR_INVALID_ARG;
+  if ((A != nullptr) != (Bm != nullptr) || (adapter && !A) || (A && d->adapters == 0)) return KDTV_ERR_INVALID_ARG;
+  if (one_byte && (d->x_stride[0] || d->x_stride[1]) &&
+      (d->x_stride[0] != (int64_t)d->N * d->d_in || d->x_stride[1] != d->d_in))
+    return KDTV_ERR_INVALID_ARG;
+  if (!d->workspace || (reinterpret_cast<uintptr_t>(d->workspace) & 255u) || d->workspace_bytes < workspace_of(d))
+    return KDTV_ERR_INVALID_ARG;
+  ProjArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = d->B; a.N = d->N; a.K = d->d_in; a.M = d->d_out; a.R = d->adapters > 0 ? d->rank : 0;
+  a.adapters = d->adapters; a.dtype = d->dtype;
+  a.x = x; a.W = W; a.A = A; a.Bm = Bm; a.x_scale = x_scale; a.W_scale = W_scale;
+  a.adapter_scale = adapter_scale; a.adapter = adapter; a.n_live = n_live;
+  a.y = y; a.status = status;
+  const bool gx = d->x_stride[0] || d->x_stride[1], gy = d->y_stride[0] || d->y_stride[1];
+  a.xs[0] = gx ? d->x_stride[0] : (long long)d->N * d->d_in;
+  a.xs[1] = gx ? d->x_stride[1] : d->d_in;
+  a.ys[0] = gy ? d->y_stride[0] : (long long)d->N * d->d_out;
+  a.ys[1] = gy ? d->y_stride[1] : d->d_out;
+  a.by_N = divisor((unsigned)d->N);
+  a.low = static_cast<float*>(d->workspace);
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
+  if (d->dtype == KDTV_F32) return launch_simt<float, float>(a, sms, stream);
+  if (d->dtype == KDTV_BF16) return launch_simt<__nv_bfloat16, __nv_bfloat16>(a, sms, stream);
+  return launch_simt<__nv_fp8_e4m3, __nv_bfloat16>(a, sms, stream);
+}

@@ -146,6 +146,12 @@ __device__ __forceinline__ int live_rows(const int32_t* n_live, int b, int N) {
   const int n = n_live[b];
   return n < 0 ? 0 : (n > N ? N : n);
 }
+// The smallest e with mx <= 448 * 2^e = 1.75 * 2^(e + 8), from mx's bits.
+__device__ __forceinline__ int exponent_of(float mx) {
+  const uint32_t bits = __float_as_uint(mx);
+  const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+  return max(-117, min(119, e));
+}
 // Value of exponent byte e + 127 (2^e, e in [-126, 127]).
 __device__ __forceinline__ float scale_of_byte(unsigned int byte) {
   return __uint_as_float(byte << 23);

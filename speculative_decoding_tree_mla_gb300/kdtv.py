@@ -20,7 +20,8 @@ KDTV_FLAG_SIMT_PROJ = 0x2
 KDTV_FLAG_TEST_STALL = 0x100
 STATUS = {0: "KDTV_OK", 1: "KDTV_ERR_INVALID_ARG", 2: "KDTV_ERR_UNSUPPORTED",
           3: "KDTV_ERR_CUDA", 4: "KDTV_ERR_BAD_TREE", 5: "KDTV_ERR_DEVICE_TIMEOUT",
-          6: "KDTV_ERR_BAD_PREFIX", 7: "KDTV_ERR_BAD_PAGE"}
+          6: "KDTV_ERR_BAD_PREFIX", 7: "KDTV_ERR_BAD_PAGE", 8: "KDTV_ERR_NO_PAGES",
+          9: "KDTV_ERR_BAD_ADAPTER"}
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
 # Every symbol include/kdtv.h declares (checked by the CPU tests).
@@ -28,7 +29,9 @@ EXPORTS = ("kdtv_workspace_size", "kdtv_verify_attn", "kdtv_get_device_status",
            "kdtv_strerror", "kdtv_launches_per_call", "kdtv_tree_accept", "kdtv_compact_kv",
            "kdtv_tree_build", "kdtv_verify_attn_noalloc", "kdtv_rope_init", "kdtv_rope",
            "kdtv_kv_append", "kdtv_kv_read", "kdtv_gqa_workspace_size",
-           "kdtv_gqa_launches_per_call", "kdtv_gqa_verify_attn")
+           "kdtv_gqa_launches_per_call", "kdtv_gqa_verify_attn", "kdtv_rmsnorm",
+           "kdtv_project_workspace_size", "kdtv_project_launches_per_call", "kdtv_project",
+           "kdtv_pages_resize")
 
 
 class KdtvDims(ctypes.Structure):
@@ -96,6 +99,30 @@ class KdtvGqaDims(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+GROUP = 32                           # elements that share an exponent byte in activations and weights
+
+
+class KdtvNormArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("x_stride", ctypes.c_int64 * 3), ("r_stride", ctypes.c_int64 * 3),
+                ("ro_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class KdtvProjectDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d_in", ctypes.c_int32),
+                ("d_out", ctypes.c_int32), ("dtype", ctypes.c_int32), ("adapters", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("flags", ctypes.c_uint32), ("x_stride", ctypes.c_int64 * 2),
+                ("y_stride", ctypes.c_int64 * 2), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class KdtvPagesDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
+
+
 class KdtvError(RuntimeError):
     def __init__(self, code, what=""):
         self.code = code
@@ -150,6 +177,17 @@ def lib():
         L.kdtv_gqa_launches_per_call.restype = ctypes.c_int
         L.kdtv_gqa_verify_attn.argtypes = [G] + [vp] * 11 + [vp]
         L.kdtv_gqa_verify_attn.restype = ctypes.c_int
+        L.kdtv_rmsnorm.argtypes = [ctypes.POINTER(KdtvNormArgs)] + [vp] * 7 + [vp]
+        L.kdtv_rmsnorm.restype = ctypes.c_int
+        J = ctypes.POINTER(KdtvProjectDims)
+        L.kdtv_project_workspace_size.argtypes = [J]
+        L.kdtv_project_workspace_size.restype = ctypes.c_size_t
+        L.kdtv_project_launches_per_call.argtypes = [J]
+        L.kdtv_project_launches_per_call.restype = ctypes.c_int
+        L.kdtv_project.argtypes = [J] + [vp] * 11 + [vp]
+        L.kdtv_project.restype = ctypes.c_int
+        L.kdtv_pages_resize.argtypes = [ctypes.POINTER(KdtvPagesDims)] + [vp] * 8 + [vp]
+        L.kdtv_pages_resize.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -692,3 +730,254 @@ def gqa_verify_attn(q, k, v, parent, prefix_len, *, stream=None, **kw):
     with _on(stream):
         op = GqaVerifyAttn(q, k, v, parent, prefix_len, **kw)
         return op(stream), op._status
+
+
+# ---- between the attention calls: norms, shared projections, pages ----------------------
+
+def _one_byte():
+    import torch
+    return (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+
+
+def _rows_like(t, shape, dtypes, device, name):
+    """A result of the given shape: last dimension contiguous, no two elements in one place."""
+    _need(tuple(t.shape) == tuple(shape) and t.dtype in dtypes and t.device == device and t.stride(-1) == 1
+          and _apart(t), f"{name}: {list(shape)}, {' or '.join(map(str, dtypes))}, no two elements in one place")
+    return t
+
+
+class RmsNorm(_Bound):
+    """Caller of kdtv_rmsnorm: h = x + residual, out = h / sqrt(mean(h^2) + eps) * (weight + weight_offset).
+
+    x: [B, N, dim] or [B, N, H, dim] (one norm per head), float32 or bfloat16, last dimension
+    contiguous.  `residual` is like x; the sum goes to `residual_out` (None: over `residual`; False:
+    it is not kept).  out: like x (also x itself), or one byte per element (`one_byte`, or a uint8 or
+    float8_e4m3fn `out`) with exponent bytes out_scale [B, N, (H,) dim / 32], contiguous: what Project
+    reads as x and x_scale.  Rows behind n_live are left as they were.
+    """
+
+    def __init__(self, x, weight=None, *, residual=None, residual_out=None, n_live=None, eps=1e-6,
+                 weight_offset=0.0, out=None, out_scale=None, one_byte=False):
+        import torch
+        _need(isinstance(x, torch.Tensor) and x.is_cuda and x.dim() in (3, 4) and x.numel() > 0
+              and x.dtype in (torch.float32, torch.bfloat16) and x.stride(-1) == 1,
+              "x: a float32 or bfloat16 CUDA tensor [B, N, dim] or [B, N, H, dim] with a contiguous last dimension")
+        shape, dev, dim = tuple(x.shape), x.device, x.shape[-1]
+        one_byte = one_byte or (out is not None and out.dtype in _one_byte()) or out_scale is not None
+        _need(weight is None or (tuple(weight.shape) == (dim,) and weight.dtype == x.dtype and weight.device == dev
+                                 and weight.is_contiguous()), f"weight: contiguous [{dim}] like x")
+        if residual is not None:
+            _need(tuple(residual.shape) == shape and residual.dtype == x.dtype and residual.device == dev
+                  and residual.stride(-1) == 1, "residual: like x")
+            if residual_out is None:
+                residual_out = residual
+        _need(residual is not None or residual_out is None or residual_out is False, "residual_out: with a residual")
+        self.residual_out = None
+        if residual_out is not None and residual_out is not False:
+            self.residual_out = _rows_like(residual_out, shape, (x.dtype,), dev, "residual_out")
+        _need(not one_byte or dim % GROUP == 0, f"one byte per element: dim a multiple of {GROUP}")
+        if out is None:
+            out = torch.empty(shape, dtype=torch.uint8 if one_byte else x.dtype, device=dev)
+        self.out = _rows_like(out, shape, _one_byte() if one_byte else (x.dtype,), dev, "out")
+        if one_byte and out_scale is None:
+            out_scale = torch.empty(shape[:-1] + (dim // GROUP,), dtype=torch.uint8, device=dev)
+        _need(not one_byte or (tuple(out_scale.shape) == shape[:-1] + (dim // GROUP,) and out_scale.dtype == torch.uint8
+                               and out_scale.device == dev and out_scale.is_contiguous()),
+              f"out_scale: contiguous uint8 {list(shape[:-1] + (dim // GROUP,))}")
+        self.out_scale = out_scale
+        heads = (lambda t: t.unsqueeze(2)) if x.dim() == 3 else (lambda t: t)
+        B, N, H, _ = heads(x).shape
+        a = KdtvNormArgs(B, N, H, dim, KDTV_F32 if x.dtype == torch.float32 else KDTV_BF16)
+        a.out_dtype = KDTV_BF16_FP8KV if one_byte else a.dtype
+        a.eps, a.weight_offset = eps, weight_offset
+        for name, t in (("x_stride", x), ("r_stride", residual), ("ro_stride", self.residual_out), ("y_stride", out)):
+            if t is not None:
+                setattr(a, name, _strides(heads(t)))
+        nl = _index(n_live, (B,), dev, "n_live")
+        self._bind("kdtv_rmsnorm", dev,
+                   (ctypes.byref(a), _p(x), _p(residual), _p(self.residual_out), _p(weight), _p(out), _p(out_scale),
+                    _p(nl)), (a, x, weight, residual, self.residual_out, out, out_scale, nl),
+                   [t for t in (self.out, self.out_scale, self.residual_out) if t is not None])
+
+    def __call__(self, stream=None):
+        self._launch(stream)
+        return self.out if self.out_scale is None else (self.out, self.out_scale)
+
+
+def rmsnorm(x, weight=None, *, stream=None, **kw):
+    """Adds the residual and norms (see RmsNorm); returns out, or (out, out_scale)."""
+    with _on(stream):
+        return RmsNorm(x, weight, **kw)(stream)
+
+
+class Project(_Bound):
+    """Caller of kdtv_project: out = x W^T, and for requests with an adapter a = adapter[b] beside it
+    adapter_scale[a] (x A[a]^T) Bm[a]^T.
+
+    x: [B, N, d_in] float32 or bfloat16 (last dimension contiguous), or one byte per element with
+    x_scale [B, N, d_in / 32] as RmsNorm writes them (contiguous); W: [d_out, d_in] of the same type,
+    W_scale [d_out, d_in / 32] (quantise_weight makes them); A: [adapters, rank, d_in], Bm: [adapters,
+    d_out, rank] (one-byte x: bfloat16); adapter: [B] int32, -1 for none; out: [B, N, d_out] float32 or
+    bfloat16, last dimension contiguous.  Rows behind n_live are left as they were.  Holds the
+    workspace: calls of one object must not overlap on the GPU.  status() reads the status word.
+    """
+
+    def __init__(self, x, W, *, x_scale=None, W_scale=None, A=None, Bm=None, adapter=None, adapter_scale=None,
+                 n_live=None, flags=0, out=None):
+        import torch
+        _need(isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 3 and x.numel() > 0 and x.stride(2) == 1
+              and x.dtype in (torch.float32, torch.bfloat16) + _one_byte(),
+              "x: a float32, bfloat16 or one-byte CUDA tensor [B, N, d_in] with a contiguous last dimension")
+        B, N, K = x.shape
+        dev, fp8 = x.device, x.dtype in _one_byte()
+        dt = torch.bfloat16 if fp8 else x.dtype
+        _need(isinstance(W, torch.Tensor) and W.dim() == 2 and W.shape[1] == K and W.numel() > 0 and W.device == dev
+              and W.is_contiguous() and (W.dtype in _one_byte() if fp8 else W.dtype == x.dtype),
+              "W: contiguous [d_out, d_in] of x's type")
+        M = W.shape[0]
+        _need(not fp8 or (x.is_contiguous() and K % GROUP == 0), f"one-byte x: contiguous, d_in a multiple of {GROUP}")
+        for t, lead, name in ((x_scale, (B, N), "x_scale"), (W_scale, (M,), "W_scale")):
+            _need((t is not None) == fp8, f"{name}: with one-byte x and W, and only there")
+            _need(t is None or (tuple(t.shape) == lead + (K // GROUP,) and t.dtype == torch.uint8 and t.device == dev
+                                and t.is_contiguous()), f"{name}: contiguous uint8 {list(lead + (K // GROUP,))}")
+        _need((A is None) == (Bm is None) and (adapter is None or A is not None), "A, Bm: both, for adapter")
+        adapters = rank = 0
+        if A is not None:
+            _need(A.dim() == 3 and Bm.dim() == 3 and A.numel() > 0, "A: [adapters, rank, d_in], Bm: [adapters, d_out, rank]")
+            adapters, rank = A.shape[:2]
+            for t, shape, name in ((A, (adapters, rank, K), "A"), (Bm, (adapters, M, rank), "Bm")):
+                _need(tuple(t.shape) == shape and t.dtype == dt and t.device == dev and t.is_contiguous(),
+                      f"{name}: contiguous {dt} {list(shape)}")
+        _need(adapter_scale is None or (A is not None and tuple(adapter_scale.shape) == (adapters,)
+                                        and adapter_scale.dtype == torch.float32 and adapter_scale.device == dev
+                                        and adapter_scale.is_contiguous()), "adapter_scale: contiguous float32 [adapters]")
+        ad = _index(adapter, (B,), dev, "adapter")
+        nl = _index(n_live, (B,), dev, "n_live")
+        self.out = torch.empty((B, N, M), dtype=dt, device=dev) if out is None else out
+        _rows_like(self.out, (B, N, M), (dt,), dev, "out")
+        D = KdtvProjectDims(B, N, K, M, KDTV_BF16_FP8KV if fp8 else KDTV_F32 if dt == torch.float32 else KDTV_BF16,
+                            adapters, rank, flags)
+        D.x_stride, D.y_stride = _row_strides(x), _row_strides(self.out)
+        with torch.cuda.device(dev):
+            nbytes = int(lib().kdtv_project_workspace_size(ctypes.byref(D)))
+        if nbytes == 0:
+            raise KdtvError(STATUS_CODE["KDTV_ERR_UNSUPPORTED"], "workspace size")
+        self.dims = D
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        D.workspace, D.workspace_bytes = self.workspace.data_ptr(), nbytes
+        self._status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._bind("kdtv_project", dev,
+                   (ctypes.byref(D), _p(x), _p(x_scale), _p(W), _p(W_scale), _p(A), _p(Bm), _p(adapter_scale), _p(ad),
+                    _p(nl), _p(self.out), _p(self._status)),
+                   (x, x_scale, W, W_scale, A, Bm, adapter_scale, ad, nl), [self.out, self.workspace, self._status])
+
+    def __call__(self, stream=None):
+        self._launch(stream)
+        return self.out
+
+    def status(self):
+        """First device-side error since it was last read (0: none), or the timeout of a wait, which
+        replaces any other; waits for the device, clears it."""
+        self.torch.cuda.synchronize(self.device)
+        code = int(self._status.item())
+        if code:
+            self._status.zero_()
+            self.torch.cuda.synchronize(self.device)
+        return code
+
+    def launches(self):
+        return int(lib().kdtv_project_launches_per_call(ctypes.byref(self.dims)))
+
+
+def _row_strides(t):
+    """Strides of [B, N, ..] for the library, where both zero means contiguous."""
+    s = t.stride()[:2]
+    _need(any(s) or t.shape[:2].numel() == 1, "a tensor that repeats one row: make it contiguous")
+    return (ctypes.c_int64 * 2)(*s)
+
+
+def project(x, W, *, stream=None, **kw):
+    """Projects with adapters (see Project); returns (out, status word)."""
+    with _on(stream):
+        op = Project(x, W, **kw)
+        return op(stream), op._status
+
+
+def quantise_weight(W):
+    """One byte per element of a weight matrix [d_out, d_in] (float32 or bfloat16, CUDA), with an
+    exponent byte per 32: (codes uint8, scale uint8) as Project takes them (kdtv_kv_append, the
+    groups as heads)."""
+    import torch
+    _need(isinstance(W, torch.Tensor) and W.is_cuda and W.dim() == 2 and W.is_contiguous() and W.numel() > 0
+          and W.dtype in (torch.float32, torch.bfloat16) and W.shape[1] % GROUP == 0,
+          f"W: a contiguous float32 or bfloat16 CUDA matrix, d_in a multiple of {GROUP}")
+    M, K = W.shape
+    codes = torch.empty((M, K), dtype=torch.uint8, device=W.device)
+    scale = torch.empty((M, K // GROUP), dtype=torch.uint8, device=W.device)
+    first = torch.zeros(1, dtype=torch.int32, device=W.device)
+    kv_append([KvPart(codes.view(1, M, K // GROUP, GROUP), src=W.view(1, M, K // GROUP, GROUP),
+                      scale=scale.view(1, M, K // GROUP))], first)
+    return codes, scale
+
+
+class PagePool:
+    """The pages of a cache and who holds them: page_table [B, max_pages], n_pages [B], free_pages
+    [num_pages] (a stack whose first free_count[0] entries are free), all int32 on one device.
+    PagePool.empty makes one whose pages are all free."""
+
+    def __init__(self, page_table, n_pages, free_pages, free_count, page_size):
+        import torch
+        _need(isinstance(page_table, torch.Tensor) and page_table.is_cuda and page_table.dim() == 2
+              and page_table.numel() > 0 and free_pages.dim() == 1, "page_table: a CUDA tensor [B, max_pages]; free_pages: [num_pages]")
+        dev, (B, width) = page_table.device, page_table.shape
+        self.page_table = _index(page_table, (B, width), dev, "page_table")
+        self.n_pages = _index(n_pages, (B,), dev, "n_pages")
+        self.free_pages = _index(free_pages, (free_pages.shape[0],), dev, "free_pages")
+        self.free_count = _index(free_count, (1,), dev, "free_count")
+        self.page_size, self.num_pages, self.device = int(page_size), free_pages.shape[0], dev
+
+    @classmethod
+    def empty(cls, B, max_pages, num_pages, page_size, device="cuda"):
+        import torch
+        def ints(*shape, fill):
+            return torch.full(shape, fill, dtype=torch.int32, device=device)
+        return cls(ints(B, max_pages, fill=-1), ints(B, fill=0),
+                   torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   ints(1, fill=num_pages), page_size)
+
+
+class PagesResize(_Bound):
+    """Caller of kdtv_pages_resize: request b is to hold the pages of rows 0 .. prefix_len[b] +
+    n_live[b] (n_live None: N more rows each).  slots [B, N] int64 (True: a new one): cache row of
+    row prefix_len[b] + i, -1 where there is none.  Calling it returns the status word, or (slots,
+    status word)."""
+
+    def __init__(self, pool, prefix_len, *, N=None, n_live=None, slots=None, status=None):
+        import torch
+        dev, (B, width) = pool.device, pool.page_table.shape
+        pl = _index(prefix_len, (B,), dev, "prefix_len")
+        nl = _index(n_live, (B,), dev, "n_live")
+        _need(pl is not None, "prefix_len")
+        if N is None:
+            _need(isinstance(slots, torch.Tensor), "N: rows per request, unless slots give it")
+            N = slots.shape[1]
+        if slots is True:
+            slots = torch.empty((B, N), dtype=torch.int64, device=dev)
+        _need(slots is None or (tuple(slots.shape) == (B, N) and slots.dtype == torch.int64 and slots.is_contiguous()
+                                and slots.device == dev), f"slots: contiguous int64 {[B, N]} on {dev}")
+        self.slots, self.status = slots, _status_word(status, dev)
+        d = KdtvPagesDims(B, N, pool.page_size, width, pool.num_pages)
+        self._bind("kdtv_pages_resize", dev,
+                   (ctypes.byref(d), _p(pl), _p(nl), _p(pool.free_pages), _p(pool.free_count), _p(pool.n_pages),
+                    _p(pool.page_table), _p(slots), _p(self.status)), (d, pool, pl, nl, slots),
+                   [t for t in (slots, self.status) if t is not None])
+
+    def __call__(self, stream=None):
+        self._launch(stream)
+        return self.status if self.slots is None else (self.slots, self.status)
+
+
+def pages_resize(pool, prefix_len, *, stream=None, **kw):
+    """Gives and takes pages (see PagesResize); returns the status word, or (slots, status word)."""
+    with _on(stream):
+        return PagesResize(pool, prefix_len, **kw)(stream)

@@ -1,0 +1,269 @@
+"""kdtv_project against the fp64 oracle.
+
+Tolerances.  With T the sum of the magnitudes of a sum's terms: CUDA cores, fp32: chains of 128 products,
+their totals (at most d_in / 128 + 8 of them) and the adapter's R terms, each addition off by 2^-24 of at
+most T, and the products' own rounding: (140 + d_in / 128 + R) 2^-24 T.  (The inner product A x has the same
+chains, 16 to a lane and the lanes' totals.)  Tensor cores: products are exact, and each of at most (d_in + 2
+R) additions may lose 2^-23 of T (truncated, not rounded); A x enters as two bf16 parts, 2^-16 of it.  Then
+half a step of the output type, 2^-8 for bf16, relative to the value.  Whole-number cases, where every sum
+is exact, are equal bit for bit."""
+
+import numpy as np
+import pytest
+
+from oracle import serve_ops as O
+from speculative_decoding_tree_mla_gb300 import kdtv
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+SIMT = kdtv.KDTV_FLAG_SIMT
+TYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16}
+
+
+def f64(t):
+    return t.float().cpu().double().numpy()
+
+
+class Case:
+    def __init__(self, B, N, K, M, dtype, adapters=0, rank=16, seed=0, whole=False, ids=None, n_live=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        dt = TYPE[dtype]
+
+        def values(*shape, std=1.0):
+            if whole:
+                return torch.randint(-2, 3, shape, generator=g, device="cuda").to(dt)
+            return (torch.randn(shape, generator=g, device="cuda") * std).to(dt)
+
+        self.B, self.N, self.K, self.M, self.dtype, self.rank = B, N, K, M, dtype, rank
+        self.x, self.W = values(B, N, K), values(M, K, std=K ** -0.5)
+        self.kw = {}
+        if dtype == "fp8":
+            self.W, ws = kdtv.quantise_weight(self.W)
+            self.x, xs = kdtv.rmsnorm(self.x, one_byte=True) if not whole else self._codes(self.x)
+            self.kw.update(x_scale=xs, W_scale=ws)
+            self.x64 = O.widen(self.x.cpu().numpy(), xs.cpu().numpy())
+            self.W64 = O.widen(self.W.cpu().numpy(), ws.cpu().numpy())
+        else:
+            self.x64, self.W64 = f64(self.x), f64(self.W)
+        self.o = {}
+        if adapters:
+            A, Bm = values(adapters, rank, K, std=K ** -0.5), values(adapters, M, rank, std=0.5)
+            s = torch.tensor([0.5, 1.0, 2.0, -1.0], device="cuda")[torch.arange(adapters, device="cuda") % 4]
+            self.ids = np.asarray(ids if ids is not None else rng.integers(-1, adapters, B), dtype=np.int32)
+            self.kw.update(A=A, Bm=Bm, adapter_scale=s, adapter=torch.tensor(self.ids, device="cuda"))
+            self.o = dict(A=f64(A), Bm=f64(Bm), adapter=self.ids, adapter_scale=f64(s))
+        self.n = np.full(B, N) if n_live is None else np.asarray(n_live)
+        if n_live is not None:
+            self.kw["n_live"] = torch.tensor(self.n, dtype=torch.int32, device="cuda")
+
+    @staticmethod
+    def _codes(x):
+        B, N, K = x.shape
+        c, s = kdtv.quantise_weight(x.reshape(B * N, K))
+        return c.view(B, N, K), s.view(B, N, K // 32)
+
+    def oracle(self):
+        return O.project(self.x64, self.W64, **self.o)
+
+    def check(self, out, flags=0, exact=False, before=7.0):
+        y, mag = self.oracle()
+        got = f64(out)
+        for b in range(self.B):
+            m = min(max(int(self.n[b]), 0), self.N)
+            assert (got[b, m:] == before).all(), (b, "rows that are not live")
+            if exact:
+                want = f64(torch.tensor(y[b, :m]).to(TYPE[self.dtype]))
+                assert np.array_equal(got[b, :m], want), (b, np.abs(got[b, :m] - want).max())
+                continue
+            R = self.rank if self.o else 0
+            if self.dtype == "f32" or flags & SIMT:
+                tol = (140 + self.K / 128 + R) * 2.0 ** -24
+            else:
+                tol = (self.K + 2 * R) * 2.0 ** -23 + (2.0 ** -16 if R else 0.0)
+            step = 2.0 ** -24 if self.dtype == "f32" else 2.0 ** -8
+            err = np.abs(got[b, :m] - y[b, :m])
+            lim = tol * mag[b, :m] + step * np.abs(y[b, :m])
+            assert (err <= lim).all(), (b, float((err / lim).max()), np.argwhere(err > lim)[:4])
+
+    def run(self, flags=0, **kw):
+        out = torch.full((self.B, self.N, self.M), 7.0, dtype=TYPE[self.dtype], device="cuda")
+        got, st = kdtv.project(self.x, self.W, flags=flags, out=out, **self.kw, **kw)
+        assert int(st) == 0
+        return got
+
+
+PATHS = [("f32", 0), ("bf16", 0), ("bf16", SIMT), ("fp8", 0), ("fp8", SIMT)]
+
+
+@pytest.mark.parametrize("dtype,flags", PATHS)
+@pytest.mark.parametrize("B,N,K,M,adapters,rank", [
+    (1, 1, 32, 1, 0, 0), (1, 1, 64, 128, 1, 16), (3, 13, 96, 130, 2, 8), (1, 1, 2048, 640, 3, 16), (64, 1, 256, 384, 40, 16),
+    (5, 33, 192, 100, 3, 24), (2, 300, 320, 256, 2, 64), (300, 1, 128, 200, 100, 8), (4, 128, 512, 1000, 4, 32),
+    (1, 700, 224, 129, 1, 128), (17, 8, 1024, 72, 5, 40), (2, 129, 64, 64, 2, 16), (9, 100, 160, 257, 3, 256)])
+def test_matches_oracle(dtype, flags, B, N, K, M, adapters, rank):
+    c = Case(B, N, K, M, dtype, adapters, rank, seed=B + N)
+    c.check(c.run(flags), flags)
+
+
+@pytest.mark.parametrize("dtype,flags", PATHS)
+@pytest.mark.parametrize("B,N,K,M,adapters,rank", [
+    (1, 1, 64, 3, 1, 8), (64, 1, 64, 300, 20, 8), (7, 9, 96, 130, 3, 16), (2, 257, 128, 140, 2, 24), (33, 8, 160, 64, 33, 16),
+    (3, 1030, 64, 260, 3, 8), (260, 1, 32, 40, 260, 8)])
+def test_whole_numbers_are_exact(dtype, flags, B, N, K, M, adapters, rank):
+    """Entries of -2 .. 2: every sum is a whole number below 2^24 (A x, up to 4 K, splits into two bf16 parts
+    exactly), so each output is the correctly rounded sum, element by element."""
+    c = Case(B, N, K, M, dtype, adapters, rank, seed=1, whole=True)
+    c.check(c.run(flags), flags, exact=True)
+
+
+@pytest.mark.parametrize("dtype,flags", PATHS)
+@pytest.mark.parametrize("B,N,K,M", [(6, 20, 128, 96), (5, 300, 64, 130), (70, 5, 64, 64), (3, 2000, 64, 40)])
+def test_ragged_rows(dtype, flags, B, N, K, M):
+    rng = np.random.default_rng(5)
+    n = rng.integers(0, N + 1, B)
+    n[0], n[1], n[-1] = 0, N, N + 5 if B > 4 else 1
+    c = Case(B, N, K, M, dtype, 3, 16, seed=2, whole=True, n_live=n)
+    if dtype != "fp8":
+        for b in range(B):
+            c.x[b, max(0, int(n[b])):] = float("nan")          # rows that do not count may hold anything
+            c.x64[b, max(0, int(n[b])):] = 0.0
+    c.check(c.run(flags), flags, exact=True)
+    n[:] = 0
+    c.kw["n_live"].zero_()
+    c.check(c.run(flags), flags, exact=True)
+
+
+@pytest.mark.parametrize("K,rank,dtype", [(7, 16, "bf16"), (100, 16, "bf16"), (64, 3, "bf16"), (33, 5, "f32"), (1, 1, "f32"),
+                                          (64, 12, "fp8"), (1001, 5, "f32")])
+def test_odd_sizes(K, rank, dtype):
+    c = Case(3, 13, K, 51, dtype, 2, rank, seed=3)
+    c.check(c.run(), SIMT)
+
+
+@pytest.mark.parametrize("dtype,flags", [("f32", 0), ("bf16", 0), ("bf16", SIMT)])
+@pytest.mark.parametrize("xpad,ypad,off", [(8, 0, 0), (0, 8, 0), (24, 3, 0), (3, 1, 0), (8, 8, 1), (64, 64, 8)])
+def test_strided_rows(dtype, flags, xpad, ypad, off):
+    """Rows that are parts of wider ones, at any alignment; what lies beside them stays."""
+    c = Case(3, 50, 128, 72, dtype, 2, 16, seed=4, whole=True)
+    wide = torch.zeros((3, 50, 128 + xpad + off), dtype=TYPE[dtype], device="cuda")
+    wide[..., off:off + 128] = c.x
+    c.x = wide[..., off:off + 128]
+    out = torch.full((3, 50, 72 + ypad + off), 5.0, dtype=TYPE[dtype], device="cuda")
+    got, st = kdtv.project(c.x, c.W, flags=flags, out=out[..., off:off + 72], **c.kw)
+    assert int(st) == 0
+    c.check(got.contiguous(), flags, exact=True)
+    assert (out[..., :off] == 5.0).all() and (out[..., off + 72:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype,flags", PATHS)
+def test_permuted_requests(dtype, flags):
+    """x [N, B, K] seen as [B, N, K], and requests in a buffer with gaps."""
+    if dtype == "fp8":
+        pytest.skip("one-byte rows are contiguous")
+    c = Case(5, 12, 64, 64, dtype, 2, 16, seed=5, whole=True)
+    c.x = c.x.transpose(0, 1).contiguous().transpose(0, 1)
+    c.check(c.run(flags), flags, exact=True)
+
+
+@pytest.mark.parametrize("dtype,flags", PATHS)
+def test_adapters_keep_to_their_requests(dtype, flags):
+    """Infinities and NaN in one adapter, or in one request's rows, reach no other request's output."""
+    B, K, M = 40, 128, 200
+    c = Case(B, 2, K, M, dtype, 5, 16, seed=6, whole=True, ids=np.arange(B) % 6 - 1)
+    clean = f64(c.run(flags))
+    for what in ("Bm", "A"):
+        keep = c.kw[what].clone()
+        c.kw[what][2, 3] = float("inf")
+        c.kw[what][2, 7] = float("nan")
+        c.kw[what][2, 9] = -float("inf")
+        got = f64(c.run(flags))
+        mine = c.ids == 2
+        assert np.array_equal(got[~mine], clean[~mine])
+        assert not np.isfinite(got[mine]).all()
+        c.kw[what].copy_(keep)
+    if dtype != "fp8":
+        c.x[7, 1] = float("nan")
+        got = f64(c.run(flags))
+        assert np.isnan(got[7, 1]).all()
+        got[7, 1] = clean[7, 1]
+        assert np.array_equal(got, clean)
+
+
+@pytest.mark.parametrize("dtype,flags", PATHS)
+def test_adapter_index_out_of_range(dtype, flags):
+    c = Case(9, 3, 64, 70, dtype, 2, 16, seed=7, whole=True, ids=[0, 1, -1, 2, 0, -2, 1, 2 ** 30, 0])
+    out = torch.full((9, 3, 70), 7.0, dtype=TYPE[dtype], device="cuda")
+    op = kdtv.Project(c.x, c.W, flags=flags, out=out, **c.kw)
+    op()
+    assert kdtv.STATUS[op.status()] == "KDTV_ERR_BAD_ADAPTER" and op.status() == 0
+    c.n = np.where(np.isin(np.arange(9), (3, 5, 7)), 0, 3)
+    c.o["adapter"] = np.where(c.n == 0, -1, c.ids)
+    c.check(out, flags, exact=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_extreme_scales(dtype):
+    """Sums far from 1, down to bf16's small values and up to its large ones, keep their relative error."""
+    for e in (-60, 50):
+        c = Case(2, 5, 128, 64, "bf16", 1, 16, seed=8, ids=[0, -1])
+        if dtype == "fp8":
+            c.dtype = "fp8"
+            c.W, ws = kdtv.quantise_weight(c.W)
+            c.x, xs = c._codes((c.x.float() * 2.0 ** e).to(torch.bfloat16))
+            c.kw.update(x_scale=xs, W_scale=ws)
+            c.x64, c.W64 = O.widen(c.x.cpu().numpy(), xs.cpu().numpy()), O.widen(c.W.cpu().numpy(), ws.cpu().numpy())
+        else:
+            c.x = (c.x.float() * 2.0 ** e).to(torch.bfloat16)
+            c.x64 = f64(c.x)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_deterministic_streams_and_capture(dtype):
+    c = Case(24, 8, 1024, 520, dtype, 7, 16, seed=9)
+    op = kdtv.Project(c.x, c.W, **c.kw)
+    first = op().clone()
+    for _ in range(20):
+        assert torch.equal(op(), first)
+    side = torch.cuda.Stream()
+    op.out.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    op(side)
+    side.synchronize()
+    assert torch.equal(op.out, first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        op()
+    op.out.zero_()
+    op.workspace.fill_(255)                                    # nothing in it outlives a call
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(op.out, first) and op.status() == 0
+    ids = c.kw["adapter"]
+    ids.copy_(ids.flip(0))
+    c.ids = ids.cpu().numpy()
+    c.o["adapter"] = c.ids
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(op.out, SIMT if dtype == "f32" else 0)
+
+
+def test_python_refusals():
+    c = Case(2, 3, 64, 40, "bf16", 2, 16, seed=10)
+    ok = dict(x=c.x, W=c.W, **c.kw)
+    bad = [dict(x=c.x.float()), dict(x=c.x.transpose(1, 2)), dict(W=c.W.t()), dict(W=c.W[:, :32]), dict(A=None), dict(Bm=None),
+           dict(A=c.kw["A"][:1]), dict(Bm=c.kw["Bm"].float()), dict(adapter=c.kw["adapter"].long()),
+           dict(adapter_scale=c.kw["adapter_scale"].double()), dict(x_scale=torch.zeros(2, 3, 2, dtype=torch.uint8, device="cuda")),
+           dict(out=torch.zeros(2, 3, 40, device="cuda")), dict(out=torch.zeros(2, 3, 1, dtype=torch.bfloat16, device="cuda").expand(2, 3, 40)),
+           dict(n_live=torch.zeros(3, dtype=torch.int32, device="cuda")), dict(x=c.x[:1, :1].expand(2, 3, 64))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            kdtv.project(**{**ok, **kw})
+    big = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(kdtv.KdtvError, match="UNSUPPORTED"):
+        kdtv.project(big, c.W, A=torch.zeros(1, 300, 64, dtype=torch.bfloat16, device="cuda"),
+                     Bm=torch.zeros(1, 40, 300, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        kdtv.quantise_weight(c.W[:, :33])
