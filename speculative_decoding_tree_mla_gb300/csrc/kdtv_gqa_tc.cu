@@ -73,6 +73,7 @@
 #include <cuda.h>
 
 #include "kdtv_gqa.cuh"
+#include "kdtv_guard.cuh"
 #include "kdtv_ptx.cuh"
 #include "kdtv_tmap.cuh"
 
@@ -160,12 +161,6 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];"
-      :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
-}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int x, int y, int z,
                                             int w) {
   asm volatile(
@@ -195,44 +190,6 @@ struct __align__(16) Piece {
   __device__ __forceinline__ bool later() const { return flags & 8; }    // not at the CTA's first unit
 };
 constexpr int kEnd = 16;     // flag: no piece is left
-
-// ---- bounded waits -------------------------------------------------------------------------
-struct Guard {
-  volatile uint32_t* abort;      // shared memory
-  unsigned int* status;
-  uint32_t limit;                // ns, below 2^32
-};
-__device__ __forceinline__ uint32_t timer_lo() {
-  uint32_t t;
-  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-  return t;
-}
-// Short code: a wait stands at some thirty places of loops that share an
-// instruction cache.
-__device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
-  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
-  const uint32_t t0 = timer_lo();
-#pragma unroll 1
-  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
-    if (*g.abort) return false;
-    if (timer_lo() - t0 > g.limit) {
-      atomicExch(g.status, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);   // over any other code: the combine kernel asks
-      *g.abort = 1u;
-      return false;
-    }
-  }
-  return true;
-}
-// Waits for asynchronous work that is in flight and will finish (limited all the same).
-__device__ __forceinline__ void drain(const Guard& g, uint32_t bar, uint32_t parity) {
-  const uint32_t t0 = timer_lo();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity))
-    if (timer_lo() - t0 > g.limit) return;
-}
-__device__ __forceinline__ bool wait_warp(const Guard& g, uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait(g, bar, parity));
-}
 
 // Four E4M3 bytes as bf16 pairs of their values times 2^-120: a code's exponent
 // and mantissa bits moved to bf16's places (also of its subnormals, which become

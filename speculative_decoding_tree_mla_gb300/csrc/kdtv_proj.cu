@@ -207,8 +207,22 @@ int check_dims(const kdtv_project_dims* d) {
   return KDTV_OK;
 }
 
+int sm_count() { return device_sm_count() > 0 ? device_sm_count() : 152; }
+
+// For either path: which one runs depends on addresses too.
 size_t workspace_of(const kdtv_project_dims* d) {
-  return align256((size_t)d->B * d->N * (d->adapters > 0 ? d->rank : 0) * sizeof(float)) + 256;
+  ProjArgs a;
+  memset(&a, 0, sizeof(a));
+  const size_t low = (size_t)d->B * d->N * (d->adapters > 0 ? d->rank : 0) * sizeof(float);
+  const size_t tc = proj_tc_sizes(d, sm_count(), &a) ? proj_tc_workspace(a, sm_count()) : 0;
+  return align256(low > tc ? low : tc) + 256;
+}
+
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Rows that TMA can read: strides (of what has more than one element) multiples of 16 bytes, not 0.
+bool tma_rows(const kdtv_project_dims* d, const ProjArgs& a) {
+  if (d->dtype == KDTV_BF16_FP8KV) return true;          // contiguous
+  return (d->N == 1 || (a.xs[1] > 0 && a.xs[1] % 8 == 0)) && (d->B == 1 || (a.xs[0] > 0 && a.xs[0] % 8 == 0));
 }
 
 }  // namespace
@@ -221,7 +235,10 @@ extern "C" size_t kdtv_project_workspace_size(const kdtv_project_dims* d) {
 }
 
 extern "C" int kdtv_project_launches_per_call(const kdtv_project_dims* d) {
-  return check_dims(d) == KDTV_OK ? 1 + (d->adapters > 0) : -1;
+  if (check_dims(d) != KDTV_OK) return -1;
+  ProjArgs a;
+  memset(&a, 0, sizeof(a));
+  return proj_tc_sizes(d, sm_count(), &a) ? 2 * proj_tc_launches(a) : 1 + (d->adapters > 0);
 }
 
 extern "C" int kdtv_project(const kdtv_project_dims* d, const void* x, const uint8_t* x_scale,
@@ -253,7 +270,9 @@ extern "C" int kdtv_project(const kdtv_project_dims* d, const void* x, const uin
   a.ys[1] = gy ? d->y_stride[1] : d->d_out;
   a.by_N = divisor((unsigned)d->N);
   a.low = static_cast<float*>(d->workspace);
-  const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
+  const int sms = sm_count();
+  if (aligned(x) && aligned(W) && aligned(A) && aligned(Bm) && tma_rows(d, a) && proj_tc_sizes(d, sms, &a))
+    return launch_proj_tc(a, sms, d->flags & KDTV_FLAG_TEST_STALL, stream);
   if (d->dtype == KDTV_F32) return launch_simt<float, float>(a, sms, stream);
   if (d->dtype == KDTV_BF16) return launch_simt<__nv_bfloat16, __nv_bfloat16>(a, sms, stream);
   return launch_simt<__nv_fp8_e4m3, __nv_bfloat16>(a, sms, stream);

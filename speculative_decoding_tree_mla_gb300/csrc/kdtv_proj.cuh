@@ -17,6 +17,21 @@ struct ProjArgs {
   long long xs[2], ys[2];                  // elements between requests, rows
   Divisor by_N;
   float* low;                              // CUDA cores: s_a A_a x, [B * N, R]
+
+  // Tensor cores.  A token tile is `requests` requests times `rows` rows of each (one of them is 1, or
+  // all rows of several requests are in a tile); its columns are request-major.
+  int requests, rows, blocks, groups;      // row blocks of a request, groups of requests
+  int cols;                                // columns of a tile, a multiple of 16
+  int base;                                // units (128 bytes of d_in each) of a tile without adapters
+  int chunks;                              // 16-rank chunks of an adapter
+  int pairs;                               // most pairs of chunks that a tile may have
+  int features;                            // 128-row tiles of W
+  int stages, scale_mode;                  // ring entries; how scale rows may be read
+  char* parts;                             // A x in two bf16 parts: [tile][pair][chunk][part][cols][16]
+  float* partial;                          // [2 * CTAs][cols][128] sums of cut tiles
+  unsigned int* counters;                  // [2 * CTAs] segments of a cut tile that are done
+  int n_counters;
+  Divisor by_requests, by_rows, by_chunks;
 };
 
 __device__ __forceinline__ void proj_error(const ProjArgs& a, unsigned int code) { atomicCAS(a.status, 0u, code); }
@@ -29,5 +44,14 @@ __device__ __forceinline__ int proj_adapter(const ProjArgs& a, int b) {
   proj_error(a, KDTV_ERR_BAD_ADAPTER);
   return -2;
 }
+
+// Bytes of A x of one pair of chunks.
+__host__ __device__ inline long long proj_pair_bytes(const ProjArgs& a) { return (long long)a.cols * 128; }
+
+// Whether the tensor cores take these sizes, and the tiles; the workspace they need.
+bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a);
+size_t proj_tc_workspace(const ProjArgs& a, int sms);
+int proj_tc_launches(const ProjArgs& a);      // ranges of requests, of two kernels each
+int launch_proj_tc(const ProjArgs& a, int sms, bool stall, cudaStream_t st);
 
 }  // namespace kdtv

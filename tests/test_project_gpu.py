@@ -250,6 +250,26 @@ def test_deterministic_streams_and_capture(dtype):
     c.check(op.out, SIMT if dtype == "f32" else 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_a_wait_that_runs_out_is_reported(dtype):
+    """A stalled pipeline ends within its limit, says so, and the next call works."""
+    c = Case(6, 8, 512, 300, dtype, 3, 16, seed=11, whole=True)
+    out = torch.full((6, 8, 300), 7.0, dtype=torch.bfloat16, device="cuda")
+    op = kdtv.Project(c.x, c.W, flags=kdtv.KDTV_FLAG_TEST_STALL, out=out, **c.kw)
+    op()
+    assert kdtv.STATUS[op.status()] == "KDTV_ERR_DEVICE_TIMEOUT"
+    assert (out == 7.0).all()
+    c.check(c.run(), exact=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,N,K,M", [(1100, 130, 32, 24), (2500, 1, 2048, 40), (5, 64, 4096, 1280), (40, 1, 4096, 2560), (1, 1, 8192, 2000)])
+def test_many_requests_and_cut_tiles(dtype, B, N, K, M):
+    """More groups of requests than one launch plans; tiles whose d_in is shared by several CTAs."""
+    c = Case(B, N, K, M, dtype, 6, 8, seed=12, whole=True)
+    c.check(c.run(), exact=True)
+
+
 def test_python_refusals():
     c = Case(2, 3, 64, 40, "bf16", 2, 16, seed=10)
     ok = dict(x=c.x, W=c.W, **c.kw)
