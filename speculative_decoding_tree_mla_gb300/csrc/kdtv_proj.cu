@@ -238,7 +238,7 @@ extern "C" int kdtv_project_launches_per_call(const kdtv_project_dims* d) {
   if (check_dims(d) != KDTV_OK) return -1;
   ProjArgs a;
   memset(&a, 0, sizeof(a));
-  return proj_tc_sizes(d, sm_count(), &a) ? 2 * proj_tc_launches(a) : 1 + (d->adapters > 0);
+  return proj_tc_sizes(d, sm_count(), &a) ? proj_tc_launches(a) : 1 + (d->adapters > 0);
 }
 
 extern "C" int kdtv_project(const kdtv_project_dims* d, const void* x, const uint8_t* x_scale,

@@ -16,11 +16,14 @@
 // launched while the first runs; only the adapters' units wait for it.
 //
 // Work.  A unit is 128 bytes of d_in (64 bf16, 128 one-byte elements) or two
-// chunks of 16 ranks, for one tile of 128 outputs and up to 256 (one byte: 224)
-// tokens.  Whole tiles go round the CTAs; what does not fill a round is cut
-// evenly by units (at least one round, so that no CTA gets little).  A tile
-// that several CTAs share: each leaves its sums, and the last to come adds them in
-// the order of the units, so that the result does not depend on who that is.
+// chunks of 16 ranks, for one tile of 256 outputs and up to 256 (one byte: 224)
+// tokens.  A pair of CTAs works on a tile: each has 128 outputs, loads those rows
+// of W and half of the tokens, and the products read both halves (cta_group::2), so
+// that a unit costs each SM 32 KiB where a CTA by itself with as many products
+// would load 48.  Whole tiles go round the pairs; what does not fill a round is
+// cut evenly by units (at least one round, so that no pair gets little).  A tile
+// that several pairs share: each leaves its sums, and proj_combine_kernel adds them in
+// the order of the units.
 //
 // One byte: exponent bytes travel as they are to the tensor cores, which take
 // one per 32 elements and operand row (block-scaled products), so sums are in true
@@ -34,17 +37,19 @@
 
 #include <string.h>
 
+#include <type_traits>
+
 namespace kdtv {
 namespace {
 
 using namespace ptx;
 
-constexpr int kFeatures = 128;             // outputs of a tile
+constexpr int kFeatures = 128;             // outputs of a CTA: half of a tile
 constexpr int kUnitBytes = 128;            // of d_in in a unit
 constexpr int kWBytes = kFeatures * kUnitBytes;
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 1024;           // groups of requests in a launch
-constexpr int kMaxCtas = 256;
+constexpr int kMaxPairs = 128;
 constexpr int kWords = KDTV_MAX_ADAPTERS / 32;
 constexpr int kScaleBytes = 3 * 512;       // a stage's exponent bytes: W, tokens 0 - 127, the others
 constexpr int kSuper = 8;                  // token tiles that share a W tile in a row
@@ -72,14 +77,60 @@ __device__ __forceinline__ int group_bitmap(const ProjArgs& a, int g, uint32_t* 
   return warp_sum(count);
 }
 
+// A request's n rows in blocks as even as they can be, so that its last one is not a small rest: rows of half a
+// block.  (Tiles of several requests: all N rows.)
+__device__ __forceinline__ int half_rows_of(const ProjArgs& a, int n) {
+  if (!a.by_rows_of) return a.N;
+  const int blocks = max(1, (n + 2 * a.half_rows - 1) / (2 * a.half_rows));
+  return max(1, ((n + blocks - 1) / blocks + 1) / 2);
+}
+// Columns of half a tile whose half blocks have hr rows.
+__device__ __forceinline__ int half_cols_of(const ProjArgs& a, int hr) { return (a.half_requests * hr + 15) & ~15; }
+
+// The request and row of a tile's column; false: the column is not in use.
+__device__ __forceinline__ bool column(const ProjArgs& a, int g, int j, int hr, int c, int* b, int* i) {
+  const int hc = half_cols_of(a, hr), h = c >= hc, e = c - (h ? hc : 0);
+  if (a.by_rows_of) {
+    *b = g;
+    *i = (2 * j + h) * hr + e;
+    return e < hr && *i < a.N;
+  }
+  const int rq = (int)divide(e, a.by_N);
+  *b = g * a.requests + h * a.half_requests + rq;
+  *i = e - rq * a.N;
+  return rq < a.half_requests && *b < a.B;
+}
+// Where the 16 ranks of chunk c, part p of row i of request b start; their two 16-byte halves lie swizzled: `flip`
+// is the one that comes second.  hr: of the request.
+__device__ __forceinline__ char* part_row(const ProjArgs& a, int b, int i, int hr, int c, int p, int* flip) {
+  int g, j, h, col;
+  if (a.by_rows_of) {
+    g = b;
+    const int half = i / hr;
+    j = half >> 1;
+    h = half & 1;
+    col = i - half * hr;
+  } else {
+    g = (int)divide(b, a.by_requests);
+    const int rq = b - g * a.requests;
+    j = 0;
+    h = rq >= a.half_requests;
+    col = (rq - (h ? a.half_requests : 0)) * a.N + i;
+  }
+  *flip = (col >> 2) & 1;
+  return a.parts + (((long long)(g * a.blocks + j) * a.pairs + (c >> 1)) * 2 + h) * proj_half_bytes(a) +
+         (long long)((c & 1) * 2 + p) * a.half_cols * 32 + col * 32;
+}
+
 // ---- v = s_a A_a x ---------------------------------------------------------------------------
 // mma.sync products of 16 ranks and 8 tokens, straight from global memory: the
 // order of d_in within a product does not matter as long as both operands have
 // the same, so a lane's 16-byte load (8 elements of a row) is two products'
 // fragments.  A warp has 16 MR ranks, 8 NT tokens and every KW-th 32 elements
-// of d_in; KW warps' sums meet in shared memory, in their order.  Bound by the
-// latency of its loads (few tokens) or L2 (many); it runs beside the
-// first units of the projection.
+// of d_in, the next U of them on their way while it multiplies; KW warps' sums
+// meet in shared memory, in a fixed order.  It runs beside the first units of the
+// projection, whose CTAs need the other half of the registers, and is bound by the
+// latency of its loads.
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -100,22 +151,19 @@ __device__ __forceinline__ uint4 widen8(uint2 w, uint32_t byte) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <bool kOneByte, int MR, int NT, int TW, int KW>
-__global__ void __launch_bounds__(32 * TW * KW) proj_low_kernel(const __grid_constant__ ProjArgs a) {
+template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
+__global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_constant__ ProjArgs a) {
   __shared__ uint32_t bits[kWords];
   __shared__ int s_slot, s_slots;
-  __shared__ float red[(KW - 1) * TW][MR * NT * 4][32];
+  __shared__ float red[KW / 2 * TW][MR * NT * 4][32];
   grid_dep_launch();                 // the projection may be launched; its adapters' units wait for this grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-    for (int i = threadIdx.x; i < a.n_counters; i += 32 * TW * KW) a.counters[i] = 0u;
-  if (!a.adapter) return;
   constexpr int kTokens = 8 * NT * TW;
   const int b = blockIdx.z, i0 = blockIdx.x * kTokens, n = live_rows(a.n_live, b, a.N);
   if (i0 >= n) return;
   const int id = proj_adapter(a, b);
   if (id == -2) return;
-  const int g = (int)divide(b, a.by_requests), rq = b - g * a.requests;
+  const int g = (int)divide(b, a.by_requests), hr = half_rows_of(a, n);
   if (a.requests == 1) {
     if (id < 0) return;
     if (threadIdx.x == 0) s_slot = 0, s_slots = 1;
@@ -130,11 +178,10 @@ __global__ void __launch_bounds__(32 * TW * KW) proj_low_kernel(const __grid_con
   }
   __syncthreads();
   const int first = s_slot * a.chunks, chunks = s_slots * a.chunks, rows = min(kTokens, n - i0);
-  // Where row i's 16 ranks of chunk c, part p start; its two 16-byte halves h lie swizzled.
   auto place = [&](int i, int c, int p, int h) {
-    const int j = (int)divide(i, a.by_rows), col = rq * a.rows + i - j * a.rows;
-    return a.parts + ((long long)(g * a.blocks + j) * a.pairs + (c >> 1)) * proj_pair_bytes(a) +
-           (long long)((c & 1) * 2 + p) * a.cols * 32 + col * 32 + ((h ^ ((col >> 2) & 1)) << 4);
+    int flip;
+    char* at = part_row(a, b, i, hr, c, p, &flip);
+    return at + ((h ^ flip) << 4);
   };
   if (blockIdx.y == 0 && a.requests > 1) {              // the other adapters' chunks
     const int others = chunks - (id < 0 ? 0 : a.chunks);
@@ -155,9 +202,13 @@ __global__ void __launch_bounds__(32 * TW * KW) proj_low_kernel(const __grid_con
     const char* x = static_cast<const char*>(a.x) + (b * a.xs[0] + (t0 + gr) * a.xs[1] + 8 * q) * (kOneByte ? 1 : 2);
     const uint8_t* xe = a.x_scale + ((long long)b * a.N + t0 + gr) * (a.K / KDTV_GROUP);
     const long long xrow = 8 * a.xs[1] * (kOneByte ? 1 : 2);
-    constexpr int U = MR * NT >= 8 ? 1 : 4;               // steps whose loads are under way together
-    for (int k0 = kw * 32; k0 < a.K; k0 += KW * 32 * U) {
-      uint4 va[U][MR][2], vx[U][NT];
+    struct Step {
+      uint4 a[U][MR][2];
+      typename std::conditional<kOneByte, uint2, uint4>::type x[U][NT];
+      uint32_t e[U][NT];
+    };
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    auto load = [&](Step& s, int k0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * KW * 32;
@@ -166,38 +217,65 @@ __global__ void __launch_bounds__(32 * TW * KW) proj_low_kernel(const __grid_con
         for (int m = 0; m < MR; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            va[u][m][h] = in && rank0 + 16 * m + 8 * h + gr < a.R
-                              ? *reinterpret_cast<const uint4*>(A + (long long)(16 * m + 8 * h) * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
+            s.a[u][m][h] = in && rank0 + 16 * m + 8 * h + gr < a.R
+                               ? *reinterpret_cast<const uint4*>(A + (long long)(16 * m + 8 * h) * a.K + k) : none;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const bool on = in && t0 + 8 * j + gr < n;
           if constexpr (kOneByte) {
-            const uint2 w = on ? *reinterpret_cast<const uint2*>(x + j * xrow + k) : make_uint2(0u, 0u);
-            vx[u][j] = widen8(w, on ? xe[(long long)8 * j * (a.K / KDTV_GROUP) + k / KDTV_GROUP] : 127u);
+            s.x[u][j] = on ? *reinterpret_cast<const uint2*>(x + j * xrow + k) : make_uint2(0u, 0u);
+            s.e[u][j] = on ? xe[(long long)8 * j * (a.K / KDTV_GROUP) + k / KDTV_GROUP] : 127u;
           } else {
-            vx[u][j] = on ? *reinterpret_cast<const uint4*>(x + j * xrow + 2 * k) : make_uint4(0u, 0u, 0u, 0u);
+            s.x[u][j] = on ? *reinterpret_cast<const uint4*>(x + j * xrow + 2 * k) : none;
           }
         }
       }
+    };
+    auto multiply = [&](const Step& s) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int m = 0; m < MR; ++m)
+        for (int j = 0; j < NT; ++j) {
+          uint4 v;
+          if constexpr (kOneByte) v = widen8(s.x[u][j], s.e[u][j]);
+          else v = s.x[u][j];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma_16x8x16(acc[m][j], va[u][m][0].x, va[u][m][1].x, va[u][m][0].y, va[u][m][1].y, vx[u][j].x, vx[u][j].y);
-            mma_16x8x16(acc[m][j], va[u][m][0].z, va[u][m][1].z, va[u][m][0].w, va[u][m][1].w, vx[u][j].z, vx[u][j].w);
+          for (int m = 0; m < MR; ++m) {
+            mma_16x8x16(acc[m][j], s.a[u][m][0].x, s.a[u][m][1].x, s.a[u][m][0].y, s.a[u][m][1].y, v.x, v.y);
+            mma_16x8x16(acc[m][j], s.a[u][m][0].z, s.a[u][m][1].z, s.a[u][m][0].w, s.a[u][m][1].w, v.z, v.w);
           }
+        }
+    };
+    constexpr int kStride = KW * 32 * U;
+    Step s0, s1;
+    load(s0, kw * 32);
+#pragma unroll 1
+    for (int k0 = kw * 32; k0 < a.K; k0 += 2 * kStride) {      // (loads behind d_in are zeros)
+      load(s1, k0 + kStride);
+      multiply(s0);
+      load(s0, k0 + 2 * kStride);
+      multiply(s1);
     }
-    if (kw > 0)
+  }
+#pragma unroll
+  for (int half = KW / 2; half > 0; half /= 2) {        // the upper half's sums to the lower half
+    if (kw >= half && kw < 2 * half)
 #pragma unroll
       for (int m = 0; m < MR; ++m)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) red[(kw - 1) * TW + tw][(m * NT + j) * 4 + k][lane] = acc[m][j][k];
+          for (int k = 0; k < 4; ++k) red[(kw - half) * TW + tw][(m * NT + j) * 4 + k][lane] = acc[m][j][k];
+    __syncthreads();
+    if (kw < half)
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][j][k] += red[kw * TW + tw][(m * NT + j) * 4 + k][lane];
+    __syncthreads();
   }
-  __syncthreads();
   if (kw > 0 || !busy) return;
   const float s = a.adapter_scale ? a.adapter_scale[id] : 1.f;
 #pragma unroll
@@ -206,9 +284,7 @@ __global__ void __launch_bounds__(32 * TW * KW) proj_low_kernel(const __grid_con
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float v = acc[m][j][k];
-        for (int w = 0; w < KW - 1; ++w) v += red[w * TW + tw][(m * NT + j) * 4 + k][lane];
-        v *= s;
+        const float v = s * acc[m][j][k];
         const int rank = rank0 + 16 * m + gr + (k >> 1) * 8, i = t0 + 8 * j + 2 * q + (k & 1), c = rank >> 4;
         if (i >= n || c >= a.chunks) continue;
         const __nv_bfloat16 hi = __float2bfloat16_rn(v);
@@ -223,10 +299,17 @@ __global__ void __launch_bounds__(32 * TW * KW) proj_low_kernel(const __grid_con
 // ---- the projection --------------------------------------------------------------------------
 enum {
   B_FULL = 0, B_EMPTY = B_FULL + kMaxStages, B_ACC_FULL = B_EMPTY + kMaxStages, B_ACC_EMPTY = B_ACC_FULL + 2,
-  B_DONE = B_ACC_EMPTY + 2, B_STALL, B_COUNT
+  B_DONE = B_ACC_EMPTY + 2, B_STALL, B_SCALES, B_PEER = B_SCALES + kMaxStages, B_COUNT = B_PEER + kMaxStages
 };
 
-constexpr int kWarpTma = 0, kWarpMma = 1, kWarpOut = 4, kWarpScale = 8;   // (2, 3: planning only)
+// Arrivals of a barrier's phase.
+__device__ __forceinline__ uint32_t arrivals(bool one_byte, int i) {
+  if (i < B_EMPTY) return one_byte ? 7 : 2;                 // both producers; four warps here, the peer's as one
+  if (i >= B_ACC_EMPTY && i < B_DONE) return 8;             // both CTAs' four warps
+  return i >= B_SCALES && i < B_PEER ? 4 : 1;
+}
+
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpOut = 4, kWarpScale = 8;   // (2, 3: one byte: relays)
 __host__ __device__ constexpr int threads_of(bool one_byte) { return one_byte ? 384 : 256; }
 __host__ __device__ constexpr int acc_columns(bool one_byte) { return one_byte ? 224 : 256; }
 constexpr uint32_t kScaleColumn = 448;      // one byte: exponents behind the two accumulators
@@ -234,11 +317,11 @@ constexpr uint32_t kScaleColumn = 448;      // one byte: exponents behind the tw
 // Shared memory behind the ring.
 struct ProjShared {
   uint64_t bars[B_COUNT];
-  uint32_t tmem, abort, last[2];
-  int total_tiles, cut, share, pad;         // token tiles times outputs' tiles; cut tiles; units of a CTA's share
+  uint32_t tmem, abort;
+  int total_tiles, cut, share, pad;         // token tiles times outputs' tiles; cut tiles; units of a pair's share
   int first[kMaxGroups + 1];                // token tiles before each group
-  int chunks[kMaxGroups];                   // 16-rank chunks of its tiles' adapters
-  int start[2 * kMaxCtas + 1];              // units before each cut tile
+  uint32_t tile[kMaxGroups];                // 16-rank chunks of its tiles' adapters, and 2^20 rows of half a block
+  int start[2 * kMaxPairs + 1];              // units before each cut tile
   long long y_at[256];                      // offset of each column's output row, -1: none
   uint32_t bits[kWords];
   uint16_t ids[256];                        // the adapters of the producer's tile
@@ -246,16 +329,18 @@ struct ProjShared {
 
 // A part of a tile: units k0 .. k1 - 1; behind a.base of d_in come pairs of chunks.
 struct Item {
-  int g, j, f, k0, k1, chunks;
+  int g, j, f, k0, k1, chunks, hr;
   int cut, seg, segs;                       // cut tile's number (-1: whole), place among its segments
 };
 
-// The items of CTA c, in the order in which every role sees them: its share of
+// The items of pair c, in the order in which every role sees them: its share of
 // the cut tiles, then whole tiles.
 struct Walk {
   int u, u_end, tile, s;                    // next unit of the share, next whole tile, current cut tile
 };
 
+// Tiles of few units are not cut.
+__host__ __device__ __forceinline__ bool may_cut(const ProjArgs& a) { return a.base >= 16; }
 __device__ __forceinline__ int units_of(const ProjArgs& a, int chunks) { return a.base + (chunks + 1) / 2; }
 
 __device__ __forceinline__ void locate(const ProjArgs& a, const ProjShared& sh, int order, Item& it) {
@@ -271,15 +356,16 @@ __device__ __forceinline__ void locate(const ProjArgs& a, const ProjShared& sh, 
   }
   it.g = lo;
   it.j = t - sh.first[lo];
-  it.chunks = sh.chunks[lo];
+  it.chunks = (int)(sh.tile[lo] & 0xfffffu);
+  it.hr = (int)(sh.tile[lo] >> 20);
 }
 
 __device__ __forceinline__ Walk walk(const ProjShared& sh) {
   Walk w;
   const int all = sh.cut ? sh.start[sh.cut] : 0;
-  w.u = min(all, (int)blockIdx.x * sh.share);
+  w.u = min(all, (int)(blockIdx.x >> 1) * sh.share);
   w.u_end = min(all, w.u + sh.share);
-  w.tile = sh.cut + blockIdx.x;
+  w.tile = sh.cut + (blockIdx.x >> 1);
   int lo = 0, hi = sh.cut - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -298,7 +384,7 @@ __device__ __forceinline__ bool next(const ProjArgs& a, const ProjShared& sh, Wa
     it.k1 = stop - start;
     const int c0 = start / sh.share;
     it.segs = (end - 1) / sh.share - c0 + 1;
-    it.seg = (int)blockIdx.x - c0;
+    it.seg = (int)(blockIdx.x >> 1) - c0;
     it.cut = it.segs > 1 ? w.s : -1;
     w.u = stop;
     if (stop == end) ++w.s;
@@ -311,14 +397,30 @@ __device__ __forceinline__ bool next(const ProjArgs& a, const ProjShared& sh, Wa
   it.cut = -1;
   it.seg = 0;
   it.segs = 1;
-  w.tile += gridDim.x;
+  w.tile += gridDim.x >> 1;
   return true;
 }
 
-// Partial of segment `seg` of a cut tile whose first segment is CTA c0's: a CTA has two
-// places, one for the tile that its share begins in.
-__device__ __forceinline__ float* partial_of(const ProjArgs& a, int c0, int seg) {
-  return a.partial + (2ll * (c0 + seg) + (seg == 0 ? 1 : 0)) * a.cols * kFeatures;
+// Pair c's sums of segment `seg` of a cut tile, those of CTA `rank`: a pair has two places, one for the tile
+// that its share begins in.
+__device__ __forceinline__ float* partial_of(const ProjArgs& a, int c, int seg, int rank) {
+  return a.partial + ((2ll * c + (seg == 0 ? 1 : 0)) * 2 + rank) * (2 * a.half_cols) * kFeatures;
+}
+
+// What the combine kernel needs to know of a cut tile; a.plan holds their number, then these.
+struct __align__(16) CutTile {
+  int first, segs, g, j;                    // pair of the first segment (segs 1: whole, nothing to do)
+  int f, chunks, hr, pad;
+};
+__device__ __forceinline__ void leave_plan(const ProjArgs& a, const ProjShared& sh, int t) {
+  if (t == 0) a.plan[0] = sh.cut;
+  CutTile* out = reinterpret_cast<CutTile*>(a.plan + 4);
+  for (int s = t; s < sh.cut; s += 128) {
+    Item it;
+    locate(a, sh, s, it);
+    const int first = sh.start[s] / sh.share;
+    out[s] = CutTile{first, (sh.start[s + 1] - 1) / sh.share - first + 1, it.g, it.j, it.f, it.chunks, it.hr, 0};
+  }
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T of E4M3 elements with an exponent
@@ -327,28 +429,23 @@ __device__ __forceinline__ void mma_scaled(uint32_t d_tmem, uint64_t a_desc, uin
                                            uint32_t a_scale, uint32_t b_scale, uint32_t accumulate) {
   asm volatile("{\n\t.reg .pred p;\n\t"
                "setp.ne.b32 p, %6, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+               "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
                :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
                : "memory");
 }
 // E4M3 A and B, exponent bytes as scales; bits 4 and 29 on: which byte of a word.
 __device__ __forceinline__ uint32_t idesc_scaled(int N, int byte) {
-  return ((uint32_t)byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(kFeatures >> 4) << 24) |
+  return ((uint32_t)byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(2 * kFeatures >> 4) << 24) |
          ((uint32_t)byte << 29);
 }
-// 512 bytes of exponents: four words of 32 lanes, the same in each quarter of TMEM's lanes.
+// 512 bytes of exponents, of each CTA: four words of 32 lanes, the same in each quarter of TMEM's lanes.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
   uint64_t d = 0;                           // no swizzle, 8-row groups 128 bytes apart
   d |= (uint64_t)((smem >> 4) & 0x3FFFu);
   d |= (uint64_t)(128u >> 4) << 32;
   d |= (uint64_t)1u << 46;
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(d) : "memory");
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(d) : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-
 // One output by itself, for a value that is not finite where several adapters share a tile.
 template <bool kOneByte>
 __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
@@ -370,7 +467,7 @@ __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
   const int id = a.adapter[b];
   if (id < 0) return sum;
   // this request's v, from its place among the tile's adapters
-  const int g = (int)divide(b, a.by_requests), col = (b - g * a.requests) * a.rows + i;
+  const int g = (int)divide(b, a.by_requests);
   int slot = 0;
   for (int c = g * a.requests; c < min(a.B, (g + 1) * a.requests); ++c) {
     const int other = a.adapter[c];
@@ -381,48 +478,57 @@ __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
   }
   for (int r = 0; r < a.R; ++r) {
     const int c = slot * a.chunks + (r >> 4);
-    const char* at = a.parts + ((long long)g * a.pairs + (c >> 1)) * proj_pair_bytes(a) +
-                     (long long)(c & 1) * 2 * a.cols * 32 + col * 32 + ((((r >> 3) & 1) ^ ((col >> 2) & 1)) << 4) + (r & 7) * 2;
-    const float v = to_f32(*reinterpret_cast<const __nv_bfloat16*>(at)) +
-                    to_f32(*reinterpret_cast<const __nv_bfloat16*>(at + (long long)a.cols * 32));
+    int flip;
+    const char* hi = part_row(a, b, i, half_rows_of(a, live_rows(a.n_live, b, a.N)), c, 0, &flip);
+    hi += (((r >> 3) & 1) ^ flip) * 16 + (r & 7) * 2;
+    const float v = to_f32(*reinterpret_cast<const __nv_bfloat16*>(hi)) +
+                    to_f32(*reinterpret_cast<const __nv_bfloat16*>(hi + (long long)a.half_cols * 32));
     sum = fmaf(v, to_f32(static_cast<const __nv_bfloat16*>(a.Bm)[((long long)id * a.M + f) * a.R + r]), sum);
   }
   return sum;
 }
 
+// (Registers for two blocks, although shared memory has room for one: the first kernel's are beside it.)
 template <bool kOneByte>
-__global__ void __launch_bounds__(threads_of(kOneByte), 1)
+__global__ void __launch_bounds__(threads_of(kOneByte), 2)
 proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-               const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ ProjArgs a, int stall) {
+               const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ ProjArgs a, int stall) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int x_bytes = a.cols * kUnitBytes, stage_bytes = kWBytes + x_bytes;
+  const int stage_bytes = kWBytes + a.half_cols * kUnitBytes;
+  const uint32_t rank = cluster_ctarank();
   ProjShared& sh = *reinterpret_cast<ProjShared*>(smem + (size_t)a.stages * (stage_bytes + (kOneByte ? kScaleBytes : 0)));
   const uint32_t ring = smem_u32(smem), scales = ring + a.stages * stage_bytes, bars = smem_u32(sh.bars);
   auto BAR = [&](int i) { return bars + 8u * i; };
   const Guard guard{&sh.abort, a.status, stall ? 20000000u : 2000000000u};
+  grid_dep_launch();                           // the combine kernel may be launched; it waits for this grid
 
   // ---- set up, and plan: every CTA derives the same tiles from n_live and adapter ------------------
   if (threadIdx.x < B_COUNT) {
     const int i = threadIdx.x;
-    mbar_init(BAR(i), i < B_EMPTY ? (kOneByte ? 5 : 1) : i >= B_ACC_EMPTY && i < B_DONE ? 4 : 1);
+    mbar_init(BAR(i), arrivals(kOneByte, i));
   }
   if (threadIdx.x == 0) sh.abort = 0u;
   fence_mbar_init();
   if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(&sh.tmem), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&sh.tmem), 512);
+    tmem_relinquish_pair();
   }
   if (warp == kWarpTma && lane == 0) {
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_x);
-    if (a.adapter) prefetch_tmap(&tm_b);
+    if (a.adapter) {
+      prefetch_tmap(&tm_b);
+      prefetch_tmap(&tm_v);
+    }
   }
   if (a.requests == 1) {
     for (int g = threadIdx.x; g < a.groups; g += threads_of(kOneByte)) {
       const int n = live_rows(a.n_live, g, a.N), id = n > 0 ? proj_adapter(a, g) : -1;
-      sh.first[g] = id == -2 ? 0 : (int)divide(n + a.rows - 1, a.by_rows);
-      sh.chunks[g] = id >= 0 ? a.chunks : 0;
+      const int hr = half_rows_of(a, n);
+      sh.first[g] = id == -2 ? 0 : (n + 2 * hr - 1) / (2 * hr);
+      sh.tile[g] = (id >= 0 ? (uint32_t)a.chunks : 0u) | ((uint32_t)hr << 20);
     }
   } else {
     uint32_t* bits = reinterpret_cast<uint32_t*>(smem) + warp * kWords;     // (the ring is not in use yet)
@@ -432,7 +538,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       __syncwarp();
       if (lane == 0) {
         sh.first[g] = live ? 1 : 0;
-        sh.chunks[g] = slots * a.chunks;
+        sh.tile[g] = (uint32_t)(slots * a.chunks) | ((uint32_t)a.N << 20);
       }
     }
     fence_async_smem();
@@ -457,9 +563,9 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     __syncwarp();
     // Whole rounds of whole tiles but the last, and what is left cut into equal shares.  Tiles of few
     // units are not cut, nor are almost full rounds.
-    const int tiles = sum * a.features, ctas = gridDim.x;
-    int cut = tiles % ctas == 0 ? 0 : tiles < 2 * ctas ? tiles : tiles % ctas + ctas;
-    if (a.base < 16 || (tiles < ctas && tiles * 20 > ctas * 19)) cut = 0;
+    const int tiles = sum * a.features, pairs = gridDim.x >> 1;
+    int cut = tiles % pairs == 0 ? 0 : tiles < 2 * pairs ? tiles : tiles % pairs + pairs;
+    if (!may_cut(a) || (tiles < pairs && tiles * 20 > pairs * 19)) cut = 0;
     Item it;
     int u = 0;
     for (int t0 = 0; t0 < cut; t0 += 32) {
@@ -481,11 +587,14 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       sh.start[cut] = u;
       sh.cut = cut;
       sh.total_tiles = tiles;
-      sh.share = max(8, (u + ctas - 1) / ctas);
+      sh.share = max(8, (u + pairs - 1) / pairs);
     }
   }
   __syncthreads();
+  cluster_sync();                              // the pair's barriers are set up
   const uint32_t tmem = sh.tmem;
+  const uint32_t lead = mapa(bars, 0);         // the first CTA's barriers: it issues the products
+  auto LEAD = [&](int i) { return lead + 8u * i; };
   Walk w = walk(sh);
   Item it;
   int slot = 0;
@@ -534,20 +643,22 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           waited = true;
         }
         if (lane == 0) {
-          const uint32_t full = BAR(B_FULL + slot), dst = ring + slot * stage_bytes;
+          const uint32_t full = LEAD(B_FULL + slot), dst = ring + slot * stage_bytes;
+          const int f = (2 * it.f + rank) * kFeatures;
           if (k < a.base) {
-            mbar_expect_tx(full, kWBytes + a.requests * a.rows * kUnitBytes);
-            tma_load_2d(dst, &tm_w, full, k * (kOneByte ? 128 : 64), it.f * kFeatures);
-            tma_load_3d(dst + kWBytes, &tm_x, full, k * (kOneByte ? 128 : 64), it.j * a.rows, it.g * a.requests);
+            mbar_expect_tx_cluster(full, kWBytes + a.half_requests * a.half_rows * kUnitBytes);
+            tma_load_2d_pair(dst, &tm_w, full, k * (kOneByte ? 128 : 64), f);
+            tma_load_3d_pair(dst + kWBytes, &tm_x, full, k * (kOneByte ? 128 : 64), a.by_rows_of ? (2 * it.j + rank) * it.hr : 0,
+                             it.g * a.requests + (a.by_rows_of ? 0 : rank * a.half_requests));
           } else {
             const int p = k - a.base, two = min(2, it.chunks - 2 * p);
-            mbar_expect_tx(full, two * (kFeatures * 32 + a.cols * 64));
+            mbar_expect_tx_cluster(full, two * (kFeatures * 32) + a.half_cols * 128);
             for (int c = 2 * p; c < 2 * p + two; ++c) {
               const int s = (int)divide(c, a.by_chunks);
-              tma_load_3d(dst + (c & 1) * (kFeatures * 32), &tm_b, full, (c - s * a.chunks) * 16, it.f * kFeatures, sh.ids[s]);
+              tma_load_3d_pair(dst + (c & 1) * (kFeatures * 32), &tm_b, full, (c - s * a.chunks) * 16, f, sh.ids[s]);
             }
-            bulk_load(dst + kWBytes, a.parts + ((long long)(it.g * a.blocks + it.j) * a.pairs + p) * proj_pair_bytes(a),
-                      two * a.cols * 64, full);
+            tma_load_2d_pair(dst + kWBytes, &tm_v, full, 0,
+                             (int)((((long long)(it.g * a.blocks + it.j) * a.pairs + p) * 2 + rank) * (a.half_cols / 2)));
           }
         }
         __syncwarp();
@@ -556,17 +667,18 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       }
       __syncwarp();
     }
-    for (int x = loads > a.stages ? loads - a.stages : 0; x < loads; ++x)    // every copy has landed
-      drain(guard, BAR(B_FULL + x % a.stages), (x / a.stages) & 1);
+    for (int x = loads > a.stages ? loads - a.stages : 0; x < loads; ++x)    // every copy has landed, and is used up
+      drain(guard, BAR(B_EMPTY + x % a.stages), (x / a.stages) & 1);
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ---- products ------------------------------------------------------------------------------
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       bool alive = true;
-      const uint32_t idesc = idesc_bf16(kFeatures, a.cols, 0, 0);
       for (int n = 0; alive && next(a, sh, w, it); ++n) {
         const uint32_t d = tmem + (n & 1) * acc_columns(kOneByte);
-        alive = wait(guard, BAR(B_ACC_EMPTY + (n & 1)), ((n >> 1) & 1) ^ 1u);
+        alive = wait<true>(guard, BAR(B_ACC_EMPTY + (n & 1)), ((n >> 1) & 1) ^ 1u);
+        const int cols = 2 * half_cols_of(a, it.hr);
+        const uint32_t idesc = idesc_bf16(2 * kFeatures, cols, 0, 0);
         uint32_t acc = 0u;
         for (int k = it.k0; alive && k < it.k1; ++k) {
           alive = wait(guard, BAR(B_FULL + slot), phase);
@@ -579,16 +691,16 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
               const uint32_t sc = tmem + kScaleColumn + (slot & 3) * 16, ss = scales + slot * kScaleBytes;
               copy_scales(sc, ss);
               copy_scales(sc + 4, ss + 512);
-              if (a.cols > 128) copy_scales(sc + 8, ss + 1024);
+              if (cols > 128) copy_scales(sc + 8, ss + 1024);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
-                mma_scaled(d, ad + 2 * kk, bd + 2 * kk, idesc_scaled(a.cols, kk), sc, sc + 4, acc);
+                mma_scaled(d, ad + 2 * kk, bd + 2 * kk, idesc_scaled(cols, kk), sc, sc + 4, acc);
                 acc = 1u;
               }
             } else {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
-                mma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
+                mma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
                 acc = 1u;
               }
             }
@@ -596,16 +708,17 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             const int two = min(2, it.chunks - 2 * (k - a.base));
             for (int c = 0; c < two; ++c)
               for (int p = 0; p < 2; ++p) {
-                mma_bf16(d, smem_desc_sw32(at + c * (kFeatures * 32)), smem_desc_sw32(at + kWBytes + (c * 2 + p) * a.cols * 32), idesc, acc);
+                mma_bf16_pair(d, smem_desc_sw32(at + c * (kFeatures * 32)),
+                              smem_desc_sw32(at + kWBytes + (c * 2 + p) * a.half_cols * 32), idesc, acc);
                 acc = 1u;
               }
           }
-          mma_commit(BAR(B_EMPTY + slot));
+          mma_commit_pair(BAR(B_EMPTY + slot), 3);
           advance();
         }
-        if (alive) mma_commit(BAR(B_ACC_FULL + (n & 1)));
+        if (alive) mma_commit_pair(BAR(B_ACC_FULL + (n & 1)), 3);
       }
-      mma_commit(BAR(B_DONE));                 // every product has finished before TMEM is freed
+      mma_commit_pair(BAR(B_DONE), 1);         // every product has finished before TMEM is freed
       drain(guard, BAR(B_DONE), 0);
     }
     __syncwarp();
@@ -620,13 +733,15 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
                    : "=r"(r) : "r"((uint32_t)ok) : "memory");
       return r != 0u;
     };
-    grid_dep_wait();                           // the counters are clear; and no CTA ends before that grid
+    grid_dep_wait();                           // (no CTA ends before the first kernel)
+    if (blockIdx.x == 0) leave_plan(a, sh, t);
     for (int n = 0; next(a, sh, w, it); ++n) {
       meet();                                  // the last tile's columns are read
-      for (int c = t; c < a.cols; c += 128) {
-        const int rq = (int)divide(c, a.by_rows), r = c - rq * a.rows, b = it.g * a.requests + rq, i = it.j * a.rows + r;
+      const int cols = 2 * half_cols_of(a, it.hr);
+      for (int c = t; c < cols; c += 128) {
+        int b, i;
         long long at = -1;
-        if (rq < a.requests && b < a.B && i < live_rows(a.n_live, b, a.N)) {
+        if (column(a, it.g, it.j, it.hr, c, &b, &i) && i < live_rows(a.n_live, b, a.N)) {
           const int id = a.adapter ? a.adapter[b] : -1;
           if (id >= -1 && id < a.adapters) at = b * a.ys[0] + i * a.ys[1];
         }
@@ -635,25 +750,26 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       if (!agree(wait_warp(guard, BAR(B_ACC_FULL + (n & 1)), (n >> 1) & 1))) break;
       tc_fence_after();
       const uint32_t acc = tmem + (n & 1) * acc_columns(kOneByte) + ((uint32_t)(32 * q) << 16);
-      const int f = it.f * kFeatures + 32 * q + lane;
+      const int f = (2 * it.f + rank) * kFeatures + 32 * q + lane;
       const bool mixed = a.requests > 1 && it.chunks > 0;
       auto put = [&](int c, float v) {
         const long long at = sh.y_at[c];
         if (at < 0 || f >= a.M) return;
         if (mixed && !(fabsf(v) < INFINITY)) {
-          const int rq = (int)divide(c, a.by_rows);
-          v = alone<kOneByte>(a, it.g * a.requests + rq, c - rq * a.rows, f);
+          int b, i;
+          column(a, it.g, it.j, it.hr, c, &b, &i);
+          v = alone<kOneByte>(a, b, i, f);
         }
         static_cast<__nv_bfloat16*>(a.y)[at + f] = __float2bfloat16_rn(v);
       };
       auto released = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_ACC_EMPTY + (n & 1)));
+        if (lane == 0) mbar_arrive_remote(LEAD(B_ACC_EMPTY + (n & 1)));
       };
       if (it.cut < 0) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < a.cols; c0 += 16) {
+        for (int c0 = 0; c0 < cols; c0 += 16) {
           float v[16];
           __syncwarp();
           tmem_ld16(acc + c0, v);
@@ -664,38 +780,17 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         released();
         continue;
       }
-      const int c0_cta = (int)blockIdx.x - it.seg;
-      float* mine = partial_of(a, c0_cta, it.seg) + 32 * q + lane;
+      float* mine = partial_of(a, (int)(blockIdx.x >> 1), it.seg, rank) + 32 * q + lane;
 #pragma unroll 1
-      for (int c0 = 0; c0 < a.cols; c0 += 16) {
+      for (int c0 = 0; c0 < cols; c0 += 16) {
         float v[16];
         __syncwarp();
         tmem_ld16(acc + c0, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (sh.y_at[c0 + c] >= 0) mine[(c0 + c) * kFeatures] = v[c];
+        for (int c = 0; c < 16; ++c) mine[(c0 + c) * kFeatures] = v[c];
       }
       released();
-      __threadfence();
-      meet();
-      if (t == 0) sh.last[0] = (int)atomicAdd(&a.counters[it.cut], 1u) == it.segs - 1;
-      meet();
-      if (!sh.last[0]) continue;
-      __threadfence();
-#pragma unroll 1
-      for (int c0 = 0; c0 < a.cols; c0 += 16) {
-        float v[16] = {};
-#pragma unroll 1
-        for (int s = 0; s < it.segs; ++s) {
-          const float* part = partial_of(a, c0_cta, s) + c0 * kFeatures + 32 * q + lane;
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (sh.y_at[c0 + c] >= 0) v[c] += __ldcg(part + c * kFeatures);
-        }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) put(c0 + c, v[c]);
-      }
     }
   } else if (kOneByte && warp >= kWarpScale) {
     // ---- exponent bytes: a thread has a row of W and up to two tokens, four units' bytes at a time ------
@@ -722,13 +817,14 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     const uint32_t at = (t & 31) * 16 + (t >> 5) * 4;
     bool alive = true;
     while (alive && next(a, sh, w, it)) {
+      const int cols = 2 * half_cols_of(a, it.hr);
       const uint8_t* rows[3] = {nullptr, nullptr, nullptr};
-      if (it.f * kFeatures + t < a.M) rows[0] = a.W_scale + (long long)(it.f * kFeatures + t) * row_bytes;
+      if ((2 * it.f + (int)rank) * kFeatures + t < a.M) rows[0] = a.W_scale + (long long)((2 * it.f + rank) * kFeatures + t) * row_bytes;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int c = t + 128 * h, rq = (int)divide(c, a.by_rows), r = c - rq * a.rows;
-        const int b = it.g * a.requests + rq, i = it.j * a.rows + r;
-        if (c < a.cols && rq < a.requests && b < a.B && i < a.N) rows[1 + h] = a.x_scale + ((long long)b * a.N + i) * row_bytes;
+        int b, i;
+        if (t + 128 * h < cols && column(a, it.g, it.j, it.hr, t + 128 * h, &b, &i))
+          rows[1 + h] = a.x_scale + ((long long)b * a.N + i) * row_bytes;
       }
       uint4 now[3], then[3];
 #pragma unroll
@@ -750,34 +846,117 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           fence_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_FULL + slot));
+        if (lane == 0) mbar_arrive(BAR((rank == 0 ? B_FULL : B_SCALES) + slot));
         advance();
       }
     }
   }
+  else if (kOneByte && (warp == 2 || warp == 3)) {
+    // ---- the second CTA's exponent bytes are ready: its relay tells the first CTA's, in turns (an arrival
+    // that orders memory across the pair takes as long as a unit; the issuing thread is spared it) ----
+    bool alive = true;
+    int turn = warp - 2;
+    while (alive && next(a, sh, w, it))
+      for (int k = it.k0; alive && k < it.k1; ++k) {
+        if (turn == 0) {
+          if (rank == 1) {
+            alive = wait_warp(guard, BAR(B_SCALES + slot), phase);
+            if (alive && lane == 0) mbar_arrive_remote(LEAD(B_PEER + slot));
+          } else {
+            alive = __all_sync(0xffffffffu, wait<true>(guard, BAR(B_PEER + slot), phase));
+            if (alive && lane == 0) mbar_arrive(BAR(B_FULL + slot));
+          }
+          __syncwarp();
+        }
+        turn ^= 1;
+        advance();
+      }
+  }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                              // neither CTA arrives at the other's barriers any more
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (warp == kWarpMma) tmem_dealloc_pair(tmem, 512);
+}
+
+// ---- outputs of cut tiles ---------------------------------------------------------------------
+// A block has 128 outputs and kCombineCols tokens of a tile; a thread one output and half of those
+// tokens, all segments' sums of four at a time under way together.  Latency
+// bound.  (The last pair to come adding them up by itself, with four warps, took 32
+// us of 53 for 64 tokens.)
+constexpr int kCombineCols = 16;
+
+template <bool kOneByte>
+__global__ void __launch_bounds__(256) proj_combine_kernel(const __grid_constant__ ProjArgs a) {
+  __shared__ long long y_at[kCombineCols];
+  grid_dep_wait();
+  // (a wait that ran out: some sums were never written)
+  if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
+  if ((int)blockIdx.x >= a.plan[0]) return;
+  const CutTile it = reinterpret_cast<const CutTile*>(a.plan + 4)[blockIdx.x];
+  const int c0 = blockIdx.z * kCombineCols, rank = blockIdx.y, cols = 2 * half_cols_of(a, it.hr);
+  if (it.segs < 2 || c0 >= cols) return;
+  if (threadIdx.x < kCombineCols) {
+    int b, i;
+    long long at = -1;
+    if (column(a, it.g, it.j, it.hr, c0 + threadIdx.x, &b, &i) && i < live_rows(a.n_live, b, a.N)) {
+      const int id = a.adapter ? a.adapter[b] : -1;
+      if (id >= -1 && id < a.adapters) at = b * a.ys[0] + i * a.ys[1];
+    }
+    y_at[threadIdx.x] = at;
+  }
+  constexpr int kCols = kCombineCols / 2, kAtOnce = 4;
+  const int lane = threadIdx.x & 127, half = (threadIdx.x >> 7) * kCols, f = (2 * it.f + rank) * kFeatures + lane;
+  float sum[kCols] = {};
+#pragma unroll 1
+  for (int s0 = 0; s0 < it.segs; s0 += kAtOnce) {
+    float v[kAtOnce][kCols];
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s) {
+      const float* part = partial_of(a, it.first + s0 + s, s0 + s, rank) + (c0 + half) * kFeatures + lane;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[s][c] = s0 + s < it.segs ? part[c * kFeatures] : 0.f;
+    }
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) sum[c] += v[s][c];
+  }
+  __syncthreads();
+  if (f >= a.M) return;
+  const bool mixed = a.requests > 1 && it.chunks > 0;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    const long long at = y_at[half + c];
+    if (at < 0) continue;
+    float v = sum[c];
+    if (mixed && !(fabsf(v) < INFINITY)) {
+      int b, i;
+      column(a, it.g, it.j, it.hr, c0 + half + c, &b, &i);
+      v = alone<kOneByte>(a, b, i, f);
+    }
+    static_cast<__nv_bfloat16*>(a.y)[at + f] = __float2bfloat16_rn(v);
+  }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int launch_groups(const ProjArgs& a) { return a.groups < kMaxGroups ? a.groups : kMaxGroups; }
-int ctas_of(int sms) { return sms < kMaxCtas ? sms : kMaxCtas; }
+int pairs_of(int sms) { return sms / 2 < 1 ? 1 : sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs; }
 
-template <bool kOneByte, int MR, int NT, int TW, int KW>
+size_t plan_bytes(int sms) { return align256(16 + (size_t)2 * pairs_of(sms) * sizeof(CutTile)); }
+
+template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
 cudaError_t launch_low(const ProjArgs& a, cudaStream_t st) {
   const int tokens = 8 * NT * TW;
-  const dim3 grid = a.adapter ? dim3((unsigned)((a.N + tokens - 1) / tokens), (unsigned)((a.R + 16 * MR - 1) / (16 * MR)), (unsigned)a.B)
-                              : dim3(1);
-  proj_low_kernel<kOneByte, MR, NT, TW, KW><<<grid, 32 * TW * KW, 0, st>>>(a);
+  const dim3 grid((unsigned)((a.N + tokens - 1) / tokens), (unsigned)((a.R + 16 * MR - 1) / (16 * MR)), (unsigned)a.B);
+  proj_low_kernel<kOneByte, MR, NT, TW, KW, U><<<grid, 32 * TW * KW, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 template <bool kOneByte>
 int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
   constexpr uint64_t e = kOneByte ? 1 : 2;
-  CUtensorMap tw, tx, tb;
+  CUtensorMap tw, tx, tb, tv;
   {
     const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.M}, strides[1] = {a.K * e};
     const uint32_t box[2] = {(uint32_t)(kUnitBytes / e), kFeatures};
@@ -787,30 +966,49 @@ int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
     const uint64_t row = (a.K * e + 15) / 16 * 16;         // strides of single rows do not matter
     const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.B};
     const uint64_t strides[2] = {a.N > 1 ? a.xs[1] * e : row, a.B > 1 ? a.xs[0] * e : row * a.N};
-    const uint32_t box[3] = {(uint32_t)(kUnitBytes / e), (uint32_t)a.rows, (uint32_t)a.requests};
+    const uint32_t box[3] = {(uint32_t)(kUnitBytes / e), (uint32_t)a.half_rows, (uint32_t)a.half_requests};
     if (encode_nd(&tx, a.x, 3, dims, strides, box, (int)e, 128) != CUDA_SUCCESS) return KDTV_ERR_CUDA;
   }
-  tb = tx;
+  tb = tv = tx;
   if (a.adapter) {
     const uint64_t dims[3] = {(uint64_t)a.R, (uint64_t)a.M, (uint64_t)a.adapters};
     const uint64_t strides[2] = {(uint64_t)a.R * 2, (uint64_t)a.M * a.R * 2};
     const uint32_t box[3] = {16, kFeatures, 1};
     if (encode_nd(&tb, a.Bm, 3, dims, strides, box, 2, 32) != CUDA_SUCCESS) return KDTV_ERR_CUDA;
+    // v lies as it is to lie in shared memory: rows of 256 bytes, copied as they are
+    const uint64_t rows = (uint64_t)launch_groups(a) * a.blocks * a.pairs * a.half_cols;
+    const uint64_t vdims[2] = {128, rows}, vstrides[1] = {256};
+    const uint32_t vbox[2] = {128, (uint32_t)a.half_cols / 2};
+    if (encode_nd(&tv, a.parts, 2, vdims, vstrides, vbox, 2, 0) != CUDA_SUCCESS) return KDTV_ERR_CUDA;
   }
-  // Few rows of a request: one rank chunk and 16 ways along d_in a block; many: 64 rows.
-  cudaError_t err;
-  if (a.N <= 8 || !a.adapter) err = launch_low<kOneByte, 1, 1, 1, 16>(a, st);
-  else if (a.R <= 16) err = launch_low<kOneByte, 1, 2, 4, 2>(a, st);
-  else if (a.R <= 32) err = launch_low<kOneByte, 2, 2, 4, 2>(a, st);
-  else err = launch_low<kOneByte, 4, 2, 4, 2>(a, st);
+  // Few rows of a request: blocks of 16 ranks, 8 ways along d_in; many: 64 rows of up to 32 ranks, 4 ways.
+  cudaError_t err = cudaSuccess;
+  if (a.adapter) {
+    if (a.N <= 8) err = launch_low<kOneByte, 1, 1, 1, 8, 2>(a, st);
+    else if (a.R <= 16) err = launch_low<kOneByte, 1, 4, 2, 4, 1>(a, st);
+    else err = launch_low<kOneByte, 2, 4, 2, 4, 1>(a, st);
+  }
   if (err != cudaSuccess) return KDTV_ERR_CUDA;
-  const size_t smem = (size_t)a.stages * (kWBytes + a.cols * kUnitBytes + (kOneByte ? kScaleBytes : 0)) + sizeof(ProjShared);
+  const size_t smem = (size_t)a.stages * (kWBytes + a.half_cols * kUnitBytes + (kOneByte ? kScaleBytes : 0)) + sizeof(ProjShared);
   const auto kern = proj_tc_kernel<kOneByte>;
   if (allow_smem(kern, smem) != cudaSuccess) return KDTV_ERR_CUDA;
-  if (launch_ex(kern, dim3((unsigned)ctas_of(sms)), dim3(threads_of(kOneByte)), smem, st, true, tw, tx, tb, a, stall ? 1 : 0) !=
-      cudaSuccess)
-    return KDTV_ERR_CUDA;
-  return KDTV_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs_of(sms)));
+  cfg.blockDim = dim3(threads_of(kOneByte));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {2, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.adapter ? 2 : 1;           // beside the first kernel, where there is one
+  if (cudaLaunchKernelEx(&cfg, kern, tw, tx, tb, tv, a, stall ? 1 : 0) != cudaSuccess) return KDTV_ERR_CUDA;
+  if (!may_cut(a)) return KDTV_OK;
+  const long long tiles = (long long)a.groups * a.blocks * a.features, most = 2ll * pairs_of(sms) - 1;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most), 2, (unsigned)((2 * a.half_cols + kCombineCols - 1) / kCombineCols));
+  return launch_ex(proj_combine_kernel<kOneByte>, grid, dim3(256), 0, st, true, a) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
 }
 
 }  // namespace
@@ -820,54 +1018,55 @@ bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a) {
   if (d->dtype == KDTV_F32 || (d->flags & KDTV_FLAG_SIMT)) return false;
   if (!one_byte && d->d_in % 8) return false;
   if (d->adapters > 0 && d->rank % 8) return false;
-  const int cap = acc_columns(one_byte);
-  if (2 * d->N > cap) {                       // row blocks of one request, as even as multiples of 8 allow
-    a->requests = 1;
+  const int cap = acc_columns(one_byte) / 2;  // columns of a half
+  a->by_rows_of = d->B == 1 || d->N > cap;
+  if (a->by_rows_of) {                        // row blocks of one request
+    a->requests = a->half_requests = 1;
     a->groups = d->B;
-    a->blocks = (d->N + cap - 1) / cap;
-    a->rows = ((d->N + a->blocks - 1) / a->blocks + 7) / 8 * 8;
-    a->blocks = (d->N + a->rows - 1) / a->rows;
+    a->half_rows = (d->N + 1) / 2 < cap ? (d->N + 1) / 2 : cap;
+    a->blocks = (d->N + 2 * a->half_rows - 1) / (2 * a->half_rows);
   } else {
-    const int most = cap / d->N;
-    a->groups = (d->B + most - 1) / most;
-    a->requests = (d->B + a->groups - 1) / a->groups;
+    a->groups = (d->B + cap / d->N * 2 - 1) / (cap / d->N * 2);
+    a->half_requests = ((d->B + a->groups - 1) / a->groups + 1) / 2;
+    a->requests = 2 * a->half_requests;
     a->groups = (d->B + a->requests - 1) / a->requests;
     a->blocks = 1;
-    a->rows = d->N;
+    a->half_rows = d->N;
   }
-  a->cols = (a->requests * a->rows + 15) / 16 * 16;
+  a->half_cols = (a->half_requests * a->half_rows + 15) / 16 * 16;
   a->base = (int)(((long long)d->d_in * (one_byte ? 1 : 2) + kUnitBytes - 1) / kUnitBytes);
   a->chunks = d->adapters > 0 ? (d->rank + 15) / 16 : 0;
   a->pairs = ((a->requests < d->adapters ? a->requests : d->adapters) * a->chunks + 1) / 2;
-  a->features = (d->d_out + kFeatures - 1) / kFeatures;
+  a->features = (d->d_out + 2 * kFeatures - 1) / (2 * kFeatures);
   if ((long long)a->groups * a->blocks * a->features > 0x3fffffffll) return false;
-  const int stage = kWBytes + a->cols * kUnitBytes + (one_byte ? kScaleBytes : 0);
+  const int stage = kWBytes + a->half_cols * kUnitBytes + (one_byte ? kScaleBytes : 0);
   // As many stages as leave room for the first kernel's blocks beside this one's (up to 17 KiB).
   a->stages = (int)((225 * 1024 - 18 * 1024 - sizeof(ProjShared)) / stage);
   if (a->stages > kMaxStages) a->stages = kMaxStages;
-  a->n_counters = 2 * ctas_of(sms);
   a->by_requests = divisor((unsigned)a->requests);
-  a->by_rows = divisor((unsigned)a->rows);
+  a->by_N = divisor((unsigned)d->N);
   a->by_chunks = divisor((unsigned)(a->chunks > 0 ? a->chunks : 1));
   return true;
 }
 
-// Counters, A x, partial sums.
+// The plan, A x, partial sums.
 size_t proj_tc_workspace(const ProjArgs& a, int sms) {
-  return align256((size_t)a.n_counters * 4) + align256((size_t)launch_groups(a) * a.blocks * a.pairs * proj_pair_bytes(a)) +
-         (size_t)2 * ctas_of(sms) * a.cols * kFeatures * 4;
+  return plan_bytes(sms) + align256((size_t)launch_groups(a) * a.blocks * a.pairs * 2 * proj_half_bytes(a)) +
+         (size_t)4 * pairs_of(sms) * 2 * a.half_cols * kFeatures * 4;
 }
 
-int proj_tc_launches(const ProjArgs& a) { return (a.groups + kMaxGroups - 1) / kMaxGroups; }
+int proj_tc_launches(const ProjArgs& a) {
+  return (a.groups + kMaxGroups - 1) / kMaxGroups * (1 + (a.chunks > 0) + may_cut(a));
+}
 
 int launch_proj_tc(const ProjArgs& call, int sms, bool stall, cudaStream_t st) {
   ProjArgs a = call;
   const bool one_byte = a.dtype == KDTV_BF16_FP8KV;
   char* at = reinterpret_cast<char*>(call.low);
-  a.counters = reinterpret_cast<unsigned int*>(at);
-  at += align256((size_t)a.n_counters * 4);
+  a.plan = reinterpret_cast<int*>(at);
+  at += plan_bytes(sms);
   a.parts = at;
-  at += align256((size_t)launch_groups(a) * a.blocks * a.pairs * proj_pair_bytes(a));
+  at += align256((size_t)launch_groups(a) * a.blocks * a.pairs * 2 * proj_half_bytes(a));
   a.partial = reinterpret_cast<float*>(at);
   a.scale_mode = 0;
   if (one_byte) {
