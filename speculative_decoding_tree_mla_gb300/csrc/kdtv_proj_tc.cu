@@ -21,7 +21,7 @@
 // of W and half of the tokens, and the products read both halves (cta_group::2), so
 // that a unit costs each SM 32 KiB where a CTA by itself with as many products
 // would load 48.  Whole tiles go round the pairs; what does not fill a round is
-// cut evenly by units (at least one round, so that no pair gets little).  A tile
+// cut evenly by units.  A tile
 // that several pairs share: each leaves its sums, and proj_combine_kernel adds them in
 // the order of the units.
 //
@@ -48,10 +48,11 @@ constexpr int kFeatures = 128;             // outputs of a CTA: half of a tile
 constexpr int kUnitBytes = 128;            // of d_in in a unit
 constexpr int kWBytes = kFeatures * kUnitBytes;
 constexpr int kMaxStages = 12;
-constexpr int kMaxGroups = 1024;           // groups of requests in a launch
+constexpr int kMaxGroups = 512;            // groups of requests in a launch
 constexpr int kMaxPairs = 128;
 constexpr int kWords = KDTV_MAX_ADAPTERS / 32;
-constexpr int kScaleBytes = 3 * 512;       // a stage's exponent bytes: W, tokens 0 - 127, the others
+constexpr int kScaleBytes = 3 * 512;       // a unit's exponent bytes: W, tokens 0 - 127, the others
+constexpr int kWindow = 4, kWindows = 3;   // units whose exponent bytes go together; such windows under way
 constexpr int kSuper = 8;                  // token tiles that share a W tile in a row
 
 // ---- which adapters a tile has -------------------------------------------------------------
@@ -299,17 +300,21 @@ __global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_
 // ---- the projection --------------------------------------------------------------------------
 enum {
   B_FULL = 0, B_EMPTY = B_FULL + kMaxStages, B_ACC_FULL = B_EMPTY + kMaxStages, B_ACC_EMPTY = B_ACC_FULL + 2,
-  B_DONE = B_ACC_EMPTY + 2, B_STALL, B_SCALES, B_PEER = B_SCALES + kMaxStages, B_COUNT = B_PEER + kMaxStages
+  B_DONE = B_ACC_EMPTY + 2, B_STALL,
+  // one byte, a window's exponents: ready in both CTAs, used up, ready in the second CTA, the same seen by the first
+  B_S_FULL, B_S_EMPTY = B_S_FULL + kWindows, B_S_LOCAL = B_S_EMPTY + kWindows, B_S_PEER = B_S_LOCAL + kWindows,
+  B_COUNT = B_S_PEER + kWindows
 };
 
 // Arrivals of a barrier's phase.
-__device__ __forceinline__ uint32_t arrivals(bool one_byte, int i) {
-  if (i < B_EMPTY) return one_byte ? 7 : 2;                 // both producers; four warps here, the peer's as one
+__device__ __forceinline__ uint32_t arrivals(int i) {
+  if (i < B_EMPTY) return 2;                                // both CTAs' producers
   if (i >= B_ACC_EMPTY && i < B_DONE) return 8;             // both CTAs' four warps
-  return i >= B_SCALES && i < B_PEER ? 4 : 1;
+  if (i >= B_S_FULL && i < B_S_EMPTY) return 5;             // four warps, and the peer's through the relay
+  return i >= B_S_LOCAL && i < B_S_PEER ? 4 : 1;
 }
 
-constexpr int kWarpTma = 0, kWarpMma = 1, kWarpOut = 4, kWarpScale = 8;   // (2, 3: one byte: relays)
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpOut = 4, kWarpRelay = 2, kWarpScale = 8;   // (3: planning only)
 __host__ __device__ constexpr int threads_of(bool one_byte) { return one_byte ? 384 : 256; }
 __host__ __device__ constexpr int acc_columns(bool one_byte) { return one_byte ? 224 : 256; }
 constexpr uint32_t kScaleColumn = 448;      // one byte: exponents behind the two accumulators
@@ -321,10 +326,11 @@ struct ProjShared {
   int total_tiles, cut, share, pad;         // token tiles times outputs' tiles; cut tiles; units of a pair's share
   int first[kMaxGroups + 1];                // token tiles before each group
   uint32_t tile[kMaxGroups];                // 16-rank chunks of its tiles' adapters, and 2^20 rows of half a block
-  int start[2 * kMaxPairs + 1];              // units before each cut tile
+  int start[kMaxPairs + 1];              // units before each cut tile
   long long y_at[256];                      // offset of each column's output row, -1: none
   uint32_t bits[kWords];
   uint16_t ids[256];                        // the adapters of the producer's tile
+  __align__(16) unsigned char rows[4][16 * 64];   // an output warp's 32 outputs of 16 tokens
 };
 
 // A part of a tile: units k0 .. k1 - 1; behind a.base of d_in come pairs of chunks.
@@ -498,7 +504,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stage_bytes = kWBytes + a.half_cols * kUnitBytes;
   const uint32_t rank = cluster_ctarank();
-  ProjShared& sh = *reinterpret_cast<ProjShared*>(smem + (size_t)a.stages * (stage_bytes + (kOneByte ? kScaleBytes : 0)));
+  ProjShared& sh = *reinterpret_cast<ProjShared*>(smem + (size_t)a.stages * stage_bytes + (kOneByte ? kWindows * kWindow * kScaleBytes : 0));
   const uint32_t ring = smem_u32(smem), scales = ring + a.stages * stage_bytes, bars = smem_u32(sh.bars);
   auto BAR = [&](int i) { return bars + 8u * i; };
   const Guard guard{&sh.abort, a.status, stall ? 20000000u : 2000000000u};
@@ -507,7 +513,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   // ---- set up, and plan: every CTA derives the same tiles from n_live and adapter ------------------
   if (threadIdx.x < B_COUNT) {
     const int i = threadIdx.x;
-    mbar_init(BAR(i), arrivals(kOneByte, i));
+    mbar_init(BAR(i), arrivals(i));
   }
   if (threadIdx.x == 0) sh.abort = 0u;
   fence_mbar_init();
@@ -561,11 +567,11 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     }
     if (lane == 0) sh.first[a.groups] = sum;
     __syncwarp();
-    // Whole rounds of whole tiles but the last, and what is left cut into equal shares.  Tiles of few
-    // units are not cut, nor are almost full rounds.
+    // Whole rounds of whole tiles, and what is left cut into equal shares.  Tiles of few units are not cut, nor
+    // are almost full rounds.
     const int tiles = sum * a.features, pairs = gridDim.x >> 1;
-    int cut = tiles % pairs == 0 ? 0 : tiles < 2 * pairs ? tiles : tiles % pairs + pairs;
-    if (!may_cut(a) || (tiles < pairs && tiles * 20 > pairs * 19)) cut = 0;
+    int cut = tiles % pairs;
+    if (!may_cut(a) || cut * 20 > pairs * 19) cut = 0;
     Item it;
     int u = 0;
     for (int t0 = 0; t0 < cut; t0 += 32) {
@@ -597,12 +603,19 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   auto LEAD = [&](int i) { return lead + 8u * i; };
   Walk w = walk(sh);
   Item it;
-  int slot = 0;
-  uint32_t phase = 0u;
+  int slot = 0, window = 0;
+  uint32_t phase = 0u, w_phase = 0u;
   auto advance = [&]() {
     if (++slot == a.stages) {
       slot = 0;
       phase ^= 1u;
+    }
+  };
+
+  auto advance_window = [&]() {
+    if (++window == kWindows) {
+      window = 0;
+      w_phase ^= 1u;
     }
   };
 
@@ -686,9 +699,16 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           tc_fence_after();
           const uint32_t at = ring + slot * stage_bytes;
           if (k < a.base) {
+            if constexpr (kOneByte) {
+              if (k == it.k0 || k % kWindow == 0) {
+                alive = wait(guard, BAR(B_S_FULL + window), w_phase);
+                if (!alive) break;
+                tc_fence_after();
+              }
+            }
             const uint64_t ad = smem_desc(at, 16, 1024), bd = smem_desc(at + kWBytes, 16, 1024);
             if constexpr (kOneByte) {
-              const uint32_t sc = tmem + kScaleColumn + (slot & 3) * 16, ss = scales + slot * kScaleBytes;
+              const uint32_t sc = tmem + kScaleColumn + (k % kWindow) * 16, ss = scales + (window * kWindow + k % kWindow) * kScaleBytes;
               copy_scales(sc, ss);
               copy_scales(sc + 4, ss + 512);
               if (cols > 128) copy_scales(sc + 8, ss + 1024);
@@ -696,6 +716,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
               for (int kk = 0; kk < 4; ++kk) {
                 mma_scaled(d, ad + 2 * kk, bd + 2 * kk, idesc_scaled(cols, kk), sc, sc + 4, acc);
                 acc = 1u;
+              }
+              if (k % kWindow == kWindow - 1 || k + 1 == min(it.k1, a.base)) {
+                mma_commit_pair(BAR(B_S_EMPTY + window), 3);
+                advance_window();
               }
             } else {
 #pragma unroll
@@ -774,28 +798,53 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           __syncwarp();
           tmem_ld16(acc + c0, v);
           tmem_wait_ld();
+          bool odd = !a.wide;
+          if (mixed)
 #pragma unroll
-          for (int c = 0; c < 16; ++c) put(c0 + c, v[c]);
+            for (int c = 0; c < 16; ++c) odd |= !(fabsf(v[c]) < INFINITY) && sh.y_at[c0 + c] >= 0;
+          if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              float x = 0.f;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x = c == k ? v[k] : x;
+              put(c0 + c, x);
+            }
+            continue;
+          }
+          // through shared memory, so that a lane writes 8 outputs of a token at once
+          __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(sh.rows[q]);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) rows[c * 32 + lane] = __float2bfloat16_rn(v[c]);
+          __syncwarp();
+          const int f8 = f - lane + (lane & 3) * 8;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = h * 8 + (lane >> 2);
+            const long long to = sh.y_at[c0 + c];
+            const uint4 w8 = *reinterpret_cast<const uint4*>(rows + c * 32 + (lane & 3) * 8);
+            if (to >= 0 && f8 < a.M) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f8) = w8;
+          }
         }
         released();
         continue;
       }
       float* mine = partial_of(a, (int)(blockIdx.x >> 1), it.seg, rank) + 32 * q + lane;
 #pragma unroll 1
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        float v[16];
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        float v[32];
         __syncwarp();
-        tmem_ld16(acc + c0, v);
+        tmem_ld32(acc + c0, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) mine[(c0 + c) * kFeatures] = v[c];
+        for (int c = 0; c < 32; ++c) mine[(c0 + c) * kFeatures] = v[c];
       }
       released();
     }
   } else if (kOneByte && warp >= kWarpScale) {
     // ---- exponent bytes: a thread has a row of W and up to two tokens, four units' bytes at a time ------
     const int t = threadIdx.x - 32 * kWarpScale, row_bytes = a.K / KDTV_GROUP;
-    auto window = [&](const uint8_t* row, int u) -> uint4 {       // units 4 u .. 4 u + 3
+    auto bytes = [&](const uint8_t* row, int u) -> uint4 {        // of window u
       uint32_t x[4] = {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
       if (row && 4 * u < a.base) {
         if (a.scale_mode == 2) return *reinterpret_cast<const uint4*>(row + 16 * u);
@@ -813,7 +862,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       }
       return make_uint4(x[0], x[1], x[2], x[3]);
     };
-    auto word = [](const uint4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; };
+    auto sts32 = [](uint32_t to, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(to), "r"(v) : "memory"); };
     const uint32_t at = (t & 31) * 16 + (t >> 5) * 4;
     bool alive = true;
     while (alive && next(a, sh, w, it)) {
@@ -826,50 +875,47 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         if (t + 128 * h < cols && column(a, it.g, it.j, it.hr, t + 128 * h, &b, &i))
           rows[1 + h] = a.x_scale + ((long long)b * a.N + i) * row_bytes;
       }
-      uint4 now[3], then[3];
+      const int last = (min(it.k1, a.base) - 1) / kWindow;
+      uint4 then[3];
+      if (it.k0 < a.base)
 #pragma unroll
-      for (int r = 0; r < 3; ++r) then[r] = window(rows[r], it.k0 >> 2);
-      for (int k = it.k0; k < it.k1; ++k) {
-        if (k < a.base && (k == it.k0 || (k & 3) == 0))
+        for (int r = 0; r < 3; ++r) then[r] = bytes(rows[r], it.k0 / kWindow);
+      for (int u = it.k0 / kWindow; it.k0 < a.base && u <= last; ++u) {
+        const uint4 now[3] = {then[0], then[1], then[2]};
 #pragma unroll
-          for (int r = 0; r < 3; ++r) {
-            now[r] = then[r];
-            then[r] = window(rows[r], (k >> 2) + 1);
-          }
-        alive = wait_warp(guard, BAR(B_EMPTY + slot), phase ^ 1u);
+        for (int r = 0; r < 3; ++r) then[r] = bytes(rows[r], u + 1);
+        alive = wait_warp(guard, BAR(B_S_EMPTY + window), w_phase ^ 1u);
         if (!alive) break;
-        if (k < a.base) {
-          const uint32_t to = scales + slot * kScaleBytes + at;
+        const uint32_t to = scales + window * (kWindow * kScaleBytes) + at;
 #pragma unroll
-          for (int r = 0; r < 3; ++r)
-            asm volatile("st.shared.b32 [%0], %1;" :: "r"(to + 512 * r), "r"(word(now[r], k & 3)) : "memory");
-          fence_async_smem();
+        for (int r = 0; r < 3; ++r) {
+          sts32(to + 512 * r, now[r].x);
+          sts32(to + 512 * r + kScaleBytes, now[r].y);
+          sts32(to + 512 * r + 2 * kScaleBytes, now[r].z);
+          sts32(to + 512 * r + 3 * kScaleBytes, now[r].w);
         }
+        fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR((rank == 0 ? B_FULL : B_SCALES) + slot));
-        advance();
+        if (lane == 0) mbar_arrive(BAR((rank == 0 ? B_S_FULL : B_S_LOCAL) + window));
+        advance_window();
       }
     }
   }
-  else if (kOneByte && (warp == 2 || warp == 3)) {
-    // ---- the second CTA's exponent bytes are ready: its relay tells the first CTA's, in turns (an arrival
-    // that orders memory across the pair takes as long as a unit; the issuing thread is spared it) ----
+  else if (kOneByte && warp == kWarpRelay) {
+    // ---- the second CTA's exponents are ready: its relay tells the first CTA's (an arrival that orders memory
+    // across the pair takes some 500 cycles; the issuing thread is spared it) -----------------------------
     bool alive = true;
-    int turn = warp - 2;
     while (alive && next(a, sh, w, it))
-      for (int k = it.k0; alive && k < it.k1; ++k) {
-        if (turn == 0) {
-          if (rank == 1) {
-            alive = wait_warp(guard, BAR(B_SCALES + slot), phase);
-            if (alive && lane == 0) mbar_arrive_remote(LEAD(B_PEER + slot));
-          } else {
-            alive = __all_sync(0xffffffffu, wait<true>(guard, BAR(B_PEER + slot), phase));
-            if (alive && lane == 0) mbar_arrive(BAR(B_FULL + slot));
-          }
-          __syncwarp();
+      for (int u = it.k0 / kWindow; alive && it.k0 < a.base && u <= (min(it.k1, a.base) - 1) / kWindow; ++u) {
+        if (rank == 1) {
+          alive = wait_warp(guard, BAR(B_S_LOCAL + window), w_phase);
+          if (alive && lane == 0) mbar_arrive_remote(LEAD(B_S_PEER + window));
+        } else {
+          alive = __all_sync(0xffffffffu, wait<true>(guard, BAR(B_S_PEER + window), w_phase));
+          if (alive && lane == 0) mbar_arrive(BAR(B_S_FULL + window));
         }
-        turn ^= 1;
-        advance();
+        __syncwarp();
+        advance_window();
       }
   }
   tc_fence_before();
@@ -892,8 +938,9 @@ __global__ void __launch_bounds__(256) proj_combine_kernel(const __grid_constant
   grid_dep_wait();
   // (a wait that ran out: some sums were never written)
   if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
-  if ((int)blockIdx.x >= a.plan[0]) return;
-  const CutTile it = reinterpret_cast<const CutTile*>(a.plan + 4)[blockIdx.x];
+  const int cut = a.plan[0];
+  const CutTile it = reinterpret_cast<const CutTile*>(a.plan + 4)[blockIdx.x];   // (there is room for it, if not a tile)
+  if ((int)blockIdx.x >= cut) return;
   const int c0 = blockIdx.z * kCombineCols, rank = blockIdx.y, cols = 2 * half_cols_of(a, it.hr);
   if (it.segs < 2 || c0 >= cols) return;
   if (threadIdx.x < kCombineCols) {
@@ -943,11 +990,20 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int launch_groups(const ProjArgs& a) { return a.groups < kMaxGroups ? a.groups : kMaxGroups; }
 int pairs_of(int sms) { return sms / 2 < 1 ? 1 : sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs; }
 
-size_t plan_bytes(int sms) { return align256(16 + (size_t)2 * pairs_of(sms) * sizeof(CutTile)); }
+size_t plan_bytes(int sms) { return align256(16 + (size_t)pairs_of(sms) * sizeof(CutTile)); }
+
+// An SM divides its memory between L1 and shared memory once for all blocks that it holds: what is to run
+// beside the projection asks for the division that the projection needs.
+template <typename... KArgs>
+cudaError_t beside(void (*kernel)(KArgs...)) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
 
 template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
 cudaError_t launch_low(const ProjArgs& a, cudaStream_t st) {
   const int tokens = 8 * NT * TW;
+  const cudaError_t err = beside(proj_low_kernel<kOneByte, MR, NT, TW, KW, U>);
+  if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)((a.N + tokens - 1) / tokens), (unsigned)((a.R + 16 * MR - 1) / (16 * MR)), (unsigned)a.B);
   proj_low_kernel<kOneByte, MR, NT, TW, KW, U><<<grid, 32 * TW * KW, 0, st>>>(a);
   return cudaGetLastError();
@@ -989,7 +1045,8 @@ int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
     else err = launch_low<kOneByte, 2, 4, 2, 4, 1>(a, st);
   }
   if (err != cudaSuccess) return KDTV_ERR_CUDA;
-  const size_t smem = (size_t)a.stages * (kWBytes + a.half_cols * kUnitBytes + (kOneByte ? kScaleBytes : 0)) + sizeof(ProjShared);
+  const size_t smem = (size_t)a.stages * (kWBytes + a.half_cols * kUnitBytes) +
+                      (kOneByte ? kWindows * kWindow * kScaleBytes : 0) + sizeof(ProjShared);
   const auto kern = proj_tc_kernel<kOneByte>;
   if (allow_smem(kern, smem) != cudaSuccess) return KDTV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -1006,8 +1063,10 @@ int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
   cfg.numAttrs = a.adapter ? 2 : 1;           // beside the first kernel, where there is one
   if (cudaLaunchKernelEx(&cfg, kern, tw, tx, tb, tv, a, stall ? 1 : 0) != cudaSuccess) return KDTV_ERR_CUDA;
   if (!may_cut(a)) return KDTV_OK;
-  const long long tiles = (long long)a.groups * a.blocks * a.features, most = 2ll * pairs_of(sms) - 1;
+  const long long tiles = (long long)a.groups * a.blocks * a.features, most = pairs_of(sms) - 1;
+  if (most == 0) return KDTV_OK;
   const dim3 grid((unsigned)(tiles < most ? tiles : most), 2, (unsigned)((2 * a.half_cols + kCombineCols - 1) / kCombineCols));
+  if (beside(proj_combine_kernel<kOneByte>) != cudaSuccess) return KDTV_ERR_CUDA;
   return launch_ex(proj_combine_kernel<kOneByte>, grid, dim3(256), 0, st, true, a) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
 }
 
@@ -1039,9 +1098,9 @@ bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a) {
   a->pairs = ((a->requests < d->adapters ? a->requests : d->adapters) * a->chunks + 1) / 2;
   a->features = (d->d_out + 2 * kFeatures - 1) / (2 * kFeatures);
   if ((long long)a->groups * a->blocks * a->features > 0x3fffffffll) return false;
-  const int stage = kWBytes + a->half_cols * kUnitBytes + (one_byte ? kScaleBytes : 0);
-  // As many stages as leave room for the first kernel's blocks beside this one's (up to 17 KiB).
-  a->stages = (int)((225 * 1024 - 18 * 1024 - sizeof(ProjShared)) / stage);
+  // As many stages as leave room for the first kernel's blocks beside this one's (17 KiB, and 1 KiB each).
+  a->stages = (int)((228 * 1024 - 20 * 1024 - sizeof(ProjShared) - (one_byte ? kWindows * kWindow * kScaleBytes : 0)) /
+                    (kWBytes + a->half_cols * kUnitBytes));
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->by_requests = divisor((unsigned)a->requests);
   a->by_N = divisor((unsigned)d->N);
@@ -1068,6 +1127,7 @@ int launch_proj_tc(const ProjArgs& call, int sms, bool stall, cudaStream_t st) {
   a.parts = at;
   at += align256((size_t)launch_groups(a) * a.blocks * a.pairs * 2 * proj_half_bytes(a));
   a.partial = reinterpret_cast<float*>(at);
+  a.wide = reinterpret_cast<uintptr_t>(call.y) % 16 == 0 && call.ys[0] % 8 == 0 && call.ys[1] % 8 == 0 && call.M % 8 == 0;
   a.scale_mode = 0;
   if (one_byte) {
     const uintptr_t both = reinterpret_cast<uintptr_t>(a.x_scale) | reinterpret_cast<uintptr_t>(a.W_scale);
