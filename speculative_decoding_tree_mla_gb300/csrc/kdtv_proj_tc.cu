@@ -153,14 +153,15 @@ __device__ __forceinline__ uint4 widen8(uint2 w, uint32_t byte) {
 }
 
 template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
-__global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_constant__ ProjArgs a) {
+__global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_constant__ ProjArgs a, int split) {
   __shared__ uint32_t bits[kWords];
   __shared__ int s_slot, s_slots;
   __shared__ float red[KW / 2 * TW][MR * NT * 4][32];
   grid_dep_launch();                 // the projection may be launched; its adapters' units wait for this grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kTokens = 8 * NT * TW;
-  const int b = blockIdx.z, i0 = blockIdx.x * kTokens, n = live_rows(a.n_live, b, a.N);
+  const int part = blockIdx.x % split;         // of d_in: the blocks of a cluster
+  const int b = blockIdx.z, i0 = blockIdx.x / split * kTokens, n = live_rows(a.n_live, b, a.N);
   if (i0 >= n) return;
   const int id = proj_adapter(a, b);
   if (id == -2) return;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_
     char* at = part_row(a, b, i, hr, c, p, &flip);
     return at + ((h ^ flip) << 4);
   };
-  if (blockIdx.y == 0 && a.requests > 1) {              // the other adapters' chunks
+  if (blockIdx.y == 0 && part == 0 && a.requests > 1) {   // the other adapters' chunks
     const int others = chunks - (id < 0 ? 0 : a.chunks);
     for (int e = threadIdx.x; e < rows * others * 4; e += 32 * TW * KW) {
       const int i = e / (others * 4), r = e - i * (others * 4), c = r >> 2;
@@ -247,14 +248,14 @@ __global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_
           }
         }
     };
-    constexpr int kStride = KW * 32 * U;
+    const int stride = split * KW * 32 * U, start = part * KW * 32 * U + kw * 32;
     Step s0, s1;
-    load(s0, kw * 32);
+    load(s0, start);
 #pragma unroll 1
-    for (int k0 = kw * 32; k0 < a.K; k0 += 2 * kStride) {      // (loads behind d_in are zeros)
-      load(s1, k0 + kStride);
+    for (int k0 = start; k0 < a.K; k0 += 2 * stride) {          // (loads behind d_in are zeros)
+      load(s1, k0 + stride);
       multiply(s0);
-      load(s0, k0 + 2 * kStride);
+      load(s0, k0 + 2 * stride);
       multiply(s1);
     }
   }
@@ -277,7 +278,31 @@ __global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_
           for (int k = 0; k < 4; ++k) acc[m][j][k] += red[kw * TW + tw][(m * NT + j) * 4 + k][lane];
     __syncthreads();
   }
-  if (kw > 0 || !busy) return;
+  if (split > 1) {                                       // the blocks' sums to the first, in their order
+    if (kw == 0 && part > 0)
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) red[tw][(m * NT + j) * 4 + k][lane] = acc[m][j][k];
+    cluster_sync();
+    if (kw == 0 && part == 0)
+      for (int c = 1; c < split; ++c)
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float v;
+              asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                           : "=f"(v) : "r"(mapa(smem_u32(&red[tw][(m * NT + j) * 4 + k][lane]), c)) : "memory");
+              acc[m][j][k] += v;
+            }
+    cluster_sync();                                      // (the others' memory is read)
+  }
+  if (kw > 0 || part > 0 || !busy) return;
   const float s = a.adapter_scale ? a.adapter_scale[id] : 1.f;
 #pragma unroll
   for (int m = 0; m < MR; ++m)
@@ -339,10 +364,10 @@ struct Item {
   int cut, seg, segs;                       // cut tile's number (-1: whole), place among its segments
 };
 
-// The items of pair c, in the order in which every role sees them: its share of
-// the cut tiles, then whole tiles.
+// The items of pair c, in the order in which every role sees them: whole tiles, then its share of the cut
+// ones from its end on: tiles begin with d_in, and the first kernel has until their adapters' units come.
 struct Walk {
-  int u, u_end, tile, s;                    // next unit of the share, next whole tile, current cut tile
+  int tile, u0, u, s;                       // next whole tile; start and end of what is left of the share, its last tile
 };
 
 // Tiles of few units are not cut.
@@ -368,14 +393,14 @@ __device__ __forceinline__ void locate(const ProjArgs& a, const ProjShared& sh, 
 
 __device__ __forceinline__ Walk walk(const ProjShared& sh) {
   Walk w;
-  const int all = sh.cut ? sh.start[sh.cut] : 0;
-  w.u = min(all, (int)(blockIdx.x >> 1) * sh.share);
-  w.u_end = min(all, w.u + sh.share);
-  w.tile = sh.cut + (blockIdx.x >> 1);
-  int lo = 0, hi = sh.cut - 1;
+  const int pair = blockIdx.x >> 1, all = sh.cut ? sh.start[sh.cut] : 0;
+  w.tile = sh.cut + pair;
+  w.u0 = min(all, pair * sh.share);
+  w.u = min(all, w.u0 + sh.share);
+  int lo = 0, hi = sh.cut - 1;              // the last tile that starts before w.u
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (sh.start[mid] <= w.u) lo = mid;
+    if (sh.start[mid] < w.u) lo = mid;
     else hi = mid - 1;
   }
   w.s = lo;
@@ -383,27 +408,26 @@ __device__ __forceinline__ Walk walk(const ProjShared& sh) {
 }
 
 __device__ __forceinline__ bool next(const ProjArgs& a, const ProjShared& sh, Walk& w, Item& it) {
-  if (w.u < w.u_end) {
-    locate(a, sh, w.s, it);
-    const int start = sh.start[w.s], end = sh.start[w.s + 1], stop = min(end, w.u_end);
-    it.k0 = w.u - start;
-    it.k1 = stop - start;
-    const int c0 = start / sh.share;
-    it.segs = (end - 1) / sh.share - c0 + 1;
-    it.seg = (int)(blockIdx.x >> 1) - c0;
-    it.cut = it.segs > 1 ? w.s : -1;
-    w.u = stop;
-    if (stop == end) ++w.s;
+  if (w.tile < sh.total_tiles) {
+    locate(a, sh, w.tile, it);
+    it.k0 = 0;
+    it.k1 = units_of(a, it.chunks);
+    it.cut = -1;
+    it.seg = 0;
+    it.segs = 1;
+    w.tile += gridDim.x >> 1;
     return true;
   }
-  if (w.tile >= sh.total_tiles) return false;
-  locate(a, sh, w.tile, it);
-  it.k0 = 0;
-  it.k1 = units_of(a, it.chunks);
-  it.cut = -1;
-  it.seg = 0;
-  it.segs = 1;
-  w.tile += gridDim.x >> 1;
+  if (w.u <= w.u0) return false;
+  locate(a, sh, w.s, it);
+  const int start = sh.start[w.s], end = sh.start[w.s + 1], from = max(start, w.u0), c0 = start / sh.share;
+  it.k0 = from - start;
+  it.k1 = w.u - start;
+  it.segs = (end - 1) / sh.share - c0 + 1;
+  it.seg = (int)(blockIdx.x >> 1) - c0;
+  it.cut = it.segs > 1 ? w.s : -1;
+  w.u = from;
+  --w.s;
   return true;
 }
 
@@ -1000,13 +1024,24 @@ cudaError_t beside(void (*kernel)(KArgs...)) {
 }
 
 template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
-cudaError_t launch_low(const ProjArgs& a, cudaStream_t st) {
+cudaError_t launch_low(const ProjArgs& a, int sms, cudaStream_t st) {
   const int tokens = 8 * NT * TW;
   const cudaError_t err = beside(proj_low_kernel<kOneByte, MR, NT, TW, KW, U>);
   if (err != cudaSuccess) return err;
-  const dim3 grid((unsigned)((a.N + tokens - 1) / tokens), (unsigned)((a.R + 16 * MR - 1) / (16 * MR)), (unsigned)a.B);
-  proj_low_kernel<kOneByte, MR, NT, TW, KW, U><<<grid, 32 * TW * KW, 0, st>>>(a);
-  return cudaGetLastError();
+  const int blocks = (a.N + tokens - 1) / tokens, ranks = (a.R + 16 * MR - 1) / (16 * MR);
+  // d_in over as many blocks as leave about one block an SM, 512 elements each at least.
+  int split = 1;
+  while (split < 8 && (long long)blocks * ranks * a.B * split * 2 <= sms && a.K / (2 * split) >= 512) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks * split), (unsigned)ranks, (unsigned)a.B);
+  cfg.blockDim = dim3(32 * TW * KW);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)split, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, proj_low_kernel<kOneByte, MR, NT, TW, KW, U>, a, split);
 }
 
 template <bool kOneByte>
@@ -1040,9 +1075,9 @@ int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
   // Few rows of a request: blocks of 16 ranks, 8 ways along d_in; many: 64 rows of up to 32 ranks, 4 ways.
   cudaError_t err = cudaSuccess;
   if (a.adapter) {
-    if (a.N <= 8) err = launch_low<kOneByte, 1, 1, 1, 8, 2>(a, st);
-    else if (a.R <= 16) err = launch_low<kOneByte, 1, 4, 2, 4, 1>(a, st);
-    else err = launch_low<kOneByte, 2, 4, 2, 4, 1>(a, st);
+    if (a.N <= 8) err = launch_low<kOneByte, 1, 1, 1, 8, 2>(a, sms, st);
+    else if (a.R <= 16) err = launch_low<kOneByte, 1, 4, 2, 4, 1>(a, sms, st);
+    else err = launch_low<kOneByte, 2, 4, 2, 4, 1>(a, sms, st);
   }
   if (err != cudaSuccess) return KDTV_ERR_CUDA;
   const size_t smem = (size_t)a.stages * (kWBytes + a.half_cols * kUnitBytes) +
