@@ -16,7 +16,7 @@
 // launched while the first runs; only the adapters' units wait for it.
 //
 // Work.  A unit is 128 bytes of d_in (64 bf16, 128 one-byte elements) or two
-// chunks of 16 ranks, for one tile of 256 outputs and up to 256 (one byte: 224)
+// chunks of 16 ranks, for one tile of 256 outputs and up to 256 (one byte: 192)
 // tokens.  A pair of CTAs works on a tile: each has 128 outputs, loads those rows
 // of W and half of the tokens, and the products read both halves (cta_group::2), so
 // that a unit costs each SM 32 KiB where a CTA by itself with as many products
@@ -27,7 +27,11 @@
 //
 // One byte: exponent bytes travel as they are to the tensor cores, which take
 // one per 32 elements and operand row (block-scaled products), so sums are in true
-// units and the adapters' bf16 products add to them.
+// units and the adapters' bf16 products add to them.  They read them from TMEM, a
+// row's four bytes of a unit a word, rows 32 j + l in lane l of column j, the same in
+// each quarter of the lanes: four warps bring them there, four units at a time.
+// (Copies from shared memory by the tensor cores' own pipe, tcgen05.cp, kept it from
+// multiplying for 20 % of the time.)
 
 #include <cuda.h>
 
@@ -52,7 +56,7 @@ constexpr int kMaxGroups = 512;            // groups of requests in a launch
 constexpr int kMaxPairs = 128;
 constexpr int kWords = KDTV_MAX_ADAPTERS / 32;
 constexpr int kScaleBytes = 3 * 512;       // a unit's exponent bytes: W, tokens 0 - 127, the others
-constexpr int kWindow = 4, kWindows = 3;   // units whose exponent bytes go together; such windows under way
+constexpr int kWindow = 4, kWindows = 2;   // units whose exponent bytes go together; such windows in TMEM
 constexpr int kSuper = 8;                  // token tiles that share a W tile in a row
 
 // ---- which adapters a tile has -------------------------------------------------------------
@@ -153,7 +157,7 @@ __device__ __forceinline__ uint4 widen8(uint2 w, uint32_t byte) {
 }
 
 template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
-__global__ void __launch_bounds__(32 * TW * KW, 2) proj_low_kernel(const __grid_constant__ ProjArgs a, int split) {
+__global__ void __launch_bounds__(32 * TW * KW, kOneByte ? 3 : 2) proj_low_kernel(const __grid_constant__ ProjArgs a, int split) {
   __shared__ uint32_t bits[kWords];
   __shared__ int s_slot, s_slots;
   __shared__ float red[KW / 2 * TW][MR * NT * 4][32];
@@ -341,8 +345,8 @@ __device__ __forceinline__ uint32_t arrivals(int i) {
 
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpOut = 4, kWarpRelay = 2, kWarpScale = 8;   // (3: planning only)
 __host__ __device__ constexpr int threads_of(bool one_byte) { return one_byte ? 384 : 256; }
-__host__ __device__ constexpr int acc_columns(bool one_byte) { return one_byte ? 224 : 256; }
-constexpr uint32_t kScaleColumn = 448;      // one byte: exponents behind the two accumulators
+__host__ __device__ constexpr int acc_columns(bool one_byte) { return one_byte ? 192 : 256; }
+constexpr uint32_t kScaleColumn = 384;      // one byte: exponents behind the two accumulators, 16 columns a unit
 
 // Shared memory behind the ring.
 struct ProjShared {
@@ -468,14 +472,27 @@ __device__ __forceinline__ uint32_t idesc_scaled(int N, int byte) {
   return ((uint32_t)byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(2 * kFeatures >> 4) << 24) |
          ((uint32_t)byte << 29);
 }
-// 512 bytes of exponents, of each CTA: four words of 32 lanes, the same in each quarter of TMEM's lanes.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
-  uint64_t d = 0;                           // no swizzle, 8-row groups 128 bytes apart
-  d |= (uint64_t)((smem >> 4) & 0x3FFFu);
-  d |= (uint64_t)(128u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(d) : "memory");
+// Twelve words of a lane, four columns each: of W's rows, of tokens 0 - 127, of the others.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
+               :: "r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// Four warps meet at named barrier `id`: whether all of them say so.
+__device__ __forceinline__ bool all_of(int id, bool ok) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+               "bar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((uint32_t)ok), "r"(id) : "memory");
+  return r != 0u;
+}
+
 // One output by itself, for a value that is not finite where several adapters share a tile.
 template <bool kOneByte>
 __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
@@ -520,7 +537,7 @@ __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
 
 // (Registers for two blocks, although shared memory has room for one: the first kernel's are beside it.)
 template <bool kOneByte>
-__global__ void __launch_bounds__(threads_of(kOneByte), 2)
+__global__ void __launch_bounds__(threads_of(kOneByte), kOneByte ? 1 : 2)
 proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ ProjArgs a, int stall) {
@@ -528,7 +545,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stage_bytes = kWBytes + a.half_cols * kUnitBytes;
   const uint32_t rank = cluster_ctarank();
-  ProjShared& sh = *reinterpret_cast<ProjShared*>(smem + (size_t)a.stages * stage_bytes + (kOneByte ? kWindows * kWindow * kScaleBytes : 0));
+  ProjShared& sh = *reinterpret_cast<ProjShared*>(smem + (size_t)a.stages * stage_bytes + (kOneByte ? 2 * kWindow * kScaleBytes : 0));
   const uint32_t ring = smem_u32(smem), scales = ring + a.stages * stage_bytes, bars = smem_u32(sh.bars);
   auto BAR = [&](int i) { return bars + 8u * i; };
   const Guard guard{&sh.abort, a.status, stall ? 20000000u : 2000000000u};
@@ -732,10 +749,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             }
             const uint64_t ad = smem_desc(at, 16, 1024), bd = smem_desc(at + kWBytes, 16, 1024);
             if constexpr (kOneByte) {
-              const uint32_t sc = tmem + kScaleColumn + (k % kWindow) * 16, ss = scales + (window * kWindow + k % kWindow) * kScaleBytes;
-              copy_scales(sc, ss);
-              copy_scales(sc + 4, ss + 512);
-              if (cols > 128) copy_scales(sc + 8, ss + 1024);
+              const uint32_t sc = tmem + kScaleColumn + (window * kWindow + k % kWindow) * 16;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
                 mma_scaled(d, ad + 2 * kk, bd + 2 * kk, idesc_scaled(cols, kk), sc, sc + 4, acc);
@@ -774,13 +788,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     // ---- sums to outputs: warp q has TMEM lanes 32 q .., one output each -------------------------------
     const int q = warp - kWarpOut, t = threadIdx.x - 32 * kWarpOut;
     auto meet = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    auto agree = [&](bool ok) {                // of the four warps
-      uint32_t r;
-      asm volatile("{\n\t.reg .pred p, r;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                   "bar.red.and.pred r, 1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}"
-                   : "=r"(r) : "r"((uint32_t)ok) : "memory");
-      return r != 0u;
-    };
+    auto agree = [&](bool ok) { return all_of(1, ok); };
     grid_dep_wait();                           // (no CTA ends before the first kernel)
     if (blockIdx.x == 0) leave_plan(a, sh, t);
     for (int n = 0; next(a, sh, w, it); ++n) {
@@ -888,8 +896,11 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     };
     auto sts32 = [](uint32_t to, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(to), "r"(v) : "memory"); };
     const uint32_t at = (t & 31) * 16 + (t >> 5) * 4;
+    // (all four warps go on, or none: they meet)
+    auto agree = [&](bool ok) { return all_of(2, ok); };
     bool alive = true;
-    while (alive && next(a, sh, w, it)) {
+    int staged = 0;
+    while (agree(alive) && next(a, sh, w, it)) {
       const int cols = 2 * half_cols_of(a, it.hr);
       const uint8_t* rows[3] = {nullptr, nullptr, nullptr};
       if ((2 * it.f + (int)rank) * kFeatures + t < a.M) rows[0] = a.W_scale + (long long)((2 * it.f + rank) * kFeatures + t) * row_bytes;
@@ -899,26 +910,41 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         if (t + 128 * h < cols && column(a, it.g, it.j, it.hr, t + 128 * h, &b, &i))
           rows[1 + h] = a.x_scale + ((long long)b * a.N + i) * row_bytes;
       }
-      const int last = (min(it.k1, a.base) - 1) / kWindow;
-      uint4 then[3];
-      if (it.k0 < a.base)
+      if (it.k0 >= a.base) continue;
+      const int last = (min(it.k1, a.base) - 1) / kWindow, parts = cols > 128 ? 3 : 2;
+      uint4 now[3], soon[3], later[3];         // two windows ahead: they come from DRAM
 #pragma unroll
-        for (int r = 0; r < 3; ++r) then[r] = bytes(rows[r], it.k0 / kWindow);
-      for (int u = it.k0 / kWindow; it.k0 < a.base && u <= last; ++u) {
-        const uint4 now[3] = {then[0], then[1], then[2]};
-#pragma unroll
-        for (int r = 0; r < 3; ++r) then[r] = bytes(rows[r], u + 1);
-        alive = wait_warp(guard, BAR(B_S_EMPTY + window), w_phase ^ 1u);
-        if (!alive) break;
-        const uint32_t to = scales + window * (kWindow * kScaleBytes) + at;
+      for (int r = 0; r < 3; ++r) {
+        soon[r] = bytes(rows[r], it.k0 / kWindow);
+        later[r] = bytes(rows[r], it.k0 / kWindow + 1);
+      }
+      for (int u = it.k0 / kWindow; u <= last; ++u) {
 #pragma unroll
         for (int r = 0; r < 3; ++r) {
-          sts32(to + 512 * r, now[r].x);
-          sts32(to + 512 * r + kScaleBytes, now[r].y);
-          sts32(to + 512 * r + 2 * kScaleBytes, now[r].z);
-          sts32(to + 512 * r + 3 * kScaleBytes, now[r].w);
+          now[r] = soon[r];
+          soon[r] = later[r];
+          later[r] = bytes(rows[r], u + 2);
         }
-        fence_async_smem();
+        const uint32_t stage = scales + (staged++ & 1) * (kWindow * kScaleBytes);
+#pragma unroll
+        for (int r = 0; r < 3; ++r) {
+          sts32(stage + at + 512 * r, now[r].x);
+          sts32(stage + at + 512 * r + kScaleBytes, now[r].y);
+          sts32(stage + at + 512 * r + 2 * kScaleBytes, now[r].z);
+          sts32(stage + at + 512 * r + 3 * kScaleBytes, now[r].w);
+        }
+        // (The next window is staged beside this one; the one after it when all four warps are past the next
+        // meeting.)
+        if (!agree(alive)) break;
+        alive = wait_warp(guard, BAR(B_S_EMPTY + window), w_phase ^ 1u);
+        if (!alive) continue;
+        tc_fence_after();
+        const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kScaleColumn + window * (kWindow * 16);
+#pragma unroll
+        for (int k = 0; k < kWindow; ++k)
+          for (int r = 0; r < parts; ++r) tmem_st4(to + 16 * k + 4 * r, lds128(stage + k * kScaleBytes + 512 * r + lane * 16));
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR((rank == 0 ? B_S_FULL : B_S_LOCAL) + window));
         advance_window();
@@ -1076,12 +1102,12 @@ int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
   cudaError_t err = cudaSuccess;
   if (a.adapter) {
     if (a.N <= 8) err = launch_low<kOneByte, 1, 1, 1, 8, 2>(a, sms, st);
-    else if (a.R <= 16) err = launch_low<kOneByte, 1, 4, 2, 4, 1>(a, sms, st);
-    else err = launch_low<kOneByte, 2, 4, 2, 4, 1>(a, sms, st);
+    else if (a.R <= 16) err = launch_low<kOneByte, 1, kOneByte ? 2 : 4, 2, 4, 1>(a, sms, st);
+    else err = launch_low<kOneByte, 2, kOneByte ? 2 : 4, 2, 4, 1>(a, sms, st);
   }
   if (err != cudaSuccess) return KDTV_ERR_CUDA;
   const size_t smem = (size_t)a.stages * (kWBytes + a.half_cols * kUnitBytes) +
-                      (kOneByte ? kWindows * kWindow * kScaleBytes : 0) + sizeof(ProjShared);
+                      (kOneByte ? 2 * kWindow * kScaleBytes : 0) + sizeof(ProjShared);
   const auto kern = proj_tc_kernel<kOneByte>;
   if (allow_smem(kern, smem) != cudaSuccess) return KDTV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -1134,7 +1160,7 @@ bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a) {
   a->features = (d->d_out + 2 * kFeatures - 1) / (2 * kFeatures);
   if ((long long)a->groups * a->blocks * a->features > 0x3fffffffll) return false;
   // As many stages as leave room for the first kernel's blocks beside this one's (17 KiB, and 1 KiB each).
-  a->stages = (int)((228 * 1024 - 20 * 1024 - sizeof(ProjShared) - (one_byte ? kWindows * kWindow * kScaleBytes : 0)) /
+  a->stages = (int)((228 * 1024 - 20 * 1024 - sizeof(ProjShared) - (one_byte ? 2 * kWindow * kScaleBytes : 0)) /
                     (kWBytes + a->half_cols * kUnitBytes));
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->by_requests = divisor((unsigned)a->requests);
