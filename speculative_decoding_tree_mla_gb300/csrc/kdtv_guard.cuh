@@ -20,16 +20,31 @@ __device__ __forceinline__ uint32_t timer_lo() {
 }
 // Short code: a wait stands at some thirty places of loops that share an
 // instruction cache.
-// kCluster: for what other CTAs of the cluster did before they arrived.
-template <bool kCluster = false>
 __device__ __forceinline__ bool wait(const Guard& g, uint32_t bar, uint32_t parity) {
-  if (__builtin_expect(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity), 1)) return true;
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
   const uint32_t t0 = timer_lo();
 #pragma unroll 1
-  while (!(kCluster ? mbar_try_wait_cluster_sleep(bar, parity, 20000u) : mbar_try_wait_sleep(bar, parity, 20000u))) {
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
     if (*g.abort) return false;
     if (timer_lo() - t0 > g.limit) {
       atomicExch(g.status, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);   // over any other code: the combine kernel asks
+      *g.abort = 1u;
+      return false;
+    }
+  }
+  return true;
+}
+// The same by polling: for a single thread on the critical path, which would pay the wake-up from a sleep (a few
+// hundred cycles) at every phase.
+__device__ __forceinline__ bool wait_poll(const Guard& g, uint32_t bar, uint32_t parity) {
+  if (__builtin_expect(mbar_test_wait(bar, parity), 1)) return true;
+  const uint32_t t0 = timer_lo();
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_test_wait(bar, parity); ++i) {
+    if (i & 63u) continue;
+    if (*g.abort) return false;
+    if (timer_lo() - t0 > g.limit) {
+      atomicExch(g.status, (unsigned)KDTV_ERR_DEVICE_TIMEOUT);
       *g.abort = 1u;
       return false;
     }

@@ -29,6 +29,7 @@ struct ProjArgs {
   int pairs;                               // most pairs of chunks that a tile may have
   int features;                            // 256-row tiles of W
   int stages, scale_mode;                  // ring entries; how scale rows may be read
+  int shared;                              // columns that the two accumulators have in common
   bool wide;                               // rows of y are written 16 bytes at a time
   char* parts;                             // A x in two bf16 parts: [tile][pair][half][chunk][part][half_cols][16]
   float* partial;                          // [pair][2 places][CTA][2 half_cols][128] sums of cut tiles

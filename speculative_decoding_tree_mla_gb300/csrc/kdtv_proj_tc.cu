@@ -16,8 +16,7 @@
 // launched while the first runs; only the adapters' units wait for it.
 //
 // Work.  A unit is 128 bytes of d_in (64 bf16, 128 one-byte elements) or two
-// chunks of 16 ranks, for one tile of 256 outputs and up to 256 (one byte: 192)
-// tokens.  A pair of CTAs works on a tile: each has 128 outputs, loads those rows
+// chunks of 16 ranks, for one tile of 256 outputs and up to 256 tokens.  A pair of CTAs works on a tile: each has 128 outputs, loads those rows
 // of W and half of the tokens, and the products read both halves (cta_group::2), so
 // that a unit costs each SM 32 KiB where a CTA by itself with as many products
 // would load 48.  Whole tiles go round the pairs; what does not fill a round is
@@ -29,7 +28,8 @@
 // one per 32 elements and operand row (block-scaled products), so sums are in true
 // units and the adapters' bf16 products add to them.  They read them from TMEM, a
 // row's four bytes of a unit a word, rows 32 j + l in lane l of column j, the same in
-// each quarter of the lanes: four warps bring them there, four units at a time.
+// each quarter of the lanes: four warps bring them there, and a unit is complete
+// when its operands have landed and both CTAs' exponents are in place.
 // (Copies from shared memory by the tensor cores' own pipe, tcgen05.cp, kept it from
 // multiplying for 20 % of the time.)
 
@@ -56,7 +56,8 @@ constexpr int kMaxGroups = 512;            // groups of requests in a launch
 constexpr int kMaxPairs = 128;
 constexpr int kWords = KDTV_MAX_ADAPTERS / 32;
 constexpr int kScaleBytes = 3 * 512;       // a unit's exponent bytes: W, tokens 0 - 127, the others
-constexpr int kWindow = 4, kWindows = 2;   // units whose exponent bytes go together; such windows in TMEM
+constexpr int kWindow = 4;                 // units whose exponent bytes are loaded together (16 bytes of a row)
+constexpr int kScaleColumns = 12;          // a unit's exponents in TMEM: W's, tokens 0 - 127, the others
 constexpr int kSuper = 8;                  // token tiles that share a W tile in a row
 
 // ---- which adapters a tile has -------------------------------------------------------------
@@ -329,24 +330,28 @@ __global__ void __launch_bounds__(32 * TW * KW, kOneByte ? 3 : 2) proj_low_kerne
 // ---- the projection --------------------------------------------------------------------------
 enum {
   B_FULL = 0, B_EMPTY = B_FULL + kMaxStages, B_ACC_FULL = B_EMPTY + kMaxStages, B_ACC_EMPTY = B_ACC_FULL + 2,
-  B_DONE = B_ACC_EMPTY + 2, B_STALL,
-  // one byte, a window's exponents: ready in both CTAs, used up, ready in the second CTA, the same seen by the first
-  B_S_FULL, B_S_EMPTY = B_S_FULL + kWindows, B_S_LOCAL = B_S_EMPTY + kWindows, B_S_PEER = B_S_LOCAL + kWindows,
-  B_COUNT = B_S_PEER + kWindows
+  B_ACC_PART = B_ACC_EMPTY + 2,                // one byte: the shared columns are read
+  B_DONE = B_ACC_PART + 2, B_STALL, B_COUNT
 };
 
 // Arrivals of a barrier's phase.
-__device__ __forceinline__ uint32_t arrivals(int i) {
-  if (i < B_EMPTY) return 2;                                // both CTAs' producers
-  if (i >= B_ACC_EMPTY && i < B_DONE) return 8;             // both CTAs' four warps
-  if (i >= B_S_FULL && i < B_S_EMPTY) return 5;             // four warps, and the peer's through the relay
-  return i >= B_S_LOCAL && i < B_S_PEER ? 4 : 1;
+__device__ __forceinline__ uint32_t arrivals(bool one_byte, int i) {
+  if (i < B_EMPTY) return one_byte ? 10 : 2;                // both CTAs' producers, and their four warps
+  return i >= B_ACC_EMPTY && i < B_DONE ? 8 : 1;            // both CTAs' four warps
 }
 
-constexpr int kWarpTma = 0, kWarpMma = 1, kWarpOut = 4, kWarpRelay = 2, kWarpScale = 8;   // (3: planning only)
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpOut = 4, kWarpScale = 8;   // (2, 3: planning only)
 __host__ __device__ constexpr int threads_of(bool one_byte) { return one_byte ? 384 : 256; }
-__host__ __device__ constexpr int acc_columns(bool one_byte) { return one_byte ? 192 : 256; }
-constexpr uint32_t kScaleColumn = 384;      // one byte: exponents behind the two accumulators, 16 columns a unit
+// Two accumulators of 256 columns take turns.  One byte: the exponents need 72 of TMEM's 512 columns, so those of
+// more than 128 columns share kShared of theirs (the first one's last are the second one's first).  They are read first and
+// given back at once, so that the next tile's products wait for that only.  (Tiles of 192 tokens without sharing: 435
+// us where 256 take 328, both without exponents, for 8192 tokens, 8192 x 8192.)
+constexpr int kTokens = 256, kShared = 80;
+__device__ __forceinline__ uint32_t acc_at(const ProjArgs& a, int n) { return (n & 1) * (kTokens - a.shared); }
+// The exponents of a ring entry: behind the accumulators, or, where those have 128 columns, between them and behind.
+__device__ __forceinline__ uint32_t scale_at(const ProjArgs& a, int slot) {
+  return a.shared ? 2 * kTokens - kShared + slot * kScaleColumns : (slot & 1) * kTokens + kTokens / 2 + (slot >> 1) * kScaleColumns;
+}
 
 // Shared memory behind the ring.
 struct ProjShared {
@@ -535,9 +540,9 @@ __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
   return sum;
 }
 
-// (Registers for two blocks, although shared memory has room for one: the first kernel's are beside it.)
+// (Registers that leave room for a block of the first kernel beside this one's.)
 template <bool kOneByte>
-__global__ void __launch_bounds__(threads_of(kOneByte), kOneByte ? 1 : 2)
+__global__ void __maxnreg__(kOneByte ? 112 : 128)
 proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ ProjArgs a, int stall) {
@@ -554,7 +559,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   // ---- set up, and plan: every CTA derives the same tiles from n_live and adapter ------------------
   if (threadIdx.x < B_COUNT) {
     const int i = threadIdx.x;
-    mbar_init(BAR(i), arrivals(i));
+    mbar_init(BAR(i), arrivals(kOneByte, i));
   }
   if (threadIdx.x == 0) sh.abort = 0u;
   fence_mbar_init();
@@ -644,19 +649,12 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   auto LEAD = [&](int i) { return lead + 8u * i; };
   Walk w = walk(sh);
   Item it;
-  int slot = 0, window = 0;
-  uint32_t phase = 0u, w_phase = 0u;
+  int slot = 0;
+  uint32_t phase = 0u;
   auto advance = [&]() {
     if (++slot == a.stages) {
       slot = 0;
       phase ^= 1u;
-    }
-  };
-
-  auto advance_window = [&]() {
-    if (++window == kWindows) {
-      window = 0;
-      w_phase ^= 1u;
     }
   };
 
@@ -689,14 +687,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         }
         __syncwarp();
       }
-      for (int k = it.k0; k < it.k1; ++k) {
-        alive = wait_warp(guard, BAR(B_EMPTY + slot), phase ^ 1u);
-        if (!alive) break;
-        if (k >= a.base && !waited) {
-          grid_dep_wait();                     // v is written
-          waited = true;
-        }
-        if (lane == 0) {
+      if (lane == 0)
+        for (int k = it.k0; k < it.k1; ++k) {
+          alive = wait_poll(guard, BAR(B_EMPTY + slot), phase ^ 1u);
+          if (!alive) break;
           const uint32_t full = LEAD(B_FULL + slot), dst = ring + slot * stage_bytes;
           const int f = (2 * it.f + rank) * kFeatures;
           if (k < a.base) {
@@ -705,6 +699,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             tma_load_3d_pair(dst + kWBytes, &tm_x, full, k * (kOneByte ? 128 : 64), a.by_rows_of ? (2 * it.j + rank) * it.hr : 0,
                              it.g * a.requests + (a.by_rows_of ? 0 : rank * a.half_requests));
           } else {
+            if (!waited) grid_dep_wait();      // v is written
+            waited = true;
             const int p = k - a.base, two = min(2, it.chunks - 2 * p);
             mbar_expect_tx_cluster(full, two * (kFeatures * 32) + a.half_cols * 128);
             for (int c = 2 * p; c < 2 * p + two; ++c) {
@@ -714,50 +710,40 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             tma_load_2d_pair(dst + kWBytes, &tm_v, full, 0,
                              (int)((((long long)(it.g * a.blocks + it.j) * a.pairs + p) * 2 + rank) * (a.half_cols / 2)));
           }
+          advance();
+          ++loads;
         }
-        __syncwarp();
-        advance();
-        ++loads;
-      }
-      __syncwarp();
+      alive = __shfl_sync(0xffffffffu, (int)alive, 0) != 0;
     }
-    for (int x = loads > a.stages ? loads - a.stages : 0; x < loads; ++x)    // every copy has landed, and is used up
-      drain(guard, BAR(B_EMPTY + x % a.stages), (x / a.stages) & 1);
+    if (lane == 0)                             // every copy has landed, and is used up
+      for (int x = loads > a.stages ? loads - a.stages : 0; x < loads; ++x)
+        drain(guard, BAR(B_EMPTY + x % a.stages), (x / a.stages) & 1);
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ---- products ------------------------------------------------------------------------------
     if (lane == 0 && rank == 0) {
       bool alive = true;
       for (int n = 0; alive && next(a, sh, w, it); ++n) {
-        const uint32_t d = tmem + (n & 1) * acc_columns(kOneByte);
-        alive = wait<true>(guard, BAR(B_ACC_EMPTY + (n & 1)), ((n >> 1) & 1) ^ 1u);
+        const uint32_t d = tmem + acc_at(a, n);
+        alive = wait(guard, BAR(B_ACC_EMPTY + (n & 1)), ((n >> 1) & 1) ^ 1u) &&
+                (!kOneByte || n == 0 || wait_poll(guard, BAR(B_ACC_PART + ((n - 1) & 1)), ((n - 1) >> 1) & 1));
+        tc_fence_after();
         const int cols = 2 * half_cols_of(a, it.hr);
         const uint32_t idesc = idesc_bf16(2 * kFeatures, cols, 0, 0);
         uint32_t acc = 0u;
         for (int k = it.k0; alive && k < it.k1; ++k) {
-          alive = wait(guard, BAR(B_FULL + slot), phase);
+          alive = wait_poll(guard, BAR(B_FULL + slot), phase);
           if (!alive) break;
           tc_fence_after();
           const uint32_t at = ring + slot * stage_bytes;
           if (k < a.base) {
-            if constexpr (kOneByte) {
-              if (k == it.k0 || k % kWindow == 0) {
-                alive = wait(guard, BAR(B_S_FULL + window), w_phase);
-                if (!alive) break;
-                tc_fence_after();
-              }
-            }
             const uint64_t ad = smem_desc(at, 16, 1024), bd = smem_desc(at + kWBytes, 16, 1024);
             if constexpr (kOneByte) {
-              const uint32_t sc = tmem + kScaleColumn + (window * kWindow + k % kWindow) * 16;
+              const uint32_t sc = tmem + scale_at(a, slot);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
                 mma_scaled(d, ad + 2 * kk, bd + 2 * kk, idesc_scaled(cols, kk), sc, sc + 4, acc);
                 acc = 1u;
-              }
-              if (k % kWindow == kWindow - 1 || k + 1 == min(it.k1, a.base)) {
-                mma_commit_pair(BAR(B_S_EMPTY + window), 3);
-                advance_window();
               }
             } else {
 #pragma unroll
@@ -805,7 +791,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       }
       if (!agree(wait_warp(guard, BAR(B_ACC_FULL + (n & 1)), (n >> 1) & 1))) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (n & 1) * acc_columns(kOneByte) + ((uint32_t)(32 * q) << 16);
+      const uint32_t acc = tmem + acc_at(a, n) + ((uint32_t)(32 * q) << 16);
       const int f = (2 * it.f + rank) * kFeatures + 32 * q + lane;
       const bool mixed = a.requests > 1 && it.chunks > 0;
       auto put = [&](int c, float v) {
@@ -818,60 +804,94 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         }
         static_cast<__nv_bfloat16*>(a.y)[at + f] = __float2bfloat16_rn(v);
       };
-      auto released = [&]() {
+      auto released = [&](int bar) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(LEAD(B_ACC_EMPTY + (n & 1)));
+        if (lane == 0) mbar_arrive_pair(LEAD(bar + (n & 1)));
       };
-      if (it.cut < 0) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          float v[16];
-          __syncwarp();
-          tmem_ld16(acc + c0, v);
-          tmem_wait_ld();
-          bool odd = !a.wide;
-          if (mixed)
-#pragma unroll
-            for (int c = 0; c < 16; ++c) odd |= !(fabsf(v[c]) < INFINITY) && sh.y_at[c0 + c] >= 0;
-          if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
-              float x = 0.f;
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x = c == k ? v[k] : x;
-              put(c0 + c, x);
-            }
-            continue;
-          }
-          // through shared memory, so that a lane writes 8 outputs of a token at once
-          __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(sh.rows[q]);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) rows[c * 32 + lane] = __float2bfloat16_rn(v[c]);
-          __syncwarp();
-          const int f8 = f - lane + (lane & 3) * 8;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = h * 8 + (lane >> 2);
-            const long long to = sh.y_at[c0 + c];
-            const uint4 w8 = *reinterpret_cast<const uint4*>(rows + c * 32 + (lane & 3) * 8);
-            if (to >= 0 && f8 < a.M) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f8) = w8;
-          }
-        }
-        released();
-        continue;
-      }
-      float* mine = partial_of(a, (int)(blockIdx.x >> 1), it.seg, rank) + 32 * q + lane;
-#pragma unroll 1
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        float v[32];
+      float* mine = it.cut < 0 ? nullptr : partial_of(a, (int)(blockIdx.x >> 1), it.seg, rank) + 32 * q + lane;
+      // 16 columns as bf16 pairs, through shared memory, so that a lane writes 8 outputs of a token at once
+      auto write = [&](int c0, const uint32_t (&p)[8]) {
+        uint16_t* rows = reinterpret_cast<uint16_t*>(sh.rows[q]);
         __syncwarp();
-        tmem_ld32(acc + c0, v);
-        tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) mine[(c0 + c) * kFeatures] = v[c];
+        for (int c = 0; c < 16; ++c) rows[c * 32 + lane] = (uint16_t)(p[c >> 1] >> (16 * (c & 1)));
+        __syncwarp();
+        const int f8 = f - lane + (lane & 3) * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = h * 8 + (lane >> 2);
+          const long long to = sh.y_at[c0 + c];
+          const uint4 w8 = *reinterpret_cast<const uint4*>(rows + c * 32 + (lane & 3) * 8);
+          if (to >= 0 && f8 < a.M) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f8) = w8;
+        }
+      };
+      auto emit = [&](int c0, const float (&v)[16]) {
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) mine[(c0 + c) * kFeatures] = v[c];
+          return;
+        }
+        bool odd = !a.wide;
+        if (mixed)
+#pragma unroll
+          for (int c = 0; c < 16; ++c) odd |= !(fabsf(v[c]) < INFINITY) && sh.y_at[c0 + c] >= 0;
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+          for (int c = 0; c < 16; ++c) {
+            float x = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x = c == k ? v[k] : x;
+            put(c0 + c, x);
+          }
+          __syncwarp();
+          return;
+        }
+        uint32_t p[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+        write(c0, p);
+      };
+      int skip0 = 0, skip1 = 0;                // columns that come first
+      if constexpr (kOneByte) {
+        skip0 = (n & 1) ? 0 : min(cols, kTokens - a.shared);
+        skip1 = (n & 1) ? min(cols, a.shared) : cols;
+        if (!mine && !mixed && a.wide) {       // read and rounded, then given back, then written
+          uint32_t p[kShared / 16][8];
+#pragma unroll
+          for (int k = 0; k < kShared / 16; ++k)
+            if (skip0 + 16 * k < skip1) {
+              float v[16];
+              tmem_ld16(acc + skip0 + 16 * k, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) p[k][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            }
+          released(B_ACC_PART);
+#pragma unroll
+          for (int k = 0; k < kShared / 16; ++k)
+            if (skip0 + 16 * k < skip1) write(skip0 + 16 * k, p[k]);
+        } else {
+#pragma unroll 1
+          for (int c0 = skip0; c0 < skip1; c0 += 16) {
+            float v[16];
+            __syncwarp();
+            tmem_ld16(acc + c0, v);
+            tmem_wait_ld();
+            emit(c0, v);
+          }
+          released(B_ACC_PART);
+        }
       }
-      released();
+#pragma unroll 1
+      for (int c0 = skip0 == 0 ? skip1 : 0, end = skip0 == 0 ? cols : skip0; c0 < end; c0 += 16) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(acc + c0, v);
+        tmem_wait_ld();
+        emit(c0, v);
+      }
+      released(B_ACC_EMPTY);
     }
   } else if (kOneByte && warp >= kWarpScale) {
     // ---- exponent bytes: a thread has a row of W and up to two tokens, four units' bytes at a time ------
@@ -900,6 +920,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     auto agree = [&](bool ok) { return all_of(2, ok); };
     bool alive = true;
     int staged = 0;
+    uint32_t stage = scales;
     while (agree(alive) && next(a, sh, w, it)) {
       const int cols = 2 * half_cols_of(a, it.hr);
       const uint8_t* rows[3] = {nullptr, nullptr, nullptr};
@@ -910,63 +931,48 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         if (t + 128 * h < cols && column(a, it.g, it.j, it.hr, t + 128 * h, &b, &i))
           rows[1 + h] = a.x_scale + ((long long)b * a.N + i) * row_bytes;
       }
-      if (it.k0 >= a.base) continue;
-      const int last = (min(it.k1, a.base) - 1) / kWindow, parts = cols > 128 ? 3 : 2;
+      const int parts = cols > 128 ? 3 : 2;
       uint4 now[3], soon[3], later[3];         // two windows ahead: they come from DRAM
 #pragma unroll
       for (int r = 0; r < 3; ++r) {
         soon[r] = bytes(rows[r], it.k0 / kWindow);
         later[r] = bytes(rows[r], it.k0 / kWindow + 1);
       }
-      for (int u = it.k0 / kWindow; u <= last; ++u) {
+      for (int k = it.k0; k < it.k1; ++k) {
+        if (k < a.base && (k == it.k0 || k % kWindow == 0)) {
 #pragma unroll
-        for (int r = 0; r < 3; ++r) {
-          now[r] = soon[r];
-          soon[r] = later[r];
-          later[r] = bytes(rows[r], u + 2);
+          for (int r = 0; r < 3; ++r) {
+            now[r] = soon[r];
+            soon[r] = later[r];
+            later[r] = bytes(rows[r], k / kWindow + 2);
+          }
+          // (The next window is staged beside this one; the one after it when all four warps are past the next
+          // meeting.)
+          stage = scales + (staged++ & 1) * (kWindow * kScaleBytes);
+#pragma unroll
+          for (int r = 0; r < 3; ++r) {
+            sts32(stage + at + 512 * r, now[r].x);
+            sts32(stage + at + 512 * r + kScaleBytes, now[r].y);
+            sts32(stage + at + 512 * r + 2 * kScaleBytes, now[r].z);
+            sts32(stage + at + 512 * r + 3 * kScaleBytes, now[r].w);
+          }
+          if (!agree(alive)) break;
         }
-        const uint32_t stage = scales + (staged++ & 1) * (kWindow * kScaleBytes);
-#pragma unroll
-        for (int r = 0; r < 3; ++r) {
-          sts32(stage + at + 512 * r, now[r].x);
-          sts32(stage + at + 512 * r + kScaleBytes, now[r].y);
-          sts32(stage + at + 512 * r + 2 * kScaleBytes, now[r].z);
-          sts32(stage + at + 512 * r + 3 * kScaleBytes, now[r].w);
+        alive = alive && wait_warp(guard, BAR(B_EMPTY + slot), phase ^ 1u);
+        if (!alive) continue;                  // (until the next meeting)
+        if (k < a.base) {
+          tc_fence_after();
+          const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + scale_at(a, slot);
+          const uint32_t from = stage + (k % kWindow) * kScaleBytes + lane * 16;
+          for (int r = 0; r < parts; ++r) tmem_st4(to + 4 * r, lds128(from + 512 * r));
+          tmem_wait_st();
+          tc_fence_before();
         }
-        // (The next window is staged beside this one; the one after it when all four warps are past the next
-        // meeting.)
-        if (!agree(alive)) break;
-        alive = wait_warp(guard, BAR(B_S_EMPTY + window), w_phase ^ 1u);
-        if (!alive) continue;
-        tc_fence_after();
-        const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kScaleColumn + window * (kWindow * 16);
-#pragma unroll
-        for (int k = 0; k < kWindow; ++k)
-          for (int r = 0; r < parts; ++r) tmem_st4(to + 16 * k + 4 * r, lds128(stage + k * kScaleBytes + 512 * r + lane * 16));
-        tmem_wait_st();
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR((rank == 0 ? B_S_FULL : B_S_LOCAL) + window));
-        advance_window();
+        if (lane == 0) mbar_arrive_pair(LEAD(B_FULL + slot));
+        advance();
       }
     }
-  }
-  else if (kOneByte && warp == kWarpRelay) {
-    // ---- the second CTA's exponents are ready: its relay tells the first CTA's (an arrival that orders memory
-    // across the pair takes some 500 cycles; the issuing thread is spared it) -----------------------------
-    bool alive = true;
-    while (alive && next(a, sh, w, it))
-      for (int u = it.k0 / kWindow; alive && it.k0 < a.base && u <= (min(it.k1, a.base) - 1) / kWindow; ++u) {
-        if (rank == 1) {
-          alive = wait_warp(guard, BAR(B_S_LOCAL + window), w_phase);
-          if (alive && lane == 0) mbar_arrive_remote(LEAD(B_S_PEER + window));
-        } else {
-          alive = __all_sync(0xffffffffu, wait<true>(guard, BAR(B_S_PEER + window), w_phase));
-          if (alive && lane == 0) mbar_arrive(BAR(B_S_FULL + window));
-        }
-        __syncwarp();
-        advance_window();
-      }
   }
   tc_fence_before();
   __syncthreads();
@@ -1138,7 +1144,7 @@ bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a) {
   if (d->dtype == KDTV_F32 || (d->flags & KDTV_FLAG_SIMT)) return false;
   if (!one_byte && d->d_in % 8) return false;
   if (d->adapters > 0 && d->rank % 8) return false;
-  const int cap = acc_columns(one_byte) / 2;  // columns of a half
+  const int cap = kTokens / 2;                // columns of a half
   a->by_rows_of = d->B == 1 || d->N > cap;
   if (a->by_rows_of) {                        // row blocks of one request
     a->requests = a->half_requests = 1;
@@ -1162,6 +1168,8 @@ bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a) {
   // As many stages as leave room for the first kernel's blocks beside this one's (17 KiB, and 1 KiB each).
   a->stages = (int)((228 * 1024 - 20 * 1024 - sizeof(ProjShared) - (one_byte ? 2 * kWindow * kScaleBytes : 0)) /
                     (kWBytes + a->half_cols * kUnitBytes));
+  a->shared = one_byte && a->half_cols > kTokens / 4 ? kShared : 0;
+  if (a->shared && a->stages > kShared / kScaleColumns) a->stages = kShared / kScaleColumns;
   if (a->stages > kMaxStages) a->stages = kMaxStages;
   a->by_requests = divisor((unsigned)a->requests);
   a->by_N = divisor((unsigned)d->N);

@@ -64,6 +64,12 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
                :: "r"(cluster_bar) : "memory");
 }
 
+// Arrive on a barrier of either CTA of a pair behind tensor-memory accesses: tcgen05.wait and
+// tcgen05.fence::before_thread_sync order those, so that no cluster-wide fence is needed (it takes some 500 cycles).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+}
+
 // Relaxed arrive on a barrier of another CTA in the cluster (no release fence:
 // only for signals that order nothing but loads whose values were consumed).
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_bar) {
