@@ -35,13 +35,10 @@
 
 #include <cuda.h>
 
-#include "kdtv_guard.cuh"
-#include "kdtv_proj.cuh"
+#include "kdtv_proj_tc.cuh"
 #include "kdtv_tmap.cuh"
 
 #include <string.h>
-
-#include <type_traits>
 
 namespace kdtv {
 namespace {
@@ -49,283 +46,14 @@ namespace {
 using namespace ptx;
 
 constexpr int kFeatures = 128;             // outputs of a CTA: half of a tile
-constexpr int kUnitBytes = 128;            // of d_in in a unit
 constexpr int kWBytes = kFeatures * kUnitBytes;
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 512;            // groups of requests in a launch
 constexpr int kMaxPairs = 128;
-constexpr int kWords = KDTV_MAX_ADAPTERS / 32;
 constexpr int kScaleBytes = 3 * 512;       // a unit's exponent bytes: W, tokens 0 - 127, the others
 constexpr int kWindow = 4;                 // units whose exponent bytes are loaded together (16 bytes of a row)
 constexpr int kScaleColumns = 12;          // a unit's exponents in TMEM: W's, tokens 0 - 127, the others
 constexpr int kSuper = 8;                  // token tiles that share a W tile in a row
-
-// ---- which adapters a tile has -------------------------------------------------------------
-// Adapters of a group of requests that have live rows, as a bitmap in shared
-// memory (by a warp); their places are the order of their numbers.
-__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
-
-__device__ __forceinline__ int group_bitmap(const ProjArgs& a, int g, uint32_t* bits, bool* live) {
-  const int lane = threadIdx.x & 31, words = (a.adapters + 31) / 32;
-  for (int w = lane; w < words; w += 32) bits[w] = 0u;
-  __syncwarp();
-  bool any = false;
-  for (int b = g * a.requests + lane; b < min(a.B, (g + 1) * a.requests); b += 32) {
-    if (live_rows(a.n_live, b, a.N) <= 0) continue;
-    const int id = proj_adapter(a, b);
-    any |= id != -2;
-    if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
-  }
-  *live = __any_sync(0xffffffffu, any);
-  __syncwarp();
-  int count = 0;
-  for (int w = lane; w < words; w += 32) count += __popc(bits[w]);
-  return warp_sum(count);
-}
-
-// A request's n rows in blocks as even as they can be, so that its last one is not a small rest: rows of half a
-// block.  (Tiles of several requests: all N rows.)
-__device__ __forceinline__ int half_rows_of(const ProjArgs& a, int n) {
-  if (!a.by_rows_of) return a.N;
-  const int blocks = max(1, (n + 2 * a.half_rows - 1) / (2 * a.half_rows));
-  return max(1, ((n + blocks - 1) / blocks + 1) / 2);
-}
-// Columns of half a tile whose half blocks have hr rows.
-__device__ __forceinline__ int half_cols_of(const ProjArgs& a, int hr) { return (a.half_requests * hr + 15) & ~15; }
-
-// The request and row of a tile's column; false: the column is not in use.
-__device__ __forceinline__ bool column(const ProjArgs& a, int g, int j, int hr, int c, int* b, int* i) {
-  const int hc = half_cols_of(a, hr), h = c >= hc, e = c - (h ? hc : 0);
-  if (a.by_rows_of) {
-    *b = g;
-    *i = (2 * j + h) * hr + e;
-    return e < hr && *i < a.N;
-  }
-  const int rq = (int)divide(e, a.by_N);
-  *b = g * a.requests + h * a.half_requests + rq;
-  *i = e - rq * a.N;
-  return rq < a.half_requests && *b < a.B;
-}
-// Where the 16 ranks of chunk c, part p of row i of request b start; their two 16-byte halves lie swizzled: `flip`
-// is the one that comes second.  hr: of the request.
-__device__ __forceinline__ char* part_row(const ProjArgs& a, int b, int i, int hr, int c, int p, int* flip) {
-  int g, j, h, col;
-  if (a.by_rows_of) {
-    g = b;
-    const int half = i / hr;
-    j = half >> 1;
-    h = half & 1;
-    col = i - half * hr;
-  } else {
-    g = (int)divide(b, a.by_requests);
-    const int rq = b - g * a.requests;
-    j = 0;
-    h = rq >= a.half_requests;
-    col = (rq - (h ? a.half_requests : 0)) * a.N + i;
-  }
-  *flip = (col >> 2) & 1;
-  return a.parts + (((long long)(g * a.blocks + j) * a.pairs + (c >> 1)) * 2 + h) * proj_half_bytes(a) +
-         (long long)((c & 1) * 2 + p) * a.half_cols * 32 + col * 32;
-}
-
-// ---- v = s_a A_a x ---------------------------------------------------------------------------
-// mma.sync products of 16 ranks and 8 tokens, straight from global memory: the
-// order of d_in within a product does not matter as long as both operands have
-// the same, so a lane's 16-byte load (8 elements of a row) is two products'
-// fragments.  A warp has 16 MR ranks, 8 NT tokens and every KW-th 32 elements
-// of d_in, the next U of them on their way while it multiplies; KW warps' sums
-// meet in shared memory, in a fixed order.  It runs beside the first units of the
-// projection, whose CTAs need the other half of the registers, and is bound by the
-// latency of its loads.
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Eight E4M3 bytes times 2^(byte - 127) as four bf16 pairs (exact where bf16 reaches).
-__device__ __forceinline__ uint4 widen8(uint2 w, uint32_t byte) {
-  const float f = scale_of_byte(byte);
-  uint32_t o[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 v = widen2(((k < 2 ? w.x : w.y) >> (16 * (k & 1))) & 0xffffu);
-    o[k] = pack_bf16x2(v.x * f, v.y * f);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
-__global__ void __launch_bounds__(32 * TW * KW, kOneByte ? 3 : 2) proj_low_kernel(const __grid_constant__ ProjArgs a, int split) {
-  __shared__ uint32_t bits[kWords];
-  __shared__ int s_slot, s_slots;
-  __shared__ float red[KW / 2 * TW][MR * NT * 4][32];
-  grid_dep_launch();                 // the projection may be launched; its adapters' units wait for this grid
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kTokens = 8 * NT * TW;
-  const int part = blockIdx.x % split;         // of d_in: the blocks of a cluster
-  const int b = blockIdx.z, i0 = blockIdx.x / split * kTokens, n = live_rows(a.n_live, b, a.N);
-  if (i0 >= n) return;
-  const int id = proj_adapter(a, b);
-  if (id == -2) return;
-  const int g = (int)divide(b, a.by_requests), hr = half_rows_of(a, n);
-  if (a.requests == 1) {
-    if (id < 0) return;
-    if (threadIdx.x == 0) s_slot = 0, s_slots = 1;
-  } else if (warp == 0) {
-    bool live;
-    const int slots = group_bitmap(a, g, bits, &live);
-    int below = 0;
-    for (int w = lane; w < kWords && 32 * w <= id; w += 32)
-      below += __popc(w == id >> 5 ? bits[w] & ((1u << (id & 31)) - 1u) : bits[w]);
-    below = warp_sum(below);
-    if (lane == 0) s_slot = below, s_slots = slots;
-  }
-  __syncthreads();
-  const int first = s_slot * a.chunks, chunks = s_slots * a.chunks, rows = min(kTokens, n - i0);
-  auto place = [&](int i, int c, int p, int h) {
-    int flip;
-    char* at = part_row(a, b, i, hr, c, p, &flip);
-    return at + ((h ^ flip) << 4);
-  };
-  if (blockIdx.y == 0 && part == 0 && a.requests > 1) {   // the other adapters' chunks
-    const int others = chunks - (id < 0 ? 0 : a.chunks);
-    for (int e = threadIdx.x; e < rows * others * 4; e += 32 * TW * KW) {
-      const int i = e / (others * 4), r = e - i * (others * 4), c = r >> 2;
-      *reinterpret_cast<uint4*>(place(i0 + i, id >= 0 && c >= first ? c + a.chunks : c, (r >> 1) & 1, r & 1)) =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-  if (id < 0) return;
-
-  const int tw = warp % TW, kw = warp / TW, q = lane & 3, gr = lane >> 2;
-  const int rank0 = blockIdx.y * 16 * MR, t0 = i0 + tw * 8 * NT;
-  const bool busy = t0 < n;
-  float acc[MR][NT][4] = {};
-  if (busy) {
-    const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(a.A) + ((long long)id * a.R + rank0 + gr) * a.K + 8 * q;
-    const char* x = static_cast<const char*>(a.x) + (b * a.xs[0] + (t0 + gr) * a.xs[1] + 8 * q) * (kOneByte ? 1 : 2);
-    const uint8_t* xe = a.x_scale + ((long long)b * a.N + t0 + gr) * (a.K / KDTV_GROUP);
-    const long long xrow = 8 * a.xs[1] * (kOneByte ? 1 : 2);
-    struct Step {
-      uint4 a[U][MR][2];
-      typename std::conditional<kOneByte, uint2, uint4>::type x[U][NT];
-      uint32_t e[U][NT];
-    };
-    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-    auto load = [&](Step& s, int k0) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * KW * 32;
-        const bool in = k + 8 * q < a.K;
-#pragma unroll
-        for (int m = 0; m < MR; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            s.a[u][m][h] = in && rank0 + 16 * m + 8 * h + gr < a.R
-                               ? *reinterpret_cast<const uint4*>(A + (long long)(16 * m + 8 * h) * a.K + k) : none;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const bool on = in && t0 + 8 * j + gr < n;
-          if constexpr (kOneByte) {
-            s.x[u][j] = on ? *reinterpret_cast<const uint2*>(x + j * xrow + k) : make_uint2(0u, 0u);
-            s.e[u][j] = on ? xe[(long long)8 * j * (a.K / KDTV_GROUP) + k / KDTV_GROUP] : 127u;
-          } else {
-            s.x[u][j] = on ? *reinterpret_cast<const uint4*>(x + j * xrow + 2 * k) : none;
-          }
-        }
-      }
-    };
-    auto multiply = [&](const Step& s) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint4 v;
-          if constexpr (kOneByte) v = widen8(s.x[u][j], s.e[u][j]);
-          else v = s.x[u][j];
-#pragma unroll
-          for (int m = 0; m < MR; ++m) {
-            mma_16x8x16(acc[m][j], s.a[u][m][0].x, s.a[u][m][1].x, s.a[u][m][0].y, s.a[u][m][1].y, v.x, v.y);
-            mma_16x8x16(acc[m][j], s.a[u][m][0].z, s.a[u][m][1].z, s.a[u][m][0].w, s.a[u][m][1].w, v.z, v.w);
-          }
-        }
-    };
-    const int stride = split * KW * 32 * U, start = part * KW * 32 * U + kw * 32;
-    Step s0, s1;
-    load(s0, start);
-#pragma unroll 1
-    for (int k0 = start; k0 < a.K; k0 += 2 * stride) {          // (loads behind d_in are zeros)
-      load(s1, k0 + stride);
-      multiply(s0);
-      load(s0, k0 + 2 * stride);
-      multiply(s1);
-    }
-  }
-#pragma unroll
-  for (int half = KW / 2; half > 0; half /= 2) {        // the upper half's sums to the lower half
-    if (kw >= half && kw < 2 * half)
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) red[(kw - half) * TW + tw][(m * NT + j) * 4 + k][lane] = acc[m][j][k];
-    __syncthreads();
-    if (kw < half)
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[m][j][k] += red[kw * TW + tw][(m * NT + j) * 4 + k][lane];
-    __syncthreads();
-  }
-  if (split > 1) {                                       // the blocks' sums to the first, in their order
-    if (kw == 0 && part > 0)
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) red[tw][(m * NT + j) * 4 + k][lane] = acc[m][j][k];
-    cluster_sync();
-    if (kw == 0 && part == 0)
-      for (int c = 1; c < split; ++c)
-#pragma unroll
-        for (int m = 0; m < MR; ++m)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float v;
-              asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                           : "=f"(v) : "r"(mapa(smem_u32(&red[tw][(m * NT + j) * 4 + k][lane]), c)) : "memory");
-              acc[m][j][k] += v;
-            }
-    cluster_sync();                                      // (the others' memory is read)
-  }
-  if (kw > 0 || part > 0 || !busy) return;
-  const float s = a.adapter_scale ? a.adapter_scale[id] : 1.f;
-#pragma unroll
-  for (int m = 0; m < MR; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v = s * acc[m][j][k];
-        const int rank = rank0 + 16 * m + gr + (k >> 1) * 8, i = t0 + 8 * j + 2 * q + (k & 1), c = rank >> 4;
-        if (i >= n || c >= a.chunks) continue;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        const float left = v - __bfloat162float(hi);       // exact; not a number where v is not finite
-        const int h = (rank >> 3) & 1, at = (rank & 7) * 2;
-        *reinterpret_cast<__nv_bfloat16*>(place(i, first + c, 0, h) + at) = hi;
-        *reinterpret_cast<__nv_bfloat16*>(place(i, first + c, 1, h) + at) =
-            __float2bfloat16_rn(fabsf(left) < INFINITY ? left : 0.f);
-      }
-}
 
 // ---- the projection --------------------------------------------------------------------------
 enum {
@@ -775,7 +503,6 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     const int q = warp - kWarpOut, t = threadIdx.x - 32 * kWarpOut;
     auto meet = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
     auto agree = [&](bool ok) { return all_of(1, ok); };
-    grid_dep_wait();                           // (no CTA ends before the first kernel)
     if (blockIdx.x == 0) leave_plan(a, sh, t);
     for (int n = 0; next(a, sh, w, it); ++n) {
       meet();                                  // the last tile's columns are read
@@ -893,6 +620,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       }
       released(B_ACC_EMPTY);
     }
+    grid_dep_wait();                           // no CTA ends before the first kernel
   } else if (kOneByte && warp >= kWarpScale) {
     // ---- exponent bytes: a thread has a row of W and up to two tokens, four units' bytes at a time ------
     const int t = threadIdx.x - 32 * kWarpScale, row_bytes = a.K / KDTV_GROUP;
@@ -982,63 +710,75 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 }
 
 // ---- outputs of cut tiles ---------------------------------------------------------------------
-// A block has 128 outputs and kCombineCols tokens of a tile; a thread one output and half of those
-// tokens, all segments' sums of four at a time under way together.  Latency
-// bound.  (The last pair to come adding them up by itself, with four warps, took 32
-// us of 53 for 64 tokens.)
-constexpr int kCombineCols = 16;
+// A warp has kCombineCols tokens of a tile and 128 outputs, four of a token a lane; the sums of kAtOnce segments
+// of all of them are under way together.  Latency bound: the plan, the tile's record, then everything else at once.
+// (The last pair to come adding the sums up by itself, with four warps, took 32 us of 53 for 64 tokens; blocks
+// of 128 outputs and 16 tokens each, those of tiles that are not there among them, 14 us of 61 for 64 drafts of 8.)
+constexpr int kCombineCols = 2, kAtOnce = 4, kCombineWarps = 8;
 
 template <bool kOneByte>
-__global__ void __launch_bounds__(256) proj_combine_kernel(const __grid_constant__ ProjArgs a) {
-  __shared__ long long y_at[kCombineCols];
+__global__ void __launch_bounds__(32 * kCombineWarps) proj_combine_kernel(const __grid_constant__ ProjArgs a) {
   grid_dep_wait();
   // (a wait that ran out: some sums were never written)
   if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
-  const int cut = a.plan[0];
-  const CutTile it = reinterpret_cast<const CutTile*>(a.plan + 4)[blockIdx.x];   // (there is room for it, if not a tile)
-  if ((int)blockIdx.x >= cut) return;
-  const int c0 = blockIdx.z * kCombineCols, rank = blockIdx.y, cols = 2 * half_cols_of(a, it.hr);
-  if (it.segs < 2 || c0 >= cols) return;
-  if (threadIdx.x < kCombineCols) {
-    int b, i;
-    long long at = -1;
-    if (column(a, it.g, it.j, it.hr, c0 + threadIdx.x, &b, &i) && i < live_rows(a.n_live, b, a.N)) {
-      const int id = a.adapter ? a.adapter[b] : -1;
-      if (id >= -1 && id < a.adapters) at = b * a.ys[0] + i * a.ys[1];
+  const int lane = threadIdx.x & 31, per_tile = 2 * (2 * a.half_cols / kCombineCols), items = a.plan[0] * per_tile;
+  for (int item = blockIdx.x * kCombineWarps + (threadIdx.x >> 5); item < items; item += gridDim.x * kCombineWarps) {
+    const int tile = item / per_tile, r = item - tile * per_tile, rank = r & 1, c0 = (r >> 1) * kCombineCols;
+    const CutTile it = reinterpret_cast<const CutTile*>(a.plan + 4)[tile];
+    if (it.segs < 2 || c0 >= 2 * half_cols_of(a, it.hr)) continue;
+    long long at[kCombineCols];
+    int b[kCombineCols], i[kCombineCols];
+    bool any = false;
+#pragma unroll
+    for (int c = 0; c < kCombineCols; ++c) {
+      at[c] = -1;
+      if (column(a, it.g, it.j, it.hr, c0 + c, &b[c], &i[c]) && i[c] < live_rows(a.n_live, b[c], a.N)) {
+        const int id = a.adapter ? a.adapter[b[c]] : -1;
+        if (id >= -1 && id < a.adapters) at[c] = b[c] * a.ys[0] + i[c] * a.ys[1];
+      }
+      any |= at[c] >= 0;
     }
-    y_at[threadIdx.x] = at;
-  }
-  constexpr int kCols = kCombineCols / 2, kAtOnce = 4;
-  const int lane = threadIdx.x & 127, half = (threadIdx.x >> 7) * kCols, f = (2 * it.f + rank) * kFeatures + lane;
-  float sum[kCols] = {};
+    if (!any) continue;
+    float4 sum[kCombineCols] = {};
 #pragma unroll 1
-  for (int s0 = 0; s0 < it.segs; s0 += kAtOnce) {
-    float v[kAtOnce][kCols];
+    for (int s0 = 0; s0 < it.segs; s0 += kAtOnce) {
+      float4 v[kAtOnce][kCombineCols];
 #pragma unroll
-    for (int s = 0; s < kAtOnce; ++s) {
-      const float* part = partial_of(a, it.first + s0 + s, s0 + s, rank) + (c0 + half) * kFeatures + lane;
+      for (int s = 0; s < kAtOnce; ++s) {
+        const float* part = partial_of(a, it.first + s0 + s, s0 + s, rank) + c0 * kFeatures + 4 * lane;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) v[s][c] = s0 + s < it.segs ? part[c * kFeatures] : 0.f;
+        for (int c = 0; c < kCombineCols; ++c)
+          v[s][c] = s0 + s < it.segs ? *reinterpret_cast<const float4*>(part + c * kFeatures) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int s = 0; s < kAtOnce; ++s)
+#pragma unroll
+        for (int c = 0; c < kCombineCols; ++c) {
+          sum[c].x += v[s][c].x;
+          sum[c].y += v[s][c].y;
+          sum[c].z += v[s][c].z;
+          sum[c].w += v[s][c].w;
+        }
     }
+    const bool mixed = a.requests > 1 && it.chunks > 0;
+    const int f = (2 * it.f + rank) * kFeatures + 4 * lane;
 #pragma unroll
-    for (int s = 0; s < kAtOnce; ++s)
+    for (int c = 0; c < kCombineCols; ++c) {
+      if (at[c] < 0 || f >= a.M) continue;
+      float v[4] = {sum[c].x, sum[c].y, sum[c].z, sum[c].w};
+      if (mixed)
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) sum[c] += v[s][c];
-  }
-  __syncthreads();
-  if (f >= a.M) return;
-  const bool mixed = a.requests > 1 && it.chunks > 0;
+        for (int k = 0; k < 4; ++k)
+          if (!(fabsf(v[k]) < INFINITY) && f + k < a.M) v[k] = alone<kOneByte>(a, b[c], i[c], f + k);
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + at[c] + f;
+      if (a.wide) {
+        *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      } else {
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    const long long at = y_at[half + c];
-    if (at < 0) continue;
-    float v = sum[c];
-    if (mixed && !(fabsf(v) < INFINITY)) {
-      int b, i;
-      column(a, it.g, it.j, it.hr, c0 + half + c, &b, &i);
-      v = alone<kOneByte>(a, b, i, f);
+        for (int k = 0; k < 4; ++k)
+          if (f + k < a.M) y[k] = __float2bfloat16_rn(v[k]);
+      }
     }
-    static_cast<__nv_bfloat16*>(a.y)[at + f] = __float2bfloat16_rn(v);
   }
 }
 
@@ -1047,34 +787,6 @@ int launch_groups(const ProjArgs& a) { return a.groups < kMaxGroups ? a.groups :
 int pairs_of(int sms) { return sms / 2 < 1 ? 1 : sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs; }
 
 size_t plan_bytes(int sms) { return align256(16 + (size_t)pairs_of(sms) * sizeof(CutTile)); }
-
-// An SM divides its memory between L1 and shared memory once for all blocks that it holds: what is to run
-// beside the projection asks for the division that the projection needs.
-template <typename... KArgs>
-cudaError_t beside(void (*kernel)(KArgs...)) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-}
-
-template <bool kOneByte, int MR, int NT, int TW, int KW, int U>
-cudaError_t launch_low(const ProjArgs& a, int sms, cudaStream_t st) {
-  const int tokens = 8 * NT * TW;
-  const cudaError_t err = beside(proj_low_kernel<kOneByte, MR, NT, TW, KW, U>);
-  if (err != cudaSuccess) return err;
-  const int blocks = (a.N + tokens - 1) / tokens, ranks = (a.R + 16 * MR - 1) / (16 * MR);
-  // d_in over as many blocks as leave about one block an SM, 512 elements each at least.
-  int split = 1;
-  while (split < 8 && (long long)blocks * ranks * a.B * split * 2 <= sms && a.K / (2 * split) >= 512) split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks * split), (unsigned)ranks, (unsigned)a.B);
-  cfg.blockDim = dim3(32 * TW * KW);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)split, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, proj_low_kernel<kOneByte, MR, NT, TW, KW, U>, a, split);
-}
 
 template <bool kOneByte>
 int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
@@ -1104,14 +816,7 @@ int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
     const uint32_t vbox[2] = {128, (uint32_t)a.half_cols / 2};
     if (encode_nd(&tv, a.parts, 2, vdims, vstrides, vbox, 2, 0) != CUDA_SUCCESS) return KDTV_ERR_CUDA;
   }
-  // Few rows of a request: blocks of 16 ranks, 8 ways along d_in; many: 64 rows of up to 32 ranks, 4 ways.
-  cudaError_t err = cudaSuccess;
-  if (a.adapter) {
-    if (a.N <= 8) err = launch_low<kOneByte, 1, 1, 1, 8, 2>(a, sms, st);
-    else if (a.R <= 16) err = launch_low<kOneByte, 1, kOneByte ? 2 : 4, 2, 4, 1>(a, sms, st);
-    else err = launch_low<kOneByte, 2, kOneByte ? 2 : 4, 2, 4, 1>(a, sms, st);
-  }
-  if (err != cudaSuccess) return KDTV_ERR_CUDA;
+  if (a.adapter && launch_proj_low(a, sms, st) != cudaSuccess) return KDTV_ERR_CUDA;
   const size_t smem = (size_t)a.stages * (kWBytes + a.half_cols * kUnitBytes) +
                       (kOneByte ? 2 * kWindow * kScaleBytes : 0) + sizeof(ProjShared);
   const auto kern = proj_tc_kernel<kOneByte>;
@@ -1131,10 +836,12 @@ int launch_t(const ProjArgs& a, int sms, bool stall, cudaStream_t st) {
   if (cudaLaunchKernelEx(&cfg, kern, tw, tx, tb, tv, a, stall ? 1 : 0) != cudaSuccess) return KDTV_ERR_CUDA;
   if (!may_cut(a)) return KDTV_OK;
   const long long tiles = (long long)a.groups * a.blocks * a.features, most = pairs_of(sms) - 1;
-  if (most == 0) return KDTV_OK;
-  const dim3 grid((unsigned)(tiles < most ? tiles : most), 2, (unsigned)((2 * a.half_cols + kCombineCols - 1) / kCombineCols));
+  const long long items = (tiles < most ? tiles : most) * 2 * (2 * a.half_cols / kCombineCols);
+  if (items == 0) return KDTV_OK;
   if (beside(proj_combine_kernel<kOneByte>) != cudaSuccess) return KDTV_ERR_CUDA;
-  return launch_ex(proj_combine_kernel<kOneByte>, grid, dim3(256), 0, st, true, a) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+  const long long blocks = (items + kCombineWarps - 1) / kCombineWarps;
+  return launch_ex(proj_combine_kernel<kOneByte>, dim3((unsigned)(blocks < 4ll * sms ? blocks : 4ll * sms)), dim3(32 * kCombineWarps), 0,
+                   st, true, a) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
 }
 
 }  // namespace
@@ -1165,8 +872,8 @@ bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a) {
   a->pairs = ((a->requests < d->adapters ? a->requests : d->adapters) * a->chunks + 1) / 2;
   a->features = (d->d_out + 2 * kFeatures - 1) / (2 * kFeatures);
   if ((long long)a->groups * a->blocks * a->features > 0x3fffffffll) return false;
-  // As many stages as leave room for the first kernel's blocks beside this one's (17 KiB, and 1 KiB each).
-  a->stages = (int)((228 * 1024 - 20 * 1024 - sizeof(ProjShared) - (one_byte ? 2 * kWindow * kScaleBytes : 0)) /
+  // As many stages as leave room for a block of the first kernel beside this one's (4 KiB; and 1 KiB each).
+  a->stages = (int)((228 * 1024 - 7 * 1024 - sizeof(ProjShared) - (one_byte ? 2 * kWindow * kScaleBytes : 0)) /
                     (kWBytes + a->half_cols * kUnitBytes));
   a->shared = one_byte && a->half_cols > kTokens / 4 ? kShared : 0;
   if (a->shared && a->stages > kShared / kScaleColumns) a->stages = kShared / kScaleColumns;
