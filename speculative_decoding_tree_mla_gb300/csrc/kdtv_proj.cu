@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(kThreads) proj_low_simt_kernel(const __grid_co
   const int b = blockIdx.y, i0 = blockIdx.x * 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = live_rows(a.n_live, b, a.N);
   if (i0 >= n) return;
-  const int id = proj_adapter(a, b);
+  const int id = proj_adapter(a, a.adapter[b]);
   if (id < 0) return;
   const float s = a.adapter_scale ? a.adapter_scale[id] : 1.f;
   const X* x = static_cast<const X*>(a.x) + b * a.xs[0] + i0 * a.xs[1];
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
     if (r < rows) {
       const int b = (int)divide((unsigned)r, a.by_N), i = (int)(r - (long long)b * a.N);
       if (i < live_rows(a.n_live, b, a.N)) {
-        id = proj_adapter(a, b);
+        id = proj_adapter(a, a.adapter ? a.adapter[b] : -1);
         if (id != -2) {
           ox = b * a.xs[0] + i * a.xs[1];
           oy = b * a.ys[0] + i * a.ys[1];

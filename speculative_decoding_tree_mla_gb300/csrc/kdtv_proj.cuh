@@ -39,10 +39,8 @@ struct ProjArgs {
 
 __device__ __forceinline__ void proj_error(const ProjArgs& a, unsigned int code) { atomicCAS(a.status, 0u, code); }
 
-// Adapter of request b: -1 for none, -2 (and an error recorded) for an index out of range.
-__device__ __forceinline__ int proj_adapter(const ProjArgs& a, int b) {
-  if (!a.adapter) return -1;
-  const int id = a.adapter[b];
+// A request's adapter from its index: -1 for none, -2 (and an error recorded) for one out of range.
+__device__ __forceinline__ int proj_adapter(const ProjArgs& a, int id) {
   if (id >= -1 && id < a.adapters) return id;
   proj_error(a, KDTV_ERR_BAD_ADAPTER);
   return -2;

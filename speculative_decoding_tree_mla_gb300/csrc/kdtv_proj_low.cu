@@ -58,8 +58,9 @@ __device__ __forceinline__ bool low_request(const ProjArgs& a, int b, int i0, Lo
   __shared__ int s_slot, s_slots;
   w.b = b;
   w.n = live_rows(a.n_live, b, a.N);
+  const int raw = a.adapter[b];                            // (both loads under way)
   if (i0 >= w.n) return false;
-  w.id = proj_adapter(a, b);
+  w.id = proj_adapter(a, raw);
   if (w.id == -2 || (w.id < 0 && a.requests == 1)) return false;
   w.hr = half_rows_of(a, w.n);
   if (a.requests == 1) {

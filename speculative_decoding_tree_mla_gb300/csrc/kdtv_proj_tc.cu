@@ -291,10 +291,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   }
   if (threadIdx.x == 0) sh.abort = 0u;
   fence_mbar_init();
-  if (warp == kWarpMma) {
-    tmem_alloc_pair(smem_u32(&sh.tmem), 512);
-    tmem_relinquish_pair();
-  }
+  __syncthreads();
+  cluster_arrive();                            // this CTA's barriers are set up
   if (warp == kWarpTma && lane == 0) {
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_x);
@@ -305,7 +303,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   }
   if (a.requests == 1) {
     for (int g = threadIdx.x; g < a.groups; g += threads_of(kOneByte)) {
-      const int n = live_rows(a.n_live, g, a.N), id = n > 0 ? proj_adapter(a, g) : -1;
+      const int n = live_rows(a.n_live, g, a.N), raw = a.adapter ? a.adapter[g] : -1;   // (both loads under way)
+      const int id = n > 0 ? proj_adapter(a, raw) : -1;
       const int hr = half_rows_of(a, n);
       sh.first[g] = id == -2 ? 0 : (n + 2 * hr - 1) / (2 * hr);
       sh.tile[g] = (id >= 0 ? (uint32_t)a.chunks : 0u) | ((uint32_t)hr << 20);
@@ -323,9 +322,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     }
     fence_async_smem();
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   if (warp == 0) {
     int sum = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 32) {
@@ -341,11 +338,18 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     }
     if (lane == 0) sh.first[a.groups] = sum;
     __syncwarp();
-    // Whole rounds of whole tiles, and what is left cut into equal shares.  Tiles of few units are not cut, nor
-    // are almost full rounds.
+    // Whole rounds of whole tiles, and what is left cut into equal shares, where that is sooner done than whole
+    // tiles that leave pairs idle.
     const int tiles = sum * a.features, pairs = gridDim.x >> 1;
     int cut = tiles % pairs;
-    if (!may_cut(a) || cut * 20 > pairs * 19) cut = 0;
+    // (In ns, as measured: a unit takes 300, joining cut tiles 4000 and what reading their sums takes at 3500 GB/s.)
+    if (may_cut(a) && cut > 0) {
+      const long long idle = (long long)(pairs - cut) * 300 * a.base / pairs;
+      const long long join = 4000 + (long long)(pairs + cut) * 2 * a.half_cols * (2 * kFeatures * 4) / 3500;
+      if (idle < join) cut = 0;
+    } else {
+      cut = 0;
+    }
     Item it;
     int u = 0;
     for (int t0 = 0; t0 < cut; t0 += 32) {
@@ -371,8 +375,19 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     }
   }
   __syncthreads();
-  cluster_sync();                              // the pair's barriers are set up
-  const uint32_t tmem = sh.tmem;
+  cluster_wait();                              // the pair's barriers are set up
+  // TMEM, for all but the producer, which is at work meanwhile.
+  uint32_t tmem = 0u;
+  if (warp != kWarpTma) {
+    if (warp == kWarpMma) {
+      tmem_alloc_pair(smem_u32(&sh.tmem), 512);
+      tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 3, %0;" :: "n"(threads_of(kOneByte) - 32) : "memory");
+    tc_fence_after();
+    tmem = sh.tmem;
+  }
   const uint32_t lead = mapa(bars, 0);         // the first CTA's barriers: it issues the products
   auto LEAD = [&](int i) { return lead + 8u * i; };
   Walk w = walk(sh);
@@ -718,25 +733,26 @@ constexpr int kCombineCols = 2, kAtOnce = 4, kCombineWarps = 8;
 
 template <bool kOneByte>
 __global__ void __launch_bounds__(32 * kCombineWarps) proj_combine_kernel(const __grid_constant__ ProjArgs a) {
+  const int lane = threadIdx.x & 31, per_tile = 2 * (2 * a.half_cols / kCombineCols);
   grid_dep_wait();
+  const unsigned int status = *reinterpret_cast<volatile unsigned int*>(a.status);
+  const int items = a.plan[0] * per_tile;
   // (a wait that ran out: some sums were never written)
-  if (*reinterpret_cast<volatile unsigned int*>(a.status) == KDTV_ERR_DEVICE_TIMEOUT) return;
-  const int lane = threadIdx.x & 31, per_tile = 2 * (2 * a.half_cols / kCombineCols), items = a.plan[0] * per_tile;
+  if (status == KDTV_ERR_DEVICE_TIMEOUT) return;
   for (int item = blockIdx.x * kCombineWarps + (threadIdx.x >> 5); item < items; item += gridDim.x * kCombineWarps) {
     const int tile = item / per_tile, r = item - tile * per_tile, rank = r & 1, c0 = (r >> 1) * kCombineCols;
     const CutTile it = reinterpret_cast<const CutTile*>(a.plan + 4)[tile];
     if (it.segs < 2 || c0 >= 2 * half_cols_of(a, it.hr)) continue;
-    long long at[kCombineCols];
+    long long at[kCombineCols];                // offset of each token's output row, -1: none
     int b[kCombineCols], i[kCombineCols];
     bool any = false;
 #pragma unroll
     for (int c = 0; c < kCombineCols; ++c) {
       at[c] = -1;
-      if (column(a, it.g, it.j, it.hr, c0 + c, &b[c], &i[c]) && i[c] < live_rows(a.n_live, b[c], a.N)) {
-        const int id = a.adapter ? a.adapter[b[c]] : -1;
-        if (id >= -1 && id < a.adapters) at[c] = b[c] * a.ys[0] + i[c] * a.ys[1];
-      }
-      any |= at[c] >= 0;
+      if (!column(a, it.g, it.j, it.hr, c0 + c, &b[c], &i[c])) continue;
+      any = true;
+      const int n = live_rows(a.n_live, b[c], a.N), id = a.adapter ? a.adapter[b[c]] : -1;
+      if (i[c] < n && id >= -1 && id < a.adapters) at[c] = b[c] * a.ys[0] + i[c] * a.ys[1];
     }
     if (!any) continue;
     float4 sum[kCombineCols] = {};

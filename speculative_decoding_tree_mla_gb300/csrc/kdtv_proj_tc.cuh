@@ -21,8 +21,9 @@ __device__ __forceinline__ int group_bitmap(const ProjArgs& a, int g, uint32_t* 
   __syncwarp();
   bool any = false;
   for (int b = g * a.requests + lane; b < min(a.B, (g + 1) * a.requests); b += 32) {
-    if (live_rows(a.n_live, b, a.N) <= 0) continue;
-    const int id = proj_adapter(a, b);
+    const int n = live_rows(a.n_live, b, a.N), raw = a.adapter ? a.adapter[b] : -1;   // (both loads under way)
+    if (n <= 0) continue;
+    const int id = proj_adapter(a, raw);
     any |= id != -2;
     if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
   }
