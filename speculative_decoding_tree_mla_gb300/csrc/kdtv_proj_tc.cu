@@ -81,6 +81,8 @@ __device__ __forceinline__ uint32_t scale_at(const ProjArgs& a, int slot) {
   return a.shared ? 2 * kTokens - kShared + slot * kScaleColumns : (slot & 1) * kTokens + kTokens / 2 + (slot >> 1) * kScaleColumns;
 }
 
+constexpr int kRowPitch = 80;               // 64 bytes, set apart so that eight rows' 16 bytes lie in different banks
+
 // Shared memory behind the ring.
 struct ProjShared {
   uint64_t bars[B_COUNT];
@@ -92,7 +94,7 @@ struct ProjShared {
   long long y_at[256];                      // offset of each column's output row, -1: none
   uint32_t bits[kWords];
   uint16_t ids[256];                        // the adapters of the producer's tile
-  __align__(16) unsigned char rows[4][16 * 64];   // an output warp's 32 outputs of 16 tokens
+  __align__(16) unsigned char rows[4][16 * kRowPitch];   // an output warp's 32 outputs of 16 tokens
 };
 
 // A part of a tile: units k0 .. k1 - 1; behind a.base of d_in come pairs of chunks.
@@ -229,20 +231,35 @@ __device__ __forceinline__ bool all_of(int id, bool ok) {
 // One output by itself, for a value that is not finite where several adapters share a tile.
 template <bool kOneByte>
 __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
+  constexpr int E = kOneByte ? 1 : 2;
+  const char* x = static_cast<const char*>(a.x) + (b * a.xs[0] + i * a.xs[1]) * E;
+  const char* w = static_cast<const char*>(a.W) + (long long)f * a.K * E;
   float sum = 0.f;
-  for (int k = 0; k < a.K; ++k) {
-    float x, w;
+#pragma unroll 4
+  for (int k = 0; k < a.K; k += 8) {         // (d_in is a multiple of 8, and rows are 16-byte aligned)
+    float u[8], v[8], scale = 1.f;
     if constexpr (kOneByte) {
       const int groups = a.K / KDTV_GROUP;
-      x = to_f32(static_cast<const __nv_fp8_e4m3*>(a.x)[b * a.xs[0] + i * a.xs[1] + k]) *
-          scale_of_byte(a.x_scale[((long long)b * a.N + i) * groups + k / KDTV_GROUP]);
-      w = to_f32(static_cast<const __nv_fp8_e4m3*>(a.W)[(long long)f * a.K + k]) *
-          scale_of_byte(a.W_scale[(long long)f * groups + k / KDTV_GROUP]);
+      const uint2 p = *reinterpret_cast<const uint2*>(x + k), q = *reinterpret_cast<const uint2*>(w + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = widen2(((e < 2 ? p.x : p.y) >> (16 * (e & 1))) & 0xffffu);
+        const float2 z = widen2(((e < 2 ? q.x : q.y) >> (16 * (e & 1))) & 0xffffu);
+        u[2 * e] = y.x;
+        u[2 * e + 1] = y.y;
+        v[2 * e] = z.x;
+        v[2 * e + 1] = z.y;
+      }
+      scale = scale_of_byte(a.x_scale[((long long)b * a.N + i) * groups + k / KDTV_GROUP]);
+      const float scale_w = scale_of_byte(a.W_scale[(long long)f * groups + k / KDTV_GROUP]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= scale_w;
     } else {
-      x = to_f32(static_cast<const __nv_bfloat16*>(a.x)[b * a.xs[0] + i * a.xs[1] + k]);
-      w = to_f32(static_cast<const __nv_bfloat16*>(a.W)[(long long)f * a.K + k]);
+      load_v<8>(reinterpret_cast<const __nv_bfloat16*>(x) + k, u);
+      load_v<8>(reinterpret_cast<const __nv_bfloat16*>(w) + k, v);
     }
-    sum = fmaf(x, w, sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(u[e] * scale, v[e], sum);
   }
   const int id = a.adapter[b];
   if (id < 0) return sum;
@@ -534,104 +551,109 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       if (!agree(wait_warp(guard, BAR(B_ACC_FULL + (n & 1)), (n >> 1) & 1))) break;
       tc_fence_after();
       const uint32_t acc = tmem + acc_at(a, n) + ((uint32_t)(32 * q) << 16);
-      const int f = (2 * it.f + rank) * kFeatures + 32 * q + lane;
+      const int f0 = (2 * it.f + rank) * kFeatures + 32 * q;
       const bool mixed = a.requests > 1 && it.chunks > 0;
-      auto put = [&](int c, float v) {
-        const long long at = sh.y_at[c];
-        if (at < 0 || f >= a.M) return;
-        if (mixed && !(fabsf(v) < INFINITY)) {
-          int b, i;
-          column(a, it.g, it.j, it.hr, c, &b, &i);
-          v = alone<kOneByte>(a, b, i, f);
-        }
-        static_cast<__nv_bfloat16*>(a.y)[at + f] = __float2bfloat16_rn(v);
-      };
       auto released = [&](int bar) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(LEAD(bar + (n & 1)));
       };
-      float* mine = it.cut < 0 ? nullptr : partial_of(a, (int)(blockIdx.x >> 1), it.seg, rank) + 32 * q + lane;
-      // 16 columns as bf16 pairs, through shared memory, so that a lane writes 8 outputs of a token at once
-      auto write = [&](int c0, const uint32_t (&p)[8]) {
-        uint16_t* rows = reinterpret_cast<uint16_t*>(sh.rows[q]);
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) rows[c * 32 + lane] = (uint16_t)(p[c >> 1] >> (16 * (c & 1)));
-        __syncwarp();
-        const int f8 = f - lane + (lane & 3) * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = h * 8 + (lane >> 2);
-          const long long to = sh.y_at[c0 + c];
-          const uint4 w8 = *reinterpret_cast<const uint4*>(rows + c * 32 + (lane & 3) * 8);
-          if (to >= 0 && f8 < a.M) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f8) = w8;
-        }
-      };
-      auto emit = [&](int c0, const float (&v)[16]) {
-        if (mine) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) mine[(c0 + c) * kFeatures] = v[c];
-          return;
-        }
-        bool odd = !a.wide;
-        if (mixed)
-#pragma unroll
-          for (int c = 0; c < 16; ++c) odd |= !(fabsf(v[c]) < INFINITY) && sh.y_at[c0 + c] >= 0;
-        if (__any_sync(0xffffffffu, odd)) {
+      // Columns that the next tile's accumulator has too come first, then the others.
+      const int first0 = (n & 1) ? 0 : min(cols, kTokens - a.shared), first1 = (n & 1) ? min(cols, a.shared) : cols;
+      const int rest0 = first0 == 0 ? first1 : 0, rest1 = first0 == 0 ? cols : first0;
+      if (it.cut >= 0) {                       // sums, for the combine kernel: an output a lane
+        float* mine = partial_of(a, (int)(blockIdx.x >> 1), it.seg, rank) + 32 * q + lane;
+        auto copy = [&](int c0, int c1) {
 #pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
-            float x = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x = c == k ? v[k] : x;
-            put(c0 + c, x);
-          }
-          __syncwarp();
-          return;
-        }
-        uint32_t p[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-        write(c0, p);
-      };
-      int skip0 = 0, skip1 = 0;                // columns that come first
-      if constexpr (kOneByte) {
-        skip0 = (n & 1) ? 0 : min(cols, kTokens - a.shared);
-        skip1 = (n & 1) ? min(cols, a.shared) : cols;
-        if (!mine && !mixed && a.wide) {       // read and rounded, then given back, then written
-          uint32_t p[kShared / 16][8];
-#pragma unroll
-          for (int k = 0; k < kShared / 16; ++k)
-            if (skip0 + 16 * k < skip1) {
-              float v[16];
-              tmem_ld16(acc + skip0 + 16 * k, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) p[k][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-            }
-          released(B_ACC_PART);
-#pragma unroll
-          for (int k = 0; k < kShared / 16; ++k)
-            if (skip0 + 16 * k < skip1) write(skip0 + 16 * k, p[k]);
-        } else {
-#pragma unroll 1
-          for (int c0 = skip0; c0 < skip1; c0 += 16) {
+          for (; c0 < c1; c0 += 16) {
             float v[16];
             __syncwarp();
             tmem_ld16(acc + c0, v);
             tmem_wait_ld();
-            emit(c0, v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) mine[(c0 + c) * kFeatures] = v[c];
           }
-          released(B_ACC_PART);
+        };
+        copy(first0, first1);
+        if (kOneByte) released(B_ACC_PART);
+        copy(rest0, rest1);
+        released(B_ACC_EMPTY);
+        continue;
+      }
+      // 16 columns as the products of 8 x 8 matrices hold them: value (k, h, j, e) is output f0 + 16 h + 8 j + lane /
+      // 4 of token c0 + 8 k + 2 (lane % 4) + e; p: pairs over e, rounded.  True if they were written one by one.
+      auto fetch = [&](int c0, uint32_t (&p)[2][4]) -> bool {
+        float v[2][8];                         // [h][4 k + 2 j + e]
+        __syncwarp();
+        tmem_ld_16x256b_x2(acc + c0, v[0]);
+        tmem_ld_16x256b_x2(acc + (16u << 16) + c0, v[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) p[k][m] = pack_bf16x2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
+        bool odd = !a.wide;
+        if (mixed) {
+          uint32_t top = 0u;                   // not finite?
+#pragma unroll
+          for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i >> 3][i & 7]) & 0x7fffffffu);
+          if (top >= 0x7f800000u)              // (in a column that is in use?)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              odd |= !(fabsf(v[i >> 3][i & 7]) < INFINITY) && sh.y_at[c0 + 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1)] >= 0;
         }
+        if (!__any_sync(0xffffffffu, odd)) return false;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+          float x = 0.f;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x = i == k ? v[k >> 3][k & 7] : x;
+          const int c = c0 + 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1), f = f0 + 16 * (i >> 3) + 8 * ((i >> 1) & 1) + (lane >> 2);
+          const long long to = sh.y_at[c];
+          if (to < 0 || f >= a.M) continue;
+          if (mixed && !(fabsf(x) < INFINITY)) {
+            int b, i;
+            column(a, it.g, it.j, it.hr, c, &b, &i);
+            x = alone<kOneByte>(a, b, i, f);
+          }
+          static_cast<__nv_bfloat16*>(a.y)[to + f] = __float2bfloat16_rn(x);
+        }
+        return true;
+      };
+      // To shared memory, transposed, and from there 8 outputs of a token a lane.
+      const uint32_t rows = smem_u32(sh.rows[q]);
+      auto write = [&](int c0, const uint32_t (&p)[2][4]) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          stmatrix_x4_trans(rows + (8 * k + (lane & 7)) * kRowPitch + (lane >> 3) * 16, p[k][0], p[k][1], p[k][2], p[k][3]);
+        __syncwarp();
+        const int f = f0 + (lane & 3) * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = h * 8 + (lane >> 2);
+          const long long to = sh.y_at[c0 + c];
+          const uint4 v = lds128(rows + c * kRowPitch + (lane & 3) * 16);
+          if (to >= 0 && f < a.M) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f) = v;
+        }
+      };
+      if constexpr (kOneByte) {                // read and rounded, then given back, then written
+        uint32_t p[kShared / 16][2][4];
+        bool done[kShared / 16];
+#pragma unroll
+        for (int k = 0; k < kShared / 16; ++k) {
+          done[k] = true;
+          if (first0 + 16 * k < first1) done[k] = fetch(first0 + 16 * k, p[k]);
+        }
+        released(B_ACC_PART);
+#pragma unroll
+        for (int k = 0; k < kShared / 16; ++k)
+          if (!done[k]) write(first0 + 16 * k, p[k]);
       }
 #pragma unroll 1
-      for (int c0 = skip0 == 0 ? skip1 : 0, end = skip0 == 0 ? cols : skip0; c0 < end; c0 += 16) {
-        float v[16];
-        __syncwarp();
-        tmem_ld16(acc + c0, v);
-        tmem_wait_ld();
-        emit(c0, v);
+      for (int c0 = rest0; c0 < rest1; c0 += 16) {
+        uint32_t p[2][4];
+        if (!fetch(c0, p)) write(c0, p);
       }
       released(B_ACC_EMPTY);
     }
