@@ -91,9 +91,9 @@ __device__ __forceinline__ int64_t slot_of(const PageArgs& a, int L, int n, int 
 // their lengths are in L2), so that the CTAs share nothing but two barriers:
 // what all of them read (counts, the free list's length, page ids that go
 // back) is read before the first one, what goes back is on the stack before
-// the second, behind which pages are taken.  Entry e of what goes back, or is
-// taken, finds its request by bisection in the sums, so that one request with
-// many pages is spread like many with one.
+// the second, behind which pages are taken.  What goes back, or is taken, is
+// spread by entries, which find their requests by bisection in the sums, so
+// that one request with many pages is spread like many with one.
 // Latency bound: two trips to L2, a scan and two barriers.
 __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid_constant__ PageArgs a, int ctas) {
   extern __shared__ __align__(16) int ps[];
@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
     const int32_t* row = a.page_table + (long long)b * a.max_pages;
     bool wrong = false;
     if (give[b])
+#pragma unroll 8
       for (int p = want[b] + (tid & 31); p < have[b]; p += 32) wrong |= row[p] < 0 || row[p] >= a.num_pages;
     if (__any_sync(0xffffffffu, wrong) && (tid & 31) == 0) {
       page_error(a, KDTV_ERR_BAD_PAGE);
@@ -164,25 +165,56 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
     if (p != have[b]) a.n_pages[b] = p;
   }
   if (me == 0 && usable) *a.free_count = top - taken;
+  // A warp takes runs of 32 kBatch entries, all of them under way together.  Requests with many pages each: an
+  // entry's request is found from the one 32 entries before; with few, by bisection each time.
+  constexpr int kBatch = 8;
+  const bool few = (long long)given + taken < 64ll * a.B;
+  const int lane = tid & 31, run0 = (me >> 5) * 32 * kBatch, runs = all * kBatch;
   if (given) {
-    for (int e = me; e < given; e += all) {
-      const int k = given - 1 - e;                     // from the last request's last page on
-      const int b = first_above(give, a.B, k), p = want[b] + k - (b ? give[b - 1] : 0);
-      int32_t* entry = a.page_table + (long long)b * a.max_pages + p;
-      a.free_pages[count + e] = *entry;
-      *entry = -1;
+    for (int e0 = run0; e0 < given; e0 += runs) {
+      int32_t* entry[kBatch];
+      int id[kBatch], b = 0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int k = given - 1 - (e0 + 32 * i + lane);  // from the last request's last page on
+        entry[i] = nullptr;
+        if (k < 0) continue;
+        if (i == 0 || few) b = first_above(give, a.B, k);
+        else
+          while (b > 0 && give[b - 1] > k) --b;
+        entry[i] = a.page_table + (long long)b * a.max_pages + want[b] + k - (b ? give[b - 1] : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) id[i] = entry[i] ? *entry[i] : 0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (entry[i]) {
+          a.free_pages[count + e0 + 32 * i + lane] = id[i];
+          *entry[i] = -1;
+        }
     }
-    __threadfence();
-    if (ctas > 1) ptx::cluster_sync();
-    else __syncthreads();
+    if (taken) {                                       // (it may be among those that are taken)
+      __threadfence();
+      if (ctas > 1) ptx::cluster_sync();
+      else __syncthreads();
+    }
   }
   // The k-th page that is taken, from the top of the stack down.
   auto page_taken = [&](int k) { return *reinterpret_cast<volatile int32_t*>(a.free_pages + (top - 1 - k)); };
-  for (int k = me; k < taken; k += all) {
-    const int b = first_above(take, a.B, k), p = have[b] + k - (b ? take[b - 1] : 0);
-    const int id = page_taken(k);
-    if (id < 0 || id >= a.num_pages) page_error(a, KDTV_ERR_BAD_PAGE);
-    a.page_table[(long long)b * a.max_pages + p] = id;
+  for (int k0 = run0; k0 < taken; k0 += runs) {
+    int id[kBatch], b = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) id[i] = k0 + 32 * i + lane < taken ? page_taken(k0 + 32 * i + lane) : 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = k0 + 32 * i + lane;
+      if (k >= taken) continue;
+      if (i == 0 || few) b = first_above(take, a.B, k);
+      else
+        while (take[b] <= k) ++b;
+      if (id[i] < 0 || id[i] >= a.num_pages) page_error(a, KDTV_ERR_BAD_PAGE);
+      a.page_table[(long long)b * a.max_pages + have[b] + k - (b ? take[b - 1] : 0)] = id[i];
+    }
   }
   if (a.slots)
     for (long long k = me; k < (long long)a.B * a.N; k += all) {
@@ -194,13 +226,20 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
 }
 
 // The slots of many rows, behind the tables.
+constexpr int kSlotRows = 8;
 __global__ void __launch_bounds__(256) page_slots_kernel(const __grid_constant__ PageArgs a) {
   ptx::grid_dep_wait();
   const int b = blockIdx.y, L = a.prefix_len[b], n = live_rows(a.n_live, b, a.N), pages = a.n_pages[b];
   const int32_t* row = a.page_table + (long long)b * a.max_pages;
   int64_t* out = a.slots + (long long)b * a.N;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < a.N; i += gridDim.x * 256)
-    out[i] = slot_of(a, L, n, pages, i, [&](int p) { return row[p]; });
+  // (the look-ups of a thread's rows are under way together)
+  int64_t slot[kSlotRows];
+  const int i0 = blockIdx.x * (256 * kSlotRows) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kSlotRows; ++k) slot[k] = slot_of(a, L, n, pages, i0 + 256 * k, [&](int p) { return row[p]; });
+#pragma unroll
+  for (int k = 0; k < kSlotRows; ++k)
+    if (i0 + 256 * k < a.N) out[i0 + 256 * k] = slot[k];
 }
 
 }  // namespace
@@ -247,7 +286,7 @@ extern "C" int kdtv_pages_resize(const kdtv_pages_dims* d, const int32_t* prefix
   if (cudaLaunchKernelEx(&cfg, pages_resize_kernel, a, ctas) != cudaSuccess) return KDTV_ERR_CUDA;
   if (apart) {
     a.slots = slots;
-    const unsigned blocks = (unsigned)((d->N + 1023) / 1024);
+    const unsigned blocks = (unsigned)((d->N + 256 * kSlotRows - 1) / (256 * kSlotRows));
     if (launch_ex(page_slots_kernel, dim3(blocks, (unsigned)d->B), dim3(256), 0, stream, true, a) != cudaSuccess)
       return KDTV_ERR_CUDA;
   }

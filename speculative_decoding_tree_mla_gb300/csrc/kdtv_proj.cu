@@ -12,11 +12,14 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// s_a A_a x of a request's rows: a warp per rank row and eight rows of x, the
-// lanes along d_in.
+// s_a A_a x of a request's rows: a CTA has eight rows of x and kRanks ranks, its
+// threads go along d_in; their sums meet by shuffles and in shared memory.
+constexpr int kRows = 8, kRanks = 4;
+
 template <typename X, typename T>
 __global__ void __launch_bounds__(kThreads) proj_low_simt_kernel(const __grid_constant__ ProjArgs a) {
-  const int b = blockIdx.y, i0 = blockIdx.x * 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float part[kThreads / 32][kRows * kRanks];
+  const int b = blockIdx.y, i0 = blockIdx.x * kRows, r0 = blockIdx.z * kRanks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = live_rows(a.n_live, b, a.N);
   if (i0 >= n) return;
   const int id = proj_adapter(a, a.adapter[b]);
@@ -24,31 +27,47 @@ __global__ void __launch_bounds__(kThreads) proj_low_simt_kernel(const __grid_co
   const float s = a.adapter_scale ? a.adapter_scale[id] : 1.f;
   const X* x = static_cast<const X*>(a.x) + b * a.xs[0] + i0 * a.xs[1];
   const uint8_t* xe = a.x_scale + ((long long)b * a.N + i0) * (a.K / KDTV_GROUP);
-  for (int r = warp; r < a.R; r += kThreads / 32) {
-    const T* A = static_cast<const T*>(a.A) + ((long long)id * a.R + r) * a.K;
-    float acc[8] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 32 * 16) {        // sums of at most 16 terms a lane, then of those
-      float part[8] = {};
-      for (int k = k0 + lane; k < min(a.K, k0 + 32 * 16); k += 32) {
-        const float w = to_f32(A[k]);
+  const T* A = static_cast<const T*>(a.A) + ((long long)id * a.R + r0) * a.K;
+  float total[kRows][kRanks] = {};
+  for (int k0 = 0; k0 < a.K; k0 += kThreads * 32) {      // chains of at most 32 terms, then their sums
+    float sum[kRows][kRanks] = {};
+#pragma unroll 2
+    for (int k = k0 + threadIdx.x; k < min(a.K, k0 + kThreads * 32); k += kThreads) {
+      float u[kRows], w[kRanks];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i0 + j < n) {
-            float v = to_f32(x[j * a.xs[1] + k]);
-            if constexpr (sizeof(X) == 1) v *= scale_of_byte(xe[(long long)j * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
-            part[j] = fmaf(v, w, part[j]);
-          }
+      for (int j = 0; j < kRows; ++j) {
+        u[j] = i0 + j < n ? to_f32(x[j * a.xs[1] + k]) : 0.f;
+        if constexpr (sizeof(X) == 1)
+          if (i0 + j < n) u[j] *= scale_of_byte(xe[(long long)j * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += part[j];
+      for (int r = 0; r < kRanks; ++r) w[r] = r0 + r < a.R ? to_f32(A[(long long)r * a.K + k]) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r) sum[j][r] = fmaf(u[j], w[r], sum[j][r]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kRows; ++j)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-      if (lane == 0 && i0 + j < n) a.low[((long long)b * a.N + i0 + j) * a.R + r] = s * acc[j];
-    }
+      for (int r = 0; r < kRanks; ++r) total[j][r] += sum[j][r];
   }
+#pragma unroll
+  for (int j = 0; j < kRows; ++j)
+#pragma unroll
+    for (int r = 0; r < kRanks; ++r) {
+      float v = total[j][r];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) part[warp][j * kRanks + r] = v;
+    }
+  __syncthreads();
+  if (threadIdx.x >= kRows * kRanks) return;
+  float v = 0.f;
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) v += part[k][threadIdx.x];
+  const int i = i0 + threadIdx.x / kRanks, r = r0 + threadIdx.x % kRanks;
+  if (i < n && r < a.R) a.low[((long long)b * a.N + i) * a.R + r] = s * v;
 }
 
 // y: a CTA has TM rows (of all requests' rows) and TN outputs, kStep elements
@@ -99,27 +118,39 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
   const X* x = static_cast<const X*>(a.x);
   const X* W = static_cast<const X*>(a.W);
   int held = 0;
-  for (int first = 0; first < steps; first += S) {
-    const int k0 = (first + g) * kStep;                // (a group behind the last step adds zeros)
-    for (int e = t; e < TM * kStep; e += kGroup) {
-      const int m = e / kStep, k = k0 + e % kStep;
+  // A step's elements: kGroup is a multiple of kStep, so a thread stays in its column; the next step's are on their
+  // way while this one's are multiplied.
+  static_assert(kGroup % kStep == 0, "a thread's column");
+  constexpr int kXs = TM * kStep / kGroup, kWs = TN * kStep / kGroup, kDown = kGroup / kStep;
+  const int col = t % kStep, row = t / kStep;
+  float nx[kXs], nw[kWs];
+  auto fetch = [&](int step) {                         // (a group behind the last step gets zeros)
+    const int k = step * kStep + col;
+#pragma unroll
+    for (int i = 0; i < kXs; ++i) {
+      const int m = row + i * kDown;
       const long long o = s_x[m];
-      float v = 0.f;
-      if (o >= 0 && k < a.K) {
-        v = to_f32(x[o + k]);
-        if constexpr (sizeof(X) == 1) v *= scale_of_byte(a.x_scale[(long long)s_row[m] * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
-      }
-      xs[g][e % kStep][m] = v;
+      const bool on = o >= 0 && k < a.K;
+      nx[i] = on ? to_f32(x[o + k]) : 0.f;
+      if constexpr (sizeof(X) == 1)
+        if (on) nx[i] *= scale_of_byte(a.x_scale[(long long)s_row[m] * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
     }
-    for (int e = t; e < TN * kStep; e += kGroup) {
-      const int f = f0 + e / kStep, k = k0 + e % kStep;
-      float v = 0.f;
-      if (f < a.M && k < a.K) {
-        v = to_f32(W[(long long)f * a.K + k]);
-        if constexpr (sizeof(X) == 1) v *= scale_of_byte(a.W_scale[(long long)f * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
-      }
-      ws[g][e % kStep][e / kStep] = v;
+#pragma unroll
+    for (int i = 0; i < kWs; ++i) {
+      const int f = f0 + row + i * kDown;
+      const bool on = f < a.M && k < a.K;
+      nw[i] = on ? to_f32(W[(long long)f * a.K + k]) : 0.f;
+      if constexpr (sizeof(X) == 1)
+        if (on) nw[i] *= scale_of_byte(a.W_scale[(long long)f * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
     }
+  };
+  fetch(g);
+  for (int first = 0; first < steps; first += S) {
+#pragma unroll
+    for (int i = 0; i < kXs; ++i) xs[g][col][row + i * kDown] = nx[i];
+#pragma unroll
+    for (int i = 0; i < kWs; ++i) ws[g][col][row + i * kDown] = nw[i];
+    if (first + S < steps) fetch(first + S + g);
     __syncthreads();
 #pragma unroll 8
     for (int k = 0; k < kStep; ++k) {
@@ -185,7 +216,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 template <typename X, typename T>
 int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
   if (a.adapter)
-    proj_low_simt_kernel<X, T><<<dim3((unsigned)((a.N + 7) / 8), (unsigned)a.B), kThreads, 0, st>>>(a);
+    proj_low_simt_kernel<X, T><<<dim3((unsigned)((a.N + kRows - 1) / kRows), (unsigned)a.B, (unsigned)((a.R + kRanks - 1) / kRanks)),
+                                 kThreads, 0, st>>>(a);
   const long long rows = (long long)a.B * a.N;
   const long long big = (rows + 63) / 64 * ((a.M + 63) / 64);
   if (big >= sms || rows > 16 * 65535)
