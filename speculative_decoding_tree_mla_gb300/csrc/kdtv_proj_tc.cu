@@ -207,10 +207,14 @@ __device__ __forceinline__ uint32_t idesc_scaled(int N, int byte) {
   return ((uint32_t)byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(2 * kFeatures >> 4) << 24) |
          ((uint32_t)byte << 29);
 }
-// Twelve words of a lane, four columns each: of W's rows, of tokens 0 - 127, of the others.
+// Words of a lane, one a column.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
                :: "r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& v, const uint4& w) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -696,7 +700,6 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         if (t + 128 * h < cols && column(a, it.g, it.j, it.hr, t + 128 * h, &b, &i))
           rows[1 + h] = a.x_scale + ((long long)b * a.N + i) * row_bytes;
       }
-      const int parts = cols > 128 ? 3 : 2;
       uint4 now[3], soon[3], later[3];         // two windows ahead: they come from DRAM
 #pragma unroll
       for (int r = 0; r < 3; ++r) {
@@ -723,13 +726,16 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           }
           if (!agree(alive)) break;
         }
+        // W's words, those of tokens 0 - 127, of the others: at hand when their place is free.
+        const uint32_t from = stage + (k % kWindow) * kScaleBytes + lane * 16;
+        const uint4 w0 = lds128(from), w1 = lds128(from + 512), w2 = lds128(from + 1024);
         alive = alive && wait_warp(guard, BAR(B_EMPTY + slot), phase ^ 1u);
         if (!alive) continue;                  // (until the next meeting)
         if (k < a.base) {
           tc_fence_after();
           const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + scale_at(a, slot);
-          const uint32_t from = stage + (k % kWindow) * kScaleBytes + lane * 16;
-          for (int r = 0; r < parts; ++r) tmem_st4(to + 4 * r, lds128(from + 512 * r));
+          tmem_st8(to, w0, w1);
+          if (cols > 128) tmem_st4(to + 8, w2);
           tmem_wait_st();
           tc_fence_before();
         }
