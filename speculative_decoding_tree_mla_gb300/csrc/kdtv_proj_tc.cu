@@ -763,13 +763,17 @@ template <bool kOneByte>
 __global__ void __launch_bounds__(32 * kCombineWarps) proj_combine_kernel(const __grid_constant__ ProjArgs a) {
   const int lane = threadIdx.x & 31, per_tile = 2 * (2 * a.half_cols / kCombineCols);
   grid_dep_wait();
+  int item = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
   const unsigned int status = *reinterpret_cast<volatile unsigned int*>(a.status);
   const int items = a.plan[0] * per_tile;
+  // (the first record at the same time: its place is there, if not the tile, since the grid covers no more of them)
+  const CutTile* records = reinterpret_cast<const CutTile*>(a.plan + 4);
+  CutTile it = records[item / per_tile];
   // (a wait that ran out: some sums were never written)
   if (status == KDTV_ERR_DEVICE_TIMEOUT) return;
-  for (int item = blockIdx.x * kCombineWarps + (threadIdx.x >> 5); item < items; item += gridDim.x * kCombineWarps) {
+  for (bool first = true; item < items; item += gridDim.x * kCombineWarps, first = false) {
     const int tile = item / per_tile, r = item - tile * per_tile, rank = r & 1, c0 = (r >> 1) * kCombineCols;
-    const CutTile it = reinterpret_cast<const CutTile*>(a.plan + 4)[tile];
+    if (!first) it = records[tile];
     if (it.segs < 2 || c0 >= 2 * half_cols_of(a, it.hr)) continue;
     long long at[kCombineCols];                // offset of each token's output row, -1: none
     int b[kCombineCols], i[kCombineCols];
