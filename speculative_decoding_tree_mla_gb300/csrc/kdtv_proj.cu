@@ -3,6 +3,7 @@
 // cores do not take).
 
 #include "kdtv_proj.cuh"
+#include "kdtv_ptx.cuh"
 
 #include <math.h>
 #include <string.h>
@@ -72,16 +73,22 @@ __global__ void __launch_bounds__(kThreads) proj_low_simt_kernel(const __grid_co
 
 // y: a CTA has TM rows (of all requests' rows) and TN outputs, kStep elements
 // of d_in at a time; its threads are S groups that take alternate steps and
-// meet at the end.  A thread has 4 x 4 sums, taken anew after 128 terms and
-// added to the totals: no chain of additions is long.
-// 64 x 64 with S = 1 is bound by the fp32 pipe and shared-memory reads (two
-// 16-byte reads for 16 multiply-adds); 16 x 32 with S = 8 is for few rows, where
-// the 64 x 64 tiles would leave SMs idle.
-template <typename X, typename T, int TM, int TN, int S, int kStep>
-__global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_constant__ ProjArgs a) {
-  constexpr int kGroup = kThreads / S;
-  static_assert(TM / 4 * (TN / 4) == kGroup, "4 x 4 sums a thread");
-  __shared__ __align__(16) float xs[S][kStep][TM + 4], ws[S][kStep][TN + 4];
+// meet at the end.  A thread has R x 4 sums, rows in fours set apart so that its
+// 16-byte reads of shared memory do not conflict; they are taken anew after 128
+// terms and added to the totals: no chain of additions is long.
+// 128 x 64 with 8 x 4 sums is bound by the fp32 pipe (three 16-byte reads for 32
+// multiply-adds, two to an instruction); the smaller tiles are for sizes of which it
+// has too few, 16 x 32 with S = 8 for those of few rows.  Where the tiles leave SMs idle, `split` CTAs of
+// a cluster share d_in and add their totals up through distributed shared memory,
+// in their order, each a part of the tile.
+template <typename X, typename T, int TM, int TN, int S, int kStep, int R>
+__global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_constant__ ProjArgs a, int split) {
+  constexpr int kGroup = kThreads / S, C = R / 4, kRowsOf = TM / C;     // fours of rows, set kRowsOf apart
+  static_assert(TM / R * (TN / 4) == kGroup, "R x 4 sums a thread");
+  constexpr int kOperands = S * kStep * (TM + 4 + TN + 4), kSums = S * kRowsOf * TN;
+  __shared__ __align__(16) float pool[kOperands > kSums ? kOperands : kSums];
+  float (*xs)[kStep][TM + 4] = reinterpret_cast<float (*)[kStep][TM + 4]>(pool);
+  float (*ws)[kStep][TN + 4] = reinterpret_cast<float (*)[kStep][TN + 4]>(pool + S * kStep * (TM + 4));
   __shared__ long long s_x[TM], s_y[TM];               // offsets of the rows, -1: not live
   __shared__ int s_row[TM], s_id[TM];
   __shared__ int s_any;
@@ -111,10 +118,12 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
     s_id[threadIdx.x] = id;
   }
   __syncthreads();
-  if (!s_any) return;
+  if (!s_any) return;                                  // (the same for all of a cluster)
+  const int part = blockIdx.z;
   const int tm = t / (TN / 4) * 4, tn = t % (TN / 4) * 4;
-  float total[4][4] = {}, sum[4][4] = {};
-  const int steps = (a.K + kStep - 1) / kStep;
+  float2 total[R][2] = {}, sum[R][2] = {};
+  const int all_steps = (a.K + kStep - 1) / kStep;
+  const int from = (int)((long long)all_steps * part / split), steps = (int)((long long)all_steps * (part + 1) / split);
   const X* x = static_cast<const X*>(a.x);
   const X* W = static_cast<const X*>(a.W);
   int held = 0;
@@ -125,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
   const int col = t % kStep, row = t / kStep;
   float nx[kXs], nw[kWs];
   auto fetch = [&](int step) {                         // (a group behind the last step gets zeros)
-    const int k = step * kStep + col;
+    const int k = step < steps ? step * kStep + col : a.K;
 #pragma unroll
     for (int i = 0; i < kXs; ++i) {
       const int m = row + i * kDown;
@@ -144,71 +153,90 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
         if (on) nw[i] *= scale_of_byte(a.W_scale[(long long)f * (a.K / KDTV_GROUP) + k / KDTV_GROUP]);
     }
   };
-  fetch(g);
-  for (int first = 0; first < steps; first += S) {
+  fetch(from + g);
+  for (int first = from; first < steps; first += S) {
 #pragma unroll
     for (int i = 0; i < kXs; ++i) xs[g][col][row + i * kDown] = nx[i];
 #pragma unroll
     for (int i = 0; i < kWs; ++i) ws[g][col][row + i * kDown] = nw[i];
-    if (first + S < steps) fetch(first + S + g);
     __syncthreads();
+    if (first + S < steps) fetch(first + S + g);
 #pragma unroll 8
     for (int k = 0; k < kStep; ++k) {
-      const float4 u = *reinterpret_cast<const float4*>(&xs[g][k][tm]), w = *reinterpret_cast<const float4*>(&ws[g][k][tn]);
-      const float uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+      float u[R];
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
+      for (int c = 0; c < C; ++c) {
+        const float4 p = *reinterpret_cast<const float4*>(&xs[g][k][c * kRowsOf + tm]);
+        u[4 * c] = p.x; u[4 * c + 1] = p.y; u[4 * c + 2] = p.z; u[4 * c + 3] = p.w;
+      }
+      const float4 q = *reinterpret_cast<const float4*>(&ws[g][k][tn]);
+      const float2 w[2] = {make_float2(q.x, q.y), make_float2(q.z, q.w)};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sum[p][q] = fmaf(uu[p], ww[q], sum[p][q]);
+      for (int p = 0; p < R; ++p)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sum[p][e] = ptx::fma2(make_float2(u[p], u[p]), w[e], sum[p][e]);
     }
     if (++held == 128 / kStep || first + S >= steps) {
       held = 0;
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
+      for (int p = 0; p < R; ++p)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          total[p][q] += sum[p][q];
-          sum[p][q] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          total[p][e] = ptx::add2(total[p][e], sum[p][e]);
+          sum[p][e] = make_float2(0.f, 0.f);
         }
     }
     __syncthreads();
   }
-  if constexpr (S > 1) {                               // the groups' totals, in their order
-    float* part = &ws[0][0][0];
-    static_assert(sizeof(ws) >= (size_t)S * TM * TN * sizeof(float), "room for the totals");
+  // Block of rows by block: the groups' totals, in their order, then the cluster's, of which a CTA finishes rows part,
+  // part + split, ..
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c > 0) {                                       // (the last block's are read)
+      if (split > 1) ptx::cluster_sync();
+      else __syncthreads();
+    }
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) part[(g * TM + tm + p) * TN + tn + q] = total[p][q];
+      for (int e = 0; e < 2; ++e) *reinterpret_cast<float2*>(pool + (g * kRowsOf + tm + p) * TN + tn + 2 * e) = total[4 * c + p][e];
     __syncthreads();
-    if (g > 0) return;
+    if constexpr (S > 1) {
+      for (int e = threadIdx.x; e < kRowsOf * TN; e += kThreads) {
+        float v = pool[e];
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        for (int s = 1; s < S; ++s) total[p][q] += part[(s * TM + tm + p) * TN + tn + q];
-  }
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    if (s_y[tm + p] < 0) continue;
-    const int id = s_id[tm + p];
-    T* y = static_cast<T*>(a.y) + s_y[tm + p];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int f = f0 + tn + q;
-      if (f >= a.M) continue;
-      float v = total[p][q];
+        for (int s = 1; s < S; ++s) v += pool[s * kRowsOf * TN + e];
+        pool[e] = v;
+      }
+      __syncthreads();
+    }
+    if (split > 1) ptx::cluster_sync();
+    for (int e = threadIdx.x; e < kRowsOf * TN; e += kThreads) {
+      const int m = c * kRowsOf + e / TN, f = f0 + e % TN;
+      if (m % split != part || s_y[m] < 0 || f >= a.M) continue;
+      float v = 0.f;
+      if (split > 1) {
+        for (int k = 0; k < split; ++k) {
+          float u;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(ptx::mapa(ptx::smem_u32(pool + e), k)) : "memory");
+          v += u;
+        }
+      } else {
+        v = pool[e];
+      }
+      const int id = s_id[m];
       if (id >= 0) {
         const T* Bm = static_cast<const T*>(a.Bm) + ((long long)id * a.M + f) * a.R;
-        const float* low = a.low + (long long)s_row[tm + p] * a.R;
+        const float* low = a.low + (long long)s_row[m] * a.R;
         float d = 0.f;
         for (int r = 0; r < a.R; ++r) d = fmaf(low[r], to_f32(Bm[r]), d);
         v += d;
       }
       const float one[1] = {v};
-      store_v<1>(y + f, one);
+      store_v<1>(static_cast<T*>(a.y) + s_y[m] + f, one);
     }
   }
+  if (split > 1) ptx::cluster_sync();                  // (the others have read this CTA's sums)
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -219,12 +247,47 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
     proj_low_simt_kernel<X, T><<<dim3((unsigned)((a.N + kRows - 1) / kRows), (unsigned)a.B, (unsigned)((a.R + kRanks - 1) / kRanks)),
                                  kThreads, 0, st>>>(a);
   const long long rows = (long long)a.B * a.N;
-  const long long big = (rows + 63) / 64 * ((a.M + 63) / 64);
-  if (big >= sms || rows > 16 * 65535)
-    proj_simt_kernel<X, T, 64, 64, 1, 32><<<dim3((unsigned)((a.M + 63) / 64), (unsigned)((rows + 63) / 64)), kThreads, 0, st>>>(a);
-  else
-    proj_simt_kernel<X, T, 16, 32, 8, 16><<<dim3((unsigned)((a.M + 31) / 32), (unsigned)((rows + 15) / 16)), kThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return KDTV_ERR_CUDA;
+  // The tile, and how many CTAs share d_in (four steps each at least), with the least time by this reckoning: the SM
+  // with the most CTAs does its products at the tile's share of the fp32 rate (measured: 55, 43 and 28 %), a step takes
+  // some 500 cycles at least, and joining a cluster 3000.
+  struct Tile {
+    int tm, tn, step, groups, percent;
+  };
+  const Tile tiles[3] = {{128, 64, 16, 1, 55}, {64, 64, 32, 1, 43}, {16, 32, 16, 8, 28}};
+  int best = 0, split = 1;
+  double least = 1e300;
+  for (int k = 0; k < 3; ++k) {
+    const Tile& e = tiles[k];
+    const long long down = (rows + e.tm - 1) / e.tm, n = down * ((a.M + e.tn - 1) / e.tn);
+    if (down > 65535) continue;
+    for (int s = 1; s <= 8; s *= 2) {
+      if (s > 1 && a.K / s < 4 * e.step * e.groups) break;
+      const double per = (double)((n * s + sms - 1) / sms), depth = (double)a.K / s;
+      const double work = per * e.tm * e.tn * depth / (1.28 * e.percent), steps = depth / (e.step * e.groups) * 500.0;
+      const double time = (work > steps ? work : steps) + (s > 1 ? 3000.0 : 0.0);
+      if (time < least) {
+        least = time;
+        best = k;
+        split = s;
+      }
+    }
+  }
+  auto go = [&](auto kern, int tm, int tn) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.M + tn - 1) / tn), (unsigned)((rows + tm - 1) / tm), (unsigned)split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {1, 1, (unsigned)split};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, split) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+  };
+  if (best == 0) return go(proj_simt_kernel<X, T, 128, 64, 1, 16, 8>, 128, 64);
+  if (best == 1) return go(proj_simt_kernel<X, T, 64, 64, 1, 32, 4>, 64, 64);
+  return go(proj_simt_kernel<X, T, 16, 32, 8, 16, 4>, 16, 32);
 }
 
 int check_dims(const kdtv_project_dims* d) {

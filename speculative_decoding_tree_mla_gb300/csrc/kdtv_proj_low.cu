@@ -282,13 +282,11 @@ proj_low_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       xe[j] = kOneByte && i < w.n ? a.x_scale + ((long long)w.b * a.N + i) * row_bytes : nullptr;
     }
     auto exponents = [&](int j, int u) -> uint32_t {
-      uint32_t v = 0x7f7f7f7fu;
-      if (!kOneByte || !xe[j] || u >= u1) return v;
+      if (!kOneByte || !xe[j] || u >= u1) return 0x7f7f7f7fu;
       if (a.scale_mode) return *reinterpret_cast<const uint32_t*>(xe[j] + 4 * u);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (4 * u + k < row_bytes) v = (v & ~(0xffu << (8 * k))) | ((uint32_t)xe[j][4 * u + k] << (8 * k));
-      return v;
+      uint32_t v[1];
+      exponent_words(xe[j], 4 * u, row_bytes, a.x_scale + (long long)a.B * a.N * row_bytes, v);
+      return v[0];
     };
     uint32_t now[NT], soon[NT], later[NT];
 #pragma unroll

@@ -665,20 +665,18 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   } else if (kOneByte && warp >= kWarpScale) {
     // ---- exponent bytes: a thread has a row of W and up to two tokens, four units' bytes at a time ------
     const int t = threadIdx.x - 32 * kWarpScale, row_bytes = a.K / KDTV_GROUP;
-    auto bytes = [&](const uint8_t* row, int u) -> uint4 {        // of window u
+    const uint8_t* const x_end = a.x_scale + (long long)a.B * a.N * row_bytes;
+    const uint8_t* const w_end = a.W_scale + (long long)a.M * row_bytes;
+    auto bytes = [&](const uint8_t* row, int u, const uint8_t* end) -> uint4 {      // of window u
       uint32_t x[4] = {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
       if (row && 4 * u < a.base) {
         if (a.scale_mode == 2) return *reinterpret_cast<const uint4*>(row + 16 * u);
+        if (a.scale_mode == 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = 16 * u + 4 * k;
-          if (a.scale_mode == 1) {
-            if (at < row_bytes) x[k] = *reinterpret_cast<const uint32_t*>(row + at);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (at + e < row_bytes) x[k] = (x[k] & ~(0xffu << (8 * e))) | ((uint32_t)row[at + e] << (8 * e));
-          }
+          for (int k = 0; k < 4; ++k)
+            if (16 * u + 4 * k < row_bytes) x[k] = *reinterpret_cast<const uint32_t*>(row + 16 * u + 4 * k);
+        } else {
+          exponent_words(row, 16 * u, row_bytes, end, x);
         }
       }
       return make_uint4(x[0], x[1], x[2], x[3]);
@@ -703,8 +701,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       uint4 now[3], soon[3], later[3];         // two windows ahead: they come from DRAM
 #pragma unroll
       for (int r = 0; r < 3; ++r) {
-        soon[r] = bytes(rows[r], it.k0 / kWindow);
-        later[r] = bytes(rows[r], it.k0 / kWindow + 1);
+        soon[r] = bytes(rows[r], it.k0 / kWindow, r ? x_end : w_end);
+        later[r] = bytes(rows[r], it.k0 / kWindow + 1, r ? x_end : w_end);
       }
       for (int k = it.k0; k < it.k1; ++k) {
         if (k < a.base && (k == it.k0 || k % kWindow == 0)) {
@@ -712,7 +710,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           for (int r = 0; r < 3; ++r) {
             now[r] = soon[r];
             soon[r] = later[r];
-            later[r] = bytes(rows[r], k / kWindow + 2);
+            later[r] = bytes(rows[r], k / kWindow + 2, r ? x_end : w_end);
           }
           // (The next window is staged beside this one; the one after it when all four warps are past the next
           // meeting.)

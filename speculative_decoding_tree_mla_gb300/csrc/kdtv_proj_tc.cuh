@@ -79,6 +79,36 @@ __device__ __forceinline__ char* part_row(const ProjArgs& a, int b, int i, int h
          (long long)((c & 1) * 2 + p) * a.half_cols * 32 + col * 32;
 }
 
+// Exponent bytes at .. at + 4 W - 1 of a row of `bytes` at any address, as words; 127 behind the row.  From the aligned
+// words that hold them, where those lie within the tensor (it ends at `end`).
+template <int W>
+__device__ __forceinline__ void exponent_words(const uint8_t* row, int at, int bytes, const uint8_t* end, uint32_t (&x)[W]) {
+  const int left = bytes - at;                 // of the row
+  const uint8_t* p = row + at;
+  if (left > 0 && p + 4 * W + 4 <= end) {
+    const uint32_t shift = ((uint32_t)reinterpret_cast<uintptr_t>(p) & 3u) * 8u;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+    uint32_t raw[W + 1];
+#pragma unroll
+    for (int k = 0; k <= W; ++k) raw[k] = words[k];
+#pragma unroll
+    for (int k = 0; k < W; ++k) x[k] = __funnelshift_r(raw[k], raw[k + 1], shift);
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      x[k] = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (4 * k + e < left) x[k] |= (uint32_t)p[4 * k + e] << (8 * e);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const int valid = min(max(left - 4 * k, 0), 4);
+    if (valid < 4) x[k] = (x[k] & ((1u << (8 * valid)) - 1u)) | (0x7f7f7f7fu << (8 * valid));
+  }
+}
+
 }  // namespace
 
 // v = s_a A_a x of all tokens into a.parts, on the current device.

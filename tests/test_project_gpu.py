@@ -135,6 +135,31 @@ def test_ragged_rows(dtype, flags, B, N, K, M):
     c.check(c.run(flags), flags, exact=True)
 
 
+@pytest.mark.parametrize("B,N,K,M", [(3, 5, 96, 70), (2, 40, 160, 130), (1, 200, 1056, 300), (5, 1, 2080, 260), (2, 70, 416, 64),
+                                     (1, 300, 2784, 100), (7, 3, 32, 9), (1, 1, 8160, 520)])
+@pytest.mark.parametrize("flags", [0, SIMT])
+def test_one_byte_exponents_at_any_address(flags, B, N, K, M):
+    """d_in whose rows of exponent bytes (K / 32 of them) start off 4 and 16 bytes; the bytes behind the
+    last group, which belong to other rows, are NaN's there and count for nothing."""
+    c = Case(B, N, K, M, "fp8", 2, 16, seed=K)
+    c.check(c.run(flags), flags)
+    for name in ("x_scale", "W_scale"):                        # the same bytes at an odd address
+        s = c.kw[name]
+        wide = torch.full((s.numel() + 7,), 255, dtype=torch.uint8, device="cuda")
+        wide[3:3 + s.numel()] = s.flatten()
+        c.kw[name] = wide[3:3 + s.numel()].view(s.shape)
+    c.check(c.run(flags), flags)
+
+
+@pytest.mark.parametrize("B,N,K,M,adapters", [(9, 1, 5649, 256, 2), (25, 20, 1592, 1152, 7), (1, 1, 4096, 4100, 1), (40, 10, 777, 640, 3),
+                                              (2, 300, 4099, 130, 2), (1, 16, 8191, 33, 1)])
+def test_fp32_shares_d_in_between_ctas(B, N, K, M, adapters):
+    c = Case(B, N, K, M, "f32", adapters, 5, seed=K)
+    out = c.run()
+    c.check(out)
+    assert torch.equal(out, c.run())
+
+
 @pytest.mark.parametrize("K,rank,dtype", [(7, 16, "bf16"), (100, 16, "bf16"), (64, 3, "bf16"), (33, 5, "f32"), (1, 1, "f32"),
                                           (64, 12, "fp8"), (1001, 5, "f32")])
 def test_odd_sizes(K, rank, dtype):
