@@ -514,8 +514,8 @@ typedef struct kdtv_norm_args {
  *                 clamped to [-117, 119]; larger magnitudes and infinities become +-448, NaN
  *                 stays NaN.  (dim must be a multiple of 32.)  Else NULL.
  *   n_live        [B] int32 or NULL
- * Computed in fp32 from the unrounded sum; each output is rounded once.  A squared row
- * beyond fp32's range gives zeros, as the formula does.  y and residual_out may be x or
+ * Computed in fp32 from the unrounded sum; each output is rounded once.  Rows whose
+ * squares leave fp32's range are scaled first.  y and residual_out may be x or
  * residual (the same strides and element size); other overlaps are not allowed.
  * dim <= 32768.
  */
@@ -524,8 +524,8 @@ int kdtv_rmsnorm(const kdtv_norm_args* args, const void* x, const void* residual
                  const int32_t* n_live, cudaStream_t stream);
 
 typedef struct kdtv_project_dims {
-  int32_t B, N;         /* requests, rows per request                              */
-  int32_t d_in, d_out;
+  int32_t B, N;         /* requests (<= 65535), rows per request (B * N <= 4194240) */
+  int32_t d_in, d_out;  /* <= 2^20                                                 */
   int32_t dtype;        /* KDTV_F32: everything fp32, on CUDA cores; KDTV_BF16;
                            KDTV_BF16_FP8KV: x and W E4M3 bytes with exponent bytes
                            per 32 elements, y, A and Bm bf16 (d_in a multiple of 32) */
@@ -560,18 +560,22 @@ size_t kdtv_project_workspace_size(const kdtv_project_dims* dims);
  * request whose adapter index is out of range (*status =
  * KDTV_ERR_BAD_ADAPTER), are left as they were.  Exponent bytes 1 .. 254 stand
  * for 2^-126 .. 2^127.  bf16 with d_in and rank multiples of 8, 16-byte
- * aligned pointers and x rows, and one-byte inputs with 16-byte aligned
- * pointers and rank a multiple of 8, run on tensor cores, everything else
- * (and KDTV_FLAG_SIMT) in fp32 on CUDA cores.
+ * aligned x, W, A, Bm and x rows, and one-byte inputs with 16-byte aligned x, W,
+ * A, Bm and rank a multiple of 8, run on tensor cores up to d_in 65536; everything
+ * else (and KDTV_FLAG_SIMT) in fp32 on CUDA cores.  (y is written 16 bytes at a
+ * time where its rows are 16-byte aligned and d_out is a multiple of 8.)
  * *status: a device word that the caller clears; the first error stays, but a
- * wait that ran out (KDTV_ERR_DEVICE_TIMEOUT) replaces it.
+ * wait that ran out (KDTV_ERR_DEVICE_TIMEOUT) replaces it.  That call's outputs
+ * are then undefined, and while the word holds it, so are later calls': clear it
+ * before the next call.
  */
 int kdtv_project(const kdtv_project_dims* dims, const void* x, const uint8_t* x_scale,
                  const void* W, const uint8_t* W_scale, const void* A, const void* Bm,
                  const float* adapter_scale, const int32_t* adapter, const int32_t* n_live,
                  void* y, unsigned int* status, cudaStream_t stream);
 
-/* Kernels kdtv_project launches for these dims, or -1. */
+/* Kernels kdtv_project launches for these dims (with adapters in use, and on
+ * tensor cores where the sizes allow them), or -1. */
 int kdtv_project_launches_per_call(const kdtv_project_dims* dims);
 
 typedef struct kdtv_pages_dims {
@@ -604,7 +608,8 @@ typedef struct kdtv_pages_dims {
  * n_pages or returned page ids are out of range, and every request where
  * *free_count is (KDTV_ERR_BAD_PAGE).  Where the free list runs out, the request
  * that it does not suffice for and all behind it that need pages keep what
- * they have (KDTV_ERR_NO_PAGES).  Requests must not share pages.
+ * they have (KDTV_ERR_NO_PAGES).  Requests must not share pages.  Where
+ * kdtv_compact_kv follows, n_live is NULL: it asks for the pages of all N rows.
  */
 int kdtv_pages_resize(const kdtv_pages_dims* dims, const int32_t* prefix_len,
                       const int32_t* n_live, int32_t* free_pages, int32_t* free_count,

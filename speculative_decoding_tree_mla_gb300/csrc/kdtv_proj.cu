@@ -314,10 +314,11 @@ size_t workspace_of(const kdtv_project_dims* d) {
 }
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-// Rows that TMA can read: strides (of what has more than one element) multiples of 16 bytes, not 0.
+// Rows that TMA can read: strides (of what has more than one element) multiples of 16 bytes, not 0, below 2^40.
 bool tma_rows(const kdtv_project_dims* d, const ProjArgs& a) {
   if (d->dtype == KDTV_BF16_FP8KV) return true;          // contiguous
-  return (d->N == 1 || (a.xs[1] > 0 && a.xs[1] % 8 == 0)) && (d->B == 1 || (a.xs[0] > 0 && a.xs[0] % 8 == 0));
+  auto fits = [](long long s) { return s > 0 && s % 8 == 0 && s < (1ll << 39); };
+  return (d->N == 1 || fits(a.xs[1])) && (d->B == 1 || fits(a.xs[0]));
 }
 
 }  // namespace
@@ -349,6 +350,8 @@ extern "C" int kdtv_project(const kdtv_project_dims* d, const void* x, const uin
   if (one_byte && (d->x_stride[0] || d->x_stride[1]) &&
       (d->x_stride[0] != (int64_t)d->N * d->d_in || d->x_stride[1] != d->d_in))
     return KDTV_ERR_INVALID_ARG;
+  if ((d->y_stride[0] || d->y_stride[1]) && ((d->B > 1 && !d->y_stride[0]) || (d->N > 1 && !d->y_stride[1])))
+    return KDTV_ERR_INVALID_ARG;                            // rows over one another
   if (!d->workspace || (reinterpret_cast<uintptr_t>(d->workspace) & 255u) || d->workspace_bytes < workspace_of(d))
     return KDTV_ERR_INVALID_ARG;
   ProjArgs a;

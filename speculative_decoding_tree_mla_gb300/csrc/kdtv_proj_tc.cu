@@ -896,6 +896,7 @@ bool proj_tc_sizes(const kdtv_project_dims* d, int sms, ProjArgs* a) {
   const bool one_byte = d->dtype == KDTV_BF16_FP8KV;
   if (d->dtype == KDTV_F32 || (d->flags & KDTV_FLAG_SIMT)) return false;
   if (!one_byte && d->d_in % 8) return false;
+  if (d->d_in > 65536) return false;          // (an output computed by itself has to be ready while others wait)
   if (d->adapters > 0 && d->rank % 8) return false;
   const int cap = kTokens / 2;                // columns of a half
   a->by_rows_of = d->B == 1 || d->N > cap;

@@ -948,7 +948,7 @@ class PagePool:
 
 class PagesResize(_Bound):
     """Caller of kdtv_pages_resize: request b is to hold the pages of rows 0 .. prefix_len[b] +
-    n_live[b] (n_live None: N more rows each).  slots [B, N] int64 (True: a new one): cache row of
+    n_live[b] (n_live None: N more rows each, as compact_kv wants them).  slots [B, N] int64 (True: a new one): cache row of
     row prefix_len[b] + i, -1 where there is none.  Calling it returns the status word, or (slots,
     status word)."""
 

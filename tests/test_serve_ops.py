@@ -37,6 +37,8 @@ INVALID, UNSUPPORTED = "KDTV_ERR_INVALID_ARG", "KDTV_ERR_UNSUPPORTED"
     (dict(y_stride=(2000, 600, 130)), dict(y=256), INVALID),            # in place with other strides
     (dict(y_stride=(2000, 600, 130)), dict(y=512), INVALID),            # over the residual
     (dict(r_stride=(2000, 600, 130)), dict(res_out=512), INVALID),
+    (dict(y_stride=(0, 512, 128)), {}, INVALID), (dict(y_stride=(1536, 0, 128)), {}, INVALID),
+    (dict(ro_stride=(1536, 512, 0)), {}, INVALID),
     (dict(out_dtype=kdtv.KDTV_BF16_FP8KV), dict(y=256, scale=256), INVALID),
     (dict(dim=32769), {}, UNSUPPORTED), (dict(B=1 << 20, N=1 << 12), {}, UNSUPPORTED),
 ])
@@ -84,6 +86,7 @@ def test_projection_dims_refused(L, fields, code):
     ({}, dict(A=None, Bm=None)), (dict(adapters=0), {}), (dict(workspace=None), {}), (dict(workspace=4096 + 16), {}),
     (dict(workspace_bytes=1), {}),
     (dict(dtype=kdtv.KDTV_BF16_FP8KV, x_stride=(1000, 200)), dict(xs=256, ws=256)),
+    (dict(y_stride=(0, 64)), {}), (dict(y_stride=(192, 0)), {}),
 ])
 def test_projection_refusals(L, fields, ptr):
     d = _proj_dims(workspace=4096, workspace_bytes=1 << 40)
