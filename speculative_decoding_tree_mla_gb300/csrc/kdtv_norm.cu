@@ -68,28 +68,44 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
     }
   }
 
-  float sum = 0.f;
+  __shared__ float part[32];
+  const int lanes = min(a.per_row, 32), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto mean_square = [&](float f) -> float {         // of the row times f
+    float sum = 0.f;
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    float part = 0.f;
+    for (int c = 0; c < CH; ++c) {
+      float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) part = fmaf(h[c][k], h[c][k], part);
-    sum += part;
+      for (int k = 0; k < V; ++k) v = fmaf(h[c][k] * f, h[c][k] * f, v);
+      sum += v;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (a.per_row > 32) {                             // one row in the block
+      if (lane == 0) part[warp] = sum;
+      __syncthreads();
+      sum = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    return sum / (float)a.dim;
+  };
+  float mean = mean_square(1.f) + a.eps, up = 1.f;
+  // Squares beyond fp32's range, or too small for it: of the row times a power of two, whose square goes to eps.
+  const float s = !(mean <= 0x1p100f) ? 0x1p-72f : mean < 0x1p-60f ? 0x1p75f : 1.f;
+  if (__any_sync(0xffffffffu, s != 1.f)) {            // (a row of more than a warp: the same for all of the block)
+    if (a.per_row > 32) __syncthreads();              // (the first sums are read)
+    mean = mean_square(s) + a.eps * s * s;
+    up = s;
   }
-  const int lanes = min(a.per_row, 32);
+  float inv = 1.f / sqrtf(mean);
+  if (up < 1.f) inv *= up;                            // (1 / the root: 2^-128 at least)
+  if (up > 1.f)                                       // (that may be more than fp32 holds)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (a.per_row > 32) {                               // one row in the block
-    __shared__ float part[32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) part[warp] = sum;
-    __syncthreads();
-    sum = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f;
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  const float inv = 1.f / sqrtf(sum / (float)a.dim + a.eps);
+      for (int k = 0; k < V; ++k) h[c][k] *= up;
 
   const T* weight = static_cast<const T*>(a.weight);
   O* y = static_cast<O*>(a.y) + b * a.ys[0] + i * a.ys[1] + head * a.ys[2];
@@ -210,6 +226,9 @@ extern "C" int kdtv_rmsnorm(const kdtv_norm_args* d, const void* x, const void* 
   strides(d->y_stride, d->N, d->H, d->dim, a.ys);
   a.by_heads = divisor((unsigned)d->H);
   a.by_N = divisor((unsigned)d->N);
+  // Rows of a result over one another.
+  for (const auto* s : {&a.ys, &a.ros})
+    if ((d->B > 1 && !(*s)[0]) || (d->N > 1 && !(*s)[1]) || (d->H > 1 && !(*s)[2])) return KDTV_ERR_INVALID_ARG;
   // In place is element by element: other strides or element sizes would overwrite what is still to be
   // read.
   if ((const void*)y == x && (one_byte || !same(a.xs, a.ys))) return KDTV_ERR_INVALID_ARG;

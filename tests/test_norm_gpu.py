@@ -161,6 +161,21 @@ def test_values_that_are_not_finite():
     assert abs(v[7]) == 448.0 * 2.0 ** (int(scale[0, 0, 0]) - 127) and np.isfinite(v).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [8, 64, 333, 8192])
+def test_squares_beyond_fp32(dtype, dim):
+    """Rows times 2^100 and 2^-100 (and up to the type's largest) beside ordinary ones."""
+    x = make((6, 5, 3, dim), dtype, 30)
+    for k, f in enumerate((2.0 ** 100, 2.0 ** -100, 2.0 ** 62, 2.0 ** -66)):
+        x[k] = (x[k].double() * f).to(x.dtype)
+    x[4, 0, 0, 0] = 3.0e38
+    x[4, 1, 2, dim - 1] = 2.0 ** -120
+    for eps in (0.0, 1e-6, 3.0):
+        near(f64(kdtv.rmsnorm(x, eps=eps)), O.rmsnorm(f64(x), None, eps)[0], ARITH + STEP[dtype], 2.0 ** -133)
+    if dim % 32 == 0:
+        check_one_byte(*kdtv.rmsnorm(x, eps=0.0, one_byte=True), O.rmsnorm(f64(x), None, 0.0)[0])
+
+
 def test_deterministic_streams_and_capture():
     x, r, w = make((64, 8, 4096), "bf16", 16), make((64, 8, 4096), "bf16", 17), make((4096,), "bf16", 18)
     op = kdtv.RmsNorm(x, w, residual=r, residual_out=torch.empty_like(r), one_byte=True)
