@@ -20,6 +20,7 @@ constexpr int kRows = 8, kRanks = 4;
 template <typename X, typename T>
 __global__ void __launch_bounds__(kThreads) proj_low_simt_kernel(const __grid_constant__ ProjArgs a) {
   __shared__ float part[kThreads / 32][kRows * kRanks];
+  ptx::grid_dep_launch();                              // the projection may start; it waits for this grid at its end
   const int b = blockIdx.y, i0 = blockIdx.x * kRows, r0 = blockIdx.z * kRanks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = live_rows(a.n_live, b, a.N);
   if (i0 >= n) return;
@@ -118,7 +119,10 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
     s_id[threadIdx.x] = id;
   }
   __syncthreads();
-  if (!s_any) return;                                  // (the same for all of a cluster)
+  if (!s_any) {                                        // (the same for all of a cluster)
+    ptx::grid_dep_wait();
+    return;
+  }
   const int part = blockIdx.z;
   const int tm = t / (TN / 4) * 4, tn = t % (TN / 4) * 4;
   float2 total[R][2] = {}, sum[R][2] = {};
@@ -188,6 +192,7 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
     }
     __syncthreads();
   }
+  ptx::grid_dep_wait();                                // A x of all rows, where there are adapters
   // Block of rows by block: the groups' totals, in their order, then the cluster's, of which a CTA finishes rows part,
   // part + split, ..
 #pragma unroll
@@ -278,11 +283,13 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)((a.M + tn - 1) / tn), (unsigned)((rows + tm - 1) / tm), (unsigned)split);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {1, 1, (unsigned)split};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.adapter ? 2 : 1;                  // beside the first kernel, where there is one
     return cudaLaunchKernelEx(&cfg, kern, a, split) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
   };
   if (best == 0) return go(proj_simt_kernel<X, T, 128, 64, 1, 16, 8>, 128, 64);
