@@ -244,7 +244,187 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
   if (split > 1) ptx::cluster_sync();                  // (the others have read this CTA's sums)
 }
 
+// y of few rows: the weights go from global memory to registers once per RT rows.  A warp has F outputs, its
+// lanes go along d_in, V neighbours at a time and U such loads of each output under way together; `slices` warps
+// share d_in.  The rows' elements come from L1, where a block's warps share them.  A lane's sums are
+// taken anew after at most 128 terms, as above.  One row is bound by DRAM (8192 x 10240: 64 us, 5300 GB/s), more by L1.
+// (16 elements a lane and step: 73 us for one row, 78 for four where 8 take 71; eight rows and two outputs a warp: 157
+// for eight rows where two passes of four take 101; two outputs and four rows: 111 for four.)
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* p, const uint8_t* scale, long long at, float* x) {
+  float v[V];
+  if constexpr (sizeof(T) == 1 && V == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p + at);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 two = widen2(((k < 2 ? w.x : w.y) >> (16 * (k & 1))) & 0xffffu);
+      v[2 * k] = two.x;
+      v[2 * k + 1] = two.y;
+    }
+  } else {
+    load_v<V>(p + at, v);
+  }
+  const float f = sizeof(T) == 1 ? scale_of_byte(scale[at / KDTV_GROUP]) : 1.f;   // (rows are whole groups)
+#pragma unroll
+  for (int k = 0; k < V; ++k) x[k] = sizeof(T) == 1 ? v[k] * f : v[k];
+}
+
+template <typename X, typename T, int V, int F, int RT>
+__global__ void __launch_bounds__(kThreads) proj_few_simt_kernel(const __grid_constant__ ProjArgs a, int slices) {
+  constexpr int E = 8, U = E / V;                  // a lane's elements of a step
+  __shared__ long long s_x[RT], s_y[RT];
+  __shared__ int s_row[RT], s_id[RT];
+  __shared__ float red[kThreads / 32][F * RT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % slices;
+  const int f0 = (blockIdx.y * (kThreads / 32 / slices) + warp / slices) * F;
+  const long long r0 = (long long)blockIdx.x * RT, rows = (long long)a.B * a.N;
+  if (threadIdx.x < 32) {
+    const long long r = r0 + lane;
+    long long ox = -1;
+    int id = -1;
+    if (lane < RT && r < rows) {
+      const int b = (int)divide((unsigned)r, a.by_N), i = (int)(r - (long long)b * a.N);
+      if (i < live_rows(a.n_live, b, a.N)) {
+        id = proj_adapter(a, a.adapter ? a.adapter[b] : -1);
+        if (id != -2) ox = b * a.xs[0] + i * a.xs[1];
+      }
+      if (ox >= 0) s_y[lane] = b * a.ys[0] + i * a.ys[1];
+    }
+    const unsigned live = __ballot_sync(0xffffffffu, ox >= 0);
+    // (rows that are not live read another's elements, for nothing)
+    const int other = live ? __ffs(live) - 1 : 0;
+    const long long its = __shfl_sync(0xffffffffu, ox, other);
+    if (lane < RT) {
+      s_x[lane] = ox >= 0 ? ox : its;
+      s_row[lane] = (int)(ox >= 0 ? r : r0 + other);
+      s_id[lane] = ox >= 0 ? id : -2;
+    }
+  }
+  __syncthreads();
+  if (s_x[0] < 0) {                                      // no row is live
+    ptx::grid_dep_wait();
+    return;
+  }
+  const X* x[RT];
+  const uint8_t* xe[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    x[r] = static_cast<const X*>(a.x) + s_x[r];
+    xe[r] = a.x_scale + (long long)s_row[r] * (a.K / KDTV_GROUP);
+  }
+  const int all = a.K / V, from = (int)((long long)all * slice / slices), end = (int)((long long)all * (slice + 1) / slices);
+  float total[F][RT] = {};
+  float2 sum[F][RT] = {};
+  auto flush = [&]() {
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        total[f][r] += sum[f][r].x + sum[f][r].y;
+        sum[f][r] = make_float2(0.f, 0.f);
+      }
+  };
+  int held = 0;
+#pragma unroll 1
+  for (int i0 = from + lane; i0 < end; i0 += 32 * U) {
+    float w[F][E];
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) w[f][u * V + k] = 0.f;
+        if (f0 + f < a.M && i0 + 32 * u < end)
+          load_row<X, V>(static_cast<const X*>(a.W), a.W_scale, (long long)(f0 + f) * a.K + (long long)(i0 + 32 * u) * V, &w[f][u * V]);
+      }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float v[E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[u * V + k] = 0.f;
+        if (i0 + 32 * u < end) load_row<X, V>(x[r], xe[r], (long long)(i0 + 32 * u) * V, &v[u * V]);
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          sum[f][r] = ptx::fma2(make_float2(v[e], v[e + 1]), make_float2(w[f][e], w[f][e + 1]), sum[f][r]);
+    }
+    if (++held == 256 / E) {
+      held = 0;
+      flush();
+    }
+  }
+  flush();
+  float mine = 0.f;                                      // lane f RT + r keeps that sum
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float v = total[f][r];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == f * RT + r) mine = v;
+    }
+  if (slices > 1) {
+    if (lane < F * RT) red[warp][lane] = mine;
+    __syncthreads();
+    if (slice > 0) {
+      ptx::grid_dep_wait();
+      return;
+    }
+    if (lane < F * RT)
+      for (int s = 1; s < slices; ++s) mine += red[warp + s][lane];
+  }
+  ptx::grid_dep_wait();                                  // A x of all rows, where there are adapters
+  const int f = f0 + lane / RT, r = lane % RT;
+  if (lane >= F * RT || f >= a.M || s_id[r] == -2) return;
+  if (s_id[r] >= 0) {
+    const T* Bm = static_cast<const T*>(a.Bm) + ((long long)s_id[r] * a.M + f) * a.R;
+    const float* low = a.low + (long long)s_row[r] * a.R;
+    float d = 0.f;
+    for (int k = 0; k < a.R; ++k) d = fmaf(low[k], to_f32(Bm[k]), d);
+    mine += d;
+  }
+  const float one[1] = {mine};
+  store_v<1>(static_cast<T*>(a.y) + s_y[r] + f, one);
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+constexpr int kFew = 4, kFewOut = 4;
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Warps that share d_in: as many as an SM holds, if their parts are two steps' at least.  (One row, 8192 x 10240: half as
+// many warps 76 us, these 64, twice as many 61; eight rows 105, 101, 109.)
+int few_slices(const ProjArgs& a, int sms) {
+  int slices = 1;
+  while (slices < 8 && (long long)(a.M + kFewOut - 1) / kFewOut * slices < 64ll * sms && a.K / (2 * slices) >= 512) slices *= 2;
+  return slices;
+}
+
+template <typename X, typename T>
+int launch_few(const ProjArgs& a, long long rows, int sms, cudaStream_t st) {
+  auto go = [&](auto kern, int rt) {
+    const int slices = few_slices(a, sms), outputs = kThreads / 32 / slices * kFewOut;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((rows + rt - 1) / rt), (unsigned)((a.M + outputs - 1) / outputs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.adapter ? 1 : 0;                  // beside the first kernel, where there is one
+    return cudaLaunchKernelEx(&cfg, kern, a, slices) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
+  };
+  constexpr int V = sizeof(X) == 4 ? 4 : 8;
+  const bool vec = a.K % 8 == 0 && aligned(a.x) && aligned(a.W) && a.xs[0] % V == 0 && a.xs[1] % V == 0;
+  if (rows == 1) return vec ? go(proj_few_simt_kernel<X, T, V, kFewOut, 1>, 1) : go(proj_few_simt_kernel<X, T, 1, kFewOut, 1>, 1);
+  return vec ? go(proj_few_simt_kernel<X, T, V, kFewOut, kFew>, kFew) : go(proj_few_simt_kernel<X, T, 1, kFewOut, kFew>, kFew);
+}
 
 template <typename X, typename T>
 int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
@@ -255,13 +435,16 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
   if (cudaGetLastError() != cudaSuccess) return KDTV_ERR_CUDA;
   // The tile, and how many CTAs share d_in (four steps each at least), with the least time by this reckoning: the SM
   // with the most CTAs does its products at the tile's share of the fp32 rate (measured: 55, 43 and 28 %), a step takes
-  // some 500 cycles at least, and joining a cluster 3000.
+  // some 500 cycles at least, and joining a cluster 3000.  Without tiles four rows take 7 weights a cycle of each SM, 4.5 where all of a block's warps
+  // share d_in and none the rows
+  // (measured with 8192 x 10240 and 4, 8, 12, 16, 24 rows: 71, 101, 139, 178, 261 us, the tiles 154 to 159 and 280; 4096 x
+  // 4096: 21, 31, 44, 57, 83, the tiles 41 to 43 and 61; 1001 x 515, 16 and 32 rows: 7.5 and 8.2, the tiles 14 and 23).
   struct Tile {
     int tm, tn, step, groups, percent;
   };
   const Tile tiles[3] = {{128, 64, 16, 1, 55}, {64, 64, 32, 1, 43}, {16, 32, 16, 8, 28}};
-  int best = 0, split = 1;
-  double least = 1e300;
+  int best = -1, split = 1;
+  double least = 2500.0 + (double)((rows + kFew - 1) / kFew) * a.M * a.K / ((few_slices(a, sms) == 8 ? 4.5 : 7.0) * sms);
   for (int k = 0; k < 3; ++k) {
     const Tile& e = tiles[k];
     const long long down = (rows + e.tm - 1) / e.tm, n = down * ((a.M + e.tn - 1) / e.tn);
@@ -292,6 +475,7 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
     cfg.numAttrs = a.adapter ? 2 : 1;                  // beside the first kernel, where there is one
     return cudaLaunchKernelEx(&cfg, kern, a, split) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
   };
+  if (best < 0) return launch_few<X, T>(a, rows, sms, st);
   if (best == 0) return go(proj_simt_kernel<X, T, 128, 64, 1, 16, 8>, 128, 64);
   if (best == 1) return go(proj_simt_kernel<X, T, 64, 64, 1, 32, 4>, 64, 64);
   return go(proj_simt_kernel<X, T, 16, 32, 8, 16, 4>, 16, 32);
@@ -320,7 +504,6 @@ size_t workspace_of(const kdtv_project_dims* d) {
   return align256(low > tc ? low : tc) + 256;
 }
 
-bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Rows that TMA can read: strides (of what has more than one element) multiples of 16 bytes, not 0, below 2^40.
 bool tma_rows(const kdtv_project_dims* d, const ProjArgs& a) {
   if (d->dtype == KDTV_BF16_FP8KV) return true;          // contiguous

@@ -160,6 +160,21 @@ def test_fp32_shares_d_in_between_ctas(B, N, K, M, adapters):
     assert torch.equal(out, c.run())
 
 
+@pytest.mark.parametrize("dtype,flags", [("f32", 0), ("bf16", SIMT), ("fp8", SIMT)])
+@pytest.mark.parametrize("B,N,K,M,adapters", [(1, 1, 8192, 2100, 1), (1, 1, 32, 3, 0), (2, 1, 4128, 77, 2), (5, 3, 992, 70, 3),
+                                              (16, 1, 4096, 33, 5), (2, 8, 64, 5000, 2), (9, 1, 544, 9, 3), (1, 16, 20000, 40, 1)])
+def test_few_rows_on_cuda_cores(dtype, flags, B, N, K, M, adapters):
+    """Weights streamed once per eight rows, one to eight warps along d_in; some of the rows not live; element by
+    element where d_in or an address is odd."""
+    n = np.random.default_rng(B + K).integers(0, N + 2, B)
+    for live in (None, n):
+        c = Case(B, N, K, M, dtype, adapters, 16, seed=K + M, n_live=live)
+        c.check(c.run(flags), flags)
+    if dtype != "fp8":
+        c = Case(B, N, K + 3, M, dtype, adapters, 5, seed=K, whole=True)
+        c.check(c.run(flags), flags, exact=True)
+
+
 @pytest.mark.parametrize("K,rank,dtype", [(7, 16, "bf16"), (100, 16, "bf16"), (64, 3, "bf16"), (33, 5, "f32"), (1, 1, "f32"),
                                           (64, 12, "fp8"), (1001, 5, "f32")])
 def test_odd_sizes(K, rank, dtype):
