@@ -13,14 +13,17 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// s_a A_a x of a request's rows: a CTA has eight rows of x and kRanks ranks, its
-// threads go along d_in; their sums meet by shuffles and in shared memory.
-constexpr int kRows = 8, kRanks = 4;
+// s_a A_a x of a request's rows: a CTA has kRows rows of x and kRanks ranks (8 and 4, or 2 and 16 where requests have
+// no more rows), its threads go along d_in; their sums meet by shuffles and in shared memory.
+constexpr int kJoin = 4;                   // outputs whose last sums a thread makes together
 
-template <typename X, typename T>
+template <typename X, typename T, int kRows, int kRanks>
 __global__ void __launch_bounds__(kThreads) proj_low_simt_kernel(const __grid_constant__ ProjArgs a) {
   __shared__ float part[kThreads / 32][kRows * kRanks];
-  ptx::grid_dep_launch();                              // the projection may start; it waits for this grid at its end
+  // proj_few_simt_kernel may start; it waits for this grid at its end.  (The tiles' kernel is launched behind this one:
+  // with blocks of this one about, it gave some SMs two blocks and others none, 514 us for 1024 rows, 4096 x 1216, where it
+  // takes 302.)
+  ptx::grid_dep_launch();
   const int b = blockIdx.y, i0 = blockIdx.x * kRows, r0 = blockIdx.z * kRanks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = live_rows(a.n_live, b, a.N);
   if (i0 >= n) return;
@@ -119,10 +122,7 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
     s_id[threadIdx.x] = id;
   }
   __syncthreads();
-  if (!s_any) {                                        // (the same for all of a cluster)
-    ptx::grid_dep_wait();
-    return;
-  }
+  if (!s_any) return;                                  // (the same for all of a cluster)
   const int part = blockIdx.z;
   const int tm = t / (TN / 4) * 4, tn = t % (TN / 4) * 4;
   float2 total[R][2] = {}, sum[R][2] = {};
@@ -192,7 +192,6 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
     }
     __syncthreads();
   }
-  ptx::grid_dep_wait();                                // A x of all rows, where there are adapters
   // Block of rows by block: the groups' totals, in their order, then the cluster's, of which a CTA finishes rows part,
   // part + split, ..
 #pragma unroll
@@ -216,29 +215,46 @@ __global__ void __launch_bounds__(kThreads) proj_simt_kernel(const __grid_consta
       __syncthreads();
     }
     if (split > 1) ptx::cluster_sync();
-    for (int e = threadIdx.x; e < kRowsOf * TN; e += kThreads) {
-      const int m = c * kRowsOf + e / TN, f = f0 + e % TN;
-      if (m % split != part || s_y[m] < 0 || f >= a.M) continue;
-      float v = 0.f;
-      if (split > 1) {
-        for (int k = 0; k < split; ++k) {
-          float u;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(ptx::mapa(ptx::smem_u32(pool + e), k)) : "memory");
-          v += u;
+    const int own = kRowsOf / split * TN;              // (kRowsOf is a multiple of 16)
+    for (int e0 = threadIdx.x; e0 < own; e0 += kJoin * kThreads) {
+      // kJoin outputs, whose look-ups are under way together
+      float v[kJoin] = {}, d[kJoin] = {};
+      long long to[kJoin];
+      const T* Bm[kJoin];
+      const float* low[kJoin];
+      bool with[kJoin], any = false;
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) {
+        const int e = min(e0 + j * kThreads, own - 1), at = (e / TN * split + part) * TN + e % TN;
+        const int m = c * kRowsOf + at / TN, f = f0 + at % TN, id = s_id[m];
+        to[j] = e0 + j * kThreads < own && s_y[m] >= 0 && f < a.M ? s_y[m] + f : -1;
+        with[j] = to[j] >= 0 && id >= 0;
+        any |= with[j];
+        Bm[j] = static_cast<const T*>(a.Bm) + (with[j] ? ((long long)id * a.M + f) * a.R : 0);
+        low[j] = a.low + (with[j] ? (long long)s_row[m] * a.R : 0);
+        if (split > 1) {
+#pragma unroll 4
+          for (int k = 0; k < split; ++k) {
+            float u;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(ptx::mapa(ptx::smem_u32(pool + at), k)) : "memory");
+            v[j] += u;
+          }
+        } else {
+          v[j] = pool[at];
         }
-      } else {
-        v = pool[e];
       }
-      const int id = s_id[m];
-      if (id >= 0) {
-        const T* Bm = static_cast<const T*>(a.Bm) + ((long long)id * a.M + f) * a.R;
-        const float* low = a.low + (long long)s_row[m] * a.R;
-        float d = 0.f;
-        for (int r = 0; r < a.R; ++r) d = fmaf(low[r], to_f32(Bm[r]), d);
-        v += d;
+      if (any) {
+#pragma unroll 4
+        for (int r = 0; r < a.R; ++r)
+#pragma unroll
+          for (int j = 0; j < kJoin; ++j) d[j] = fmaf(low[j][r], to_f32(Bm[j][r]), d[j]);
       }
-      const float one[1] = {v};
-      store_v<1>(static_cast<T*>(a.y) + s_y[m] + f, one);
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j)
+        if (to[j] >= 0) {
+          const float one[1] = {with[j] ? v[j] + d[j] : v[j]};
+          store_v<1>(static_cast<T*>(a.y) + to[j], one);
+        }
     }
   }
   if (split > 1) ptx::cluster_sync();                  // (the others have read this CTA's sums)
@@ -428,9 +444,10 @@ int launch_few(const ProjArgs& a, long long rows, int sms, cudaStream_t st) {
 
 template <typename X, typename T>
 int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
-  if (a.adapter)
-    proj_low_simt_kernel<X, T><<<dim3((unsigned)((a.N + kRows - 1) / kRows), (unsigned)a.B, (unsigned)((a.R + kRanks - 1) / kRanks)),
-                                 kThreads, 0, st>>>(a);
+  if (a.adapter && a.N <= 2)
+    proj_low_simt_kernel<X, T, 2, 16><<<dim3(1, (unsigned)a.B, (unsigned)((a.R + 15) / 16)), kThreads, 0, st>>>(a);
+  else if (a.adapter)
+    proj_low_simt_kernel<X, T, 8, 4><<<dim3((unsigned)((a.N + 7) / 8), (unsigned)a.B, (unsigned)((a.R + 3) / 4)), kThreads, 0, st>>>(a);
   const long long rows = (long long)a.B * a.N;
   if (cudaGetLastError() != cudaSuccess) return KDTV_ERR_CUDA;
   // The tile, and how many CTAs share d_in (four steps each at least), with the least time by this reckoning: the SM
@@ -451,7 +468,8 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
     if (down > 65535) continue;
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && a.K / s < 4 * e.step * e.groups) break;
-      const double per = (double)((n * s + sms - 1) / sms), depth = (double)a.K / s;
+      const int usable = s >= 4 && n * s <= 2 * sms ? sms * 8 / 9 : sms;     // (larger clusters leave SMs out)
+      const double per = (double)((n * s + usable - 1) / usable), depth = (double)a.K / s;
       const double work = per * e.tm * e.tn * depth / (1.28 * e.percent), steps = depth / (e.step * e.groups) * 500.0;
       const double time = (work > steps ? work : steps) + (s > 1 ? 3000.0 : 0.0);
       if (time < least) {
@@ -466,13 +484,11 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)((a.M + tn - 1) / tn), (unsigned)((rows + tm - 1) / tm), (unsigned)split);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {1, 1, (unsigned)split};
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.adapter ? 2 : 1;                  // beside the first kernel, where there is one
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, a, split) == cudaSuccess ? KDTV_OK : KDTV_ERR_CUDA;
   };
   if (best < 0) return launch_few<X, T>(a, rows, sms, st);

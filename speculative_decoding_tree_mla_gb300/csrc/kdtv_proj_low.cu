@@ -67,13 +67,24 @@ __device__ __forceinline__ bool low_request(const ProjArgs& a, int b, int i0, Lo
     w.first = 0;
     w.chunks = a.chunks;
   } else {
+    // the tile's adapters, a request a thread
+    const int words = (a.adapters + 31) / 32, g = (int)divide(b, a.by_requests);
+    for (int k = threadIdx.x; k < words; k += blockDim.x) bits[k] = 0u;
+    __syncthreads();
+    for (int c = g * a.requests + threadIdx.x; c < min(a.B, (g + 1) * a.requests); c += blockDim.x) {
+      const int n = live_rows(a.n_live, c, a.N), id = a.adapter[c];
+      if (n > 0 && id >= 0 && id < a.adapters) atomicOr(&bits[id >> 5], 1u << (id & 31));
+    }
+    __syncthreads();
     if (threadIdx.x < 32) {
-      bool live;
-      const int lane = threadIdx.x, slots = group_bitmap(a, (int)divide(b, a.by_requests), bits, &live);
-      int below = 0;
-      for (int k = lane; k < kWords && 32 * k <= w.id; k += 32)
-        below += __popc(k == w.id >> 5 ? bits[k] & ((1u << (w.id & 31)) - 1u) : bits[k]);
+      const int lane = threadIdx.x;
+      int below = 0, slots = 0;
+      for (int k = lane; k < words; k += 32) {
+        slots += __popc(bits[k]);
+        if (32 * k <= w.id) below += __popc(k == w.id >> 5 ? bits[k] & ((1u << (w.id & 31)) - 1u) : bits[k]);
+      }
       below = warp_sum(below);
+      slots = warp_sum(slots);
       if (lane == 0) s_slot = below, s_slots = slots;
     }
     __syncthreads();

@@ -596,7 +596,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int m = 0; m < 4; ++m) p[k][m] = pack_bf16x2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
-        bool odd = !a.wide;
+        bool odd = false;
         if (mixed) {
           uint32_t top = 0u;                   // not finite?
 #pragma unroll
@@ -632,6 +632,16 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         for (int k = 0; k < 2; ++k)
           stmatrix_x4_trans(rows + (8 * k + (lane & 7)) * kRowPitch + (lane >> 3) * 16, p[k][0], p[k][1], p[k][2], p[k][3]);
         __syncwarp();
+        if (!a.wide) {                         // an output a lane
+#pragma unroll 1
+          for (int c = 0; c < 16; ++c) {
+            const long long to = sh.y_at[c0 + c];
+            unsigned short v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(rows + c * kRowPitch + lane * 2) : "memory");
+            if (to >= 0 && f0 + lane < a.M) static_cast<unsigned short*>(a.y)[to + f0 + lane] = v;
+          }
+          return;
+        }
         const int f = f0 + (lane & 3) * 8;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

@@ -20,12 +20,23 @@ __device__ __forceinline__ int group_bitmap(const ProjArgs& a, int g, uint32_t* 
   for (int w = lane; w < words; w += 32) bits[w] = 0u;
   __syncwarp();
   bool any = false;
-  for (int b = g * a.requests + lane; b < min(a.B, (g + 1) * a.requests); b += 32) {
-    const int n = live_rows(a.n_live, b, a.N), raw = a.adapter ? a.adapter[b] : -1;   // (both loads under way)
-    if (n <= 0) continue;
-    const int id = proj_adapter(a, raw);
-    any |= id != -2;
-    if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
+  constexpr int kAtOnce = 2;                // a lane's requests whose loads are under way together
+  for (int b0 = g * a.requests + lane; b0 < min(a.B, (g + 1) * a.requests); b0 += 32 * kAtOnce) {
+    int n[kAtOnce], raw[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int b = b0 + 32 * k;
+      const bool in = b < min(a.B, (g + 1) * a.requests);
+      n[k] = in ? live_rows(a.n_live, b, a.N) : 0;
+      raw[k] = in && a.adapter ? a.adapter[b] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (n[k] <= 0) continue;
+      const int id = proj_adapter(a, raw[k]);
+      any |= id != -2;
+      if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
+    }
   }
   *live = __any_sync(0xffffffffu, any);
   __syncwarp();
