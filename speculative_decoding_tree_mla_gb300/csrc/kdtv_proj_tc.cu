@@ -232,6 +232,19 @@ __device__ __forceinline__ bool all_of(int id, bool ok) {
   return r != 0u;
 }
 
+// 16 tokens' 32 outputs from shared memory, an output a lane: rows of y that are not 16-byte aligned.  (By itself, so
+// that the aligned rows' code stays short: inlined it cost 64 drafts of 8 two us of 52.)
+__device__ __noinline__ void write_narrow(uint32_t rows, const long long* y_at, unsigned short* y, bool on) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(rows + c * kRowPitch + lane * 2) : "memory");
+    const long long to = y_at[c];
+    if (on && to >= 0) y[to + lane] = v;
+  }
+}
+
 // One output by itself, for a value that is not finite where several adapters share a tile.
 template <bool kOneByte>
 __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
@@ -632,14 +645,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         for (int k = 0; k < 2; ++k)
           stmatrix_x4_trans(rows + (8 * k + (lane & 7)) * kRowPitch + (lane >> 3) * 16, p[k][0], p[k][1], p[k][2], p[k][3]);
         __syncwarp();
-        if (!a.wide) {                         // an output a lane
-#pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
-            const long long to = sh.y_at[c0 + c];
-            unsigned short v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(rows + c * kRowPitch + lane * 2) : "memory");
-            if (to >= 0 && f0 + lane < a.M) static_cast<unsigned short*>(a.y)[to + f0 + lane] = v;
-          }
+        if (!a.wide) {
+          write_narrow(rows, sh.y_at + c0, static_cast<unsigned short*>(a.y) + f0, f0 + lane < a.M);
           return;
         }
         const int f = f0 + (lane & 3) * 8;
