@@ -89,11 +89,11 @@ enum kdtv_status {
 #define KDTV_FLAG_SIMT_PROJ 0x2u     /* bf16: tensor-core attention, but the absorb,
                                         split combine and up-projection on CUDA
                                         cores                                     */
-#define KDTV_FLAG_TEST_STALL 0x100u  /* TEST ONLY: the attention kernel waits on a
-                                        barrier that nothing arrives on, with a
-                                        ~20 ms limit, so the timeout path can be
-                                        checked; the call then reports
-                                        KDTV_ERR_DEVICE_TIMEOUT                  */
+#define KDTV_FLAG_TEST_STALL 0x100u  /* TEST ONLY: the attention kernel (or
+                                        kdtv_project's) waits on a barrier that
+                                        nothing arrives on, with a ~20 ms limit,
+                                        so the timeout path can be checked; the
+                                        call then reports KDTV_ERR_DEVICE_TIMEOUT */
 
 typedef struct kdtv_dims {
   int32_t B;          /* requests in the batch                                  */

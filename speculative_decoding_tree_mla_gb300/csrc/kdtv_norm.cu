@@ -1,6 +1,7 @@
 // kdtv_rmsnorm: the residual's addition and the root-mean-square norm of rows,
 // to the inputs' type or to E4M3 bytes with an exponent byte per 32 elements.
 
+#include "kdtv_ptx.cuh"
 #include "kdtv_rope.cuh"
 
 #include <math.h>
@@ -22,13 +23,72 @@ struct NormArgs {
   int H, per_row, rows_block;    // threads of a row, rows of a block
 };
 
+// Two elements an instruction where there are eight.
+template <int V>
+__device__ __forceinline__ void add_v(float (&x)[V], const float (&y)[V]) {
+  if constexpr (V == 1) {
+    x[0] += y[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      const float2 s = ptx::add2(make_float2(x[k], x[k + 1]), make_float2(y[k], y[k + 1]));
+      x[k] = s.x;
+      x[k + 1] = s.y;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void scale_v(float (&x)[V], float f) {
+  if constexpr (V == 1) {
+    x[0] *= f;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      const float2 s = ptx::mul2(make_float2(x[k], x[k + 1]), make_float2(f, f));
+      x[k] = s.x;
+      x[k + 1] = s.y;
+    }
+  }
+}
+// x (w + offset)
+template <int V>
+__device__ __forceinline__ void weigh_v(float (&x)[V], const float (&w)[V], float offset) {
+  if constexpr (V == 1) {
+    x[0] *= w[0] + offset;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      const float2 s = ptx::mul2(make_float2(x[k], x[k + 1]), ptx::add2(make_float2(w[k], w[k + 1]), make_float2(offset, offset)));
+      x[k] = s.x;
+      x[k + 1] = s.y;
+    }
+  }
+}
+// Sum of the squares of f x.
+template <int V>
+__device__ __forceinline__ float squares(const float (&x)[V], float f) {
+  if constexpr (V == 1) {
+    return x[0] * f * (x[0] * f);
+  } else {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      const float2 v = f == 1.f ? make_float2(x[k], x[k + 1]) : ptx::mul2(make_float2(x[k], x[k + 1]), make_float2(f, f));
+      sum = ptx::fma2(v, v, sum);
+    }
+    return sum.x + sum.y;
+  }
+}
+
 // h = x + r stays in registers: x and r are read once, all of a row's loads
 // are under way together, and the second pass (scale and round) reads nothing
 // but the weights, which L1 or L2 holds.  A row has a part of a warp, or a
 // block; a thread has CH chunks of V elements, per_row chunks apart, so that
 // a warp's accesses are whole lines.
-// Bound by DRAM where there are rows enough, else by the latency of one load,
-// one reduction and one store.
+// Bound by DRAM where there are rows enough (8000 bf16 rows of 8192 with the
+// residual, to one byte: 70 us, 6530 GB/s; before its arithmetic took two
+// elements an instruction and its loads waited as they lie in memory, 82), else by
+// the latency of one load, one reduction and one store (one row 3.3 us).
 // The statistics are fp32; y is (h * (1 / sqrt(mean + eps))) * w, each step
 // rounded to fp32, and rounded once more to its type.
 template <typename T, typename O, int V, int CH>
@@ -39,31 +99,43 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
   const unsigned b = divide(bi, a.by_N), i = bi - b * a.N;
   const bool live = r < a.rows && (int)i < live_rows(a.n_live, b, a.N);
 
-  float h[CH][V];
-  const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + i * a.xs[1] + head * a.xs[2];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int at = c * a.per_row + t;
-#pragma unroll
-    for (int k = 0; k < V; ++k) h[c][k] = 0.f;
-    if (live && at < a.chunks) load_v<V>(x + (long long)at * V, h[c]);
-  }
-  if (a.residual) {
-    const T* res = static_cast<const T*>(a.residual) + b * a.rs[0] + i * a.rs[1] + head * a.rs[2];
-    T* out = static_cast<T*>(a.residual_out) + b * a.ros[0] + i * a.ros[1] + head * a.ros[2];
-    float u[CH][V];
+  // (as they lie in memory until all of them are there: half the registers)
+  constexpr int kWords = V == 8 ? (int)sizeof(T) / 2 : 1;
+  uint4 words[2][CH][kWords];
+  float single[2][CH];
+  auto load = [&](const T* p, uint4 (&w)[CH][kWords], float (&s)[CH]) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int at = c * a.per_row + t;
+      s[c] = 0.f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) u[c][k] = 0.f;
-      if (live && at < a.chunks) load_v<V>(res + (long long)at * V, u[c]);
+      for (int k = 0; k < kWords; ++k) w[c][k] = make_uint4(0u, 0u, 0u, 0u);
+      if (!live || at >= a.chunks) continue;
+      if constexpr (V == 8) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[c][k] = reinterpret_cast<const uint4*>(p + (long long)at * V)[k];
+      } else {
+        s[c] = to_f32(p[at]);
+      }
     }
+  };
+  auto floats = [&](const uint4 (&w)[kWords], float s, float (&x)[V]) {
+    if constexpr (V == 8) unpack8<T>(w, x);
+    else x[0] = s;
+  };
+  load(static_cast<const T*>(a.x) + b * a.xs[0] + i * a.xs[1] + head * a.xs[2], words[0], single[0]);
+  if (a.residual) load(static_cast<const T*>(a.residual) + b * a.rs[0] + i * a.rs[1] + head * a.rs[2], words[1], single[1]);
+  float h[CH][V];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) floats(words[0][c], single[0][c], h[c]);
+  if (a.residual) {
+    T* out = static_cast<T*>(a.residual_out) + b * a.ros[0] + i * a.ros[1] + head * a.ros[2];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int at = c * a.per_row + t;
-#pragma unroll
-      for (int k = 0; k < V; ++k) h[c][k] += u[c][k];
+      float u[V];
+      floats(words[1][c], single[1][c], u);
+      add_v<V>(h[c], u);
       if (a.residual_out && live && at < a.chunks) store_v<V>(out + (long long)at * V, h[c]);
     }
   }
@@ -73,12 +145,7 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
   auto mean_square = [&](float f) -> float {         // of the row times f
     float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < V; ++k) v = fmaf(h[c][k] * f, h[c][k] * f, v);
-      sum += v;
-    }
+    for (int c = 0; c < CH; ++c) sum += squares<V>(h[c], f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -103,9 +170,7 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
   if (up < 1.f) inv *= up;                            // (1 / the root: 2^-128 at least)
   if (up > 1.f)                                       // (that may be more than fp32 holds)
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < V; ++k) h[c][k] *= up;
+    for (int c = 0; c < CH; ++c) scale_v<V>(h[c], up);
 
   const T* weight = static_cast<const T*>(a.weight);
   O* y = static_cast<O*>(a.y) + b * a.ys[0] + i * a.ys[1] + head * a.ys[2];
@@ -114,25 +179,30 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
   for (int c = 0; c < CH; ++c) {
     const int at = c * a.per_row + t;
     const bool on = live && at < a.chunks;
+    scale_v<V>(h[c], inv);
     if (weight && at < a.chunks) {
       float w[V];
       load_v<V>(weight + at * V, w);
-#pragma unroll
-      for (int k = 0; k < V; ++k) h[c][k] = h[c][k] * inv * (w[k] + a.weight_offset);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) h[c][k] *= inv;
+      weigh_v<V>(h[c], w, a.weight_offset);
     }
     if constexpr (sizeof(O) == 1) {                   // 32 / V lanes share an exponent
-      float mx = 0.f;
+      uint32_t top = 0u;                              // (magnitudes in the order of their bits)
 #pragma unroll
-      for (int k = 0; k < V; ++k) mx = fabsf(h[c][k]) < INFINITY ? fmaxf(mx, fabsf(h[c][k])) : mx;
+      for (int k = 0; k < V; ++k) top = max(top, __float_as_uint(h[c][k]) & 0x7fffffffu);
 #pragma unroll
-      for (int o = 1; o < KDTV_GROUP / V; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const int e = exponent_of(mx);
-      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+      for (int o = 1; o < KDTV_GROUP / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {        // the finite ones only
+        top = 0u;
 #pragma unroll
-      for (int k = 0; k < V; ++k) h[c][k] *= f;
+        for (int k = 0; k < V; ++k) {
+          const uint32_t bits = __float_as_uint(h[c][k]) & 0x7fffffffu;
+          top = max(top, bits < 0x7f800000u ? bits : 0u);
+        }
+#pragma unroll
+        for (int o = 1; o < KDTV_GROUP / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      const int e = exponent_of(__uint_as_float(top));
+      scale_v<V>(h[c], __uint_as_float((uint32_t)(127 - e) << 23));
       if (on && at % (KDTV_GROUP / V) == 0) scale[at / (KDTV_GROUP / V)] = (uint8_t)(e + 127);
     }
     if (on) store_v<V>(y + (long long)at * V, h[c]);
@@ -152,9 +222,12 @@ bool same(const long long (&s)[3], const long long (&t)[3]) { return s[0] == t[0
 template <typename T, typename O, int V>
 int launch_v(NormArgs& a, cudaStream_t st) {
   a.chunks = a.dim / V;
-  // Threads of a row: four chunks each (up to 32 where a chunk is one element), or one each where the rows are too few
-  // to fill the device.  (8000 rows of 8192 with the residual: 1, 2, 4, 8 chunks 106, 98, 79, 94 us.)
-  constexpr int most = V == 1 ? 32 : 4, some = V == 1 ? 8 : 4;
+  // Threads of a row: chunks each so that a thread has 128 bytes on their way (up to 32 where a chunk is one
+  // element), or one each where the rows are too few to fill the device.  (8192 elements a row: 8000 bf16 rows with the
+  // residual, to one byte, 2, 4, 8 chunks 103, 70, 76 us, without it -, 50, 58; 4000 fp32 rows, 2 and 4 chunks, with the
+  // residual 80 and 91, without it 56 and 46.)
+  constexpr int most = V == 1 ? 32 : 4;
+  const int some = V == 1 ? 8 : sizeof(T) == 4 && a.residual ? 2 : 4;
   const int least = sizeof(O) == 1 ? KDTV_GROUP / V : 1;       // lanes that share an exponent stay together
   const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
   int ch = a.rows <= 2u * sms ? 1 : some;
