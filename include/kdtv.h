@@ -580,7 +580,7 @@ int kdtv_project_launches_per_call(const kdtv_project_dims* dims);
 
 typedef struct kdtv_pages_dims {
   int32_t B, N;         /* requests (<= KDTV_MAX_POOL_REQUESTS); rows per request
-                           behind the prefix, >= 0                                 */
+                           behind the prefix, >= 0 (B * N <= 2^30)                 */
   int32_t page_size;    /* rows per page, > 0                                      */
   int32_t max_pages;    /* length of each page_table row                           */
   int32_t num_pages;    /* pages of the pool, length of free_pages                 */

@@ -254,7 +254,7 @@ extern "C" int kdtv_pages_resize(const kdtv_pages_dims* d, const int32_t* prefix
   if (!d || !prefix_len || !free_pages || !free_count || !n_pages || !page_table || !status) return KDTV_ERR_INVALID_ARG;
   if (d->B <= 0 || d->N < 0 || d->page_size <= 0 || d->max_pages <= 0 || d->num_pages <= 0) return KDTV_ERR_INVALID_ARG;
   if ((long long)d->max_pages * d->page_size > (1ll << 30)) return KDTV_ERR_INVALID_ARG;
-  if (d->B > KDTV_MAX_POOL_REQUESTS || (long long)d->B * d->N >= (1ll << 31) ||
+  if (d->B > KDTV_MAX_POOL_REQUESTS || (long long)d->B * d->N > (1ll << 30) ||
       (long long)d->B * d->max_pages >= (1ll << 31))          // 32-bit sums
     return KDTV_ERR_UNSUPPORTED;
   PageArgs a;

@@ -450,18 +450,20 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
     proj_low_simt_kernel<X, T, 8, 4><<<dim3((unsigned)((a.N + 7) / 8), (unsigned)a.B, (unsigned)((a.R + 3) / 4)), kThreads, 0, st>>>(a);
   const long long rows = (long long)a.B * a.N;
   if (cudaGetLastError() != cudaSuccess) return KDTV_ERR_CUDA;
-  // The tile, and how many CTAs share d_in (four steps each at least), with the least time by this reckoning: the SM
-  // with the most CTAs does its products at the tile's share of the fp32 rate (measured: 55, 43 and 28 %), a step takes
-  // some 500 cycles at least, and joining a cluster 3000.  Without tiles four rows take 7 weights a cycle of each SM, 4.5 where all of a block's warps
-  // share d_in and none the rows
-  // (measured with 8192 x 10240 and 4, 8, 12, 16, 24 rows: 71, 101, 139, 178, 261 us, the tiles 154 to 159 and 280; 4096 x
+  // The tile, and how many CTAs share d_in (four steps each at least), with the least time in cycles by this reckoning:
+  // the SM with the most CTAs does its products at the tile's share of the fp32 rate (measured: 55, 43 and 28 %), a step
+  // takes some 500 at least, a CTA as much besides, and joining a cluster 3000.  Without tiles four rows take 7 weights a
+  // cycle of each SM, 4.5 where all of a block's warps share d_in and none the rows, and four blocks 1000 besides.
+  // (Measured with 8192 x 10240 and 4, 8, 12, 16, 24 rows: 71, 101, 139, 178, 261 us, the tiles 154 to 159 and 280; 4096 x
   // 4096: 21, 31, 44, 57, 83, the tiles 41 to 43 and 61; 1001 x 515, 16 and 32 rows: 7.5 and 8.2, the tiles 14 and 23).
   struct Tile {
     int tm, tn, step, groups, percent;
   };
   const Tile tiles[3] = {{128, 64, 16, 1, 55}, {64, 64, 32, 1, 43}, {16, 32, 16, 8, 28}};
   int best = -1, split = 1;
-  double least = 2500.0 + (double)((rows + kFew - 1) / kFew) * a.M * a.K / ((few_slices(a, sms) == 8 ? 4.5 : 7.0) * sms);
+  const int slices = few_slices(a, sms);
+  const double fours = (double)((rows + kFew - 1) / kFew), blocks = fours * ((a.M + 32 / slices - 1) / (32 / slices));
+  double least = 2500.0 + fours * a.M * a.K / ((slices == 8 ? 4.5 : 7.0) * sms) + blocks / (4.0 * sms) * 1000.0;
   for (int k = 0; k < 3; ++k) {
     const Tile& e = tiles[k];
     const long long down = (rows + e.tm - 1) / e.tm, n = down * ((a.M + e.tn - 1) / e.tn);
@@ -471,7 +473,7 @@ int launch_simt(const ProjArgs& a, int sms, cudaStream_t st) {
       const int usable = s >= 4 && n * s <= 2 * sms ? sms * 8 / 9 : sms;     // (larger clusters leave SMs out)
       const double per = (double)((n * s + usable - 1) / usable), depth = (double)a.K / s;
       const double work = per * e.tm * e.tn * depth / (1.28 * e.percent), steps = depth / (e.step * e.groups) * 500.0;
-      const double time = (work > steps ? work : steps) + (s > 1 ? 3000.0 : 0.0);
+      const double time = (work > steps ? work : steps) + per * 500.0 + (s > 1 ? 3000.0 : 0.0);
       if (time < least) {
         least = time;
         best = k;

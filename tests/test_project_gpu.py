@@ -175,6 +175,12 @@ def test_few_rows_on_cuda_cores(dtype, flags, B, N, K, M, adapters):
         c.check(c.run(flags), flags, exact=True)
 
 
+@pytest.mark.parametrize("B,N,K,M", [(60000, 1, 3, 2), (300, 200, 5, 1), (2, 3000, 1, 7), (700, 9, 40, 33)])
+def test_many_small_rows_on_cuda_cores(B, N, K, M):
+    c = Case(B, N, K, M, "f32", 4, 2, seed=B, whole=True)
+    c.check(c.run(), exact=True)
+
+
 @pytest.mark.parametrize("K,rank,dtype", [(7, 16, "bf16"), (100, 16, "bf16"), (64, 3, "bf16"), (33, 5, "f32"), (1, 1, "f32"),
                                           (64, 12, "fp8"), (1001, 5, "f32")])
 def test_odd_sizes(K, rank, dtype):

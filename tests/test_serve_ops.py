@@ -110,7 +110,7 @@ def test_projection_workspace(L, fields):
 @pytest.mark.parametrize("fields,ptr,code", [
     (dict(B=0), {}, INVALID), (dict(N=-1), {}, INVALID), (dict(page_size=0), {}, INVALID), (dict(max_pages=0), {}, INVALID),
     (dict(num_pages=0), {}, INVALID), (dict(max_pages=1 << 26, page_size=64), {}, INVALID),
-    (dict(B=8193), {}, UNSUPPORTED), (dict(B=4096, N=1 << 20), {}, UNSUPPORTED),
+    (dict(B=8193), {}, UNSUPPORTED), (dict(B=4096, N=1 << 20), {}, UNSUPPORTED), (dict(B=1, N=(1 << 30) + 1), {}, UNSUPPORTED),
     (dict(B=8192, max_pages=1 << 18), {}, UNSUPPORTED),
 ] + [({}, {k: None}, INVALID) for k in ("prefix", "free", "count", "held", "table", "status")])
 def test_pages_refusals(L, fields, ptr, code):
