@@ -441,55 +441,62 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     int loads = 0, listed = -1;
     if (stall) alive = wait_warp(guard, BAR(B_STALL), 0);
     while (alive && next(a, sh, w, it)) {
-      if (it.k1 > a.base) {                    // the tile's adapters, once their units come
-        if (a.requests == 1) {
-          if (lane == 0) sh.ids[0] = (uint16_t)a.adapter[it.g];
-        } else if (listed != it.g) {
-          bool live;
-          group_bitmap(a, it.g, sh.bits, &live);
-          int before = 0;
-          for (int w0 = 0; w0 < (a.adapters + 31) / 32; w0 += 32) {
-            uint32_t m = w0 + lane < (a.adapters + 31) / 32 ? sh.bits[w0 + lane] : 0u;
-            int incl = __popc(m);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const int v = __shfl_up_sync(0xffffffffu, incl, o);
-              if (lane >= o) incl += v;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const int first = min(min(it.k1, max(it.k0, a.base)), it.k0 + a.stages);
+        const int from = part ? first : it.k0, to = part ? it.k1 : first;
+        if (from >= to) continue;
+        if (part && it.k1 > a.base) {          // the tile's adapters, while a ring full of d_in is on its way
+          if (a.requests == 1) {
+            if (lane == 0) sh.ids[0] = (uint16_t)a.adapter[it.g];
+          } else if (listed != it.g) {
+            bool live;
+            group_bitmap(a, it.g, sh.bits, &live);
+            int before = 0;
+            for (int w0 = 0; w0 < (a.adapters + 31) / 32; w0 += 32) {
+              uint32_t m = w0 + lane < (a.adapters + 31) / 32 ? sh.bits[w0 + lane] : 0u;
+              int incl = __popc(m);
+  #pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+              }
+              int at = before + incl - __popc(m);
+              for (; m; m &= m - 1) sh.ids[at++] = (uint16_t)((w0 + lane) * 32 + __ffs(m) - 1);
+              before += __shfl_sync(0xffffffffu, incl, 31);
             }
-            int at = before + incl - __popc(m);
-            for (; m; m &= m - 1) sh.ids[at++] = (uint16_t)((w0 + lane) * 32 + __ffs(m) - 1);
-            before += __shfl_sync(0xffffffffu, incl, 31);
+            listed = it.g;
           }
-          listed = it.g;
+          __syncwarp();
         }
+        if (lane == 0)
+          for (int k = from; alive && k < to; ++k) {
+            alive = wait_poll(guard, BAR(B_EMPTY + slot), phase ^ 1u);
+            if (!alive) break;
+            const uint32_t full = LEAD(B_FULL + slot), dst = ring + slot * stage_bytes;
+            const int f = (2 * it.f + rank) * kFeatures;
+            if (k < a.base) {
+              mbar_expect_tx_cluster(full, kWBytes + a.half_requests * a.half_rows * kUnitBytes);
+              tma_load_2d_pair(dst, &tm_w, full, k * (kOneByte ? 128 : 64), f);
+              tma_load_3d_pair(dst + kWBytes, &tm_x, full, k * (kOneByte ? 128 : 64), a.by_rows_of ? (2 * it.j + rank) * it.hr : 0,
+                               it.g * a.requests + (a.by_rows_of ? 0 : rank * a.half_requests));
+            } else {
+              if (!waited) grid_dep_wait();      // v is written
+              waited = true;
+              const int p = k - a.base, two = min(2, it.chunks - 2 * p);
+              mbar_expect_tx_cluster(full, two * (kFeatures * 32) + a.half_cols * 128);
+              for (int c = 2 * p; c < 2 * p + two; ++c) {
+                const int s = (int)divide(c, a.by_chunks);
+                tma_load_3d_pair(dst + (c & 1) * (kFeatures * 32), &tm_b, full, (c - s * a.chunks) * 16, f, sh.ids[s]);
+              }
+              tma_load_2d_pair(dst + kWBytes, &tm_v, full, 0,
+                               (int)((((long long)(it.g * a.blocks + it.j) * a.pairs + p) * 2 + rank) * (a.half_cols / 2)));
+            }
+            advance();
+            ++loads;
+          }
         __syncwarp();
       }
-      if (lane == 0)
-        for (int k = it.k0; k < it.k1; ++k) {
-          alive = wait_poll(guard, BAR(B_EMPTY + slot), phase ^ 1u);
-          if (!alive) break;
-          const uint32_t full = LEAD(B_FULL + slot), dst = ring + slot * stage_bytes;
-          const int f = (2 * it.f + rank) * kFeatures;
-          if (k < a.base) {
-            mbar_expect_tx_cluster(full, kWBytes + a.half_requests * a.half_rows * kUnitBytes);
-            tma_load_2d_pair(dst, &tm_w, full, k * (kOneByte ? 128 : 64), f);
-            tma_load_3d_pair(dst + kWBytes, &tm_x, full, k * (kOneByte ? 128 : 64), a.by_rows_of ? (2 * it.j + rank) * it.hr : 0,
-                             it.g * a.requests + (a.by_rows_of ? 0 : rank * a.half_requests));
-          } else {
-            if (!waited) grid_dep_wait();      // v is written
-            waited = true;
-            const int p = k - a.base, two = min(2, it.chunks - 2 * p);
-            mbar_expect_tx_cluster(full, two * (kFeatures * 32) + a.half_cols * 128);
-            for (int c = 2 * p; c < 2 * p + two; ++c) {
-              const int s = (int)divide(c, a.by_chunks);
-              tma_load_3d_pair(dst + (c & 1) * (kFeatures * 32), &tm_b, full, (c - s * a.chunks) * 16, f, sh.ids[s]);
-            }
-            tma_load_2d_pair(dst + kWBytes, &tm_v, full, 0,
-                             (int)((((long long)(it.g * a.blocks + it.j) * a.pairs + p) * 2 + rank) * (a.half_cols / 2)));
-          }
-          advance();
-          ++loads;
-        }
       alive = __shfl_sync(0xffffffffu, (int)alive, 0) != 0;
     }
     if (lane == 0)                             // every copy has landed, and is used up
@@ -658,7 +665,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           if (to >= 0 && f < a.M) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f) = v;
         }
       };
-      if constexpr (kOneByte) {                // read and rounded, then given back, then written
+      // One byte, another tile behind this one: the shared columns are read and rounded, then given back, then written.
+      // (Where none is, one copy of the code for all columns: it runs once, from a cold cache; 64 drafts of 8: @@ us.)
+      const bool more = w.tile < sh.total_tiles || w.u > w.u0;
+      if (kOneByte && more) {
         uint32_t p[kShared / 16][2][4];
         bool done[kShared / 16];
 #pragma unroll
@@ -672,7 +682,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           if (!done[k]) write(first0 + 16 * k, p[k]);
       }
 #pragma unroll 1
-      for (int c0 = rest0; c0 < rest1; c0 += 16) {
+      for (int c0 = more ? rest0 : 0; c0 < (more ? rest1 : cols); c0 += 16) {
         uint32_t p[2][4];
         if (!fetch(c0, p)) write(c0, p);
       }
