@@ -232,6 +232,20 @@ __device__ __forceinline__ bool all_of(int id, bool ok) {
   return r != 0u;
 }
 
+// Sixteen exponent bytes of a row that is not 16-byte aligned.  (By itself: nine copies of it made the first loads, whose
+// code comes from a cold cache, us later.)
+__device__ __noinline__ uint4 exponent_window(const uint8_t* row, int at, int bytes, const uint8_t* end, int mode) {
+  uint32_t x[4] = {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
+  if (mode == 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + 4 * k < bytes) x[k] = *reinterpret_cast<const uint32_t*>(row + at + 4 * k);
+  } else {
+    exponent_words(row, at, bytes, end, x);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 // 16 tokens' 32 outputs from shared memory, an output a lane: rows of y that are not 16-byte aligned.  (By itself, so
 // that the aligned rows' code stays short: inlined it cost 64 drafts of 8 two us of 52.)
 __device__ __noinline__ void write_narrow(uint32_t rows, const long long* y_at, unsigned short* y, bool on) {
@@ -666,7 +680,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         }
       };
       // One byte, another tile behind this one: the shared columns are read and rounded, then given back, then written.
-      // (Where none is, one copy of the code for all columns: it runs once, from a cold cache; 64 drafts of 8: @@ us.)
+      // (Where none is, one copy of the code for all columns: it runs once, from a cold cache; 64 drafts of 8: 3.3 us.)
       const bool more = w.tile < sh.total_tiles || w.u > w.u0;
       if (kOneByte && more) {
         uint32_t p[kShared / 16][2][4];
@@ -695,18 +709,9 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     const uint8_t* const x_end = a.x_scale + (long long)a.B * a.N * row_bytes;
     const uint8_t* const w_end = a.W_scale + (long long)a.M * row_bytes;
     auto bytes = [&](const uint8_t* row, int u, const uint8_t* end) -> uint4 {      // of window u
-      uint32_t x[4] = {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
-      if (row && 4 * u < a.base) {
-        if (a.scale_mode == 2) return *reinterpret_cast<const uint4*>(row + 16 * u);
-        if (a.scale_mode == 1) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (16 * u + 4 * k < row_bytes) x[k] = *reinterpret_cast<const uint32_t*>(row + 16 * u + 4 * k);
-        } else {
-          exponent_words(row, 16 * u, row_bytes, end, x);
-        }
-      }
-      return make_uint4(x[0], x[1], x[2], x[3]);
+      if (!row || 4 * u >= a.base) return make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+      if (a.scale_mode == 2) return *reinterpret_cast<const uint4*>(row + 16 * u);
+      return exponent_window(row, 16 * u, row_bytes, end, a.scale_mode);
     };
     auto sts32 = [](uint32_t to, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(to), "r"(v) : "memory"); };
     const uint32_t at = (t & 31) * 16 + (t >> 5) * 4;
