@@ -3,7 +3,7 @@
 //
 // Mathematics.  y = W x + Bm_a (s_a A_a x), a the request's adapter.  Outputs are
 // the rows (TMEM lanes) of a product, tokens its columns: D[f, t] = sum_k W[f, k]
-// x[t, k], so that one token costs a 16-column product, not a 128-row one.  The
+// x[t, k], so that one token costs a 32-column product, not a 256-row one.  The
 // adapters are more of the same sum: with the adapters of a tile's requests
 // side by side, [W | Bm_0 | Bm_1 ..] [x ; v_0 ; v_1 ..], where v_a = s_a A_a x for the
 // tokens of adapter a and 0 for the others.  v is fp32, split into two bf16 parts
@@ -11,18 +11,27 @@
 // one adapter's values into another's tokens: an output that is not finite, in a
 // tile with several adapters, is computed again on its own.
 //
-// Kernels: proj_low_kernel (v of all tokens, in the tiles' order, as the second
-// kernel's operands lie in shared memory) and proj_tc_kernel (everything else),
-// launched while the first runs; only the adapters' units wait for it.
+// Kernels: one of kdtv_proj_low.cu (v of all tokens, in the tiles' order, as the
+// second kernel's operands lie in shared memory), proj_tc_kernel (everything else),
+// launched while the first runs, of which only the adapters' units wait for it, and
+// proj_combine_kernel for tiles that were cut.
 //
 // Work.  A unit is 128 bytes of d_in (64 bf16, 128 one-byte elements) or two
-// chunks of 16 ranks, for one tile of 256 outputs and up to 256 tokens.  A pair of CTAs works on a tile: each has 128 outputs, loads those rows
-// of W and half of the tokens, and the products read both halves (cta_group::2), so
-// that a unit costs each SM 32 KiB where a CTA by itself with as many products
-// would load 48.  Whole tiles go round the pairs; what does not fill a round is
-// cut evenly by units.  A tile
-// that several pairs share: each leaves its sums, and proj_combine_kernel adds them in
-// the order of the units.
+// chunks of 16 ranks, for one tile of 256 outputs and up to 256 tokens.  A pair of
+// CTAs works on a tile: each has 128 outputs, loads those rows of W and half of the
+// tokens, and the products read both halves (cta_group::2), so that a unit costs
+// each SM 32 KiB where a CTA by itself with as many products would load 48 (prompts
+// 595 us with single CTAs, 403 with pairs and whole tiles first).  Whole tiles go
+// round the pairs; what does not fill a round is cut evenly by units, where that is
+// sooner done.  A tile that several pairs share: each leaves its sums, and
+// proj_combine_kernel adds them in the order of the units.
+//
+// Bound by the tensor cores for prompts (4 x up to 2000 rows, 4096 x 12288, rank 64:
+// 367 us, 1610 TFLOP/s; one byte, 8192 rows, 8192 x 8192: 422 us, 2610), by
+// DRAM and some 12 us of ways in and out for few tokens (one, 8192 x 10240: 38.8 us;
+// twice the outputs 64, four times 111).  Of those 12: 2.5 to plan, 1 to the first
+// load and 1 until it is there, 1.5 to write, 3 to join, the rest launches; code that
+// runs once comes from a cold cache, so what every call passes through is kept short.
 //
 // One byte: exponent bytes travel as they are to the tensor cores, which take
 // one per 32 elements and operand row (block-scaled products), so sums are in true

@@ -203,6 +203,21 @@ def test_strided_rows(dtype, flags, xpad, ypad, off):
     assert (out[..., :off] == 5.0).all() and (out[..., off + 72:] == 5.0).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("over", ["requests", "rows", "windows"])
+def test_rows_that_share_memory(dtype, over):
+    """One request's rows for all, one row for all of a request, and rows that overlap."""
+    B, N, K = 5, 6, 64
+    c = Case(B, N, K, 96, dtype, 3, 16, seed=8)
+    if over == "windows":                     # row i of request b starts 8 elements behind the one before
+        base = c.x.reshape(-1)[:8 * B * N + K]
+        c.x = base.as_strided((B, N, K), (8 * N, 8, 1))
+    else:
+        c.x = c.x[:1].expand(B, N, K) if over == "requests" else c.x[:, :1].expand(B, N, K)
+    c.x64 = f64(c.x)
+    c.check(c.run(), flags=0 if over == "windows" else SIMT)          # (a stride of 0 runs on CUDA cores)
+
+
 @pytest.mark.parametrize("dtype,flags", PATHS)
 def test_permuted_requests(dtype, flags):
     """x [N, B, K] seen as [B, N, K], and requests in a buffer with gaps."""
