@@ -105,18 +105,23 @@ __device__ __forceinline__ void low_zeros(const ProjArgs& a, const Low& w, int i
 }
 // A lane's sums of 16 ranks from rank0 on and 8 tokens from row t0 on, in two parts (16 significant bits).
 __device__ __forceinline__ void low_store(const ProjArgs& a, const Low& w, const float (&acc)[4], int rank0, int t0) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, c = rank0 >> 4;       // (rank0 is a multiple of 16)
+  if (c >= a.chunks) return;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float v = w.s * acc[k];
-    const int rank = rank0 + (lane >> 2) + (k >> 1) * 8, i = t0 + 2 * (lane & 3) + (k & 1), c = rank >> 4;
-    if (i >= w.n || c >= a.chunks) continue;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-    const float left = v - __bfloat162float(hi);           // exact; not a number where v is not finite
-    const int h = (rank >> 3) & 1, at = (rank & 7) * 2;
-    *reinterpret_cast<__nv_bfloat16*>(low_place(a, w, i, w.first + c, 0, h) + at) = hi;
-    *reinterpret_cast<__nv_bfloat16*>(low_place(a, w, i, w.first + c, 1, h) + at) =
-        __float2bfloat16_rn(fabsf(left) < INFINITY ? left : 0.f);
+  for (int e = 0; e < 2; ++e) {
+    const int i = t0 + 2 * (lane & 3) + e;
+    if (i >= w.n) continue;
+    int flip;
+    char* const row = part_row(a, w.b, i, w.hr, w.first + c, 0, &flip) + (lane >> 2) * 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float v = w.s * acc[2 * h + e];
+      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+      const float left = v - __bfloat162float(hi);         // exact; not a number where v is not finite
+      char* const at = row + ((h ^ flip) << 4);
+      *reinterpret_cast<__nv_bfloat16*>(at) = hi;
+      *reinterpret_cast<__nv_bfloat16*>(at + (long long)a.half_cols * 32) = __float2bfloat16_rn(fabsf(left) < INFINITY ? left : 0.f);
+    }
   }
 }
 // The sums of a cluster's blocks to its first one, in their order.
@@ -357,10 +362,10 @@ proj_low_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
   }
 }
 
-// d_in over as many blocks of a cluster as keep the grid within `most`, 512 elements each at least.
-int split_of(const ProjArgs& a, long long blocks, long long most) {
+// d_in over as many blocks of a cluster, `cap` at most, as keep the grid within `most`, 512 elements each at least.
+int split_of(const ProjArgs& a, long long blocks, long long most, int cap) {
   int split = 1;
-  while (split < 8 && blocks * split * 2 <= most && a.K / (2 * split) >= 512) split *= 2;
+  while (split < cap && blocks * split * 2 <= most && a.K / (2 * split) >= 512) split *= 2;
   return split;
 }
 
@@ -398,7 +403,10 @@ cudaError_t launch_rows(const ProjArgs& a, int sms, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int blocks = (a.N + kRows - 1) / kRows, rank_blocks = (a.R + ranks - 1) / ranks;
   const long long all = (long long)blocks * rank_blocks * a.B;
-  const int split = split_of(a, all, 2 * sms);
+  // (8000 rows of 4096, 64 ranks, a call with 256 outputs: 128 blocks 64 us, twice as many that share d_in 69; 1003 rows of
+  // 6656, one byte: four share d_in 35 us, eight 36.)  Where some of the rows may not be live, long sums are shared more:
+  // (4 x up to 2000 rows of 4096, half of them live, 12288 outputs: 378 and 367 us.)
+  const int split = split_of(a, all, a.n_live && a.base >= 32 ? 2 * sms : sms, 4);
   // one block an SM: a deep ring; more: two of them
   int stages = (all * split <= sms ? 190 : 92) * 1024 / stage;
   stages = stages < kRowStages ? stages : kRowStages;
@@ -413,7 +421,7 @@ cudaError_t launch_rows(const ProjArgs& a, int sms, cudaStream_t st) {
 template <bool kOneByte>
 cudaError_t launch_t(const ProjArgs& a, int sms, cudaStream_t st) {
   if (a.N <= kFew) {
-    const int ranks = (a.R + 15) / 16, split = split_of(a, (long long)ranks * a.B, sms);
+    const int ranks = (a.R + 15) / 16, split = split_of(a, (long long)ranks * a.B, sms, 8);
     return launch_split(proj_low_few_kernel<kOneByte>, dim3((unsigned)split, (unsigned)ranks, (unsigned)a.B), 32 * kWays, 0, split, st, a, split);
   }
   if (a.R <= 16) return launch_rows<kOneByte, 1, 1>(a, sms, st);
