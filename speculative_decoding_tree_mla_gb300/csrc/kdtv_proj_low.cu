@@ -321,27 +321,29 @@ proj_low_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
       }
       if (!wait_warp(guard, full + 8 * slot, phase)) break;
       const uint32_t xs = ring + slot * kStage, as = xs + kXBytes;
+      // 32 elements a step: lane q's are 16 q + 8 (step % 2) .. + 7 of 64, every other 16 bytes of A's rows, so that two rows'
+      // lie in different banks (with 8 q .. + 7 of 32 every read took twice as long).
+      uint4 both[NT];                          // one byte: two steps' elements of x
 #pragma unroll
       for (int step = 0; step < kElems / 32; ++step) {
+        const int h = step & 1, box = step >> 1;
         uint4 x[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int row = (wt * NT + j) * 8 + g;
           if constexpr (kOneByte) {
-            uint2 v;
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y)
-                         : "r"(xs + row * 128 + (((2 * step + (q >> 1)) ^ (row & 7)) << 4) + (q & 1) * 8) : "memory");
-            x[j] = widen8(v, (now[j] >> (8 * step)) & 0xffu);
+            if (h == 0) both[j] = lds(xs, row, 4 * box + q);
+            x[j] = widen8(h ? make_uint2(both[j].z, both[j].w) : make_uint2(both[j].x, both[j].y),
+                          (now[j] >> (8 * (2 * box + (q >> 1)))) & 0xffu);
           } else {
-            x[j] = lds(xs, row, 4 * step + q);
+            x[j] = lds(xs, row, 2 * q + h);
           }
         }
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
           const int row = (wr * MR + m) * 16 + g;
-          const uint32_t at = as + (step >> 1) * kABytes * (kBoxes - 1);
-          const int chunk = kOneByte ? 4 * (step & 1) + q : 4 * step + q;
-          const uint4 lo = lds(at, row, chunk), hi = lds(at, row + 8, chunk);
+          const uint32_t at = as + box * kABytes;          // (bf16: one box)
+          const uint4 lo = lds(at, row, 2 * q + h), hi = lds(at, row + 8, 2 * q + h);
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma_32(reinterpret_cast<float(&)[4]>(acc[(m * NT + j) * 4]), lo, hi, x[j]);
         }
