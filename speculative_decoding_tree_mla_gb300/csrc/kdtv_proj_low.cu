@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(32 * kWays, 3) proj_low_few_kernel(const __gri
 // multiply all of a stage.  `split` blocks of a cluster share d_in.  Its blocks take an SM
 // for themselves and the projection's follow them: loads from global memory
 // to registers, beside the projection, took 57 us for 6000 rows of 4096 and
-// 64 ranks, where this takes 43 by itself from a cold cache and leaves x in L2.
-// Bound by DRAM (x) and, with many ranks, by the SMs' loads (A once per 64 rows).
+// 64 ranks, where this takes 32 by itself from a cold cache and leaves x in L2.
+// Bound by the reads of shared memory (48 KiB for each 16 that land, with 64 ranks).
 constexpr int kRows = 64, kRowStages = 12;
 
 template <bool kOneByte, int WR, int MR>
@@ -407,7 +407,7 @@ cudaError_t launch_rows(const ProjArgs& a, int sms, cudaStream_t st) {
   const long long all = (long long)blocks * rank_blocks * a.B;
   // (8000 rows of 4096, 64 ranks, a call with 256 outputs: 128 blocks 64 us, twice as many that share d_in 69; 1003 rows of
   // 6656, one byte: four share d_in 35 us, eight 36.)  Where some of the rows may not be live, long sums are shared more:
-  // (4 x up to 2000 rows of 4096, half of them live, 12288 outputs: 378 and 367 us.)
+  // (4 x up to 2000 rows of 4096, half of them live, 12288 outputs: 378 us, 367 with that.)
   const int split = split_of(a, all, a.n_live && a.base >= 32 ? 2 * sms : sms, 4);
   // one block an SM: a deep ring; more: two of them
   int stages = (all * split <= sms ? 190 : 92) * 1024 / stage;
