@@ -479,7 +479,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             for (int w0 = 0; w0 < (a.adapters + 31) / 32; w0 += 32) {
               uint32_t m = w0 + lane < (a.adapters + 31) / 32 ? sh.bits[w0 + lane] : 0u;
               int incl = __popc(m);
-  #pragma unroll
+#pragma unroll
               for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
