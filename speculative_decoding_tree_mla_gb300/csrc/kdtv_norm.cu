@@ -37,6 +37,18 @@ __device__ __forceinline__ void add_v(float (&x)[V], const float (&y)[V]) {
     }
   }
 }
+// Eight elements to their 16-byte words (exact: they come from there).
+template <typename T>
+__device__ __forceinline__ void pack8(const float (&x)[8], uint4* w) {
+  if constexpr (sizeof(T) == 2) {
+    auto two = [](float lo, float hi) { return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u); };
+    w[0] = make_uint4(two(x[0], x[1]), two(x[2], x[3]), two(x[4], x[5]), two(x[6], x[7]));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = make_uint4(__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]), __float_as_uint(x[4 * h + 2]), __float_as_uint(x[4 * h + 3]));
+  }
+}
 template <int V>
 __device__ __forceinline__ void scale_v(float (&x)[V], float f) {
   if constexpr (V == 1) {
@@ -91,7 +103,9 @@ __device__ __forceinline__ float squares(const float (&x)[V], float f) {
 // the latency of one load, one reduction and one store (one row 3.3 us).
 // The statistics are fp32; y is (h * (1 / sqrt(mean + eps))) * w, each step
 // rounded to fp32, and rounded once more to its type.
-template <typename T, typename O, int V, int CH>
+// kShifted: rows that start anywhere, all of a row's tensors at the same distance behind a multiple of 16 bytes: the
+// chunks are those of memory, of which the first and the last may lie in the row in part.
+template <typename T, typename O, int V, int CH, bool kShifted = false>
 __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   const int row_in = threadIdx.x / a.per_row, t = threadIdx.x - row_in * a.per_row;
   const unsigned r = blockIdx.x * (unsigned)a.rows_block + row_in;
@@ -99,6 +113,12 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
   const unsigned b = divide(bi, a.by_N), i = bi - b * a.N;
   const bool live = r < a.rows && (int)i < live_rows(a.n_live, b, a.N);
 
+  static_assert(!kShifted || (V == 8 && sizeof(O) == sizeof(T)), "whole chunks");
+  const T* const xrow = static_cast<const T*>(a.x) + b * a.xs[0] + i * a.xs[1] + head * a.xs[2];
+  // Elements of chunk 0 before the row; a chunk's first element; whether all of it, or of its element k, lies in the row.
+  const int off = kShifted ? (int)(reinterpret_cast<uintptr_t>(xrow) % 16 / sizeof(T)) : 0;
+  auto whole = [&](int at) { return !kShifted || (at * V >= off && at * V - off + V <= a.dim); };
+  auto within = [&](int at, int k) { return (unsigned)(at * V - off + k) < (unsigned)a.dim; };
   // (as they lie in memory until all of them are there: half the registers)
   constexpr int kWords = V == 8 ? (int)sizeof(T) / 2 : 1;
   uint4 words[2][CH][kWords];
@@ -112,8 +132,16 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
       for (int k = 0; k < kWords; ++k) w[c][k] = make_uint4(0u, 0u, 0u, 0u);
       if (!live || at >= a.chunks) continue;
       if constexpr (V == 8) {
+        const T* const q = p + ((long long)at * V - off);
+        if (whole(at)) {
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) w[c][k] = reinterpret_cast<const uint4*>(p + (long long)at * V)[k];
+          for (int k = 0; k < kWords; ++k) w[c][k] = reinterpret_cast<const uint4*>(q)[k];
+        } else {
+          float v[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[k] = within(at, k) ? to_f32(q[k]) : 0.f;
+          pack8<T>(v, w[c]);
+        }
       } else {
         s[c] = to_f32(p[at]);
       }
@@ -123,8 +151,19 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
     if constexpr (V == 8) unpack8<T>(w, x);
     else x[0] = s;
   };
-  load(static_cast<const T*>(a.x) + b * a.xs[0] + i * a.xs[1] + head * a.xs[2], words[0], single[0]);
+  load(xrow, words[0], single[0]);
   if (a.residual) load(static_cast<const T*>(a.residual) + b * a.rs[0] + i * a.rs[1] + head * a.rs[2], words[1], single[1]);
+  auto store = [&](auto* p, int at, const float (&x)[V]) {
+    if (whole(at)) {
+      store_v<V>(p + ((long long)at * V - off), x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float one[1] = {x[k]};
+        if (within(at, k)) store_v<1>(p + ((long long)at * V - off + k), one);
+      }
+    }
+  };
   float h[CH][V];
 #pragma unroll
   for (int c = 0; c < CH; ++c) floats(words[0][c], single[0][c], h[c]);
@@ -136,7 +175,7 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
       float u[V];
       floats(words[1][c], single[1][c], u);
       add_v<V>(h[c], u);
-      if (a.residual_out && live && at < a.chunks) store_v<V>(out + (long long)at * V, h[c]);
+      if (a.residual_out && live && at < a.chunks) store(out, at, h[c]);
     }
   }
 
@@ -182,7 +221,12 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
     scale_v<V>(h[c], inv);
     if (weight && at < a.chunks) {
       float w[V];
-      load_v<V>(weight + at * V, w);
+      if constexpr (kShifted) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) w[k] = within(at, k) ? to_f32(weight[at * V - off + k]) : 0.f;
+      } else {
+        load_v<V>(weight + at * V, w);
+      }
       weigh_v<V>(h[c], w, a.weight_offset);
     }
     if constexpr (sizeof(O) == 1) {                   // 32 / V lanes share an exponent
@@ -205,7 +249,7 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
       scale_v<V>(h[c], __uint_as_float((uint32_t)(127 - e) << 23));
       if (on && at % (KDTV_GROUP / V) == 0) scale[at / (KDTV_GROUP / V)] = (uint8_t)(e + 127);
     }
-    if (on) store_v<V>(y + (long long)at * V, h[c]);
+    if (on) store(y, at, h[c]);
   }
 }
 
@@ -219,9 +263,9 @@ void strides(const int64_t (&in)[3], long long N, long long H, long long dim, lo
 }
 bool same(const long long (&s)[3], const long long (&t)[3]) { return s[0] == t[0] && s[1] == t[1] && s[2] == t[2]; }
 
-template <typename T, typename O, int V>
+template <typename T, typename O, int V, bool kShifted = false>
 int launch_v(NormArgs& a, cudaStream_t st) {
-  a.chunks = a.dim / V;
+  a.chunks = kShifted ? (a.dim + 16 / (int)sizeof(T) - 1 + V - 1) / V : a.dim / V;
   // Threads of a row: chunks each so that a thread has 128 bytes on their way (up to 32 where a chunk is one
   // element), or one each where the rows are too few to fill the device.  (8192 elements a row: 8000 bf16 rows with the
   // residual, to one byte, 2, 4, 8 chunks 103, 70, 76 us, without it -, 50, 58; 4000 fp32 rows, 2 and 4 chunks, with the
@@ -253,7 +297,8 @@ int launch_v(NormArgs& a, cudaStream_t st) {
   if constexpr (V == 1) {
     return ch <= 1 ? go(rmsnorm_kernel<T, O, 1, 1>) : ch <= 8 ? go(rmsnorm_kernel<T, O, 1, 8>) : go(rmsnorm_kernel<T, O, 1, 32>);
   } else {
-    return ch == 1 ? go(rmsnorm_kernel<T, O, V, 1>) : ch == 2 ? go(rmsnorm_kernel<T, O, V, 2>) : go(rmsnorm_kernel<T, O, V, 4>);
+    return ch == 1 ? go(rmsnorm_kernel<T, O, V, 1, kShifted>)
+                   : ch == 2 ? go(rmsnorm_kernel<T, O, V, 2, kShifted>) : go(rmsnorm_kernel<T, O, V, 4, kShifted>);
   }
 }
 
@@ -265,7 +310,21 @@ int launch(NormArgs& a, cudaStream_t st) {
                    aligned(a.weight, 16) && aligned(a.y, sizeof(O) == 1 ? 8 : 16) && multiple(a.xs, v) &&
                    (!a.residual || multiple(a.rs, v)) && (!a.residual_out || multiple(a.ros, v)) &&
                    multiple(a.ys, sizeof(O) == 1 ? 8 : v);
-  return vec ? launch_v<T, O, 8>(a, st) : launch_v<T, O, 1>(a, st);
+  if (vec) return launch_v<T, O, 8>(a, st);
+  // Rows that start anywhere, the same distance behind 16 bytes in all tensors (8000 bf16 rows of 8190 with the residual 112 us,
+  // element by element 253; 7134 of 4365 56 and 107; 12000 of 101 7.6 and 6.8).
+  if constexpr (sizeof(O) == sizeof(T)) {
+    auto together = [&](const void* p, const long long (&s)[3]) {
+      if (!p) return true;
+      bool ok = (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(a.x)) % 16 == 0;
+      for (int k = 0; k < 3; ++k) ok = ok && (s[k] - a.xs[k]) % v == 0;
+      return ok;
+    };
+    if (a.dim >= 256 && reinterpret_cast<uintptr_t>(a.x) % sizeof(T) == 0 && together(a.residual, a.rs) &&
+        together(a.residual_out, a.ros) && together(a.y, a.ys) && a.dim <= 32768 - 16)
+      return launch_v<T, O, 8, true>(a, st);
+  }
+  return launch_v<T, O, 1>(a, st);
 }
 
 }  // namespace

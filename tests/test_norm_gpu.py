@@ -122,6 +122,42 @@ def test_strides_and_live_rows(one_byte):
             assert (scale[b, m:] == 78).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,pad,off", [(64, 1, 0), (65, 0, 0), (66, 3, 5), (100, 7, 3), (333, 0, 0), (858, 0, 2), (4365, 4, 1),
+                                         (8191, 2, 7), (16383, 0, 0), (32750, 1, 1), (72, 9, 4)])
+def test_rows_that_start_anywhere(dtype, dim, pad, off):
+    """All of a row's tensors the same distance behind 16 bytes (or not: the last run); what lies beside the rows stays."""
+    B, N = 3, (200 if dim < 1000 else 7)
+
+    def part(seed, shift=off):
+        wide = make((B * N * (dim + pad) + 64,), dtype, seed)
+        return wide, wide[shift:].as_strided((B, N, dim), (N * (dim + pad), dim + pad, 1))
+
+    w = make((dim,), dtype, 43)
+    n = torch.tensor([N, 3, 0], dtype=torch.int32, device="cuda")
+    for shifts in ((off,) * 4, (off, off + 1, off, off + 2)):
+        (_, x), (rw, r), (kw, kept), (ow, out) = (part(40 + k, s) for k, s in enumerate(shifts))
+        before = rw.clone(), kw.clone(), ow.clone()
+        y, h = O.rmsnorm(f64(x), f64(w), 1e-6, f64(r))
+        kdtv.rmsnorm(x, w, residual=r, residual_out=kept, out=out, n_live=n)
+        for b, m in enumerate((N, 3, 0)):
+            near(f64(out[b, :m]), y[b, :m], ARITH + STEP[dtype])
+            near(f64(kept[b, :m]), h[b, :m], STEP[dtype])
+        assert torch.equal(rw, before[0])
+        for wide, was, t in ((kw, before[1], kept), (ow, before[2], out)):
+            for b, m in enumerate((N, 3, 0)):
+                t[b, :m] = 0
+            s = shifts[2] if t is kept else shifts[3]
+            mine = was[s:].as_strided((B, N, dim), (N * (dim + pad), dim + pad, 1))
+            for b, m in enumerate((N, 3, 0)):
+                mine[b, :m] = 0
+            assert torch.equal(wide, was)
+    _, x = part(44)
+    y, _ = O.rmsnorm(f64(x), f64(w), 1e-6)
+    kdtv.rmsnorm(x, w, out=x)                                  # in place
+    near(f64(x), y, ARITH + STEP[dtype])
+
+
 @pytest.mark.parametrize("dim", [64, 1000, 8192])
 def test_in_place(dim):
     for where in ("x", "residual"):
