@@ -124,8 +124,8 @@ __device__ __forceinline__ float squares(const float (&x)[V], float f) {
 // block; a thread has CH chunks of V elements, per_row chunks apart, so that
 // a warp's accesses are whole lines.
 // Bound by DRAM where there are rows enough (8000 bf16 rows of 8192 with the
-// residual, to one byte: 70 us, 6530 GB/s; before its arithmetic took two
-// elements an instruction and its loads waited as they lie in memory, 82), else by
+// residual 78 us, 6710 GB/s, to one byte 74, 6200; before its arithmetic took two
+// elements an instruction and its loads waited as they lie in memory, 81 and 82), else by
 // the latency of one load, one reduction and one store (one row 3.3 us).
 // The statistics are fp32; y is (h * (1 / sqrt(mean + eps))) * w, each step
 // rounded to fp32, and rounded once more to its type.
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
   }
   float inv = 1.f / sqrtf(mean), left = 0.f;
   // One byte: what the root's reciprocal lost, by a step of Newton's method.  (Values near the middle between two codes
-  // are told apart as well as fp32 sums allow: 298 of 441 million codes were not the nearest without it, 220 with, for 6 of 104 us.)
+  // are told apart as well as fp32 sums allow: without this and the products' 298 of 441 million codes were not the
+  // nearest, 220 with them, for 6 of 105 us.)
   if (sizeof(O) == 1 && mean < INFINITY && inv < INFINITY) {
     const float p = mean * inv;
     left = -0.5f * inv * fmaf(fmaf(mean, inv, -p), inv, fmaf(p, inv, -1.f));
@@ -311,7 +312,7 @@ int launch_v(NormArgs& a, cudaStream_t st) {
   a.chunks = kShifted ? (a.dim + 16 / (int)sizeof(T) - 1 + V - 1) / V : a.dim / V;
   // Threads of a row: chunks each so that a thread has 128 bytes on their way (up to 32 where a chunk is one
   // element), or one each where the rows are too few to fill the device.  (8192 elements a row: 8000 bf16 rows with the
-  // residual, to one byte, 2, 4, 8 chunks 103, 70, 76 us, without it -, 50, 58; 4000 fp32 rows, 2 and 4 chunks, with the
+  // residual, to one byte, 2, 4, 8 chunks 103, 70, 76 us when products were rounded as they came, without it -, 50, 58; 4000 fp32 rows, 2 and 4 chunks, with the
   // residual 80 and 91, without it 56 and 46.)
   constexpr int most = V == 1 ? 32 : 4;
   const int some = V == 1 ? 8 : sizeof(T) == 4 && a.residual ? 2 : 4;
