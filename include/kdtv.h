@@ -533,7 +533,8 @@ typedef struct kdtv_project_dims {
   int32_t rank;         /* of every adapter (lower ones padded with zeros), 1..256 */
   uint32_t flags;       /* KDTV_FLAG_SIMT, KDTV_FLAG_TEST_STALL                    */
   int64_t x_stride[2];  /* elements between requests and rows ({0, 0}: contiguous; */
-  int64_t y_stride[2];  /* one-byte x: contiguous)                                 */
+  int64_t y_stride[2];  /* one-byte x: contiguous; of a dimension of one element:
+                           any)                                                    */
   void* workspace;      /* >= kdtv_project_workspace_size() bytes, 256-byte aligned */
   size_t workspace_bytes;
 } kdtv_project_dims;

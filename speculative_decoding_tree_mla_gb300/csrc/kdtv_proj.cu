@@ -555,8 +555,9 @@ extern "C" int kdtv_project(const kdtv_project_dims* d, const void* x, const uin
   const bool one_byte = d->dtype == KDTV_BF16_FP8KV;
   if (one_byte != (x_scale != nullptr) || one_byte != (W_scale != nullptr)) return KDTV_ERR_INVALID_ARG;
   if ((A != nullptr) != (Bm != nullptr) || (adapter && !A) || (A && d->adapters == 0)) return KDTV_ERR_INVALID_ARG;
+  // (strides of dimensions of one element mean nothing, here and below)
   if (one_byte && (d->x_stride[0] || d->x_stride[1]) &&
-      (d->x_stride[0] != (int64_t)d->N * d->d_in || d->x_stride[1] != d->d_in))
+      ((d->B > 1 && d->x_stride[0] != (int64_t)d->N * d->d_in) || (d->N > 1 && d->x_stride[1] != d->d_in)))
     return KDTV_ERR_INVALID_ARG;
   if ((d->y_stride[0] || d->y_stride[1]) && ((d->B > 1 && !d->y_stride[0]) || (d->N > 1 && !d->y_stride[1])))
     return KDTV_ERR_INVALID_ARG;                            // rows over one another
@@ -569,11 +570,13 @@ extern "C" int kdtv_project(const kdtv_project_dims* d, const void* x, const uin
   a.x = x; a.W = W; a.A = A; a.Bm = Bm; a.x_scale = x_scale; a.W_scale = W_scale;
   a.adapter_scale = adapter_scale; a.adapter = adapter; a.n_live = n_live;
   a.y = y; a.status = status;
-  const bool gx = d->x_stride[0] || d->x_stride[1], gy = d->y_stride[0] || d->y_stride[1];
-  a.xs[0] = gx ? d->x_stride[0] : (long long)d->N * d->d_in;
-  a.xs[1] = gx ? d->x_stride[1] : d->d_in;
-  a.ys[0] = gy ? d->y_stride[0] : (long long)d->N * d->d_out;
-  a.ys[1] = gy ? d->y_stride[1] : d->d_out;
+  auto strides = [&](const int64_t (&in)[2], long long width, long long (&out)[2]) {
+    const bool given = in[0] || in[1];
+    out[0] = d->B > 1 ? (given ? in[0] : d->N * width) : 0;
+    out[1] = d->N > 1 ? (given ? in[1] : width) : 0;
+  };
+  strides(d->x_stride, d->d_in, a.xs);
+  strides(d->y_stride, d->d_out, a.ys);
   a.by_N = divisor((unsigned)d->N);
   a.low = static_cast<float*>(d->workspace);
   const int sms = sm_count();

@@ -348,3 +348,37 @@ def test_python_refusals():
                      Bm=torch.zeros(1, 40, 300, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError):
         kdtv.quantise_weight(c.W[:, :33])
+
+
+@pytest.mark.parametrize("flags", [0, SIMT])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("part", ["first rows", "last row", "one row each", "one request"])
+def test_strides_of_single_rows_and_requests(dtype, flags, part):
+    """x and out where B or N is 1, as parts of larger buffers: what stands beside a dimension of one element, whatever
+    its stride, does not matter (one byte: contiguous but for that)."""
+    whole = Case(1, 6, 64, 40, dtype, 2, 16, seed=13, whole=True, ids=[1])
+    scale = whole.kw.get("x_scale")
+    c = Case(*{"first rows": (1, 4), "last row": (1, 1), "one row each": (6, 1), "one request": (1, 6)}[part], 64, 40, dtype, 2, 16,
+             seed=14, whole=True)
+
+    def inside(t):
+        wide = t.new_zeros((2, 8, t.shape[2]))
+        wide[1, 1:7] = t[0]
+        return wide[1:, 1:7]
+
+    cut = {"first rows": lambda t: t[:, :4], "last row": lambda t: t[:, -1:], "one row each": lambda t: t.transpose(0, 1),
+           "one request": inside}[part]
+    c.x, c.x64 = cut(whole.x), cut(torch.from_numpy(whole.x64)).numpy()
+    if scale is not None:
+        c.kw["x_scale"] = cut(scale).contiguous()
+    c.W, c.W64 = whole.W, whole.W64
+    if dtype == "fp8":
+        c.kw["W_scale"] = whole.kw["W_scale"]
+    out = torch.full((1, 6, 43), 7.0, dtype=TYPE[dtype], device="cuda")
+    mine = cut(out[..., :40]) if part != "one request" else out[..., :40]
+    got, st = kdtv.project(c.x, c.W, flags=flags, out=mine, **c.kw)
+    assert int(st) == 0
+    c.check(got, flags, exact=True)
+    assert (out[..., 40:] == 7.0).all()
+    if part == "first rows":
+        assert (out[:, 4:] == 7.0).all()
