@@ -8,8 +8,9 @@
 // side by side, [W | Bm_0 | Bm_1 ..] [x ; v_0 ; v_1 ..], where v_a = s_a A_a x for the
 // tokens of adapter a and 0 for the others.  v is fp32, split into two bf16 parts
 // (16 significant bits), each multiplied with Bm.  0 * infinity must not carry
-// one adapter's values into another's tokens: an output that is not finite, in a
-// tile with several adapters, is computed again on its own.
+// one adapter's values into another's tokens, and infinity times a part that is 0 or
+// of the other sign is not infinity times v: an output that is not finite, in a
+// tile with adapters, is computed again on its own.
 //
 // Kernels: one of kdtv_proj_low.cu (v of all tokens, in the tiles' order, as the
 // second kernel's operands lie in shared memory), proj_tc_kernel (everything else),
@@ -268,9 +269,22 @@ __device__ __noinline__ void write_narrow(uint32_t rows, const long long* y_at, 
   }
 }
 
-// One output by itself, for a value that is not finite where several adapters share a tile.
+// One output by itself, for a value that is not finite in a tile with adapters.  A tile of one request: such a value is
+// wrong only as a NaN for which an infinity in the output's row of Bm met the two parts of v; any other stays (rows
+// of x that are NaN are not summed again).
+// Slow: a thread's loop over d_in and the tile's requests, for each such output of several requests' tiles.
 template <bool kOneByte>
-__device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
+__device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f, float value) {
+  if (a.requests == 1) {
+    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Bm) + ((long long)a.adapter[b] * a.M + f) * a.R);
+    bool infinite = false;
+    if (value != value)
+      for (int r = 0; r < a.R / 8; ++r) {      // (the rank is a multiple of 8, and Bm is 16-byte aligned)
+        const uint4 w = row[r];
+        for (uint32_t two : {w.x, w.y, w.z, w.w}) infinite |= (two & 0x7fffu) == 0x7f80u || (two & 0x7fff0000u) == 0x7f800000u;
+      }
+    if (!infinite) return value;
+  }
   constexpr int E = kOneByte ? 1 : 2;
   const char* x = static_cast<const char*>(a.x) + (b * a.xs[0] + i * a.xs[1]) * E;
   const char* w = static_cast<const char*>(a.W) + (long long)f * a.K * E;
@@ -599,7 +613,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       tc_fence_after();
       const uint32_t acc = tmem + acc_at(a, n) + ((uint32_t)(32 * q) << 16);
       const int f0 = (2 * it.f + rank) * kFeatures + 32 * q;
-      const bool mixed = a.requests > 1 && it.chunks > 0;
+      const bool adapted = it.chunks > 0;
       auto released = [&](int bar) {
         tc_fence_before();
         __syncwarp();
@@ -640,7 +654,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 #pragma unroll
           for (int m = 0; m < 4; ++m) p[k][m] = pack_bf16x2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
         bool odd = false;
-        if (mixed) {
+        if (adapted) {
           uint32_t top = 0u;                   // not finite?
 #pragma unroll
           for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i >> 3][i & 7]) & 0x7fffffffu);
@@ -658,10 +672,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           const int c = c0 + 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1), f = f0 + 16 * (i >> 3) + 8 * ((i >> 1) & 1) + (lane >> 2);
           const long long to = sh.y_at[c];
           if (to < 0 || f >= a.M) continue;
-          if (mixed && !(fabsf(x) < INFINITY)) {
+          if (adapted && !(fabsf(x) < INFINITY)) {
             int b, i;
             column(a, it.g, it.j, it.hr, c, &b, &i);
-            x = alone<kOneByte>(a, b, i, f);
+            x = alone<kOneByte>(a, b, i, f, x);
           }
           static_cast<__nv_bfloat16*>(a.y)[to + f] = __float2bfloat16_rn(x);
         }
@@ -847,16 +861,16 @@ __global__ void __launch_bounds__(32 * kCombineWarps) proj_combine_kernel(const 
           sum[c].w += v[s][c].w;
         }
     }
-    const bool mixed = a.requests > 1 && it.chunks > 0;
+    const bool adapted = it.chunks > 0;
     const int f = (2 * it.f + rank) * kFeatures + 4 * lane;
 #pragma unroll
     for (int c = 0; c < kCombineCols; ++c) {
       if (at[c] < 0 || f >= a.M) continue;
       float v[4] = {sum[c].x, sum[c].y, sum[c].z, sum[c].w};
-      if (mixed)
+      if (adapted)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (!(fabsf(v[k]) < INFINITY) && f + k < a.M) v[k] = alone<kOneByte>(a, b[c], i[c], f + k);
+          if (!(fabsf(v[k]) < INFINITY) && f + k < a.M) v[k] = alone<kOneByte>(a, b[c], i[c], f + k, v[k]);
       __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + at[c] + f;
       if (a.wide) {
         *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));

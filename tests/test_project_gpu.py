@@ -382,3 +382,38 @@ def test_strides_of_single_rows_and_requests(dtype, flags, part):
     assert (out[..., 40:] == 7.0).all()
     if part == "first rows":
         assert (out[:, 4:] == 7.0).all()
+
+
+def _by_definition(c):
+    """c.oracle()'s y, product by product: 0 times an infinity is NaN, and nothing else is."""
+    y = c.x64 @ c.W64.T
+    for b in range(c.B):
+        a = int(c.ids[b])
+        if a >= 0:
+            low = np.einsum("ik,rk->ir", c.x64[b], c.o["A"][a])
+            Bm = f64(c.kw["Bm"][a])
+            with np.errstate(invalid="ignore"):
+                add = sum(low[:, r, None] * Bm[None, :, r] for r in range(c.rank))
+                y[b] += c.o["adapter_scale"][a] * add
+    return y
+
+
+@pytest.mark.parametrize("dtype,flags", PATHS)
+@pytest.mark.parametrize("B,N,K,M", [(1, 1, 128, 200), (1, 300, 128, 200), (2, 300, 64, 72), (1, 5, 2048, 640), (40, 2, 2048, 200),
+                                     (3, 200, 2048, 129), (8, 64, 128, 12800), (1, 600, 128, 12800)])
+def test_infinities_of_an_adapter(dtype, flags, B, N, K, M):
+    """An infinity in Bm times a finite A x is that infinity, whatever the batch: one request's tile or
+    several's, cut over several CTAs or whole.  (Whole numbers: everything else is exact.)"""
+    if flags & SIMT and M > 10000:
+        pytest.skip("a size for the tensor cores' tiles")
+    c = Case(B, N, K, M, dtype, 3, 16, seed=15, whole=True, ids=(np.arange(B) + 2) % 4 - 1)
+    Bm = c.kw["Bm"]
+    Bm[1, 3, 4], Bm[1, 7, 0], Bm[1, M - 1, 15] = float("inf"), -float("inf"), float("inf")
+    Bm[0, 5, 2] = float("nan")
+    want = _by_definition(c)
+    got = f64(c.run(flags))
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.isinf(want).any()
+    far = np.isinf(want)
+    assert np.array_equal(got[far], want[far])
+    rest = np.isfinite(want)
+    assert np.array_equal(got[rest], f64(torch.tensor(want[rest]).to(TYPE[dtype])))
