@@ -115,7 +115,8 @@ __device__ __forceinline__ void low_store(const ProjArgs& a, const Low& w, const
     char* const row = part_row(a, w.b, i, w.hr, w.first + c, 0, &flip) + (lane >> 2) * 2;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float v = w.s * acc[2 * h + e];
+      // (ranks that fill up the last 16: 0, not the NaN of an infinite x times A's zeros behind the rank, a multiple of 8)
+      const float v = rank0 + 8 * h < a.R ? w.s * acc[2 * h + e] : 0.f;
       const __nv_bfloat16 hi = __float2bfloat16_rn(v);
       const float left = v - __bfloat162float(hi);         // exact; not a number where v is not finite
       char* const at = row + ((h ^ flip) << 4);

@@ -417,3 +417,22 @@ def test_infinities_of_an_adapter(dtype, flags, B, N, K, M):
     assert np.array_equal(got[far], want[far])
     rest = np.isfinite(want)
     assert np.array_equal(got[rest], f64(torch.tensor(want[rest]).to(TYPE[dtype])))
+
+
+@pytest.mark.parametrize("flags", [0, SIMT])
+@pytest.mark.parametrize("B,N", [(1, 1), (1, 5), (1, 300), (40, 1)])
+@pytest.mark.parametrize("rank", [8, 16, 24])
+def test_infinite_rows_and_ranks(flags, B, N, rank):
+    """An infinity in x, where every weight that it meets is positive, gives infinities, whether or not the ranks fill the
+    products' sixteens."""
+    c = Case(B, N, 128, 72, "bf16", 2, rank, seed=16, whole=True, ids=[0] * B)
+    c.W[:, 3], c.kw["A"][:, :, 3] = 1.0, 1.0
+    c.kw["Bm"].abs_().add_(1.0)
+    other = c.x[..., 3].clone()
+    c.x[0, N // 2, 3] = float("inf")
+    got = f64(c.run(flags))
+    assert (got[0, N // 2] == np.inf).all()
+    c.x[..., 3] = other
+    clean = f64(c.run(flags))
+    got[0, N // 2] = clean[0, N // 2]
+    assert np.array_equal(got, clean)
