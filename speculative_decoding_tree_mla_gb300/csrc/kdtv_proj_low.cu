@@ -117,7 +117,9 @@ __device__ __forceinline__ void low_store(const ProjArgs& a, const Low& w, const
     for (int h = 0; h < 2; ++h) {
       // (ranks that fill up the last 16: 0, not the NaN of an infinite x times A's zeros behind the rank, a multiple of 8)
       const float v = rank0 + 8 * h < a.R ? w.s * acc[2 * h + e] : 0.f;
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+      // (bf16's largest value for what would round beyond it: the other part has the rest)
+      constexpr float most = 0x1.fep127f;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(fabsf(v) < INFINITY ? fminf(fmaxf(v, -most), most) : v);
       const float left = v - __bfloat162float(hi);         // exact; not a number where v is not finite
       char* const at = row + ((h ^ flip) << 4);
       *reinterpret_cast<__nv_bfloat16*>(at) = hi;

@@ -436,3 +436,20 @@ def test_infinite_rows_and_ranks(flags, B, N, rank):
     clean = f64(c.run(flags))
     got[0, N // 2] = clean[0, N // 2]
     assert np.array_equal(got, clean)
+
+
+@pytest.mark.parametrize("flags", [0, SIMT])
+@pytest.mark.parametrize("B,N", [(1, 1), (1, 20), (30, 1)])
+def test_largest_inner_products(flags, B, N):
+    """A x between bf16's largest value and fp32's, times 1 / 2: finite."""
+    c = Case(B, N, 64, 72, "bf16", 2, 16, seed=17, ids=[1] * B)
+    c.x.zero_()
+    c.W.zero_()
+    c.kw["A"].zero_()
+    c.kw["Bm"].zero_()
+    c.x[..., :2] = 2.0 ** 100
+    c.kw["A"][1, 5, 0], c.kw["A"][1, 5, 1] = 1.9921875 * 2.0 ** 27, 0.75 * 2.0 ** 20
+    c.kw["Bm"][1, :, 5] = torch.tensor([0.5, -0.5], dtype=torch.bfloat16, device="cuda").repeat(36)
+    c.x64, c.W64 = f64(c.x), f64(c.W)
+    c.o.update(A=f64(c.kw["A"]), Bm=f64(c.kw["Bm"]))
+    c.check(c.run(flags), flags)
