@@ -496,8 +496,8 @@ typedef struct kdtv_norm_args {
   float weight_offset;  /* added to every weight (1 for models that store w - 1)   */
   int64_t x_stride[3];  /* elements between requests, rows, heads (the last        */
   int64_t r_stride[3];  /* dimension is contiguous); {0, 0, 0}: contiguous.  r:    */
-  int64_t ro_stride[3]; /* residual, ro: residual_out                              */
-  int64_t y_stride[3];
+  int64_t ro_stride[3]; /* residual, ro: residual_out.  Of a dimension of one       */
+  int64_t y_stride[3];  /* element: any                                            */
 } kdtv_norm_args;
 
 /*

@@ -299,11 +299,12 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
 
 bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool multiple(const long long (&s)[3], int v) { return s[0] % v == 0 && s[1] % v == 0 && s[2] % v == 0; }
-void strides(const int64_t (&in)[3], long long N, long long H, long long dim, long long (&out)[3]) {
+// (Of a dimension of one element: 0, whatever was given.)
+void strides(const int64_t (&in)[3], const kdtv_norm_args& d, long long (&out)[3]) {
   const bool given = in[0] || in[1] || in[2];
-  out[0] = given ? in[0] : N * H * dim;
-  out[1] = given ? in[1] : H * dim;
-  out[2] = given ? in[2] : dim;
+  out[0] = d.B == 1 ? 0 : given ? in[0] : (long long)d.N * d.H * d.dim;
+  out[1] = d.N == 1 ? 0 : given ? in[1] : (long long)d.H * d.dim;
+  out[2] = d.H == 1 ? 0 : given ? in[2] : d.dim;
 }
 bool same(const long long (&s)[3], const long long (&t)[3]) { return s[0] == t[0] && s[1] == t[1] && s[2] == t[2]; }
 
@@ -396,10 +397,10 @@ extern "C" int kdtv_rmsnorm(const kdtv_norm_args* d, const void* x, const void* 
   a.x = x; a.residual = residual; a.residual_out = residual_out; a.weight = weight;
   a.y = y; a.y_scale = y_scale; a.n_live = n_live;
   a.eps = d->eps; a.weight_offset = d->weight_offset;
-  strides(d->x_stride, d->N, d->H, d->dim, a.xs);
-  strides(d->r_stride, d->N, d->H, d->dim, a.rs);
-  strides(d->ro_stride, d->N, d->H, d->dim, a.ros);
-  strides(d->y_stride, d->N, d->H, d->dim, a.ys);
+  strides(d->x_stride, *d, a.xs);
+  strides(d->r_stride, *d, a.rs);
+  strides(d->ro_stride, *d, a.ros);
+  strides(d->y_stride, *d, a.ys);
   a.by_heads = divisor((unsigned)d->H);
   a.by_N = divisor((unsigned)d->N);
   // Rows of a result over one another.

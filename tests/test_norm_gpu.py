@@ -243,3 +243,20 @@ def test_python_refusals():
         kdtv.rmsnorm(x.cpu())
     with pytest.raises(kdtv.KdtvError, match="UNSUPPORTED"):
         kdtv.rmsnorm(make((1, 1, 32776), "bf16", 20))
+
+
+def test_strides_of_single_rows():
+    """A dimension of one element may have any stride: in place by two views of the same row, and rows of 16-byte
+    words whatever lies beside them."""
+    buf, w = make((1, 6, 64), "bf16", 45), make((64,), "bf16", 46)
+    x = buf[:, 2:3]
+    y, _ = O.rmsnorm(f64(x), f64(w), 1e-6)
+    before = buf.clone()
+    kdtv.rmsnorm(x, w, out=x.as_strided((1, 1, 64), (64, 64, 1), x.storage_offset()))
+    near(f64(x), y, ARITH + STEP["bf16"])
+    assert torch.equal(buf[:, :2], before[:, :2]) and torch.equal(buf[:, 3:], before[:, 3:])
+    res = buf[:, 4:5]
+    y, h = O.rmsnorm(f64(x), f64(w), 1e-6, f64(res))
+    kdtv.rmsnorm(x, w, residual=res, residual_out=res.as_strided((1, 1, 64), (1, 3, 1), res.storage_offset()), out=x)
+    near(f64(x), y, ARITH + STEP["bf16"])
+    near(f64(res), h, STEP["bf16"])
