@@ -224,12 +224,17 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
     return sum / (float)a.dim;
   };
   float mean = mean_square(1.f) + a.eps, up = 1.f;
-  // Squares beyond fp32's range, or too small for it: of the row times a power of two, whose square goes to eps.
-  const float s = !(mean <= 0x1p100f) ? 0x1p-72f : mean < 0x1p-60f ? 0x1p75f : 1.f;
-  if (__any_sync(0xffffffffu, s != 1.f)) {            // (a row of more than a warp: the same for all of the block)
-    if (a.per_row > 32) __syncthreads();              // (the first sums are read)
+  // Squares beyond fp32's range, or too small for it: of the row times a power of two, whose square goes to eps.  Rows of
+  // subnormals, whose squares are still too small then, take a second, larger one: the mean is a normal number in the end
+  // (at least (2^-23)^2 / 32768), and a row of which one power makes too little is below 2^-97, so that the other makes
+  // no square too large.
+  float s = !(mean <= 0x1p100f) ? 0x1p-72f : mean < 0x1p-60f ? 0x1p75f : 1.f;
+#pragma unroll 1
+  while (__any_sync(0xffffffffu, s != up)) {          // (a row of more than a warp: the same for all of the block)
+    if (a.per_row > 32) __syncthreads();              // (the last sums are read)
     mean = mean_square(s) + a.eps * s * s;
     up = s;
+    if (up > 1.f && mean < 0x1p-60f) s = 0x1p126f;
   }
   float inv = 1.f / sqrtf(mean), left = 0.f;
   // One byte: what the root's reciprocal lost, by a step of Newton's method.  (Values near the middle between two codes

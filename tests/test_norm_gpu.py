@@ -260,3 +260,39 @@ def test_strides_of_single_rows():
     kdtv.rmsnorm(x, w, residual=res, residual_out=res.as_strided((1, 1, 64), (1, 3, 1), res.storage_offset()), out=x)
     near(f64(x), y, ARITH + STEP["bf16"])
     near(f64(res), h, STEP["bf16"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [8, 64, 333, 8190, 8192, 32768])
+def test_rows_of_subnormals(dtype, dim):
+    """No eps, rows down to the type's smallest values: one such element among zeros, several, a row full of them,
+    and such elements beside larger ones.  (The elements and their sums are exact, as everywhere; the statistic is of the row
+    scaled by a power of two, so the bounds are those of ordinary rows.)"""
+    least = 2.0 ** -149 if dtype == "f32" else 2.0 ** -133
+    x = torch.zeros((12, 1, dim), dtype=torch.float64)
+    x[0, 0, dim // 2] = 2.0 ** -145 if dtype == "f32" else least
+    x[1, 0, 0] = -least
+    x[2, 0, ::3] = 3 * least
+    x[3] = least
+    x[4] = 2.0 ** -126
+    x[5, 0, : dim // 2] = least
+    x[5, 0, dim - 1] = 2.0 ** -118
+    x[6, 0, 1] = 2.0 ** -106
+    x[7, 0, ::2] = -5 * 2.0 ** -109
+    x[8, 0, ::5] = 2.0 ** -103
+    x[9, 0, 3] = 1.75 * 2.0 ** -90
+    x[10, 0, dim - 1] = 2.0 ** -31
+    x[11] = torch.linspace(-40, 40, dim).round().double() * least
+    x[11, 0, 0] = 40 * least
+    x = x.to("cuda", TYPE[dtype])
+    y, _ = O.rmsnorm(f64(x), None, 0.0)
+    near(f64(kdtv.rmsnorm(x, eps=0.0)), y, ARITH + STEP[dtype])
+    ordinary = make((1, 1, dim), dtype, 47)                    # beside an ordinary row, and with a residual that takes all away
+    both = torch.cat((ordinary, x, -x, ordinary))
+    near(f64(kdtv.rmsnorm(both, eps=0.0)), O.rmsnorm(f64(both), None, 0.0)[0], ARITH + STEP[dtype])
+    near(f64(kdtv.rmsnorm(x, eps=0.0, residual=x.clone())), O.rmsnorm(f64(x), None, 0.0, f64(x))[0], ARITH + STEP[dtype])
+    if dim % 32 == 0:
+        check_one_byte(*kdtv.rmsnorm(x, eps=0.0, one_byte=True), y)
+    tiny = float(np.float32(2.0 ** -140))                      # an eps of that size counts
+    x = torch.full((1, 1, dim), 2.0 ** -70, dtype=TYPE[dtype], device="cuda")
+    near(f64(kdtv.rmsnorm(x, eps=tiny)), O.rmsnorm(f64(x), None, tiny)[0], ARITH + STEP[dtype])
