@@ -244,13 +244,15 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_kernel(const __grid_constant_
     const float p = mean * inv;
     left = -0.5f * inv * fmaf(fmaf(mean, inv, -p), inv, fmaf(p, inv, -1.f));
   }
+  // The power of two, to the row where the reciprocal may be more than fp32 holds; a large row's to both, since its
+  // reciprocal may be subnormal: what 2^-24 makes subnormal of a row above 2^50 is 0 in the result.
   if (up < 1.f) {
-    inv *= up;
-    left *= up;
+    inv *= up * 0x1p24f;
+    left *= up * 0x1p24f;
   }
-  if (up > 1.f)                                       // (that may be more than fp32 holds)
+  if (up != 1.f)
 #pragma unroll
-    for (int c = 0; c < CH; ++c) scale_v<V>(h[c], up);
+    for (int c = 0; c < CH; ++c) scale_v<V>(h[c], up < 1.f ? 0x1p-24f : up);
 
   const T* weight = static_cast<const T*>(a.weight);
   O* y = static_cast<O*>(a.y) + b * a.ys[0] + i * a.ys[1] + head * a.ys[2];

@@ -296,3 +296,19 @@ def test_rows_of_subnormals(dtype, dim):
     tiny = float(np.float32(2.0 ** -140))                      # an eps of that size counts
     x = torch.full((1, 1, dim), 2.0 ** -70, dtype=TYPE[dtype], device="cuda")
     near(f64(kdtv.rmsnorm(x, eps=tiny)), O.rmsnorm(f64(x), None, tiny)[0], ARITH + STEP[dtype])
+
+
+@pytest.mark.parametrize("where", ["whole", "any address"])
+def test_largest_rows_keep_their_bits(where):
+    """Rows of +-m / 128 * 2^127: squares, their sum and its root are exact in fp32 once a power of two is taken out, so
+    1 is off by the reciprocal's rounding and the product's: 2^-23."""
+    m = torch.tensor([129, 200, 216, 217, 222, 231, 244, 253, 255], dtype=torch.float64)
+    x = ((m / 128)[:, None, None] * 2.0 ** 127 * torch.tensor([1.0, -1.0], dtype=torch.float64).repeat(256)[None, None]).float().cuda()
+    if where != "whole":
+        wide = torch.zeros((9, 1, 515), device="cuda")
+        wide[..., 3:] = x
+        x = wide[..., 3:]
+    got = f64(kdtv.rmsnorm(x, eps=0.0))
+    near(got, np.sign(f64(x)), 2.0 ** -23)
+    codes, scale = kdtv.rmsnorm(x, eps=0.0, one_byte=True)
+    assert np.array_equal(O.widen(codes.cpu().numpy(), scale.cpu().numpy()), np.sign(f64(x)))
