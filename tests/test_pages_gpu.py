@@ -166,3 +166,44 @@ def test_python_refusals():
             kdtv.pages_resize(P, L, **kw)
     with pytest.raises(ValueError):
         kdtv.PagePool(dev([[0]]), dev([0, 0]), dev([0]), dev([1]), 16)
+
+
+@pytest.mark.parametrize("N", [5, 5000])
+def test_one_row_too_many(N):
+    """A request whose rows fill its row of the table to the last place, and one that has one row more."""
+    width = (N + 40) // 16
+    room = width * 16
+    P = Pool(4, width, 4 * width, 16, 9)
+    assert P.resize([3, 0, room - N, 7], [N] * 4, N) == (False, "KDTV_OK")
+    assert P.held[2] == width
+    held = list(P.held)
+    short, st = P.resize([0, 0, room - N + 1, 0], [0, 0, N, 0], N)
+    assert not short and st == "KDTV_ERR_BAD_PREFIX" and P.held == [0, 0, held[2], 0]
+    assert P.resize([0, 0, room, 0], [N, N, 0, N], N) == (False, "KDTV_OK")
+    assert P.resize([room, 0, 0, 0], [1, 0, 0, 0], N)[1] == "KDTV_ERR_BAD_PREFIX"
+
+
+@pytest.mark.parametrize("B,N", [(64, 8), (300, 40), (64, 1000)])
+def test_replays_give_the_same_slots(B, N):
+    """Growing and trimming back leaves the stack as it was, so every replay of the two gives the first call's slots."""
+    P = Pool(B, 80, B * 80, 16, 10)
+    L = dev(np.arange(B) % 97 * 2)
+    grow, trim = kdtv.PagesResize(P.gpu, L, N=N, slots=True), kdtv.PagesResize(P.gpu, L, N=0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    slots = grow(side)[0]
+    trim(side)
+    side.synchronize()
+    first = slots.clone()
+    assert (first >= 0).all() and len(torch.unique(first)) == B * N
+    state = [t.clone() for t in (P.gpu.free_pages, P.gpu.free_count, P.gpu.n_pages, P.gpu.page_table)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        grow()
+        trim()
+    for _ in range(3):
+        slots.zero_()
+        g.replay()
+        assert torch.equal(slots, first)
+    assert all(torch.equal(a, b) for a, b in zip(state, (P.gpu.free_pages, P.gpu.free_count, P.gpu.n_pages, P.gpu.page_table)))
+    assert int(grow.status) == 0 and int(trim.status) == 0
