@@ -609,8 +609,11 @@ typedef struct kdtv_pages_dims {
  * n_pages or returned page ids are out of range, and every request where
  * *free_count is (KDTV_ERR_BAD_PAGE).  Where the free list runs out, the request
  * that it does not suffice for and all behind it that need pages keep what
- * they have (KDTV_ERR_NO_PAGES).  Requests must not share pages.  Where
- * kdtv_compact_kv follows, n_live is NULL: it asks for the pages of all N rows.
+ * they have (KDTV_ERR_NO_PAGES); likewise where a request would get a page id
+ * that is out of range (KDTV_ERR_BAD_PAGE; the table's entries that were to be
+ * filled are -1 then, and the id stays on the stack).  Requests must not share
+ * pages.  Where kdtv_compact_kv follows, n_live is NULL: it asks for the pages of
+ * all N rows.
  */
 int kdtv_pages_resize(const kdtv_pages_dims* dims, const int32_t* prefix_len,
                       const int32_t* n_live, int32_t* free_pages, int32_t* free_count,

@@ -64,7 +64,8 @@ def project(x, W, A=None, Bm=None, adapter=None, adapter_scale=None):
 
 def pages_resize(rows, page_size, max_pages, num_pages, free, n_pages, table):
     """One resize to `rows[b]` rows (None: a request that is refused).  free: the stack as a list, n_pages
-    a list, table a list of lists; all changed in place.  Returns whether the free list ran out."""
+    a list, table a list of lists; all changed in place.  Returns whether the free list ran out.  (A request that
+    would get an id out of range stops the taking too.)"""
     B = len(rows)
     want = [n_pages[b] if r is None else -(-r // page_size) for b, r in enumerate(rows)]
     for b in reversed(range(B)):
@@ -77,9 +78,9 @@ def pages_resize(rows, page_size, max_pages, num_pages, free, n_pages, table):
         need = want[b] - n_pages[b]
         if need <= 0:
             continue
-        short = short or need > len(free)
-        if short:
-            continue
+        short = need > len(free)
+        if short or not all(0 <= p < num_pages for p in free[len(free) - need:]):
+            break
         for p in range(n_pages[b], want[b]):
             table[b][p] = free.pop()
         n_pages[b] = want[b]

@@ -4,6 +4,7 @@
 #include "kdtv_rope.cuh"
 #include "kdtv_ptx.cuh"
 
+#include <limits.h>
 #include <string.h>
 
 namespace kdtv {
@@ -88,10 +89,11 @@ __device__ __forceinline__ int64_t slot_of(const PageArgs& a, int L, int n, int 
 }
 
 // One cluster of CTAs.  Each scans all requests by itself (they are few, and
-// their lengths are in L2), so that the CTAs share nothing but two barriers:
+// their lengths are in L2), so that the CTAs share nothing but barriers:
 // what all of them read (counts, the free list's length, page ids that go
 // back) is read before the first one, what goes back is on the stack before
-// the second, behind which pages are taken.  What goes back, or is taken, is
+// the second, behind which pages are taken, and behind the third all know
+// whether an id that was taken is no page's.  What goes back, or is taken, is
 // spread by entries, which find their requests by bisection in the sums, so
 // that one request with many pages is spread like many with one.
 // Latency bound: two trips to L2, a scan and two barriers (64 requests with 8 rows each: 4.5 us, one CTA; 512 prompts of up
@@ -100,9 +102,11 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
   extern __shared__ __align__(16) int ps[];
   int *give = ps, *take = give + a.B, *want = take + a.B, *have = want + a.B;
   uint32_t* bad = reinterpret_cast<uint32_t*>(have + a.B);       // one bit a request
+  __shared__ int s_wrong;                              // the first of the entries that are taken whose id is no page's
   const int rank = ctas > 1 ? (int)ptx::cluster_ctarank() : 0, tid = threadIdx.x;
   const int all = ctas * kPageThreads, me = rank * kPageThreads + tid;
   for (int i = tid; i < (a.B + 31) / 32; i += kPageThreads) bad[i] = 0u;
+  if (tid == 0) s_wrong = INT_MAX;
   const int count = *a.free_count;
   const bool usable = count >= 0 && count <= a.num_pages;
   for (int b = tid; b < a.B; b += kPageThreads) {
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
     take[b] = max(w - h, 0);
   }
   __syncthreads();
-  if (ctas > 1) ptx::cluster_sync();                   // every CTA's bits are clear
+  if (ctas > 1) ptx::cluster_sync();                   // every CTA's bits and s_wrong are set up
   // Pages that go back must be pages: each CTA looks at its share of the requests.
   for (int b = rank * (kPageThreads / 32) + (tid >> 5); b < a.B; b += ctas * (kPageThreads / 32)) {
     const int32_t* row = a.page_table + (long long)b * a.max_pages;
@@ -202,6 +206,8 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
   }
   // The k-th page that is taken, from the top of the stack down.
   auto page_taken = [&](int k) { return *reinterpret_cast<volatile int32_t*>(a.free_pages + (top - 1 - k)); };
+  auto entry_taken = [&](int b, int k) { return a.page_table + (long long)b * a.max_pages + have[b] + k - (b ? take[b - 1] : 0); };
+  int wrong = INT_MAX;
   for (int k0 = run0; k0 < taken; k0 += runs) {
     int id[kBatch], b = 0;
 #pragma unroll
@@ -213,8 +219,35 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
       if (i == 0 || few) b = first_above(take, a.B, k);
       else
         while (take[b] <= k) ++b;
-      if (id[i] < 0 || id[i] >= a.num_pages) page_error(a, KDTV_ERR_BAD_PAGE);
-      a.page_table[(long long)b * a.max_pages + have[b] + k - (b ? take[b - 1] : 0)] = id[i];
+      if (id[i] < 0 || id[i] >= a.num_pages) wrong = min(wrong, k);
+      *entry_taken(b, k) = id[i];
+    }
+  }
+  // An id that is no page's: the request that would get it, and those behind it, get none after all.  (The stack still holds
+  // what was taken.)
+  if (taken) {
+    if (wrong != INT_MAX) {
+      const uint32_t at = ptx::smem_u32(&s_wrong);
+      for (int c = 0; c < ctas; ++c)
+        asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" :: "r"(ctas > 1 ? ptx::mapa(at, c) : at), "r"(wrong) : "memory");
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    // (relaxed: the tables' stores need not be done; ordered 34.4 us a pass for the 512 prompts, so 33.7)
+    if (ctas > 1) ptx::cluster_sync_relaxed();
+    else __syncthreads();
+    if (s_wrong != INT_MAX) {
+      if (ctas > 1) ptx::cluster_sync();               // the stores that are taken back are done
+      else __syncthreads();
+      const int first = first_above(take, a.B, s_wrong), left = first ? take[first - 1] : 0;
+      for (int k = left + me; k < taken; k += all) *entry_taken(first_above(take, a.B, k), k) = -1;
+      for (int b = first + me; b < grant; b += all)
+        if (want[b] > have[b]) a.n_pages[b] = have[b];
+      if (me == 0) {
+        *a.free_count = top - left;
+        page_error(a, KDTV_ERR_BAD_PAGE);
+      }
+      grant = first;
     }
   }
   if (a.slots)

@@ -207,3 +207,34 @@ def test_replays_give_the_same_slots(B, N):
         assert torch.equal(slots, first)
     assert all(torch.equal(a, b) for a, b in zip(state, (P.gpu.free_pages, P.gpu.free_count, P.gpu.n_pages, P.gpu.page_table)))
     assert int(grow.status) == 0 and int(trim.status) == 0
+
+
+@pytest.mark.parametrize("bad", [-1, "num", 2 ** 31 - 1])
+@pytest.mark.parametrize("B,N,page", [(30, 50, 16), (600, 50, 16), (30, 3000, 64)])
+def test_bad_ids_on_the_free_stack(bad, B, N, page):
+    """The request that would get an id out of range, and those behind it that need pages, keep what they have; nothing
+    of the bad id leaves the stack, and once it is mended the pool goes on."""
+    need = -(-N // page)
+    P = Pool(B, need + 5, B * (need + 5), page, 11)
+    assert P.resize([page] * B, [0] * B, N) == (False, "KDTV_OK")             # a page each
+    for where in (0, need, 7 * need + 1, B * need - 1, B * need):              # places from the top; the last one is not taken
+        at = len(P.free) - 1 - where
+        was = P.free[at]
+        P.free[at] = P.num if bad == "num" else bad
+        P.gpu.free_pages[at] = P.free[at]
+        short, st = P.resize([page] * B, [N] * B, N)                           # (tables, counts, stack and slots as the oracle's)
+        assert not short and st == ("KDTV_ERR_BAD_PAGE" if where < B * need else "KDTV_OK")
+        assert P.held == [1 + (need if b < where // need or where == B * need else 0) for b in range(B)]
+        assert P.resize([page] * B, [0] * B, N) == (False, "KDTV_OK")
+        P.free[at] = was
+        P.gpu.free_pages[at] = was
+    # some give back, some need: pages that went back are on top of the bad id
+    P.resize([page] * B, [N if b < B // 2 else 0 for b in range(B)], N)
+    at = len(P.free) - 1
+    was, P.free[at] = P.free[at], -5
+    P.gpu.free_pages[at] = -5
+    short, st = P.resize([page] * B, [0 if b < B // 2 else N for b in range(B)], N)
+    assert not short and st == "KDTV_OK"
+    short, st = P.resize([page] * B, [page if b < B // 2 else N for b in range(B)], N)
+    assert not short and st == "KDTV_ERR_BAD_PAGE" and P.held[0] == 1
+    assert P.free[at] == -5
