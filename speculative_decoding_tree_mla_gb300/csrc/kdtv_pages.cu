@@ -174,14 +174,15 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
   // entry's request is found from the one 32 entries before; with few, by bisection each time.
   constexpr int kBatch = 8;
   const bool few = (long long)given + taken < 64ll * a.B;
-  const int lane = tid & 31, run0 = (me >> 5) * 32 * kBatch, runs = all * kBatch;
+  // (a run that begins behind the last entry may begin behind 2^31 too)
+  const unsigned lane = tid & 31, run0 = (me >> 5) * 32 * kBatch, runs = all * kBatch;
   if (given) {
-    for (int e0 = run0; e0 < given; e0 += runs) {
+    for (unsigned e0 = run0; e0 < (unsigned)given; e0 += runs) {
       int32_t* entry[kBatch];
       int id[kBatch], b = 0;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int k = given - 1 - (e0 + 32 * i + lane);  // from the last request's last page on
+        const int k = (int)(given - 1 - (e0 + 32 * i + lane));       // from the last request's last page on
         entry[i] = nullptr;
         if (k < 0) continue;
         if (i == 0 || few) b = first_above(give, a.B, k);
@@ -208,14 +209,14 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
   auto page_taken = [&](int k) { return *reinterpret_cast<volatile int32_t*>(a.free_pages + (top - 1 - k)); };
   auto entry_taken = [&](int b, int k) { return a.page_table + (long long)b * a.max_pages + have[b] + k - (b ? take[b - 1] : 0); };
   int wrong = INT_MAX;
-  for (int k0 = run0; k0 < taken; k0 += runs) {
+  for (unsigned k0 = run0; k0 < (unsigned)taken; k0 += runs) {
     int id[kBatch], b = 0;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) id[i] = k0 + 32 * i + lane < taken ? page_taken(k0 + 32 * i + lane) : 0;
+    for (int i = 0; i < kBatch; ++i) id[i] = k0 + 32 * i + lane < (unsigned)taken ? page_taken(k0 + 32 * i + lane) : 0;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int k = k0 + 32 * i + lane;
-      if (k >= taken) continue;
+      if (k0 + 32 * i + lane >= (unsigned)taken) continue;
+      const int k = (int)(k0 + 32 * i + lane);
       if (i == 0 || few) b = first_above(take, a.B, k);
       else
         while (take[b] <= k) ++b;
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid
       if (ctas > 1) ptx::cluster_sync();               // the stores that are taken back are done
       else __syncthreads();
       const int first = first_above(take, a.B, s_wrong), left = first ? take[first - 1] : 0;
-      for (int k = left + me; k < taken; k += all) *entry_taken(first_above(take, a.B, k), k) = -1;
+      for (unsigned k = left + me; k < (unsigned)taken; k += all) *entry_taken(first_above(take, a.B, k), k) = -1;
       for (int b = first + me; b < grant; b += all)
         if (want[b] > have[b]) a.n_pages[b] = have[b];
       if (me == 0) {

@@ -238,3 +238,19 @@ def test_bad_ids_on_the_free_stack(bad, B, N, page):
     short, st = P.resize([page] * B, [page if b < B // 2 else N for b in range(B)], N)
     assert not short and st == "KDTV_ERR_BAD_PAGE" and P.held[0] == 1
     assert P.free[at] == -5
+
+
+def test_nearly_two_to_the_31_entries():
+    """All that the table may hold: counters that run past the last entry by whole runs stay unsigned.  (26 GB.)"""
+    B, width, page = 8192, (1 << 18) - 1, 4096
+    num = B * width
+    ids = torch.arange(num, dtype=torch.int32, device="cuda")
+    P = kdtv.PagePool(torch.full((B, width), -1, dtype=torch.int32, device="cuda"), dev(np.zeros(B)), ids.flip(0), dev([num]), page)
+    full = dev(np.full(B, width * page))
+    assert kdtv.STATUS[int(kdtv.pages_resize(P, full, N=0))] == "KDTV_OK"
+    assert int(P.free_count) == 0 and (P.n_pages == width).all() and torch.equal(P.page_table.view(-1), ids)
+    assert kdtv.STATUS[int(kdtv.pages_resize(P, dev(np.zeros(B)), N=0))] == "KDTV_OK"
+    assert int(P.free_count) == num and (P.n_pages == 0).all() and (P.page_table == -1).all()
+    assert torch.equal(P.free_pages.flip(0), ids)
+    del P, ids, full
+    torch.cuda.empty_cache()
