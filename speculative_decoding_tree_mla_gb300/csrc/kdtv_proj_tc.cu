@@ -269,22 +269,28 @@ __device__ __noinline__ void write_narrow(uint32_t rows, const long long* y_at, 
   }
 }
 
-// One output by itself, for a value that is not finite in a tile with adapters.  A tile of one request: such a value is
-// wrong only as a NaN for which an infinity in the output's row of Bm met the two parts of v; any other stays (rows
-// of x that are NaN are not summed again).
-// Slow: a thread's loop over d_in and the tile's requests, for each such output of several requests' tiles.
-template <bool kOneByte>
-__device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f, float value) {
-  if (a.requests == 1) {
-    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Bm) + ((long long)a.adapter[b] * a.M + f) * a.R);
-    bool infinite = false;
-    if (value != value)
-      for (int r = 0; r < a.R / 8; ++r) {      // (the rank is a multiple of 8, and Bm is 16-byte aligned)
-        const uint4 w = row[r];
-        for (uint32_t two : {w.x, w.y, w.z, w.w}) infinite |= (two & 0x7fffu) == 0x7f80u || (two & 0x7fff0000u) == 0x7f800000u;
-      }
-    if (!infinite) return value;
+// Which of outputs f, f + step, f + 2 step, f + 3 step have an infinity in request b's rows of Bm: in a tile of one request
+// their NaN may have been made by the two parts of v.
+__device__ __noinline__ uint32_t infinite_rows(const ProjArgs& a, int b, int f, int step) {
+  const __nv_bfloat16* Bm = static_cast<const __nv_bfloat16*>(a.Bm) + (long long)a.adapter[b] * a.M * a.R;
+  uint32_t found = 0u;
+  for (int m = 0; m < 4; ++m) {
+    if (f + m * step >= a.M) break;
+    const uint4* row = reinterpret_cast<const uint4*>(Bm + (long long)(f + m * step) * a.R);
+    for (int r = 0; r < a.R / 8; ++r) {        // (the rank is a multiple of 8, and Bm is 16-byte aligned)
+      const uint4 w = row[r];
+      for (uint32_t two : {w.x, w.y, w.z, w.w})
+        if ((two & 0x7fffu) == 0x7f80u || (two & 0x7fff0000u) == 0x7f800000u) found |= 1u << m;
+    }
   }
+  return found;
+}
+
+// One output by itself, for a value that is not finite in a tile with adapters.  Slow (a thread's loop over d_in and the
+// tile's requests), so a tile of one request takes it for a NaN beside an infinity in Bm only, not for rows of x that
+// are NaN.
+template <bool kOneByte>
+__device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
   constexpr int E = kOneByte ? 1 : 2;
   const char* x = static_cast<const char*>(a.x) + (b * a.xs[0] + i * a.xs[1]) * E;
   const char* w = static_cast<const char*>(a.W) + (long long)f * a.K * E;
@@ -337,6 +343,36 @@ __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f, floa
     sum = fmaf(v, to_f32(static_cast<const __nv_bfloat16*>(a.Bm)[((long long)id * a.M + f) * a.R + r]), sum);
   }
   return sum;
+}
+
+// Columns c0 .. c1 - 1 of a tile with adapters, in which something is not finite, once they are written: such outputs of a
+// warp's 32, from f0 on, are computed by themselves where they may be wrong.  All of the warp comes along.
+template <bool kOneByte>
+__device__ __noinline__ void look_again(const ProjArgs& a, const long long* y_at, int g, int j, int hr, uint32_t acc, int f0, int c0, int c1) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t rows = a.requests > 1 ? 15u : infinite_rows(a, g, f0 + (lane >> 2), 8);
+  if (!__any_sync(0xffffffffu, rows)) return;
+#pragma unroll 1
+  for (; c0 < c1; c0 += 16) {
+    float v[2][8];                             // as in the kernel's fetch
+    __syncwarp();                              // (the other lanes' stores too, which come before these)
+    tmem_ld_16x256b_x2(acc + c0, v[0]);
+    tmem_ld_16x256b_x2(acc + (16u << 16) + c0, v[1]);
+    tmem_wait_ld();
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x = i == k ? v[k >> 3][k & 7] : x;
+      const int m = 2 * (i >> 3) + ((i >> 1) & 1), c = c0 + 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1), f = f0 + 8 * m + (lane >> 2);
+      const long long to = y_at[c];
+      if (to < 0 || f >= a.M || !((rows >> m) & 1u) || (a.requests > 1 ? fabsf(x) < INFINITY : x == x)) continue;
+      int b, row;
+      column(a, g, j, hr, c, &b, &row);
+      static_cast<__nv_bfloat16*>(a.y)[to + f] = __float2bfloat16_rn(alone<kOneByte>(a, b, row, f));
+    }
+  }
+  __syncwarp();
 }
 
 // (Registers that leave room for a block of the first kernel beside this one's.)
@@ -642,8 +678,9 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         continue;
       }
       // 16 columns as the products of 8 x 8 matrices hold them: value (k, h, j, e) is output f0 + 16 h + 8 j + lane /
-      // 4 of token c0 + 8 k + 2 (lane % 4) + e; p: pairs over e, rounded.  True if they were written one by one.
-      auto fetch = [&](int c0, uint32_t (&p)[2][4]) -> bool {
+      // 4 of token c0 + 8 k + 2 (lane % 4) + e; p: pairs over e, rounded.
+      float2 zero = make_float2(0.f, 0.f);     // 0 times all of them: NaN where one is not finite
+      auto fetch = [&](int c0, uint32_t (&p)[2][4]) {
         float v[2][8];                         // [h][4 k + 2 j + e]
         __syncwarp();
         tmem_ld_16x256b_x2(acc + c0, v[0]);
@@ -652,35 +689,15 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int m = 0; m < 4; ++m) p[k][m] = pack_bf16x2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
-        bool odd = false;
-        if (adapted) {
-          uint32_t top = 0u;                   // not finite?
-#pragma unroll
-          for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i >> 3][i & 7]) & 0x7fffffffu);
-          if (top >= 0x7f800000u)              // (in a column that is in use?)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              odd |= !(fabsf(v[i >> 3][i & 7]) < INFINITY) && sh.y_at[c0 + 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1)] >= 0;
-        }
-        if (!__any_sync(0xffffffffu, odd)) return false;
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i) {
-          float x = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x = i == k ? v[k >> 3][k & 7] : x;
-          const int c = c0 + 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1), f = f0 + 16 * (i >> 3) + 8 * ((i >> 1) & 1) + (lane >> 2);
-          const long long to = sh.y_at[c];
-          if (to < 0 || f >= a.M) continue;
-          if (adapted && !(fabsf(x) < INFINITY)) {
-            int b, i;
-            column(a, it.g, it.j, it.hr, c, &b, &i);
-            x = alone<kOneByte>(a, b, i, f, x);
+          for (int m = 0; m < 4; ++m) {
+            const float2 two = make_float2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
+            p[k][m] = pack_bf16x2(two.x, two.y);
+            zero = fma2(two, make_float2(0.f, 0.f), zero);
           }
-          static_cast<__nv_bfloat16*>(a.y)[to + f] = __float2bfloat16_rn(x);
-        }
-        return true;
       };
+      // Whether to look at them again: once a tile, since a vote for each 16 columns cost as much as it says (drafts 46.5 us for 46.0).
+      auto odd = [&]() { return adapted && __any_sync(0xffffffffu, !(zero.x + zero.y == 0.f)); };
+      auto again = [&](int c0, int c1) { look_again<kOneByte>(a, sh.y_at, it.g, it.j, it.hr, acc, f0, c0, c1); };
       // To shared memory, transposed, and from there 8 outputs of a token a lane.
       const uint32_t rows = smem_u32(sh.rows[q]);
       auto write = [&](int c0, const uint32_t (&p)[2][4]) {
@@ -707,22 +724,27 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       const bool more = w.tile < sh.total_tiles || w.u > w.u0;
       if (kOneByte && more) {
         uint32_t p[kShared / 16][2][4];
-        bool done[kShared / 16];
-#pragma unroll
-        for (int k = 0; k < kShared / 16; ++k) {
-          done[k] = true;
-          if (first0 + 16 * k < first1) done[k] = fetch(first0 + 16 * k, p[k]);
-        }
-        released(B_ACC_PART);
 #pragma unroll
         for (int k = 0; k < kShared / 16; ++k)
-          if (!done[k]) write(first0 + 16 * k, p[k]);
+          if (first0 + 16 * k < first1) fetch(first0 + 16 * k, p[k]);
+        const bool look = odd();
+        if (!look) released(B_ACC_PART);
+#pragma unroll
+        for (int k = 0; k < kShared / 16; ++k)
+          if (first0 + 16 * k < first1) write(first0 + 16 * k, p[k]);
+        if (look) {
+          again(first0, first1);
+          released(B_ACC_PART);
+          zero = make_float2(0.f, 0.f);
+        }
       }
 #pragma unroll 1
       for (int c0 = more ? rest0 : 0; c0 < (more ? rest1 : cols); c0 += 16) {
         uint32_t p[2][4];
-        if (!fetch(c0, p)) write(c0, p);
+        fetch(c0, p);
+        write(c0, p);
       }
+      if (odd()) again(more ? rest0 : 0, more ? rest1 : cols);
       released(B_ACC_EMPTY);
     }
     grid_dep_wait();                           // no CTA ends before the first kernel
@@ -867,10 +889,13 @@ __global__ void __launch_bounds__(32 * kCombineWarps) proj_combine_kernel(const 
     for (int c = 0; c < kCombineCols; ++c) {
       if (at[c] < 0 || f >= a.M) continue;
       float v[4] = {sum[c].x, sum[c].y, sum[c].z, sum[c].w};
-      if (adapted)
+      if (adapted && !(fabsf(v[0]) < INFINITY && fabsf(v[1]) < INFINITY && fabsf(v[2]) < INFINITY && fabsf(v[3]) < INFINITY)) {
+        const uint32_t again = a.requests > 1 ? 15u : infinite_rows(a, b[c], f, 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (!(fabsf(v[k]) < INFINITY) && f + k < a.M) v[k] = alone<kOneByte>(a, b[c], i[c], f + k, v[k]);
+          if ((a.requests > 1 ? !(fabsf(v[k]) < INFINITY) : v[k] != v[k]) && ((again >> k) & 1u) && f + k < a.M)
+            v[k] = alone<kOneByte>(a, b[c], i[c], f + k);
+      }
       __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + at[c] + f;
       if (a.wide) {
         *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
