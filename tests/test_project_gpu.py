@@ -453,3 +453,30 @@ def test_largest_inner_products(flags, B, N):
     c.x64, c.W64 = f64(c.x), f64(c.W)
     c.o.update(A=f64(c.kw["A"]), Bm=f64(c.kw["Bm"]))
     c.check(c.run(flags), flags)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,N,M", [(1, 1, 640), (64, 1, 384), (2, 150, 256), (6, 9, 130)])
+def test_long_sums_of_ordinary_values(dtype, B, N, M):
+    """d_in 8192.  An addition loses at most 2^-23 of the running sum or of what is added to it: with P the largest of an
+    output's running sums in d_in's order, a sum that begins anywhere is at most 2 P, within 32 elements (whose order
+    is the hardware's) at most G = their terms' magnitudes more; the adapter's terms U, all of them, may be added too.  So
+    d_in + 2 R additions lose 2^-23 (2 P + G + U) each at most and, of what they add, 2^-23 T; A x enters as two bf16
+    parts, 2^-16 of U.  Then half a step of bf16.  (A twentieth of the terms' magnitudes' bound.)"""
+    K, R = 8192, 16
+    c = Case(B, N, K, M, dtype, 3, R, seed=18)
+    out = torch.full((B, N, M), 7.0, dtype=torch.bfloat16, device="cuda")
+    got, st = kdtv.project(c.x, c.W, out=out, **c.kw)
+    assert int(st) == 0
+    y, mag = c.oracle()
+    x, W = torch.from_numpy(c.x64).cuda().view(B * N, K), torch.from_numpy(c.W64).cuda()
+    U = mag.reshape(B * N, M) - (np.abs(c.x64) @ np.abs(c.W64).T).reshape(B * N, M)
+    y, got, T = y.reshape(B * N, M), f64(got).reshape(B * N, M), mag.reshape(B * N, M)
+    worst = 0.0
+    for t in range(0, B * N, 7):
+        terms = x[t][None] * W
+        P = terms.cumsum(1).abs().amax(1).cpu().numpy()
+        G = terms.abs().view(M, K // 32, 32).sum(2).amax(1).cpu().numpy()
+        lim = 2.0 ** -23 * ((K + 2 * R) * (2 * P + G + U[t]) + T[t]) + 2.0 ** -16 * U[t] + 2.0 ** -8 * np.abs(y[t])
+        worst = max(worst, float((np.abs(got[t] - y[t]) / lim).max()))
+    assert worst <= 1.0
