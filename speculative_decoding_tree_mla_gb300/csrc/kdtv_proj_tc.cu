@@ -679,7 +679,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       }
       // 16 columns as the products of 8 x 8 matrices hold them: value (k, h, j, e) is output f0 + 16 h + 8 j + lane /
       // 4 of token c0 + 8 k + 2 (lane % 4) + e; p: pairs over e, rounded.
-      float2 zero = make_float2(0.f, 0.f);     // 0 times all of them: NaN where one is not finite
+      uint32_t zero[2] = {};                   // 0 times all of them, rounded, in pairs: NaN where one is not finite
       auto fetch = [&](int c0, uint32_t (&p)[2][4]) {
         float v[2][8];                         // [h][4 k + 2 j + e]
         __syncwarp();
@@ -692,11 +692,13 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           for (int m = 0; m < 4; ++m) {
             const float2 two = make_float2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
             p[k][m] = pack_bf16x2(two.x, two.y);
-            zero = fma2(two, make_float2(0.f, 0.f), zero);
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(zero[k]) : "r"(p[k][m]), "r"(0u));
           }
       };
-      // Whether to look at them again (asked once a tile: a vote for each 16 columns took 64 drafts of 8 from 46.0 to 46.5 us).
-      auto odd = [&]() { return adapted && __any_sync(0xffffffffu, !(zero.x + zero.y == 0.f)); };
+      // Whether to look at them again, asked once a tile.  (By a vote for each 16 columns, as several requests' tiles were looked
+      // at, and one request's not at all, 64 drafts of 8 took 46.1 us, not 45.0; one request's tiles pay 1 %, prompts 369 for
+      // 365, which a search of Bm's rows for infinities while the products run would cost too.)
+      auto odd = [&]() { return adapted && __any_sync(0xffffffffu, (((zero[0] | zero[1]) & 0x7fff7fffu) != 0u)); };
       auto again = [&](int c0, int c1) { look_again<kOneByte>(a, sh.y_at, it.g, it.j, it.hr, acc, f0, c0, c1); };
       // To shared memory, transposed, and from there 8 outputs of a token a lane.
       const uint32_t rows = smem_u32(sh.rows[q]);
@@ -735,7 +737,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         if (look) {
           again(first0, first1);
           released(B_ACC_PART);
-          zero = make_float2(0.f, 0.f);
+          zero[0] = zero[1] = 0u;
         }
       }
 #pragma unroll 1
