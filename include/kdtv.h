@@ -556,8 +556,11 @@ size_t kdtv_project_workspace_size(const kdtv_project_dims* dims);
  *   adapter    [B] int32, -1 .. adapters - 1, or NULL (no request has one)
  *   n_live     [B] int32 or NULL
  *   y          [B, N, d_out] fp32 or bf16 (one-byte x: bf16); no overlap with the inputs
- * Sums in fp32, rounded once.  An adapter reaches the rows of its requests
- * only, whatever values it holds.  Rows that are not live, and the rows of a
+ * Sums in fp32, rounded once; on tensor cores A x enters its product with Bm as two
+ * bf16 parts (16 significant bits).  An adapter reaches the rows of its requests
+ * only, whatever values it holds.  (On tensor cores, outputs that are not finite are
+ * computed one by one where several requests share a tile, B > 1 and N <= 128, or
+ * an infinity in Bm is beside: right, but up to a few hundred times slower.)  Rows that are not live, and the rows of a
  * request whose adapter index is out of range (*status =
  * KDTV_ERR_BAD_ADAPTER), are left as they were.  Exponent bytes 1 .. 254 stand
  * for 2^-126 .. 2^127.  bf16 with d_in and rank multiples of 8, 16-byte

@@ -124,7 +124,7 @@ __device__ __forceinline__ float squares(const float (&x)[V], float f) {
 // block; a thread has CH chunks of V elements, per_row chunks apart, so that
 // a warp's accesses are whole lines.
 // Bound by DRAM where there are rows enough (8000 bf16 rows of 8192 with the
-// residual 78 us, 6710 GB/s, to one byte 74, 6200; before its arithmetic took two
+// residual 79 us, 6640 GB/s, to one byte 75, 6100; before its arithmetic took two
 // elements an instruction and its loads waited as they lie in memory, 81 and 82), else by
 // the latency of one load, one reduction and one store (one row 3.3 us).
 // The statistics are fp32; y is (h * (1 / sqrt(mean + eps))) * w, each step
@@ -320,8 +320,8 @@ int launch_v(NormArgs& a, cudaStream_t st) {
   a.chunks = kShifted ? (a.dim + 16 / (int)sizeof(T) - 1 + V - 1) / V : a.dim / V;
   // Threads of a row: chunks each so that a thread has 128 bytes on their way (up to 32 where a chunk is one
   // element), or one each where the rows are too few to fill the device.  (8192 elements a row: 8000 bf16 rows with the
-  // residual, to one byte, 2, 4, 8 chunks 103, 70, 76 us when products were rounded as they came, without it -, 50, 58; 4000 fp32 rows, 2 and 4 chunks, with the
-  // residual 80 and 91, without it 56 and 46.)
+  // residual, to one byte, 2, 4, 8 chunks 103, 70, 76 us when products were rounded as they came (4 take 75 since),
+  // without the residual -, 50, 58; 4000 fp32 rows, 2 and 4 chunks, with the residual 80 and 91, without it 56 and 46.)
   constexpr int most = V == 1 ? 32 : 4;
   const int some = V == 1 ? 8 : sizeof(T) == 4 && a.residual ? 2 : 4;
   const int least = sizeof(O) == 1 ? KDTV_GROUP / V : 1;       // lanes that share an exponent stay together

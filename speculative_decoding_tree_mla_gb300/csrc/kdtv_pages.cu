@@ -96,7 +96,7 @@ __device__ __forceinline__ int64_t slot_of(const PageArgs& a, int L, int n, int 
 // whether an id that was taken is no page's.  What goes back, or is taken, is
 // spread by entries, which find their requests by bisection in the sums, so
 // that one request with many pages is spread like many with one.
-// Latency bound: two trips to L2, a scan and two barriers (64 requests with 8 rows each: 4.5 us, one CTA; 512 prompts of up
+// Latency bound: trips to L2, a scan and barriers (64 requests with 8 rows each: 4.5 us, one CTA; 512 prompts of up
 // to 6000 rows in pages of 16: 11 us to take 96000 pages and 20 to give them back, eight CTAs).
 __global__ void __launch_bounds__(kPageThreads) pages_resize_kernel(const __grid_constant__ PageArgs a, int ctas) {
   extern __shared__ __align__(16) int ps[];
