@@ -256,32 +256,32 @@ __device__ __noinline__ uint4 exponent_window(const uint8_t* row, int at, int by
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// 16 tokens' 32 outputs from shared memory, an output a lane: rows of y that are not 16-byte aligned.  (By itself, so
-// that the aligned rows' code stays short: inlined it cost 64 drafts of 8 two us of 52.)
-__device__ __noinline__ void write_narrow(uint32_t rows, const long long* y_at, unsigned short* y, bool on) {
+// 16 tokens' 32 outputs from shared memory, an output a lane: rows of y that are not 16-byte aligned; whether one of the
+// lane's is not finite.  (By itself, so that the aligned rows' code stays short: inlined it cost 64 drafts of 8 two us of 52.)
+__device__ __noinline__ bool write_narrow(uint32_t rows, const long long* y_at, unsigned short* y, bool on) {
   const int lane = threadIdx.x & 31;
+  bool odd = false;
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
     unsigned short v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(rows + c * kRowPitch + lane * 2) : "memory");
     const long long to = y_at[c];
-    if (on && to >= 0) y[to + lane] = v;
+    if (on && to >= 0) {
+      y[to + lane] = v;
+      odd |= (v & 0x7f80u) == 0x7f80u;
+    }
   }
+  return odd;
 }
 
-// Which of outputs f, f + step, f + 2 step, f + 3 step have an infinity in request b's rows of Bm: in a tile of one request
-// their NaN may have been made by the two parts of v.
-__device__ __noinline__ uint32_t infinite_rows(const ProjArgs& a, int b, int f, int step) {
-  const __nv_bfloat16* Bm = static_cast<const __nv_bfloat16*>(a.Bm) + (long long)a.adapter[b] * a.M * a.R;
-  uint32_t found = 0u;
-  for (int m = 0; m < 4; ++m) {
-    if (f + m * step >= a.M) break;
-    const uint4* row = reinterpret_cast<const uint4*>(Bm + (long long)(f + m * step) * a.R);
-    for (int r = 0; r < a.R / 8; ++r) {        // (the rank is a multiple of 8, and Bm is 16-byte aligned)
-      const uint4 w = row[r];
-      for (uint32_t two : {w.x, w.y, w.z, w.w})
-        if ((two & 0x7fffu) == 0x7f80u || (two & 0x7fff0000u) == 0x7f800000u) found |= 1u << m;
-    }
+// Whether request b's row of Bm for output f has an infinity: in a tile of one request a NaN of that output may have been
+// made by the two parts of v.
+__device__ __noinline__ bool infinite_row(const ProjArgs& a, int b, int f) {
+  const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Bm) + ((long long)a.adapter[b] * a.M + f) * a.R);
+  bool found = false;
+  for (int r = 0; r < a.R / 8; ++r) {          // (the rank is a multiple of 8, and Bm is 16-byte aligned)
+    const uint4 w = row[r];
+    for (uint32_t two : {w.x, w.y, w.z, w.w}) found |= (two & 0x7fffu) == 0x7f80u || (two & 0x7fff0000u) == 0x7f800000u;
   }
   return found;
 }
@@ -345,31 +345,23 @@ __device__ __noinline__ float alone(const ProjArgs& a, int b, int i, int f) {
   return sum;
 }
 
-// Columns c0 .. c1 - 1 of a tile with adapters, in which something is not finite, once they are written: such outputs of a
-// warp's 32, from f0 on, are computed by themselves where they may be wrong.  All of the warp comes along.
+// A tile with adapters in which something is not finite, once it is written: such outputs of a warp's 32, from f0 on, an
+// output a lane, are computed by themselves where they may be wrong.  All of the warp comes along.
 template <bool kOneByte>
-__device__ __noinline__ void look_again(const ProjArgs& a, const long long* y_at, int g, int j, int hr, uint32_t acc, int f0, int c0, int c1) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t rows = a.requests > 1 ? 15u : infinite_rows(a, g, f0 + (lane >> 2), 8);
-  if (!__any_sync(0xffffffffu, rows)) return;
+__device__ __noinline__ void look_again(const ProjArgs& a, const long long* y_at, int g, int j, int hr, int f0, int cols) {
+  const int f = f0 + (threadIdx.x & 31);
+  __syncwarp();                                // (the other lanes' stores)
+  if (f < a.M && (a.requests > 1 || infinite_row(a, g, f))) {
 #pragma unroll 1
-  for (; c0 < c1; c0 += 16) {
-    float v[2][8];                             // as in the kernel's fetch
-    __syncwarp();                              // (the other lanes' stores too, which come before these)
-    tmem_ld_16x256b_x2(acc + c0, v[0]);
-    tmem_ld_16x256b_x2(acc + (16u << 16) + c0, v[1]);
-    tmem_wait_ld();
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      float x = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x = i == k ? v[k >> 3][k & 7] : x;
-      const int m = 2 * (i >> 3) + ((i >> 1) & 1), c = c0 + 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1), f = f0 + 8 * m + (lane >> 2);
+    for (int c = 0; c < cols; ++c) {
       const long long to = y_at[c];
-      if (to < 0 || f >= a.M || !((rows >> m) & 1u) || (a.requests > 1 ? fabsf(x) < INFINITY : x == x)) continue;
-      int b, row;
-      column(a, g, j, hr, c, &b, &row);
-      static_cast<__nv_bfloat16*>(a.y)[to + f] = __float2bfloat16_rn(alone<kOneByte>(a, b, row, f));
+      if (to < 0) continue;
+      __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(a.y) + to + f;
+      const float x = __bfloat162float(*y);
+      if (a.requests > 1 ? fabsf(x) < INFINITY : x == x) continue;
+      int b, i;
+      column(a, g, j, hr, c, &b, &i);
+      *y = __float2bfloat16_rn(alone<kOneByte>(a, b, i, f));
     }
   }
   __syncwarp();
@@ -679,7 +671,6 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       }
       // 16 columns as the products of 8 x 8 matrices hold them: value (k, h, j, e) is output f0 + 16 h + 8 j + lane /
       // 4 of token c0 + 8 k + 2 (lane % 4) + e; p: pairs over e, rounded.
-      uint32_t zero[2] = {};                   // 0 times all of them, rounded, in pairs: NaN where one is not finite
       auto fetch = [&](int c0, uint32_t (&p)[2][4]) {
         float v[2][8];                         // [h][4 k + 2 j + e]
         __syncwarp();
@@ -689,19 +680,11 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float2 two = make_float2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
-            p[k][m] = pack_bf16x2(two.x, two.y);
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(zero[k]) : "r"(p[k][m]), "r"(0u));
-          }
+          for (int m = 0; m < 4; ++m) p[k][m] = pack_bf16x2(v[m >> 1][4 * k + 2 * (m & 1)], v[m >> 1][4 * k + 2 * (m & 1) + 1]);
       };
-      // Whether to look at them again, asked once a tile.  (By a vote for each 16 columns, as several requests' tiles were looked
-      // at, and one request's not at all, 64 drafts of 8 took 46.1 us, not 45.0; one request's tiles pay 1 %, prompts 369 for
-      // 365, which a search of Bm's rows for infinities while the products run would cost too.)
-      auto odd = [&]() { return adapted && __any_sync(0xffffffffu, (((zero[0] | zero[1]) & 0x7fff7fffu) != 0u)); };
-      auto again = [&](int c0, int c1) { look_again<kOneByte>(a, sh.y_at, it.g, it.j, it.hr, acc, f0, c0, c1); };
       // To shared memory, transposed, and from there 8 outputs of a token a lane.
       const uint32_t rows = smem_u32(sh.rows[q]);
+      uint32_t zero = 0u;                      // 0 times all that is written, in pairs: NaN where one is not finite
       auto write = [&](int c0, const uint32_t (&p)[2][4]) {
         __syncwarp();
 #pragma unroll
@@ -709,7 +692,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           stmatrix_x4_trans(rows + (8 * k + (lane & 7)) * kRowPitch + (lane >> 3) * 16, p[k][0], p[k][1], p[k][2], p[k][3]);
         __syncwarp();
         if (!a.wide) {
-          write_narrow(rows, sh.y_at + c0, static_cast<unsigned short*>(a.y) + f0, f0 + lane < a.M);
+          if (write_narrow(rows, sh.y_at + c0, static_cast<unsigned short*>(a.y) + f0, f0 + lane < a.M)) zero = 0x7fffu;
           return;
         }
         const int f = f0 + (lane & 3) * 8;
@@ -718,7 +701,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           const int c = h * 8 + (lane >> 2);
           const long long to = sh.y_at[c0 + c];
           const uint4 v = lds128(rows + c * kRowPitch + (lane & 3) * 16);
-          if (to >= 0 && f < a.M) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f) = v;
+          if (to >= 0 && f < a.M) {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + to + f) = v;
+            for (uint32_t two : {v.x, v.y, v.z, v.w}) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(zero) : "r"(two), "r"(0u));
+          }
         }
       };
       // One byte, another tile behind this one: the shared columns are read and rounded, then given back, then written.
@@ -729,16 +715,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 #pragma unroll
         for (int k = 0; k < kShared / 16; ++k)
           if (first0 + 16 * k < first1) fetch(first0 + 16 * k, p[k]);
-        const bool look = odd();
-        if (!look) released(B_ACC_PART);
+        released(B_ACC_PART);
 #pragma unroll
         for (int k = 0; k < kShared / 16; ++k)
           if (first0 + 16 * k < first1) write(first0 + 16 * k, p[k]);
-        if (look) {
-          again(first0, first1);
-          released(B_ACC_PART);
-          zero[0] = zero[1] = 0u;
-        }
       }
 #pragma unroll 1
       for (int c0 = more ? rest0 : 0; c0 < (more ? rest1 : cols); c0 += 16) {
@@ -746,8 +726,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         fetch(c0, p);
         write(c0, p);
       }
-      if (odd()) again(more ? rest0 : 0, more ? rest1 : cols);
       released(B_ACC_EMPTY);
+      if (adapted && __any_sync(0xffffffffu, (zero & 0x7fff7fffu) != 0u)) look_again<kOneByte>(a, sh.y_at, it.g, it.j, it.hr, f0, cols);
     }
     grid_dep_wait();                           // no CTA ends before the first kernel
   } else if (kOneByte && warp >= kWarpScale) {
@@ -892,10 +872,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) proj_combine_kernel(const 
       if (at[c] < 0 || f >= a.M) continue;
       float v[4] = {sum[c].x, sum[c].y, sum[c].z, sum[c].w};
       if (adapted && !(fabsf(v[0]) < INFINITY && fabsf(v[1]) < INFINITY && fabsf(v[2]) < INFINITY && fabsf(v[3]) < INFINITY)) {
-        const uint32_t again = a.requests > 1 ? 15u : infinite_rows(a, b[c], f, 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if ((a.requests > 1 ? !(fabsf(v[k]) < INFINITY) : v[k] != v[k]) && ((again >> k) & 1u) && f + k < a.M)
+          if (f + k < a.M && (a.requests > 1 ? !(fabsf(v[k]) < INFINITY) : v[k] != v[k] && infinite_row(a, b[c], f + k)))
             v[k] = alone<kOneByte>(a, b[c], i[c], f + k);
       }
       __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + at[c] + f;
