@@ -28,8 +28,8 @@
 // proj_combine_kernel adds them in the order of the units.
 //
 // Bound by the tensor cores for prompts (4 x up to 2000 rows, 4096 x 12288, rank 64:
-// 366 us, 1615 TFLOP/s; one byte, 8192 rows, 8192 x 8192: 416 us, 2650), by
-// DRAM and some 12 us of ways in and out for few tokens (one, 8192 x 10240: 38.7 us;
+// 364 us, 1620 TFLOP/s; one byte, 8192 rows, 8192 x 8192: 410 us, 2690), by
+// DRAM and some 12 us of ways in and out for few tokens (one, 8192 x 10240: 38.8 us;
 // twice the outputs 64, four times 111).  Of those 12: 2.5 to plan, 1 to the first
 // load and 1 until it is there, 1.5 to write, 3 to join, the rest launches; code that
 // runs once comes from a cold cache, so what every call passes through is kept short.
